@@ -37,10 +37,16 @@ class c2kv_geometry(ctypes.Structure):
                 ("rope_theta", ctypes.c_double)]
 
 
+class c2kv_pages8(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32)]
+
+
 _i32, _sz, _vp = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
 _pi32 = ctypes.POINTER(ctypes.c_int32)
 _pvp = ctypes.POINTER(ctypes.c_void_p)
 _pg = ctypes.POINTER(c2kv_geometry)
+_pp = ctypes.POINTER(c2kv_pages8)
 
 _SIGNATURES = {
     "c2kv_store_save": (_i32, [_vp, ctypes.c_char_p]),
@@ -75,6 +81,12 @@ _SIGNATURES = {
     "c2kv_linear": (_i32, [_vp, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _sz,
                            ctypes.c_uint32, _vp]),
     "c2kv_rmsnorm": (_i32, [_vp, _i32, _i32, _vp, ctypes.c_float, _vp, ctypes.c_uint32, _vp]),
+    "c2kv_pages8_fill": (_i32, [_pg, _pp, _i32, _i32, _i32, _pvp, _pvp, _i32, _pi32, _vp, _i32, _vp]),
+    "c2kv_pages8_append": (_i32, [_pg, _pp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "c2kv_attend_pages8_workspace_size": (_sz, [_pg, _i32, _i32]),
+    "c2kv_attend_pages8": (_i32, [_pg, _pp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
+                                  _vp, _sz, ctypes.c_uint32, _vp]),
+    "c2kv_token_logprobs": (_i32, [_vp, _i32, _i32, _i32, ctypes.c_int64, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
 }
 
 _lib = None
@@ -489,3 +501,150 @@ def c2kv_rmsnorm(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, eps: float =
     _check(load_library().c2kv_rmsnorm(_dev(x, torch.bfloat16, "x"), int(tokens), int(dim),
                                        _dev(w, torch.bfloat16, "w"), float(eps), _dev(y, torch.bfloat16, "y"),
                                        int(flags), _stream(stream)))
+
+
+# ---------------------------------------------------------------- 8-bit paged cache
+C2KV_BF16, C2KV_F32 = 0, 1
+_E4M3 = torch.float8_e4m3fn
+
+
+def _same_device(named, stream) -> None:
+    """Every tensor on the current device, where the launch goes, and with a
+    torch stream given, the stream as well."""
+    dev = torch.cuda.current_device()
+    for name, t in named:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on the current CUDA device ({dev})")
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
+        raise ValueError(f"stream must be on the current CUDA device ({dev})")
+
+
+def _shape(t: torch.Tensor, shape, dtype, name: str) -> int:
+    """The address of t, which must have this shape and type and be contiguous."""
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _pages8(g, k8, v8, k_scale, v_scale) -> c2kv_pages8:
+    if k8.dim() != 5:
+        raise ValueError("k8 must be [n_layers][n_pages][n_kv_heads][page][head_dim]")
+    n_pages, page = k8.shape[1], k8.shape[3]
+    pool = (g.n_layers, n_pages, g.n_kv_heads, page, g.head_dim)
+    return c2kv_pages8(_shape(k8, pool, _E4M3, "k8"), _shape(v8, pool, _E4M3, "v8"),
+                       _shape(k_scale, pool[:3], torch.float32, "k_scale"),
+                       _shape(v_scale, pool[:3], torch.float32, "v_scale"), n_pages, page)
+
+
+def _rope_rows(g, rope_table, rope_row_dev, batch: int):
+    """(address, rows) of a RoPE table and the address of the [batch] rows."""
+    row = g.head_dim // 2 * 16
+    return _dev(rope_table, None, "rope_table"), _nbytes(rope_table) // row, \
+        _shape(rope_row_dev, (batch,), torch.int32, "rope_row_dev")
+
+
+def c2kv_pages8_fill(geom, layer_begin: int, layer_end: int, k_caches, v_caches, cap: int, n_rows,
+                     k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                     page_table: torch.Tensor, stream=None) -> None:
+    """Rows [0, n_rows[b]) of composed bf16 caches to 8-bit pages (float8_e4m3fn
+    codes [n_layers][n_pages][n_kv_heads][page][head_dim], fp32 scales
+    [n_layers][n_pages][n_kv_heads]); page_table: int32 [batch][max_pages]."""
+    g = as_geometry(geom)
+    batch = len(k_caches)
+    if not (len(v_caches) == len(n_rows) == batch):
+        raise ValueError("k_caches, v_caches and n_rows need one entry per sequence")
+    cache = 2 * g.n_layers * g.n_kv_heads * max(0, int(cap)) * g.head_dim
+    named = [("k8", k8), ("v8", v8), ("k_scale", k_scale), ("v_scale", v_scale), ("page_table", page_table)]
+    for b in range(batch):
+        _need(k_caches[b], cache, f"k_caches[{b}]")
+        _need(v_caches[b], cache, f"v_caches[{b}]")
+        named += [(f"k_caches[{b}]", k_caches[b]), (f"v_caches[{b}]", v_caches[b])]
+    pages = _pages8(g, k8, v8, k_scale, v_scale)
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be [batch][max_pages]")
+    table = _shape(page_table, (batch, page_table.shape[1]), torch.int32, "page_table")
+    _same_device(named, stream)
+    _check(load_library().c2kv_pages8_fill(
+        ctypes.byref(g), ctypes.byref(pages), int(layer_begin), int(layer_end), batch, _ptrs(k_caches, "k_cache"),
+        _ptrs(v_caches, "v_cache"), int(cap), _i32arr(n_rows), table, page_table.shape[1], _stream(stream)))
+
+
+def c2kv_pages8_append(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
+                       v_scale: torch.Tensor, page_table: torch.Tensor, n_cached_dev: torch.Tensor,
+                       k_new: torch.Tensor, v_new: torch.Tensor, rope_table: torch.Tensor,
+                       rope_row_dev: torch.Tensor, n_new_dev: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rotates and appends k_new, v_new [batch][t_len][n_kv_heads][head_dim] to
+    8-bit pages; n_new_dev: int32 [batch] tokens of a padded batch."""
+    g = as_geometry(geom)
+    batch, t_len = k_new.shape[:2]
+    pages = _pages8(g, k8, v8, k_scale, v_scale)
+    new = (batch, t_len, g.n_kv_heads, g.head_dim)
+    table = _shape(page_table, (batch, page_table.shape[-1]), torch.int32, "page_table")
+    rope, rope_rows, rope_row = _rope_rows(g, rope_table, rope_row_dev, batch)
+    _same_device([("k8", k8), ("v8", v8), ("k_scale", k_scale), ("v_scale", v_scale), ("page_table", page_table),
+                  ("n_cached_dev", n_cached_dev), ("n_new_dev", n_new_dev), ("k_new", k_new), ("v_new", v_new),
+                  ("rope_table", rope_table), ("rope_row_dev", rope_row_dev)], stream)
+    _check(load_library().c2kv_pages8_append(
+        ctypes.byref(g), ctypes.byref(pages), int(layer), batch, t_len, table, page_table.shape[1],
+        _shape(n_cached_dev, (batch,), torch.int32, "n_cached_dev"),
+        0 if n_new_dev is None else _shape(n_new_dev, (batch,), torch.int32, "n_new_dev"),
+        _shape(k_new, new, torch.bfloat16, "k_new"), _shape(v_new, new, torch.bfloat16, "v_new"), rope, rope_rows,
+        rope_row, _stream(stream)))
+
+
+def c2kv_attend_pages8_workspace_size(geom, batch: int, max_keys: int) -> int:
+    g = as_geometry(geom)
+    return int(load_library().c2kv_attend_pages8_workspace_size(ctypes.byref(g), int(batch), int(max_keys)))
+
+
+def c2kv_attend_pages8(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
+                       v_scale: torch.Tensor, page_table: torch.Tensor, n_cached_dev: torch.Tensor, max_keys: int,
+                       q: torch.Tensor, k_new: Optional[torch.Tensor], v_new: Optional[torch.Tensor],
+                       rope_table: torch.Tensor, rope_row_dev: torch.Tensor, out: torch.Tensor,
+                       workspace: torch.Tensor, stream=None, flags: int = 0) -> None:
+    """One decode step of one layer over 8-bit pages, its token's append
+    included (k_new, v_new None: over the held rows alone)."""
+    g = as_geometry(geom)
+    batch = q.shape[0]
+    pages = _pages8(g, k8, v8, k_scale, v_scale)
+    heads, new = (batch, g.n_q_heads, g.head_dim), (batch, g.n_kv_heads, g.head_dim)
+    table = _shape(page_table, (batch, page_table.shape[-1]), torch.int32, "page_table")
+    rope, rope_rows, rope_row = _rope_rows(g, rope_table, rope_row_dev, batch)
+    _same_device([("k8", k8), ("v8", v8), ("k_scale", k_scale), ("v_scale", v_scale), ("page_table", page_table),
+                  ("n_cached_dev", n_cached_dev), ("q", q), ("k_new", k_new), ("v_new", v_new),
+                  ("rope_table", rope_table), ("rope_row_dev", rope_row_dev), ("out", out),
+                  ("workspace", workspace)], stream)
+    _check(load_library().c2kv_attend_pages8(
+        ctypes.byref(g), ctypes.byref(pages), int(layer), batch, table, page_table.shape[1],
+        _shape(n_cached_dev, (batch,), torch.int32, "n_cached_dev"), int(max_keys),
+        _shape(q, heads, torch.bfloat16, "q"),
+        0 if k_new is None else _shape(k_new, new, torch.bfloat16, "k_new"),
+        0 if v_new is None else _shape(v_new, new, torch.bfloat16, "v_new"), rope, rope_rows, rope_row,
+        _shape(out, heads, torch.bfloat16, "out"), _dev(workspace, None, "workspace"), _nbytes(workspace),
+        int(flags), _stream(stream)))
+
+
+def c2kv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], top_k: int,
+                        logprob: Optional[torch.Tensor], entropy: Optional[torch.Tensor],
+                        top_ids: Optional[torch.Tensor] = None, top_logprobs: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Log probability of tokens[row], entropy and the top_k alternatives of
+    each row of logits [rows][vocab] (bf16 or fp32, rows any stride apart)."""
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows][vocab] with neighbouring logits of a row side by side")
+    if logits.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    rows, vocab = logits.shape
+    f32, i32 = torch.float32, torch.int32
+
+    def opt(t, shape, dtype, name):
+        return 0 if t is None else _shape(t, shape, dtype, name)
+
+    _same_device([("logits", logits), ("tokens", tokens), ("logprob", logprob), ("entropy", entropy),
+                  ("top_ids", top_ids), ("top_logprobs", top_logprobs)], stream)
+    _check(load_library().c2kv_token_logprobs(
+        logits.data_ptr(), C2KV_F32 if logits.dtype == f32 else C2KV_BF16, rows, vocab,
+        logits.stride(0) if rows > 1 else max(vocab, logits.stride(0)),
+        opt(tokens, (rows,), i32, "tokens"), int(top_k), opt(logprob, (rows,), f32, "logprob"),
+        opt(entropy, (rows,), f32, "entropy"), opt(top_ids, (rows, top_k), i32, "top_ids"),
+        opt(top_logprobs, (rows, top_k), f32, "top_logprobs"), _stream(stream)))

@@ -17,6 +17,7 @@
 
 #include "c2kv_internal.h"
 #include "decode_plan.h"
+#include "pages8.h"
 
 using namespace c2kv;
 
@@ -1304,3 +1305,28 @@ extern "C" c2kv_status c2kv_attend_decode_noalloc(const c2kv_geometry* geom, int
   return c2kv_attend_decode(geom, layer, batch, k_caches, v_caches, rope_tables, cap, n_cached_dev, max_keys, q,
                             k_new, v_new, out, scratch, kNoallocScratchBytes, 0, stream);
 }
+
+// ---------------------------------------------------------------------------
+// What the entry points of the other translation units share with these.
+// ---------------------------------------------------------------------------
+namespace c2kv {
+
+c2kv_status api_fail(c2kv_status st, const char* msg) { return fail(st, msg); }
+
+c2kv_status api_cuda(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return C2KV_OK;
+  return fail(C2KV_ECUDA, std::string(what) + ": " + cudaGetErrorString(e));
+}
+
+c2kv_status api_launched(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) g_kernel_launches.fetch_add(1, std::memory_order_relaxed);
+  return api_cuda(e, what);
+}
+
+c2kv_status api_check_geom(const c2kv_geometry* g) { return check_geom(g); }
+
+c2kv_status api_device_state(unsigned** err, int* num_sms) { return device_state(err, num_sms); }
+
+int api_sm_count_for_sizing() { return sm_count_for_sizing(); }
+
+}  // namespace c2kv

@@ -1,0 +1,118 @@
+// The 8-bit paged cache: device layout, parameters and launchers shared by
+// its kernels (pages8.cu, attend_pages8.cu) and entry points (api_pages8.cu).
+#pragma once
+
+#include "c2kv_internal.h"
+
+namespace c2kv {
+
+constexpr int kMaxPagedSeqs = 256;      // sequences in one append or attention call over pages
+constexpr int kMinScaleExponent = -120;
+
+// Largest magnitude of e4m3 and the smallest exponent e with a <= 448 * 2^e
+// (448 = 1.75 * 2^8), for finite a >= 0 given by its fp32 bits.  The clamp
+// keeps both 2^e and 2^-e normal fp32 numbers (the largest e is 120).
+__device__ __forceinline__ int scale_exponent(uint32_t abs_bits) {
+  const int e = (int)(abs_bits >> 23) - 127 - 8 + ((abs_bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return max(e, kMinScaleExponent);
+}
+
+__device__ __forceinline__ float pow2_float(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+
+// Exponent of a scale that the library wrote (a power of two).
+__device__ __forceinline__ int exponent_of_scale(float s) { return (int)((__float_as_uint(s) >> 23) & 0xFFu) - 127; }
+
+// Two fp32 values -> two e4m3 codes (nearest even), `a` in the low byte; NaN
+// becomes the NaN code.
+__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// Two e4m3 codes -> fp32 (every e4m3 value is an fp16 value).
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
+  float2 f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
+
+// One layer's range of a page pool: codes [n_pages][n_kv][page][d] per layer,
+// scales [n_pages][n_kv] per layer; index 0 is K, 1 is V.
+struct PagePool {
+  uint8_t* codes[2];
+  float* scales[2];
+  int32_t n_pages, page, n_kv;
+};
+
+// Writes rows of sequences into their pages (pages8.cu): bf16 cache rows
+// (fill) or new tokens (append).
+struct PutParams {
+  PagePool pool;                 // of the first layer written
+  int64_t code_layer, scale_layer;   // elements from one layer to the next (fill)
+  const int32_t* page_table;     // [batch][max_pages]
+  int32_t max_pages, batch, n_layers;
+  unsigned* err;
+  // fill: rows [0, n_rows[b]) of caches [n_layers][n_kv][cap][d]
+  const __nv_bfloat16* src[2][kMaxBatch];
+  int32_t n_rows[kMaxBatch];
+  int32_t cap;
+  // append: [batch][t_len][n_kv][d]; token i of sequence b goes to row
+  // n_cached[b] + i and is rotated by row rope_row[b] + i of the table
+  const __nv_bfloat16* fresh[2];
+  const int32_t* n_cached;
+  const int32_t* n_new;          // null: t_len each
+  const CosSin2* tab;
+  const int32_t* rope_row;
+  int32_t t_len, table_rows;
+};
+
+// One decode step over the pages of `batch` sequences (attend_pages8.cu).
+struct AttendPages8Params {
+  PagePool pool;
+  const int32_t* page_table;
+  const int32_t* n_cached;
+  const __nv_bfloat16* q;        // [batch][n_q][d]
+  const CosSin2* tab;
+  const int32_t* rope_row;
+  __nv_bfloat16* out;            // [batch][n_q][d]
+  float* part_o;
+  float* part_ml;
+  int32_t* counters;
+  unsigned* err;
+  int32_t batch, n_q, max_pages, max_keys, table_rows, has_new, splits, split_keys;
+  float scale_log2;
+};
+
+struct LogprobParams {
+  const void* logits;
+  const int32_t* tokens;
+  float* logprob;
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  unsigned* err;
+  int64_t row_stride;
+  int32_t rows, vocab, top_k, is_f32;
+};
+
+constexpr int kMaxTopK = 64;
+
+cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, cudaStream_t st);
+cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st);
+cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, cudaStream_t st);
+cudaError_t launch_token_logprobs(const LogprobParams& p, cudaStream_t st);
+
+// What the entry points of another translation unit share with api.cu.
+c2kv_status api_fail(c2kv_status st, const char* msg);
+c2kv_status api_cuda(cudaError_t e, const char* what);
+c2kv_status api_launched(cudaError_t e, const char* what);   // counts the launch if it succeeded
+c2kv_status api_check_geom(const c2kv_geometry* g);
+c2kv_status api_device_state(unsigned** err, int* num_sms);
+int api_sm_count_for_sizing();
+
+}  // namespace c2kv

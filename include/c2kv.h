@@ -434,6 +434,114 @@ c2kv_status c2kv_rmsnorm(const void* x, int32_t tokens, int32_t dim, const void*
                          uint32_t flags, void* stream);
 
 /*
+ * The 8-bit paged cache: half the bytes of the composed bf16 cache, which is
+ * what bounds a decode step ([EXPL] "results": every generated token reads the
+ * whole composed cache).
+ *
+ * A pool of n_pages pages; a page holds `page` tokens of one layer: for each
+ * kv head, page rows of head_dim e4m3 codes of K (after RoPE) and of V, and
+ * one scale each.  A held value is code * scale.  A sequence's rows are in
+ * the pages its row of the page table names: row j in entry j / page, place
+ * j % page.  page_table: device int32 [batch][max_pages]; entries behind a
+ * sequence's last row are never read.  Sequences may share pages that no call
+ * writes; a page that a call writes must belong to one sequence of it.
+ *
+ * Scales: a scale is 2^e.  For the rows first written to a page, e is the
+ * smallest integer with a <= 448 * 2^e, a being their largest finite
+ * magnitude of that kv head (e >= -120).  Rows added later raise e to what
+ * they need, never lower it; when it rises from e to e', the page's earlier
+ * codes c become e4m3(c * 2^(e - e')).  Codes are rounded to nearest even; a
+ * value that is not finite is held as NaN.  The scales of K and V pages must
+ * be ones that these calls wrote.
+ *
+ * Device-side values (lengths, page ids, table rows) are checked on the
+ * device: a bad one is recorded in the device error word (C2KV_EDEVICE) and
+ * what it would reach is left out.  A length n_cached_dev[b] < 0 marks an
+ * empty place of the batch: nothing of it is read or written, which is no
+ * error.
+ */
+typedef struct {
+  void* k;          /* device e4m3 [n_layers][n_pages][n_kv_heads][page][head_dim] */
+  void* v;          /* same layout; both 16-byte aligned */
+  float* k_scale;   /* device fp32 [n_layers][n_pages][n_kv_heads] */
+  float* v_scale;
+  int32_t n_pages;
+  int32_t page;     /* tokens of a page: 16, 32, 64 or 128 */
+} c2kv_pages8;
+
+/*
+ * Fills pages from composed bf16 caches, layers [layer_begin, layer_end):
+ * rows [0, n_rows[b]) (host array) of sequence b's caches (as for
+ * c2kv_attend_prefill, batch <= 16) go to its pages; the places behind them
+ * in the last page are left as they were.  One pass over the rows, one
+ * launch.  Errors: C2KV_EINVAL, C2KV_ECAPACITY (n_rows above cap or above
+ * max_pages * page), C2KV_ECUDA.
+ */
+c2kv_status c2kv_pages8_fill(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer_begin,
+                             int32_t layer_end, int32_t batch, void* const* k_caches, void* const* v_caches,
+                             int32_t cap, const int32_t* n_rows, const int32_t* page_table, int32_t max_pages,
+                             void* stream);
+
+/*
+ * Appends new tokens of one layer: token i of sequence b, i < n_new_dev[b]
+ * (device int32 [batch], 0 <= n_new_dev[b] <= t_len; NULL: t_len each), goes
+ * to row n_cached_dev[b] + i.  k_new, v_new: device bf16 [batch][t_len]
+ * [n_kv_heads][head_dim], k before RoPE.  rope_table: device table of
+ * table_rows rows (layout of c2kv_rope_table); token i's key is rotated by its
+ * row rope_row_dev[b] + i and rounded to bf16, as a bf16 cache would hold it,
+ * before it is rounded to its code.  The lengths are not advanced
+ * (c2kv_seq_advance).  batch <= 256.  A sequence whose tokens would not fit
+ * max_pages pages, or whose table rows are out of range, is left out whole.
+ */
+c2kv_status c2kv_pages8_append(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
+                               int32_t t_len, const int32_t* page_table, int32_t max_pages,
+                               const int32_t* n_cached_dev, const int32_t* n_new_dev, const void* k_new,
+                               const void* v_new, const void* rope_table, int32_t table_rows,
+                               const int32_t* rope_row_dev, void* stream);
+
+/*
+ * One decode step of one layer over the pages, the append of its own token
+ * included: as c2kv_pages8_append with t_len 1, then out[b] = softmax(q_b K^T
+ * / sqrt(d)) V over the n_cached_dev[b] + 1 held rows, q_b rotated by table
+ * row rope_row_dev[b].  k_new and v_new NULL: nothing is appended and the
+ * n_cached_dev[b] held rows are attended over; with none, out[b] is 0.
+ * q, out: device bf16 [batch][n_q_heads][head_dim].  max_keys bounds the rows
+ * attended over by every sequence and sizes the launch; a sequence with more
+ * is left out.  workspace: c2kv_attend_pages8_workspace_size bytes, 16-byte
+ * aligned, zeroed once (c2kv_workspace_init), then reused by calls that do
+ * not overlap on the GPU.  flags: C2KV_DECODE_OVERLAP_PREVIOUS, as in
+ * c2kv_attend_decode: the kernel before on `stream` must not write the
+ * lengths, the page table, the RoPE table or this layer's held rows.
+ */
+size_t c2kv_attend_pages8_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t max_keys);
+c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
+                               const int32_t* page_table, int32_t max_pages, const int32_t* n_cached_dev,
+                               int32_t max_keys, const void* q, const void* k_new, const void* v_new,
+                               const void* rope_table, int32_t table_rows, const int32_t* rope_row_dev, void* out,
+                               void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
+
+/*
+ * Log probabilities from logits x [rows][vocab] (device, C2KV_BF16 or
+ * C2KV_F32, row_stride elements from one row to the next): for each row, with
+ * m = max x and S = sum exp(x - m),
+ *   logprob  = x[tokens[row]] - m - log S   (a negative token: none is given, 0),
+ *   entropy  = log S - sum exp(x - m) (x - m) / S,
+ *   top_ids, top_logprobs [rows][top_k]: the top_k largest logits, largest
+ *              first, equal ones by the lower index (NaN counts as largest).
+ * Sums are in fp32; outputs are fp32 and int32.  tokens (device int32) and
+ * logprob go together and may both be NULL, entropy may be NULL, top_k is at
+ * most 64 and may be 0.  Logits of -inf are tokens ruled out: probability 0,
+ * log probability -inf.  A row of nothing else has no distribution: its log
+ * probabilities are -inf and its entropy 0.  A row with NaN or +inf gives NaN.
+ * A token >= vocab gives NaN and is recorded in the device error word.
+ */
+#define C2KV_BF16 0
+#define C2KV_F32 1
+c2kv_status c2kv_token_logprobs(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
+                                const int32_t* tokens, int32_t top_k, float* logprob, float* entropy,
+                                int32_t* top_ids, float* top_logprobs, void* stream);
+
+/*
  * Reads and clears the device error word of the current device (waits for
  * the device).  *code receives C2KV_OK, C2KV_ETIMEOUT or C2KV_EDEVICE; the
  * return value is C2KV_ECUDA only if the read itself failed.
