@@ -1329,4 +1329,20 @@ c2kv_status api_device_state(unsigned** err, int* num_sms) { return device_state
 
 int api_sm_count_for_sizing() { return sm_count_for_sizing(); }
 
+int api_take_injected_timeout() { return take_injected_timeout() ? 1 : 0; }
+
+c2kv_status api_encode_rows128(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+  if (enc == nullptr) return fail(C2KV_ECUDA, "cuTensorMapEncodeTiled is unavailable");
+  const cuuint64_t dims[2] = {128, rows};
+  const cuuint64_t strides[1] = {128};
+  const cuuint32_t box[2] = {128, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(C2KV_ECUDA, "cuTensorMapEncodeTiled failed: " + std::to_string((int)r));
+  return C2KV_OK;
+}
+
 }  // namespace c2kv

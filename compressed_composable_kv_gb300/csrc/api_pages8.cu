@@ -53,17 +53,20 @@ c2kv_status check_new_tokens(int32_t batch, const int32_t* n_cached_dev, const v
   return C2KV_OK;
 }
 
-// Splits of the keys of one (sequence, kv head).
-void attend_splits(const c2kv_geometry* g, int batch, int max_keys, int sms, int* splits, int* keys) {
-  const int units = batch * g->n_kv_heads;
-  int s = std::max(1, std::min({(2 * sms + units - 1) / units, (max_keys + 127) / 128, 64}));
-  *keys = (max_keys + s - 1) / s;
-  *splits = (max_keys + *keys - 1) / *keys;
-}
+// Scratch of the attention: arrival counters at offset 0 (sized for the
+// largest batch, so that no call's partials overlap counters another call
+// relies on being zero), then two partial results per CTA.
+struct AttendWs {
+  size_t ml_off, o_off, total;
+};
 
-size_t attend_bytes(const c2kv_geometry* g, int batch, int splits) {
-  const size_t rows = (size_t)batch * g->n_q_heads * splits;
-  return up256((size_t)kMaxPagedSeqs * g->n_kv_heads * 4) + up256(rows * 8) + up256(rows * g->head_dim * 4);
+AttendWs attend_workspace(const c2kv_geometry* g, int sms) {
+  const size_t rows = (size_t)2 * std::min(2 * sms, kMaxPageCtas) * (g->n_q_heads / g->n_kv_heads);
+  AttendWs w;
+  w.ml_off = up256((size_t)kMaxPagedSeqs * g->n_kv_heads * sizeof(int32_t));
+  w.o_off = w.ml_off + up256(rows * 2 * sizeof(float));
+  w.total = w.o_off + up256(rows * 128 * sizeof(float));
+  return w;
 }
 
 }  // namespace
@@ -144,9 +147,7 @@ c2kv_status c2kv_pages8_append(const c2kv_geometry* geom, const c2kv_pages8* pag
 
 size_t c2kv_attend_pages8_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t max_keys) {
   if (api_check_geom(geom) != C2KV_OK || batch < 1 || batch > kMaxPagedSeqs || max_keys < 1) return 0;
-  int splits, keys;
-  attend_splits(geom, batch, max_keys, api_sm_count_for_sizing(), &splits, &keys);
-  return attend_bytes(geom, batch, splits);
+  return attend_workspace(geom, api_sm_count_for_sizing()).total;
 }
 
 c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
@@ -166,20 +167,27 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
   if (!aligned(q, 16)) return api_fail(C2KV_EINVAL, "q must be 16-byte aligned");
   if (max_keys < 1 || max_keys > max_pages * pages->page)
     return api_fail(C2KV_EINVAL, "max_keys must be in [1, max_pages * page]");
-  attend_splits(geom, batch, max_keys, api_sm_count_for_sizing(), &p.splits, &p.split_keys);
-  if (workspace_bytes < attend_bytes(geom, batch, p.splits) || !aligned(workspace, 16))
+  const int sms = std::min(api_sm_count_for_sizing(), kMaxPageCtas / 2);
+  const AttendWs w = attend_workspace(geom, sms);
+  if (workspace_bytes < w.total || !aligned(workspace, 16))
     return api_fail(C2KV_EINVAL, "workspace too small or not 16-byte aligned");
   s = api_device_state(&p.err, nullptr);
   if (s != C2KV_OK) return s;
+  for (int kv = 0; kv < 2; ++kv) {
+    s = api_encode_rows128(&p.tm[kv], p.pool.codes[kv],
+                           (uint64_t)p.pool.n_pages * p.pool.n_kv * p.pool.page * geom->head_dim / 128,
+                           (uint32_t)(p.pool.page * geom->head_dim / 128));
+    if (s != C2KV_OK) return s;
+  }
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  const size_t rows = (size_t)batch * geom->n_q_heads * p.splits;
   p.counters = reinterpret_cast<int32_t*>(ws);
-  ws += up256((size_t)kMaxPagedSeqs * geom->n_kv_heads * 4);
-  p.part_ml = reinterpret_cast<float*>(ws);
-  p.part_o = reinterpret_cast<float*>(ws + up256(rows * 8));
+  p.part_ml = reinterpret_cast<float*>(ws + w.ml_off);
+  p.part_o = reinterpret_cast<float*>(ws + w.o_off);
   p.page_table = page_table;
   p.n_cached = n_cached_dev;
   p.q = static_cast<const __nv_bfloat16*>(q);
+  p.fresh[0] = static_cast<const __nv_bfloat16*>(k_new);
+  p.fresh[1] = static_cast<const __nv_bfloat16*>(v_new);
   p.tab = static_cast<const CosSin2*>(rope_table);
   p.rope_row = rope_row_dev;
   p.out = static_cast<__nv_bfloat16*>(out);
@@ -188,16 +196,13 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
   p.max_pages = max_pages;
   p.max_keys = max_keys;
   p.table_rows = table_rows;
-  p.has_new = k_new != nullptr;
+  p.has_new = k_new != nullptr ? 1 : 0;
+  p.inject_timeout = api_take_injected_timeout();
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)geom->head_dim));
-  if (k_new != nullptr) {
-    s = c2kv_pages8_append(geom, pages, layer, batch, 1, page_table, max_pages, n_cached_dev, nullptr, k_new, v_new,
-                           rope_table, table_rows, rope_row_dev, stream);
-    if (s != C2KV_OK) return s;
-  }
-  return api_launched(
-      launch_attend_pages8(p, geom->head_dim, geom->n_q_heads / geom->n_kv_heads, static_cast<cudaStream_t>(stream)),
-      "c2kv_attend_pages8");
+  return api_launched(launch_attend_pages8(p, geom->head_dim, geom->n_q_heads / geom->n_kv_heads, sms,
+                                           (flags & C2KV_DECODE_OVERLAP_PREVIOUS) != 0,
+                                           static_cast<cudaStream_t>(stream)),
+                      "c2kv_attend_pages8");
 }
 
 c2kv_status c2kv_token_logprobs(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,

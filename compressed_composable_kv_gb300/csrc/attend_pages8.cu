@@ -1,160 +1,941 @@
-// One decode step over the 8-bit paged cache.
+// One decode step (one layer) over the 8-bit paged cache on the 5th-generation
+// tensor cores, the append of each sequence's new token included.
 //
-// s_j = (R q . K_j) / sqrt(d), out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)
-// over the rows j of a sequence, K_j and V_j = code * scale of their page.
+//   s_j = (R q . K_j) / sqrt(d),  out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)
+// over the rows j of a sequence; K_j and V_j = code * scale of their page.
 //
-// CTA (split, kv head, sequence): its 8 warps take the split's rows in turn,
-// one row at a time, the row's codes spread over the lanes, with a running
-// maximum and sum per query head.  The splits' partial (m, l, O) meet in the
-// last CTA of the (sequence, kv head) to finish.
+// The step is bound by the bytes of the pages (one byte per key, kv head and
+// element of K and of V), so the codes go from HBM to the tensor cores as they
+// are: pages by TMA into shared memory, K and V as e4m3 operands of
+// tcgen05.mma (kind::f8f6f4), and no thread touches them.  What is not e4m3 is
+// split: the query, and the softmax weights, are sums of three e4m3 numbers,
+//   x = x1 + 2^-4 x2 + 2^-9 x3,
+// each part the rounding of what the parts before it leave (a part leaves at
+// most 2^-4 of it), which holds the query to 2^-14.8 of its largest element
+// and a weight to 2^-12 of itself and 2^-27 of the largest.  The parts are
+// separate columns of the same product, which is nearly free: M = 128 rows of
+// K against N = 16 to 48 columns.  The K scale multiplies the score, the V
+// scale the weight, per key.
+//
+// A tile is 128 rows of 128 bytes of K and of V: 128 keys at head_dim 128, 256
+// keys at head_dim 64, where a row holds two keys, the query takes one column
+// with zeros in the upper half and one with zeros in the lower half, and each
+// output lane reads the columns of its own half.  A page of 16 to 128 tokens
+// is 1 to 16 KB of a tile and one TMA load.
+//
+// Work: the tiles of all (sequence, kv head) units are laid end to end and cut
+// into one equal range per CTA, from the device-side lengths, so that any mix
+// of lengths keeps every SM streaming.  A unit that one CTA holds whole is
+// written at once; else its CTAs write partial (m, l, O), and the one whose
+// tiles complete the unit's counter merges them.
+//
+// Roles: warps 0-3 softmax and epilogue (thread t owns row t of a tile, then
+// lane t of O^T), warp 4 page ids, scales and TMA, warp 5 MMA, warp 6 the
+// rotated query of each unit and the last tile of a unit: the new token, and
+// zeros in V's places behind it (they may hold any bits, NaN among them, and
+// 0 * NaN would reach the sum).
+#include <float.h>
+
 #include "pages8.h"
+#include "tcgen05.h"
 
 namespace c2kv {
 
 namespace {
 
-constexpr int AT_THREADS = 256;
-constexpr int AT_WARPS = AT_THREADS / 32;
+constexpr int AP_THREADS = 224;
+constexpr int AP_SM_THREADS = 128;
+constexpr int AP_PARTS = 3;
+constexpr int AP_KV_BYTES = 128 * 128;          // K (or V) of one tile
+constexpr int AP_STAGE = 2 * AP_KV_BYTES;
+constexpr int AP_MAX_PPT = 16;                  // pages of a tile
+
+// The tiles of a launch, from the device-side lengths.
+struct PageMap {
+  int64_t start[kMaxPagedSeqs + 1];   // first tile of each sequence; [batch] is the total
+  int32_t tb[kMaxPagedSeqs];          // tiles of each unit of the sequence (0: nothing to do)
+  int32_t keys[kMaxPagedSeqs];        // rows attended over, -1: left out
+};
 
 template <int D, int G>
-__global__ void __launch_bounds__(AT_THREADS) attend_pages8_kernel(const __grid_constant__ AttendPages8Params p) {
-  constexpr int E = D / 32;   // elements of a row per lane (2 or 4)
-  __shared__ float qs[G][D];
-  __shared__ float sm[AT_WARPS][G], sl[AT_WARPS][G], so[AT_WARPS][G][D];
-  __shared__ int last;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-  const int n = p.n_cached[b];
-  if (n < 0) return;
-  const int keys = n + p.has_new;
-  const int rr = p.rope_row[b];
-  if (keys > p.max_keys || rr < 0 || rr >= p.table_rows) {
-    if (threadIdx.x == 0) atomicOr(p.err, kErrLength);
-    return;
-  }
-  const size_t head0 = (size_t)b * p.n_q + (size_t)h * G;
-  for (int i = threadIdx.x; i < G * D / 2; i += AT_THREADS) {
-    const int g = i / (D / 2), f = i % (D / 2);
-    const CosSin2 t = p.tab[(size_t)rr * (D / 2) + f];
-    const __nv_bfloat16* q = p.q + (head0 + g) * D;
-    const float x = __bfloat162float(q[f]), y = __bfloat162float(q[f + D / 2]);
-    qs[g][f] = (x * t.ch - y * t.sh) * p.scale_log2;
-    qs[g][f + D / 2] = (y * t.ch + x * t.sh) * p.scale_log2;
-  }
-  __syncthreads();
-  float m[G], l[G], o[G][E];
+struct ApCfg {
+  static constexpr int KPR = 128 / D;                   // keys per row of a tile
+  static constexpr int TILE_KEYS = 128 * KPR;
+  static constexpr int HCOL = AP_PARTS * G;             // columns of one key of a row
+  static constexpr int NCOL = KPR * HCOL;
+  static constexpr int NPAD = (NCOL + 15) / 16 * 16;
+  // 16 columns leave room for two CTAs on an SM, which hide each other's
+  // softmax; wider operands take the SM for one CTA with twice the stages.
+  static constexpr int CTAS_PER_SM = NPAD == 16 ? 2 : 1;
+  static constexpr int STAGES = NPAD == 16 ? 3 : 6;
+  static constexpr int OP_BYTES = NPAD * 128;           // query or P^T operand [NPAD][128 bytes]
+  static constexpr int RED = 12;                        // per warp: G maxima (or sums), the largest V scale
+  static constexpr int OFF_Q = STAGES * AP_STAGE;       // two buffers each
+  static constexpr int OFF_P = OFF_Q + 2 * OP_BYTES;
+  static constexpr int OFF_MAP = OFF_P + 2 * OP_BYTES;
+  static constexpr int OFF_RED = OFF_MAP + (int)((sizeof(PageMap) + 15) / 16 * 16);
+  static constexpr int OFF_SC = OFF_RED + 2 * 4 * RED * 4;                  // [STAGES][2][AP_MAX_PPT] scales
+  static constexpr int OFF_QS = OFF_SC + STAGES * 2 * AP_MAX_PPT * 4;       // [4][8] the query's scales: read
+  // until s_free, two units behind q_free
+  static constexpr int OFF_X = OFF_QS + 4 * 8 * 4;                          // KPR == 2: [G][128] output exchange
+  static constexpr int OFF_BAR = OFF_X + (KPR == 2 ? G * 128 * 4 : 0);
+  static constexpr int N_BAR = 2 * STAGES + 2 * 8 + 5;
+  static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
+  static constexpr int SMEM = OFF_MISC + 64 + 1024;     // + slack for 1024-byte alignment
+  static_assert(OP_BYTES % 1024 == 0, "swizzled operands need 1024-byte alignment");
+  static_assert(SMEM <= (CTAS_PER_SM == 2 ? 113 * 1024 : 227 * 1024), "shared memory per CTA");
+  static constexpr int TMEM_O = 2 * NPAD;               // two S^T buffers, then two O^T buffers
+  static constexpr int TMEM_COLS = 4 * NPAD <= 64 ? 64 : 4 * NPAD <= 128 ? 128 : 256;
+  static constexpr int LD = (HCOL + 3) / 4 * 4;         // columns loaded of one key
+  static constexpr int MERGE = CTAS_PER_SM == 2 && G > 2 ? 4 : 8;   // partials whose loads are in flight together
+};
+
+// Instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D, M = 128.
+__host__ __device__ constexpr uint32_t idesc_e4m3_m128(int n, bool a_mn_major) {
+  return (1u << 4) | ((a_mn_major ? 1u : 0u) << 15) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+// N consecutive TMEM columns (N a multiple of 4) of the thread's lane.
+template <int N>
+__device__ __forceinline__ void tmem_ld_n(uint32_t addr, float* r) {
+  if constexpr (N >= 16) {
+    float t[16];
+    tmem_ld_cols<16>(addr, t);
 #pragma unroll
-  for (int g = 0; g < G; ++g) {
-    m[g] = -INFINITY;
-    l[g] = 0.f;
+    for (int i = 0; i < 16; ++i) r[i] = t[i];
+    tmem_ld_n<N - 16>(addr + 16, r + 16);
+  } else if constexpr (N >= 8) {
+    float t[8];
+    tmem_ld_cols<8>(addr, t);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[g][e] = 0.f;
-  }
-  const int lo = split * p.split_keys, hi = min(keys, lo + p.split_keys);
-  for (int j = lo + warp; j < hi; j += AT_WARPS) {
-    const int pid = p.page_table[(size_t)b * p.max_pages + j / p.pool.page];
-    if (pid < 0 || pid >= p.pool.n_pages) {
-      if (lane == 0) atomicOr(p.err, kErrLength);
-      continue;
-    }
-    const size_t block = (size_t)pid * p.pool.n_kv + h;
-    const size_t at = (block * p.pool.page + j % p.pool.page) * D + lane * E;
-    float kf[E], vf[E];
+    for (int i = 0; i < 8; ++i) r[i] = t[i];
+    tmem_ld_n<N - 8>(addr + 8, r + 8);
+  } else if constexpr (N >= 4) {
+    float t[4];
+    tmem_ld_cols<4>(addr, t);
 #pragma unroll
-    for (int e = 0; e < E; e += 2) {
-      const float2 a = e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(p.pool.codes[0] + at + e));
-      const float2 c = e4m3x2_to_float2(*reinterpret_cast<const uint16_t*>(p.pool.codes[1] + at + e));
-      kf[e] = a.x, kf[e + 1] = a.y;
-      vf[e] = c.x, vf[e + 1] = c.y;
-    }
-    const float ks = p.pool.scales[0][block], vs = p.pool.scales[1][block];
-#pragma unroll
-    for (int g = 0; g < G; ++g) {
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) s = fmaf(kf[e], qs[g][lane * E + e], s);
-#pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-      s *= ks;
-      const float mn = fmaxf(m[g], s);
-      const float a = m[g] == -INFINITY ? 0.f : exp2f(m[g] - mn), pr = exp2f(s - mn);
-      m[g] = mn;
-      l[g] = l[g] * a + pr;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[g][e] = fmaf(o[g][e], a, pr * vs * vf[e]);
-    }
-  }
-#pragma unroll
-  for (int g = 0; g < G; ++g) {
-    if (lane == 0) {
-      sm[warp][g] = m[g];
-      sl[warp][g] = l[g];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) so[warp][g][lane * E + e] = o[g][e];
-  }
-  __syncthreads();
-  const size_t unit = (size_t)b * p.pool.n_kv + h;
-  for (int i = threadIdx.x; i < G * D; i += AT_THREADS) {
-    const int g = i / D, d = i % D;
-    float mx = -INFINITY, lt = 0.f, ot = 0.f;
-    for (int w = 0; w < AT_WARPS; ++w) mx = fmaxf(mx, sm[w][g]);
-    for (int w = 0; w < AT_WARPS; ++w) {
-      const float a = sm[w][g] == -INFINITY ? 0.f : exp2f(sm[w][g] - mx);
-      lt = fmaf(a, sl[w][g], lt);
-      ot = fmaf(a, so[w][g][d], ot);
-    }
-    const size_t at = (unit * p.splits + split) * G + g;
-    p.part_o[at * D + d] = ot;
-    if (d == 0) {
-      p.part_ml[at * 2] = mx;
-      p.part_ml[at * 2 + 1] = lt;
-    }
-  }
-  __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    const int prev = atomicAdd(p.counters + unit, 1);
-    last = prev == p.splits - 1;
-    if (last) p.counters[unit] = 0;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!last) return;
-  for (int i = threadIdx.x; i < G * D; i += AT_THREADS) {
-    const int g = i / D, d = i % D;
-    float mx = -INFINITY, lt = 0.f, ot = 0.f;
-    const size_t at0 = unit * p.splits * G + g;
-    for (int s = 0; s < p.splits; ++s) mx = fmaxf(mx, __ldcg(p.part_ml + (at0 + (size_t)s * G) * 2));
-    for (int s = 0; s < p.splits; ++s) {
-      const size_t at = at0 + (size_t)s * G;
-      const float ms = __ldcg(p.part_ml + at * 2);
-      const float a = ms == -INFINITY ? 0.f : exp2f(ms - mx);
-      lt = fmaf(a, __ldcg(p.part_ml + at * 2 + 1), lt);
-      ot = fmaf(a, __ldcg(p.part_o + at * D + d), ot);
-    }
-    p.out[(head0 + g) * D + d] = __float2bfloat16_rn(keys == 0 ? 0.f : ot / lt);
+    for (int i = 0; i < 4; ++i) r[i] = t[i];
   }
 }
 
+// Three e4m3 parts of two values: the codes of part k of a in the low byte of
+// out[k], of b in the high byte.
+__device__ __forceinline__ void split3(float a, float b, uint32_t (&out)[3]) {
+  out[0] = e4m3x2(a, b);
+  float2 f = e4m3x2_to_float2(out[0]);
+  a = (a - f.x) * 16.f;
+  b = (b - f.y) * 16.f;
+  out[1] = e4m3x2(a, b);
+  f = e4m3x2_to_float2(out[1]);
+  out[2] = e4m3x2((a - f.x) * 32.f, (b - f.y) * 32.f);
+}
+
+struct PageTile {
+  int32_t b, h, t;   // sequence, kv head, tile of the unit
+};
+
+__device__ __forceinline__ PageTile tile_at(const PageMap& m, int batch, int64_t x) {
+  int lo = 0, hi = batch;   // the last sequence with start <= x
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (m.start[mid] <= x) lo = mid;
+    else hi = mid;
+  }
+  const uint32_t r = (uint32_t)(x - m.start[lo]), tb = (uint32_t)m.tb[lo];   // below 2^30: tb <= 2^23, 128 heads
+  PageTile d;
+  d.b = lo;
+  d.h = (int)(r / tb);
+  d.t = (int)(r % tb);
+  return d;
+}
+
+// The tile after d, while there is one.
+__device__ __forceinline__ PageTile tile_next(const PageMap& m, int n_kv, PageTile d) {
+  if (++d.t < m.tb[d.b]) return d;
+  d.t = 0;
+  if (++d.h < n_kv) return d;
+  d.h = 0;
+  do ++d.b;
+  while (d.b < kMaxPagedSeqs - 1 && m.tb[d.b] == 0);
+  return d;
+}
+
+// The part of one unit that the CTA owns: its tiles [j0, j0 + n), starting at
+// tile t0 of unit (b, h).
+struct PageSeg {
+  int b, h, t0, j0, n;
+};
+
+__device__ __forceinline__ int64_t cta_first(int64_t total, int c, int ctas) { return (int64_t)c * total / ctas; }
+__device__ __forceinline__ int cta_of(int64_t total, int64_t x, int ctas) {
+  return (int)(((x + 1) * ctas - 1) / total);
+}
+
+template <int D, int G>
+__global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
+    attend_pages8_kernel(const __grid_constant__ AttendPages8Params p) {
+  using C = ApCfg<D, G>;
+  constexpr int KPR = C::KPR, CH = D / 16;   // CH: 8-element chunks of half a head, 16-byte chunks of a row
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sQ = smem + C::OFF_Q;
+  uint8_t* sP = smem + C::OFF_P;
+  PageMap& M = *reinterpret_cast<PageMap*>(smem + C::OFF_MAP);
+  float* red = reinterpret_cast<float*>(smem + C::OFF_RED);
+  float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
+  float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
+  float* xo = reinterpret_cast<float*>(smem + C::OFF_X);
+  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* kv_empty = kv_full + C::STAGES;
+  uint64_t* s_full = kv_empty + C::STAGES;
+  uint64_t* s_free = s_full + 2;
+  uint64_t* p_full = s_free + 2;
+  uint64_t* p_free = p_full + 2;
+  uint64_t* o_full = p_free + 2;
+  uint64_t* o_free = o_full + 2;
+  uint64_t* q_full = o_free + 2;
+  uint64_t* q_free = q_full + 2;
+  uint64_t* fix_req = q_free + 2;     // a unit's last tile has landed
+  uint64_t* fix_bar = fix_req + 1;    // and is complete: new token in, V's tail zero
+  uint64_t* grp_bar = fix_bar + 1;    // the softmax warps' group barrier
+  uint64_t* mma_done = grp_bar + 1;   // every MMA of the CTA has completed
+  uint64_t* never = mma_done + 1;     // test hook: nothing arrives
+  volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
+  volatile int* last_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);
+  volatile int* none_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 24);
+
+  const int tid = threadIdx.x;
+  const int warp = tid >> 5, lane = tid & 31;
+  const int cta = blockIdx.x, ctas = gridDim.x;
+  auto stage_k = [&](int s) { return smem + s * AP_STAGE; };
+  auto stage_v = [&](int s) { return smem + s * AP_STAGE + AP_KV_BYTES; };
+
+  if (warp == 0) {
+    // The map, 8 sequences to a lane: lengths, page table and held rows are
+    // what the previous kernel does not write, so this does not wait for it.
+    constexpr int PER = kMaxPagedSeqs / 32;
+    int32_t tb[PER];
+    int64_t sum = 0;
+    bool bad = false, none = false;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int b = lane * PER + i;
+      int32_t keys = -1;
+      if (b < p.batch) {
+        const int32_t n = p.n_cached[b];
+        if (n >= 0) {
+          const int32_t rr = p.rope_row[b];
+          if (n > p.max_keys - p.has_new || rr < 0 || rr >= p.table_rows) bad = true;
+          else keys = n + p.has_new;
+        }
+      }
+      none |= keys == 0;
+      M.keys[b] = keys;
+      tb[i] = keys > 0 ? (keys + C::TILE_KEYS - 1) / C::TILE_KEYS : 0;
+      M.tb[b] = tb[i];
+      sum += (int64_t)tb[i] * p.pool.n_kv;
+    }
+    int64_t incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += o;
+    }
+    int64_t at = incl - sum;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      M.start[lane * PER + i] = at;
+      at += (int64_t)tb[i] * p.pool.n_kv;
+    }
+    if (lane == 31) M.start[kMaxPagedSeqs] = at;
+    bad = __any_sync(0xffffffffu, bad);
+    none = __any_sync(0xffffffffu, none);
+    if (lane == 0) {
+      *none_flag = none;
+      if (bad && cta == 0) atomicOr(p.err, kErrLength);
+    }
+  } else if (warp == 4) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr((const void*)tmem_slot)),
+                 "r"(C::TMEM_COLS)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp == 5) {
+    if (lane == 0) {
+      for (int s = 0; s < C::STAGES; ++s) {
+        mbar_init(&kv_full[s], 1);
+        mbar_init(&kv_empty[s], 1);
+      }
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&s_full[i], 1);
+        mbar_init(&s_free[i], AP_SM_THREADS);
+        mbar_init(&p_full[i], AP_SM_THREADS);
+        mbar_init(&p_free[i], 1);
+        mbar_init(&o_full[i], 1);
+        mbar_init(&o_free[i], AP_SM_THREADS);
+        mbar_init(&q_full[i], 1);
+        mbar_init(&q_free[i], 1);
+      }
+      mbar_init(fix_req, 1);
+      mbar_init(fix_bar, 1);
+      mbar_init(grp_bar, 4);
+      mbar_init(mma_done, 1);
+      mbar_init(never, 1);
+      *abort_flag = 0;
+      fence_barrier_init();
+    }
+  } else {
+    // rows and halves of the operands that nothing writes stay zero
+    for (int i = (warp == 6 ? 3 : warp - 1) * 32 + lane; i < 4 * C::OP_BYTES / 16; i += 128)
+      reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const int64_t total = M.start[kMaxPagedSeqs];
+  const int64_t x0 = cta_first(total, cta, ctas), x1 = cta_first(total, cta + 1, ctas);
+  const int ntiles = (int)(x1 - x0);
+  if (*none_flag) {
+    // sequences without a row: their output is zero
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int b = cta; b < p.batch; b += ctas)
+      if (M.keys[b] == 0)
+        for (int i = tid; i < p.n_q * D / 8; i += AP_THREADS)
+          reinterpret_cast<uint4*>(p.out + (size_t)b * p.n_q * D)[i] = make_uint4(0, 0, 0, 0);
+  }
+  if (ntiles == 0) {   // uniform over the CTA
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp == 4)
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
+    return;
+  }
+  auto seg_at = [&](int j) {
+    const PageTile d = tile_at(M, p.batch, x0 + j);
+    PageSeg s;
+    s.b = d.b;
+    s.h = d.h;
+    s.t0 = d.t;
+    s.j0 = j;
+    s.n = min(M.tb[d.b] - d.t, ntiles - j);
+    return s;
+  };
+  const int page = p.pool.page;
+  const int lg = 31 - __clz(page);            // log2 of the page
+  const int prows = page / KPR;               // rows of 128 bytes of a page
+  int issued = 0;                             // the TMA warp's count of tiles requested
+
+  if (warp == 4) {
+    // ---------------- page ids, scales and TMA.  The pages of the CTA's tiles,
+    // laid end to end, are taken 32 at a time, one to a lane: while a batch is
+    // loaded, the scales of the next and the ids of the one after are on their
+    // way (two dependent reads, about a microsecond).
+    const int lgp = (31 - __clz(C::TILE_KEYS)) - lg;   // log2 of a tile's pages
+    const int ppt = 1 << lgp, per = 32 >> lgp;         // pages of a tile, tiles of a batch
+    struct Ref {
+      int32_t id, h;   // id: -1 no page here, -2 outside the pool
+      float ks, vs;
+    };
+    auto ask = [&](int batch0) {
+      Ref r;
+      r.id = -1;
+      r.h = 0;
+      const int j = batch0 + (lane >> lgp);
+      if (j < ntiles) {
+        const PageTile d = tile_at(M, p.batch, x0 + j);
+        const int pg = (d.t << lgp) + (lane & (ppt - 1));
+        r.h = d.h;
+        if (pg <= (M.keys[d.b] - 1) >> lg) {
+          r.id = p.page_table[(size_t)d.b * p.max_pages + pg];
+          if (r.id < 0) r.id = -2;
+        }
+      }
+      return r;
+    };
+    auto ask_scales = [&](Ref& r) {
+      r.ks = r.vs = 0.f;
+      if (r.id >= p.pool.n_pages) r.id = -2;
+      if (r.id >= 0) {
+        const size_t block = (size_t)r.id * p.pool.n_kv + r.h;
+        r.ks = p.pool.scales[0][block];
+        r.vs = p.pool.scales[1][block];
+      }
+    };
+    Ref cur = ask(0), nxt = ask(per);
+    ask_scales(cur);
+    bool ok = true;
+    for (int j0 = 0; ok && j0 < ntiles; j0 += per) {
+      ask_scales(nxt);
+      const Ref third = ask(j0 + 2 * per);
+      if (cur.id == -2) atomicOr(p.err, kErrLength);
+      for (int tt = 0; ok && tt < per && j0 + tt < ntiles; ++tt) {
+        const int j = j0 + tt, s = j % C::STAGES;
+        if (j >= C::STAGES &&
+            !__all_sync(0xffffffffu, wait_or_abort(&kv_empty[s], ((j - C::STAGES) / C::STAGES) & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        if ((lane >> lgp) == tt) {
+          const int i = lane & (ppt - 1);
+          // no page, or one outside the pool: a load from before the pool,
+          // which TMA fills with zeros; its scale 0 masks the keys
+          const int y = cur.id >= 0 ? (cur.id * p.pool.n_kv + cur.h) * prows : -prows;
+          tma_load_2d(stage_k(s) + i * prows * 128, &p.tm[0], 0, y, &kv_full[s]);
+          tma_load_2d(stage_v(s) + i * prows * 128, &p.tm[1], 0, y, &kv_full[s]);
+          sc[(s * 2 + 0) * AP_MAX_PPT + i] = cur.ks;
+          sc[(s * 2 + 1) * AP_MAX_PPT + i] = cur.vs;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], AP_STAGE);
+        ++issued;
+      }
+      cur = nxt;
+      nxt = third;
+    }
+  } else if (warp == 5) {
+    if (lane == 0) {
+      // ---------------- MMA issuer
+      constexpr uint32_t idesc_qk = idesc_e4m3_m128(C::NPAD, false);   // A = K (K-major), B = query (K-major)
+      constexpr uint32_t idesc_pv = idesc_e4m3_m128(C::NPAD, true);    // A = V^T (MN-major), B = P^T (K-major)
+      auto issue_pv = [&](int i) -> bool {
+        const int pb = i & 1, s = i % C::STAGES;
+        if (!wait_or_abort(&p_full[pb], (i >> 1) & 1, abort_flag, p.err)) return false;
+        if (i >= 2 && !wait_or_abort(&o_free[pb], ((i - 2) >> 1) & 1, abort_flag, p.err)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)   // 32 rows of V at a time
+          mma_e4m3(tmem + C::TMEM_O + pb * C::NPAD, sw128_desc(smem_addr(stage_v(s)) + kk * 4096, AP_KV_BYTES, 1024),
+                   sw128_desc(smem_addr(sP + pb * C::OP_BYTES) + kk * 32, 16, 1024), idesc_pv, kk > 0 ? 1u : 0u);
+        mma_commit(&kv_empty[s]);
+        mma_commit(&p_free[pb]);
+        mma_commit(&o_full[pb]);
+        return true;
+      };
+      bool ok = true;
+      int seg = -1, fixes = 0;
+      PageTile d = tile_at(M, p.batch, x0);
+      for (int j = 0; ok && j < ntiles; ++j) {
+        const bool first = j == 0 || d.t == 0;
+        const bool unit_last = d.t == M.tb[d.b] - 1;
+        const bool seg_last = j == ntiles - 1 || unit_last;
+        if (first) ++seg;
+        const int s = j % C::STAGES;
+        ok = wait_or_abort(&kv_full[s], (j / C::STAGES) & 1, abort_flag, p.err);
+        if (ok && first) ok = wait_or_abort(&q_full[seg & 1], (seg >> 1) & 1, abort_flag, p.err);
+        if (ok && unit_last) {
+          mbar_arrive(fix_req);
+          ok = wait_or_abort(fix_bar, (fixes++) & 1, abort_flag, p.err);
+        }
+        if (ok && j >= 2) ok = wait_or_abort(&s_free[j & 1], ((j - 2) >> 1) & 1, abort_flag, p.err);
+        if (!ok) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)   // 32 bytes of the rows at a time
+          mma_e4m3(tmem + (j & 1) * C::NPAD, sw128_desc(smem_addr(stage_k(s)) + kk * 32, 16, 1024),
+                   sw128_desc(smem_addr(sQ + (seg & 1) * C::OP_BYTES) + kk * 32, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
+        mma_commit(&s_full[j & 1]);
+        if (seg_last) mma_commit(&q_free[seg & 1]);
+        if (j >= 1) ok = issue_pv(j - 1);
+        if (j + 1 < ntiles) d = tile_next(M, p.pool.n_kv, d);
+      }
+      if (ok) issue_pv(ntiles - 1);
+      // every MMA issued above must complete before TMEM is released
+      mma_commit(mma_done);
+      mbar_wait(mma_done, 0);
+    }
+  } else if (warp == 6) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // ---------------- the query of each unit: rotated, times log2(e)/sqrt(d),
+    // over a power of two that brings its largest element into (224, 448], in
+    // three parts.  Item (g, c): elements 8c.. and D/2 + 8c.. of head g.
+    auto prep_q = [&](int i, const PageSeg& sg) -> bool {
+      if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&q_free[i & 1], ((i - 2) >> 1) & 1, abort_flag, p.err)))
+        return false;
+      const CosSin2* trow = p.tab + (size_t)p.rope_row[sg.b] * (D / 2);
+      uint8_t* qb = sQ + (i & 1) * C::OP_BYTES;
+#pragma unroll
+      for (int it = 0; it < (G * CH + 31) / 32; ++it) {
+        const int item = it * 32 + lane;
+        const int g = item / CH, c = item % CH;
+        const bool on = g < G;
+        float x[8], y[8];
+        uint32_t m = 0;
+        if (on) {
+          const uint4* row = reinterpret_cast<const uint4*>(p.q + ((size_t)sg.b * p.n_q + sg.h * G + g) * D);
+          unpack8(row[c], x);
+          unpack8(row[c + CH], y);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const CosSin2 t = trow[c * 8 + e];
+            const float a = (x[e] * t.ch - y[e] * t.sh) * p.scale_log2;
+            y[e] = (y[e] * t.ch + x[e] * t.sh) * p.scale_log2;
+            x[e] = a;
+            m = max(m, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
+          }
+        }
+#pragma unroll
+        for (int off = CH / 2; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+        const int e = m < 0x7F800000u ? scale_exponent(m) : 0;   // a query that is not finite answers NaN
+        const float inv = pow2_float(-e);
+        if (on) {
+          uint32_t cx[4][3], cy[4][3];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            split3(x[2 * k] * inv, x[2 * k + 1] * inv, cx[k]);
+            split3(y[2 * k] * inv, y[2 * k + 1] * inv, cy[k]);
+          }
+#pragma unroll
+          for (int par = 0; par < KPR; ++par)
+#pragma unroll
+            for (int k = 0; k < AP_PARTS; ++k) {
+              const int r = par * C::HCOL + k * G + g;
+              const int b0 = par * D + 8 * c, b1 = b0 + D / 2;   // bytes of the row
+              *reinterpret_cast<uint2*>(qb + r * 128 + (((b0 >> 4) ^ (r & 7)) << 4) + (b0 & 8)) =
+                  make_uint2(cx[0][k] | (cx[1][k] << 16), cx[2][k] | (cx[3][k] << 16));
+              *reinterpret_cast<uint2*>(qb + r * 128 + (((b1 >> 4) ^ (r & 7)) << 4) + (b1 & 8)) =
+                  make_uint2(cy[0][k] | (cy[1][k] << 16), cy[2][k] | (cy[3][k] << 16));
+            }
+          if (c == 0) qs[(i & 3) * 8 + g] = m < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
+        }
+      }
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[i & 1]);
+      return true;
+    };
+    // The last tile of a unit, tile j of the CTA.  Lanes 0.. hold the new key,
+    // lanes 16.. the new value, 16 elements each as above.
+    int fixes = 0;
+    auto fixup = [&](int j, const PageSeg& sg) -> bool {
+      const int s = j % C::STAGES;
+      const int n = M.keys[sg.b] - 1;                       // the last row
+      const int at = n - (sg.t0 + (j - sg.j0)) * C::TILE_KEYS;   // its key in the tile
+      const int pi = at >> lg, pl = n & (page - 1);         // its page of the tile, its place there
+      const int id = p.page_table[(size_t)sg.b * p.max_pages + (n >> lg)];
+      const bool in = id >= 0 && id < p.pool.n_pages;
+      const int kv = lane >> 4, c = lane & 15;
+      const bool mine = p.has_new && in && c < CH;
+      float lo[8], hi[8];
+      uint32_t m = 0;
+      if (mine) {
+        const uint4* src = reinterpret_cast<const uint4*>(p.fresh[kv] + ((size_t)sg.b * p.pool.n_kv + sg.h) * D);
+        uint4 x = src[c], y = src[c + CH];
+        new_row8(x, y, kv == 0 ? p.tab + (size_t)p.rope_row[sg.b] * (D / 2) + c * 8 : nullptr, lo, hi);
+        m = max(max_finite8(lo), max_finite8(hi));
+      }
+#pragma unroll
+      for (int off = 8; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+      // The request comes once the tile has landed, so the stage's current
+      // fill is this tile's and its wait below returns at once.
+      if (!__all_sync(0xffffffffu, wait_or_abort(fix_req, (fixes++) & 1, abort_flag, p.err))) return false;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&kv_full[s], (j / C::STAGES) & 1, abort_flag, p.err))) return false;
+      // byte `byte` (a multiple of 8) of key `key` of the tile
+      auto place = [&](uint8_t* tile, int key, int byte) {
+        const int row = key / KPR, b = key % KPR * D + byte;
+        return tile + row * 128 + (((b >> 4) ^ (row & 7)) << 4) + (b & 8);
+      };
+      const size_t block = in ? (size_t)id * p.pool.n_kv + sg.h : 0;
+      if (p.has_new && in) {   // uniform over the warp
+        float* scs = sc + (s * 2 + kv) * AP_MAX_PPT + pi;
+        int e = scale_exponent(m), e_old = e;
+        if (pl > 0) {
+          e_old = exponent_of_scale(*scs);
+          e = max(e, e_old);
+        }
+        __syncwarp();
+        uint8_t* tile = kv == 0 ? stage_k(s) : stage_v(s);
+        if (mine) {
+          const float inv = pow2_float(-e);
+          const uint2 a = codes8(lo, inv), b = codes8(hi, inv);
+          *reinterpret_cast<uint2*>(place(tile, at, 8 * c)) = a;
+          *reinterpret_cast<uint2*>(place(tile, at, D / 2 + 8 * c)) = b;
+          uint8_t* dst = p.pool.codes[kv] + (block * page + pl) * D;
+          *reinterpret_cast<uint2*>(dst + 8 * c) = a;
+          *reinterpret_cast<uint2*>(dst + D / 2 + 8 * c) = b;
+          if (c == 0) {
+            *scs = pow2_float(e);
+            p.pool.scales[kv][block] = pow2_float(e);
+          }
+        }
+        // a larger scale: the page's earlier codes follow (rare)
+#pragma unroll 1
+        for (int k = 0; k < 2; ++k) {
+          const int d_e = __shfl_sync(0xffffffffu, e_old - e, k * 16);
+          if (d_e >= 0) continue;
+          const float by = pow2_float(max(d_e, -100));
+          uint8_t* t = k == 0 ? stage_k(s) : stage_v(s);
+          for (int i = lane; i < pl * CH; i += 32) {
+            const int key = i / CH, byte = i % CH * 16;
+            uint4* u = reinterpret_cast<uint4*>(place(t, at - pl + key, byte));
+            const uint4 r = make_uint4(rescale4(u->x, by), rescale4(u->y, by), rescale4(u->z, by), rescale4(u->w, by));
+            *u = r;
+            *reinterpret_cast<uint4*>(p.pool.codes[k] + (block * page + key) * D + byte) = r;
+          }
+        }
+      }
+      for (int i = lane; i < (page - 1 - pl) * CH; i += 32)
+        *reinterpret_cast<uint4*>(place(stage_v(s), at + 1 + i / CH, i % CH * 16)) = make_uint4(0, 0, 0, 0);
+      // the other key of the last row of K would reach this one's score
+      if (KPR == 2 && (pl & 1) == 0 && lane < CH)
+        *reinterpret_cast<uint4*>(place(stage_k(s), at + 1, lane * 16)) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(fix_bar);
+      return true;
+    };
+    PageSeg cur = seg_at(0);
+    bool ok = prep_q(0, cur);
+    for (int i = 0; ok; ++i) {
+      const bool more = cur.j0 + cur.n < ntiles;
+      PageSeg nxt = cur;
+      if (more) {
+        nxt = seg_at(cur.j0 + cur.n);
+        ok = prep_q(i + 1, nxt);
+      }
+      if (ok && cur.t0 + cur.n == M.tb[cur.b]) ok = fixup(cur.j0 + cur.n - 1, cur);
+      if (!more) break;
+      cur = nxt;
+    }
+  } else {
+    // ---------------- softmax and epilogue: thread tid owns row tid of each
+    // tile (lane tid of S^T) and lane tid of O^T
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
+    const uint32_t o_col = C::TMEM_O + (tid / D) * C::HCOL;   // the columns of this lane's half
+    int k_sync = 0;
+    bool ok = true;
+    int arrived = -1;   // last segment whose tiles were added to its unit's counter
+    // out[b][h * G + g] from the lanes' o[g] over l[g]
+    auto write_out = [&](int b, int h, const float (&o)[G], const float (&l)[G]) -> bool {
+      __nv_bfloat16* out = p.out + ((size_t)b * p.n_q + (size_t)h * G) * D;
+      if constexpr (KPR == 1) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) out[g * D + tid] = __float2bfloat16_rn(l[g] == 0.f ? 0.f : o[g] / l[g]);
+      } else {
+#pragma unroll
+        for (int g = 0; g < G; ++g) xo[g * 128 + tid] = l[g] == 0.f ? 0.f : o[g] / l[g];
+        if (!group_sync(grp_bar, k_sync, abort_flag, p.err)) return false;
+        for (int i = tid; i < G * D; i += AP_SM_THREADS)
+          out[i] = __float2bfloat16_rn(xo[i / D * 128 + i % D] + xo[i / D * 128 + D + i % D]);
+        if (!group_sync(grp_bar, k_sync, abort_flag, p.err)) return false;
+      }
+      return true;
+    };
+    int i = 0;
+    PageSeg sg = seg_at(0);
+    for (;; ++i) {
+      const int nkeys = M.keys[sg.b];
+      const bool whole = sg.t0 == 0 && sg.n == M.tb[sg.b];
+      float m_ref[G], l_part[G], o_acc[G], a_prev[G];
+      float v_prev = 0.f;   // V factor of the tile before
+#pragma unroll
+      for (int g = 0; g < G; ++g) {
+        m_ref[g] = -INFINITY;
+        l_part[g] = 0.f;
+        o_acc[g] = 0.f;
+        a_prev[g] = 0.f;
+      }
+      auto consume_o = [&](int jj) -> bool {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&o_full[jj & 1], (jj >> 1) & 1, abort_flag, p.err))) return false;
+        tc_fence_after();
+        float ov[C::LD];
+        tmem_ld_n<C::LD>(lane_base + o_col + (jj & 1) * C::NPAD, ov);
+        tmem_wait_ld();
+        tc_fence_before();
+        mbar_arrive(&o_free[jj & 1]);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+          o_acc[g] = fmaf(o_acc[g], a_prev[g], fmaf(fmaf(ov[2 * G + g], 0x1p-5f, ov[G + g]), 0x1p-4f, ov[g]) * v_prev);
+        return true;
+      };
+      for (int tt = 0; ok && tt < sg.n; ++tt) {
+        const int j = sg.j0 + tt;
+        const int sb = j & 1, st = j % C::STAGES;
+        const int key0 = (sg.t0 + tt) * C::TILE_KEYS + tid * KPR;
+        if (p.inject_timeout && j == 0 && !__all_sync(0xffffffffu, mbar_wait(never, 0, kInjectWaitCycles))) {
+          *abort_flag = 1;
+          atomicOr(p.err, kErrTimeout);
+          ok = false;
+          break;
+        }
+        if (!__all_sync(0xffffffffu, wait_or_abort(&s_full[sb], (j >> 1) & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        float s[KPR][G], vs[KPR];
+        float vmax = 0.f;
+#pragma unroll
+        for (int par = 0; par < KPR; ++par) {
+          float sv[C::LD];
+          tmem_ld_n<C::LD>(lane_base + sb * C::NPAD + par * C::HCOL, sv);
+          const int pg = (tid * KPR + par) >> lg;
+          const float ks = sc[(st * 2 + 0) * AP_MAX_PPT + pg];
+          vs[par] = sc[(st * 2 + 1) * AP_MAX_PPT + pg];
+          const bool valid = key0 + par < nkeys && ks > 0.f;
+          if (!valid) vs[par] = 0.f;
+          vmax = fmaxf(vmax, vs[par]);
+          tmem_wait_ld();
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            const float f = fmaf(fmaf(sv[2 * G + g], 0x1p-5f, sv[G + g]), 0x1p-4f, sv[g]);
+            s[par][g] = valid ? f * (ks * qs[(i & 3) * 8 + g]) : -INFINITY;
+          }
+        }
+        tc_fence_before();
+        mbar_arrive(&s_free[sb]);
+        float* rb = red + (k_sync & 1) * 4 * C::RED;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          float t = s[0][g];
+          if constexpr (KPR == 2) t = fmaxf(t, s[1][g]);
+          t = warp_max(t);
+          if (lane == 0) rb[warp * C::RED + g] = t;
+        }
+        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+        if (lane == 0) rb[warp * C::RED + 8] = vmax;
+        if (!group_sync(grp_bar, k_sync, abort_flag, p.err)) {
+          ok = false;
+          break;
+        }
+        vmax = fmaxf(fmaxf(rb[8], rb[C::RED + 8]), fmaxf(rb[2 * C::RED + 8], rb[3 * C::RED + 8]));
+        // weights are written as 256 p (V scale / the tile's largest): at most 256
+        const float v_inv = vmax > 0.f ? 1.f / vmax : 0.f;
+        float alpha[G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float tmax =
+              fmaxf(fmaxf(rb[g], rb[C::RED + g]), fmaxf(rb[2 * C::RED + g], rb[3 * C::RED + g]));
+          const float mn = fmaxf(m_ref[g], tmax);
+          alpha[g] = m_ref[g] == -INFINITY ? 0.f : ex2_approx(m_ref[g] - mn);
+          m_ref[g] = mn;
+          const float base = mn == -INFINITY ? 0.f : mn;   // every key masked so far
+          l_part[g] *= alpha[g];
+#pragma unroll
+          for (int par = 0; par < KPR; ++par) {
+            s[par][g] = ex2_approx(s[par][g] - base);
+            l_part[g] += s[par][g];
+          }
+        }
+        if (j >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&p_free[sb], ((j - 2) >> 1) & 1, abort_flag, p.err))) {
+          ok = false;
+          break;
+        }
+        uint8_t* pb = sP + sb * C::OP_BYTES + (tid & 15);
+#pragma unroll
+        for (int par = 0; par < KPR; ++par) {
+          const float w = vs[par] * v_inv * 256.f;
+#pragma unroll
+          for (int g = 0; g < G; g += 2) {
+            uint32_t part[3];
+            const float a = s[par][g] * w, b = g + 1 < G ? s[par][g + 1 < G ? g + 1 : g] * w : 0.f;
+            split3(a, b, part);
+#pragma unroll
+            for (int k = 0; k < AP_PARTS; ++k) {
+              const int r = par * C::HCOL + k * G + g;
+              pb[r * 128 + (((tid >> 4) ^ (r & 7)) << 4)] = (uint8_t)part[k];
+              if (g + 1 < G) pb[(r + 1) * 128 + (((tid >> 4) ^ ((r + 1) & 7)) << 4)] = (uint8_t)(part[k] >> 8);
+            }
+          }
+        }
+        fence_proxy_async();
+        mbar_arrive(&p_full[sb]);
+        if (tt > 0 && !consume_o(j - 1)) {
+          ok = false;
+          break;
+        }
+        v_prev = vmax * 0x1p-8f;
+#pragma unroll
+        for (int g = 0; g < G; ++g) a_prev[g] = alpha[g];
+      }
+      if (ok) ok = consume_o(sg.j0 + sg.n - 1);
+
+      // ---------------- segment epilogue
+      const int u = sg.b * p.pool.n_kv + sg.h;
+      float L[G];
+      if (ok) {
+        float* rb = red + (k_sync & 1) * 4 * C::RED;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          const float ls = warp_sum(l_part[g]);
+          if (lane == 0) rb[warp * C::RED + g] = ls;
+        }
+        ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
+#pragma unroll
+        for (int g = 0; g < G; ++g) L[g] = (rb[g] + rb[C::RED + g]) + (rb[2 * C::RED + g] + rb[3 * C::RED + g]);
+      }
+      if (ok && whole) {
+        ok = write_out(sg.b, sg.h, o_acc, L);
+      } else if (ok) {
+        const int slot = 2 * cta + (i == 0 ? 0 : 1);
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+          p.part_o[((size_t)slot * G + g) * 128 + tid] = o_acc[g];
+          if (tid == g) {
+            p.part_ml[((size_t)slot * G + g) * 2 + 0] = m_ref[g];
+            p.part_ml[((size_t)slot * G + g) * 2 + 1] = L[g];
+          }
+        }
+        // every partial store of the CTA is ordered before tid 0's arrival
+        // (a release at GPU scope, cumulative over the group barrier)
+        ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
+        if (ok && tid == 0) {
+          int prev;
+          asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;"
+                       : "=r"(prev)
+                       : "l"(p.counters + u), "r"(sg.n)
+                       : "memory");
+          const bool last = prev + sg.n == M.tb[sg.b];
+          if (last) p.counters[u] = 0;   // every CTA of the unit has arrived
+          *last_flag = last ? 1 : 0;
+          arrived = i;
+        }
+        if (ok) ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
+        if (ok && *last_flag) {
+          // ---- merge: the CTAs from the one with the unit's first tile to the
+          // one with its last; a CTA's slot is 2c, or 2c + 1 if the unit is not
+          // where its range starts.  Their order is fixed, so the result is.
+          const int64_t uf = M.start[sg.b] + (int64_t)sg.h * M.tb[sg.b];
+          const int cf = cta_of(total, uf, ctas), nctr = cta_of(total, uf + M.tb[sg.b] - 1, ctas) - cf + 1;
+          float mx[G], lt[G], ot[G];
+#pragma unroll
+          for (int g = 0; g < G; ++g) {
+            mx[g] = -INFINITY;
+            lt[g] = 0.f;
+            ot[g] = 0.f;
+          }
+          for (int k0 = 0; k0 < nctr; k0 += C::MERGE) {
+            float mv[C::MERGE][G], lv[C::MERGE][G], ov[C::MERGE][G];
+#pragma unroll
+            for (int k = 0; k < C::MERGE; ++k) {
+              const int c = cf + k0 + k;
+              const int64_t f = cta_first(total, c, ctas);
+              const bool on = k0 + k < nctr && f < cta_first(total, c + 1, ctas);
+              const int sl = on ? 2 * c + (f < uf ? 1 : 0) : 0;
+#pragma unroll
+              for (int g = 0; g < G; ++g) {
+                const size_t r = (size_t)sl * G + g;
+                mv[k][g] = on ? __ldcg(&p.part_ml[r * 2]) : -INFINITY;
+                lv[k][g] = on ? __ldcg(&p.part_ml[r * 2 + 1]) : 0.f;
+                ov[k][g] = on ? __ldcg(&p.part_o[r * 128 + tid]) : 0.f;
+              }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+              float cm = mx[g];
+#pragma unroll
+              for (int k = 0; k < C::MERGE; ++k) cm = fmaxf(cm, mv[k][g]);
+              const float base = cm == -INFINITY ? 0.f : cm;
+              const float f = mx[g] == -INFINITY ? 0.f : ex2_approx(mx[g] - base);
+              lt[g] *= f;
+              ot[g] *= f;
+#pragma unroll
+              for (int k = 0; k < C::MERGE; ++k) {
+                const float w = mv[k][g] == -INFINITY ? 0.f : ex2_approx(mv[k][g] - base);
+                lt[g] = fmaf(w, lv[k][g], lt[g]);
+                ot[g] = fmaf(w, ov[k][g], ot[g]);
+              }
+              mx[g] = cm;
+            }
+          }
+          ok = write_out(sg.b, sg.h, ot, lt);
+        }
+      }
+      if (!ok) break;
+      if (sg.j0 + sg.n >= ntiles) break;
+      sg = seg_at(sg.j0 + sg.n);
+    }
+    if (!ok && tid == 0) {
+      // The CTA gave up: still add the tiles of its remaining shared units to
+      // their counters (their outputs are undefined), so that every counter is
+      // back at zero when the launch ends.
+      PageSeg q = seg_at(0);
+      for (int k = 0;; ++k) {
+        if (k > arrived && !(q.t0 == 0 && q.n == M.tb[q.b])) {
+          const int prev = atomicAdd(p.counters + q.b * p.pool.n_kv + q.h, q.n);
+          if (prev + q.n == M.tb[q.b]) p.counters[q.b * p.pool.n_kv + q.h] = 0;
+        }
+        if (q.j0 + q.n >= ntiles) break;
+        q = seg_at(q.j0 + q.n);
+      }
+    }
+  }
+
+  // ---------------- teardown
+  tc_fence_before();
+  __syncthreads();
+  if (*abort_flag && warp == 4 && lane == 0) {
+    // let the copies in flight land before the shared memory is released
+    for (int j = max(0, issued - C::STAGES); j < issued; ++j)
+      mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1);
+  }
+  __syncthreads();
+  if (warp == 4) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
+  }
+}
+
+template <int D, int G>
+cudaError_t launch_ap(const AttendPages8Params& p, int sms, bool overlap, cudaStream_t st) {
+  using C = ApCfg<D, G>;
+  static KernelSetup s;
+  const int dev = setup_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  {
+    std::lock_guard<std::mutex> lk(s.mu);
+    if (s.state[dev] == 0) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(attend_pages8_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      if (e != cudaSuccess) cudaGetLastError();
+      s.state[dev] = e == cudaSuccess ? 1 : -(int)e;
+    }
+    if (s.state[dev] != 1) return (cudaError_t)(-s.state[dev]);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(C::CTAS_PER_SM * sms);
+  cfg.blockDim = dim3(AP_THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = overlap ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, attend_pages8_kernel<D, G>, p);
+}
+
 template <int D>
-void launch_g(const AttendPages8Params& p, int group, dim3 grid, cudaStream_t st) {
+cudaError_t launch_group(const AttendPages8Params& p, int group, int sms, bool overlap, cudaStream_t st) {
   switch (group) {
-    case 1: attend_pages8_kernel<D, 1><<<grid, AT_THREADS, 0, st>>>(p); break;
-    case 2: attend_pages8_kernel<D, 2><<<grid, AT_THREADS, 0, st>>>(p); break;
-    case 4: attend_pages8_kernel<D, 4><<<grid, AT_THREADS, 0, st>>>(p); break;
-    case 5: attend_pages8_kernel<D, 5><<<grid, AT_THREADS, 0, st>>>(p); break;
-    case 8: attend_pages8_kernel<D, 8><<<grid, AT_THREADS, 0, st>>>(p); break;
+    case 1: return launch_ap<D, 1>(p, sms, overlap, st);
+    case 2: return launch_ap<D, 2>(p, sms, overlap, st);
+    case 4: return launch_ap<D, 4>(p, sms, overlap, st);
+    case 5: return launch_ap<D, 5>(p, sms, overlap, st);
+    case 8: return launch_ap<D, 8>(p, sms, overlap, st);
+    default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, cudaStream_t st) {
-  const dim3 grid(p.splits, p.pool.n_kv, p.batch);
-  if (head_dim == 128) launch_g<128>(p, group, grid, st);
-  else launch_g<64>(p, group, grid, st);
-  return cudaGetLastError();
+cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, bool overlap,
+                                 cudaStream_t st) {
+  return head_dim == 128 ? launch_group<128>(p, group, sms, overlap, st)
+                         : launch_group<64>(p, group, sms, overlap, st);
 }
 
 }  // namespace c2kv

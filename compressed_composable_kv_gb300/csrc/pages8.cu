@@ -25,34 +25,6 @@ constexpr int PUT_THREADS = 256;
 constexpr int PUT_ROWS = 128;
 constexpr int PUT_WARP_ROWS = 16;
 
-// 8 bf16 bit patterns in a uint4 -> fp32, NaN where not finite.
-__device__ __forceinline__ void finite_or_nan8(const uint4& u, float (&f)[8]) {
-  unpack8(u, f);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if ((__float_as_uint(f[e]) & 0x7F800000u) == 0x7F800000u) f[e] = __uint_as_float(0x7FFFFFFFu);
-}
-
-__device__ __forceinline__ uint32_t max_finite8(const float (&f)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = __float_as_uint(f[e]) & 0x7FFFFFFFu;
-    if (b < 0x7F800000u) m = max(m, b);
-  }
-  return m;
-}
-
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
-  return make_uint2(e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16),
-                    e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16));
-}
-
-__device__ __forceinline__ uint32_t rescale4(uint32_t c, float by) {
-  const float2 a = e4m3x2_to_float2(c & 0xFFFFu), b = e4m3x2_to_float2(c >> 16);
-  return e4m3x2(a.x * by, a.y * by) | (e4m3x2(b.x * by, b.y * by) << 16);
-}
-
 // D: head_dim.  APPEND: rows [n_cached, n_cached + new) from the new tokens,
 // K rotated; else rows [0, n_rows) from the bf16 caches.
 template <int D, bool APPEND>
@@ -105,21 +77,9 @@ __global__ void __launch_bounds__(PUT_THREADS) put_kernel(const __grid_constant_
       src = p.fresh[kv] + (((size_t)b * p.t_len + (r - first)) * p.pool.n_kv + h) * D;
     else
       src = p.src[kv][b] + (((size_t)layer * p.pool.n_kv + h) * p.cap + r) * D;
-    uint4 x = reinterpret_cast<const uint4*>(src)[c], y = reinterpret_cast<const uint4*>(src)[c + CH];
-    if (APPEND && kv == 0) {
-      float xf[8], yf[8];
-      unpack8(x, xf);
-      unpack8(y, yf);
-      rotate8_df(x, y, p.tab + (size_t)(p.rope_row[b] + (r - first)) * (D / 2) + c * 8);
-      finite_or_nan8(x, lo[it]);
-      finite_or_nan8(y, hi[it]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (!(fabsf(xf[e]) < INFINITY && fabsf(yf[e]) < INFINITY)) lo[it][e] = hi[it][e] = __uint_as_float(0x7FFFFFFFu);
-    } else {
-      finite_or_nan8(x, lo[it]);
-      finite_or_nan8(y, hi[it]);
-    }
+    const uint4 x = reinterpret_cast<const uint4*>(src)[c], y = reinterpret_cast<const uint4*>(src)[c + CH];
+    const CosSin2* t = APPEND && kv == 0 ? p.tab + (size_t)(p.rope_row[b] + (r - first)) * (D / 2) + c * 8 : nullptr;
+    new_row8(x, y, t, lo[it], hi[it]);
     m = max(m, max(max_finite8(lo[it]), max_finite8(hi[it])));
   }
   m = __reduce_max_sync(0xffffffffu, m);

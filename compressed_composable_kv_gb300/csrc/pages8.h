@@ -41,6 +41,55 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   return f;
 }
 
+// 8 bf16 bit patterns -> fp32, NaN where not finite.
+__device__ __forceinline__ void finite_or_nan8(const uint4& u, float (&f)[8]) {
+  unpack8(u, f);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if ((__float_as_uint(f[e]) & 0x7F800000u) == 0x7F800000u) f[e] = __uint_as_float(0x7FFFFFFFu);
+}
+
+// The values to hold of one 8-element chunk of each half of a bf16 row: as
+// they are, or (t: the 8 cos/sin of these pairs) rotated and rounded to bf16,
+// as a bf16 cache holds a key.  NaN where not finite; a pair with a member
+// that is not finite is NaN in both.
+__device__ __forceinline__ void new_row8(uint4 x, uint4 y, const CosSin2* t, float (&lo)[8], float (&hi)[8]) {
+  finite_or_nan8(x, lo);
+  finite_or_nan8(y, hi);
+  if (t == nullptr) return;
+  bool bad[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) bad[e] = !(lo[e] == lo[e] && hi[e] == hi[e]);
+  rotate8_df(x, y, t);
+  finite_or_nan8(x, lo);
+  finite_or_nan8(y, hi);
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (bad[e]) lo[e] = hi[e] = __uint_as_float(0x7FFFFFFFu);
+}
+
+// Bits of the largest finite magnitude.
+__device__ __forceinline__ uint32_t max_finite8(const float (&f)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t b = __float_as_uint(f[e]) & 0x7FFFFFFFu;
+    if (b < 0x7F800000u) m = max(m, b);
+  }
+  return m;
+}
+
+__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
+  return make_uint2(e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16),
+                    e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16));
+}
+
+// Four codes times a power of two, rounded again.
+__device__ __forceinline__ uint32_t rescale4(uint32_t c, float by) {
+  const float2 a = e4m3x2_to_float2(c & 0xFFFFu), b = e4m3x2_to_float2(c >> 16);
+  return e4m3x2(a.x * by, a.y * by) | (e4m3x2(b.x * by, b.y * by) << 16);
+}
+
 // One layer's range of a page pool: codes [n_pages][n_kv][page][d] per layer,
 // scales [n_pages][n_kv] per layer; index 0 is K, 1 is V.
 struct PagePool {
@@ -72,21 +121,26 @@ struct PutParams {
 };
 
 // One decode step over the pages of `batch` sequences (attend_pages8.cu).
+// tm: the layer's K and V codes as rows of 128 bytes (2-D map {128, rows}, one
+// page and kv head per box, 128-byte swizzle).
 struct AttendPages8Params {
+  CUtensorMap tm[2];
   PagePool pool;
   const int32_t* page_table;
   const int32_t* n_cached;
   const __nv_bfloat16* q;        // [batch][n_q][d]
+  const __nv_bfloat16* fresh[2]; // [batch][n_kv][d] new k (before RoPE) and v
   const CosSin2* tab;
   const int32_t* rope_row;
   __nv_bfloat16* out;            // [batch][n_q][d]
-  float* part_o;
-  float* part_ml;
-  int32_t* counters;
+  float* part_o;                 // [2 * CTAs][G][128] partial O of shared units
+  float* part_ml;                // [2 * CTAs][G][2] their (m, l)
+  int32_t* counters;             // [batch * n_kv] tiles merged so far per unit
   unsigned* err;
-  int32_t batch, n_q, max_pages, max_keys, table_rows, has_new, splits, split_keys;
+  int32_t batch, n_q, max_pages, max_keys, table_rows, has_new, inject_timeout;
   float scale_log2;
 };
+constexpr int kMaxPageCtas = 512;   // CTAs of one launch (at most two per SM)
 
 struct LogprobParams {
   const void* logits;
@@ -104,7 +158,8 @@ constexpr int kMaxTopK = 64;
 
 cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, cudaStream_t st);
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st);
-cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, cudaStream_t st);
+cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, bool overlap,
+                                 cudaStream_t st);
 cudaError_t launch_token_logprobs(const LogprobParams& p, cudaStream_t st);
 
 // What the entry points of another translation unit share with api.cu.
@@ -114,5 +169,8 @@ c2kv_status api_launched(cudaError_t e, const char* what);   // counts the launc
 c2kv_status api_check_geom(const c2kv_geometry* g);
 c2kv_status api_device_state(unsigned** err, int* num_sms);
 int api_sm_count_for_sizing();
+int api_take_injected_timeout();
+// uint8 tensor map {128, rows} of 128-byte rows, box {128, box_rows}, 128-byte swizzle
+c2kv_status api_encode_rows128(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows);
 
 }  // namespace c2kv
