@@ -31,9 +31,9 @@
 //
 // Roles: warps 0-3 softmax and epilogue (thread t owns row t of a tile, then
 // lane t of O^T), warp 4 page ids, scales and TMA, warp 5 MMA, warp 6 the
-// rotated query of each unit and the last tile of a unit: the new token, and
-// zeros in V's places behind it (they may hold any bits, NaN among them, and
-// 0 * NaN would reach the sum).
+// rotated query of each unit, warp 7 the last tile of a unit: the new token,
+// and zeros in V's places behind it (they may hold any bits, NaN among them,
+// and 0 * NaN would reach the sum).
 #include <float.h>
 
 #include "pages8.h"
@@ -43,31 +43,37 @@ namespace c2kv {
 
 namespace {
 
-constexpr int AP_THREADS = 224;
+constexpr int AP_THREADS = 256;
 constexpr int AP_SM_THREADS = 128;
 constexpr int AP_PARTS = 3;
 constexpr int AP_KV_BYTES = 128 * 128;          // K (or V) of one tile
 constexpr int AP_STAGE = 2 * AP_KV_BYTES;
 constexpr int AP_MAX_PPT = 16;                  // pages of a tile
 
+constexpr int kMinTiles = 4;     // tiles of a CTA below which fewer CTAs work
+constexpr int kWholeTiles = 4;   // units of at most so many tiles are not shared
+constexpr int kMergeRows = 64;   // partials of one round of a merge
+
 // The tiles of a launch, from the device-side lengths.
 struct PageMap {
-  int64_t start[kMaxPagedSeqs + 1];   // first tile of each sequence; [batch] is the total
-  int32_t tb[kMaxPagedSeqs];          // tiles of each unit of the sequence (0: nothing to do)
-  int32_t keys[kMaxPagedSeqs];        // rows attended over, -1: left out
+  int64_t start[kMaxPagedSeqs + 1];   // first tile of each sequence; the last one is the total
+  int32_t keys[kMaxPagedSeqs];        // rows attended over; -1: left out
+  int32_t rope[kMaxPagedSeqs];        // the sequence's row of the RoPE table
+  int32_t longest;                    // tiles of the longest unit
 };
 
 template <int D, int G>
 struct ApCfg {
   static constexpr int KPR = 128 / D;                   // keys per row of a tile
   static constexpr int TILE_KEYS = 128 * KPR;
+  static constexpr int TILE_LG = KPR == 1 ? 7 : 8;      // its log2
   static constexpr int HCOL = AP_PARTS * G;             // columns of one key of a row
   static constexpr int NCOL = KPR * HCOL;
   static constexpr int NPAD = (NCOL + 15) / 16 * 16;
-  // 16 columns leave room for two CTAs on an SM, which hide each other's
-  // softmax; wider operands take the SM for one CTA with twice the stages.
-  static constexpr int CTAS_PER_SM = NPAD == 16 ? 2 : 1;
-  static constexpr int STAGES = NPAD == 16 ? 3 : 6;
+  // Two CTAs to an SM hide each other's softmax (a tile's chain of steps takes
+  // about 0.8 us, an SM's share of HBM brings one in 0.73 us); each has as many
+  // stages as half an SM holds.
+  static constexpr int STAGES = NPAD == 16 ? 3 : 2;
   static constexpr int OP_BYTES = NPAD * 128;           // query or P^T operand [NPAD][128 bytes]
   static constexpr int RED = 12;                        // per warp: G maxima (or sums), the largest V scale
   static constexpr int OFF_Q = STAGES * AP_STAGE;       // two buffers each
@@ -83,11 +89,12 @@ struct ApCfg {
   static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;     // + slack for 1024-byte alignment
   static_assert(OP_BYTES % 1024 == 0, "swizzled operands need 1024-byte alignment");
-  static_assert(SMEM <= (CTAS_PER_SM == 2 ? 113 * 1024 : 227 * 1024), "shared memory per CTA");
+  static_assert(SMEM <= 113 * 1024, "shared memory per CTA");
   static constexpr int TMEM_O = 2 * NPAD;               // two S^T buffers, then two O^T buffers
   static constexpr int TMEM_COLS = 4 * NPAD <= 64 ? 64 : 4 * NPAD <= 128 ? 128 : 256;
   static constexpr int LD = (HCOL + 3) / 4 * 4;         // columns loaded of one key
-  static constexpr int MERGE = CTAS_PER_SM == 2 && G > 2 ? 4 : 8;   // partials whose loads are in flight together
+  static constexpr int MERGE = G > 4 ? 4 : 8;           // partials whose loads are in flight together
+  static_assert(kMergeRows * G * 4 <= 2 * OP_BYTES, "the weights of a merge are kept in P^T's buffers");
 };
 
 // Instruction descriptor, kind::f8f6f4: e4m3 A and B, fp32 D, M = 128.
@@ -143,29 +150,19 @@ struct PageTile {
   int32_t b, h, t;   // sequence, kv head, tile of the unit
 };
 
-__device__ __forceinline__ PageTile tile_at(const PageMap& m, int batch, int64_t x) {
+__device__ __forceinline__ PageTile tile_at(const PageMap& m, int batch, int tb_shift, int64_t x) {
   int lo = 0, hi = batch;   // the last sequence with start <= x
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (m.start[mid] <= x) lo = mid;
     else hi = mid;
   }
-  const uint32_t r = (uint32_t)(x - m.start[lo]), tb = (uint32_t)m.tb[lo];   // below 2^30: tb <= 2^23, 128 heads
+  const uint32_t r = (uint32_t)(x - m.start[lo]);   // below 2^30: tb <= 2^23, 128 heads
+  const uint32_t tb = (uint32_t)(m.keys[lo] - 1 >> tb_shift) + 1;
   PageTile d;
   d.b = lo;
   d.h = (int)(r / tb);
   d.t = (int)(r % tb);
-  return d;
-}
-
-// The tile after d, while there is one.
-__device__ __forceinline__ PageTile tile_next(const PageMap& m, int n_kv, PageTile d) {
-  if (++d.t < m.tb[d.b]) return d;
-  d.t = 0;
-  if (++d.h < n_kv) return d;
-  d.h = 0;
-  do ++d.b;
-  while (d.b < kMaxPagedSeqs - 1 && m.tb[d.b] == 0);
   return d;
 }
 
@@ -175,13 +172,23 @@ struct PageSeg {
   int b, h, t0, j0, n;
 };
 
-__device__ __forceinline__ int64_t cta_first(int64_t total, int c, int ctas) { return (int64_t)c * total / ctas; }
-__device__ __forceinline__ int cta_of(int64_t total, int64_t x, int ctas) {
-  return (int)(((x + 1) * ctas - 1) / total);
-}
+// How the tiles are cut: CTA c owns [first(c), first(c + 1)).
+struct PageCut {
+  int64_t total, base;
+  int rem, ctas;   // the first rem of the ctas working CTAs own base + 1 tiles, the others base
+
+  __device__ __forceinline__ int64_t div(int64_t a, int64_t b) const {
+    return total < INT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+  }
+  __device__ __forceinline__ int64_t first(int c) const { return c < ctas ? c * base + min(c, rem) : total; }
+  __device__ __forceinline__ int of(int64_t x) const {   // the CTA that owns tile x
+    const int64_t big = rem * (base + 1);
+    return (int)(x < big ? div(x, base + 1) : rem + div(x - big, base));
+  }
+};
 
 template <int D, int G>
-__global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
+__global__ void __launch_bounds__(AP_THREADS, 2)
     attend_pages8_kernel(const __grid_constant__ AttendPages8Params p) {
   using C = ApCfg<D, G>;
   constexpr int KPR = C::KPR, CH = D / 16;   // CH: 8-element chunks of half a head, 16-byte chunks of a row
@@ -221,46 +228,47 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
   auto stage_v = [&](int s) { return smem + s * AP_STAGE + AP_KV_BYTES; };
 
   if (warp == 0) {
-    // The map, 8 sequences to a lane: lengths, page table and held rows are
-    // what the previous kernel does not write, so this does not wait for it.
-    constexpr int PER = kMaxPagedSeqs / 32;
-    int32_t tb[PER];
-    int64_t sum = 0;
+    // The map, 32 sequences at a time: lengths, table rows, page table and held
+    // rows are what the previous kernel does not write, so this does not wait.
+    int64_t at = 0;
+    int longest = 0;
     bool bad = false, none = false;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int b = lane * PER + i;
-      int32_t keys = -1;
+    for (int b0 = 0; b0 < kMaxPagedSeqs; b0 += 32) {
+      const int b = b0 + lane;
+      if (b0 >= p.batch) {   // nothing behind the batch
+        M.start[b] = at;
+        continue;
+      }
+      int32_t n = -1, rr = 0, keys = -1;
       if (b < p.batch) {
-        const int32_t n = p.n_cached[b];
-        if (n >= 0) {
-          const int32_t rr = p.rope_row[b];
-          if (n > p.max_keys - p.has_new || rr < 0 || rr >= p.table_rows) bad = true;
-          else keys = n + p.has_new;
-        }
+        n = p.n_cached[b];
+        rr = p.rope_row[b];
+      }
+      if (n >= 0) {
+        if (n > p.max_keys - p.has_new || rr < 0 || rr >= p.table_rows) bad = true;
+        else keys = n + p.has_new;
       }
       none |= keys == 0;
       M.keys[b] = keys;
-      tb[i] = keys > 0 ? (keys + C::TILE_KEYS - 1) / C::TILE_KEYS : 0;
-      M.tb[b] = tb[i];
-      sum += (int64_t)tb[i] * p.pool.n_kv;
-    }
-    int64_t incl = sum;
+      M.rope[b] = rr;
+      const int tb = keys > 0 ? ((keys - 1) >> C::TILE_LG) + 1 : 0;
+      longest = max(longest, tb);
+      const int64_t mine = (int64_t)tb * p.pool.n_kv;
+      int64_t incl = mine;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
-      if (lane >= off) incl += o;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
+      }
+      M.start[b] = at + incl - mine;
+      at += __shfl_sync(0xffffffffu, incl, 31);
     }
-    int64_t at = incl - sum;
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      M.start[lane * PER + i] = at;
-      at += (int64_t)tb[i] * p.pool.n_kv;
-    }
-    if (lane == 31) M.start[kMaxPagedSeqs] = at;
+    longest = __reduce_max_sync(0xffffffffu, longest);
     bad = __any_sync(0xffffffffu, bad);
     none = __any_sync(0xffffffffu, none);
     if (lane == 0) {
+      M.start[kMaxPagedSeqs] = at;
+      M.longest = longest;
       *none_flag = none;
       if (bad && cta == 0) atomicOr(p.err, kErrLength);
     }
@@ -296,7 +304,7 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
     }
   } else {
     // rows and halves of the operands that nothing writes stay zero
-    for (int i = (warp == 6 ? 3 : warp - 1) * 32 + lane; i < 4 * C::OP_BYTES / 16; i += 128)
+    for (int i = (warp >= 6 ? warp - 3 : warp - 1) * 32 + lane; i < 4 * C::OP_BYTES / 16; i += 160)
       reinterpret_cast<uint4*>(sQ)[i] = make_uint4(0, 0, 0, 0);
     fence_proxy_async();
   }
@@ -304,9 +312,28 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  const int64_t total = M.start[kMaxPagedSeqs];
-  const int64_t x0 = cta_first(total, cta, ctas), x1 = cta_first(total, cta + 1, ctas);
+  auto unit_tiles = [&](int b) { return ((M.keys[b] - 1) >> C::TILE_LG) + 1; };   // 0 for -1 and 0 keys
+  PageCut cut;
+  cut.total = M.start[kMaxPagedSeqs];
+  int64_t x0, x1;
+  if (M.longest <= kWholeTiles && p.batch * p.pool.n_kv <= ctas) {
+    // one short unit to a CTA: nothing to merge
+    const int b = cta / p.pool.n_kv;
+    cut.ctas = 0;
+    x0 = x1 = 0;
+    if (b < p.batch) {
+      x0 = M.start[b] + (int64_t)(cta % p.pool.n_kv) * unit_tiles(b);
+      x1 = x0 + unit_tiles(b);
+    }
+  } else {
+    cut.ctas = (int)min((int64_t)ctas, max((int64_t)1, cut.div(cut.total, kMinTiles)));
+    cut.base = cut.div(cut.total, cut.ctas);
+    cut.rem = (int)(cut.total - cut.base * cut.ctas);
+    x0 = cut.first(cta);
+    x1 = cut.first(cta + 1);
+  }
   const int ntiles = (int)(x1 - x0);
+  if (warp == 4 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.tm[lane]) : "memory");
   if (*none_flag) {
     // sequences without a row: their output is zero
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -322,13 +349,13 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
     return;
   }
   auto seg_at = [&](int j) {
-    const PageTile d = tile_at(M, p.batch, x0 + j);
+    const PageTile d = tile_at(M, p.batch, C::TILE_LG, x0 + j);
     PageSeg s;
     s.b = d.b;
     s.h = d.h;
     s.t0 = d.t;
     s.j0 = j;
-    s.n = min(M.tb[d.b] - d.t, ntiles - j);
+    s.n = min(unit_tiles(d.b) - d.t, ntiles - j);
     return s;
   };
   const int page = p.pool.page;
@@ -353,7 +380,7 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
       r.h = 0;
       const int j = batch0 + (lane >> lgp);
       if (j < ntiles) {
-        const PageTile d = tile_at(M, p.batch, x0 + j);
+        const PageTile d = tile_at(M, p.batch, C::TILE_LG, x0 + j);
         const int pg = (d.t << lgp) + (lane & (ppt - 1));
         r.h = d.h;
         if (pg <= (M.keys[d.b] - 1) >> lg) {
@@ -372,8 +399,21 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
         r.vs = p.pool.scales[1][block];
       }
     };
-    Ref cur = ask(0), nxt = ask(per);
+    auto load = [&](const Ref& r, int s) {   // this lane's page of the tile in stage s
+      const int i = lane & (ppt - 1);
+      // no page, or one outside the pool: a load from before the pool, which
+      // TMA fills with zeros; its scale 0 masks the keys
+      const int y = r.id >= 0 ? (r.id * p.pool.n_kv + r.h) * prows : -prows;
+      tma_load_2d(stage_k(s) + i * prows * 128, &p.tm[0], 0, y, &kv_full[s]);
+      tma_load_2d(stage_v(s) + i * prows * 128, &p.tm[1], 0, y, &kv_full[s]);
+    };
+    Ref cur = ask(0);
+    if (cur.id >= p.pool.n_pages) cur.id = -2;
+    // the first stages' loads go out before their scales are asked for
+    const int early = min(min(C::STAGES, per), ntiles);
+    if ((lane >> lgp) < early) load(cur, lane >> lgp);
     ask_scales(cur);
+    Ref nxt = ask(per);
     bool ok = true;
     for (int j0 = 0; ok && j0 < ntiles; j0 += per) {
       ask_scales(nxt);
@@ -387,14 +427,9 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
           break;
         }
         if ((lane >> lgp) == tt) {
-          const int i = lane & (ppt - 1);
-          // no page, or one outside the pool: a load from before the pool,
-          // which TMA fills with zeros; its scale 0 masks the keys
-          const int y = cur.id >= 0 ? (cur.id * p.pool.n_kv + cur.h) * prows : -prows;
-          tma_load_2d(stage_k(s) + i * prows * 128, &p.tm[0], 0, y, &kv_full[s]);
-          tma_load_2d(stage_v(s) + i * prows * 128, &p.tm[1], 0, y, &kv_full[s]);
-          sc[(s * 2 + 0) * AP_MAX_PPT + i] = cur.ks;
-          sc[(s * 2 + 1) * AP_MAX_PPT + i] = cur.vs;
+          if (j >= early) load(cur, s);
+          sc[(s * 2 + 0) * AP_MAX_PPT + (lane & (ppt - 1))] = cur.ks;
+          sc[(s * 2 + 1) * AP_MAX_PPT + (lane & (ppt - 1))] = cur.vs;
         }
         __syncwarp();
         if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], AP_STAGE);
@@ -423,31 +458,30 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
         return true;
       };
       bool ok = true;
-      int seg = -1, fixes = 0;
-      PageTile d = tile_at(M, p.batch, x0);
-      for (int j = 0; ok && j < ntiles; ++j) {
-        const bool first = j == 0 || d.t == 0;
-        const bool unit_last = d.t == M.tb[d.b] - 1;
-        const bool seg_last = j == ntiles - 1 || unit_last;
-        if (first) ++seg;
-        const int s = j % C::STAGES;
-        ok = wait_or_abort(&kv_full[s], (j / C::STAGES) & 1, abort_flag, p.err);
-        if (ok && first) ok = wait_or_abort(&q_full[seg & 1], (seg >> 1) & 1, abort_flag, p.err);
-        if (ok && unit_last) {
-          mbar_arrive(fix_req);
-          ok = wait_or_abort(fix_bar, (fixes++) & 1, abort_flag, p.err);
-        }
-        if (ok && j >= 2) ok = wait_or_abort(&s_free[j & 1], ((j - 2) >> 1) & 1, abort_flag, p.err);
-        if (!ok) break;
-        tc_fence_after();
+      int fixes = 0, j = 0;
+      for (int seg = 0; ok && j < ntiles; ++seg) {
+        const PageSeg sg = seg_at(j);
+        const bool fix = sg.t0 + sg.n == unit_tiles(sg.b);
+        for (int tt = 0; ok && tt < sg.n; ++tt, ++j) {
+          const int s = j % C::STAGES;
+          ok = wait_or_abort(&kv_full[s], (j / C::STAGES) & 1, abort_flag, p.err);
+          if (ok && tt == 0) ok = wait_or_abort(&q_full[seg & 1], (seg >> 1) & 1, abort_flag, p.err);
+          if (ok && fix && tt == sg.n - 1) {
+            mbar_arrive(fix_req);
+            ok = wait_or_abort(fix_bar, (fixes++) & 1, abort_flag, p.err);
+          }
+          if (ok && j >= 2) ok = wait_or_abort(&s_free[j & 1], ((j - 2) >> 1) & 1, abort_flag, p.err);
+          if (!ok) break;
+          tc_fence_after();
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)   // 32 bytes of the rows at a time
-          mma_e4m3(tmem + (j & 1) * C::NPAD, sw128_desc(smem_addr(stage_k(s)) + kk * 32, 16, 1024),
-                   sw128_desc(smem_addr(sQ + (seg & 1) * C::OP_BYTES) + kk * 32, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
-        mma_commit(&s_full[j & 1]);
-        if (seg_last) mma_commit(&q_free[seg & 1]);
-        if (j >= 1) ok = issue_pv(j - 1);
-        if (j + 1 < ntiles) d = tile_next(M, p.pool.n_kv, d);
+          for (int kk = 0; kk < 4; ++kk)   // 32 bytes of the rows at a time
+            mma_e4m3(tmem + (j & 1) * C::NPAD, sw128_desc(smem_addr(stage_k(s)) + kk * 32, 16, 1024),
+                     sw128_desc(smem_addr(sQ + (seg & 1) * C::OP_BYTES) + kk * 32, 16, 1024), idesc_qk,
+                     kk > 0 ? 1u : 0u);
+          mma_commit(&s_full[j & 1]);
+          if (tt == sg.n - 1) mma_commit(&q_free[seg & 1]);
+          if (j >= 1) ok = issue_pv(j - 1);
+        }
       }
       if (ok) issue_pv(ntiles - 1);
       // every MMA issued above must complete before TMEM is released
@@ -463,7 +497,7 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
     auto prep_q = [&](int i, const PageSeg& sg) -> bool {
       if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&q_free[i & 1], ((i - 2) >> 1) & 1, abort_flag, p.err)))
         return false;
-      const CosSin2* trow = p.tab + (size_t)p.rope_row[sg.b] * (D / 2);
+      const CosSin2* trow = p.tab + (size_t)M.rope[sg.b] * (D / 2);
       uint8_t* qb = sQ + (i & 1) * C::OP_BYTES;
 #pragma unroll
       for (int it = 0; it < (G * CH + 31) / 32; ++it) {
@@ -515,7 +549,16 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
       if (lane == 0) mbar_arrive(&q_full[i & 1]);
       return true;
     };
-    // The last tile of a unit, tile j of the CTA.  Lanes 0.. hold the new key,
+    bool ok = true;
+    for (int i = 0, j = 0; ok && j < ntiles; ++i) {
+      const PageSeg sg = seg_at(j);
+      ok = prep_q(i, sg);
+      j += sg.n;
+    }
+  } else if (warp == 7) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // ---------------- the last tile of a unit, tile j of the CTA.  Lanes 0.. hold the new key,
     // lanes 16.. the new value, 16 elements each as above.
     int fixes = 0;
     auto fixup = [&](int j, const PageSeg& sg) -> bool {
@@ -532,7 +575,7 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
       if (mine) {
         const uint4* src = reinterpret_cast<const uint4*>(p.fresh[kv] + ((size_t)sg.b * p.pool.n_kv + sg.h) * D);
         uint4 x = src[c], y = src[c + CH];
-        new_row8(x, y, kv == 0 ? p.tab + (size_t)p.rope_row[sg.b] * (D / 2) + c * 8 : nullptr, lo, hi);
+        new_row8(x, y, kv == 0 ? p.tab + (size_t)M.rope[sg.b] * (D / 2) + c * 8 : nullptr, lo, hi);
         m = max(max_finite8(lo), max_finite8(hi));
       }
 #pragma unroll
@@ -595,18 +638,11 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
       if (lane == 0) mbar_arrive(fix_bar);
       return true;
     };
-    PageSeg cur = seg_at(0);
-    bool ok = prep_q(0, cur);
-    for (int i = 0; ok; ++i) {
-      const bool more = cur.j0 + cur.n < ntiles;
-      PageSeg nxt = cur;
-      if (more) {
-        nxt = seg_at(cur.j0 + cur.n);
-        ok = prep_q(i + 1, nxt);
-      }
-      if (ok && cur.t0 + cur.n == M.tb[cur.b]) ok = fixup(cur.j0 + cur.n - 1, cur);
-      if (!more) break;
-      cur = nxt;
+    bool ok = true;
+    for (int j = 0; ok && j < ntiles;) {
+      const PageSeg sg = seg_at(j);
+      j += sg.n;
+      if (sg.t0 + sg.n == unit_tiles(sg.b)) ok = fixup(j - 1, sg);
     }
   } else {
     // ---------------- softmax and epilogue: thread tid owns row tid of each
@@ -638,7 +674,7 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
     PageSeg sg = seg_at(0);
     for (;; ++i) {
       const int nkeys = M.keys[sg.b];
-      const bool whole = sg.t0 == 0 && sg.n == M.tb[sg.b];
+      const bool whole = sg.t0 == 0 && sg.n == unit_tiles(sg.b);
       float m_ref[G], l_part[G], o_acc[G], a_prev[G];
       float v_prev = 0.f;   // V factor of the tile before
 #pragma unroll
@@ -798,7 +834,7 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
                        : "=r"(prev)
                        : "l"(p.counters + u), "r"(sg.n)
                        : "memory");
-          const bool last = prev + sg.n == M.tb[sg.b];
+          const bool last = prev + sg.n == unit_tiles(sg.b);
           if (last) p.counters[u] = 0;   // every CTA of the unit has arrived
           *last_flag = last ? 1 : 0;
           arrived = i;
@@ -806,51 +842,71 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
         if (ok) ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
         if (ok && *last_flag) {
           // ---- merge: the CTAs from the one with the unit's first tile to the
-          // one with its last; a CTA's slot is 2c, or 2c + 1 if the unit is not
-          // where its range starts.  Their order is fixed, so the result is.
-          const int64_t uf = M.start[sg.b] + (int64_t)sg.h * M.tb[sg.b];
-          const int cf = cta_of(total, uf, ctas), nctr = cta_of(total, uf + M.tb[sg.b] - 1, ctas) - cf + 1;
-          float mx[G], lt[G], ot[G];
+          // one with its last, in that order whoever merges; a CTA's slot is
+          // 2c, or 2c + 1 if the unit is not where its range starts.  A round
+          // takes kMergeRows of them: warp w turns the (m, l) of heads w, w + 4
+          // into weights, then thread tid adds up its lane of O, with the
+          // loads of C::MERGE partials in flight (the first of them since
+          // before the weights).
+          const int64_t uf = M.start[sg.b] + (int64_t)sg.h * unit_tiles(sg.b);
+          const int cf = cut.of(uf), nctr = cut.of(uf + unit_tiles(sg.b) - 1) - cf + 1;
+          const int slot0 = 2 * cf + (cut.first(cf) < uf ? 1 : 0);
+          auto slot = [&](int k) { return k == 0 ? slot0 : 2 * (cf + k); };
+          float* wts = reinterpret_cast<float*>(sP);   // [kMergeRows][G]; every PV that read P has completed
+          float* tot = red;                            // [G] (scale of what is summed so far, sum of weights)
+          float mx[(G + 3) / 4];                       // of heads warp, warp + 4
+          float lt[G], ot[G];
 #pragma unroll
-          for (int g = 0; g < G; ++g) {
-            mx[g] = -INFINITY;
-            lt[g] = 0.f;
-            ot[g] = 0.f;
-          }
-          for (int k0 = 0; k0 < nctr; k0 += C::MERGE) {
-            float mv[C::MERGE][G], lv[C::MERGE][G], ov[C::MERGE][G];
+          for (int g = 0; g < G; ++g) lt[g] = ot[g] = 0.f;
 #pragma unroll
-            for (int k = 0; k < C::MERGE; ++k) {
-              const int c = cf + k0 + k;
-              const int64_t f = cta_first(total, c, ctas);
-              const bool on = k0 + k < nctr && f < cta_first(total, c + 1, ctas);
-              const int sl = on ? 2 * c + (f < uf ? 1 : 0) : 0;
+          for (int q = 0; q < (G + 3) / 4; ++q) mx[q] = -INFINITY;
+          for (int k0 = 0; ok && k0 < nctr; k0 += kMergeRows) {
+            const int nk = min(kMergeRows, nctr - k0);
+            float ov[C::MERGE][G];
+            auto fetch = [&](int k) {
 #pragma unroll
-              for (int g = 0; g < G; ++g) {
-                const size_t r = (size_t)sl * G + g;
-                mv[k][g] = on ? __ldcg(&p.part_ml[r * 2]) : -INFINITY;
-                lv[k][g] = on ? __ldcg(&p.part_ml[r * 2 + 1]) : 0.f;
-                ov[k][g] = on ? __ldcg(&p.part_o[r * 128 + tid]) : 0.f;
+              for (int r = 0; r < C::MERGE; ++r)
+#pragma unroll
+                for (int g = 0; g < G; ++g)
+                  ov[r][g] = k + r < nk ? __ldcg(&p.part_o[((size_t)slot(k0 + k + r) * G + g) * 128 + tid]) : 0.f;
+            };
+            fetch(0);
+#pragma unroll
+            for (int q = 0; q < (G + 3) / 4; ++q) {
+              const int g = warp + 4 * q;
+              if (g >= G) break;
+              float2 a = make_float2(-INFINITY, 0.f), b = a;
+              if (lane < nk) a = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot(k0 + lane) * G + g);
+              if (lane + 32 < nk)
+                b = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot(k0 + lane + 32) * G + g);
+              const float cm = fmaxf(mx[q], warp_max(fmaxf(a.x, b.x)));
+              const float base = cm == -INFINITY ? 0.f : cm;
+              const float wa = ex2_approx(a.x - base), wb = ex2_approx(b.x - base);
+              const float sum = warp_sum(wa * a.y + wb * b.y);
+              wts[lane * G + g] = wa;
+              wts[(lane + 32) * G + g] = wb;
+              if (lane == 0) {
+                tot[2 * g] = ex2_approx(mx[q] - base);
+                tot[2 * g + 1] = sum;
               }
+              mx[q] = cm;
             }
+            ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-              float cm = mx[g];
-#pragma unroll
-              for (int k = 0; k < C::MERGE; ++k) cm = fmaxf(cm, mv[k][g]);
-              const float base = cm == -INFINITY ? 0.f : cm;
-              const float f = mx[g] == -INFINITY ? 0.f : ex2_approx(mx[g] - base);
-              lt[g] *= f;
-              ot[g] *= f;
-#pragma unroll
-              for (int k = 0; k < C::MERGE; ++k) {
-                const float w = mv[k][g] == -INFINITY ? 0.f : ex2_approx(mv[k][g] - base);
-                lt[g] = fmaf(w, lv[k][g], lt[g]);
-                ot[g] = fmaf(w, ov[k][g], ot[g]);
-              }
-              mx[g] = cm;
+              lt[g] = fmaf(lt[g], tot[2 * g], tot[2 * g + 1]);
+              ot[g] *= tot[2 * g];
             }
+            for (int k = 0; k < nk; k += C::MERGE) {
+              if (k > 0) fetch(k);
+#pragma unroll
+              for (int r = 0; r < C::MERGE; ++r)
+#pragma unroll
+                for (int g = 0; g < G; ++g) ot[g] = fmaf(wts[(k + r) * G + g], ov[r][g], ot[g]);
+            }
+            if (ok) ok = group_sync(grp_bar, k_sync, abort_flag, p.err);   // wts and tot are free again
           }
+          if (!ok) break;
           ok = write_out(sg.b, sg.h, ot, lt);
         }
       }
@@ -864,9 +920,9 @@ __global__ void __launch_bounds__(AP_THREADS, (ApCfg<D, G>::CTAS_PER_SM))
       // back at zero when the launch ends.
       PageSeg q = seg_at(0);
       for (int k = 0;; ++k) {
-        if (k > arrived && !(q.t0 == 0 && q.n == M.tb[q.b])) {
+        if (k > arrived && !(q.t0 == 0 && q.n == unit_tiles(q.b))) {
           const int prev = atomicAdd(p.counters + q.b * p.pool.n_kv + q.h, q.n);
-          if (prev + q.n == M.tb[q.b]) p.counters[q.b * p.pool.n_kv + q.h] = 0;
+          if (prev + q.n == unit_tiles(q.b)) p.counters[q.b * p.pool.n_kv + q.h] = 0;
         }
         if (q.j0 + q.n >= ntiles) break;
         q = seg_at(q.j0 + q.n);
@@ -906,7 +962,7 @@ cudaError_t launch_ap(const AttendPages8Params& p, int sms, bool overlap, cudaSt
     if (s.state[dev] != 1) return (cudaError_t)(-s.state[dev]);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(C::CTAS_PER_SM * sms);
+  cfg.gridDim = dim3(2 * sms);
   cfg.blockDim = dim3(AP_THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
