@@ -50,16 +50,17 @@ constexpr int AP_KV_BYTES = 128 * 128;          // K (or V) of one tile
 constexpr int AP_STAGE = 2 * AP_KV_BYTES;
 constexpr int AP_MAX_PPT = 16;                  // pages of a tile
 
-constexpr int kMinTiles = 4;     // tiles of a CTA below which fewer CTAs work
-constexpr int kWholeTiles = 4;   // units of at most so many tiles are not shared
+constexpr int kMinTiles = 2;     // tiles of a CTA below which fewer CTAs work
 constexpr int kMergeRows = 64;   // partials of one round of a merge
 
-// The tiles of a launch, from the device-side lengths.
+// The tiles of a launch, from the device-side lengths (fewer than 2^31, which
+// the host checks for max_keys).
 struct PageMap {
-  int64_t start[kMaxPagedSeqs + 1];   // first tile of each sequence; the last one is the total
+  int32_t start[kMaxPagedSeqs + 1];   // first tile of each sequence; the last one is the total
+  int32_t part[kMaxPagedSeqs + 1];    // split by unit: first CTA of each sequence
   int32_t keys[kMaxPagedSeqs];        // rows attended over; -1: left out
   int32_t rope[kMaxPagedSeqs];        // the sequence's row of the RoPE table
-  int32_t longest;                    // tiles of the longest unit
+  int32_t most;                       // split by unit: tiles of a part at most; 0: split evenly
 };
 
 template <int D, int G>
@@ -85,7 +86,7 @@ struct ApCfg {
   // until s_free, two units behind q_free
   static constexpr int OFF_X = OFF_QS + 4 * 8 * 4;                          // KPR == 2: [G][128] output exchange
   static constexpr int OFF_BAR = OFF_X + (KPR == 2 ? G * 128 * 4 : 0);
-  static constexpr int N_BAR = 2 * STAGES + 2 * 8 + 5;
+  static constexpr int N_BAR = 2 * STAGES + 2 * 8 + 6;
   static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;     // + slack for 1024-byte alignment
   static_assert(OP_BYTES % 1024 == 0, "swizzled operands need 1024-byte alignment");
@@ -150,17 +151,21 @@ struct PageTile {
   int32_t b, h, t;   // sequence, kv head, tile of the unit
 };
 
-__device__ __forceinline__ PageTile tile_at(const PageMap& m, int batch, int tb_shift, int64_t x) {
-  int lo = 0, hi = batch;   // the last sequence with start <= x
+// The last sequence b < batch with from[b] <= x.
+__device__ __forceinline__ int seq_of(const int32_t* from, int batch, int x) {
+  int lo = 0, hi = batch;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (m.start[mid] <= x) lo = mid;
+    if (from[mid] <= x) lo = mid;
     else hi = mid;
   }
-  const uint32_t r = (uint32_t)(x - m.start[lo]);   // below 2^30: tb <= 2^23, 128 heads
-  const uint32_t tb = (uint32_t)(m.keys[lo] - 1 >> tb_shift) + 1;
+  return lo;
+}
+
+__device__ __forceinline__ PageTile tile_at(const PageMap& m, int batch, int tile_lg, int x) {
   PageTile d;
-  d.b = lo;
+  d.b = seq_of(m.start, batch, x);
+  const uint32_t r = (uint32_t)(x - m.start[d.b]), tb = (uint32_t)((m.keys[d.b] - 1) >> tile_lg) + 1;
   d.h = (int)(r / tb);
   d.t = (int)(r % tb);
   return d;
@@ -172,18 +177,14 @@ struct PageSeg {
   int b, h, t0, j0, n;
 };
 
-// How the tiles are cut: CTA c owns [first(c), first(c + 1)).
+// An even split: CTA c owns tiles [first(c), first(c + 1)).
 struct PageCut {
-  int64_t total, base;
-  int rem, ctas;   // the first rem of the ctas working CTAs own base + 1 tiles, the others base
+  int base, rem, ctas;   // the first rem CTAs own base + 1 tiles, the others base
 
-  __device__ __forceinline__ int64_t div(int64_t a, int64_t b) const {
-    return total < INT32_MAX ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-  }
-  __device__ __forceinline__ int64_t first(int c) const { return c < ctas ? c * base + min(c, rem) : total; }
-  __device__ __forceinline__ int of(int64_t x) const {   // the CTA that owns tile x
-    const int64_t big = rem * (base + 1);
-    return (int)(x < big ? div(x, base + 1) : rem + div(x - big, base));
+  __device__ __forceinline__ int first(int c) const { return c * base + min(c, rem); }
+  __device__ __forceinline__ int of(int x) const {   // the CTA that owns tile x
+    const int big = rem * (base + 1);
+    return x < big ? (int)((uint32_t)x / (uint32_t)(base + 1)) : rem + (int)((uint32_t)(x - big) / (uint32_t)base);
   }
 };
 
@@ -212,8 +213,9 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   uint64_t* q_full = o_free + 2;
   uint64_t* q_free = q_full + 2;
   uint64_t* fix_req = q_free + 2;     // a unit's last tile has landed
-  uint64_t* fix_bar = fix_req + 1;    // and is complete: new token in, V's tail zero
-  uint64_t* grp_bar = fix_bar + 1;    // the softmax warps' group barrier
+  uint64_t* fix_k = fix_req + 1;      // the new key is in it
+  uint64_t* fix_v = fix_k + 1;        // and the new value, and V's tail is zero
+  uint64_t* grp_bar = fix_v + 1;      // the softmax warps' group barrier
   uint64_t* mma_done = grp_bar + 1;   // every MMA of the CTA has completed
   uint64_t* never = mma_done + 1;     // test hook: nothing arrives
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
@@ -230,15 +232,21 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   if (warp == 0) {
     // The map, 32 sequences at a time: lengths, table rows, page table and held
     // rows are what the previous kernel does not write, so this does not wait.
-    int64_t at = 0;
-    int longest = 0;
+    int at = 0;
     bool bad = false, none = false;
-    for (int b0 = 0; b0 < kMaxPagedSeqs; b0 += 32) {
-      const int b = b0 + lane;
-      if (b0 >= p.batch) {   // nothing behind the batch
-        M.start[b] = at;
-        continue;
+    auto scan = [&](int v, int& sum) {   // exclusive prefix over the warp on top of sum, which takes the total
+      int incl = v;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += o;
       }
+      const int before = sum + incl - v;
+      sum += __shfl_sync(0xffffffffu, incl, 31);
+      return before;
+    };
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const int b = b0 + lane;
       int32_t n = -1, rr = 0, keys = -1;
       if (b < p.batch) {
         n = p.n_cached[b];
@@ -251,24 +259,39 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       none |= keys == 0;
       M.keys[b] = keys;
       M.rope[b] = rr;
-      const int tb = keys > 0 ? ((keys - 1) >> C::TILE_LG) + 1 : 0;
-      longest = max(longest, tb);
-      const int64_t mine = (int64_t)tb * p.pool.n_kv;
-      int64_t incl = mine;
-#pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int64_t o = __shfl_up_sync(0xffffffffu, incl, off);
-        if (lane >= off) incl += o;
-      }
-      M.start[b] = at + incl - mine;
-      at += __shfl_sync(0xffffffffu, incl, 31);
+      M.start[b] = scan((((keys - 1) >> C::TILE_LG) + 1) * p.pool.n_kv, at);
     }
-    longest = __reduce_max_sync(0xffffffffu, longest);
+    // Split by unit where there are CTAs enough: every unit in parts of at most
+    // `most` tiles, so that no CTA works on two units and waits for the end of
+    // one before it goes on.  `most` is the smallest that the CTAs suffice for;
+    // where that is over 1.5 times an even share (units of very different
+    // lengths), an even split it is.
+    int most = 0;
+    if (p.batch * p.pool.n_kv <= ctas && at > 0) {
+      const int even = (at + ctas - 1) / ctas;
+      for (int t = max(even, kMinTiles); most == 0 && t <= even + even / 2 + kMinTiles; t += 1 + t / 16) {
+        int parts = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+          const int tb = b0 + lane < p.batch ? ((M.keys[b0 + lane] - 1) >> C::TILE_LG) + 1 : 0;
+          parts += __reduce_add_sync(0xffffffffu, (tb + t - 1) / t);
+        }
+        if (parts * p.pool.n_kv <= ctas) most = t;
+      }
+      if (most > 0) {
+        int sum = 0;
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+          const int tb = b0 + lane < p.batch ? ((M.keys[b0 + lane] - 1) >> C::TILE_LG) + 1 : 0;
+          const int first = scan((tb + most - 1) / most * p.pool.n_kv, sum);
+          M.part[b0 + lane] = first;
+        }
+        if (lane == 0) M.part[kMaxPagedSeqs] = sum;
+      }
+    }
     bad = __any_sync(0xffffffffu, bad);
     none = __any_sync(0xffffffffu, none);
     if (lane == 0) {
       M.start[kMaxPagedSeqs] = at;
-      M.longest = longest;
+      M.most = most;
       *none_flag = none;
       if (bad && cta == 0) atomicOr(p.err, kErrLength);
     }
@@ -295,7 +318,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         mbar_init(&q_free[i], 1);
       }
       mbar_init(fix_req, 1);
-      mbar_init(fix_bar, 1);
+      mbar_init(fix_k, 1);
+      mbar_init(fix_v, 1);
       mbar_init(grp_bar, 4);
       mbar_init(mma_done, 1);
       mbar_init(never, 1);
@@ -313,26 +337,24 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   auto unit_tiles = [&](int b) { return ((M.keys[b] - 1) >> C::TILE_LG) + 1; };   // 0 for -1 and 0 keys
+  const int total = M.start[kMaxPagedSeqs], most = M.most;
   PageCut cut;
-  cut.total = M.start[kMaxPagedSeqs];
-  int64_t x0, x1;
-  if (M.longest <= kWholeTiles && p.batch * p.pool.n_kv <= ctas) {
-    // one short unit to a CTA: nothing to merge
-    const int b = cta / p.pool.n_kv;
-    cut.ctas = 0;
-    x0 = x1 = 0;
-    if (b < p.batch) {
-      x0 = M.start[b] + (int64_t)(cta % p.pool.n_kv) * unit_tiles(b);
-      x1 = x0 + unit_tiles(b);
+  int x0 = 0, x1 = 0;
+  if (most > 0) {
+    if (cta < M.part[kMaxPagedSeqs]) {
+      const int b = seq_of(M.part, p.batch, cta), tb = unit_tiles(b), parts = (tb + most - 1) / most;
+      const int r = cta - M.part[b], h = r / parts, i = r - h * parts;
+      x0 = M.start[b] + h * tb + (int)((uint32_t)i * (uint32_t)tb / (uint32_t)parts);
+      x1 = M.start[b] + h * tb + (int)((uint32_t)(i + 1) * (uint32_t)tb / (uint32_t)parts);
     }
   } else {
-    cut.ctas = (int)min((int64_t)ctas, max((int64_t)1, cut.div(cut.total, kMinTiles)));
-    cut.base = cut.div(cut.total, cut.ctas);
-    cut.rem = (int)(cut.total - cut.base * cut.ctas);
-    x0 = cut.first(cta);
-    x1 = cut.first(cta + 1);
+    cut.ctas = min(ctas, max(1, total / kMinTiles));
+    cut.base = total / cut.ctas;
+    cut.rem = total - cut.base * cut.ctas;
+    x0 = min(total, cut.first(cta));
+    x1 = min(total, cut.first(cta + 1));
   }
-  const int ntiles = (int)(x1 - x0);
+  const int ntiles = x1 - x0;
   if (warp == 4 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.tm[lane]) : "memory");
   if (*none_flag) {
     // sequences without a row: their output is zero
@@ -407,13 +429,11 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       tma_load_2d(stage_k(s) + i * prows * 128, &p.tm[0], 0, y, &kv_full[s]);
       tma_load_2d(stage_v(s) + i * prows * 128, &p.tm[1], 0, y, &kv_full[s]);
     };
-    Ref cur = ask(0);
-    if (cur.id >= p.pool.n_pages) cur.id = -2;
-    // the first stages' loads go out before their scales are asked for
-    const int early = min(min(C::STAGES, per), ntiles);
-    if ((lane >> lgp) < early) load(cur, lane >> lgp);
+    // The scales' reads go out ahead of the loads: they would wait behind the
+    // megabytes that all CTAs ask for at once.  A tile is announced before the
+    // next one is asked for, since the TMA queue holds a few loads only.
+    Ref cur = ask(0), nxt = ask(per);
     ask_scales(cur);
-    Ref nxt = ask(per);
     bool ok = true;
     for (int j0 = 0; ok && j0 < ntiles; j0 += per) {
       ask_scales(nxt);
@@ -427,7 +447,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           break;
         }
         if ((lane >> lgp) == tt) {
-          if (j >= early) load(cur, s);
+          load(cur, s);
           sc[(s * 2 + 0) * AP_MAX_PPT + (lane & (ppt - 1))] = cur.ks;
           sc[(s * 2 + 1) * AP_MAX_PPT + (lane & (ppt - 1))] = cur.vs;
         }
@@ -443,8 +463,15 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       // ---------------- MMA issuer
       constexpr uint32_t idesc_qk = idesc_e4m3_m128(C::NPAD, false);   // A = K (K-major), B = query (K-major)
       constexpr uint32_t idesc_pv = idesc_e4m3_m128(C::NPAD, true);    // A = V^T (MN-major), B = P^T (K-major)
-      auto issue_pv = [&](int i) -> bool {
+      int fixes = 0, fixed_v = 0;   // last tiles asked for; those whose V is known to be complete
+      auto v_fixed = [&](int n) -> bool {
+        for (; fixed_v < n; ++fixed_v)
+          if (!wait_or_abort(fix_v, fixed_v & 1, abort_flag, p.err)) return false;
+        return true;
+      };
+      auto issue_pv = [&](int i, int n_fixes) -> bool {   // n_fixes: the last tiles up to tile i
         const int pb = i & 1, s = i % C::STAGES;
+        if (!v_fixed(n_fixes)) return false;
         if (!wait_or_abort(&p_full[pb], (i >> 1) & 1, abort_flag, p.err)) return false;
         if (i >= 2 && !wait_or_abort(&o_free[pb], ((i - 2) >> 1) & 1, abort_flag, p.err)) return false;
         tc_fence_after();
@@ -458,17 +485,18 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         return true;
       };
       bool ok = true;
-      int fixes = 0, j = 0;
+      int j = 0;
       for (int seg = 0; ok && j < ntiles; ++seg) {
         const PageSeg sg = seg_at(j);
         const bool fix = sg.t0 + sg.n == unit_tiles(sg.b);
         for (int tt = 0; ok && tt < sg.n; ++tt, ++j) {
-          const int s = j % C::STAGES;
+          const int s = j % C::STAGES, before = fixes;
           ok = wait_or_abort(&kv_full[s], (j / C::STAGES) & 1, abort_flag, p.err);
           if (ok && tt == 0) ok = wait_or_abort(&q_full[seg & 1], (seg >> 1) & 1, abort_flag, p.err);
+          if (ok && fix && tt == sg.n - 1) ok = v_fixed(fixes);   // one at a time
           if (ok && fix && tt == sg.n - 1) {
             mbar_arrive(fix_req);
-            ok = wait_or_abort(fix_bar, (fixes++) & 1, abort_flag, p.err);
+            ok = wait_or_abort(fix_k, (fixes++) & 1, abort_flag, p.err);
           }
           if (ok && j >= 2) ok = wait_or_abort(&s_free[j & 1], ((j - 2) >> 1) & 1, abort_flag, p.err);
           if (!ok) break;
@@ -480,10 +508,10 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
                      kk > 0 ? 1u : 0u);
           mma_commit(&s_full[j & 1]);
           if (tt == sg.n - 1) mma_commit(&q_free[seg & 1]);
-          if (j >= 1) ok = issue_pv(j - 1);
+          if (j >= 1) ok = issue_pv(j - 1, before);
         }
       }
-      if (ok) issue_pv(ntiles - 1);
+      if (ok) issue_pv(ntiles - 1, fixes);
       // every MMA issued above must complete before TMEM is released
       mma_commit(mma_done);
       mbar_wait(mma_done, 0);
@@ -590,6 +618,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         return tile + row * 128 + (((b >> 4) ^ (row & 7)) << 4) + (b & 8);
       };
       const size_t block = in ? (size_t)id * p.pool.n_kv + sg.h : 0;
+      int grow[2] = {0, 0};
       if (p.has_new && in) {   // uniform over the warp
         float* scs = sc + (s * 2 + kv) * AP_MAX_PPT + pi;
         int e = scale_exponent(m), e_old = e;
@@ -612,30 +641,35 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
             p.pool.scales[kv][block] = pow2_float(e);
           }
         }
-        // a larger scale: the page's earlier codes follow (rare)
-#pragma unroll 1
-        for (int k = 0; k < 2; ++k) {
-          const int d_e = __shfl_sync(0xffffffffu, e_old - e, k * 16);
-          if (d_e >= 0) continue;
-          const float by = pow2_float(max(d_e, -100));
-          uint8_t* t = k == 0 ? stage_k(s) : stage_v(s);
-          for (int i = lane; i < pl * CH; i += 32) {
-            const int key = i / CH, byte = i % CH * 16;
-            uint4* u = reinterpret_cast<uint4*>(place(t, at - pl + key, byte));
-            const uint4 r = make_uint4(rescale4(u->x, by), rescale4(u->y, by), rescale4(u->z, by), rescale4(u->w, by));
-            *u = r;
-            *reinterpret_cast<uint4*>(p.pool.codes[k] + (block * page + key) * D + byte) = r;
-          }
-        }
+        grow[0] = __shfl_sync(0xffffffffu, e_old - e, 0);
+        grow[1] = __shfl_sync(0xffffffffu, e_old - e, 16);
       }
-      for (int i = lane; i < (page - 1 - pl) * CH; i += 32)
-        *reinterpret_cast<uint4*>(place(stage_v(s), at + 1 + i / CH, i % CH * 16)) = make_uint4(0, 0, 0, 0);
+      // a larger scale: the page's earlier codes follow (rare)
+      auto rescale = [&](int k) {
+        const float by = pow2_float(max(grow[k], -100));
+        uint8_t* t = k == 0 ? stage_k(s) : stage_v(s);
+#pragma unroll 1
+        for (int i = lane; i < pl * CH; i += 32) {
+          const int key = i / CH, byte = i % CH * 16;
+          uint4* u = reinterpret_cast<uint4*>(place(t, at - pl + key, byte));
+          const uint4 r = make_uint4(rescale4(u->x, by), rescale4(u->y, by), rescale4(u->z, by), rescale4(u->w, by));
+          *u = r;
+          *reinterpret_cast<uint4*>(p.pool.codes[k] + (block * page + key) * D + byte) = r;
+        }
+      };
+      if (grow[0] < 0) rescale(0);
       // the other key of the last row of K would reach this one's score
       if (KPR == 2 && (pl & 1) == 0 && lane < CH)
         *reinterpret_cast<uint4*>(place(stage_k(s), at + 1, lane * 16)) = make_uint4(0, 0, 0, 0);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(fix_bar);
+      if (lane == 0) mbar_arrive(fix_k);
+      if (grow[1] < 0) rescale(1);
+      for (int i = lane; i < (page - 1 - pl) * CH; i += 32)
+        *reinterpret_cast<uint4*>(place(stage_v(s), at + 1 + i / CH, i % CH * 16)) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(fix_v);
       return true;
     };
     bool ok = true;
@@ -848,9 +882,17 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           // into weights, then thread tid adds up its lane of O, with the
           // loads of C::MERGE partials in flight (the first of them since
           // before the weights).
-          const int64_t uf = M.start[sg.b] + (int64_t)sg.h * unit_tiles(sg.b);
-          const int cf = cut.of(uf), nctr = cut.of(uf + unit_tiles(sg.b) - 1) - cf + 1;
-          const int slot0 = 2 * cf + (cut.first(cf) < uf ? 1 : 0);
+          const int tb = unit_tiles(sg.b), uf = M.start[sg.b] + sg.h * tb;
+          int cf, nctr, slot0;
+          if (most > 0) {
+            nctr = (tb + most - 1) / most;
+            cf = M.part[sg.b] + sg.h * nctr;
+            slot0 = 2 * cf;
+          } else {
+            cf = cut.of(uf);
+            nctr = cut.of(uf + tb - 1) - cf + 1;
+            slot0 = 2 * cf + (cut.first(cf) < uf ? 1 : 0);
+          }
           auto slot = [&](int k) { return k == 0 ? slot0 : 2 * (cf + k); };
           float* wts = reinterpret_cast<float*>(sP);   // [kMergeRows][G]; every PV that read P has completed
           float* tot = red;                            // [G] (scale of what is summed so far, sum of weights)
