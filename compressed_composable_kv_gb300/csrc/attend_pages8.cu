@@ -30,10 +30,10 @@
 // tiles complete the unit's counter merges them.
 //
 // Roles: warps 0-3 softmax and epilogue (thread t owns row t of a tile, then
-// lane t of O^T), warp 4 page ids, scales and TMA, warp 5 MMA, warp 6 the
-// rotated query of each unit, warp 7 the last tile of a unit: the new token,
-// and zeros in V's places behind it (they may hold any bits, NaN among them,
-// and 0 * NaN would reach the sum).
+// lane t of O^T), warp 4 K's pages and the scales, warp 5 MMA, warp 6 the
+// rotated query of each unit, warp 7 V's pages and the last tile of a unit:
+// the new token, and zeros in V's places behind it (they may hold any bits,
+// NaN among them, and 0 * NaN would reach the sum).
 #include <float.h>
 
 #include "pages8.h"
@@ -86,7 +86,7 @@ struct ApCfg {
   // until s_free, two units behind q_free
   static constexpr int OFF_X = OFF_QS + 4 * 8 * 4;                          // KPR == 2: [G][128] output exchange
   static constexpr int OFF_BAR = OFF_X + (KPR == 2 ? G * 128 * 4 : 0);
-  static constexpr int N_BAR = 2 * STAGES + 2 * 8 + 6;
+  static constexpr int N_BAR = 5 * STAGES + 2 * 8 + 2;
   static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;     // + slack for 1024-byte alignment
   static_assert(OP_BYTES % 1024 == 0, "swizzled operands need 1024-byte alignment");
@@ -147,6 +147,37 @@ __device__ __forceinline__ void split3(float a, float b, uint32_t (&out)[3]) {
   out[2] = e4m3x2((a - f.x) * 32.f, (b - f.y) * 32.f);
 }
 
+// Bounded wait that gives up once another thread has aborted the CTA.  Waiting
+// is kept out of line: the kernel's loops have to stay in the instruction cache.
+__device__ __noinline__ bool slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+  return wait_or_abort(bar, parity, abort_flag, err);
+}
+__device__ __forceinline__ bool ap_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+  return mbar_try_wait(bar, parity) || slow_wait(bar, parity, abort_flag, err);
+}
+
+// Barrier of the softmax warps (all of them reach it on every path, their
+// waits being bounded); true if any thread brings `failed`.
+__device__ __forceinline__ bool softmax_sync(bool failed) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.or.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(failed ? 1u : 0u)
+      : "memory");
+  return any != 0;
+}
+
+// Max over the warp; a NaN is passed over.
+__device__ __forceinline__ float warp_max_f32(float v) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
+
 struct PageTile {
   int32_t b, h, t;   // sequence, kv head, tile of the unit
 };
@@ -202,8 +233,11 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   float* sc = reinterpret_cast<float*>(smem + C::OFF_SC);
   float* qs = reinterpret_cast<float*>(smem + C::OFF_QS);
   float* xo = reinterpret_cast<float*>(smem + C::OFF_X);
-  uint64_t* kv_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
-  uint64_t* kv_empty = kv_full + C::STAGES;
+  uint64_t* k_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+  uint64_t* v_full = k_full + C::STAGES;
+  uint64_t* fix_k = v_full + C::STAGES;    // a unit's last tile: the new key is in it
+  uint64_t* fix_v = fix_k + C::STAGES;     // and the new value, and V's tail is zero
+  uint64_t* kv_empty = fix_v + C::STAGES;
   uint64_t* s_full = kv_empty + C::STAGES;
   uint64_t* s_free = s_full + 2;
   uint64_t* p_full = s_free + 2;
@@ -212,11 +246,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   uint64_t* o_free = o_full + 2;
   uint64_t* q_full = o_free + 2;
   uint64_t* q_free = q_full + 2;
-  uint64_t* fix_req = q_free + 2;     // a unit's last tile has landed
-  uint64_t* fix_k = fix_req + 1;      // the new key is in it
-  uint64_t* fix_v = fix_k + 1;        // and the new value, and V's tail is zero
-  uint64_t* grp_bar = fix_v + 1;      // the softmax warps' group barrier
-  uint64_t* mma_done = grp_bar + 1;   // every MMA of the CTA has completed
+  uint64_t* mma_done = q_free + 2;    // every MMA of the CTA has completed
   uint64_t* never = mma_done + 1;     // test hook: nothing arrives
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
@@ -304,23 +334,22 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   } else if (warp == 5) {
     if (lane == 0) {
       for (int s = 0; s < C::STAGES; ++s) {
-        mbar_init(&kv_full[s], 1);
+        mbar_init(&k_full[s], 1);
+        mbar_init(&v_full[s], 1);
+        mbar_init(&fix_k[s], 1);
+        mbar_init(&fix_v[s], 1);
         mbar_init(&kv_empty[s], 1);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s_full[i], 1);
-        mbar_init(&s_free[i], AP_SM_THREADS);
-        mbar_init(&p_full[i], AP_SM_THREADS);
+        mbar_init(&s_free[i], 4);   // one arrival per softmax warp
+        mbar_init(&p_full[i], 4);
         mbar_init(&p_free[i], 1);
         mbar_init(&o_full[i], 1);
-        mbar_init(&o_free[i], AP_SM_THREADS);
+        mbar_init(&o_free[i], 4);
         mbar_init(&q_full[i], 1);
         mbar_init(&q_free[i], 1);
       }
-      mbar_init(fix_req, 1);
-      mbar_init(fix_k, 1);
-      mbar_init(fix_v, 1);
-      mbar_init(grp_bar, 4);
       mbar_init(mma_done, 1);
       mbar_init(never, 1);
       *abort_flag = 0;
@@ -383,15 +412,19 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   const int page = p.pool.page;
   const int lg = 31 - __clz(page);            // log2 of the page
   const int prows = page / KPR;               // rows of 128 bytes of a page
-  int issued = 0;                             // the TMA warp's count of tiles requested
+  int issued = 0;                             // a loading warp's count of tiles requested
 
-  if (warp == 4) {
-    // ---------------- page ids, scales and TMA.  The pages of the CTA's tiles,
-    // laid end to end, are taken 32 at a time, one to a lane: while a batch is
-    // loaded, the scales of the next and the ids of the one after are on their
-    // way (two dependent reads, about a microsecond).
-    const int lgp = (31 - __clz(C::TILE_KEYS)) - lg;   // log2 of a tile's pages
+  // ---------------- the loads of K (kv 0, with the scales of both) or V (kv 1)
+  // of every tile.  The pages of the CTA's tiles, laid end to end, are taken 32
+  // at a time, one to a lane: while a batch is loaded, the scales of the next
+  // and the ids of the one after are on their way (two dependent reads, about
+  // a microsecond).  K and V have a warp each: a warp issues a TMA load in about
+  // 140 cycles whatever its size, so one warp with 16-token pages (16 loads a
+  // tile) was what bounded the kernel.  before(j) runs before tile j is asked for.
+  auto load_tiles = [&](int kv, auto&& before) -> bool {
+    const int lgp = C::TILE_LG - lg;                   // log2 of a tile's pages
     const int ppt = 1 << lgp, per = 32 >> lgp;         // pages of a tile, tiles of a batch
+    uint64_t* full = kv == 0 ? k_full : v_full;
     struct Ref {
       int32_t id, h;   // id: -1 no page here, -2 outside the pool
       float ks, vs;
@@ -400,6 +433,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       Ref r;
       r.id = -1;
       r.h = 0;
+      r.ks = r.vs = 0.f;
       const int j = batch0 + (lane >> lgp);
       if (j < ntiles) {
         const PageTile d = tile_at(M, p.batch, C::TILE_LG, x0 + j);
@@ -413,67 +447,64 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       return r;
     };
     auto ask_scales = [&](Ref& r) {
-      r.ks = r.vs = 0.f;
       if (r.id >= p.pool.n_pages) r.id = -2;
-      if (r.id >= 0) {
+      if (r.id >= 0 && kv == 0) {
         const size_t block = (size_t)r.id * p.pool.n_kv + r.h;
         r.ks = p.pool.scales[0][block];
         r.vs = p.pool.scales[1][block];
       }
     };
-    auto load = [&](const Ref& r, int s) {   // this lane's page of the tile in stage s
-      const int i = lane & (ppt - 1);
-      // no page, or one outside the pool: a load from before the pool, which
-      // TMA fills with zeros; its scale 0 masks the keys
-      const int y = r.id >= 0 ? (r.id * p.pool.n_kv + r.h) * prows : -prows;
-      tma_load_2d(stage_k(s) + i * prows * 128, &p.tm[0], 0, y, &kv_full[s]);
-      tma_load_2d(stage_v(s) + i * prows * 128, &p.tm[1], 0, y, &kv_full[s]);
-    };
     // The scales' reads go out ahead of the loads: they would wait behind the
-    // megabytes that all CTAs ask for at once.  A tile is announced before the
-    // next one is asked for, since the TMA queue holds a few loads only.
+    // megabytes that all CTAs ask for at once.
     Ref cur = ask(0), nxt = ask(per);
     ask_scales(cur);
-    bool ok = true;
-    for (int j0 = 0; ok && j0 < ntiles; j0 += per) {
+    for (int j0 = 0; j0 < ntiles; j0 += per) {
       ask_scales(nxt);
       const Ref third = ask(j0 + 2 * per);
-      if (cur.id == -2) atomicOr(p.err, kErrLength);
-      for (int tt = 0; ok && tt < per && j0 + tt < ntiles; ++tt) {
-        const int j = j0 + tt, s = j % C::STAGES;
+      if (kv == 0 && cur.id == -2) atomicOr(p.err, kErrLength);
+      for (int tt = 0; tt < per && j0 + tt < ntiles; ++tt) {
+        const int j = j0 + tt, s = j % C::STAGES, i = lane & (ppt - 1);
+        if (!before(j)) return false;
         if (j >= C::STAGES &&
-            !__all_sync(0xffffffffu, wait_or_abort(&kv_empty[s], ((j - C::STAGES) / C::STAGES) & 1, abort_flag, p.err))) {
-          ok = false;
-          break;
-        }
+            !__all_sync(0xffffffffu, ap_wait(&kv_empty[s], ((j - C::STAGES) / C::STAGES) & 1, abort_flag, p.err)))
+          return false;
         if ((lane >> lgp) == tt) {
-          load(cur, s);
-          sc[(s * 2 + 0) * AP_MAX_PPT + (lane & (ppt - 1))] = cur.ks;
-          sc[(s * 2 + 1) * AP_MAX_PPT + (lane & (ppt - 1))] = cur.vs;
+          // no page, or one outside the pool: a load from before the pool, which
+          // TMA fills with zeros; its scale 0 masks the keys
+          const int y = cur.id >= 0 ? (cur.id * p.pool.n_kv + cur.h) * prows : -prows;
+          tma_load_2d((kv == 0 ? stage_k(s) : stage_v(s)) + i * prows * 128, &p.tm[kv], 0, y, &full[s]);
+          if (kv == 0) {
+            sc[(s * 2 + 0) * AP_MAX_PPT + i] = cur.ks;
+            sc[(s * 2 + 1) * AP_MAX_PPT + i] = cur.vs;
+          }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&kv_full[s], AP_STAGE);
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], AP_KV_BYTES);
         ++issued;
       }
       cur = nxt;
       nxt = third;
     }
+    return true;
+  };
+
+  if (warp == 4) {
+    load_tiles(0, [](int) { return true; });
   } else if (warp == 5) {
     if (lane == 0) {
       // ---------------- MMA issuer
       constexpr uint32_t idesc_qk = idesc_e4m3_m128(C::NPAD, false);   // A = K (K-major), B = query (K-major)
       constexpr uint32_t idesc_pv = idesc_e4m3_m128(C::NPAD, true);    // A = V^T (MN-major), B = P^T (K-major)
-      int fixes = 0, fixed_v = 0;   // last tiles asked for; those whose V is known to be complete
-      auto v_fixed = [&](int n) -> bool {
-        for (; fixed_v < n; ++fixed_v)
-          if (!wait_or_abort(fix_v, fixed_v & 1, abort_flag, p.err)) return false;
-        return true;
-      };
-      auto issue_pv = [&](int i, int n_fixes) -> bool {   // n_fixes: the last tiles up to tile i
+      uint32_t fix_par = 0;   // phase of each stage's fix barriers
+      auto issue_pv = [&](int i, bool last_tile) -> bool {
         const int pb = i & 1, s = i % C::STAGES;
-        if (!v_fixed(n_fixes)) return false;
-        if (!wait_or_abort(&p_full[pb], (i >> 1) & 1, abort_flag, p.err)) return false;
-        if (i >= 2 && !wait_or_abort(&o_free[pb], ((i - 2) >> 1) & 1, abort_flag, p.err)) return false;
+        if (!ap_wait(&v_full[s], (i / C::STAGES) & 1, abort_flag, p.err)) return false;
+        if (last_tile) {
+          if (!ap_wait(&fix_v[s], (fix_par >> s) & 1, abort_flag, p.err)) return false;
+          fix_par ^= 1u << s;
+        }
+        if (!ap_wait(&p_full[pb], (i >> 1) & 1, abort_flag, p.err)) return false;
+        if (i >= 2 && !ap_wait(&o_free[pb], ((i - 2) >> 1) & 1, abort_flag, p.err)) return false;
         tc_fence_after();
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)   // 32 rows of V at a time
@@ -484,21 +515,18 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         mma_commit(&o_full[pb]);
         return true;
       };
-      bool ok = true;
+      bool ok = true, before = false;   // before: tile j - 1 is the last of its unit
       int j = 0;
       for (int seg = 0; ok && j < ntiles; ++seg) {
         const PageSeg sg = seg_at(j);
-        const bool fix = sg.t0 + sg.n == unit_tiles(sg.b);
+        const bool ends = sg.t0 + sg.n == unit_tiles(sg.b);
         for (int tt = 0; ok && tt < sg.n; ++tt, ++j) {
-          const int s = j % C::STAGES, before = fixes;
-          ok = wait_or_abort(&kv_full[s], (j / C::STAGES) & 1, abort_flag, p.err);
-          if (ok && tt == 0) ok = wait_or_abort(&q_full[seg & 1], (seg >> 1) & 1, abort_flag, p.err);
-          if (ok && fix && tt == sg.n - 1) ok = v_fixed(fixes);   // one at a time
-          if (ok && fix && tt == sg.n - 1) {
-            mbar_arrive(fix_req);
-            ok = wait_or_abort(fix_k, (fixes++) & 1, abort_flag, p.err);
-          }
-          if (ok && j >= 2) ok = wait_or_abort(&s_free[j & 1], ((j - 2) >> 1) & 1, abort_flag, p.err);
+          const int s = j % C::STAGES;
+          const bool last_tile = ends && tt == sg.n - 1;
+          ok = ap_wait(&k_full[s], (j / C::STAGES) & 1, abort_flag, p.err);
+          if (ok && tt == 0) ok = ap_wait(&q_full[seg & 1], (seg >> 1) & 1, abort_flag, p.err);
+          if (ok && last_tile) ok = ap_wait(&fix_k[s], (fix_par >> s) & 1, abort_flag, p.err);
+          if (ok && j >= 2) ok = ap_wait(&s_free[j & 1], ((j - 2) >> 1) & 1, abort_flag, p.err);
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
@@ -509,9 +537,10 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           mma_commit(&s_full[j & 1]);
           if (tt == sg.n - 1) mma_commit(&q_free[seg & 1]);
           if (j >= 1) ok = issue_pv(j - 1, before);
+          before = last_tile;
         }
       }
-      if (ok) issue_pv(ntiles - 1, fixes);
+      if (ok) issue_pv(ntiles - 1, before);
       // every MMA issued above must complete before TMEM is released
       mma_commit(mma_done);
       mbar_wait(mma_done, 0);
@@ -523,7 +552,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     // over a power of two that brings its largest element into (224, 448], in
     // three parts.  Item (g, c): elements 8c.. and D/2 + 8c.. of head g.
     auto prep_q = [&](int i, const PageSeg& sg) -> bool {
-      if (i >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&q_free[i & 1], ((i - 2) >> 1) & 1, abort_flag, p.err)))
+      if (i >= 2 && !__all_sync(0xffffffffu, ap_wait(&q_free[i & 1], ((i - 2) >> 1) & 1, abort_flag, p.err)))
         return false;
       const CosSin2* trow = p.tab + (size_t)M.rope[sg.b] * (D / 2);
       uint8_t* qb = sQ + (i & 1) * C::OP_BYTES;
@@ -584,34 +613,36 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       j += sg.n;
     }
   } else if (warp == 7) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // ---------------- the last tile of a unit, tile j of the CTA.  Lanes 0.. hold the new key,
-    // lanes 16.. the new value, 16 elements each as above.
-    int fixes = 0;
-    auto fixup = [&](int j, const PageSeg& sg) -> bool {
-      const int s = j % C::STAGES;
-      const int n = M.keys[sg.b] - 1;                       // the last row
-      const int at = n - (sg.t0 + (j - sg.j0)) * C::TILE_KEYS;   // its key in the tile
-      const int pi = at >> lg, pl = n & (page - 1);         // its page of the tile, its place there
-      const int id = p.page_table[(size_t)sg.b * p.max_pages + (n >> lg)];
-      const bool in = id >= 0 && id < p.pool.n_pages;
-      const int kv = lane >> 4, c = lane & 15;
-      const bool mine = p.has_new && in && c < CH;
-      float lo[8], hi[8];
-      uint32_t m = 0;
-      if (mine) {
+    // ---------------- V's loads, and the last tile of a unit, tile j of the CTA.
+    // Lanes 0.. hold the new key, lanes 16.. the new value, 16 elements each
+    // as in prep_q.
+    const int kv = lane >> 4, c = lane & 15;
+    float lo[8], hi[8];   // this lane's part of the new row of the unit whose turn is next
+    uint32_t m = 0;       // bits of its largest magnitude, over the 16 lanes of K or V
+    int id = -1;          // and its page
+    auto ask_row = [&](const PageSeg& sg) {
+      id = p.page_table[(size_t)sg.b * p.max_pages + ((M.keys[sg.b] - 1) >> lg)];
+      m = 0;
+      if (p.has_new && c < CH) {
         const uint4* src = reinterpret_cast<const uint4*>(p.fresh[kv] + ((size_t)sg.b * p.pool.n_kv + sg.h) * D);
-        uint4 x = src[c], y = src[c + CH];
+        const uint4 x = src[c], y = src[c + CH];
         new_row8(x, y, kv == 0 ? p.tab + (size_t)M.rope[sg.b] * (D / 2) + c * 8 : nullptr, lo, hi);
         m = max(max_finite8(lo), max_finite8(hi));
       }
 #pragma unroll
       for (int off = 8; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
-      // The request comes once the tile has landed, so the stage's current
-      // fill is this tile's and its wait below returns at once.
-      if (!__all_sync(0xffffffffu, wait_or_abort(fix_req, (fixes++) & 1, abort_flag, p.err))) return false;
-      if (!__all_sync(0xffffffffu, wait_or_abort(&kv_full[s], (j / C::STAGES) & 1, abort_flag, p.err))) return false;
+    };
+    auto fixup = [&](int j, const PageSeg& sg) -> bool {
+      const int s = j % C::STAGES;
+      const int n = M.keys[sg.b] - 1;                            // the last row
+      const int at = n - (sg.t0 + (j - sg.j0)) * C::TILE_KEYS;   // its key in the tile
+      const int pi = at >> lg, pl = n & (page - 1);              // its page of the tile, its place there
+      const bool in = id >= 0 && id < p.pool.n_pages;
+      const bool mine = p.has_new && in && c < CH;
+      // this warp has asked for V's part of the tile, so the stage's phases are
+      // this tile's
+      if (!__all_sync(0xffffffffu, ap_wait(&k_full[s], (j / C::STAGES) & 1, abort_flag, p.err))) return false;
+      if (!__all_sync(0xffffffffu, ap_wait(&v_full[s], (j / C::STAGES) & 1, abort_flag, p.err))) return false;
       // byte `byte` (a multiple of 8) of key `key` of the tile
       auto place = [&](uint8_t* tile, int key, int byte) {
         const int row = key / KPR, b = key % KPR * D + byte;
@@ -663,21 +694,39 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         *reinterpret_cast<uint4*>(place(stage_k(s), at + 1, lane * 16)) = make_uint4(0, 0, 0, 0);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(fix_k);
+      if (lane == 0) mbar_arrive(&fix_k[s]);
       if (grow[1] < 0) rescale(1);
       for (int i = lane; i < (page - 1 - pl) * CH; i += 32)
         *reinterpret_cast<uint4*>(place(stage_v(s), at + 1 + i / CH, i % CH * 16)) = make_uint4(0, 0, 0, 0);
       fence_proxy_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(fix_v);
+      if (lane == 0) mbar_arrive(&fix_v[s]);
       return true;
     };
-    bool ok = true;
-    for (int j = 0; ok && j < ntiles;) {
-      const PageSeg sg = seg_at(j);
-      j += sg.n;
-      if (sg.t0 + sg.n == unit_tiles(sg.b)) ok = fixup(j - 1, sg);
-    }
+    // Tile t's stage is free for tile t + STAGES once PV(t) has run, so nothing
+    // waits for this warp while it completes tile t before it asks for V of tile
+    // t + STAGES - 1.
+    PageSeg next = seg_at(0);
+    bool ready = false, done = false;
+    auto fix_to = [&](int t) -> bool {   // the units' last tiles up to tile t
+      if (t < 0) return true;            // the first stages' loads come first
+      if (!ready) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        ask_row(next);
+        ready = true;
+      }
+      while (!done && next.j0 + next.n - 1 <= t) {
+        if (next.t0 + next.n == unit_tiles(next.b) && !fixup(next.j0 + next.n - 1, next)) return false;
+        done = next.j0 + next.n >= ntiles;
+        if (!done) {
+          next = seg_at(next.j0 + next.n);
+          ask_row(next);
+        }
+      }
+      return true;
+    };
+    if (load_tiles(1, [&](int j) { return fix_to(j - C::STAGES + 1); })) fix_to(ntiles - 1);
   } else {
     // ---------------- softmax and epilogue: thread tid owns row tid of each
     // tile (lane tid of S^T) and lane tid of O^T
@@ -685,11 +734,13 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t o_col = C::TMEM_O + (tid / D) * C::HCOL;   // the columns of this lane's half
-    int k_sync = 0;
-    bool ok = true;
+    // A wait that runs out is noted and the step goes on with what is there;
+    // the next softmax_sync ends the work of all four warps.
+    bool failed = false;
+    int k_red = 0;      // uses of red, whose two halves take turns
     int arrived = -1;   // last segment whose tiles were added to its unit's counter
     // out[b][h * G + g] from the lanes' o[g] over l[g]
-    auto write_out = [&](int b, int h, const float (&o)[G], const float (&l)[G]) -> bool {
+    auto write_out = [&](int b, int h, const float (&o)[G], const float (&l)[G]) {
       __nv_bfloat16* out = p.out + ((size_t)b * p.n_q + (size_t)h * G) * D;
       if constexpr (KPR == 1) {
 #pragma unroll
@@ -697,12 +748,17 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       } else {
 #pragma unroll
         for (int g = 0; g < G; ++g) xo[g * 128 + tid] = l[g] == 0.f ? 0.f : o[g] / l[g];
-        if (!group_sync(grp_bar, k_sync, abort_flag, p.err)) return false;
+        failed = softmax_sync(failed);
         for (int i = tid; i < G * D; i += AP_SM_THREADS)
           out[i] = __float2bfloat16_rn(xo[i / D * 128 + i % D] + xo[i / D * 128 + D + i % D]);
-        if (!group_sync(grp_bar, k_sync, abort_flag, p.err)) return false;
+        failed = softmax_sync(failed);
       }
-      return true;
+    };
+    uint32_t p_at[8];   // this thread's byte of row r of P^T, less 128 r, by r & 7
+#pragma unroll
+    for (int r = 0; r < 8; ++r) p_at[r] = smem_addr(sP) + (((tid >> 4) ^ r) << 4) + (tid & 15);
+    auto put_p = [&](int buf, int r, uint32_t code) {
+      asm volatile("st.shared.u8 [%0], %1;" ::"r"(p_at[r & 7] + buf * C::OP_BYTES + r * 128), "r"(code) : "memory");
     };
     int i = 0;
     PageSeg sg = seg_at(0);
@@ -718,33 +774,33 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         o_acc[g] = 0.f;
         a_prev[g] = 0.f;
       }
-      auto consume_o = [&](int jj) -> bool {
-        if (!__all_sync(0xffffffffu, wait_or_abort(&o_full[jj & 1], (jj >> 1) & 1, abort_flag, p.err))) return false;
+      auto consume_o = [&](int jj) {
+        failed |= !ap_wait(&o_full[jj & 1], (jj >> 1) & 1, abort_flag, p.err);
+        __syncwarp();
         tc_fence_after();
         float ov[C::LD];
         tmem_ld_n<C::LD>(lane_base + o_col + (jj & 1) * C::NPAD, ov);
         tmem_wait_ld();
         tc_fence_before();
-        mbar_arrive(&o_free[jj & 1]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&o_free[jj & 1]);
 #pragma unroll
         for (int g = 0; g < G; ++g)
           o_acc[g] = fmaf(o_acc[g], a_prev[g], fmaf(fmaf(ov[2 * G + g], 0x1p-5f, ov[G + g]), 0x1p-4f, ov[g]) * v_prev);
-        return true;
       };
-      for (int tt = 0; ok && tt < sg.n; ++tt) {
+      for (int tt = 0; tt < sg.n; ++tt) {
         const int j = sg.j0 + tt;
         const int sb = j & 1, st = j % C::STAGES;
         const int key0 = (sg.t0 + tt) * C::TILE_KEYS + tid * KPR;
-        if (p.inject_timeout && j == 0 && !__all_sync(0xffffffffu, mbar_wait(never, 0, kInjectWaitCycles))) {
-          *abort_flag = 1;
-          atomicOr(p.err, kErrTimeout);
-          ok = false;
-          break;
+        if (p.inject_timeout && j == 0) {
+          failed = !mbar_wait(never, 0, kInjectWaitCycles);
+          if (tid == 0) {
+            *abort_flag = 1;
+            atomicOr(p.err, kErrTimeout);
+          }
         }
-        if (!__all_sync(0xffffffffu, wait_or_abort(&s_full[sb], (j >> 1) & 1, abort_flag, p.err))) {
-          ok = false;
-          break;
-        }
+        failed |= !ap_wait(&s_full[sb], (j >> 1) & 1, abort_flag, p.err);
+        __syncwarp();
         tc_fence_after();
         float s[KPR][G], vs[KPR];
         float vmax = 0.f;
@@ -766,33 +822,30 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           }
         }
         tc_fence_before();
-        mbar_arrive(&s_free[sb]);
-        float* rb = red + (k_sync & 1) * 4 * C::RED;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[sb]);
+        float* rb = red + (k_red++ & 1) * 4 * C::RED;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           float t = s[0][g];
           if constexpr (KPR == 2) t = fmaxf(t, s[1][g]);
-          t = warp_max(t);
+          t = warp_max_f32(t);
           if (lane == 0) rb[warp * C::RED + g] = t;
         }
-        vmax = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vmax)));
+        vmax = warp_max_f32(vmax);
         if (lane == 0) rb[warp * C::RED + 8] = vmax;
-        if (!group_sync(grp_bar, k_sync, abort_flag, p.err)) {
-          ok = false;
-          break;
-        }
+        if (failed = softmax_sync(failed)) break;
         vmax = fmaxf(fmaxf(rb[8], rb[C::RED + 8]), fmaxf(rb[2 * C::RED + 8], rb[3 * C::RED + 8]));
-        // weights are written as 256 p (V scale / the tile's largest): at most 256
-        const float v_inv = vmax > 0.f ? 1.f / vmax : 0.f;
         float alpha[G];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
           const float tmax =
               fmaxf(fmaxf(rb[g], rb[C::RED + g]), fmaxf(rb[2 * C::RED + g], rb[3 * C::RED + g]));
           const float mn = fmaxf(m_ref[g], tmax);
-          alpha[g] = m_ref[g] == -INFINITY ? 0.f : ex2_approx(m_ref[g] - mn);
+          // -inf: every key masked so far
+          const float base = mn == -INFINITY ? 0.f : mn;
+          alpha[g] = ex2_approx(m_ref[g] - base);
           m_ref[g] = mn;
-          const float base = mn == -INFINITY ? 0.f : mn;   // every key masked so far
           l_part[g] *= alpha[g];
 #pragma unroll
           for (int par = 0; par < KPR; ++par) {
@@ -800,56 +853,51 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
             l_part[g] += s[par][g];
           }
         }
-        if (j >= 2 && !__all_sync(0xffffffffu, wait_or_abort(&p_free[sb], ((j - 2) >> 1) & 1, abort_flag, p.err))) {
-          ok = false;
-          break;
-        }
-        uint8_t* pb = sP + sb * C::OP_BYTES + (tid & 15);
+        if (j >= 2) failed |= !ap_wait(&p_free[sb], ((j - 2) >> 1) & 1, abort_flag, p.err);
+        // weights are written as 256 p (V scale / the tile's largest): at most 256
+        const float v_inv = vmax > 0.f ? 1.f / vmax : 0.f;
 #pragma unroll
         for (int par = 0; par < KPR; ++par) {
           const float w = vs[par] * v_inv * 256.f;
 #pragma unroll
           for (int g = 0; g < G; g += 2) {
+            constexpr int last = G - 1;
             uint32_t part[3];
-            const float a = s[par][g] * w, b = g + 1 < G ? s[par][g + 1 < G ? g + 1 : g] * w : 0.f;
-            split3(a, b, part);
+            split3(s[par][g] * w, g < last ? s[par][g < last ? g + 1 : g] * w : 0.f, part);
 #pragma unroll
             for (int k = 0; k < AP_PARTS; ++k) {
               const int r = par * C::HCOL + k * G + g;
-              pb[r * 128 + (((tid >> 4) ^ (r & 7)) << 4)] = (uint8_t)part[k];
-              if (g + 1 < G) pb[(r + 1) * 128 + (((tid >> 4) ^ ((r + 1) & 7)) << 4)] = (uint8_t)(part[k] >> 8);
+              put_p(sb, r, part[k]);
+              if (g < last) put_p(sb, r + 1, part[k] >> 8);
             }
           }
         }
         fence_proxy_async();
-        mbar_arrive(&p_full[sb]);
-        if (tt > 0 && !consume_o(j - 1)) {
-          ok = false;
-          break;
-        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[sb]);
+        if (tt > 0) consume_o(j - 1);
         v_prev = vmax * 0x1p-8f;
 #pragma unroll
         for (int g = 0; g < G; ++g) a_prev[g] = alpha[g];
       }
-      if (ok) ok = consume_o(sg.j0 + sg.n - 1);
+      if (failed) break;
+      consume_o(sg.j0 + sg.n - 1);
 
       // ---------------- segment epilogue
       const int u = sg.b * p.pool.n_kv + sg.h;
       float L[G];
-      if (ok) {
-        float* rb = red + (k_sync & 1) * 4 * C::RED;
+      float* rb = red + (k_red++ & 1) * 4 * C::RED;
 #pragma unroll
-        for (int g = 0; g < G; ++g) {
-          const float ls = warp_sum(l_part[g]);
-          if (lane == 0) rb[warp * C::RED + g] = ls;
-        }
-        ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
-#pragma unroll
-        for (int g = 0; g < G; ++g) L[g] = (rb[g] + rb[C::RED + g]) + (rb[2 * C::RED + g] + rb[3 * C::RED + g]);
+      for (int g = 0; g < G; ++g) {
+        const float ls = warp_sum(l_part[g]);
+        if (lane == 0) rb[warp * C::RED + g] = ls;
       }
-      if (ok && whole) {
-        ok = write_out(sg.b, sg.h, o_acc, L);
-      } else if (ok) {
+      if (failed = softmax_sync(failed)) break;
+#pragma unroll
+      for (int g = 0; g < G; ++g) L[g] = (rb[g] + rb[C::RED + g]) + (rb[2 * C::RED + g] + rb[3 * C::RED + g]);
+      if (whole) {
+        write_out(sg.b, sg.h, o_acc, L);
+      } else {
         const int slot = 2 * cta + (i == 0 ? 0 : 1);
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -860,9 +908,9 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           }
         }
         // every partial store of the CTA is ordered before tid 0's arrival
-        // (a release at GPU scope, cumulative over the group barrier)
-        ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
-        if (ok && tid == 0) {
+        // (a release at GPU scope, cumulative over the barrier)
+        if (failed = softmax_sync(failed)) break;
+        if (tid == 0) {
           int prev;
           asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;"
                        : "=r"(prev)
@@ -871,10 +919,10 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           const bool last = prev + sg.n == unit_tiles(sg.b);
           if (last) p.counters[u] = 0;   // every CTA of the unit has arrived
           *last_flag = last ? 1 : 0;
-          arrived = i;
         }
-        if (ok) ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
-        if (ok && *last_flag) {
+        arrived = i;
+        if (failed = softmax_sync(failed)) break;
+        if (*last_flag) {
           // ---- merge: the CTAs from the one with the unit's first tile to the
           // one with its last, in that order whoever merges; a CTA's slot is
           // 2c, or 2c + 1 if the unit is not where its range starts.  A round
@@ -902,7 +950,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           for (int g = 0; g < G; ++g) lt[g] = ot[g] = 0.f;
 #pragma unroll
           for (int q = 0; q < (G + 3) / 4; ++q) mx[q] = -INFINITY;
-          for (int k0 = 0; ok && k0 < nctr; k0 += kMergeRows) {
+          for (int k0 = 0; k0 < nctr; k0 += kMergeRows) {
             const int nk = min(kMergeRows, nctr - k0);
             float ov[C::MERGE][G];
             auto fetch = [&](int k) {
@@ -921,7 +969,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
               if (lane < nk) a = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot(k0 + lane) * G + g);
               if (lane + 32 < nk)
                 b = __ldcg(reinterpret_cast<const float2*>(p.part_ml) + (size_t)slot(k0 + lane + 32) * G + g);
-              const float cm = fmaxf(mx[q], warp_max(fmaxf(a.x, b.x)));
+              const float cm = fmaxf(mx[q], warp_max_f32(fmaxf(a.x, b.x)));
               const float base = cm == -INFINITY ? 0.f : cm;
               const float wa = ex2_approx(a.x - base), wb = ex2_approx(b.x - base);
               const float sum = warp_sum(wa * a.y + wb * b.y);
@@ -933,7 +981,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
               }
               mx[q] = cm;
             }
-            ok = group_sync(grp_bar, k_sync, abort_flag, p.err);
+            softmax_sync(false);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
               lt[g] = fmaf(lt[g], tot[2 * g], tot[2 * g + 1]);
@@ -946,17 +994,16 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
 #pragma unroll
                 for (int g = 0; g < G; ++g) ot[g] = fmaf(wts[(k + r) * G + g], ov[r][g], ot[g]);
             }
-            if (ok) ok = group_sync(grp_bar, k_sync, abort_flag, p.err);   // wts and tot are free again
+            softmax_sync(false);   // wts and tot are free again
           }
-          if (!ok) break;
-          ok = write_out(sg.b, sg.h, ot, lt);
+          write_out(sg.b, sg.h, ot, lt);
         }
       }
-      if (!ok) break;
+      if (failed) break;
       if (sg.j0 + sg.n >= ntiles) break;
       sg = seg_at(sg.j0 + sg.n);
     }
-    if (!ok && tid == 0) {
+    if (failed && tid == 0) {
       // The CTA gave up: still add the tiles of its remaining shared units to
       // their counters (their outputs are undefined), so that every counter is
       // back at zero when the launch ends.
@@ -975,10 +1022,10 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   // ---------------- teardown
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag && warp == 4 && lane == 0) {
+  if (*abort_flag && (warp == 4 || warp == 7) && lane == 0) {
     // let the copies in flight land before the shared memory is released
-    for (int j = max(0, issued - C::STAGES); j < issued; ++j)
-      mbar_wait(&kv_full[j % C::STAGES], (j / C::STAGES) & 1);
+    uint64_t* full = warp == 4 ? k_full : v_full;
+    for (int j = max(0, issued - C::STAGES); j < issued; ++j) mbar_wait(&full[j % C::STAGES], (j / C::STAGES) & 1);
   }
   __syncthreads();
   if (warp == 4) {
