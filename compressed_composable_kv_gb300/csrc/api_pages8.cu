@@ -221,7 +221,8 @@ c2kv_status c2kv_token_logprobs(const void* logits, int32_t dtype, int32_t rows,
   if ((logprob == nullptr) != (tokens == nullptr)) return api_fail(C2KV_EINVAL, "tokens and logprob go together");
   if (top_k > 0 && (!top_ids || !top_logprobs)) return api_fail(C2KV_EINVAL, "top_ids / top_logprobs is null");
   if (!aligned(logits, dtype == C2KV_BF16 ? 2 : 4)) return api_fail(C2KV_EINVAL, "logits must be aligned to their type");
-  const c2kv_status s = api_device_state(&p.err, nullptr);
+  int sms = 0;
+  const c2kv_status s = api_device_state(&p.err, &sms);
   if (s != C2KV_OK) return s;
   p.logits = logits;
   p.tokens = tokens;
@@ -234,7 +235,7 @@ c2kv_status c2kv_token_logprobs(const void* logits, int32_t dtype, int32_t rows,
   p.vocab = vocab;
   p.top_k = top_k;
   p.is_f32 = dtype == C2KV_F32;
-  return api_launched(launch_token_logprobs(p, static_cast<cudaStream_t>(stream)), "c2kv_token_logprobs");
+  return api_launched(launch_token_logprobs(p, sms, static_cast<cudaStream_t>(stream)), "c2kv_token_logprobs");
 }
 
 }  // extern "C"

@@ -152,6 +152,7 @@ struct LogprobParams {
   unsigned* err;
   int64_t row_stride;
   int32_t rows, vocab, top_k, is_f32;
+  int32_t cluster;               // CTAs of a row (set by the launcher)
 };
 
 constexpr int kMaxTopK = 64;
@@ -160,7 +161,7 @@ cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, c
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st);
 cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, bool overlap,
                                  cudaStream_t st);
-cudaError_t launch_token_logprobs(const LogprobParams& p, cudaStream_t st);
+cudaError_t launch_token_logprobs(const LogprobParams& p, int sms, cudaStream_t st);
 
 // What the entry points of another translation unit share with api.cu.
 c2kv_status api_fail(c2kv_status st, const char* msg);
