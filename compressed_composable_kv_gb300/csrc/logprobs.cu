@@ -3,25 +3,22 @@
 //   m = max x, S = sum exp(x - m), lp(t) = x_t - m - log S,
 //   H = log S - sum exp(x - m) (x - m) / S.
 //
-// One pass over the logits, which is what bounds it: a CTA takes 32 KB of a
-// row at a time into registers (128 bytes a thread, every load in flight), and
-// the CTAs of a row are a thread-block cluster whose partial (m, S, sum) and
-// top lists meet in its first CTA through distributed shared memory.  A thread
-// sums against its own maximum, so nothing is waited for before the sums;
-// partial sums are brought to a common maximum when they meet, in a fixed
-// order.
+// One pass over the logits, which is what bounds it: a thread takes 128 bytes
+// at a time, every load in flight, and sums against its own maximum, so nothing
+// is waited for on the way; partial sums are brought to a common maximum when
+// they meet, in a fixed order.  Few rows are split over thread-block clusters,
+// whose CTAs store their partial results and lists into the first one's shared
+// memory.
 //
 // Top alternatives: the CTA's 64 groups of 4 threads have 64 maxima; the k-th
 // largest of them is a bound that at least k logits reach, and as a rule few
-// more do.  Those go to a list, whose ranks are counted.  Where too many reach
-// it (rows of equal logits, or all but a few ruled out) the k largest are found
-// one after another instead.  Logits are ordered as whole numbers, (value,
-// lower index first), so that equal ones have one order.
-#include <cooperative_groups.h>
-
+// more do.  The threads whose maximum reaches it (about k of them) look through
+// their logits once more, which are in L2, and list those that do; the list's
+// ranks are counted.  Where too many reach the bound (rows of equal logits, or
+// all but a few ruled out) the k largest are found one after another instead.
+// Logits are ordered as whole numbers, (value, lower index first), so that
+// equal ones have one order.
 #include "pages8.h"
-
-namespace cg = cooperative_groups;
 
 namespace c2kv {
 
@@ -30,7 +27,6 @@ namespace {
 constexpr int LP_THREADS = 256;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_VECS = 8;                            // 16-byte loads of a thread
-constexpr int LP_SLICE = LP_VECS * LP_THREADS;        // vectors of a CTA's step
 constexpr int LP_GROUPS = 64;
 constexpr int LP_CAND = 1024;                         // list of a step; the cluster's lists: 16 * 64
 constexpr int LP_MAX_CLUSTER = 16;
@@ -89,11 +85,6 @@ struct Vec<__nv_bfloat16> {
     const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
     return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);
   }
-  static __device__ __forceinline__ void set(uint4& v, int e, __nv_bfloat16 x) {
-    const uint32_t b = __bfloat16_as_ushort(x);
-    uint32_t& w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
-    w = (e & 1) ? (w & 0xFFFFu) | (b << 16) : (w & 0xFFFF0000u) | b;
-  }
 };
 template <>
 struct Vec<float> {
@@ -102,29 +93,43 @@ struct Vec<float> {
   static __device__ __forceinline__ float at(const uint4& v, int e) {
     return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
   }
-  static __device__ __forceinline__ void set(uint4& v, int e, float x) {
-    (e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w) = __float_as_uint(x);
-  }
 };
 
 struct LpShared {
-  alignas(16) uint64_t cand[LP_CAND];
-  uint64_t top[kMaxTopK];     // the CTA's list so far, largest first; 0: none
+  uint64_t cand[LP_CAND];                      // a CTA's list
+  uint64_t lists[LP_MAX_CLUSTER * kMaxTopK];   // in a row's first CTA: the cluster's top lists, k each
+  uint64_t top[kMaxTopK];                      // the largest, in order; 0: none
   uint64_t red[LP_WARPS];
   Part part[LP_WARPS];
-  Part all;                   // the CTA's partial result
-  uint32_t group[LP_GROUPS];
+  Part all[LP_MAX_CLUSTER];                    // in a row's first CTA: the partial results of the cluster
+  alignas(16) uint32_t group[LP_GROUPS];
   uint32_t bound;
   int count;
 };
 
-// The k-th list entries of n candidates, by counting how many are larger.
+// A CTA's part of a row: vectors [v0, v1) behind its first `head` logits and,
+// in the row's first CTA, the `extra` logits before and behind the vectors.
+template <typename T>
+struct Piece {
+  const T* x;
+  const uint4* vec;
+  int head, v0, v1, extra, vocab;
+
+  __device__ __forceinline__ int extra_at(int i) const { return i < head ? i : vocab - extra + i; }
+  __device__ __forceinline__ int index(int v, int e) const { return head + v * Vec<T>::N + e; }
+};
+
+// top[0..k) from n candidates, by counting how many are larger; four threads to
+// a candidate.
 __device__ __forceinline__ void rank_into(LpShared& sh, int n, int k) {
-  for (int i = threadIdx.x; i < n; i += LP_THREADS) {
-    const uint64_t key = sh.cand[i];
+  for (int i0 = 0; i0 < n; i0 += LP_THREADS / 4) {
+    const int i = i0 + (threadIdx.x >> 2);
+    const uint64_t key = i < n ? sh.cand[i] : 0;
     int rank = 0;
-    for (int j = 0; j < n; ++j) rank += sh.cand[j] > key ? 1 : 0;
-    if (rank < k) sh.top[rank] = key;
+    for (int j = threadIdx.x & 3; j < n; j += 4) rank += sh.cand[j] > key ? 1 : 0;
+    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+    if (i < n && (threadIdx.x & 3) == 0 && rank < k) sh.top[rank] = key;
   }
 }
 
@@ -132,19 +137,20 @@ __device__ __forceinline__ uint64_t list_key(float x, int i) {
   return ((uint64_t)order_bits(x) << 32) | (uint32_t)~i;
 }
 
-// The same from logits [lo, hi) of the row and the list so far (cand[0..k)),
-// one after another: the way out where too many logits reach the bound.
+// The same from all logits of the piece, one after another: the way out where
+// too many reach the bound.
 template <typename T>
-__device__ __noinline__ void one_by_one(LpShared& sh, const T* x, int lo, int hi, int k) {
+__device__ __noinline__ void one_by_one(LpShared& sh, const Piece<T>& pc, int k) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint64_t before = ~0ull;
   for (int r = 0; r < k; ++r) {
     uint64_t best = 0;
-    auto see = [&](uint64_t key) {
+    auto see = [&](int i) {
+      const uint64_t key = list_key((float)pc.x[i], i);
       if (key < before && key > best) best = key;
     };
-    for (int i = lo + threadIdx.x; i < hi; i += LP_THREADS) see(list_key((float)x[i], i));
-    if (threadIdx.x < k) see(sh.cand[threadIdx.x]);
+    for (int i = pc.index(pc.v0, 0) + threadIdx.x; i < pc.index(pc.v1, 0); i += LP_THREADS) see(i);
+    if (threadIdx.x < pc.extra) see(pc.extra_at(threadIdx.x));
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) {
       const uint64_t o = __shfl_xor_sync(0xffffffffu, best, off);
@@ -160,39 +166,51 @@ __device__ __noinline__ void one_by_one(LpShared& sh, const T* x, int lo, int hi
   }
 }
 
+// A thread's LP_VECS vectors v, v + LP_THREADS, ... of the piece; -inf behind its end.
 template <typename T>
-__global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const __grid_constant__ LogprobParams p) {
+__device__ __forceinline__ void load_vecs(const Piece<T>& pc, int v, uint4 (&d)[LP_VECS]) {
+#pragma unroll
+  for (int c = 0; c < LP_VECS; ++c) {
+    const uint32_t none = Vec<T>::kNone;
+    d[c] = v + c * LP_THREADS < pc.v1 ? __ldg(pc.vec + v + c * LP_THREADS) : make_uint4(none, none, none, none);
+  }
+}
+
+// The address of `p` of this CTA's shared memory in the cluster's first CTA.
+__device__ __forceinline__ uint32_t in_first_cta(const void* p) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
+  return r;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __grid_constant__ LogprobParams p) {
   using V = Vec<T>;
   __shared__ LpShared sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int cs = p.cluster, row = blockIdx.x / cs, rank = blockIdx.x % cs, k = p.top_k;
-  const T* x = static_cast<const T*>(p.logits) + (int64_t)row * p.row_stride;
-  // The row as 16-byte vectors: the first and the last may reach beyond it.
-  const int mis = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const int end = mis + p.vocab, nvec = (end + V::N - 1) / V::N;
-  const uint4* base = reinterpret_cast<const uint4*>(x - mis);
-  const int share = (nvec + cs - 1) / cs;
-  const int v0 = min(nvec, rank * share), v1 = min(nvec, v0 + share);
-  Part mine = {-INFINITY, 0.f, 0.f};
-  if (tid < k) sh.top[tid] = 0;
-  if (tid == 0) sh.count = 0;
+  // every CTA of a cluster runs before another stores into its shared memory
+  if (cs > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  Piece<T> pc;
+  pc.x = static_cast<const T*>(p.logits) + (int64_t)row * p.row_stride;
+  pc.vocab = p.vocab;
+  pc.head = min(p.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(pc.x) & 15)) / sizeof(T)) % V::N);
+  pc.vec = reinterpret_cast<const uint4*>(pc.x + pc.head);
+  const int nvec = (p.vocab - pc.head) / V::N, share = (nvec + cs - 1) / cs;
+  pc.v0 = min(nvec, rank * share);
+  pc.v1 = min(nvec, pc.v0 + share);
+  pc.extra = rank == 0 ? p.vocab - nvec * V::N : 0;
 
-  for (int vb = v0; vb < v1; vb += LP_SLICE) {
+  Part mine = {-INFINITY, 0.f, 0.f};
+  uint32_t most = 0;   // order of the thread's largest logit; 0: it has none
+  auto add = [&](Part q) {
+    const float M = fmaxf(mine.m, q.m);
+    const Part a = at_max(mine, M), b = at_max(q, M);
+    mine = {M, a.s + b.s, a.t + b.t};
+  };
+  for (int v = pc.v0 + tid; v < pc.v1; v += LP_VECS * LP_THREADS) {
     uint4 d[LP_VECS];
-#pragma unroll
-    for (int c = 0; c < LP_VECS; ++c) {
-      const int v = vb + c * LP_THREADS + tid;
-      if (v < v1 && v * V::N >= mis && v * V::N + V::N <= end) {
-        d[c] = __ldcs(base + v);
-      } else {
-        d[c] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
-        if (v < v1)
-          for (int e = 0; e < V::N; ++e) {
-            const int i = v * V::N + e;
-            if (i >= mis && i < end) V::set(d[c], e, x[i - mis]);
-          }
-      }
-    }
+    load_vecs(pc, v, d);
     Part q = {-INFINITY, 0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < LP_VECS; ++c)
@@ -208,104 +226,127 @@ __global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const __g
         q.s += w;
         q.t = fmaf(w, y, q.t);
       }
-    const float M = fmaxf(mine.m, q.m);
-    const Part a = at_max(mine, M), b = at_max(q, M);
-    mine = {M, a.s + b.s, a.t + b.t};
-    if (k == 0) continue;
-
-    // ---- top alternatives of this step and the list so far
-    const uint32_t most = q.s == q.s ? order_bits(q.m) : 0xFFFFFFFFu;   // NaN or +inf: look
-    uint32_t g = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
-    if ((lane & 3) == 0) sh.group[tid >> 2] = g;
-    __syncthreads();
-    if (tid < LP_GROUPS) {
-      const uint32_t v = sh.group[tid];
-      int r = 0;
-      for (int j = 0; j < LP_GROUPS; ++j) {
-        const uint32_t o = sh.group[j];
-        r += o > v || (o == v && j < tid) ? 1 : 0;
-      }
-      if (r == k - 1) sh.bound = v;
-    }
-    if (tid < k) sh.cand[tid] = sh.top[tid];
-    __syncthreads();
-    const uint32_t bound = sh.bound;
-    if (most >= bound) {
-#pragma unroll
-      for (int c = 0; c < LP_VECS; ++c) {
-        const int v = vb + c * LP_THREADS + tid;
-#pragma unroll
-        for (int e = 0; e < V::N; ++e) {
-          const float xe = V::at(d[c], e);
-          const int i = v * V::N + e;
-          if (order_bits(xe) >= bound && v < v1 && i >= mis && i < end) {
-            const int at = k + atomicAdd(&sh.count, 1);
-            if (at < LP_CAND) sh.cand[at] = list_key(xe, i - mis);
-          }
-        }
-      }
-    }
-    __syncthreads();
-    const int found = sh.count;
-    const int lo = max(vb * V::N, mis) - mis, hi = min(min(v1, vb + LP_SLICE) * V::N, end) - mis;
-    __syncthreads();
-    if (tid == 0) sh.count = 0;
-    if (k + found <= LP_CAND && found >= min(k, hi - lo))
-      rank_into(sh, k + found, k);
-    else
-      one_by_one<T>(sh, x, lo, hi, k);
-    __syncthreads();
+    add(q);
+    most = 1;
   }
+  if (tid < pc.extra) {
+    const float xe = (float)pc.x[pc.extra_at(tid)];
+    add({xe, xe == -INFINITY ? 0.f : xe - xe + 1.f, 0.f});   // NaN and +inf sum up to NaN
+    most = 1;
+  }
+  if (most) most = mine.s == mine.s ? order_bits(mine.m) : 0xFFFFFFFFu;   // NaN or +inf: look
 
-  // ---- the CTA's partial result: threads, then warps, in order
+  // ---- the CTA's partial result (threads, then warps, in order) and the bound
   {
     float M = mine.m;
 #pragma unroll
     for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-    mine = at_max(mine, M);
-    mine.s = warp_sum_f32(mine.s);
-    mine.t = warp_sum_f32(mine.t);
-    if (lane == 0) sh.part[warp] = mine;
-    __syncthreads();
-    if (tid == 0) {
-      float m = -INFINITY;
-      for (int w = 0; w < LP_WARPS; ++w) m = fmaxf(m, sh.part[w].m);
-      Part all = {m, 0.f, 0.f};
-      for (int w = 0; w < LP_WARPS; ++w) {
-        const Part q = at_max(sh.part[w], m);
-        all.s += q.s;
-        all.t += q.t;
-      }
-      sh.all = all;
-    }
-    __syncthreads();
+    Part w = at_max(mine, M);
+    w.s = warp_sum_f32(w.s);
+    w.t = warp_sum_f32(w.t);
+    if (lane == 0) sh.part[warp] = w;
+    uint32_t g = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
+    if ((lane & 3) == 0) sh.group[tid >> 2] = g;
+    if (tid < k) sh.top[tid] = 0;
+    if (tid == 0) sh.count = 0;
   }
-  Part all = sh.all;
-  if (cs > 1) {
-    cg::cluster_group cl = cg::this_cluster();
-    cl.sync();
-    if (rank == 0) {
-      float m = -INFINITY;
-      Part q[LP_MAX_CLUSTER];
+  __syncthreads();
+  if (tid == 0) {
+    float m = -INFINITY;
 #pragma unroll
-      for (int r = 0; r < LP_MAX_CLUSTER; ++r) {
-        q[r] = r < cs ? *cl.map_shared_rank(&sh.all, r) : Part{-INFINITY, 0.f, 0.f};
-        m = fmaxf(m, q[r].m);
-      }
-      all = {m, 0.f, 0.f};
+    for (int w = 0; w < LP_WARPS; ++w) m = fmaxf(m, sh.part[w].m);
+    Part all = {m, 0.f, 0.f};
 #pragma unroll
-      for (int r = 0; r < LP_MAX_CLUSTER; ++r) {
-        const Part o = at_max(q[r], m);
-        all.s += o.s;
-        all.t += o.t;
-      }
-      for (int i = tid; i < cs * k; i += LP_THREADS) sh.cand[i] = cl.map_shared_rank(sh.top, i / k)[i % k];
+    for (int w = 0; w < LP_WARPS; ++w) {
+      const Part q = at_max(sh.part[w], m);
+      all.s += q.s;
+      all.t += q.t;
     }
-    cl.sync();   // everything of the other CTAs has been read
-    if (rank != 0) return;
-    rank_into(sh, cs * k, k);
+    sh.all[0] = all;
+  }
+  if (k > 0) {
+    {
+      const int i = tid >> 2;   // four threads to a group
+      const uint32_t v = sh.group[i];
+      int r = 0;
+#pragma unroll
+      for (int j0 = 0; j0 < LP_GROUPS; j0 += 16) {
+        const uint4 o = *reinterpret_cast<const uint4*>(&sh.group[j0 + (tid & 3) * 4]);
+        const int j = j0 + (tid & 3) * 4;
+        r += (o.x > v || (o.x == v && j < i)) + (o.y > v || (o.y == v && j + 1 < i)) +
+             (o.z > v || (o.z == v && j + 2 < i)) + (o.w > v || (o.w == v && j + 3 < i));
+      }
+      r += __shfl_xor_sync(0xffffffffu, r, 1);
+      r += __shfl_xor_sync(0xffffffffu, r, 2);
+      if ((tid & 3) == 0 && r == k - 1) sh.bound = v;
+    }
     __syncthreads();
+    const uint32_t bound = max(sh.bound, 1u);
+    if (most >= bound) {
+      auto see = [&](float xe, int i) {
+        if (order_bits(xe) < bound) return;
+        const int at = atomicAdd(&sh.count, 1);
+        if (at < LP_CAND) sh.cand[at] = list_key(xe, i);
+      };
+      for (int v = pc.v0 + tid; v < pc.v1; v += LP_VECS * LP_THREADS) {
+        uint4 d[LP_VECS];
+        load_vecs(pc, v, d);
+#pragma unroll
+        for (int c = 0; c < LP_VECS; ++c)
+          if (v + c * LP_THREADS < pc.v1)
+#pragma unroll
+            for (int e = 0; e < V::N; ++e) see(V::at(d[c], e), pc.index(v + c * LP_THREADS, e));
+      }
+      if (tid < pc.extra) see((float)pc.x[pc.extra_at(tid)], pc.extra_at(tid));
+    }
+    __syncthreads();
+    const int found = sh.count, there = (pc.v1 - pc.v0) * V::N + pc.extra;
+    if (found <= LP_CAND && found >= min(k, there)) rank_into(sh, found, k);
+    else one_by_one(sh, pc, k);
+  }
+  __syncthreads();
+
+  if (cs > 1) {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank > 0) {
+      if (tid < k)
+        asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(in_first_cta(&sh.lists[rank * k + tid])), "l"(sh.top[tid])
+                     : "memory");
+      if (tid == 0) {
+        const uint32_t at = in_first_cta(&sh.all[rank]);
+        const Part q = sh.all[0];
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(q.m) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(q.s) : "memory");
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(q.t) : "memory");
+      }
+    }
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (rank != 0) return;
+  }
+  Part all = sh.all[0];
+  if (cs > 1) {
+    float m = all.m;
+    for (int r = 1; r < cs; ++r) m = fmaxf(m, sh.all[r].m);
+    all = at_max(all, m);
+    for (int r = 1; r < cs; ++r) {
+      const Part q = at_max(sh.all[r], m);
+      all.s += q.s;
+      all.t += q.t;
+    }
+    if (k > 0) {
+      if (tid < k) sh.lists[tid] = sh.top[tid];
+      if (tid == 0) sh.count = 0;
+      __syncthreads();
+      uint64_t least = 1;   // every list's last entry has k logits at or above it
+      for (int r = 0; r < cs; ++r) least = max(least, sh.lists[r * k + k - 1]);
+      for (int i = tid; i < cs * k; i += LP_THREADS)
+        if (sh.lists[i] >= least) sh.cand[atomicAdd(&sh.count, 1)] = sh.lists[i];
+      __syncthreads();
+      rank_into(sh, sh.count, k);
+      __syncthreads();
+    }
   }
   const float ls = logf(all.s);
   const bool none = all.m == -INFINITY && all.s == 0.f;   // nothing but -inf
@@ -314,7 +355,7 @@ __global__ void __launch_bounds__(LP_THREADS, 3) token_logprobs_kernel(const __g
     if (p.logprob) {
       const int tok = p.tokens[row];
       if (tok >= p.vocab) atomicOr(p.err, kErrLength);
-      p.logprob[row] = tok < 0 ? 0.f : tok >= p.vocab ? NAN : lp((float)x[tok]);
+      p.logprob[row] = tok < 0 ? 0.f : tok >= p.vocab ? NAN : lp((float)pc.x[tok]);
     }
     if (p.entropy) p.entropy[row] = none ? 0.f : ls - all.t / all.s;
   }
@@ -340,14 +381,11 @@ cudaError_t launch_lp(LogprobParams p, int sms, cudaStream_t st) {
     }
     if (s.state[dev] != 1) return (cudaError_t)(-s.state[dev]);
   }
-  // As many CTAs to a row as leave each one step of it, and where the rows are
-  // few, up to 16 for the sake of latency, but at least 2 vectors a thread.
-  const int64_t nvec = (p.vocab + Vec<T>::N - 1) / Vec<T>::N;
+  // Two CTAs for each SM where the rows are fewer, but at least two vectors for
+  // each thread and at most 16 CTAs to a row.
+  const int64_t nvec = p.vocab / Vec<T>::N;
   int cs = 1;
-  while (cs < LP_MAX_CLUSTER &&
-         (nvec > (int64_t)cs * LP_SLICE || (p.rows * cs * 2 <= sms && nvec >= (int64_t)cs * 4 * LP_THREADS)))
-    cs *= 2;
-  while (cs > 1 && (int64_t)p.rows * cs > INT32_MAX) cs /= 2;
+  while (cs < LP_MAX_CLUSTER && (int64_t)p.rows * cs < 2 * sms && nvec >= (int64_t)cs * 4 * LP_THREADS) cs *= 2;
   p.cluster = cs;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.rows * cs));
