@@ -10,14 +10,13 @@
 // whose CTAs store their partial results and lists into the first one's shared
 // memory.
 //
-// Top alternatives: the CTA's 64 groups of 4 threads have 64 maxima; the k-th
-// largest of them is a bound that at least k logits reach, and as a rule few
-// more do.  The threads whose maximum reaches it (about k of them) look through
-// their logits once more, which are in L2, and list those that do; the list's
-// ranks are counted.  Where too many reach the bound (rows of equal logits, or
-// all but a few ruled out) the k largest are found one after another instead.
-// Logits are ordered as whole numbers, (value, lower index first), so that
-// equal ones have one order.
+// Top alternatives: in the CTA's first 2048 vectors, the k-th largest of the
+// maxima of its 64 groups of 4 threads is a bound that at least k logits reach.
+// Vectors that reach it, a few for each 2048, are noted on the way; behind the
+// stream their logits are listed and the list's ranks counted.  Where too many
+// reach the bound (rows of equal or rising logits, or all but a few ruled out)
+// the k largest are found one after another instead.  Logits are ordered as
+// whole numbers, (value, lower index first), so that equal ones have one order.
 #include "pages8.h"
 
 namespace c2kv {
@@ -29,6 +28,7 @@ constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_VECS = 8;                            // 16-byte loads of a thread
 constexpr int LP_GROUPS = 64;
 constexpr int LP_CAND = 1024;                         // list of a step; the cluster's lists: 16 * 64
+constexpr int LP_HITS = 1024;                         // vectors noted
 constexpr int LP_MAX_CLUSTER = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFaint = -200.f;                      // exp of it is 0 in fp32
@@ -51,9 +51,37 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return r;
 }
 
-__device__ __forceinline__ float exp_faint(float y) {   // e^y for y >= kFaint
+__device__ __forceinline__ float ex2_ftz(float z) {
   float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y * kLog2e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(z));
+  return r;
+}
+__device__ __forceinline__ float exp_faint(float y) { return ex2_ftz(y * kLog2e); }   // e^y for y >= kFaint
+
+// Pairs of fp32 numbers in one register pair, as the packed instructions take them.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 halves(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
 }
 
@@ -85,6 +113,15 @@ struct Vec<__nv_bfloat16> {
     const uint32_t w = e < 2 ? v.x : e < 4 ? v.y : e < 6 ? v.z : v.w;
     return __uint_as_float((e & 1) ? w & 0xFFFF0000u : w << 16);
   }
+  static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+  }
+  static __device__ __forceinline__ float largest(const uint4& v) {
+    const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+  }
 };
 template <>
 struct Vec<float> {
@@ -93,18 +130,22 @@ struct Vec<float> {
   static __device__ __forceinline__ float at(const uint4& v, int e) {
     return __uint_as_float(e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w);
   }
+  static __device__ __forceinline__ float largest(const uint4& v) {
+    return max_nan(max_nan(at(v, 0), at(v, 1)), max_nan(at(v, 2), at(v, 3)));
+  }
 };
 
 struct LpShared {
   uint64_t cand[LP_CAND];                      // a CTA's list
   uint64_t lists[LP_MAX_CLUSTER * kMaxTopK];   // in a row's first CTA: the cluster's top lists, k each
   uint64_t top[kMaxTopK];                      // the largest, in order; 0: none
+  int hits[LP_HITS];                           // vectors that reach the bound
   uint64_t red[LP_WARPS];
   Part part[LP_WARPS];
   Part all[LP_MAX_CLUSTER];                    // in a row's first CTA: the partial results of the cluster
   alignas(16) uint32_t group[LP_GROUPS];
-  uint32_t bound;
-  int count;
+  float bound;
+  int count, n_hits;
 };
 
 // A CTA's part of a row: vectors [v0, v1) behind its first `head` logits and,
@@ -176,6 +217,35 @@ __device__ __forceinline__ void load_vecs(const Piece<T>& pc, int v, uint4 (&d)[
   }
 }
 
+// A value that at least k logits of the CTA's first vectors reach (all of them,
+// if they are fewer): the k-th largest of the maxima of groups of 4 threads.
+// vm: the thread's maxima, -inf where it has no vector.
+__device__ __forceinline__ float group_bound(LpShared& sh, const float (&vm)[LP_VECS], int tid, int k) {
+  float most = vm[0];
+#pragma unroll
+  for (int c = 1; c < LP_VECS; ++c) most = max_nan(most, vm[c]);
+  uint32_t g = order_bits(most);
+  g = max(g, __shfl_xor_sync(0xffffffffu, g, 1));
+  g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
+  if ((tid & 3) == 0) sh.group[tid >> 2] = g;
+  __syncthreads();
+  const int i = tid >> 2;   // four threads to a group
+  const uint32_t v = sh.group[i];
+  int r = 0;
+#pragma unroll
+  for (int j0 = 0; j0 < LP_GROUPS; j0 += 16) {
+    const int j = j0 + (tid & 3) * 4;
+    const uint4 o = *reinterpret_cast<const uint4*>(&sh.group[j]);
+    r += (o.x > v || (o.x == v && j < i)) + (o.y > v || (o.y == v && j + 1 < i)) +
+         (o.z > v || (o.z == v && j + 2 < i)) + (o.w > v || (o.w == v && j + 3 < i));
+  }
+  r += __shfl_xor_sync(0xffffffffu, r, 1);
+  r += __shfl_xor_sync(0xffffffffu, r, 2);
+  if ((tid & 3) == 0 && r == k - 1) sh.bound = v == 0xFFFFFFFFu ? NAN : from_order(v);
+  __syncthreads();
+  return sh.bound;
+}
+
 // The address of `p` of this CTA's shared memory in the cluster's first CTA.
 __device__ __forceinline__ uint32_t in_first_cta(const void* p) {
   uint32_t r;
@@ -201,42 +271,64 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
   pc.v1 = min(nvec, pc.v0 + share);
   pc.extra = rank == 0 ? p.vocab - nvec * V::N : 0;
 
+  if (tid < k) sh.top[tid] = 0;
+  if (tid == 0) sh.count = sh.n_hits = 0;
+
   Part mine = {-INFINITY, 0.f, 0.f};
-  uint32_t most = 0;   // order of the thread's largest logit; 0: it has none
   auto add = [&](Part q) {
     const float M = fmaxf(mine.m, q.m);
     const Part a = at_max(mine, M), b = at_max(q, M);
     mine = {M, a.s + b.s, a.t + b.t};
   };
-  for (int v = pc.v0 + tid; v < pc.v1; v += LP_VECS * LP_THREADS) {
+  float bound = -INFINITY;
+  for (int vb = pc.v0; vb < pc.v1; vb += LP_VECS * LP_THREADS) {
     uint4 d[LP_VECS];
-    load_vecs(pc, v, d);
+    load_vecs(pc, vb + tid, d);
+    float vm[LP_VECS];
     Part q = {-INFINITY, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < LP_VECS; ++c)
+    for (int c = 0; c < LP_VECS; ++c) {
+      vm[c] = V::largest(d[c]);
+      q.m = fmaxf(q.m, vm[c]);
+    }
+    if (k > 0) {
+      if (vb == pc.v0) bound = group_bound(sh, vm, tid, k);
 #pragma unroll
-      for (int e = 0; e < V::N; ++e) q.m = fmaxf(q.m, V::at(d[c], e));
-    const float from = q.m == -INFINITY ? 0.f : q.m;
-#pragma unroll
-    for (int c = 0; c < LP_VECS; ++c)
-#pragma unroll
-      for (int e = 0; e < V::N; ++e) {
-        const float y = max_nan(V::at(d[c], e) - from, kFaint);
-        const float w = exp_faint(y);
-        q.s += w;
-        q.t = fmaf(w, y, q.t);
+      for (int c = 0; c < LP_VECS; ++c) {
+        const int v = vb + c * LP_THREADS + tid;
+        if (!(vm[c] < bound) && v < pc.v1) {
+          const int at = atomicAdd(&sh.n_hits, 1);
+          if (at < LP_HITS) sh.hits[at] = v;
+        }
       }
+    }
+    const float from = q.m == -INFINITY ? 0.f : q.m;
+    // two logits at a time: the sums of the even and of the odd ones
+    const uint64_t minus = pair(-from, -from), scale = pair(kLog2e, kLog2e);
+    uint64_t s2 = 0, t2 = 0;
+#pragma unroll
+    for (int c = 0; c < LP_VECS; ++c)
+#pragma unroll
+      for (int e = 0; e < V::N; e += 2) {
+        const float2 y = halves(add2(pair(V::at(d[c], e), V::at(d[c], e + 1)), minus));
+        const uint64_t yc = pair(max_nan(y.x, kFaint), max_nan(y.y, kFaint));
+        const float2 z = halves(mul2(yc, scale));
+        const uint64_t w = pair(ex2_ftz(z.x), ex2_ftz(z.y));
+        s2 = add2(s2, w);
+        t2 = fma2(w, yc, t2);
+      }
+    const float2 sh2 = halves(s2), th2 = halves(t2);
+    q.s = sh2.x + sh2.y;
+    q.t = th2.x + th2.y;
     add(q);
-    most = 1;
   }
+  float xe = -INFINITY;
   if (tid < pc.extra) {
-    const float xe = (float)pc.x[pc.extra_at(tid)];
-    add({xe, xe == -INFINITY ? 0.f : xe - xe + 1.f, 0.f});   // NaN and +inf sum up to NaN
-    most = 1;
+    xe = (float)pc.x[pc.extra_at(tid)];
+    add({xe == xe ? xe : -INFINITY, xe == -INFINITY ? 0.f : xe - xe + 1.f, 0.f});   // NaN and +inf sum up to NaN
   }
-  if (most) most = mine.s == mine.s ? order_bits(mine.m) : 0xFFFFFFFFu;   // NaN or +inf: look
 
-  // ---- the CTA's partial result (threads, then warps, in order) and the bound
+  // ---- the CTA's partial result: threads, then warps, in order
   {
     float M = mine.m;
 #pragma unroll
@@ -245,11 +337,6 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
     w.s = warp_sum_f32(w.s);
     w.t = warp_sum_f32(w.t);
     if (lane == 0) sh.part[warp] = w;
-    uint32_t g = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
-    g = max(g, __shfl_xor_sync(0xffffffffu, g, 2));
-    if ((lane & 3) == 0) sh.group[tid >> 2] = g;
-    if (tid < k) sh.top[tid] = 0;
-    if (tid == 0) sh.count = 0;
   }
   __syncthreads();
   if (tid == 0) {
@@ -266,43 +353,22 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
     sh.all[0] = all;
   }
   if (k > 0) {
-    {
-      const int i = tid >> 2;   // four threads to a group
-      const uint32_t v = sh.group[i];
-      int r = 0;
-#pragma unroll
-      for (int j0 = 0; j0 < LP_GROUPS; j0 += 16) {
-        const uint4 o = *reinterpret_cast<const uint4*>(&sh.group[j0 + (tid & 3) * 4]);
-        const int j = j0 + (tid & 3) * 4;
-        r += (o.x > v || (o.x == v && j < i)) + (o.y > v || (o.y == v && j + 1 < i)) +
-             (o.z > v || (o.z == v && j + 2 < i)) + (o.w > v || (o.w == v && j + 3 < i));
+    const int n_hits = sh.n_hits;
+    auto list = [&](float v, int i) {
+      if (v < bound) return;
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < LP_CAND) sh.cand[at] = list_key(v, i);
+    };
+    if (n_hits <= LP_HITS) {
+      for (int i = tid; i < n_hits * V::N; i += LP_THREADS) {
+        const int at = pc.index(sh.hits[i / V::N], i % V::N);
+        list((float)pc.x[at], at);
       }
-      r += __shfl_xor_sync(0xffffffffu, r, 1);
-      r += __shfl_xor_sync(0xffffffffu, r, 2);
-      if ((tid & 3) == 0 && r == k - 1) sh.bound = v;
-    }
-    __syncthreads();
-    const uint32_t bound = max(sh.bound, 1u);
-    if (most >= bound) {
-      auto see = [&](float xe, int i) {
-        if (order_bits(xe) < bound) return;
-        const int at = atomicAdd(&sh.count, 1);
-        if (at < LP_CAND) sh.cand[at] = list_key(xe, i);
-      };
-      for (int v = pc.v0 + tid; v < pc.v1; v += LP_VECS * LP_THREADS) {
-        uint4 d[LP_VECS];
-        load_vecs(pc, v, d);
-#pragma unroll
-        for (int c = 0; c < LP_VECS; ++c)
-          if (v + c * LP_THREADS < pc.v1)
-#pragma unroll
-            for (int e = 0; e < V::N; ++e) see(V::at(d[c], e), pc.index(v + c * LP_THREADS, e));
-      }
-      if (tid < pc.extra) see((float)pc.x[pc.extra_at(tid)], pc.extra_at(tid));
+      if (tid < pc.extra) list(xe, pc.extra_at(tid));
     }
     __syncthreads();
     const int found = sh.count, there = (pc.v1 - pc.v0) * V::N + pc.extra;
-    if (found <= LP_CAND && found >= min(k, there)) rank_into(sh, found, k);
+    if (n_hits <= LP_HITS && found <= LP_CAND && found >= min(k, there)) rank_into(sh, found, k);
     else one_by_one(sh, pc, k);
   }
   __syncthreads();
