@@ -10,37 +10,61 @@
 // that fall below e4m3's normal range.  A value that is not finite is held as
 // NaN and takes no part in a.
 //
-// A CTA of 8 warps owns 128 consecutive rows of one (sequence, kv head), of K
-// or of V: a whole number of pages whatever the page size (16 to 128), so a
-// page's largest magnitude never leaves the CTA.  A warp owns 16 rows and
-// keeps them in registers between the two steps (largest magnitude, codes),
-// so the data are read once.  Bound by the bytes moved.
+// A CTA owns 64 consecutive rows of one (sequence, kv head), of K or of V (128
+// where a page is that long): a whole number of pages, so a page's largest
+// magnitude never leaves the CTA.  A warp owns 16 rows and keeps them, as bf16,
+// in registers between the two steps (largest magnitude, codes), so the data
+// are read once, with all loads of a warp in flight.  Bound by the bytes moved.
 #include "pages8.h"
 
 namespace c2kv {
 
 namespace {
 
-constexpr int PUT_THREADS = 256;
-constexpr int PUT_ROWS = 128;
+constexpr int PUT_MAX_ROWS = 128;
+constexpr int PUT_MIN_ROWS = 64;
 constexpr int PUT_WARP_ROWS = 16;
+
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Bits (as fp32) of the larger half.
+__device__ __forceinline__ uint32_t larger_half(uint32_t v) { return max(v & 0xFFFF0000u, v << 16); }
+
+// The codes of the two values of a word.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, float inv) {
+  return e4m3x2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xFFFF0000u) * inv);
+}
+
+// A word's halves that are not finite become NaN and take no part in m.
+__device__ __forceinline__ void tame(uint32_t& w, uint32_t& m) {
+  const uint32_t lo = w & 0x7FFFu, hi = (w >> 16) & 0x7FFFu;
+  if (lo >= 0x7F80u) w |= 0x7FFFu;
+  else m = max(m, lo << 16);
+  if (hi >= 0x7F80u) w |= 0x7FFF0000u;
+  else m = max(m, hi << 16);
+}
 
 // D: head_dim.  APPEND: rows [n_cached, n_cached + new) from the new tokens,
 // K rotated; else rows [0, n_rows) from the bf16 caches.
 template <int D, bool APPEND>
-__global__ void __launch_bounds__(PUT_THREADS) put_kernel(const __grid_constant__ PutParams p) {
-  constexpr int CH = D / 16;              // 8-element chunks of half a row
-  constexpr int IT = D / 32;              // items (one chunk of each half) per lane
+__global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, 3) put_kernel(const __grid_constant__ PutParams p) {
+  constexpr int CH = D / 16;              // items (16 elements) of a row
+  constexpr int IT = D / 32;              // items of a lane
   __shared__ uint32_t warp_max[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y / p.pool.n_kv, h = blockIdx.y % p.pool.n_kv;
   const int kv = blockIdx.z & 1, layer = blockIdx.z >> 1;
-  int first = 0, count;
+  const int rows = blockDim.x / 32 * PUT_WARP_ROWS;   // of a CTA
+  int first = 0, count, rr = 0;
   if (APPEND) {
     first = p.n_cached[b];
     count = p.n_new ? p.n_new[b] : p.t_len;
+    rr = p.rope_row[b];
     if (first < 0) return;   // an empty place of the batch
-    const int rr = p.rope_row[b];
     if (count < 0 || count > p.t_len || (int64_t)first + count > (int64_t)p.max_pages * p.pool.page ||
         (count > 0 && (rr < 0 || (int64_t)rr + count > p.table_rows))) {
       if (threadIdx.x == 0) atomicOr(p.err, kErrLength);
@@ -49,7 +73,7 @@ __global__ void __launch_bounds__(PUT_THREADS) put_kernel(const __grid_constant_
   } else {
     count = p.n_rows[b];
   }
-  const int row0 = (first / PUT_ROWS + (int)blockIdx.x) * PUT_ROWS;   // of this CTA's 128 rows
+  const int row0 = (first / rows + (int)blockIdx.x) * rows;   // of this CTA
   const int end = first + count;
   if (row0 >= end || count == 0) return;
   const int page = p.pool.page;
@@ -64,23 +88,76 @@ __global__ void __launch_bounds__(PUT_THREADS) put_kernel(const __grid_constant_
   float* scale = p.pool.scales[kv] + block;
   const bool has_old = APPEND && ok && prow < first;    // the page holds earlier rows
   const float old = has_old ? *scale : 0.f;
-
-  float lo[IT][8], hi[IT][8];
-  uint32_t m = 0;
+  auto source = [&](int r) {
+    return APPEND ? p.fresh[kv] + (((size_t)b * p.t_len + (r - first)) * p.pool.n_kv + h) * D
+                  : p.src[kv][b] + (((size_t)layer * p.pool.n_kv + h) * p.cap + r) * D;
+  };
+  auto in = [&](int r) { return ok && r >= first && r < end; };
+  // The values of the 16 rows, as bf16.  Rows to be rotated are held by pairs
+  // of a head's halves, two to a lane (w[2i] and w[2i + 1]: of the lane's i-th
+  // row), so that a warp reads a row of the RoPE table end to end; other rows
+  // by 16 neighbouring elements to a lane (w[8i..]: of its i-th item).
+  const bool turn = APPEND && kv == 0;
+  constexpr int LPR = D / 4, RPI = 32 / LPR, NI = PUT_WARP_ROWS / RPI;   // lanes of a row, rows at a time, times
+  uint32_t w[8 * IT];
+  static_assert(8 * IT == 2 * NI, "both forms hold 16 rows");
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int item = it * 32 + lane;
-    const int r = wrow + item / CH, c = item % CH;
-    if (!ok || r < first || r >= end) continue;
-    const __nv_bfloat16* src;
-    if (APPEND)
-      src = p.fresh[kv] + (((size_t)b * p.t_len + (r - first)) * p.pool.n_kv + h) * D;
-    else
-      src = p.src[kv][b] + (((size_t)layer * p.pool.n_kv + h) * p.cap + r) * D;
-    const uint4 x = reinterpret_cast<const uint4*>(src)[c], y = reinterpret_cast<const uint4*>(src)[c + CH];
-    const CosSin2* t = APPEND && kv == 0 ? p.tab + (size_t)(p.rope_row[b] + (r - first)) * (D / 2) + c * 8 : nullptr;
-    new_row8(x, y, t, lo[it], hi[it]);
-    m = max(m, max(max_finite8(lo[it]), max_finite8(hi[it])));
+  for (int i = 0; i < 8 * IT; ++i) w[i] = 0;
+  if (turn) {
+    const int pr = lane % LPR;   // the lane's pairs of the row: 2 pr, 2 pr + 1
+    uint32_t raw = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = wrow + i * RPI + lane / LPR;
+      if (in(r)) {
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(source(r));
+        w[2 * i] = src[pr];
+        w[2 * i + 1] = src[D / 4 + pr];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NI; ++i) raw = max_nan_bf16x2(raw, w[i] & 0x7FFF7FFFu);
+    const bool odd = __any_sync(0xffffffffu, larger_half(raw) >= 0x7F800000u);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int r = wrow + i * RPI + lane / LPR;
+      if (!in(r)) continue;
+      const CosSin2* t = p.tab + (size_t)(rr + r - first) * (D / 2) + 2 * pr;
+      const CosSin2 t0 = t[0], t1 = t[1];
+      const float x0 = __uint_as_float(w[2 * i] << 16), x1 = __uint_as_float(w[2 * i] & 0xFFFF0000u);
+      const float y0 = __uint_as_float(w[2 * i + 1] << 16), y1 = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u);
+      w[2 * i] = rot_bf16_bits(x0, t0.ch, t0.cl, -y0, t0.sh, t0.sl) |
+                 (rot_bf16_bits(x1, t1.ch, t1.cl, -y1, t1.sh, t1.sl) << 16);
+      w[2 * i + 1] = rot_bf16_bits(y0, t0.ch, t0.cl, x0, t0.sh, t0.sl) |
+                     (rot_bf16_bits(y1, t1.ch, t1.cl, x1, t1.sh, t1.sl) << 16);
+      if (odd) {   // a pair with a member that is not finite is NaN in both
+        const uint32_t nan = (fabsf(x0) < INFINITY && fabsf(y0) < INFINITY ? 0u : 0x7FFFu) |
+                             (fabsf(x1) < INFINITY && fabsf(y1) < INFINITY ? 0u : 0x7FFF0000u);
+        w[2 * i] |= nan;
+        w[2 * i + 1] |= nan;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int item = it * 32 + lane;
+      const int r = wrow + item / CH;
+      if (in(r)) {
+        const uint4* src = reinterpret_cast<const uint4*>(source(r)) + 2 * (item % CH);
+        const uint4 x = __ldcs(src), y = __ldcs(src + 1);
+        w[8 * it + 0] = x.x, w[8 * it + 1] = x.y, w[8 * it + 2] = x.z, w[8 * it + 3] = x.w;
+        w[8 * it + 4] = y.x, w[8 * it + 5] = y.y, w[8 * it + 6] = y.z, w[8 * it + 7] = y.w;
+      }
+    }
+  }
+  uint32_t m2 = 0;
+#pragma unroll
+  for (int i = 0; i < 8 * IT; ++i) m2 = max_nan_bf16x2(m2, w[i] & 0x7FFF7FFFu);
+  uint32_t m = larger_half(m2);
+  if (__any_sync(0xffffffffu, m >= 0x7F800000u)) {
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8 * IT; ++i) tame(w[i], m);
   }
   m = __reduce_max_sync(0xffffffffu, m);
   if (lane == 0) warp_max[warp] = m;
@@ -96,38 +173,62 @@ __global__ void __launch_bounds__(PUT_THREADS) put_kernel(const __grid_constant_
     e = max(e, e_old);
   }
   const float inv = pow2_float(-e);
-  const float by = pow2_float(max(e_old - e, -100));
+  if (turn) {
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int item = it * 32 + lane;
-    const int r = wrow + item / CH, c = item % CH;
-    uint2* dst = reinterpret_cast<uint2*>(codes + (size_t)(r - prow) * D);
-    if (r >= first && r < end) {
-      dst[c] = codes8(lo[it], inv);
-      dst[c + CH] = codes8(hi[it], inv);
-    } else if (APPEND && r < first && e > e_old) {
-      uint2 u = dst[c], v = dst[c + CH];
-      dst[c] = make_uint2(rescale4(u.x, by), rescale4(u.y, by));
-      dst[c + CH] = make_uint2(rescale4(v.x, by), rescale4(v.y, by));
+    for (int i = 0; i < NI; ++i) {
+      const int r = wrow + i * RPI + lane / LPR;
+      if (!in(r)) continue;
+      uint16_t* dst = reinterpret_cast<uint16_t*>(codes + (size_t)(r - prow) * D) + lane % LPR;
+      dst[0] = (uint16_t)codes2(w[2 * i], inv);
+      dst[D / 4] = (uint16_t)codes2(w[2 * i + 1], inv);
+    }
+  } else {
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int item = it * 32 + lane;
+      const int r = wrow + item / CH;
+      if (!in(r)) continue;
+      uint32_t c[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) c[k] = codes2(w[8 * it + 2 * k], inv) | (codes2(w[8 * it + 2 * k + 1], inv) << 16);
+      reinterpret_cast<uint4*>(codes + (size_t)(r - prow) * D)[item % CH] = make_uint4(c[0], c[1], c[2], c[3]);
+    }
+  }
+  if (APPEND && e > e_old) {   // a larger scale: the page's earlier codes follow
+    const float by = pow2_float(max(e_old - e, -100));
+#pragma unroll
+    for (int it = 0; it < IT; ++it) {
+      const int item = it * 32 + lane;
+      const int r = wrow + item / CH;
+      uint4* dst = reinterpret_cast<uint4*>(codes + (size_t)(r - prow) * D) + item % CH;
+      if (r < first) {
+        const uint4 u = *dst;
+        *dst = make_uint4(rescale4(u.x, by), rescale4(u.y, by), rescale4(u.z, by), rescale4(u.w, by));
+      }
     }
   }
   if (warp == w0 && lane == 0) *scale = pow2_float(e);
 }
 
+// Rows of a CTA for this page size.
+int put_rows(const PutParams& p) { return p.pool.page > PUT_MIN_ROWS ? PUT_MAX_ROWS : PUT_MIN_ROWS; }
+
 }  // namespace
 
 cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, cudaStream_t st) {
-  const dim3 grid((max_rows + PUT_ROWS - 1) / PUT_ROWS, p.batch * p.pool.n_kv, 2 * p.n_layers);
-  if (head_dim == 128) put_kernel<128, false><<<grid, PUT_THREADS, 0, st>>>(p);
-  else put_kernel<64, false><<<grid, PUT_THREADS, 0, st>>>(p);
+  const int rows = put_rows(p), threads = rows / PUT_WARP_ROWS * 32;
+  const dim3 grid((max_rows + rows - 1) / rows, p.batch * p.pool.n_kv, 2 * p.n_layers);
+  if (head_dim == 128) put_kernel<128, false><<<grid, threads, 0, st>>>(p);
+  else put_kernel<64, false><<<grid, threads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st) {
-  // rows [n, n + t_len) meet at most this many groups of 128 rows
-  const dim3 grid((p.t_len + 2 * PUT_ROWS - 2) / PUT_ROWS, p.batch * p.pool.n_kv, 2);
-  if (head_dim == 128) put_kernel<128, true><<<grid, PUT_THREADS, 0, st>>>(p);
-  else put_kernel<64, true><<<grid, PUT_THREADS, 0, st>>>(p);
+  // rows [n, n + t_len) meet at most this many CTAs' rows
+  const int rows = put_rows(p), threads = rows / PUT_WARP_ROWS * 32;
+  const dim3 grid((p.t_len + 2 * rows - 2) / rows, p.batch * p.pool.n_kv, 2);
+  if (head_dim == 128) put_kernel<128, true><<<grid, threads, 0, st>>>(p);
+  else put_kernel<64, true><<<grid, threads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
