@@ -504,43 +504,59 @@ def c2kv_rmsnorm(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, eps: float =
 
 
 # ---------------------------------------------------------------- 8-bit paged cache
+# These calls check every tensor (type, shape, contiguity, device) and still have
+# to be short: a decode step makes one per layer, and the kernel behind it may
+# take 10 us.
 C2KV_BF16, C2KV_F32 = 0, 1
-_E4M3 = torch.float8_e4m3fn
+_E4M3, _BF, _F32, _I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
 
 
-def _same_device(named, stream) -> None:
-    """Every tensor on the current device, where the launch goes, and with a
-    torch stream given, the stream as well."""
-    dev = torch.cuda.current_device()
-    for name, t in named:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{name} must be on the current CUDA device ({dev})")
-    if isinstance(stream, torch.cuda.Stream) and stream.device_index != dev:
-        raise ValueError(f"stream must be on the current CUDA device ({dev})")
-
-
-def _shape(t: torch.Tensor, shape, dtype, name: str) -> int:
-    """The address of t, which must have this shape and type and be contiguous."""
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+def _at(t: torch.Tensor, shape: tuple, dtype, dev: int, name: str) -> int:
+    """The address of t: contiguous, of this shape and type, on device dev."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current CUDA device, like the call's other tensors")
     return t.data_ptr()
 
 
-def _pages8(g, k8, v8, k_scale, v_scale) -> c2kv_pages8:
-    if k8.dim() != 5:
+def _launch_stream(stream, dev: int) -> int:
+    """The raw stream, and that the tensors' device is the current one, where the launch goes."""
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current CUDA device")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"stream must be on the current CUDA device ({dev})")
+        return stream.cuda_stream
+    return int(stream)
+
+
+def _pages8(g, k8, v8, k_scale, v_scale, dev: int) -> c2kv_pages8:
+    shape = k8.shape
+    if len(shape) != 5:
         raise ValueError("k8 must be [n_layers][n_pages][n_kv_heads][page][head_dim]")
-    n_pages, page = k8.shape[1], k8.shape[3]
-    pool = (g.n_layers, n_pages, g.n_kv_heads, page, g.head_dim)
-    return c2kv_pages8(_shape(k8, pool, _E4M3, "k8"), _shape(v8, pool, _E4M3, "v8"),
-                       _shape(k_scale, pool[:3], torch.float32, "k_scale"),
-                       _shape(v_scale, pool[:3], torch.float32, "v_scale"), n_pages, page)
+    n_pages, page = shape[1], shape[3]
+    layers, heads = g.n_layers, g.n_kv_heads
+    pool, scales = (layers, n_pages, heads, page, g.head_dim), (layers, n_pages, heads)
+    return c2kv_pages8(_at(k8, pool, _E4M3, dev, "k8"), _at(v8, pool, _E4M3, dev, "v8"),
+                       _at(k_scale, scales, _F32, dev, "k_scale"), _at(v_scale, scales, _F32, dev, "v_scale"),
+                       n_pages, page)
 
 
-def _rope_rows(g, rope_table, rope_row_dev, batch: int):
-    """(address, rows) of a RoPE table and the address of the [batch] rows."""
-    row = g.head_dim // 2 * 16
-    return _dev(rope_table, None, "rope_table"), _nbytes(rope_table) // row, \
-        _shape(rope_row_dev, (batch,), torch.int32, "rope_row_dev")
+def _page_table(t: torch.Tensor, batch: int, dev: int):
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError("page_table must be [batch][max_pages]")
+    return _at(t, (batch, shape[1]), _I32, dev, "page_table"), shape[1]
+
+
+def _rope_rows(g, rope_table, dev: int):
+    """Address and rows of a RoPE table (any type)."""
+    if not rope_table.is_contiguous() or rope_table.get_device() != dev:
+        raise ValueError("rope_table must be contiguous and on the current CUDA device")
+    return rope_table.data_ptr(), rope_table.nbytes // (g.head_dim // 2 * 16)
 
 
 def c2kv_pages8_fill(geom, layer_begin: int, layer_end: int, k_caches, v_caches, cap: int, n_rows,
@@ -553,20 +569,23 @@ def c2kv_pages8_fill(geom, layer_begin: int, layer_end: int, k_caches, v_caches,
     batch = len(k_caches)
     if not (len(v_caches) == len(n_rows) == batch):
         raise ValueError("k_caches, v_caches and n_rows need one entry per sequence")
-    cache = 2 * g.n_layers * g.n_kv_heads * max(0, int(cap)) * g.head_dim
-    named = [("k8", k8), ("v8", v8), ("k_scale", k_scale), ("v_scale", v_scale), ("page_table", page_table)]
-    for b in range(batch):
-        _need(k_caches[b], cache, f"k_caches[{b}]")
-        _need(v_caches[b], cache, f"v_caches[{b}]")
-        named += [(f"k_caches[{b}]", k_caches[b]), (f"v_caches[{b}]", v_caches[b])]
-    pages = _pages8(g, k8, v8, k_scale, v_scale)
-    if page_table.dim() != 2:
-        raise ValueError("page_table must be [batch][max_pages]")
-    table = _shape(page_table, (batch, page_table.shape[1]), torch.int32, "page_table")
-    _same_device(named, stream)
-    _check(load_library().c2kv_pages8_fill(
-        ctypes.byref(g), ctypes.byref(pages), int(layer_begin), int(layer_end), batch, _ptrs(k_caches, "k_cache"),
-        _ptrs(v_caches, "v_cache"), int(cap), _i32arr(n_rows), table, page_table.shape[1], _stream(stream)))
+    dev = k8.get_device()
+    pages = _pages8(g, k8, v8, k_scale, v_scale, dev)
+    table, max_pages = _page_table(page_table, batch, dev)
+    need = g.n_layers * g.n_kv_heads * max(0, int(cap)) * g.head_dim
+    ptrs = []
+    for caches, name in ((k_caches, "k_caches"), (v_caches, "v_caches")):
+        at = (ctypes.c_void_p * batch)()
+        for b, t in enumerate(caches):
+            if t.dtype is not _BF or t.numel() < need or not t.is_contiguous() or t.get_device() != dev:
+                raise ValueError(f"{name}[{b}] must be a contiguous bfloat16 tensor of at least {need} elements "
+                                 f"on the current CUDA device, got {t.dtype} {tuple(t.shape)} on {t.device}")
+            at[b] = t.data_ptr()
+        ptrs.append(at)
+    st = _launch_stream(stream, dev)
+    _check((_lib or load_library()).c2kv_pages8_fill(
+        ctypes.byref(g), ctypes.byref(pages), int(layer_begin), int(layer_end), batch, ptrs[0], ptrs[1], int(cap),
+        _i32arr(n_rows), table, max_pages, st))
 
 
 def c2kv_pages8_append(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
@@ -576,20 +595,18 @@ def c2kv_pages8_append(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_s
     """Rotates and appends k_new, v_new [batch][t_len][n_kv_heads][head_dim] to
     8-bit pages; n_new_dev: int32 [batch] tokens of a padded batch."""
     g = as_geometry(geom)
+    dev = k8.get_device()
     batch, t_len = k_new.shape[:2]
-    pages = _pages8(g, k8, v8, k_scale, v_scale)
-    new = (batch, t_len, g.n_kv_heads, g.head_dim)
-    table = _shape(page_table, (batch, page_table.shape[-1]), torch.int32, "page_table")
-    rope, rope_rows, rope_row = _rope_rows(g, rope_table, rope_row_dev, batch)
-    _same_device([("k8", k8), ("v8", v8), ("k_scale", k_scale), ("v_scale", v_scale), ("page_table", page_table),
-                  ("n_cached_dev", n_cached_dev), ("n_new_dev", n_new_dev), ("k_new", k_new), ("v_new", v_new),
-                  ("rope_table", rope_table), ("rope_row_dev", rope_row_dev)], stream)
-    _check(load_library().c2kv_pages8_append(
-        ctypes.byref(g), ctypes.byref(pages), int(layer), batch, t_len, table, page_table.shape[1],
-        _shape(n_cached_dev, (batch,), torch.int32, "n_cached_dev"),
-        0 if n_new_dev is None else _shape(n_new_dev, (batch,), torch.int32, "n_new_dev"),
-        _shape(k_new, new, torch.bfloat16, "k_new"), _shape(v_new, new, torch.bfloat16, "v_new"), rope, rope_rows,
-        rope_row, _stream(stream)))
+    pages = _pages8(g, k8, v8, k_scale, v_scale, dev)
+    table, max_pages = _page_table(page_table, batch, dev)
+    new, one = (batch, t_len, g.n_kv_heads, g.head_dim), (batch,)
+    rope, rope_rows = _rope_rows(g, rope_table, dev)
+    st = _at(n_cached_dev, one, _I32, dev, "n_cached_dev"), \
+        0 if n_new_dev is None else _at(n_new_dev, one, _I32, dev, "n_new_dev"), \
+        _at(k_new, new, _BF, dev, "k_new"), _at(v_new, new, _BF, dev, "v_new"), rope, rope_rows, \
+        _at(rope_row_dev, one, _I32, dev, "rope_row_dev"), _launch_stream(stream, dev)
+    _check((_lib or load_library()).c2kv_pages8_append(
+        ctypes.byref(g), ctypes.byref(pages), int(layer), batch, t_len, table, max_pages, *st))
 
 
 def c2kv_attend_pages8_workspace_size(geom, batch: int, max_keys: int) -> int:
@@ -605,23 +622,21 @@ def c2kv_attend_pages8(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_s
     """One decode step of one layer over 8-bit pages, its token's append
     included (k_new, v_new None: over the held rows alone)."""
     g = as_geometry(geom)
-    batch = q.shape[0]
-    pages = _pages8(g, k8, v8, k_scale, v_scale)
-    heads, new = (batch, g.n_q_heads, g.head_dim), (batch, g.n_kv_heads, g.head_dim)
-    table = _shape(page_table, (batch, page_table.shape[-1]), torch.int32, "page_table")
-    rope, rope_rows, rope_row = _rope_rows(g, rope_table, rope_row_dev, batch)
-    _same_device([("k8", k8), ("v8", v8), ("k_scale", k_scale), ("v_scale", v_scale), ("page_table", page_table),
-                  ("n_cached_dev", n_cached_dev), ("q", q), ("k_new", k_new), ("v_new", v_new),
-                  ("rope_table", rope_table), ("rope_row_dev", rope_row_dev), ("out", out),
-                  ("workspace", workspace)], stream)
-    _check(load_library().c2kv_attend_pages8(
-        ctypes.byref(g), ctypes.byref(pages), int(layer), batch, table, page_table.shape[1],
-        _shape(n_cached_dev, (batch,), torch.int32, "n_cached_dev"), int(max_keys),
-        _shape(q, heads, torch.bfloat16, "q"),
-        0 if k_new is None else _shape(k_new, new, torch.bfloat16, "k_new"),
-        0 if v_new is None else _shape(v_new, new, torch.bfloat16, "v_new"), rope, rope_rows, rope_row,
-        _shape(out, heads, torch.bfloat16, "out"), _dev(workspace, None, "workspace"), _nbytes(workspace),
-        int(flags), _stream(stream)))
+    dev = k8.get_device()
+    batch, d = q.shape[0], g.head_dim
+    pages = _pages8(g, k8, v8, k_scale, v_scale, dev)
+    table, max_pages = _page_table(page_table, batch, dev)
+    heads, new, one = (batch, g.n_q_heads, d), (batch, g.n_kv_heads, d), (batch,)
+    rope, rope_rows = _rope_rows(g, rope_table, dev)
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous and on the current CUDA device")
+    _check((_lib or load_library()).c2kv_attend_pages8(
+        ctypes.byref(g), ctypes.byref(pages), int(layer), batch, table, max_pages,
+        _at(n_cached_dev, one, _I32, dev, "n_cached_dev"), int(max_keys), _at(q, heads, _BF, dev, "q"),
+        0 if k_new is None else _at(k_new, new, _BF, dev, "k_new"),
+        0 if v_new is None else _at(v_new, new, _BF, dev, "v_new"), rope, rope_rows,
+        _at(rope_row_dev, one, _I32, dev, "rope_row_dev"), _at(out, heads, _BF, dev, "out"), workspace.data_ptr(),
+        workspace.nbytes, int(flags), _launch_stream(stream, dev)))
 
 
 def c2kv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], top_k: int,
@@ -632,19 +647,17 @@ def c2kv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], to
     each row of logits [rows][vocab] (bf16 or fp32, rows any stride apart)."""
     if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         raise ValueError("logits must be [rows][vocab] with neighbouring logits of a row side by side")
-    if logits.dtype not in (torch.bfloat16, torch.float32):
-        raise ValueError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    dtype = logits.dtype
+    if dtype is not _BF and dtype is not _F32:
+        raise ValueError(f"logits must be bfloat16 or float32, got {dtype}")
     rows, vocab = logits.shape
-    f32, i32 = torch.float32, torch.int32
-
-    def opt(t, shape, dtype, name):
-        return 0 if t is None else _shape(t, shape, dtype, name)
-
-    _same_device([("logits", logits), ("tokens", tokens), ("logprob", logprob), ("entropy", entropy),
-                  ("top_ids", top_ids), ("top_logprobs", top_logprobs)], stream)
-    _check(load_library().c2kv_token_logprobs(
-        logits.data_ptr(), C2KV_F32 if logits.dtype == f32 else C2KV_BF16, rows, vocab,
+    dev, one, k = logits.get_device(), (rows,), int(top_k)
+    _check((_lib or load_library()).c2kv_token_logprobs(
+        logits.data_ptr(), C2KV_F32 if dtype is _F32 else C2KV_BF16, rows, vocab,
         logits.stride(0) if rows > 1 else max(vocab, logits.stride(0)),
-        opt(tokens, (rows,), i32, "tokens"), int(top_k), opt(logprob, (rows,), f32, "logprob"),
-        opt(entropy, (rows,), f32, "entropy"), opt(top_ids, (rows, top_k), i32, "top_ids"),
-        opt(top_logprobs, (rows, top_k), f32, "top_logprobs"), _stream(stream)))
+        0 if tokens is None else _at(tokens, one, _I32, dev, "tokens"), k,
+        0 if logprob is None else _at(logprob, one, _F32, dev, "logprob"),
+        0 if entropy is None else _at(entropy, one, _F32, dev, "entropy"),
+        0 if top_ids is None else _at(top_ids, (rows, k), _I32, dev, "top_ids"),
+        0 if top_logprobs is None else _at(top_logprobs, (rows, k), _F32, dev, "top_logprobs"),
+        _launch_stream(stream, dev)))
