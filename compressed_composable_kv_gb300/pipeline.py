@@ -24,10 +24,17 @@ class RequestSpec:
 
 
 class RequestBatch:
-    """Device state of `len(requests)` composed requests sharing one store."""
+    """Device state of `len(requests)` composed requests sharing one store.
+
+    page8: tokens of a page (16, 32, 64 or 128) to decode over an 8-bit paged
+    cache, half the bytes of the bf16 one: after composition and question
+    prefill, fill_pages8 takes the bf16 rows over, and decode appends to and
+    attends over the pages.
+    """
 
     def __init__(self, store: int, geom, requests: Sequence[RequestSpec], k: int, q_len: int,
-                 decode_steps: int, device: str = "cuda", cap_multiple: int = 32, realign: bool = True):
+                 decode_steps: int, device: str = "cuda", cap_multiple: int = 32, realign: bool = True,
+                 page8: Optional[int] = None):
         self.store, self.geom, self.k = store, geom, k
         # realign=False: the "no position re-alignment" ablation (documents
         # keep their extraction positions)
@@ -54,17 +61,34 @@ class RequestBatch:
         self.pos = [torch.full((self.cap,), -1, dtype=torch.int32, device=device)
                     for _ in range(self.batch)]
         tb = B.c2kv_rope_table_bytes(geom, self.cap)
-        self.rope_tables = [torch.empty(tb // 4, dtype=torch.float32, device=device)
-                            for _ in range(self.batch)]
-        self.n_cached_dev = torch.zeros(self.batch, dtype=torch.int32, device=device)
+        # one allocation, so that it is also the table of the paged calls, where
+        # request b's row r is row b * cap + r
+        self.rope_table = torch.empty((self.batch, tb // 4), dtype=torch.float32, device=device)
+        self.rope_tables = list(self.rope_table)
+        # lengths and RoPE rows advance together
+        self._lengths = torch.zeros((2, self.batch), dtype=torch.int32, device=device)
+        self.n_cached_dev, self.rope_row_dev = self._lengths
         self.max_keys_decode = max(self.n_slots) + q_len + decode_steps
         ws = 256
         if q_len > 0:
             ws = max(ws, B.c2kv_attend_workspace_size(geom, self.batch, q_len, max(self.n_slots) + q_len))
         ws = max(ws, B.c2kv_attend_workspace_size(geom, self.batch, 1, self.max_keys_decode))
+        self.page8 = page8
+        if page8 is not None:
+            most = -(-self.max_keys_decode // page8)
+            n_pages = most * self.batch
+            self.page_table = torch.arange(n_pages, dtype=torch.int32, device=device).reshape(self.batch, most)
+            self.k8 = torch.empty((L, n_pages, H, page8, D), dtype=torch.float8_e4m3fn, device=device)
+            self.v8 = torch.empty_like(self.k8)
+            self.k_scale = torch.empty((L, n_pages, H), dtype=torch.float32, device=device)
+            self.v_scale = torch.empty_like(self.k_scale)
+            # of its own: the other calls' scratch would overwrite its counters
+            self.workspace8 = torch.zeros(B.c2kv_attend_pages8_workspace_size(geom, self.batch, self.max_keys_decode),
+                                          dtype=torch.uint8, device=device)
         self.workspace = torch.zeros(ws, dtype=torch.uint8, device=device)
         B.c2kv_workspace_init(self.workspace)
-        self._dec_start = torch.tensor([n + q_len for n in self.n_slots], dtype=torch.int32)
+        start = [n + q_len for n in self.n_slots]
+        self._dec_start = torch.tensor([start, [b * self.cap + n for b, n in enumerate(start)]], dtype=torch.int32)
 
     def compose(self, stream=None) -> None:
         self.compose_layers(0, self.geom.n_layers, stream)
@@ -90,7 +114,13 @@ class RequestBatch:
         """Point the device lengths at the first decode step (after the question)."""
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
-            self.n_cached_dev.copy_(self._dec_start, non_blocking=True)
+            self._lengths.copy_(self._dec_start, non_blocking=True)
+
+    def fill_pages8(self, layer_begin: int = 0, layer_end: Optional[int] = None, stream=None) -> None:
+        """The composed and prefilled rows of layers [layer_begin, layer_end) to the 8-bit pages."""
+        B.c2kv_pages8_fill(self.geom, layer_begin, self.geom.n_layers if layer_end is None else layer_end,
+                           self.k_caches, self.v_caches, self.cap, [n + self.q_len for n in self.n_slots],
+                           self.k8, self.v8, self.k_scale, self.v_scale, self.page_table, stream)
 
     def decode(self, layer: int, q, k_new, v_new, out, stream=None, overlap_previous: Optional[bool] = None) -> None:
         """One decode step of one layer.  By default a layer > 0 call may start
@@ -98,12 +128,20 @@ class RequestBatch:
         layer before) finishes: see C2KV_DECODE_OVERLAP_PREVIOUS."""
         if overlap_previous is None:
             overlap_previous = layer > 0
+        if self.page8 is not None:
+            B.c2kv_attend_pages8(self.geom, layer, self.k8, self.v8, self.k_scale, self.v_scale, self.page_table,
+                                 self.n_cached_dev, self.max_keys_decode, q.view(self.batch, -1, self.geom.head_dim),
+                                 k_new.view(self.batch, -1, self.geom.head_dim),
+                                 v_new.view(self.batch, -1, self.geom.head_dim), self.rope_table, self.rope_row_dev,
+                                 out.view(self.batch, -1, self.geom.head_dim), self.workspace8, stream,
+                                 B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0)
+            return
         B.c2kv_attend_decode(self.geom, layer, self.k_caches, self.v_caches, self.rope_tables, self.cap,
                              self.n_cached_dev, self.max_keys_decode, q, k_new, v_new, out, self.workspace,
                              stream, B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0)
 
     def advance(self, stream=None) -> None:
-        B.c2kv_seq_advance(self.n_cached_dev, 1, stream)
+        B.c2kv_seq_advance(self._lengths, 1, stream)
 
 
 class DecoderModel:
@@ -121,7 +159,7 @@ class DecoderModel:
     weights: dict as synth.make_decoder_weights, values device bf16 tensors.
     """
 
-    def __init__(self, geom, shape, weights: dict, batch: int, device: str = "cuda"):
+    def __init__(self, geom, shape, weights: dict, batch: int, device: str = "cuda", top_k: int = 0):
         self.geom, self.shape, self.w = geom, shape, weights
         self.batch = batch
         d = geom.head_dim
@@ -137,6 +175,10 @@ class DecoderModel:
         self.att, self.m = buf(nb, self.nq), buf(nb, F)
         has_head = "lm_head" in weights
         self.logits = buf(nb, shape.vocab) if has_head else None
+        # token_logprobs' results
+        self.logprob, self.entropy = (torch.zeros(nb, device=device) for _ in range(2))
+        self.top_ids = torch.zeros((nb, top_k), dtype=torch.int32, device=device)
+        self.top_logprobs = torch.zeros((nb, top_k), device=device)
         widest = max(self.nq + 2 * self.nkv, 2 * F, dim, shape.vocab if has_head else 0)
         self.workspace = torch.zeros(B.c2kv_linear_workspace_size(nb, widest), dtype=torch.uint8, device=device)
         B.c2kv_workspace_init(self.workspace)
@@ -169,6 +211,13 @@ class DecoderModel:
             B.c2kv_linear(self.h, self.w["lm_head"], self.logits, self.workspace, stream=stream,
                            flags=B.C2KV_LINEAR_OVERLAP_PREVIOUS)
         rb.advance(stream)
+
+    def token_logprobs(self, tokens: torch.Tensor, stream=None) -> None:
+        """Of the last step's logits: logprob of tokens [batch] (int32 on the
+        device; negative: none), entropy, and the top_k alternatives in top_ids
+        and top_logprobs."""
+        B.c2kv_token_logprobs(self.logits, tokens, self.top_ids.shape[1], self.logprob, self.entropy, self.top_ids,
+                              self.top_logprobs, stream)
 
     def linears_only(self, stream=None) -> None:
         """The step's linear layers and norms without the attention (their

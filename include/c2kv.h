@@ -508,8 +508,9 @@ c2kv_status c2kv_pages8_append(const c2kv_geometry* geom, const c2kv_pages8* pag
  * q, out: device bf16 [batch][n_q_heads][head_dim].  max_keys bounds the rows
  * attended over by every sequence and sizes the launch; a sequence with more
  * is left out.  workspace: c2kv_attend_pages8_workspace_size bytes, 16-byte
- * aligned, zeroed once (c2kv_workspace_init), then reused by calls that do
- * not overlap on the GPU.  flags: C2KV_DECODE_OVERLAP_PREVIOUS, as in
+ * aligned, zeroed once (c2kv_workspace_init), then reused by c2kv_attend_pages8
+ * calls of the same geometry that do not overlap on the GPU (other calls'
+ * scratch would overwrite its counters).  flags: C2KV_DECODE_OVERLAP_PREVIOUS, as in
  * c2kv_attend_decode: the kernel before on `stream` must not write the
  * lengths, the page table, the RoPE table or this layer's held rows.
  */
@@ -564,7 +565,8 @@ c2kv_status c2kv_kernel_launches(uint64_t* count);
  * the kernel takes its timeout path: it records C2KV_ETIMEOUT in the device
  * error word, lets its copies in flight land and returns; that launch's
  * outputs are undefined, the cache rows it appends are written, and the
- * context stays usable.  0 disarms it.  Process-wide; C2KV_EINVAL for n < 0.
+ * context stays usable.  c2kv_attend_pages8 counts among them; the rows it
+ * appends may then be missing.  0 disarms it.  Process-wide; C2KV_EINVAL for n < 0.
  */
 c2kv_status c2kv_test_expire_next_waits(int32_t n_launches);
 
