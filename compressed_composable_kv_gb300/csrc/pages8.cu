@@ -126,10 +126,10 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, 3) put_kern
       const CosSin2 t0 = t[0], t1 = t[1];
       const float x0 = __uint_as_float(w[2 * i] << 16), x1 = __uint_as_float(w[2 * i] & 0xFFFF0000u);
       const float y0 = __uint_as_float(w[2 * i + 1] << 16), y1 = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u);
-      w[2 * i] = rot_bf16_bits(x0, t0.ch, t0.cl, -y0, t0.sh, t0.sl) |
-                 (rot_bf16_bits(x1, t1.ch, t1.cl, -y1, t1.sh, t1.sl) << 16);
-      w[2 * i + 1] = rot_bf16_bits(y0, t0.ch, t0.cl, x0, t0.sh, t0.sl) |
-                     (rot_bf16_bits(y1, t1.ch, t1.cl, x1, t1.sh, t1.sl) << 16);
+      w[2 * i] = rot_key_bits(x0, t0.ch, t0.cl, -y0, t0.sh, t0.sl) |
+                 (rot_key_bits(x1, t1.ch, t1.cl, -y1, t1.sh, t1.sl) << 16);
+      w[2 * i + 1] = rot_key_bits(y0, t0.ch, t0.cl, x0, t0.sh, t0.sl) |
+                     (rot_key_bits(y1, t1.ch, t1.cl, x1, t1.sh, t1.sl) << 16);
       if (odd) {   // a pair with a member that is not finite is NaN in both
         const uint32_t nan = (fabsf(x0) < INFINITY && fabsf(y0) < INFINITY ? 0u : 0x7FFFu) |
                              (fabsf(x1) < INFINITY && fabsf(y1) < INFINITY ? 0u : 0x7FFF0000u);

@@ -41,6 +41,26 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   return f;
 }
 
+// a (bh + bl) + c (dh + dl), one element of a rotated key, rounded to fp32 and
+// from there to bf16 (the two roundings of a conversion that goes by way of
+// fp32; they differ from a single one in about 2^-17 of elements).  Where the
+// fp32 evaluation decides, it is rot_bf16_bits' fast path; the bounds are its.
+static __device__ __noinline__ uint32_t rot_key_slow(float a, float bh, float bl, float c, float dh, float dl) {
+  float hi, lo;
+  dot2_df(a, bh, bl, c, dh, dl, hi, lo);
+  return bf16_bits_rn(hi);
+}
+
+__device__ __forceinline__ uint32_t rot_key_bits(float a, float bh, float bl, float c, float dh, float dl) {
+  const float p = __fmul_rn(c, dh);
+  const float r = fmaf(a, bh, p);
+  const float m = __fadd_rn(fabsf(__fmul_rn(a, bh)), fabsf(p));   // 2^21 times the error bound
+  const uint32_t bits = __float_as_uint(r);
+  const float mid = __uint_as_float((bits & 0xFFFF0000u) | 0x8000u);
+  if (__fmul_rn(fabsf(__fsub_rn(r, mid)), 0x1p21f) > m && __fmul_rn(fabsf(r), 0x1p11f) > m) return bf16_bits_rn(r);
+  return rot_key_slow(a, bh, bl, c, dh, dl);
+}
+
 // 8 bf16 bit patterns -> fp32, NaN where not finite.
 __device__ __forceinline__ void finite_or_nan8(const uint4& u, float (&f)[8]) {
   unpack8(u, f);
@@ -53,16 +73,22 @@ __device__ __forceinline__ void finite_or_nan8(const uint4& u, float (&f)[8]) {
 // they are, or (t: the 8 cos/sin of these pairs) rotated and rounded to bf16,
 // as a bf16 cache holds a key.  NaN where not finite; a pair with a member
 // that is not finite is NaN in both.
-__device__ __forceinline__ void new_row8(uint4 x, uint4 y, const CosSin2* t, float (&lo)[8], float (&hi)[8]) {
+__device__ __forceinline__ void new_row8(const uint4& x, const uint4& y, const CosSin2* t, float (&lo)[8], float (&hi)[8]) {
   finite_or_nan8(x, lo);
   finite_or_nan8(y, hi);
   if (t == nullptr) return;
   bool bad[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) bad[e] = !(lo[e] == lo[e] && hi[e] == hi[e]);
-  rotate8_df(x, y, t);
-  finite_or_nan8(x, lo);
-  finite_or_nan8(y, hi);
+  uint32_t xo[8], yo[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const CosSin2 te = t[e];
+    xo[e] = rot_key_bits(lo[e], te.ch, te.cl, -hi[e], te.sh, te.sl);   // x cos - y sin
+    yo[e] = rot_key_bits(hi[e], te.ch, te.cl, lo[e], te.sh, te.sl);    // y cos + x sin
+  }
+  finite_or_nan8(pack_bits8(xo), lo);
+  finite_or_nan8(pack_bits8(yo), hi);
 #pragma unroll
   for (int e = 0; e < 8; ++e)
     if (bad[e]) lo[e] = hi[e] = __uint_as_float(0x7FFFFFFFu);

@@ -488,8 +488,8 @@ c2kv_status c2kv_pages8_fill(const c2kv_geometry* geom, const c2kv_pages8* pages
  * to row n_cached_dev[b] + i.  k_new, v_new: device bf16 [batch][t_len]
  * [n_kv_heads][head_dim], k before RoPE.  rope_table: device table of
  * table_rows rows (layout of c2kv_rope_table); token i's key is rotated by its
- * row rope_row_dev[b] + i and rounded to bf16, as a bf16 cache would hold it,
- * before it is rounded to its code.  The lengths are not advanced
+ * row rope_row_dev[b] + i, rounded to fp32 and from there to bf16, about as a
+ * bf16 cache would hold it, before it is rounded to its code.  The lengths are not advanced
  * (c2kv_seq_advance).  batch <= 256.  A sequence whose tokens would not fit
  * max_pages pages, or whose table rows are out of range, is left out whole.
  */

@@ -1,8 +1,9 @@
 """The 8-bit paged cache (filling, appending, attending) and the token log
 probabilities against the fp64 oracle (oracle/pages8_oracle.py).
 
-Bars.  Codes and scales: equal.  The rotated key is the correctly rounded
-bf16 rotation (the RoPE table holds cos and sin to 2^-48), the scaling is by a
+Bars.  Codes and scales: equal.  The rotated key is the exact rotation rounded
+to fp32 and then to bf16 (the RoPE table holds cos and sin to 2^-48, so the
+kernel's value before the first rounding is exact to 2^-44), the scaling is by a
 power of two and the code is one rounding, so there is nothing to be off by.
 Attention: the output's own bf16 rounding, 2^-8 |ref|, and the kernel's error:
 its logits are off by at most ds = 2^-14 max|q| sum_i|K_ji| / sqrt(d) (the
@@ -120,11 +121,11 @@ def _rotate(g, x, pos):
 
 
 def _round_key(x):
-    """To bf16; a pair with a member that is not finite is not finite."""
+    """To fp32, then to bf16; a pair with a member that is not finite is not finite."""
     h = x.shape[-1] // 2
     bad = ~np.isfinite(x[..., :h]) | ~np.isfinite(x[..., h:])
     bad = np.concatenate([bad, bad], -1)
-    y = O.bf16_to_f64(O.f64_to_bf16(np.where(bad, 0.0, x)))
+    y = O.bf16_to_f64(O.f64_to_bf16(np.where(bad, 0.0, x).astype(np.float32).astype(np.float64)))
     return np.where(bad, np.nan, y)
 
 
