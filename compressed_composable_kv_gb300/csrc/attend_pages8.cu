@@ -75,18 +75,21 @@ struct ApCfg {
   // about 0.8 us, an SM's share of HBM brings one in 0.73 us); each has as many
   // stages as half an SM holds.
   static constexpr int STAGES = NPAD == 16 ? 3 : 2;
+  // A tile's scales are read until its s_free, a stage of K may be filled again
+  // from QK on: twice the slots.
+  static constexpr int SCALES = 2 * STAGES;
   static constexpr int OP_BYTES = NPAD * 128;           // query or P^T operand [NPAD][128 bytes]
   static constexpr int RED = 12;                        // per warp: G maxima (or sums), the largest V scale
   static constexpr int OFF_Q = STAGES * AP_STAGE;       // two buffers each
   static constexpr int OFF_P = OFF_Q + 2 * OP_BYTES;
   static constexpr int OFF_MAP = OFF_P + 2 * OP_BYTES;
   static constexpr int OFF_RED = OFF_MAP + (int)((sizeof(PageMap) + 15) / 16 * 16);
-  static constexpr int OFF_SC = OFF_RED + 2 * 4 * RED * 4;                  // [STAGES][2][AP_MAX_PPT] scales
-  static constexpr int OFF_QS = OFF_SC + STAGES * 2 * AP_MAX_PPT * 4;       // [4][8] the query's scales: read
+  static constexpr int OFF_SC = OFF_RED + 2 * 4 * RED * 4;                  // [SCALES][2][AP_MAX_PPT] scales
+  static constexpr int OFF_QS = OFF_SC + SCALES * 2 * AP_MAX_PPT * 4;       // [4][8] the query's scales: read
   // until s_free, two units behind q_free
   static constexpr int OFF_X = OFF_QS + 4 * 8 * 4;                          // KPR == 2: [G][128] output exchange
   static constexpr int OFF_BAR = OFF_X + (KPR == 2 ? G * 128 * 4 : 0);
-  static constexpr int N_BAR = 5 * STAGES + 2 * 8 + 2;
+  static constexpr int N_BAR = 6 * STAGES + 2 * 8 + 2;
   static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;     // + slack for 1024-byte alignment
   static_assert(OP_BYTES % 1024 == 0, "swizzled operands need 1024-byte alignment");
@@ -237,8 +240,9 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   uint64_t* v_full = k_full + C::STAGES;
   uint64_t* fix_k = v_full + C::STAGES;    // a unit's last tile: the new key is in it
   uint64_t* fix_v = fix_k + C::STAGES;     // and the new value, and V's tail is zero
-  uint64_t* kv_empty = fix_v + C::STAGES;
-  uint64_t* s_full = kv_empty + C::STAGES;
+  uint64_t* k_empty = fix_v + C::STAGES;
+  uint64_t* v_empty = k_empty + C::STAGES;
+  uint64_t* s_full = v_empty + C::STAGES;
   uint64_t* s_free = s_full + 2;
   uint64_t* p_full = s_free + 2;
   uint64_t* p_free = p_full + 2;
@@ -338,7 +342,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         mbar_init(&v_full[s], 1);
         mbar_init(&fix_k[s], 1);
         mbar_init(&fix_v[s], 1);
-        mbar_init(&kv_empty[s], 1);
+        mbar_init(&k_empty[s], 1);
+        mbar_init(&v_empty[s], 1);
       }
       for (int i = 0; i < 2; ++i) {
         mbar_init(&s_full[i], 1);
@@ -425,6 +430,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     const int lgp = C::TILE_LG - lg;                   // log2 of a tile's pages
     const int ppt = 1 << lgp, per = 32 >> lgp;         // pages of a tile, tiles of a batch
     uint64_t* full = kv == 0 ? k_full : v_full;
+    uint64_t* empty = kv == 0 ? k_empty : v_empty;
     struct Ref {
       int32_t id, h;   // id: -1 no page here, -2 outside the pool
       float ks, vs;
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         const int j = j0 + tt, s = j % C::STAGES, i = lane & (ppt - 1);
         if (!before(j)) return false;
         if (j >= C::STAGES &&
-            !__all_sync(0xffffffffu, ap_wait(&kv_empty[s], ((j - C::STAGES) / C::STAGES) & 1, abort_flag, p.err)))
+            !__all_sync(0xffffffffu, ap_wait(&empty[s], ((j - C::STAGES) / C::STAGES) & 1, abort_flag, p.err)))
           return false;
         if ((lane >> lgp) == tt) {
           // no page, or one outside the pool: a load from before the pool, which
@@ -474,8 +480,9 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           const int y = cur.id >= 0 ? (cur.id * p.pool.n_kv + cur.h) * prows : -prows;
           tma_load_2d((kv == 0 ? stage_k(s) : stage_v(s)) + i * prows * 128, &p.tm[kv], 0, y, &full[s]);
           if (kv == 0) {
-            sc[(s * 2 + 0) * AP_MAX_PPT + i] = cur.ks;
-            sc[(s * 2 + 1) * AP_MAX_PPT + i] = cur.vs;
+            float* scs = sc + j % C::SCALES * 2 * AP_MAX_PPT;
+            scs[i] = cur.ks;
+            scs[AP_MAX_PPT + i] = cur.vs;
           }
         }
         __syncwarp();
@@ -510,7 +517,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         for (int kk = 0; kk < 4; ++kk)   // 32 rows of V at a time
           mma_e4m3(tmem + C::TMEM_O + pb * C::NPAD, sw128_desc(smem_addr(stage_v(s)) + kk * 4096, AP_KV_BYTES, 1024),
                    sw128_desc(smem_addr(sP + pb * C::OP_BYTES) + kk * 32, 16, 1024), idesc_pv, kk > 0 ? 1u : 0u);
-        mma_commit(&kv_empty[s]);
+        mma_commit(&v_empty[s]);
         mma_commit(&p_free[pb]);
         mma_commit(&o_full[pb]);
         return true;
@@ -535,6 +542,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
                      sw128_desc(smem_addr(sQ + (seg & 1) * C::OP_BYTES) + kk * 32, 16, 1024), idesc_qk,
                      kk > 0 ? 1u : 0u);
           mma_commit(&s_full[j & 1]);
+          mma_commit(&k_empty[s]);
           if (tt == sg.n - 1) mma_commit(&q_free[seg & 1]);
           if (j >= 1) ok = issue_pv(j - 1, before);
           before = last_tile;
@@ -651,7 +659,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       const size_t block = in ? (size_t)id * p.pool.n_kv + sg.h : 0;
       int grow[2] = {0, 0};
       if (p.has_new && in) {   // uniform over the warp
-        float* scs = sc + (s * 2 + kv) * AP_MAX_PPT + pi;
+        float* scs = sc + (j % C::SCALES * 2 + kv) * AP_MAX_PPT + pi;
         int e = scale_exponent(m), e_old = e;
         if (pl > 0) {
           e_old = exponent_of_scale(*scs);
@@ -790,7 +798,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       };
       for (int tt = 0; tt < sg.n; ++tt) {
         const int j = sg.j0 + tt;
-        const int sb = j & 1, st = j % C::STAGES;
+        const int sb = j & 1;
+        const float* scs = sc + j % C::SCALES * 2 * AP_MAX_PPT;
         const int key0 = (sg.t0 + tt) * C::TILE_KEYS + tid * KPR;
         if (p.inject_timeout && j == 0) {
           failed = !mbar_wait(never, 0, kInjectWaitCycles);
@@ -809,8 +818,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           float sv[C::LD];
           tmem_ld_n<C::LD>(lane_base + sb * C::NPAD + par * C::HCOL, sv);
           const int pg = (tid * KPR + par) >> lg;
-          const float ks = sc[(st * 2 + 0) * AP_MAX_PPT + pg];
-          vs[par] = sc[(st * 2 + 1) * AP_MAX_PPT + pg];
+          const float ks = scs[pg];
+          vs[par] = scs[AP_MAX_PPT + pg];
           const bool valid = key0 + par < nkeys && ks > 0.f;
           if (!valid) vs[par] = 0.f;
           vmax = fmaxf(vmax, vs[par]);
