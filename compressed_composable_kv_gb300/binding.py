@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -46,7 +47,6 @@ _i32, _sz, _vp = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
 _pi32 = ctypes.POINTER(ctypes.c_int32)
 _pvp = ctypes.POINTER(ctypes.c_void_p)
 _pg = ctypes.POINTER(c2kv_geometry)
-_pp = ctypes.POINTER(c2kv_pages8)
 
 _SIGNATURES = {
     "c2kv_store_save": (_i32, [_vp, ctypes.c_char_p]),
@@ -81,10 +81,11 @@ _SIGNATURES = {
     "c2kv_linear": (_i32, [_vp, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _sz,
                            ctypes.c_uint32, _vp]),
     "c2kv_rmsnorm": (_i32, [_vp, _i32, _i32, _vp, ctypes.c_float, _vp, ctypes.c_uint32, _vp]),
-    "c2kv_pages8_fill": (_i32, [_pg, _pp, _i32, _i32, _i32, _pvp, _pvp, _i32, _pi32, _vp, _i32, _vp]),
-    "c2kv_pages8_append": (_i32, [_pg, _pp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
+    # (the structures of these calls are passed as packed bytes)
+    "c2kv_pages8_fill": (_i32, [_vp, _vp, _i32, _i32, _i32, _pvp, _pvp, _i32, _pi32, _vp, _i32, _vp]),
+    "c2kv_pages8_append": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
     "c2kv_attend_pages8_workspace_size": (_sz, [_pg, _i32, _i32]),
-    "c2kv_attend_pages8": (_i32, [_pg, _pp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
+    "c2kv_attend_pages8": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
                                   _vp, _sz, ctypes.c_uint32, _vp]),
     "c2kv_token_logprobs": (_i32, [_vp, _i32, _i32, _i32, ctypes.c_int64, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
 }
@@ -509,6 +510,8 @@ def c2kv_rmsnorm(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, eps: float =
 # take 10 us.
 C2KV_BF16, C2KV_F32 = 0, 1
 _E4M3, _BF, _F32, _I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
+_pack_geometry = struct.Struct("iiiid").pack   # c2kv_geometry
+_pack_pages8 = struct.Struct("PPPPii").pack    # c2kv_pages8
 
 
 def _at(t: torch.Tensor, shape: tuple, dtype, dev: int, name: str) -> int:
@@ -533,16 +536,18 @@ def _launch_stream(stream, dev: int) -> int:
     return int(stream)
 
 
-def _pages8(g, k8, v8, k_scale, v_scale, dev: int) -> c2kv_pages8:
+def _pages8(g, k8, v8, k_scale, v_scale, dev: int):
+    """c2kv_geometry and c2kv_pages8 as bytes."""
     shape = k8.shape
     if len(shape) != 5:
         raise ValueError("k8 must be [n_layers][n_pages][n_kv_heads][page][head_dim]")
     n_pages, page = shape[1], shape[3]
-    layers, heads = g.n_layers, g.n_kv_heads
-    pool, scales = (layers, n_pages, heads, page, g.head_dim), (layers, n_pages, heads)
-    return c2kv_pages8(_at(k8, pool, _E4M3, dev, "k8"), _at(v8, pool, _E4M3, dev, "v8"),
-                       _at(k_scale, scales, _F32, dev, "k_scale"), _at(v_scale, scales, _F32, dev, "v_scale"),
-                       n_pages, page)
+    layers, heads, d = g.n_layers, g.n_kv_heads, g.head_dim
+    pool, scales = (layers, n_pages, heads, page, d), (layers, n_pages, heads)
+    return _pack_geometry(layers, g.n_q_heads, heads, d, g.rope_theta), \
+        _pack_pages8(_at(k8, pool, _E4M3, dev, "k8"), _at(v8, pool, _E4M3, dev, "v8"),
+                     _at(k_scale, scales, _F32, dev, "k_scale"), _at(v_scale, scales, _F32, dev, "v_scale"),
+                     n_pages, page)
 
 
 def _page_table(t: torch.Tensor, batch: int, dev: int):
@@ -565,14 +570,13 @@ def c2kv_pages8_fill(geom, layer_begin: int, layer_end: int, k_caches, v_caches,
     """Rows [0, n_rows[b]) of composed bf16 caches to 8-bit pages (float8_e4m3fn
     codes [n_layers][n_pages][n_kv_heads][page][head_dim], fp32 scales
     [n_layers][n_pages][n_kv_heads]); page_table: int32 [batch][max_pages]."""
-    g = as_geometry(geom)
     batch = len(k_caches)
     if not (len(v_caches) == len(n_rows) == batch):
         raise ValueError("k_caches, v_caches and n_rows need one entry per sequence")
     dev = k8.get_device()
-    pages = _pages8(g, k8, v8, k_scale, v_scale, dev)
+    g, pages = _pages8(geom, k8, v8, k_scale, v_scale, dev)
     table, max_pages = _page_table(page_table, batch, dev)
-    need = g.n_layers * g.n_kv_heads * max(0, int(cap)) * g.head_dim
+    need = geom.n_layers * geom.n_kv_heads * max(0, int(cap)) * geom.head_dim
     ptrs = []
     for caches, name in ((k_caches, "k_caches"), (v_caches, "v_caches")):
         at = (ctypes.c_void_p * batch)()
@@ -584,7 +588,7 @@ def c2kv_pages8_fill(geom, layer_begin: int, layer_end: int, k_caches, v_caches,
         ptrs.append(at)
     st = _launch_stream(stream, dev)
     _check((_lib or load_library()).c2kv_pages8_fill(
-        ctypes.byref(g), ctypes.byref(pages), int(layer_begin), int(layer_end), batch, ptrs[0], ptrs[1], int(cap),
+        g, pages, int(layer_begin), int(layer_end), batch, ptrs[0], ptrs[1], int(cap),
         _i32arr(n_rows), table, max_pages, st))
 
 
@@ -594,19 +598,18 @@ def c2kv_pages8_append(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_s
                        rope_row_dev: torch.Tensor, n_new_dev: Optional[torch.Tensor] = None, stream=None) -> None:
     """Rotates and appends k_new, v_new [batch][t_len][n_kv_heads][head_dim] to
     8-bit pages; n_new_dev: int32 [batch] tokens of a padded batch."""
-    g = as_geometry(geom)
     dev = k8.get_device()
     batch, t_len = k_new.shape[:2]
-    pages = _pages8(g, k8, v8, k_scale, v_scale, dev)
+    g, pages = _pages8(geom, k8, v8, k_scale, v_scale, dev)
     table, max_pages = _page_table(page_table, batch, dev)
-    new, one = (batch, t_len, g.n_kv_heads, g.head_dim), (batch,)
-    rope, rope_rows = _rope_rows(g, rope_table, dev)
+    new, one = (batch, t_len, geom.n_kv_heads, geom.head_dim), (batch,)
+    rope, rope_rows = _rope_rows(geom, rope_table, dev)
     st = _at(n_cached_dev, one, _I32, dev, "n_cached_dev"), \
         0 if n_new_dev is None else _at(n_new_dev, one, _I32, dev, "n_new_dev"), \
         _at(k_new, new, _BF, dev, "k_new"), _at(v_new, new, _BF, dev, "v_new"), rope, rope_rows, \
         _at(rope_row_dev, one, _I32, dev, "rope_row_dev"), _launch_stream(stream, dev)
     _check((_lib or load_library()).c2kv_pages8_append(
-        ctypes.byref(g), ctypes.byref(pages), int(layer), batch, t_len, table, max_pages, *st))
+        g, pages, int(layer), batch, t_len, table, max_pages, *st))
 
 
 def c2kv_attend_pages8_workspace_size(geom, batch: int, max_keys: int) -> int:
@@ -621,17 +624,16 @@ def c2kv_attend_pages8(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_s
                        workspace: torch.Tensor, stream=None, flags: int = 0) -> None:
     """One decode step of one layer over 8-bit pages, its token's append
     included (k_new, v_new None: over the held rows alone)."""
-    g = as_geometry(geom)
     dev = k8.get_device()
-    batch, d = q.shape[0], g.head_dim
-    pages = _pages8(g, k8, v8, k_scale, v_scale, dev)
+    batch, d = q.shape[0], geom.head_dim
+    g, pages = _pages8(geom, k8, v8, k_scale, v_scale, dev)
     table, max_pages = _page_table(page_table, batch, dev)
-    heads, new, one = (batch, g.n_q_heads, d), (batch, g.n_kv_heads, d), (batch,)
-    rope, rope_rows = _rope_rows(g, rope_table, dev)
+    heads, new, one = (batch, geom.n_q_heads, d), (batch, geom.n_kv_heads, d), (batch,)
+    rope, rope_rows = _rope_rows(geom, rope_table, dev)
     if not workspace.is_contiguous() or workspace.get_device() != dev:
         raise ValueError("workspace must be contiguous and on the current CUDA device")
     _check((_lib or load_library()).c2kv_attend_pages8(
-        ctypes.byref(g), ctypes.byref(pages), int(layer), batch, table, max_pages,
+        g, pages, int(layer), batch, table, max_pages,
         _at(n_cached_dev, one, _I32, dev, "n_cached_dev"), int(max_keys), _at(q, heads, _BF, dev, "q"),
         0 if k_new is None else _at(k_new, new, _BF, dev, "k_new"),
         0 if v_new is None else _at(v_new, new, _BF, dev, "v_new"), rope, rope_rows,
