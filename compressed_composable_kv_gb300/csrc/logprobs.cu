@@ -28,7 +28,7 @@ constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_VECS = 8;                            // 16-byte loads of a thread
 constexpr int LP_GROUPS = 64;
 constexpr int LP_CAND = 1024;                         // list of a step; the cluster's lists: 16 * 64
-constexpr int LP_HITS = 1024;                         // vectors noted
+constexpr int LP_HITS = 512;                          // vectors noted
 constexpr int LP_MAX_CLUSTER = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kFaint = -200.f;                      // exp of it is 0 in fp32
@@ -135,11 +135,12 @@ struct Vec<float> {
   }
 };
 
-struct LpShared {
+struct alignas(16) LpShared {
   uint64_t cand[LP_CAND];                      // a CTA's list
   uint64_t lists[LP_MAX_CLUSTER * kMaxTopK];   // in a row's first CTA: the cluster's top lists, k each
   uint64_t top[kMaxTopK];                      // the largest, in order; 0: none
-  int hits[LP_HITS];                           // vectors that reach the bound
+  uint4 hit[LP_HITS];                          // vectors that reach the bound
+  int hit_at[LP_HITS];                         // and where they are
   uint64_t red[LP_WARPS];
   Part part[LP_WARPS];
   Part all[LP_MAX_CLUSTER];                    // in a row's first CTA: the partial results of the cluster
@@ -298,7 +299,10 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
         const int v = vb + c * LP_THREADS + tid;
         if (!(vm[c] < bound) && v < pc.v1) {
           const int at = atomicAdd(&sh.n_hits, 1);
-          if (at < LP_HITS) sh.hits[at] = v;
+          if (at < LP_HITS) {
+            sh.hit[at] = d[c];
+            sh.hit_at[at] = v;
+          }
         }
       }
     }
@@ -307,7 +311,8 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
     const uint64_t minus = pair(-from, -from), scale = pair(kLog2e, kLog2e);
     uint64_t s2 = 0, t2 = 0;
 #pragma unroll
-    for (int c = 0; c < LP_VECS; ++c)
+    for (int c = 0; c < LP_VECS; ++c) {
+      if (vb + c * LP_THREADS >= pc.v1) break;   // the same for the whole CTA
 #pragma unroll
       for (int e = 0; e < V::N; e += 2) {
         const float2 y = halves(add2(pair(V::at(d[c], e), V::at(d[c], e + 1)), minus));
@@ -317,6 +322,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
         s2 = add2(s2, w);
         t2 = fma2(w, yc, t2);
       }
+    }
     const float2 sh2 = halves(s2), th2 = halves(t2);
     q.s = sh2.x + sh2.y;
     q.t = th2.x + th2.y;
@@ -360,10 +366,8 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
       if (at < LP_CAND) sh.cand[at] = list_key(v, i);
     };
     if (n_hits <= LP_HITS) {
-      for (int i = tid; i < n_hits * V::N; i += LP_THREADS) {
-        const int at = pc.index(sh.hits[i / V::N], i % V::N);
-        list((float)pc.x[at], at);
-      }
+      for (int i = tid; i < n_hits * V::N; i += LP_THREADS)
+        list((float)reinterpret_cast<const T*>(sh.hit)[i], pc.index(sh.hit_at[i / V::N], i % V::N));
       if (tid < pc.extra) list(xe, pc.extra_at(tid));
     }
     __syncthreads();

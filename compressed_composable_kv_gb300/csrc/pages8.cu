@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, 3) put_kern
     return APPEND ? p.fresh[kv] + (((size_t)b * p.t_len + (r - first)) * p.pool.n_kv + h) * D
                   : p.src[kv][b] + (((size_t)layer * p.pool.n_kv + h) * p.cap + r) * D;
   };
-  auto in = [&](int r) { return ok && r >= first && r < end; };
+  auto in = [&](int r) { return r >= first && r < end; };   // read whether or not its page is there yet
   // The values of the 16 rows, as bf16.  Rows to be rotated are held by pairs
   // of a head's halves, two to a lane (w[2i] and w[2i + 1]: of the lane's i-th
   // row), so that a warp reads a row of the RoPE table end to end; other rows
