@@ -34,6 +34,18 @@ __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
 // Bits (as fp32) of the larger half.
 __device__ __forceinline__ uint32_t larger_half(uint32_t v) { return max(v & 0xFFFF0000u, v << 16); }
 
+// The pair (x, y) rotated, in fp32; whether rounding these to bf16 gives what
+// rounding the exact values does: rot_key_bits' test, with the bound |x| + |y|
+// >= |x cos| + |y sin| that serves both, about half its work.
+__device__ __forceinline__ bool turn_pair(float x, float y, float c, float s, float& a, float& b) {
+  a = fmaf(x, c, -__fmul_rn(y, s));
+  b = fmaf(y, c, __fmul_rn(x, s));
+  const float m = fabsf(x) + fabsf(y), near = m * 0x1p-21f, small = m * 0x1p-11f;
+  const float mid_a = __uint_as_float((__float_as_uint(a) & 0xFFFF0000u) | 0x8000u);
+  const float mid_b = __uint_as_float((__float_as_uint(b) & 0xFFFF0000u) | 0x8000u);
+  return fabsf(a - mid_a) > near && fabsf(b - mid_b) > near && fabsf(a) > small && fabsf(b) > small;
+}
+
 // The codes of the two values of a word.
 __device__ __forceinline__ uint32_t codes2(uint32_t w, float inv) {
   return e4m3x2(__uint_as_float(w << 16) * inv, __uint_as_float(w & 0xFFFF0000u) * inv);
@@ -51,7 +63,7 @@ __device__ __forceinline__ void tame(uint32_t& w, uint32_t& m) {
 // D: head_dim.  APPEND: rows [n_cached, n_cached + new) from the new tokens,
 // K rotated; else rows [0, n_rows) from the bf16 caches.
 template <int D, bool APPEND>
-__global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, 3) put_kernel(const __grid_constant__ PutParams p) {
+__global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 : 3) put_kernel(const __grid_constant__ PutParams p) {
   constexpr int CH = D / 16;              // items (16 elements) of a row
   constexpr int IT = D / 32;              // items of a lane
   __shared__ uint32_t warp_max[8];
@@ -126,10 +138,17 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, 3) put_kern
       const CosSin2 t0 = t[0], t1 = t[1];
       const float x0 = __uint_as_float(w[2 * i] << 16), x1 = __uint_as_float(w[2 * i] & 0xFFFF0000u);
       const float y0 = __uint_as_float(w[2 * i + 1] << 16), y1 = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u);
-      w[2 * i] = rot_key_bits(x0, t0.ch, t0.cl, -y0, t0.sh, t0.sl) |
-                 (rot_key_bits(x1, t1.ch, t1.cl, -y1, t1.sh, t1.sl) << 16);
-      w[2 * i + 1] = rot_key_bits(y0, t0.ch, t0.cl, x0, t0.sh, t0.sl) |
-                     (rot_key_bits(y1, t1.ch, t1.cl, x1, t1.sh, t1.sl) << 16);
+      float a0, b0, a1, b1;
+      const bool clear0 = turn_pair(x0, y0, t0.ch, t0.sh, a0, b0), clear1 = turn_pair(x1, y1, t1.ch, t1.sh, a1, b1);
+      if (clear0 && clear1) {
+        w[2 * i] = pack2(a0, a1);
+        w[2 * i + 1] = pack2(b0, b1);
+      } else {
+        w[2 * i] = rot_key_slow(x0, t0.ch, t0.cl, -y0, t0.sh, t0.sl) |
+                   (rot_key_slow(x1, t1.ch, t1.cl, -y1, t1.sh, t1.sl) << 16);
+        w[2 * i + 1] = rot_key_slow(y0, t0.ch, t0.cl, x0, t0.sh, t0.sl) |
+                       (rot_key_slow(y1, t1.ch, t1.cl, x1, t1.sh, t1.sl) << 16);
+      }
       if (odd) {   // a pair with a member that is not finite is NaN in both
         const uint32_t nan = (fabsf(x0) < INFINITY && fabsf(y0) < INFINITY ? 0u : 0x7FFFu) |
                              (fabsf(x1) < INFINITY && fabsf(y1) < INFINITY ? 0u : 0x7FFF0000u);
