@@ -1044,7 +1044,7 @@ c2kv_status c2kv_attend_decode(const c2kv_geometry* geom, int32_t layer, int32_t
 }
 
 c2kv_status c2kv_seq_advance(int32_t batch, int32_t* n_cached_dev, int32_t delta, void* stream) {
-  if (batch < 1 || batch > 32) return fail(C2KV_EINVAL, "batch must be in [1, 32]");
+  if (batch < 1 || batch > 1024) return fail(C2KV_EINVAL, "batch must be in [1, 1024]");
   if (!n_cached_dev) return fail(C2KV_EINVAL, "null device array");
   C2KV_LAUNCH(launch_advance(batch, n_cached_dev, delta, static_cast<cudaStream_t>(stream)));
   return C2KV_OK;

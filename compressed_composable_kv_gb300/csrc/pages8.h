@@ -48,7 +48,7 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
 static __device__ __noinline__ uint32_t rot_key_slow(float a, float bh, float bl, float c, float dh, float dl) {
   float hi, lo;
   dot2_df(a, bh, bl, c, dh, dl, hi, lo);
-  return bf16_bits_rn(hi);
+  return fabsf(hi) < INFINITY ? bf16_bits_rn(hi) : 0x7FFFu;   // beyond fp32's range: NaN
 }
 
 __device__ __forceinline__ uint32_t rot_key_bits(float a, float bh, float bl, float c, float dh, float dl) {

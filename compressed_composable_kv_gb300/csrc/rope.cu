@@ -218,7 +218,7 @@ __global__ void append_kernel(const __grid_constant__ AppendParams p) {
 }
 
 __global__ void advance_kernel(int batch, int32_t* n_cached, int delta) {
-  const int b = threadIdx.x;
+  const int b = blockIdx.x * blockDim.x + threadIdx.x;
   if (b < batch) n_cached[b] += delta;
 }
 
@@ -241,7 +241,7 @@ cudaError_t launch_append(const AppendParams& p, int head_dim, int batch, cudaSt
 }
 
 cudaError_t launch_advance(int batch, int32_t* n_cached, int delta, cudaStream_t st) {
-  advance_kernel<<<1, 32, 0, st>>>(batch, n_cached, delta);
+  advance_kernel<<<(batch + 31) / 32, 32, 0, st>>>(batch, n_cached, delta);
   return cudaGetLastError();
 }
 

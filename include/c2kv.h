@@ -352,7 +352,7 @@ c2kv_status c2kv_attend_decode_noalloc(const c2kv_geometry* geom, int32_t layer,
                                        int32_t max_keys, const void* q, const void* k_new,
                                        const void* v_new, void* out, void* stream);
 
-/* Adds `delta` to n_cached_dev[b] for b < batch (device kernel). */
+/* Adds `delta` to n_cached_dev[b] for b < batch <= 1024 (device kernel). */
 c2kv_status c2kv_seq_advance(int32_t batch, int32_t* n_cached_dev, int32_t delta,
                              void* stream);
 
@@ -458,7 +458,8 @@ c2kv_status c2kv_rmsnorm(const void* x, int32_t tokens, int32_t dim, const void*
  * device: a bad one is recorded in the device error word (C2KV_EDEVICE) and
  * what it would reach is left out.  A length n_cached_dev[b] < 0 marks an
  * empty place of the batch: nothing of it is read or written, which is no
- * error.
+ * error (c2kv_seq_advance adds to every length: a place that is to stay empty
+ * takes one far below 0).
  */
 typedef struct {
   void* k;          /* device e4m3 [n_layers][n_pages][n_kv_heads][page][head_dim] */
@@ -512,7 +513,8 @@ c2kv_status c2kv_pages8_append(const c2kv_geometry* geom, const c2kv_pages8* pag
  * calls of the same geometry that do not overlap on the GPU (other calls'
  * scratch would overwrite its counters).  flags: C2KV_DECODE_OVERLAP_PREVIOUS, as in
  * c2kv_attend_decode: the kernel before on `stream` must not write the
- * lengths, the page table, the RoPE table or this layer's held rows.
+ * lengths, the page table, the RoPE table and rope_row_dev, or this layer's
+ * held rows and their scales.
  */
 size_t c2kv_attend_pages8_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t max_keys);
 c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,

@@ -237,6 +237,37 @@ def test_append_token_by_token(kind):
     pool.check(f"token by token, {kind}")
 
 
+@pytest.mark.parametrize("fused", [False, True])
+def test_rotation_beyond_the_range_is_nan(fused):
+    """Keys of the largest numbers: what the rotation takes beyond the range of
+    bf16 is held as NaN, its partner and the rest as what they are."""
+    g = _geom(128, 1, 2)
+    pool = Pool(g, 16, [40])
+    for kv in (0, 1):
+        pool.put(0, 0, 0, kv, _f64(_values(pool.rng, (2, 20, 128))))
+    pool.upload()
+    k = _values(pool.rng, (1, 1, 2, 128))
+    k[0, 0, 0, :], k[0, 0, 1, ::5] = 0x7F7F, 0xFF7F   # +- 3.39e38
+    v = _values(pool.rng, (1, 1, 2, 128))
+    pos = 12345
+    n, row = (torch.tensor([x], dtype=torch.int32, device="cuda") for x in (20, 0))
+    if fused:
+        ws = torch.zeros(P.c2kv_attend_pages8_workspace_size(g, 1, 21), dtype=torch.uint8, device="cuda")
+        q = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device="cuda")
+        P.c2kv_attend_pages8(g, 0, *pool.args(), n, 21, q, _dev(k)[:, 0], _dev(v)[:, 0], _rope(g, [pos]), row,
+                             torch.empty_like(q), ws)
+    else:
+        P.c2kv_pages8_append(g, 0, *pool.args(), n, _dev(k), _dev(v), _rope(g, [pos]), row)
+    _ok()
+    with np.errstate(over="ignore"):
+        kr = _round_key(_rotate(g, _f64(k[0]), [pos]))
+    kr[~np.isfinite(kr)] = np.nan
+    assert np.isnan(kr).any() and np.isfinite(kr).any()
+    pool.put(0, 0, 20, 0, kr.transpose(1, 0, 2))
+    pool.put(0, 0, 20, 1, _f64(v[0]).transpose(1, 0, 2))
+    pool.check("overflowing rotation")
+
+
 # ------------------------------------------------------------------ attention
 
 def _attend_case(g, page, held, has_new=True, sharp=1.0, seed=0, kind="normal", slack=0, layer=0, bad_tail=True):
@@ -313,6 +344,12 @@ def test_attend_batches(d, has_new, held):
 def test_attend_sharp_and_uneven_pages(d, kind, sharp):
     _attend_case(_geom(d, 4, 2), 16, [900, 90, 33], sharp=sharp, kind=kind)
     _attend_case(_geom(d, 8, 1), 128, [900, 90, 33], sharp=sharp, kind=kind)
+
+
+def test_advance_of_a_large_batch():
+    n = torch.arange(-3, 297, dtype=torch.int32, device="cuda")
+    P.c2kv_seq_advance(n, 2)
+    assert torch.equal(n.cpu(), torch.arange(-1, 299, dtype=torch.int32))
 
 
 def test_attend_second_layer_and_generous_bound():
