@@ -50,7 +50,7 @@ constexpr int AP_KV_BYTES = 128 * 128;          // K (or V) of one tile
 constexpr int AP_STAGE = 2 * AP_KV_BYTES;
 constexpr int AP_MAX_PPT = 16;                  // pages of a tile
 
-constexpr int kMinTiles = 2;     // tiles of a CTA below which fewer CTAs work
+constexpr int kMinTiles = 4;     // tiles of a CTA below which fewer CTAs work
 constexpr int kMergeRows = 64;   // partials of one round of a merge
 
 // The tiles of a launch, from the device-side lengths (fewer than 2^31, which
@@ -714,6 +714,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     // Tile t's stage is free for tile t + STAGES once PV(t) has run, so nothing
     // waits for this warp while it completes tile t before it asks for V of tile
     // t + STAGES - 1.
+    auto ends = [&](const PageSeg& sg) { return sg.t0 + sg.n == unit_tiles(sg.b); };
     PageSeg next = seg_at(0);
     bool ready = false, done = false;
     auto fix_to = [&](int t) -> bool {   // the units' last tiles up to tile t
@@ -721,15 +722,15 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       if (!ready) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
         asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-        ask_row(next);
+        if (ends(next)) ask_row(next);
         ready = true;
       }
       while (!done && next.j0 + next.n - 1 <= t) {
-        if (next.t0 + next.n == unit_tiles(next.b) && !fixup(next.j0 + next.n - 1, next)) return false;
+        if (ends(next) && !fixup(next.j0 + next.n - 1, next)) return false;
         done = next.j0 + next.n >= ntiles;
         if (!done) {
           next = seg_at(next.j0 + next.n);
-          ask_row(next);
+          if (ends(next)) ask_row(next);
         }
       }
       return true;
