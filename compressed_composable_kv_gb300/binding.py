@@ -8,14 +8,15 @@ library raises ImportError: there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
 from typing import Optional, Sequence
 
 import numpy as np
 import torch
 
-from .build import LIB
+from .build import LIB, MARSHAL
 
 C2KV_OK, C2KV_EINVAL, C2KV_ENOMEM, C2KV_ENOTFOUND = 0, 1, 2, 3
 C2KV_ECAPACITY, C2KV_ECUDA, C2KV_ETIMEOUT, C2KV_EDEVICE, C2KV_EIO = 4, 5, 6, 7, 8
@@ -47,6 +48,7 @@ _i32, _sz, _vp = ctypes.c_int32, ctypes.c_size_t, ctypes.c_void_p
 _pi32 = ctypes.POINTER(ctypes.c_int32)
 _pvp = ctypes.POINTER(ctypes.c_void_p)
 _pg = ctypes.POINTER(c2kv_geometry)
+_pp = ctypes.POINTER(c2kv_pages8)
 
 _SIGNATURES = {
     "c2kv_store_save": (_i32, [_vp, ctypes.c_char_p]),
@@ -81,11 +83,10 @@ _SIGNATURES = {
     "c2kv_linear": (_i32, [_vp, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _i32, _vp, _sz,
                            ctypes.c_uint32, _vp]),
     "c2kv_rmsnorm": (_i32, [_vp, _i32, _i32, _vp, ctypes.c_float, _vp, ctypes.c_uint32, _vp]),
-    # (the structures of these calls are passed as packed bytes)
-    "c2kv_pages8_fill": (_i32, [_vp, _vp, _i32, _i32, _i32, _pvp, _pvp, _i32, _pi32, _vp, _i32, _vp]),
-    "c2kv_pages8_append": (_i32, [_vp, _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
+    "c2kv_pages8_fill": (_i32, [_pg, _pp, _i32, _i32, _i32, _pvp, _pvp, _i32, _pi32, _vp, _i32, _vp]),
+    "c2kv_pages8_append": (_i32, [_pg, _pp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp]),
     "c2kv_attend_pages8_workspace_size": (_sz, [_pg, _i32, _i32]),
-    "c2kv_attend_pages8": (_i32, [_vp, _vp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
+    "c2kv_attend_pages8": (_i32, [_pg, _pp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
                                   _vp, _sz, ctypes.c_uint32, _vp]),
     "c2kv_token_logprobs": (_i32, [_vp, _i32, _i32, _i32, ctypes.c_int64, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
 }
@@ -505,27 +506,34 @@ def c2kv_rmsnorm(x: torch.Tensor, w: torch.Tensor, y: torch.Tensor, eps: float =
 
 
 # ---------------------------------------------------------------- 8-bit paged cache
-# These calls check every tensor (type, shape, contiguity, device) and still have
-# to be short: a decode step makes one per layer, and the kernel behind it may
-# take 10 us.
+# Arguments of these calls are checked and passed on by a module in C++
+# (csrc/marshal.cpp): every tensor's type, shape, contiguity and device.  A
+# decode step makes one such call per layer, and the kernel behind it may take
+# 10 us, as long as the checks took in Python.
 C2KV_BF16, C2KV_F32 = 0, 1
-_E4M3, _BF, _F32, _I32 = torch.float8_e4m3fn, torch.bfloat16, torch.float32, torch.int32
-_pack_geometry = struct.Struct("iiiid").pack   # c2kv_geometry
-_pack_pages8 = struct.Struct("PPPPii").pack    # c2kv_pages8
+
+_marshal_module = None
 
 
-def _at(t: torch.Tensor, shape: tuple, dtype, dev: int, name: str) -> int:
-    """The address of t: contiguous, of this shape and type, on device dev."""
-    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {shape}, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be on the current CUDA device, like the call's other tensors")
-    return t.data_ptr()
+def _load_marshal():
+    global _marshal_module
+    load_library()
+    if not os.path.exists(MARSHAL):
+        raise ImportError(f"_marshal.so is not built ({MARSHAL}); run "
+                          "compressed_composable_kv_gb300.build.build_library()")
+    loader = importlib.machinery.ExtensionFileLoader("_marshal", MARSHAL)
+    spec = importlib.util.spec_from_file_location("_marshal", MARSHAL, loader=loader)
+    _marshal_module = importlib.util.module_from_spec(spec)
+    loader.exec_module(_marshal_module)
+    return _marshal_module
 
 
 def _launch_stream(stream, dev: int) -> int:
-    """The raw stream, and that the tensors' device is the current one, where the launch goes."""
-    if dev < 0 or dev != torch.cuda.current_device():
+    """The raw stream for tensors on device dev, which has to be the current
+    one, where the launch goes (tensors of the host are refused by name later)."""
+    if dev < 0:
+        return 0
+    if dev != torch.cuda.current_device():
         raise ValueError("the tensors must be on the current CUDA device")
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(dev)
@@ -536,60 +544,16 @@ def _launch_stream(stream, dev: int) -> int:
     return int(stream)
 
 
-def _pages8(g, k8, v8, k_scale, v_scale, dev: int):
-    """c2kv_geometry and c2kv_pages8 as bytes."""
-    shape = k8.shape
-    if len(shape) != 5:
-        raise ValueError("k8 must be [n_layers][n_pages][n_kv_heads][page][head_dim]")
-    n_pages, page = shape[1], shape[3]
-    layers, heads, d = g.n_layers, g.n_kv_heads, g.head_dim
-    pool, scales = (layers, n_pages, heads, page, d), (layers, n_pages, heads)
-    return _pack_geometry(layers, g.n_q_heads, heads, d, g.rope_theta), \
-        _pack_pages8(_at(k8, pool, _E4M3, dev, "k8"), _at(v8, pool, _E4M3, dev, "v8"),
-                     _at(k_scale, scales, _F32, dev, "k_scale"), _at(v_scale, scales, _F32, dev, "v_scale"),
-                     n_pages, page)
-
-
-def _page_table(t: torch.Tensor, batch: int, dev: int):
-    shape = t.shape
-    if len(shape) != 2:
-        raise ValueError("page_table must be [batch][max_pages]")
-    return _at(t, (batch, shape[1]), _I32, dev, "page_table"), shape[1]
-
-
-def _rope_rows(g, rope_table, dev: int):
-    """Address and rows of a RoPE table (any type)."""
-    if not rope_table.is_contiguous() or rope_table.get_device() != dev:
-        raise ValueError("rope_table must be contiguous and on the current CUDA device")
-    return rope_table.data_ptr(), rope_table.nbytes // (g.head_dim // 2 * 16)
-
-
 def c2kv_pages8_fill(geom, layer_begin: int, layer_end: int, k_caches, v_caches, cap: int, n_rows,
                      k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                      page_table: torch.Tensor, stream=None) -> None:
     """Rows [0, n_rows[b]) of composed bf16 caches to 8-bit pages (float8_e4m3fn
     codes [n_layers][n_pages][n_kv_heads][page][head_dim], fp32 scales
     [n_layers][n_pages][n_kv_heads]); page_table: int32 [batch][max_pages]."""
-    batch = len(k_caches)
-    if not (len(v_caches) == len(n_rows) == batch):
-        raise ValueError("k_caches, v_caches and n_rows need one entry per sequence")
     dev = k8.get_device()
-    g, pages = _pages8(geom, k8, v8, k_scale, v_scale, dev)
-    table, max_pages = _page_table(page_table, batch, dev)
-    need = geom.n_layers * geom.n_kv_heads * max(0, int(cap)) * geom.head_dim
-    ptrs = []
-    for caches, name in ((k_caches, "k_caches"), (v_caches, "v_caches")):
-        at = (ctypes.c_void_p * batch)()
-        for b, t in enumerate(caches):
-            if t.dtype is not _BF or t.numel() < need or not t.is_contiguous() or t.get_device() != dev:
-                raise ValueError(f"{name}[{b}] must be a contiguous bfloat16 tensor of at least {need} elements "
-                                 f"on the current CUDA device, got {t.dtype} {tuple(t.shape)} on {t.device}")
-            at[b] = t.data_ptr()
-        ptrs.append(at)
-    st = _launch_stream(stream, dev)
-    _check((_lib or load_library()).c2kv_pages8_fill(
-        g, pages, int(layer_begin), int(layer_end), batch, ptrs[0], ptrs[1], int(cap),
-        _i32arr(n_rows), table, max_pages, st))
+    _check((_marshal_module or _load_marshal()).pages8_fill(
+        geom.n_layers, geom.n_q_heads, geom.n_kv_heads, geom.head_dim, geom.rope_theta, dev, k8, v8, k_scale,
+        v_scale, page_table, k_caches, v_caches, cap, n_rows, layer_begin, layer_end, _launch_stream(stream, dev)))
 
 
 def c2kv_pages8_append(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
@@ -599,17 +563,10 @@ def c2kv_pages8_append(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_s
     """Rotates and appends k_new, v_new [batch][t_len][n_kv_heads][head_dim] to
     8-bit pages; n_new_dev: int32 [batch] tokens of a padded batch."""
     dev = k8.get_device()
-    batch, t_len = k_new.shape[:2]
-    g, pages = _pages8(geom, k8, v8, k_scale, v_scale, dev)
-    table, max_pages = _page_table(page_table, batch, dev)
-    new, one = (batch, t_len, geom.n_kv_heads, geom.head_dim), (batch,)
-    rope, rope_rows = _rope_rows(geom, rope_table, dev)
-    st = _at(n_cached_dev, one, _I32, dev, "n_cached_dev"), \
-        0 if n_new_dev is None else _at(n_new_dev, one, _I32, dev, "n_new_dev"), \
-        _at(k_new, new, _BF, dev, "k_new"), _at(v_new, new, _BF, dev, "v_new"), rope, rope_rows, \
-        _at(rope_row_dev, one, _I32, dev, "rope_row_dev"), _launch_stream(stream, dev)
-    _check((_lib or load_library()).c2kv_pages8_append(
-        g, pages, int(layer), batch, t_len, table, max_pages, *st))
+    _check((_marshal_module or _load_marshal()).pages8_append(
+        geom.n_layers, geom.n_q_heads, geom.n_kv_heads, geom.head_dim, geom.rope_theta, dev, k8, v8, k_scale,
+        v_scale, page_table, layer, n_cached_dev, n_new_dev, k_new, v_new, rope_table, rope_row_dev,
+        _launch_stream(stream, dev)))
 
 
 def c2kv_attend_pages8_workspace_size(geom, batch: int, max_keys: int) -> int:
@@ -625,20 +582,10 @@ def c2kv_attend_pages8(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_s
     """One decode step of one layer over 8-bit pages, its token's append
     included (k_new, v_new None: over the held rows alone)."""
     dev = k8.get_device()
-    batch, d = q.shape[0], geom.head_dim
-    g, pages = _pages8(geom, k8, v8, k_scale, v_scale, dev)
-    table, max_pages = _page_table(page_table, batch, dev)
-    heads, new, one = (batch, geom.n_q_heads, d), (batch, geom.n_kv_heads, d), (batch,)
-    rope, rope_rows = _rope_rows(geom, rope_table, dev)
-    if not workspace.is_contiguous() or workspace.get_device() != dev:
-        raise ValueError("workspace must be contiguous and on the current CUDA device")
-    _check((_lib or load_library()).c2kv_attend_pages8(
-        g, pages, int(layer), batch, table, max_pages,
-        _at(n_cached_dev, one, _I32, dev, "n_cached_dev"), int(max_keys), _at(q, heads, _BF, dev, "q"),
-        0 if k_new is None else _at(k_new, new, _BF, dev, "k_new"),
-        0 if v_new is None else _at(v_new, new, _BF, dev, "v_new"), rope, rope_rows,
-        _at(rope_row_dev, one, _I32, dev, "rope_row_dev"), _at(out, heads, _BF, dev, "out"), workspace.data_ptr(),
-        workspace.nbytes, int(flags), _launch_stream(stream, dev)))
+    _check((_marshal_module or _load_marshal()).attend_pages8(
+        geom.n_layers, geom.n_q_heads, geom.n_kv_heads, geom.head_dim, geom.rope_theta, dev, k8, v8, k_scale,
+        v_scale, page_table, layer, n_cached_dev, max_keys, q, k_new, v_new, rope_table, rope_row_dev, out,
+        workspace, flags, _launch_stream(stream, dev)))
 
 
 def c2kv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], top_k: int,
@@ -647,19 +594,6 @@ def c2kv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], to
                         stream=None) -> None:
     """Log probability of tokens[row], entropy and the top_k alternatives of
     each row of logits [rows][vocab] (bf16 or fp32, rows any stride apart)."""
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
-        raise ValueError("logits must be [rows][vocab] with neighbouring logits of a row side by side")
-    dtype = logits.dtype
-    if dtype is not _BF and dtype is not _F32:
-        raise ValueError(f"logits must be bfloat16 or float32, got {dtype}")
-    rows, vocab = logits.shape
-    dev, one, k = logits.get_device(), (rows,), int(top_k)
-    _check((_lib or load_library()).c2kv_token_logprobs(
-        logits.data_ptr(), C2KV_F32 if dtype is _F32 else C2KV_BF16, rows, vocab,
-        logits.stride(0) if rows > 1 else max(vocab, logits.stride(0)),
-        0 if tokens is None else _at(tokens, one, _I32, dev, "tokens"), k,
-        0 if logprob is None else _at(logprob, one, _F32, dev, "logprob"),
-        0 if entropy is None else _at(entropy, one, _F32, dev, "entropy"),
-        0 if top_ids is None else _at(top_ids, (rows, k), _I32, dev, "top_ids"),
-        0 if top_logprobs is None else _at(top_logprobs, (rows, k), _F32, dev, "top_logprobs"),
-        _launch_stream(stream, dev)))
+    dev = logits.get_device()
+    _check((_marshal_module or _load_marshal()).token_logprobs(
+        dev, logits, tokens, top_k, logprob, entropy, top_ids, top_logprobs, _launch_stream(stream, dev)))

@@ -1,15 +1,18 @@
 """In-tree build of libc2kv.so for sm_103a (nvcc, no cmake).
 
 Each CUDA translation unit is compiled in parallel, then linked into one
-shared library with the CUDA runtime linked statically.  The result lives
-in compressed_composable_kv_gb300/_build/ (git-ignored).
+shared library with the CUDA runtime linked statically.  The binding's
+marshalling module (_marshal.so, C++ against torch's headers) is built beside
+it.  The results live in compressed_composable_kv_gb300/_build/ (git-ignored).
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -18,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libc2kv.so")
+MARSHAL = os.path.join(BUILD, "_marshal.so")
 
 SOURCES = ["api.cu", "rope.cu", "attn.cu", "prefill_tc.cu", "decode_tc.cu", "linear_tc.cu",
            "api_pages8.cu", "pages8.cu", "attend_pages8.cu", "logprobs.cu"]
@@ -38,17 +42,42 @@ def _flags(extra=()):
 
 def _deps():
     files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".h")]
+    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cpp"))]
     files.append(os.path.join(INCLUDE, "c2kv.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
     return all(os.path.getmtime(f) <= t for f in _deps())
+
+
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _compile_marshal():
+    """marshal.cpp to an object; it is linked once libc2kv.so is there."""
+    obj = os.path.join(BUILD, "marshal.o")
+    inc = os.path.join(_torch_dir(), "include")
+    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-c", os.path.join(CSRC, "marshal.cpp"), "-o", obj]
+    return obj, subprocess.run(cmd, capture_output=True, text=True)
+
+
+def _link_marshal(obj: str) -> None:
+    lib = os.path.join(_torch_dir(), "lib")
+    cmd = ["g++", "-shared", "-o", MARSHAL + ".tmp", obj, LIB, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("linking _marshal.so failed")
+    os.replace(MARSHAL + ".tmp", MARSHAL)
 
 
 def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
@@ -65,15 +94,20 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: boo
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        marshal = ex.submit(_compile_marshal)
         results = list(ex.map(compile_one, SOURCES))
+        marshal_obj, r = marshal.result()
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError("g++ failed on marshal.cpp")
     for src, _, r in results:
         if verbose or ptxas_verbose or r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}")
     tmp = LIB + ".tmp"
-    cmd = [cc] + ARCH + ["-shared", "-o", tmp] + [o for _, o, _ in results] + ["-lcuda"]
+    cmd = [cc] + ARCH + ["-shared", "-Xlinker", "-soname=libc2kv.so", "-o", tmp] + [o for _, o, _ in results] + ["-lcuda"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         # libcuda.so may be absent on a build host without a driver; the
@@ -84,6 +118,7 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: boo
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("linking libc2kv.so failed")
     os.replace(tmp, LIB)
+    _link_marshal(marshal_obj)
     return LIB
 
 
