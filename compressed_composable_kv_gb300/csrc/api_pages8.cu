@@ -199,10 +199,10 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
   p.max_keys = max_keys;
   p.table_rows = table_rows;
   p.has_new = k_new != nullptr ? 1 : 0;
+  p.early = (flags & C2KV_DECODE_OVERLAP_PREVIOUS) != 0 ? 1 : 0;
   p.inject_timeout = api_take_injected_timeout();
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)geom->head_dim));
   return api_launched(launch_attend_pages8(p, geom->head_dim, geom->n_q_heads / geom->n_kv_heads, sms,
-                                           (flags & C2KV_DECODE_OVERLAP_PREVIOUS) != 0,
                                            static_cast<cudaStream_t>(stream)),
                       "c2kv_attend_pages8");
 }

@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   auto stage_v = [&](int s) { return smem + s * AP_STAGE + AP_KV_BYTES; };
 
   if (warp == 0) {
-    // The map, 32 sequences at a time: lengths, table rows, page table and held
-    // rows are what the previous kernel does not write, so this does not wait.
+    // The map, 32 sequences at a time.
+    if (!p.early) grid_wait();
     int at = 0;
     bool bad = false, none = false;
     auto scan = [&](int v, int& sum) {   // exclusive prefix over the warp on top of sum, which takes the total
@@ -392,14 +392,14 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   if (warp == 4 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.tm[lane]) : "memory");
   if (*none_flag) {
     // sequences without a row: their output is zero
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     for (int b = cta; b < p.batch; b += ctas)
       if (M.keys[b] == 0)
         for (int i = tid; i < p.n_q * D / 8; i += AP_THREADS)
           reinterpret_cast<uint4*>(p.out + (size_t)b * p.n_q * D)[i] = make_uint4(0, 0, 0, 0);
   }
   if (ntiles == 0) {   // uniform over the CTA
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_wait();
     if (warp == 4)
       asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(C::TMEM_COLS) : "memory");
     return;
@@ -554,8 +554,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       mbar_wait(mma_done, 0);
     }
   } else if (warp == 6) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait();
+    grid_release();
     // ---------------- the query of each unit: rotated, times log2(e)/sqrt(d),
     // over a power of two that brings its largest element into (224, 448], in
     // three parts.  Item (g, c): elements 8c.. and D/2 + 8c.. of head g.
@@ -720,8 +720,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     auto fix_to = [&](int t) -> bool {   // the units' last tiles up to tile t
       if (t < 0) return true;            // the first stages' loads come first
       if (!ready) {
-        asm volatile("griddepcontrol.wait;" ::: "memory");
-        asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+        grid_wait();
+        grid_release();
         if (ends(next)) ask_row(next);
         ready = true;
       }
@@ -739,8 +739,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   } else {
     // ---------------- softmax and epilogue: thread tid owns row tid of each
     // tile (lane tid of S^T) and lane tid of O^T
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_wait();
+    grid_release();
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t o_col = C::TMEM_O + (tid / D) * C::HCOL;   // the columns of this lane's half
     // A wait that runs out is noted and the step goes on with what is there;
@@ -1045,7 +1045,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
 }
 
 template <int D, int G>
-cudaError_t launch_ap(const AttendPages8Params& p, int sms, bool overlap, cudaStream_t st) {
+cudaError_t launch_ap(const AttendPages8Params& p, int sms, cudaStream_t st) {
   using C = ApCfg<D, G>;
   static KernelSetup s;
   const int dev = setup_device();
@@ -1069,28 +1069,26 @@ cudaError_t launch_ap(const AttendPages8Params& p, int sms, bool overlap, cudaSt
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = overlap ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, attend_pages8_kernel<D, G>, p);
 }
 
 template <int D>
-cudaError_t launch_group(const AttendPages8Params& p, int group, int sms, bool overlap, cudaStream_t st) {
+cudaError_t launch_group(const AttendPages8Params& p, int group, int sms, cudaStream_t st) {
   switch (group) {
-    case 1: return launch_ap<D, 1>(p, sms, overlap, st);
-    case 2: return launch_ap<D, 2>(p, sms, overlap, st);
-    case 4: return launch_ap<D, 4>(p, sms, overlap, st);
-    case 5: return launch_ap<D, 5>(p, sms, overlap, st);
-    case 8: return launch_ap<D, 8>(p, sms, overlap, st);
+    case 1: return launch_ap<D, 1>(p, sms, st);
+    case 2: return launch_ap<D, 2>(p, sms, st);
+    case 4: return launch_ap<D, 4>(p, sms, st);
+    case 5: return launch_ap<D, 5>(p, sms, st);
+    case 8: return launch_ap<D, 8>(p, sms, st);
     default: return cudaErrorInvalidValue;
   }
 }
 
 }  // namespace
 
-cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, bool overlap,
-                                 cudaStream_t st) {
-  return head_dim == 128 ? launch_group<128>(p, group, sms, overlap, st)
-                         : launch_group<64>(p, group, sms, overlap, st);
+cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, cudaStream_t st) {
+  return head_dim == 128 ? launch_group<128>(p, group, sms, st) : launch_group<64>(p, group, sms, st);
 }
 
 }  // namespace c2kv

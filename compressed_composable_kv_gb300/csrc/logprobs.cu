@@ -265,6 +265,8 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
   Piece<T> pc;
   pc.x = static_cast<const T*>(p.logits) + (int64_t)row * p.row_stride;
   pc.vocab = p.vocab;
+  grid_wait();
+  grid_release();
   pc.head = min(p.vocab, (int)((16 - (reinterpret_cast<uintptr_t>(pc.x) & 15)) / sizeof(T)) % V::N);
   pc.vec = reinterpret_cast<const uint4*>(pc.x + pc.head);
   const int nvec = (p.vocab - pc.head) / V::N, share = (nvec + cs - 1) / cs;
@@ -461,13 +463,15 @@ cudaError_t launch_lp(LogprobParams p, int sms, cudaStream_t st) {
   cfg.gridDim = dim3((unsigned)(p.rows * cs));
   cfg.blockDim = dim3(LP_THREADS);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = cs;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cs;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = cs > 1 ? 1 : 0;
+  cfg.numAttrs = cs > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T>, p);
 }
 

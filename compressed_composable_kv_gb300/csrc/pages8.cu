@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   const int b = blockIdx.y / p.pool.n_kv, h = blockIdx.y % p.pool.n_kv;
   const int kv = blockIdx.z & 1, layer = blockIdx.z >> 1;
   const int rows = blockDim.x / 32 * PUT_WARP_ROWS;   // of a CTA
+  grid_wait();
+  grid_release();
   int first = 0, count, rr = 0;
   if (APPEND) {
     first = p.n_cached[b];
@@ -229,6 +231,20 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   if (warp == w0 && lane == 0) *scale = pow2_float(e);
 }
 
+template <int D, bool APPEND>
+cudaError_t launch_put(const PutParams& p, dim3 grid, int threads, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, put_kernel<D, APPEND>, p);
+}
+
 // Rows of a CTA for this page size.
 int put_rows(const PutParams& p) { return p.pool.page > PUT_MIN_ROWS ? PUT_MAX_ROWS : PUT_MIN_ROWS; }
 
@@ -237,18 +253,14 @@ int put_rows(const PutParams& p) { return p.pool.page > PUT_MIN_ROWS ? PUT_MAX_R
 cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, cudaStream_t st) {
   const int rows = put_rows(p), threads = rows / PUT_WARP_ROWS * 32;
   const dim3 grid((max_rows + rows - 1) / rows, p.batch * p.pool.n_kv, 2 * p.n_layers);
-  if (head_dim == 128) put_kernel<128, false><<<grid, threads, 0, st>>>(p);
-  else put_kernel<64, false><<<grid, threads, 0, st>>>(p);
-  return cudaGetLastError();
+  return head_dim == 128 ? launch_put<128, false>(p, grid, threads, st) : launch_put<64, false>(p, grid, threads, st);
 }
 
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st) {
   // rows [n, n + t_len) meet at most this many CTAs' rows
   const int rows = put_rows(p), threads = rows / PUT_WARP_ROWS * 32;
   const dim3 grid((p.t_len + 2 * rows - 2) / rows, p.batch * p.pool.n_kv, 2);
-  if (head_dim == 128) put_kernel<128, true><<<grid, threads, 0, st>>>(p);
-  else put_kernel<64, true><<<grid, threads, 0, st>>>(p);
-  return cudaGetLastError();
+  return head_dim == 128 ? launch_put<128, true>(p, grid, threads, st) : launch_put<64, true>(p, grid, threads, st);
 }
 
 }  // namespace c2kv

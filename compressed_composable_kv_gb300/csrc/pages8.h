@@ -164,6 +164,7 @@ struct AttendPages8Params {
   int32_t* counters;             // [batch * n_kv] tiles merged so far per unit
   unsigned* err;
   int32_t batch, n_q, max_pages, max_keys, table_rows, has_new, inject_timeout;
+  int32_t early;                 // lengths, page table, RoPE rows and held rows may be read before the wait
   float scale_log2;
 };
 constexpr int kMaxPageCtas = 512;   // CTAs of one launch (at most two per SM)
@@ -183,10 +184,17 @@ struct LogprobParams {
 
 constexpr int kMaxTopK = 64;
 
+// The launches below may be set up while the kernel before them on the stream
+// finishes (programmatic dependent launch), which takes about 2 us off a call
+// among others.  Each waits for that kernel before it touches global memory,
+// unless its caller says what may be read earlier, and lets the next launch be
+// set up from then on.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, cudaStream_t st);
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st);
-cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, bool overlap,
-                                 cudaStream_t st);
+cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, cudaStream_t st);
 cudaError_t launch_token_logprobs(const LogprobParams& p, int sms, cudaStream_t st);
 
 // What the entry points of another translation unit share with api.cu.
