@@ -67,6 +67,8 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   constexpr int CH = D / 16;              // items (16 elements) of a row
   constexpr int IT = D / 32;              // items of a lane
   __shared__ uint32_t warp_max[8];
+  __shared__ uint64_t rope_bar[8];
+  extern __shared__ __align__(128) CosSin2 rope_rows[];   // APPEND: 8 KB for each warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y / p.pool.n_kv, h = blockIdx.y % p.pool.n_kv;
   const int kv = blockIdx.z & 1, layer = blockIdx.z >> 1;
@@ -95,7 +97,7 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   const int prow = wrow / page * page;                  // first row of this warp's page
   const bool touched = prow < end && prow + page > first;
   const int pid = touched ? p.page_table[(size_t)b * p.max_pages + wrow / page] : -1;
-  const bool ok = touched && pid >= 0 && pid < p.pool.n_pages;
+  bool ok = touched && pid >= 0 && pid < p.pool.n_pages;
   if (touched && !ok && lane == 0) atomicOr(p.err, kErrLength);
   const size_t block = ok ? (size_t)layer * p.scale_layer + (size_t)pid * p.pool.n_kv + h : 0;
   uint8_t* codes = p.pool.codes[kv] + block * (size_t)page * D;
@@ -120,6 +122,27 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   if (turn) {
     const int pr = lane % LPR;   // the lane's pairs of the row: 2 pr, 2 pr + 1
     uint32_t raw = 0;
+    // The RoPE rows come by bulk copies, 8 KB at a time, the first while the
+    // keys are read (the rows are most of what this path reads, and registers
+    // would hold a few of them at a time, a wait for each few).
+    constexpr int CROWS = 8192 / (D / 2 * 16);   // rows of a copy
+    CosSin2* tab = rope_rows + warp * 512;
+    auto copy = [&](int c0) {   // rows c0 .. c0 + CROWS of the warp's, those of them that are new
+      const int lo = max(wrow + c0, first), hi = min(wrow + c0 + CROWS, end);
+      if (lane == 0 && lo < hi) {
+        const uint32_t bytes = (uint32_t)(hi - lo) * (D / 2) * sizeof(CosSin2);
+        mbar_arrive_expect_tx(&rope_bar[warp], bytes);
+        bulk_g2s(tab + (lo - wrow - c0) * (D / 2), p.tab + (size_t)(rr + lo - first) * (D / 2), bytes, &rope_bar[warp]);
+      }
+      return lo < hi;
+    };
+    if (lane == 0) {
+      mbar_init(&rope_bar[warp], 1);
+      fence_barrier_init();
+    }
+    __syncwarp();
+    bool coming = copy(0);
+    int phase = 0;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = wrow + i * RPI + lane / LPR;
@@ -135,8 +158,20 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
       const int r = wrow + i * RPI + lane / LPR;
+      if (i * RPI % CROWS == 0) {
+        if (i > 0) {
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+          coming = copy(i * RPI);
+        }
+        if (coming && !mbar_wait(&rope_bar[warp], phase++ & 1)) {
+          atomicOr(p.err, kErrTimeout);
+          ok = false;
+        }
+        __syncwarp();
+      }
       if (!in(r)) continue;
-      const CosSin2* t = p.tab + (size_t)(rr + r - first) * (D / 2) + 2 * pr;
+      const CosSin2* t = tab + (r - wrow - i * RPI / CROWS * CROWS) * (D / 2) + 2 * pr;
       const CosSin2 t0 = t[0], t1 = t[1];
       const float x0 = __uint_as_float(w[2 * i] << 16), x1 = __uint_as_float(w[2 * i] & 0xFFFF0000u);
       const float y0 = __uint_as_float(w[2 * i + 1] << 16), y1 = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u);
@@ -233,7 +268,21 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
 
 template <int D, bool APPEND>
 cudaError_t launch_put(const PutParams& p, dim3 grid, int threads, cudaStream_t st) {
+  static KernelSetup s;
+  const int dev = setup_device();
+  if (dev < 0) return cudaErrorInvalidDevice;
+  if (APPEND) {
+    std::lock_guard<std::mutex> lk(s.mu);
+    if (s.state[dev] == 0) {
+      const cudaError_t e = cudaFuncSetAttribute(put_kernel<D, APPEND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 PUT_MAX_ROWS / PUT_WARP_ROWS * 8192);
+      if (e != cudaSuccess) cudaGetLastError();
+      s.state[dev] = e == cudaSuccess ? 1 : -(int)e;
+    }
+    if (s.state[dev] != 1) return (cudaError_t)(-s.state[dev]);
+  }
   cudaLaunchConfig_t cfg = {};
+  cfg.dynamicSmemBytes = APPEND ? threads / 32 * 8192 : 0;
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
