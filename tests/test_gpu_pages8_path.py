@@ -244,3 +244,68 @@ def test_model_step_and_its_log_probabilities():
                 assert (a == want).all()
     assert int(r.rb.n_cached_dev[0]) == r.rows[0] + 2
     r.sc.close()
+
+
+def test_shared_pages_and_calls_at_once():
+    """Two sequences read the same pages (a shared prefix, nothing appended) and
+    answer alike; two batches decoded at once on two streams, each with its own
+    pages and scratch, answer as one after the other."""
+    a, b = (Requests(S.Geometry(1, 32, 8, 128, 5.0e5), 32, batch=4, seed=s) for s in (1, 2))
+    rb = a.rb
+    table = rb.page_table.clone()
+    table[1] = table[0]
+    n = rb.n_cached_dev.clone()
+    n[1] = n[0]
+    q = a.dev["qd_pre"][0, 0].clone()
+    q[1] = q[0]
+    row = rb.rope_row_dev.clone()
+    row[1] = row[0]
+    out = torch.empty_like(q)
+    P.c2kv_attend_pages8(a.g, 0, rb.k8, rb.v8, rb.k_scale, rb.v_scale, table, n, rb.max_keys_decode, q, None, None,
+                         rb.rope_table, row, out, rb.workspace8)
+    torch.cuda.synchronize()
+    assert P.c2kv_device_error() == P.C2KV_OK
+    assert torch.equal(out[0], out[1]) and out.isfinite().all()
+
+    def run(streams):
+        outs = []
+        for r, st in zip((a, b), streams):
+            r.rb.reset_decode(st)
+        torch.cuda.synchronize()
+        for t in range(a.steps):
+            for r, st in zip((a, b), streams):
+                o = torch.empty_like(r.dev["qd_pre"][t, 0])
+                r.rb.decode(0, r.dev["qd_pre"][t, 0], r.dev["kd_pre"][t, 0], r.dev["vd"][t, 0], o, st)
+                r.rb.advance(st)
+                outs.append(o)
+        torch.cuda.synchronize()
+        assert P.c2kv_device_error() == P.C2KV_OK
+        return torch.stack(outs)
+
+    one = torch.cuda.current_stream()
+    serial = run((one, one))
+    at_once = run((torch.cuda.Stream(), torch.cuda.Stream()))
+    assert torch.equal(serial, at_once)
+    a.sc.close()
+    b.sc.close()
+
+
+def test_many_launches_give_the_same_bits():
+    """Which CTA finishes last varies; what it merges, and in what order, does not."""
+    r = Requests(S.Geometry(1, 32, 8, 128, 5.0e5), 16, batch=4)
+    outs = []
+    for _ in range(40):
+        o = torch.empty_like(r.dev["qd_pre"][0, 0])
+        r.rb.decode(0, r.dev["qd_pre"][0, 0], r.dev["kd_pre"][0, 0], r.dev["vd"][0, 0], o)
+        outs.append(o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, outs[0]) for o in outs[1:])
+    x = torch.randn(16, 128256, device="cuda").to(torch.bfloat16)
+    got = []
+    for _ in range(10):
+        lp, ent, tops = (torch.empty(s, device="cuda") for s in ((16,), (16,), (16, 12)))
+        ids = torch.empty((16, 12), dtype=torch.int32, device="cuda")
+        P.c2kv_token_logprobs(x, torch.arange(16, dtype=torch.int32, device="cuda"), 12, lp, ent, ids, tops)
+        got.append(torch.cat([lp, ent, ids.float().flatten(), tops.flatten()]))
+    assert all(torch.equal(t, got[0]) for t in got[1:])
+    r.sc.close()
