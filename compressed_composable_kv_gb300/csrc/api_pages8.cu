@@ -125,6 +125,7 @@ c2kv_status c2kv_pages8_append(const c2kv_geometry* geom, const c2kv_pages8* pag
   s = check_new_tokens(batch, n_cached_dev, k_new, v_new, rope_table, table_rows, rope_row_dev);
   if (s != C2KV_OK) return s;
   if (!k_new || !v_new) return api_fail(C2KV_EINVAL, "null pointer");
+  if ((int64_t)batch * geom->n_kv_heads > 65535) return api_fail(C2KV_EINVAL, "batch * n_kv_heads must be below 65536");
   if (t_len < 1 || t_len > INT32_MAX / 2) return api_fail(C2KV_EINVAL, "t_len must be >= 1");
   if (t_len > max_pages * pages->page) return api_fail(C2KV_ECAPACITY, "t_len exceeds max_pages * page");
   s = api_device_state(&p.err, nullptr);

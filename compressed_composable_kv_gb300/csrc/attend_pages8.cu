@@ -23,11 +23,28 @@
 // output lane reads the columns of its own half.  A page of 16 to 128 tokens
 // is 1 to 16 KB of a tile and one TMA load.
 //
-// Work: the tiles of all (sequence, kv head) units are laid end to end and cut
-// into one equal range per CTA, from the device-side lengths, so that any mix
-// of lengths keeps every SM streaming.  A unit that one CTA holds whole is
-// written at once; else its CTAs write partial (m, l, O), and the one whose
-// tiles complete the unit's counter merges them.
+// Work: two CTAs to an SM share the tiles of all (sequence, kv head) units, from
+// the device-side lengths.  Where the CTAs suffice every unit is cut into parts
+// of about one length, a CTA to a part, so that no CTA works on two units and
+// holds up the loads of one while it ends the other; else (more units than
+// CTAs, or lengths so mixed that the longest part would be 1.5 times an even
+// share) the tiles are laid end to end and cut into one equal range per CTA.
+// 8 x 8000 keys of 5 heads to a kv head: 33 us by parts, 39 us by ranges; 16
+// sequences of 2 to 16 thousand keys 35 and 39; 4 x 32768 52 and 58.
+// A unit that one CTA holds whole is written at once; else its CTAs write
+// partial (m, l, O), and the one whose tiles complete the unit's counter merges
+// them, in the order of the keys whoever it is.
+//
+// Measured (one call among others in a graph; 6.8 TB/s is a plain copy's rate):
+//   4 x 32768 keys, 8 kv heads of 4 (269 MB)   51 us   5.2 TB/s
+//   8 x 8000 keys, 8 kv heads of 5 (131 MB)    33 us   4.0 TB/s
+//   16 ragged, 4 heads (142 MB)                36 us   4.0 TB/s
+//   1 x 8000 keys, 4 heads (16 MB)             12.7 us
+//   16 sequences of up to 100 keys              9.3 us
+// While tiles stream they come at 6.9 TB/s.  What is left is the latency of a
+// call: 4 us to the first tile (launch, lengths, page ids, the load itself),
+// 1.4 us from the last tile to the CTA's partial, 2.5 to 3 us for arrival and
+// merge, and at mixed lengths the wait for the longest part.
 //
 // Roles: warps 0-3 softmax and epilogue (thread t owns row t of a tile, then
 // lane t of O^T), warp 4 K's pages and the scales, warp 5 MMA, warp 6 the
@@ -50,7 +67,9 @@ constexpr int AP_KV_BYTES = 128 * 128;          // K (or V) of one tile
 constexpr int AP_STAGE = 2 * AP_KV_BYTES;
 constexpr int AP_MAX_PPT = 16;                  // pages of a tile
 
-constexpr int kMinTiles = 4;     // tiles of a CTA below which fewer CTAs work
+// Tiles of a CTA below which fewer CTAs work: more partials cost the merge more
+// than they save the stream (1 x 8000 keys at 2, 3, 4: 13.4, 12.9, 12.4 us).
+constexpr int kMinTiles = 4;
 constexpr int kMergeRows = 64;   // partials of one round of a merge
 
 // The tiles of a launch, from the device-side lengths (fewer than 2^31, which
@@ -391,12 +410,11 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   const int ntiles = x1 - x0;
   if (warp == 4 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.tm[lane]) : "memory");
   if (*none_flag) {
-    // sequences without a row: their output is zero
+    // sequences without a row: their output is zero (out need not be 16-byte aligned)
     grid_wait();
     for (int b = cta; b < p.batch; b += ctas)
       if (M.keys[b] == 0)
-        for (int i = tid; i < p.n_q * D / 8; i += AP_THREADS)
-          reinterpret_cast<uint4*>(p.out + (size_t)b * p.n_q * D)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < p.n_q * D; i += AP_THREADS) p.out[(size_t)b * p.n_q * D + i] = __float2bfloat16_rn(0.f);
   }
   if (ntiles == 0) {   // uniform over the CTA
     grid_wait();

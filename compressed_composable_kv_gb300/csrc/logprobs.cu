@@ -12,11 +12,11 @@
 //
 // Top alternatives: in the CTA's first 2048 vectors, the k-th largest of the
 // maxima of its 64 groups of 4 threads is a bound that at least k logits reach.
-// Vectors that reach it, a few for each 2048, are noted on the way; behind the
-// stream their logits are listed and the list's ranks counted.  Where too many
-// reach the bound (rows of equal or rising logits, or all but a few ruled out)
-// the k largest are found one after another instead.  Logits are ordered as
-// whole numbers, (value, lower index first), so that equal ones have one order.
+// Vectors that reach it (later ones: that exceed it), a few for each 2048, are
+// noted on the way; behind the stream their logits are listed and the list's
+// ranks counted.  Where very many do (rows of rising logits) the k largest are
+// found one after another instead.  Logits are ordered as whole numbers,
+// (value, lower index first), so that equal ones have one order.
 #include "pages8.h"
 
 namespace c2kv {
@@ -36,7 +36,7 @@ constexpr float kFaint = -200.f;                      // exp of it is 0 in fp32
 // Larger logit first (NaN above all, -0 and +0 alike).
 __device__ __forceinline__ uint32_t order_bits(float x) {
   uint32_t u = __float_as_uint(x);
-  if (x != x) return 0xFFFFFFFFu;
+  if (x != x) return 0xFFFFFFFEu;   // a NaN too; with any index below ~0ull
   if (u == 0x80000000u) u = 0;
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
@@ -242,7 +242,7 @@ __device__ __forceinline__ float group_bound(LpShared& sh, const float (&vm)[LP_
   }
   r += __shfl_xor_sync(0xffffffffu, r, 1);
   r += __shfl_xor_sync(0xffffffffu, r, 2);
-  if ((tid & 3) == 0 && r == k - 1) sh.bound = v == 0xFFFFFFFFu ? NAN : from_order(v);
+  if ((tid & 3) == 0 && r == k - 1) sh.bound = from_order(v);
   __syncthreads();
   return sh.bound;
 }
@@ -295,17 +295,45 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
       q.m = fmaxf(q.m, vm[c]);
     }
     if (k > 0) {
-      if (vb == pc.v0) bound = group_bound(sh, vm, tid, k);
+      const bool first = vb == pc.v0;
+      if (first) bound = group_bound(sh, vm, tid, k);
+      auto note = [&](int c) {
+        const int at = atomicAdd(&sh.n_hits, 1);
+        if (at < LP_HITS) {
+          sh.hit[at] = d[c];
+          sh.hit_at[at] = vb + c * LP_THREADS + tid;
+        }
+      };
+      auto reaches = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && !(vm[c] < bound); };
+      auto above = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && bound == bound && !(vm[c] <= bound); };
+      if (first) {
 #pragma unroll
-      for (int c = 0; c < LP_VECS; ++c) {
-        const int v = vb + c * LP_THREADS + tid;
-        if (!(vm[c] < bound) && v < pc.v1) {
-          const int at = atomicAdd(&sh.n_hits, 1);
-          if (at < LP_HITS) {
-            sh.hit[at] = d[c];
-            sh.hit_at[at] = v;
+        for (int c = 0; c < LP_VECS; ++c)
+          if (reaches(c)) note(c);
+        __syncthreads();
+        if (sh.n_hits > LP_HITS) {
+          // Many equal the bound (a mask's value, say): of these the first k in
+          // order will do.
+#pragma unroll
+          for (int c = 0; c < LP_VECS; ++c) {
+            const uint32_t eq = __ballot_sync(0xffffffffu, reaches(c) && !above(c));
+            if (lane == 0) sh.group[c * LP_WARPS + warp] = __popc(eq);
+          }
+          __syncthreads();
+          if (tid == 0) sh.n_hits = 0;
+          __syncthreads();
+#pragma unroll
+          for (int c = 0; c < LP_VECS; ++c) {
+            const bool is = reaches(c) && !above(c);
+            int place = __popc(__ballot_sync(0xffffffffu, is) & ((1u << lane) - 1u));
+            for (int j = 0; j < c * LP_WARPS + warp; ++j) place += sh.group[j];
+            if (above(c) || (is && place < k)) note(c);
           }
         }
+      } else {   // k logits at or above the bound lie before these: they have to be above it
+#pragma unroll
+        for (int c = 0; c < LP_VECS; ++c)
+          if (above(c)) note(c);
       }
     }
     const float from = q.m == -INFINITY ? 0.f : q.m;

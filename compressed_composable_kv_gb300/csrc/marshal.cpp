@@ -214,7 +214,7 @@ PyObject* attend_pages8(PyObject*, PyObject* const* a, Py_ssize_t n) {
         optional(r[4], "k_new", at::kBFloat16, {batch, h, d}, p.dev),
         optional(r[5], "v_new", at::kBFloat16, {batch, h, d}, p.dev), rope, rows,
         (const int32_t*)address(r[7], "rope_row_dev", at::kInt, {batch}, p.dev),
-        address(r[8], "out", at::kBFloat16, {batch, hq, d}, p.dev), ws, ws_bytes, (uint32_t)as_int(r[10]),
+        address(r[8], "out", at::kBFloat16, {batch, hq, d}, p.dev), ws, ws_bytes, (uint32_t)as_int32(r[10], "flags"),
         (void*)as_int(r[11])));
   });
 }

@@ -127,8 +127,10 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
     // would hold a few of them at a time, a wait for each few).
     constexpr int CROWS = 8192 / (D / 2 * 16);   // rows of a copy
     CosSin2* tab = rope_rows + warp * 512;
+    bool late = false;   // a copy did not come in time
     auto copy = [&](int c0) {   // rows c0 .. c0 + CROWS of the warp's, those of them that are new
       const int lo = max(wrow + c0, first), hi = min(wrow + c0 + CROWS, end);
+      if (late) return false;
       if (lane == 0 && lo < hi) {
         const uint32_t bytes = (uint32_t)(hi - lo) * (D / 2) * sizeof(CosSin2);
         mbar_arrive_expect_tx(&rope_bar[warp], bytes);
@@ -164,10 +166,14 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
           __syncwarp();
           coming = copy(i * RPI);
         }
-        if (coming && !mbar_wait(&rope_bar[warp], phase++ & 1)) {
+        if (coming && !mbar_wait(&rope_bar[warp], phase & 1)) {
           atomicOr(p.err, kErrTimeout);
           ok = false;
+          late = true;
+          mbar_wait(&rope_bar[warp], phase & 1);   // let it land before the shared memory is released
         }
+        if (coming) ++phase;
+        late = __any_sync(0xffffffffu, late);
         __syncwarp();
       }
       if (!in(r)) continue;

@@ -128,7 +128,7 @@ struct PagePool {
 // (fill) or new tokens (append).
 struct PutParams {
   PagePool pool;                 // of the first layer written
-  int64_t code_layer, scale_layer;   // elements from one layer to the next (fill)
+  int64_t scale_layer;           // scales from one layer to the next (fill)
   const int32_t* page_table;     // [batch][max_pages]
   int32_t max_pages, batch, n_layers;
   unsigned* err;

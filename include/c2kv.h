@@ -491,7 +491,7 @@ c2kv_status c2kv_pages8_fill(const c2kv_geometry* geom, const c2kv_pages8* pages
  * table_rows rows (layout of c2kv_rope_table); token i's key is rotated by its
  * row rope_row_dev[b] + i, rounded to fp32 and from there to bf16, about as a
  * bf16 cache would hold it, before it is rounded to its code.  The lengths are not advanced
- * (c2kv_seq_advance).  batch <= 256.  A sequence whose tokens would not fit
+ * (c2kv_seq_advance).  batch <= 256, batch * n_kv_heads < 65536.  A sequence whose tokens would not fit
  * max_pages pages, or whose table rows are out of range, is left out whole.
  */
 c2kv_status c2kv_pages8_append(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,

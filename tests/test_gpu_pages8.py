@@ -363,6 +363,25 @@ def test_attend_long(n_kv, batch):
     _attend_case(_geom(64, 1, n_kv), 16, [4000 - 1000 * b for b in range(batch)])
 
 
+def test_attend_output_at_any_element():
+    """out starts at an odd element; one sequence has rows, one has none."""
+    g = S.Geometry(1, 4, 2, 128, 1e4)
+    k8 = torch.zeros((1, 2, 2, 16, 128), dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    sc = torch.ones((1, 2, 2), device="cuda")
+    v8 = torch.full((1, 2, 2, 16, 128), 0x38, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)   # 1.0
+    table = torch.tensor([[0], [1]], dtype=torch.int32, device="cuda")
+    n = torch.tensor([5, 0], dtype=torch.int32, device="cuda")
+    q = torch.randn(2, 4, 128, device="cuda").to(torch.bfloat16)
+    buf = torch.full((2 * 4 * 128 + 9,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[1:1 + 2 * 4 * 128].view(2, 4, 128)
+    rope = torch.zeros((16, 64, 4), device="cuda")
+    ws = torch.zeros(P.c2kv_attend_pages8_workspace_size(g, 2, 16), dtype=torch.uint8, device="cuda")
+    P.c2kv_attend_pages8(g, 0, k8, v8, sc, sc, table, n, 16, q, None, None, rope, torch.zeros_like(n), out, ws)
+    assert P.c2kv_device_error() == P.C2KV_OK
+    assert (out[0] == 1.0).all() and (out[1] == 0.0).all()
+    assert buf[0] == 7.0 and (buf[-8:] == 7.0).all()
+
+
 def test_many_faint_rows_keep_their_weight():
     """One row with weight 1 and 20000 rows of 2^-14 each, their V all ones:
     the faint rows make up over half of the answer."""
@@ -539,6 +558,29 @@ def test_logprobs_ties_masks_and_strange_rows(dtype, vocab):
     x[10] = -torch.arange(vocab, device="cuda") / 8.0
     x[11] = torch.finfo(dtype).min
     _check_logprobs(x.to(dtype), 64)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("vocab", [200, 40000, 300007])
+@pytest.mark.parametrize("k", [1, 20, 64])
+def test_logprobs_of_many_equal_and_unordered_logits(dtype, vocab, k):
+    """NaN everywhere, in most places, from the second logit on; +inf in most
+    places; masks that leave a range at the end, every 50th token, a random
+    tenth; equal logits but for a few larger ones late in the row."""
+    gen = torch.Generator(device="cuda").manual_seed(vocab + k)
+    x = torch.randn(9, vocab, generator=gen, device="cuda")
+    few = torch.rand(vocab, generator=gen, device="cuda") < 0.1
+    x[0] = torch.nan
+    x[1, ~few] = torch.nan
+    x[2, 1:] = torch.nan
+    x[3, ~few] = torch.inf
+    x[4, : vocab - vocab // 3] = -torch.inf
+    x[5, : vocab - vocab // 3] = torch.finfo(dtype).min
+    x[6, torch.arange(vocab, device="cuda") % 50 != 7] = torch.finfo(dtype).min
+    x[7, ~few] = -torch.inf
+    x[8] = 1.0
+    x[8, vocab - 30 :: 7] = 2.0
+    _check_logprobs(x.to(dtype), k)
 
 
 def test_logprobs_strides_offsets_and_options():

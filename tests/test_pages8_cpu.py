@@ -100,6 +100,8 @@ def test_refusals_of_append_and_attend_alone(P):
     assert _append(P, pages=pg, t_len=0) == P.C2KV_EINVAL
     assert _append(P, pages=pg, k=None) == P.C2KV_EINVAL
     assert _append(P, pages=pg, t_len=65) == P.C2KV_ECAPACITY      # 4 pages of 16
+    many = S.Geometry(1, 256, 256, 64, 1e4)
+    assert _append(P, g=many, pages=pg, batch=256) == P.C2KV_EINVAL     # 65536 heads of sequences
     for bad in (dict(q=None), dict(out=None), dict(ws=None), dict(ws=A + 4), dict(k=None), dict(v=None), dict(q=A + 2),
                 dict(max_keys=0), dict(max_keys=65), dict(flags=2), dict(ws_bytes=64)):
         assert _attend(P, pages=pg, **bad) == P.C2KV_EINVAL, bad
