@@ -14,15 +14,26 @@
 // maxima of its 64 groups of 4 threads is a bound that at least k logits reach.
 // Vectors that reach it (later ones: that exceed it), a few for each 2048, are
 // noted on the way; behind the stream their logits are listed and the list's
-// ranks counted.  Where very many do (rows of rising logits) the k largest are
-// found one after another instead.  Logits are ordered as whole numbers,
+// ranks counted.  Where very many do (logits that rise along the row, a mask
+// that leaves a late part of it) a second pass takes new bounds on its way, and
+// where even these leave too many the k largest are found one after another.
+// Logits are ordered as whole numbers,
 // (value, lower index first), so that equal ones have one order.
+//
+// Measured (one call among others in a graph; 6.8 TB/s is a plain copy's rate):
+// 256 x 50257 fp32 logits with a fifth masked, top 20: 18 us (2.8 TB/s), with no
+// alternatives 13 us (4.0 TB/s), all but 50 masked 24 us, rising along the row
+// 89 us; 256 x 128256 bf16, top 5: 20 us (3.3 TB/s); 4 x 128256: 5.8 us.  About
+// 5 us of a call are launch, first loads and the join of a row's CTAs, 4 us more
+// the lists, while no logits stream: at these sizes every CTA runs at once.
 #include "pages8.h"
 
 namespace c2kv {
 
 namespace {
 
+// 512 threads take 1.2 us off 256 rows and add 1 us to 4 rows; steps of 4 vectors
+// with the next ones loaded ahead add 4 us to 256 rows.
 constexpr int LP_THREADS = 256;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_VECS = 8;                            // 16-byte loads of a thread
@@ -180,7 +191,7 @@ __device__ __forceinline__ uint64_t list_key(float x, int i) {
 }
 
 // The same from all logits of the piece, one after another: the way out where
-// too many reach the bound.
+// too many reach every bound.
 template <typename T>
 __device__ __noinline__ void one_by_one(LpShared& sh, const Piece<T>& pc, int k) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -247,6 +258,89 @@ __device__ __forceinline__ float group_bound(LpShared& sh, const float (&vm)[LP_
   return sh.bound;
 }
 
+// A vector that reaches the bound; n_hits says if there was room for all.
+__device__ __forceinline__ void note(LpShared& sh, const uint4& d, int v) {
+  const int at = atomicAdd(&sh.n_hits, 1);
+  if (at < LP_HITS) {
+    sh.hit[at] = d;
+    sh.hit_at[at] = v;
+  }
+}
+
+// Notes a step's vectors that reach the step's bound.  Where many equal it (a
+// mask's value, say) the first k of these in order will do.
+template <typename T>
+__device__ __forceinline__ void note_step(LpShared& sh, const Piece<T>& pc, const uint4 (&d)[LP_VECS],
+                                          const float (&vm)[LP_VECS], int vb, float bound, int k) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  auto reaches = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && !(vm[c] < bound); };
+  auto above = [&](int c) { return reaches(c) && bound == bound && !(vm[c] <= bound); };
+#pragma unroll
+  for (int c = 0; c < LP_VECS; ++c)
+    if (reaches(c)) note(sh, d[c], vb + c * LP_THREADS + tid);
+  __syncthreads();
+  if (sh.n_hits <= LP_HITS) return;
+#pragma unroll
+  for (int c = 0; c < LP_VECS; ++c) {
+    const uint32_t eq = __ballot_sync(0xffffffffu, reaches(c) && !above(c));
+    if (lane == 0) sh.group[c * LP_WARPS + warp] = __popc(eq);
+  }
+  __syncthreads();
+  if (tid == 0) sh.n_hits = 0;
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < LP_VECS; ++c) {
+    const bool is = reaches(c) && !above(c);
+    int place = __popc(__ballot_sync(0xffffffffu, is) & ((1u << lane) - 1u));
+    for (int j = 0; j < c * LP_WARPS + warp; ++j) place += sh.group[j];
+    if (above(c) || (is && place < k)) note(sh, d[c], vb + c * LP_THREADS + tid);
+  }
+}
+
+// top[0..k) in a second pass that takes a bound of its own for every 2048
+// vectors: where logits rise along the row, or a mask leaves a later part of
+// it.  False where still too many reach it.
+template <typename T>
+__device__ __noinline__ bool step_by_step(LpShared& sh, const Piece<T>& pc, int k) {
+  const int tid = threadIdx.x;
+  constexpr int STEP = LP_VECS * LP_THREADS, N = Vec<T>::N;
+  int have = 0;
+  for (int vb = pc.v0; vb < pc.v1; vb += STEP) {
+    const int w = max(pc.v0, min(vb, pc.v1 - STEP));   // a whole step, vectors before vb again
+    uint4 d[LP_VECS];
+    load_vecs(pc, w + tid, d);
+    float vm[LP_VECS];
+#pragma unroll
+    for (int c = 0; c < LP_VECS; ++c) vm[c] = Vec<T>::largest(d[c]);
+    __syncthreads();   // the list of the step before has been ranked
+    if (tid == 0) {
+      sh.n_hits = 0;
+      sh.count = have;
+    }
+    if (tid < have) sh.cand[tid] = sh.top[tid];
+    const float bound = group_bound(sh, vm, tid, k);
+    note_step(sh, pc, d, vm, w, bound, k);
+    __syncthreads();
+    if (sh.n_hits > LP_HITS) return false;
+    if (tid < k) sh.top[tid] = 0;
+    auto list = [&](float v, int i) {
+      const int at = atomicAdd(&sh.count, 1);
+      if (at < LP_CAND) sh.cand[at] = list_key(v, i);
+    };
+    for (int i = tid; i < sh.n_hits * N; i += LP_THREADS) {
+      const float v = (float)reinterpret_cast<const T*>(sh.hit)[i];
+      if (sh.hit_at[i / N] >= vb && !(v < bound)) list(v, pc.index(sh.hit_at[i / N], i % N));
+    }
+    if (vb == pc.v0 && tid < pc.extra) list((float)pc.x[pc.extra_at(tid)], pc.extra_at(tid));
+    __syncthreads();
+    const int found = sh.count;
+    if (found > LP_CAND) return false;
+    rank_into(sh, found, k);
+    have = min(k, found);
+  }
+  return true;
+}
+
 // The address of `p` of this CTA's shared memory in the cluster's first CTA.
 __device__ __forceinline__ uint32_t in_first_cta(const void* p) {
   uint32_t r;
@@ -295,45 +389,15 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
       q.m = fmaxf(q.m, vm[c]);
     }
     if (k > 0) {
-      const bool first = vb == pc.v0;
-      if (first) bound = group_bound(sh, vm, tid, k);
-      auto note = [&](int c) {
-        const int at = atomicAdd(&sh.n_hits, 1);
-        if (at < LP_HITS) {
-          sh.hit[at] = d[c];
-          sh.hit_at[at] = vb + c * LP_THREADS + tid;
-        }
-      };
-      auto reaches = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && !(vm[c] < bound); };
-      auto above = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && bound == bound && !(vm[c] <= bound); };
-      if (first) {
-#pragma unroll
-        for (int c = 0; c < LP_VECS; ++c)
-          if (reaches(c)) note(c);
-        __syncthreads();
-        if (sh.n_hits > LP_HITS) {
-          // Many equal the bound (a mask's value, say): of these the first k in
-          // order will do.
-#pragma unroll
-          for (int c = 0; c < LP_VECS; ++c) {
-            const uint32_t eq = __ballot_sync(0xffffffffu, reaches(c) && !above(c));
-            if (lane == 0) sh.group[c * LP_WARPS + warp] = __popc(eq);
-          }
-          __syncthreads();
-          if (tid == 0) sh.n_hits = 0;
-          __syncthreads();
-#pragma unroll
-          for (int c = 0; c < LP_VECS; ++c) {
-            const bool is = reaches(c) && !above(c);
-            int place = __popc(__ballot_sync(0xffffffffu, is) & ((1u << lane) - 1u));
-            for (int j = 0; j < c * LP_WARPS + warp; ++j) place += sh.group[j];
-            if (above(c) || (is && place < k)) note(c);
-          }
-        }
+      if (vb == pc.v0) {
+        bound = group_bound(sh, vm, tid, k);
+        note_step(sh, pc, d, vm, vb, bound, k);
       } else {   // k logits at or above the bound lie before these: they have to be above it
 #pragma unroll
-        for (int c = 0; c < LP_VECS; ++c)
-          if (above(c)) note(c);
+        for (int c = 0; c < LP_VECS; ++c) {
+          const int v = vb + c * LP_THREADS + tid;
+          if (v < pc.v1 && bound == bound && !(vm[c] <= bound)) note(sh, d[c], v);
+        }
       }
     }
     const float from = q.m == -INFINITY ? 0.f : q.m;
@@ -403,7 +467,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
     __syncthreads();
     const int found = sh.count, there = (pc.v1 - pc.v0) * V::N + pc.extra;
     if (n_hits <= LP_HITS && found <= LP_CAND && found >= min(k, there)) rank_into(sh, found, k);
-    else one_by_one(sh, pc, k);
+    else if (!step_by_step(sh, pc, k)) one_by_one(sh, pc, k);
   }
   __syncthreads();
 
@@ -482,7 +546,8 @@ cudaError_t launch_lp(LogprobParams p, int sms, cudaStream_t st) {
     if (s.state[dev] != 1) return (cudaError_t)(-s.state[dev]);
   }
   // Two CTAs for each SM where the rows are fewer, but at least two vectors for
-  // each thread and at most 16 CTAs to a row.
+  // each thread and at most 16 CTAs to a row (256 x 50257 fp32: 19.8 us with half
+  // as many CTAs, 17.9 so, 21 with twice as many).
   const int64_t nvec = p.vocab / Vec<T>::N;
   int cs = 1;
   while (cs < LP_MAX_CLUSTER && (int64_t)p.rows * cs < 2 * sms && nvec >= (int64_t)cs * 4 * LP_THREADS) cs *= 2;

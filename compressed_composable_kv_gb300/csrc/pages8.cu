@@ -13,8 +13,16 @@
 // A CTA owns 64 consecutive rows of one (sequence, kv head), of K or of V (128
 // where a page is that long): a whole number of pages, so a page's largest
 // magnitude never leaves the CTA.  A warp owns 16 rows and keeps them, as bf16,
-// in registers between the two steps (largest magnitude, codes), so the data
-// are read once, with all loads of a warp in flight.  Bound by the bytes moved.
+// // in registers between the two steps (largest magnitude, codes), so the data
+// are read once, with all loads of a warp in flight.
+//
+// Fill is bound by the bytes moved: 32 layers of 8000 rows, 8 kv heads of 128
+// (1.57 GB) 224 us, 7.0 TB/s (a plain copy: 6.8).  Append is bound by the
+// rotation and by latency: the two halves of a pair must round as the exact
+// values do, which costs a test for each and cos/sin in two parts, 1 KB of table
+// for each token of each kv head (from L2).  1 x 4000 tokens 12.4 us (28 MB),
+// 4 x 4000 38 us, 8 ragged sequences of up to 128 9.0 us, 16 x 1 4.6 us, which is
+// a launch and four dependent reads.
 #include "pages8.h"
 
 namespace c2kv {
@@ -62,6 +70,8 @@ __device__ __forceinline__ void tame(uint32_t& w, uint32_t& m) {
 
 // D: head_dim.  APPEND: rows [n_cached, n_cached + new) from the new tokens,
 // K rotated; else rows [0, n_rows) from the bf16 caches.
+// CTAs per SM: append at 2, 3, 4 takes 14.8, 17.8, 18.7 us for 1 x 4000 tokens
+// (registers for the rows in flight); fill is fastest at 3.
 template <int D, bool APPEND>
 __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 : 3) put_kernel(const __grid_constant__ PutParams p) {
   constexpr int CH = D / 16;              // items (16 elements) of a row

@@ -566,9 +566,10 @@ def test_logprobs_ties_masks_and_strange_rows(dtype, vocab):
 def test_logprobs_of_many_equal_and_unordered_logits(dtype, vocab, k):
     """NaN everywhere, in most places, from the second logit on; +inf in most
     places; masks that leave a range at the end, every 50th token, a random
-    tenth; equal logits but for a few larger ones late in the row."""
+    tenth; equal logits but for a few larger ones late in the row; logits that
+    rise along the row, smoothly and by steps; parts of every 2048 ruled out."""
     gen = torch.Generator(device="cuda").manual_seed(vocab + k)
-    x = torch.randn(9, vocab, generator=gen, device="cuda")
+    x = torch.randn(13, vocab, generator=gen, device="cuda")
     few = torch.rand(vocab, generator=gen, device="cuda") < 0.1
     x[0] = torch.nan
     x[1, ~few] = torch.nan
@@ -580,6 +581,10 @@ def test_logprobs_of_many_equal_and_unordered_logits(dtype, vocab, k):
     x[7, ~few] = -torch.inf
     x[8] = 1.0
     x[8, vocab - 30 :: 7] = 2.0
+    x[9] = torch.arange(vocab, device="cuda") / 1000.0
+    x[10] = torch.arange(vocab, device="cuda") // 5000 + x[10].clamp(-0.4, 0.4)
+    x[11, torch.arange(vocab, device="cuda") % 2048 < 64] = -100.0   # some of a step's groups far below the others
+    x[12, (torch.arange(vocab, device="cuda") % 1024 < 32) | ~few] = -torch.inf
     _check_logprobs(x.to(dtype), k)
 
 
