@@ -349,6 +349,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       if (bad && cta == 0) atomicOr(p.err, kErrLength);
     }
   } else if (warp == 4) {
+    if (lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.tm[lane]) : "memory");
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr((const void*)tmem_slot)),
                  "r"(C::TMEM_COLS)
@@ -408,7 +409,6 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     x1 = min(total, cut.first(cta + 1));
   }
   const int ntiles = x1 - x0;
-  if (warp == 4 && lane < 2) asm volatile("prefetch.tensormap [%0];" ::"l"(&p.tm[lane]) : "memory");
   if (*none_flag) {
     // sequences without a row: their output is zero (out need not be 16-byte aligned)
     grid_wait();
