@@ -486,26 +486,39 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       ask_scales(nxt);
       const Ref third = ask(j0 + 2 * per);
       if (kv == 0 && cur.id == -2) atomicOr(p.err, kErrLength);
-      for (int tt = 0; tt < per && j0 + tt < ntiles; ++tt) {
-        const int j = j0 + tt, s = j % C::STAGES, i = lane & (ppt - 1);
-        if (!before(j)) return false;
-        if (j >= C::STAGES &&
-            !__all_sync(0xffffffffu, ap_wait(&empty[s], ((j - C::STAGES) / C::STAGES) & 1, abort_flag, p.err)))
-          return false;
-        if ((lane >> lgp) == tt) {
-          // no page, or one outside the pool: a load from before the pool, which
-          // TMA fills with zeros; its scale 0 masks the keys
-          const int y = cur.id >= 0 ? (cur.id * p.pool.n_kv + cur.h) * prows : -prows;
-          tma_load_2d((kv == 0 ? stage_k(s) : stage_v(s)) + i * prows * 128, &p.tm[kv], 0, y, &full[s]);
-          if (kv == 0) {
-            float* scs = sc + j % C::SCALES * 2 * AP_MAX_PPT;
-            scs[i] = cur.ks;
-            scs[AP_MAX_PPT + i] = cur.vs;
-          }
+      const int i = lane & (ppt - 1);
+      auto request = [&](int j) {
+        if ((lane >> lgp) != j - j0) return;
+        // no page, or one outside the pool: a load from before the pool, which
+        // TMA fills with zeros; its scale 0 masks the keys
+        const int s = j % C::STAGES, y = cur.id >= 0 ? (cur.id * p.pool.n_kv + cur.h) * prows : -prows;
+        tma_load_2d((kv == 0 ? stage_k(s) : stage_v(s)) + i * prows * 128, &p.tm[kv], 0, y, &full[s]);
+      };
+      auto settle = [&](int j) {   // its scales, and what its loads will bring
+        if (kv == 0 && (lane >> lgp) == j - j0) {
+          float* scs = sc + j % C::SCALES * 2 * AP_MAX_PPT;
+          scs[i] = cur.ks;
+          scs[AP_MAX_PPT + i] = cur.vs;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], AP_KV_BYTES);
+        if (lane == 0) mbar_arrive_expect_tx(&full[j % C::STAGES], AP_KV_BYTES);
         ++issued;
+      };
+      int j = j0;
+      const int end = min(ntiles, j0 + per);
+      if (j0 == 0) {
+        // the first stages are asked for before the first scales are waited for
+        const int n0 = min(end, C::STAGES);
+        for (int t = 0; t < n0; ++t) request(t);
+        for (; j < n0; ++j) settle(j);
+      }
+      for (; j < end; ++j) {
+        if (!before(j)) return false;
+        if (j >= C::STAGES && !__all_sync(0xffffffffu, ap_wait(&empty[j % C::STAGES],
+                                                               ((j - C::STAGES) / C::STAGES) & 1, abort_flag, p.err)))
+          return false;
+        request(j);
+        settle(j);
       }
       cur = nxt;
       nxt = third;
