@@ -131,7 +131,6 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   for (int i = 0; i < 8 * IT; ++i) w[i] = 0;
   if (turn) {
     const int pr = lane % LPR;   // the lane's pairs of the row: 2 pr, 2 pr + 1
-    uint32_t raw = 0;
     // The RoPE rows come by bulk copies, 8 KB at a time, the first while the
     // keys are read (the rows are most of what this path reads, and registers
     // would hold a few of them at a time, a wait for each few).
@@ -164,49 +163,60 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
         w[2 * i + 1] = src[D / 4 + pr];
       }
     }
+    // Rows whose fp32 evaluation does not decide (a pair in 300 or so) are put
+    // off to the end of their copy, where each lane takes its own: the exact
+    // evaluation takes as long for one lane as for all.  Values that are not
+    // finite never decide, and come out as NaN in both of the pair.
+    constexpr int PER = CROWS / RPI;   // times of a copy
+    static_assert(NI % PER == 0, "whole copies");
 #pragma unroll
-    for (int i = 0; i < 2 * NI; ++i) raw = max_nan_bf16x2(raw, w[i] & 0x7FFF7FFFu);
-    const bool odd = __any_sync(0xffffffffu, larger_half(raw) >= 0x7F800000u);
-#pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int r = wrow + i * RPI + lane / LPR;
-      if (i * RPI % CROWS == 0) {
-        if (i > 0) {
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-          coming = copy(i * RPI);
-        }
-        if (coming && !mbar_wait(&rope_bar[warp], phase & 1)) {
-          atomicOr(p.err, kErrTimeout);
-          ok = false;
-          late = true;
-          mbar_wait(&rope_bar[warp], phase & 1);   // let it land before the shared memory is released
-        }
-        if (coming) ++phase;
-        late = __any_sync(0xffffffffu, late);
+    for (int i0 = 0; i0 < NI; i0 += PER) {
+      if (i0 > 0) {
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         __syncwarp();
+        coming = copy(i0 * RPI);
       }
-      if (!in(r)) continue;
-      const CosSin2* t = tab + (r - wrow - i * RPI / CROWS * CROWS) * (D / 2) + 2 * pr;
-      const CosSin2 t0 = t[0], t1 = t[1];
-      const float x0 = __uint_as_float(w[2 * i] << 16), x1 = __uint_as_float(w[2 * i] & 0xFFFF0000u);
-      const float y0 = __uint_as_float(w[2 * i + 1] << 16), y1 = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u);
-      float a0, b0, a1, b1;
-      const bool clear0 = turn_pair(x0, y0, t0.ch, t0.sh, a0, b0), clear1 = turn_pair(x1, y1, t1.ch, t1.sh, a1, b1);
-      if (clear0 && clear1) {
-        w[2 * i] = pack2(a0, a1);
-        w[2 * i + 1] = pack2(b0, b1);
-      } else {
-        w[2 * i] = rot_key_slow(x0, t0.ch, t0.cl, -y0, t0.sh, t0.sl) |
-                   (rot_key_slow(x1, t1.ch, t1.cl, -y1, t1.sh, t1.sl) << 16);
-        w[2 * i + 1] = rot_key_slow(y0, t0.ch, t0.cl, x0, t0.sh, t0.sl) |
-                       (rot_key_slow(y1, t1.ch, t1.cl, x1, t1.sh, t1.sl) << 16);
+      if (coming && !mbar_wait(&rope_bar[warp], phase & 1)) {
+        atomicOr(p.err, kErrTimeout);
+        ok = false;
+        late = true;
+        mbar_wait(&rope_bar[warp], phase & 1);   // let it land before the shared memory is released
       }
-      if (odd) {   // a pair with a member that is not finite is NaN in both
-        const uint32_t nan = (fabsf(x0) < INFINITY && fabsf(y0) < INFINITY ? 0u : 0x7FFFu) |
-                             (fabsf(x1) < INFINITY && fabsf(y1) < INFINITY ? 0u : 0x7FFF0000u);
-        w[2 * i] |= nan;
-        w[2 * i + 1] |= nan;
+      if (coming) ++phase;
+      late = __any_sync(0xffffffffu, late);
+      const CosSin2* t = tab + lane / LPR * (D / 2) + 2 * pr;
+      uint32_t open = 0;
+#pragma unroll
+      for (int i = i0; i < i0 + PER; ++i) {
+        if (!in(wrow + i * RPI + lane / LPR)) continue;
+        const CosSin2 t0 = t[(i - i0) * RPI * (D / 2)], t1 = t[(i - i0) * RPI * (D / 2) + 1];
+        const float x0 = __uint_as_float(w[2 * i] << 16), x1 = __uint_as_float(w[2 * i] & 0xFFFF0000u);
+        const float y0 = __uint_as_float(w[2 * i + 1] << 16), y1 = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u);
+        float a0, b0, a1, b1;
+        const bool clear0 = turn_pair(x0, y0, t0.ch, t0.sh, a0, b0), clear1 = turn_pair(x1, y1, t1.ch, t1.sh, a1, b1);
+        if (clear0 && clear1) {
+          w[2 * i] = pack2(a0, a1);
+          w[2 * i + 1] = pack2(b0, b1);
+        } else {
+          open |= 1u << (i - i0);
+        }
+      }
+      while (__any_sync(0xffffffffu, open != 0)) {
+        if (open == 0) continue;
+        const int k = __ffs(open) - 1;
+        open &= open - 1;
+        uint32_t wx = 0, wy = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i == k) wx = w[2 * (i0 + i)], wy = w[2 * (i0 + i) + 1];
+        const CosSin2 t0 = t[k * RPI * (D / 2)], t1 = t[k * RPI * (D / 2) + 1];
+        const float x0 = __uint_as_float(wx << 16), x1 = __uint_as_float(wx & 0xFFFF0000u);
+        const float y0 = __uint_as_float(wy << 16), y1 = __uint_as_float(wy & 0xFFFF0000u);
+        wx = rot_key_slow(x0, t0.ch, t0.cl, -y0, t0.sh, t0.sl) | (rot_key_slow(x1, t1.ch, t1.cl, -y1, t1.sh, t1.sl) << 16);
+        wy = rot_key_slow(y0, t0.ch, t0.cl, x0, t0.sh, t0.sl) | (rot_key_slow(y1, t1.ch, t1.cl, x1, t1.sh, t1.sl) << 16);
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (i == k) w[2 * (i0 + i)] = wx, w[2 * (i0 + i) + 1] = wy;
       }
     }
   } else {
