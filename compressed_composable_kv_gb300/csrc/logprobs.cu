@@ -114,6 +114,23 @@ __device__ __forceinline__ Part at_max(Part p, float M) {
   return {M, p.s * f, (p.t + p.s * d) * f};
 }
 
+// n <= 16 partial results as one, in a fixed order, in every lane of a warp.
+__device__ __forceinline__ Part join16(const Part* from, int n, int lane) {
+  const int i = lane & 15;
+  Part q = {-INFINITY, 0.f, 0.f};
+  if (i < n) q = from[i];
+  float M = q.m;
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  q = at_max(q, M);
+#pragma unroll
+  for (int off = 8; off >= 1; off >>= 1) {
+    q.s += __shfl_xor_sync(0xffffffffu, q.s, off);
+    q.t += __shfl_xor_sync(0xffffffffu, q.t, off);
+  }
+  return q;
+}
+
 template <typename T>
 struct Vec;
 template <>
@@ -370,6 +387,9 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
 
   if (tid < k) sh.top[tid] = 0;
   if (tid == 0) sh.count = sh.n_hits = 0;
+  // the given token is asked for here, its logit behind the stream, both needed at the end
+  int tok = -1;
+  if (tid == 0 && rank == 0 && p.logprob) tok = p.tokens[row];
 
   Part mine = {-INFINITY, 0.f, 0.f};
   auto add = [&](Part q) {
@@ -428,7 +448,10 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
     add({xe == xe ? xe : -INFINITY, xe == -INFINITY ? 0.f : xe - xe + 1.f, 0.f});   // NaN and +inf sum up to NaN
   }
 
-  // ---- the CTA's partial result: threads, then warps, in order
+  float xt = NAN;
+  if (tok >= 0 && tok < p.vocab) xt = (float)pc.x[tok];
+
+  // ---- the CTA's partial result: threads, then warps
   {
     float M = mine.m;
 #pragma unroll
@@ -439,18 +462,9 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
     if (lane == 0) sh.part[warp] = w;
   }
   __syncthreads();
-  if (tid == 0) {
-    float m = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < LP_WARPS; ++w) m = fmaxf(m, sh.part[w].m);
-    Part all = {m, 0.f, 0.f};
-#pragma unroll
-    for (int w = 0; w < LP_WARPS; ++w) {
-      const Part q = at_max(sh.part[w], m);
-      all.s += q.s;
-      all.t += q.t;
-    }
-    sh.all[0] = all;
+  if (warp == 0) {
+    const Part all = join16(sh.part, LP_WARPS, lane);
+    if (lane == 0) sh.all[0] = all;
   }
   if (k > 0) {
     const int n_hits = sh.n_hits;
@@ -489,16 +503,8 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (rank != 0) return;
   }
-  Part all = sh.all[0];
+  const Part all = join16(sh.all, cs, lane);   // in every warp
   if (cs > 1) {
-    float m = all.m;
-    for (int r = 1; r < cs; ++r) m = fmaxf(m, sh.all[r].m);
-    all = at_max(all, m);
-    for (int r = 1; r < cs; ++r) {
-      const Part q = at_max(sh.all[r], m);
-      all.s += q.s;
-      all.t += q.t;
-    }
     if (k > 0) {
       if (tid < k) sh.lists[tid] = sh.top[tid];
       if (tid == 0) sh.count = 0;
@@ -517,9 +523,8 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
   auto lp = [&](float v) { return none ? -INFINITY : (v - all.m) - ls; };
   if (tid == 0) {
     if (p.logprob) {
-      const int tok = p.tokens[row];
       if (tok >= p.vocab) atomicOr(p.err, kErrLength);
-      p.logprob[row] = tok < 0 ? 0.f : tok >= p.vocab ? NAN : lp((float)pc.x[tok]);
+      p.logprob[row] = tok < 0 ? 0.f : tok >= p.vocab ? NAN : lp(xt);
     }
     if (p.entropy) p.entropy[row] = none ? 0.f : ls - all.t / all.s;
   }
