@@ -189,17 +189,23 @@ struct Piece {
   __device__ __forceinline__ int index(int v, int e) const { return head + v * Vec<T>::N + e; }
 };
 
-// top[0..k) from n candidates, by counting how many are larger; four threads to
-// a candidate.
-__device__ __forceinline__ void rank_into(LpShared& sh, int n, int k) {
+// top[0..k) from n candidates (16-byte aligned), by counting how many are
+// larger; four threads to a candidate.
+__device__ __forceinline__ void rank_into(LpShared& sh, const uint64_t* cand, int n, int k) {
   for (int i0 = 0; i0 < n; i0 += LP_THREADS / 4) {
     const int i = i0 + (threadIdx.x >> 2);
-    const uint64_t key = i < n ? sh.cand[i] : 0;
+    const uint64_t key = i < n ? cand[i] : ~0ull;
     int rank = 0;
-    for (int j = threadIdx.x & 3; j < n; j += 4) rank += sh.cand[j] > key ? 1 : 0;
-    rank += __shfl_xor_sync(0xffffffffu, rank, 1);
-    rank += __shfl_xor_sync(0xffffffffu, rank, 2);
-    if (i < n && (threadIdx.x & 3) == 0 && rank < k) sh.top[rank] = key;
+    if (i0 + (int)(threadIdx.x >> 5) * 8 < n) {   // the same for a warp
+#pragma unroll 2
+      for (int j = 2 * (threadIdx.x & 3); j < n; j += 8) {
+        const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(cand + j);
+        rank += (o.x > key ? 1 : 0) + (j + 1 < n && o.y > key ? 1 : 0);
+      }
+      rank += __shfl_xor_sync(0xffffffffu, rank, 1);
+      rank += __shfl_xor_sync(0xffffffffu, rank, 2);
+      if (i < n && (threadIdx.x & 3) == 0 && rank < k) sh.top[rank] = key;
+    }
   }
 }
 
@@ -352,7 +358,7 @@ __device__ __noinline__ bool step_by_step(LpShared& sh, const Piece<T>& pc, int 
     __syncthreads();
     const int found = sh.count;
     if (found > LP_CAND) return false;
-    rank_into(sh, found, k);
+    rank_into(sh, sh.cand, found, k);
     have = min(k, found);
   }
   return true;
@@ -480,7 +486,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
     }
     __syncthreads();
     const int found = sh.count, there = (pc.v1 - pc.v0) * V::N + pc.extra;
-    if (n_hits <= LP_HITS && found <= LP_CAND && found >= min(k, there)) rank_into(sh, found, k);
+    if (n_hits <= LP_HITS && found <= LP_CAND && found >= min(k, there)) rank_into(sh, sh.cand, found, k);
     else if (!step_by_step(sh, pc, k)) one_by_one(sh, pc, k);
   }
   __syncthreads();
@@ -509,12 +515,16 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
       if (tid < k) sh.lists[tid] = sh.top[tid];
       if (tid == 0) sh.count = 0;
       __syncthreads();
-      uint64_t least = 1;   // every list's last entry has k logits at or above it
-      for (int r = 0; r < cs; ++r) least = max(least, sh.lists[r * k + k - 1]);
-      for (int i = tid; i < cs * k; i += LP_THREADS)
-        if (sh.lists[i] >= least) sh.cand[atomicAdd(&sh.count, 1)] = sh.lists[i];
-      __syncthreads();
-      rank_into(sh, sh.count, k);
+      if (cs * k <= LP_THREADS / 4) {   // one round
+        rank_into(sh, sh.lists, cs * k, k);
+      } else {
+        uint64_t least = 1;   // every list's last entry has k logits at or above it
+        for (int r = 0; r < cs; ++r) least = max(least, sh.lists[r * k + k - 1]);
+        for (int i = tid; i < cs * k; i += LP_THREADS)
+          if (sh.lists[i] >= least) sh.cand[atomicAdd(&sh.count, 1)] = sh.lists[i];
+        __syncthreads();
+        rank_into(sh, sh.cand, sh.count, k);
+      }
       __syncthreads();
     }
   }
