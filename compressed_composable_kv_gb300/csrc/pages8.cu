@@ -20,8 +20,8 @@
 // (1.57 GB) 224 us, 7.0 TB/s (a plain copy: 6.8).  Append is bound by the
 // rotation and by latency: the two halves of a pair must round as the exact
 // values do, which costs a test for each and cos/sin in two parts, 1 KB of table
-// for each token of each kv head (from L2).  1 x 4000 tokens 12.1 us (28 MB), 8
-// ragged sequences of up to 128 7.7 us, 16 x 1 4.8 us, which is a launch and four
+// for each token of each kv head (from L2).  1 x 4000 tokens 11.6 us (28 MB), 8
+// ragged sequences of up to 128 7.6 us, 16 x 1 4.8 us, which is a launch and four
 // dependent reads.
 #include "pages8.h"
 
@@ -189,11 +189,15 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
 #pragma unroll
       for (int i = i0; i < i0 + PER; ++i) {
         if (!in(wrow + i * RPI + lane / LPR)) continue;
-        const CosSin2 t0 = t[(i - i0) * RPI * (D / 2)], t1 = t[(i - i0) * RPI * (D / 2) + 1];
+        // every other four lanes read their two entries in the other order: eight
+        // neighbours then read all banks once
+        const bool odd = lane & 4;
+        const CosSin2 ta = t[(i - i0) * RPI * (D / 2) + odd], tb = t[(i - i0) * RPI * (D / 2) + !odd];
+        const float c0 = odd ? tb.ch : ta.ch, s0 = odd ? tb.sh : ta.sh, c1 = odd ? ta.ch : tb.ch, s1 = odd ? ta.sh : tb.sh;
         const float x0 = __uint_as_float(w[2 * i] << 16), x1 = __uint_as_float(w[2 * i] & 0xFFFF0000u);
         const float y0 = __uint_as_float(w[2 * i + 1] << 16), y1 = __uint_as_float(w[2 * i + 1] & 0xFFFF0000u);
         float a0, b0, a1, b1;
-        const bool clear0 = turn_pair(x0, y0, t0.ch, t0.sh, a0, b0), clear1 = turn_pair(x1, y1, t1.ch, t1.sh, a1, b1);
+        const bool clear0 = turn_pair(x0, y0, c0, s0, a0, b0), clear1 = turn_pair(x1, y1, c1, s1, a1, b1);
         if (clear0 && clear1) {
           w[2 * i] = pack2(a0, a1);
           w[2 * i + 1] = pack2(b0, b1);
