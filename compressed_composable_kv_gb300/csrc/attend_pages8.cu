@@ -29,18 +29,19 @@
 // holds up the loads of one while it ends the other; else (more units than
 // CTAs, or lengths so mixed that the longest part would be 1.5 times an even
 // share) the tiles are laid end to end and cut into one equal range per CTA.
-// 8 x 8000 keys of 5 heads to a kv head: 33 us by parts, 39 us by ranges; 16
-// sequences of 2 to 16 thousand keys 35 and 39; 4 x 32768 52 and 58.
+// 8 x 8000 keys of 5 heads to a kv head: 34 us by parts, 39 us by ranges; 16
+// sequences of 1 to 8 thousand keys 35 and 39; 4 x 32768 52 and 58.  (A cluster
+// to a unit, merged in shared memory: 40, 34 and 68: its CTAs stream slower.)
 // A unit that one CTA holds whole is written at once; else its CTAs write
 // partial (m, l, O), and the one whose tiles complete the unit's counter merges
 // them, in the order of the keys whoever it is.
 //
 // Measured (one call among others in a graph; 6.8 TB/s is a plain copy's rate):
-//   4 x 32768 keys, 8 kv heads of 4 (269 MB)   51 us   5.2 TB/s
-//   8 x 8000 keys, 8 kv heads of 5 (131 MB)    33 us   4.0 TB/s
-//   16 ragged, 4 heads (142 MB)                36 us   4.0 TB/s
-//   1 x 8000 keys, 4 heads (16 MB)             12.7 us
-//   16 sequences of up to 100 keys              9.3 us
+//   4 x 32768 keys, 8 kv heads of 4 (269 MB)   50 us   5.4 TB/s
+//   8 x 8000 keys, 8 kv heads of 5 (131 MB)    32 us   4.1 TB/s
+//   16 ragged, 8 kv heads of 4 (142 MB)        34 us   4.1 TB/s
+//   1 x 8000 keys, 8 kv heads of 4 (16 MB)     12.5 us
+//   16 sequences of up to 300 keys, 2 heads     9.1 us
 // While tiles stream they come at 6.9 TB/s.  What is left is the latency of a
 // call: 4 us to the first tile (launch, lengths, page ids, the load itself),
 // 1.4 us from the last tile to the CTA's partial, 2.5 to 3 us for arrival and

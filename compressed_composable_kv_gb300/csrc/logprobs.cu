@@ -21,11 +21,12 @@
 // (value, lower index first), so that equal ones have one order.
 //
 // Measured (one call among others in a graph; 6.8 TB/s is a plain copy's rate):
-// 256 x 50257 fp32 logits with a fifth masked, top 20: 18 us (2.8 TB/s), with no
-// alternatives 13 us (4.0 TB/s), all but 50 masked 24 us, rising along the row
-// 89 us; 256 x 128256 bf16, top 5: 20 us (3.3 TB/s); 4 x 128256: 5.8 us.  About
-// 5 us of a call are launch, first loads and the join of a row's CTAs, 4 us more
-// the lists, while no logits stream: at these sizes every CTA runs at once.
+// 256 x 50257 fp32 logits with a fifth masked, top 20: 17.6 us (2.9 TB/s), with
+// no alternatives 13 us (4.0 TB/s), all but 50 masked 23 us, rising along the row
+// 80 us; 256 x 128256 bf16, top 5: 19.7 us (3.3 TB/s); 4 x 128256: 5.3 us.  About
+// 5 us of a call are launch, first loads and the join of a row's CTAs, 5 us more
+// the bound and the lists: at these sizes every CTA runs at once, so no logits
+// stream meanwhile.
 #include "pages8.h"
 
 namespace c2kv {

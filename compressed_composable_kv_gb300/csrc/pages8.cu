@@ -13,7 +13,7 @@
 // A CTA owns 64 consecutive rows of one (sequence, kv head), of K or of V (128
 // where a page is that long): a whole number of pages, so a page's largest
 // magnitude never leaves the CTA.  A warp owns 16 rows and keeps them, as bf16,
-// // in registers between the two steps (largest magnitude, codes), so the data
+// in registers between the two steps (largest magnitude, codes), so the data
 // are read once, with all loads of a warp in flight.
 //
 // Fill is bound by the bytes moved: 32 layers of 8000 rows, 8 kv heads of 128
