@@ -523,7 +523,7 @@ def _check_logprobs(x, k, seed=0, tokens=None):
         assert np.array_equal(np.isnan(got), np.isnan(ref)) and np.array_equal(np.isneginf(got), np.isneginf(ref))
         fine = np.isfinite(ref)
         bar = (tol if ref.ndim == 1 else tol[:, None]) + 2.0 ** -22 * np.where(fine, np.abs(ref), 0.0)
-        assert np.all((np.abs(np.where(fine, got - ref, 0.0)) <= bar))
+        assert np.all(np.abs(np.where(fine, got, 0.0) - np.where(fine, ref, 0.0)) <= bar)
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -614,3 +614,47 @@ def test_wrong_device_tensors_are_refused():
     x = torch.zeros((2, 10), device="cuda")
     with pytest.raises(ValueError, match="current CUDA device"):
         P.c2kv_token_logprobs(x, torch.zeros(2, dtype=torch.int32), 0, torch.zeros(2, device="cuda"), None)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages 4 GB and more into their pool, in the second layer, and rows of
+    logits beyond 2^31 elements: as in a small pool, as on their own."""
+    g = S.Geometry(2, 16, 8, 128, 1e4)
+    t_len, page, many = 300, 128, 20000      # 128 KB a page, 2.6 GB a layer
+    ids = torch.tensor([many - 1, many - 3, many - 2], dtype=torch.int32, device="cuda")
+    rng = np.random.default_rng(5)
+    kn, vn = (_dev(S.normal_bf16(rng, (1, t_len, 8, 128))) for _ in range(2))
+    k1, v1 = (_dev(S.normal_bf16(rng, (1, 8, 128))) for _ in range(2))
+    q = _dev(S.normal_bf16(rng, (1, 16, 128)))
+    tab = _rope(g, np.arange(t_len + 1))
+    zero = torch.zeros(1, dtype=torch.int32, device="cuda")
+    caches = [torch.randn(2, 8, 320, 128, device="cuda").to(torch.bfloat16) for _ in range(2)]
+    got = []
+    for n, table in ((many, ids[None]), (3, torch.arange(3, dtype=torch.int32, device="cuda")[None])):
+        k8, v8 = (torch.empty((2, n, 8, page, 128), dtype=E4, device="cuda") for _ in range(2))
+        ks, vs = (torch.empty((2, n, 8), device="cuda") for _ in range(2))
+        table = table.contiguous()
+        at = table[0].long()
+        for t in (k8, v8):
+            t[1].view(torch.uint8)[at] = 0
+        pool = (k8, v8, ks, vs, table)
+        P.c2kv_pages8_append(g, 1, *pool, zero, kn, vn, tab, zero)
+        ws = torch.zeros(P.c2kv_attend_pages8_workspace_size(g, 1, t_len + 1), dtype=torch.uint8, device="cuda")
+        out = torch.empty((1, 16, 128), dtype=torch.bfloat16, device="cuda")
+        P.c2kv_attend_pages8(g, 1, *pool, zero + t_len, t_len + 1, q, k1, v1, tab, zero + t_len, out, ws)
+        res = [out.float()] + [t[1].view(torch.uint8)[at] for t in (k8, v8)] + [t[1][at] for t in (ks, vs)]
+        P.c2kv_pages8_fill(g, 0, 2, caches[:1], caches[1:], 320, [257], *pool)
+        got.append(res + [t[1].view(torch.uint8)[at] for t in (k8, v8)] + [t[1][at] for t in (ks, vs)])
+        _ok()
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert got[0][0].isfinite().all() and got[0][0].abs().max() > 0
+    del got, pool, k8, v8
+    x = torch.empty((18000, 128256), dtype=torch.bfloat16, device="cuda")
+    x[:] = torch.randn(128256, device="cuda").to(torch.bfloat16)
+    x[-1] = x[-1].flip(0)
+    tok = torch.full((18000,), 77, dtype=torch.int32, device="cuda")
+    all_rows, last = _logprobs(x, tok, 4), _logprobs(x[-1:].clone(), tok[:1], 4)
+    for a, b in zip(all_rows, last):
+        # sums of the row in another order: a few fp32 roundings of values below 32
+        assert (a[-1:].double() - b.double()).abs().max() <= 2.0 ** -17
+        assert torch.equal(a[0], a[-2])
