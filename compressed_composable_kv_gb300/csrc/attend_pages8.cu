@@ -54,6 +54,8 @@
 // NaN among them, and 0 * NaN would reach the sum).
 #include <float.h>
 
+#include <algorithm>
+
 #include "pages8.h"
 #include "tcgen05.h"
 
@@ -1092,8 +1094,10 @@ cudaError_t launch_ap(const AttendPages8Params& p, int sms, cudaStream_t st) {
     }
     if (s.state[dev] != 1) return (cudaError_t)(-s.state[dev]);
   }
+  // Two CTAs to an SM, but no more than the longest sequences could use.
+  const int64_t parts = ((p.max_keys - 1) / C::TILE_KEYS + kMinTiles) / kMinTiles;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * sms);
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(2 * sms, parts * p.batch * p.pool.n_kv));
   cfg.blockDim = dim3(AP_THREADS);
   cfg.dynamicSmemBytes = C::SMEM;
   cfg.stream = st;
