@@ -35,6 +35,8 @@ class RequestBatch:
     def __init__(self, store: int, geom, requests: Sequence[RequestSpec], k: int, q_len: int,
                  decode_steps: int, device: str = "cuda", cap_multiple: int = 32, realign: bool = True,
                  page8: Optional[int] = None):
+        if page8 not in (None, 16, 32, 64, 128):
+            raise ValueError(f"page8 must be None, 16, 32, 64 or 128, not {page8}")
         self.store, self.geom, self.k = store, geom, k
         # realign=False: the "no position re-alignment" ablation (documents
         # keep their extraction positions)
@@ -118,6 +120,8 @@ class RequestBatch:
 
     def fill_pages8(self, layer_begin: int = 0, layer_end: Optional[int] = None, stream=None) -> None:
         """The composed and prefilled rows of layers [layer_begin, layer_end) to the 8-bit pages."""
+        if self.page8 is None:
+            raise ValueError("this batch was made without page8")
         B.c2kv_pages8_fill(self.geom, layer_begin, self.geom.n_layers if layer_end is None else layer_end,
                            self.k_caches, self.v_caches, self.cap, [n + self.q_len for n in self.n_slots],
                            self.k8, self.v8, self.k_scale, self.v_scale, self.page_table, stream)

@@ -165,3 +165,9 @@ def test_binding_checks_shapes_and_types(P):
         P.c2kv_token_logprobs(x.t(), None, 0, None, None)
     with pytest.raises(ValueError, match="bfloat16 or float32"):
         P.c2kv_token_logprobs(x.half(), None, 0, None, None)
+
+
+def test_request_batch_refuses_other_page_sizes(P):
+    for page8 in (0, 8, 48, 256):
+        with pytest.raises(ValueError, match="page8"):
+            P.RequestBatch(None, S.TINY, [], 4, 0, 1, page8=page8)
