@@ -363,6 +363,15 @@ def test_attend_long(n_kv, batch):
     _attend_case(_geom(64, 1, n_kv), 16, [4000 - 1000 * b for b in range(batch)])
 
 
+@pytest.mark.parametrize("d,group", [(64, 1), (64, 8), (128, 4), (128, 5), (128, 8)])
+@pytest.mark.parametrize("page", [16, 128])
+def test_attend_more_units_than_ctas(d, group, page):
+    """Every CTA's range of tiles spans several units and ends inside others."""
+    rng = np.random.default_rng(d + group + page)
+    lens = [int(x) for x in np.exp(rng.uniform(0.0, np.log(1800.0), 47))] + [0, -1, 1500, 256, 255]
+    _attend_case(_geom(d, group, 8), page, lens, seed=group)
+
+
 def test_attend_output_at_any_element():
     """out starts at an odd element; one sequence has rows, one has none."""
     g = S.Geometry(1, 4, 2, 128, 1e4)
