@@ -168,7 +168,8 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
   if (!aligned(q, 16)) return api_fail(C2KV_EINVAL, "q must be 16-byte aligned");
   if (max_keys < 1 || max_keys > max_pages * pages->page)
     return api_fail(C2KV_EINVAL, "max_keys must be in [1, max_pages * page]");
-  if ((int64_t)batch * geom->n_kv_heads * ((max_keys - 1) / (128 * 128 / geom->head_dim) + 1) > INT32_MAX)
+  // a tile for every 128 rows of 128 bytes, and a few for the end of each head's
+  if ((int64_t)batch * geom->n_kv_heads * ((max_keys - 1) / (128 * 128 / geom->head_dim) + 8) > INT32_MAX)
     return api_fail(C2KV_EINVAL, "batch * n_kv_heads * max_keys is above 2^31 tiles of 128 rows of 128 bytes");
   const int sms = std::min(api_sm_count_for_sizing(), kMaxPageCtas / 2);
   const AttendWs w = attend_workspace(geom, sms);

@@ -74,13 +74,14 @@ constexpr int AP_MAX_PPT = 16;                  // pages of a tile
 // Tiles of a CTA below which fewer CTAs work: more partials cost the merge more
 // than they save the stream (1 x 8000 keys at 2, 3, 4: 13.4, 12.9, 12.4 us).
 constexpr int kMinTiles = 4;
+constexpr int kUnitTiles = 3;    // what the end of a unit costs a CTA, in tiles (see PageCut)
 constexpr int kMergeRows = 64;   // partials of one round of a merge
 
 // The tiles of a launch, from the device-side lengths (fewer than 2^31, which
 // the host checks for max_keys).
 struct PageMap {
   int32_t start[kMaxPagedSeqs + 1];   // first tile of each sequence; the last one is the total
-  int32_t part[kMaxPagedSeqs + 1];    // split by unit: first CTA of each sequence
+  int32_t part[kMaxPagedSeqs + 1];    // split by unit: first CTA of each sequence; evenly: its first place
   int32_t keys[kMaxPagedSeqs];        // rows attended over; -1: left out
   int32_t rope[kMaxPagedSeqs];        // the sequence's row of the RoPE table
   int32_t most;                       // split by unit: tiles of a part at most; 0: split evenly
@@ -234,12 +235,13 @@ struct PageSeg {
   int b, h, t0, j0, n;
 };
 
-// An even split: CTA c owns tiles [first(c), first(c + 1)).
+// An even split: a unit's tiles take a place each and its end kUnitTiles more;
+// CTA c owns the tiles in places [first(c), first(c + 1)).
 struct PageCut {
-  int base, rem, ctas;   // the first rem CTAs own base + 1 tiles, the others base
+  int base, rem, ctas;   // the first rem CTAs own base + 1 places, the others base
 
   __device__ __forceinline__ int first(int c) const { return c * base + min(c, rem); }
-  __device__ __forceinline__ int of(int x) const {   // the CTA that owns tile x
+  __device__ __forceinline__ int of(int x) const {   // the CTA that owns place x
     const int big = rem * (base + 1);
     return x < big ? (int)((uint32_t)x / (uint32_t)(base + 1)) : rem + (int)((uint32_t)(x - big) / (uint32_t)base);
   }
@@ -344,6 +346,15 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         if (lane == 0) M.part[kMaxPagedSeqs] = sum;
       }
     }
+    if (most == 0) {
+      int sum = 0;
+      for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int tb = b0 + lane < p.batch ? ((M.keys[b0 + lane] - 1) >> C::TILE_LG) + 1 : 0;
+        const int first = scan(tb > 0 ? (tb + kUnitTiles) * p.pool.n_kv : 0, sum);
+        M.part[b0 + lane] = first;
+      }
+      if (lane == 0) M.part[kMaxPagedSeqs] = sum;
+    }
     bad = __any_sync(0xffffffffu, bad);
     none = __any_sync(0xffffffffu, none);
     if (lane == 0) {
@@ -397,6 +408,12 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
   auto unit_tiles = [&](int b) { return ((M.keys[b] - 1) >> C::TILE_LG) + 1; };   // 0 for -1 and 0 keys
   const int total = M.start[kMaxPagedSeqs], most = M.most;
   PageCut cut;
+  auto tile_from = [&](int place) {   // the first tile at this place or behind it
+    if (place >= M.part[kMaxPagedSeqs]) return total;
+    const int b = seq_of(M.part, p.batch, place), tb = unit_tiles(b);
+    const uint32_t r = (uint32_t)(place - M.part[b]), h = r / (uint32_t)(tb + kUnitTiles);
+    return M.start[b] + (int)h * tb + min((int)(r - h * (uint32_t)(tb + kUnitTiles)), tb);
+  };
   int x0 = 0, x1 = 0;
   if (most > 0) {
     if (cta < M.part[kMaxPagedSeqs]) {
@@ -406,11 +423,12 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       x1 = M.start[b] + h * tb + (int)((uint32_t)(i + 1) * (uint32_t)tb / (uint32_t)parts);
     }
   } else {
+    const int places = M.part[kMaxPagedSeqs];
     cut.ctas = min(ctas, max(1, total / kMinTiles));
-    cut.base = total / cut.ctas;
-    cut.rem = total - cut.base * cut.ctas;
-    x0 = min(total, cut.first(cta));
-    x1 = min(total, cut.first(cta + 1));
+    cut.base = places / cut.ctas;
+    cut.rem = places - cut.base * cut.ctas;
+    x0 = tile_from(cut.first(cta));
+    x1 = tile_from(cut.first(cta + 1));
   }
   const int ntiles = x1 - x0;
   if (*none_flag) {
@@ -982,9 +1000,10 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
             cf = M.part[sg.b] + sg.h * nctr;
             slot0 = 2 * cf;
           } else {
-            cf = cut.of(uf);
-            nctr = cut.of(uf + tb - 1) - cf + 1;
-            slot0 = 2 * cf + (cut.first(cf) < uf ? 1 : 0);
+            const int place = M.part[sg.b] + sg.h * (tb + kUnitTiles);
+            cf = cut.of(place);
+            nctr = cut.of(place + tb - 1) - cf + 1;
+            slot0 = 2 * cf + (tile_from(cut.first(cf)) < uf ? 1 : 0);
           }
           auto slot = [&](int k) { return k == 0 ? slot0 : 2 * (cf + k); };
           float* wts = reinterpret_cast<float*>(sP);   // [kMergeRows][G]; every PV that read P has completed
