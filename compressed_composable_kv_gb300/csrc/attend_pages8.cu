@@ -675,23 +675,42 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     }
   } else if (warp == 7) {
     // ---------------- V's loads, and the last tile of a unit, tile j of the CTA.
-    // Lanes 0.. hold the new key, lanes 16.. the new value, 16 elements each
-    // as in prep_q.
-    const int kv = lane >> 4, c = lane & 15;
-    float lo[8], hi[8];   // this lane's part of the new row of the unit whose turn is next
-    uint32_t m = 0;       // bits of its largest magnitude, over the 16 lanes of K or V
-    int id = -1;          // and its page
+    // A lane holds elements 2 lane, 2 lane + 1 of each half of the new key and of
+    // the new value (at head_dim 64 the first 16 lanes do).
+    const bool on = lane < D / 4;
+    float fresh[2][4];    // [K, V][lower half, upper half] of the unit whose turn is next, as held
+    uint32_t m[2];        // bits of their largest magnitudes, over the row
+    int id = -1;          // and the row's page
     auto ask_row = [&](const PageSeg& sg) {
       id = p.page_table[(size_t)sg.b * p.max_pages + ((M.keys[sg.b] - 1) >> lg)];
-      m = 0;
-      if (p.has_new && c < CH) {
-        const uint4* src = reinterpret_cast<const uint4*>(p.fresh[kv] + ((size_t)sg.b * p.pool.n_kv + sg.h) * D);
-        const uint4 x = src[c], y = src[c + CH];
-        new_row8(x, y, kv == 0 ? p.tab + (size_t)M.rope[sg.b] * (D / 2) + c * 8 : nullptr, lo, hi);
-        m = max(max_finite8(lo), max_finite8(hi));
-      }
+      m[0] = m[1] = 0;
+      if (!p.has_new) return;
+      if (on) {
+        const size_t at = ((size_t)sg.b * p.pool.n_kv + sg.h) * D;
+        const uint32_t* ks = reinterpret_cast<const uint32_t*>(p.fresh[0] + at);
+        const uint32_t* vs = reinterpret_cast<const uint32_t*>(p.fresh[1] + at);
+        const uint32_t kx = ks[lane], ky = ks[D / 4 + lane], vx = vs[lane], vy = vs[D / 4 + lane];
+        const CosSin2* t = p.tab + (size_t)M.rope[sg.b] * (D / 2) + 2 * lane;
+        const CosSin2 t0 = t[0], t1 = t[1];
+        const float x0 = __uint_as_float(kx << 16), x1 = __uint_as_float(kx & 0xFFFF0000u);
+        const float y0 = __uint_as_float(ky << 16), y1 = __uint_as_float(ky & 0xFFFF0000u);
+        // a pair with a member that is not finite comes out as NaN in both
+        const uint32_t bits[2][4] = {{rot_key_bits(x0, t0.ch, t0.cl, -y0, t0.sh, t0.sl) << 16,
+                                      rot_key_bits(x1, t1.ch, t1.cl, -y1, t1.sh, t1.sl) << 16,
+                                      rot_key_bits(y0, t0.ch, t0.cl, x0, t0.sh, t0.sl) << 16,
+                                      rot_key_bits(y1, t1.ch, t1.cl, x1, t1.sh, t1.sl) << 16},
+                                     {vx << 16, vx & 0xFFFF0000u, vy << 16, vy & 0xFFFF0000u}};
 #pragma unroll
-      for (int off = 8; off >= 1; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+        for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t a = bits[kv][e] & 0x7FFFFFFFu;
+            fresh[kv][e] = __uint_as_float(a < 0x7F800000u ? bits[kv][e] : 0x7FFFFFFFu);
+            if (a < 0x7F800000u) m[kv] = max(m[kv], a);
+          }
+      }
+      m[0] = __reduce_max_sync(0xffffffffu, m[0]);
+      m[1] = __reduce_max_sync(0xffffffffu, m[1]);
     };
     auto fixup = [&](int j, const PageSeg& sg) -> bool {
       const int s = j % C::STAGES;
@@ -699,42 +718,44 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       const int at = n - (sg.t0 + (j - sg.j0)) * C::TILE_KEYS;   // its key in the tile
       const int pi = at >> lg, pl = n & (page - 1);              // its page of the tile, its place there
       const bool in = id >= 0 && id < p.pool.n_pages;
-      const bool mine = p.has_new && in && c < CH;
       // this warp has asked for V's part of the tile, so the stage's phases are
       // this tile's
       if (!__all_sync(0xffffffffu, ap_wait(&k_full[s], (j / C::STAGES) & 1, abort_flag, p.err))) return false;
       if (!__all_sync(0xffffffffu, ap_wait(&v_full[s], (j / C::STAGES) & 1, abort_flag, p.err))) return false;
-      // byte `byte` (a multiple of 8) of key `key` of the tile
+      // byte `byte` of key `key` of the tile
       auto place = [&](uint8_t* tile, int key, int byte) {
         const int row = key / KPR, b = key % KPR * D + byte;
-        return tile + row * 128 + (((b >> 4) ^ (row & 7)) << 4) + (b & 8);
+        return tile + row * 128 + (((b >> 4) ^ (row & 7)) << 4) + (b & 15);
       };
       const size_t block = in ? (size_t)id * p.pool.n_kv + sg.h : 0;
       int grow[2] = {0, 0};
       if (p.has_new && in) {   // uniform over the warp
-        float* scs = sc + (j % C::SCALES * 2 + kv) * AP_MAX_PPT + pi;
-        int e = scale_exponent(m), e_old = e;
-        if (pl > 0) {
-          e_old = exponent_of_scale(*scs);
-          e = max(e, e_old);
-        }
-        __syncwarp();
-        uint8_t* tile = kv == 0 ? stage_k(s) : stage_v(s);
-        if (mine) {
-          const float inv = pow2_float(-e);
-          const uint2 a = codes8(lo, inv), b = codes8(hi, inv);
-          *reinterpret_cast<uint2*>(place(tile, at, 8 * c)) = a;
-          *reinterpret_cast<uint2*>(place(tile, at, D / 2 + 8 * c)) = b;
-          uint8_t* dst = p.pool.codes[kv] + (block * page + pl) * D;
-          *reinterpret_cast<uint2*>(dst + 8 * c) = a;
-          *reinterpret_cast<uint2*>(dst + D / 2 + 8 * c) = b;
-          if (c == 0) {
-            *scs = pow2_float(e);
-            p.pool.scales[kv][block] = pow2_float(e);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+          float* scs = sc + (j % C::SCALES * 2 + kv) * AP_MAX_PPT + pi;
+          int e = scale_exponent(m[kv]), e_old = e;
+          if (pl > 0) {
+            e_old = exponent_of_scale(*scs);
+            e = max(e, e_old);
+          }
+          grow[kv] = e_old - e;
+          __syncwarp();
+          if (on) {
+            const float inv = pow2_float(-e);
+            const uint16_t a = (uint16_t)e4m3x2(fresh[kv][0] * inv, fresh[kv][1] * inv);
+            const uint16_t b = (uint16_t)e4m3x2(fresh[kv][2] * inv, fresh[kv][3] * inv);
+            uint8_t* tile = kv == 0 ? stage_k(s) : stage_v(s);
+            *reinterpret_cast<uint16_t*>(place(tile, at, 2 * lane)) = a;
+            *reinterpret_cast<uint16_t*>(place(tile, at, D / 2 + 2 * lane)) = b;
+            uint8_t* dst = p.pool.codes[kv] + (block * page + pl) * D;
+            *reinterpret_cast<uint16_t*>(dst + 2 * lane) = a;
+            *reinterpret_cast<uint16_t*>(dst + D / 2 + 2 * lane) = b;
+            if (lane == 0) {
+              *scs = pow2_float(e);
+              p.pool.scales[kv][block] = pow2_float(e);
+            }
           }
         }
-        grow[0] = __shfl_sync(0xffffffffu, e_old - e, 0);
-        grow[1] = __shfl_sync(0xffffffffu, e_old - e, 16);
       }
       // a larger scale: the page's earlier codes follow (rare)
       auto rescale = [&](int k) {

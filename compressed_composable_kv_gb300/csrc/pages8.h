@@ -61,55 +61,6 @@ __device__ __forceinline__ uint32_t rot_key_bits(float a, float bh, float bl, fl
   return rot_key_slow(a, bh, bl, c, dh, dl);
 }
 
-// 8 bf16 bit patterns -> fp32, NaN where not finite.
-__device__ __forceinline__ void finite_or_nan8(const uint4& u, float (&f)[8]) {
-  unpack8(u, f);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if ((__float_as_uint(f[e]) & 0x7F800000u) == 0x7F800000u) f[e] = __uint_as_float(0x7FFFFFFFu);
-}
-
-// The values to hold of one 8-element chunk of each half of a bf16 row: as
-// they are, or (t: the 8 cos/sin of these pairs) rotated and rounded to bf16,
-// as a bf16 cache holds a key.  NaN where not finite; a pair with a member
-// that is not finite is NaN in both.
-__device__ __forceinline__ void new_row8(const uint4& x, const uint4& y, const CosSin2* t, float (&lo)[8], float (&hi)[8]) {
-  finite_or_nan8(x, lo);
-  finite_or_nan8(y, hi);
-  if (t == nullptr) return;
-  bool bad[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) bad[e] = !(lo[e] == lo[e] && hi[e] == hi[e]);
-  uint32_t xo[8], yo[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const CosSin2 te = t[e];
-    xo[e] = rot_key_bits(lo[e], te.ch, te.cl, -hi[e], te.sh, te.sl);   // x cos - y sin
-    yo[e] = rot_key_bits(hi[e], te.ch, te.cl, lo[e], te.sh, te.sl);    // y cos + x sin
-  }
-  finite_or_nan8(pack_bits8(xo), lo);
-  finite_or_nan8(pack_bits8(yo), hi);
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (bad[e]) lo[e] = hi[e] = __uint_as_float(0x7FFFFFFFu);
-}
-
-// Bits of the largest finite magnitude.
-__device__ __forceinline__ uint32_t max_finite8(const float (&f)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t b = __float_as_uint(f[e]) & 0x7FFFFFFFu;
-    if (b < 0x7F800000u) m = max(m, b);
-  }
-  return m;
-}
-
-__device__ __forceinline__ uint2 codes8(const float (&f)[8], float inv) {
-  return make_uint2(e4m3x2(f[0] * inv, f[1] * inv) | (e4m3x2(f[2] * inv, f[3] * inv) << 16),
-                    e4m3x2(f[4] * inv, f[5] * inv) | (e4m3x2(f[6] * inv, f[7] * inv) << 16));
-}
-
 // Four codes times a power of two, rounded again.
 __device__ __forceinline__ uint32_t rescale4(uint32_t c, float by) {
   const float2 a = e4m3x2_to_float2(c & 0xFFFFu), b = e4m3x2_to_float2(c >> 16);
