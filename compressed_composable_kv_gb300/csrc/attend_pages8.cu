@@ -37,11 +37,12 @@
 // them, in the order of the keys whoever it is.
 //
 // Measured (one call among others in a graph; 6.8 TB/s is a plain copy's rate):
-//   4 x 32768 keys, 8 kv heads of 4 (269 MB)   50 us   5.4 TB/s
+//   4 x 32768 keys, 8 kv heads of 4 (269 MB)   49 us   5.5 TB/s
 //   8 x 8000 keys, 8 kv heads of 5 (131 MB)    32 us   4.1 TB/s
-//   16 ragged, 8 kv heads of 4 (142 MB)        34 us   4.1 TB/s
+//   16 ragged, 8 kv heads of 4 (142 MB)        33 us   4.2 TB/s
+//   64 of up to 1560 keys, as these (105 MB)   31 us   3.4 TB/s
 //   1 x 8000 keys, 8 kv heads of 4 (16 MB)     12.0 us
-//   16 sequences of up to 300 keys, 2 heads     8.7 us
+//   16 sequences of up to 300 keys, 2 heads     7.9 us
 // While tiles stream they come at 6.9 TB/s.  What is left is the latency of a
 // call: 2.5 to 3.5 us for a launch that finds nothing to do, about 2 us to the
 // first tile (page ids, the load itself), 1.5 us from the last tile to the
@@ -74,7 +75,9 @@ constexpr int AP_MAX_PPT = 16;                  // pages of a tile
 // Tiles of a CTA below which fewer CTAs work: more partials cost the merge more
 // than they save the stream (1 x 8000 keys at 2, 3, 4: 13.4, 12.9, 12.4 us).
 constexpr int kMinTiles = 4;
-constexpr int kUnitTiles = 3;    // what the end of a unit costs a CTA, in tiles (see PageCut)
+// What the end of a unit costs a CTA, in tiles (see PageCut): 64 sequences of up to
+// 1560 keys take 39.9, 32.5, 31.5, 31.2, 31.6 us at 0 to 4.
+constexpr int kUnitTiles = 3;
 constexpr int kMergeRows = 64;   // partials of one round of a merge
 
 // The tiles of a launch, from the device-side lengths (fewer than 2^31, which
