@@ -291,13 +291,18 @@ __device__ __forceinline__ void note(LpShared& sh, const uint4& d, int v) {
   }
 }
 
+// Whether x reaches a bound that is its step's k-th largest group maximum; a NaN
+// bound (k groups hold one) is reached by NaN alone, which rank above the rest.
+__device__ __forceinline__ bool reaches_bound(float x, float bound) { return bound == bound ? !(x < bound) : x != x; }
+
 // Notes a step's vectors that reach the step's bound.  Where many equal it (a
-// mask's value, say) the first k of these in order will do.
+// mask's value, say, or NaN) the first k of these in order will do: each holds
+// one logit at least that no later one precedes.
 template <typename T>
 __device__ __forceinline__ void note_step(LpShared& sh, const Piece<T>& pc, const uint4 (&d)[LP_VECS],
                                           const float (&vm)[LP_VECS], int vb, float bound, int k) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto reaches = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && !(vm[c] < bound); };
+  auto reaches = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && reaches_bound(vm[c], bound); };
   auto above = [&](int c) { return reaches(c) && bound == bound && !(vm[c] <= bound); };
 #pragma unroll
   for (int c = 0; c < LP_VECS; ++c)
@@ -353,7 +358,7 @@ __device__ __noinline__ bool step_by_step(LpShared& sh, const Piece<T>& pc, int 
     };
     for (int i = tid; i < sh.n_hits * N; i += LP_THREADS) {
       const float v = (float)reinterpret_cast<const T*>(sh.hit)[i];
-      if (sh.hit_at[i / N] >= vb && !(v < bound)) list(v, pc.index(sh.hit_at[i / N], i % N));
+      if (sh.hit_at[i / N] >= vb && reaches_bound(v, bound)) list(v, pc.index(sh.hit_at[i / N], i % N));
     }
     if (vb == pc.v0 && tid < pc.extra) list((float)pc.x[pc.extra_at(tid)], pc.extra_at(tid));
     __syncthreads();
@@ -476,7 +481,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
   if (k > 0) {
     const int n_hits = sh.n_hits;
     auto list = [&](float v, int i) {
-      if (v < bound) return;
+      if (!reaches_bound(v, bound)) return;
       const int at = atomicAdd(&sh.count, 1);
       if (at < LP_CAND) sh.cand[at] = list_key(v, i);
     };
