@@ -820,9 +820,19 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     grid_release();
     const uint32_t lane_base = tmem + ((uint32_t)(warp * 32) << 16);
     const uint32_t o_col = C::TMEM_O + (tid / D) * C::HCOL;   // the columns of this lane's half
-    // A wait that runs out is noted and the step goes on with what is there;
-    // the next softmax_sync ends the work of all four warps.
-    bool failed = false;
+    // A wait that runs out is noted by the thread that waited (`failed`; its
+    // neighbours may have been in time), which goes on with what is there. The
+    // next softmax_sync tells all four warps (`gave_up`, the same in each thread),
+    // and that alone decides who leaves: a barrier or a tensor memory load that
+    // some had left before would never end.
+    bool failed = false, gave_up = false;
+    auto expire = [&]() {   // test hook: a wait that runs out
+      failed |= !mbar_wait(never, 0, kInjectWaitCycles);
+      if (lane == 0) {
+        *abort_flag = 1;
+        atomicOr(p.err, kErrTimeout);
+      }
+    };
     int k_red = 0;      // uses of red, whose two halves take turns
     int arrived = -1;   // last segment whose tiles were added to its unit's counter
     // out[b][h * G + g] from the lanes' o[g] over l[g]
@@ -834,10 +844,10 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       } else {
 #pragma unroll
         for (int g = 0; g < G; ++g) xo[g * 128 + tid] = l[g] == 0.f ? 0.f : o[g] / l[g];
-        failed = softmax_sync(failed);
+        gave_up = softmax_sync(failed);
         for (int i = tid; i < G * D; i += AP_SM_THREADS)
           out[i] = __float2bfloat16_rn(xo[i / D * 128 + i % D] + xo[i / D * 128 + D + i % D]);
-        failed = softmax_sync(failed);
+        gave_up = softmax_sync(failed);
       }
     };
     uint32_t p_at[8];   // this thread's byte of row r of P^T, less 128 r, by r & 7
@@ -879,13 +889,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         const int sb = j & 1;
         const float* scs = sc + j % C::SCALES * 2 * AP_MAX_PPT;
         const int key0 = (sg.t0 + tt) * C::TILE_KEYS + tid * KPR;
-        if (p.inject_timeout && j == 0) {
-          failed = !mbar_wait(never, 0, kInjectWaitCycles);
-          if (tid == 0) {
-            *abort_flag = 1;
-            atomicOr(p.err, kErrTimeout);
-          }
-        }
+        if (p.inject_timeout && (cta & 1) == 0 && j == 0) expire();
         failed |= !ap_wait(&s_full[sb], (j >> 1) & 1, abort_flag, p.err);
         __syncwarp();
         tc_fence_after();
@@ -921,7 +925,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         }
         vmax = warp_max_f32(vmax);
         if (lane == 0) rb[warp * C::RED + 8] = vmax;
-        if (failed = softmax_sync(failed)) break;
+        if (gave_up = softmax_sync(failed)) break;
         vmax = fmaxf(fmaxf(rb[8], rb[C::RED + 8]), fmaxf(rb[2 * C::RED + 8], rb[3 * C::RED + 8]));
         float alpha[G];
 #pragma unroll
@@ -940,6 +944,8 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
             l_part[g] += s[par][g];
           }
         }
+        // in every other CTA one warp alone gives up, where no barrier follows before the unit's end
+        if (p.inject_timeout && (cta & 1) != 0 && tt == sg.n - 1 && warp == 2) expire();
         if (j >= 2) failed |= !ap_wait(&p_free[sb], ((j - 2) >> 1) & 1, abort_flag, p.err);
         // weights are written as 256 p (V scale / the tile's largest): at most 256
         const float v_inv = vmax > 0.f ? 1.f / vmax : 0.f;
@@ -967,7 +973,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
 #pragma unroll
         for (int g = 0; g < G; ++g) a_prev[g] = alpha[g];
       }
-      if (failed) break;
+      if (gave_up) break;
       consume_o(sg.j0 + sg.n - 1);
 
       // ---------------- segment epilogue
@@ -979,7 +985,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         const float ls = warp_sum(l_part[g]);
         if (lane == 0) rb[warp * C::RED + g] = ls;
       }
-      if (failed = softmax_sync(failed)) break;
+      if (gave_up = softmax_sync(failed)) break;
 #pragma unroll
       for (int g = 0; g < G; ++g) L[g] = (rb[g] + rb[C::RED + g]) + (rb[2 * C::RED + g] + rb[3 * C::RED + g]);
       if (whole) {
@@ -996,7 +1002,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         }
         // every partial store of the CTA is ordered before tid 0's arrival
         // (a release at GPU scope, cumulative over the barrier)
-        if (failed = softmax_sync(failed)) break;
+        if (gave_up = softmax_sync(failed)) break;
         if (tid == 0) {
           int prev;
           asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;"
@@ -1008,7 +1014,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           *last_flag = last ? 1 : 0;
         }
         arrived = i;
-        if (failed = softmax_sync(failed)) break;
+        if (gave_up = softmax_sync(failed)) break;
         if (*last_flag) {
           // ---- merge: the CTAs from the one with the unit's first tile to the
           // one with its last, in that order whoever merges; a CTA's slot is
@@ -1087,11 +1093,11 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
           write_out(sg.b, sg.h, ot, lt);
         }
       }
-      if (failed) break;
+      if (gave_up) break;
       if (sg.j0 + sg.n >= ntiles) break;
       sg = seg_at(sg.j0 + sg.n);
     }
-    if (failed && tid == 0) {
+    if (gave_up && tid == 0) {
       // The CTA gave up: still add the tiles of its remaining shared units to
       // their counters (their outputs are undefined), so that every counter is
       // back at zero when the launch ends.
