@@ -308,7 +308,9 @@ __device__ __forceinline__ void note_step(LpShared& sh, const Piece<T>& pc, cons
   for (int c = 0; c < LP_VECS; ++c)
     if (reaches(c)) note(sh, d[c], vb + c * LP_THREADS + tid);
   __syncthreads();
-  if (sh.n_hits <= LP_HITS) return;
+  const int noted = sh.n_hits;
+  __syncthreads();   // every thread has read it before one that goes on notes the next step's
+  if (noted <= LP_HITS) return;
 #pragma unroll
   for (int c = 0; c < LP_VECS; ++c) {
     const uint32_t eq = __ballot_sync(0xffffffffu, reaches(c) && !above(c));

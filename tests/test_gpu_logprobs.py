@@ -60,3 +60,22 @@ def test_a_few_nan_rank_first(dtype, vocab, k, copies):
     bad = sorted({int(r) for r in np.argwhere((got != want).any((0, 2)))[:, 0]})
     assert not bad, f"rows {bad}: {got[0, bad[0]][:6]} for {want[bad[0]][:6]}"
     assert ent.isnan().all() and tops.isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows", [2, 320])   # several CTAs to a row; one
+def test_rows_whose_notes_run_over_behind_their_first_step(dtype, rows):
+    """A first step whose notes fit, a second one (and every later one) whose
+    notes do not: every launch decides alike, and right."""
+    vocab, k = 300000, 7
+    step = 2048 * 128 // torch.finfo(dtype).bits   # logits of a CTA's step
+    gen = torch.Generator().manual_seed(rows)
+    x = torch.randn(2, vocab, generator=gen)
+    x[0] += 3 * (torch.arange(vocab) // step)
+    x[1, step:] += 6.0
+    x = x.to(dtype)
+    _, _, want, _ = Q.token_logprobs(x.double().numpy(), None, k)
+    big = x.cuda().repeat(rows // 2, 1)
+    runs = [_run(big, k)[1] for _ in range(20)]
+    want = torch.from_numpy(want).cuda().repeat(rows // 2, 1)
+    assert all(torch.equal(r, want) for r in runs)
