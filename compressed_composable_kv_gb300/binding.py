@@ -371,6 +371,7 @@ def c2kv_attend_prefill(geom, layer: int, k_caches, v_caches, rope_tables, cap: 
 
 
 C2KV_DECODE_OVERLAP_PREVIOUS = 1
+C2KV_DECODE_ROW_AT_LENGTH = 4
 
 
 def c2kv_attend_decode(geom, layer: int, k_caches, v_caches, rope_tables, cap: int, n_cached_dev: torch.Tensor,

@@ -158,7 +158,7 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
                                void* workspace, size_t workspace_bytes, uint32_t flags, void* stream) {
   AttendPages8Params p;
   std::memset(&p, 0, sizeof(p));
-  if (flags & ~uint32_t(C2KV_DECODE_OVERLAP_PREVIOUS)) return api_fail(C2KV_EINVAL, "unknown decode flags");
+  if (flags & ~uint32_t(C2KV_DECODE_OVERLAP_PREVIOUS | C2KV_DECODE_ROW_AT_LENGTH)) return api_fail(C2KV_EINVAL, "unknown decode flags");
   c2kv_status s = check_pages(geom, pages, layer, page_table, max_pages, &p.pool);
   if (s != C2KV_OK) return s;
   s = check_new_tokens(batch, n_cached_dev, k_new, v_new, rope_table, table_rows, rope_row_dev);
@@ -201,6 +201,7 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
   p.max_keys = max_keys;
   p.table_rows = table_rows;
   p.has_new = k_new != nullptr ? 1 : 0;
+  p.row_at_length = (flags & C2KV_DECODE_ROW_AT_LENGTH) != 0 ? 1 : 0;
   p.early = (flags & C2KV_DECODE_OVERLAP_PREVIOUS) != 0 ? 1 : 0;
   p.inject_timeout = api_take_injected_timeout();
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)geom->head_dim));

@@ -309,10 +309,11 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     };
     for (int b0 = 0; b0 < p.batch; b0 += 32) {
       const int b = b0 + lane;
-      int32_t n = -1, rr = 0, keys = -1;
+      int32_t n = -1, keys = -1;
+      int64_t rr = 0;
       if (b < p.batch) {
         n = p.n_cached[b];
-        rr = p.rope_row[b];
+        rr = (int64_t)p.rope_row[b] + (p.row_at_length ? n : 0);
       }
       if (n >= 0) {
         if (n > p.max_keys - p.has_new || rr < 0 || rr >= p.table_rows) bad = true;
@@ -320,7 +321,7 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
       }
       none |= keys == 0;
       M.keys[b] = keys;
-      M.rope[b] = rr;
+      M.rope[b] = (int32_t)rr;   // of an empty or bad place: not used
       M.start[b] = scan((((keys - 1) >> C::TILE_LG) + 1) * p.pool.n_kv, at);
     }
     // Split by unit where there are CTAs enough: every unit in parts of at most

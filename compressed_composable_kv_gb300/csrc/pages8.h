@@ -115,6 +115,7 @@ struct AttendPages8Params {
   int32_t* counters;             // [batch * n_kv] tiles merged so far per unit
   unsigned* err;
   int32_t batch, n_q, max_pages, max_keys, table_rows, has_new, inject_timeout;
+  int32_t row_at_length;         // a sequence's table row is rope_row + its length
   int32_t early;                 // lengths, page table, RoPE rows and held rows may be read before the wait
   float scale_log2;
 };

@@ -67,9 +67,7 @@ class RequestBatch:
         # request b's row r is row b * cap + r
         self.rope_table = torch.empty((self.batch, tb // 4), dtype=torch.float32, device=device)
         self.rope_tables = list(self.rope_table)
-        # lengths and RoPE rows advance together
-        self._lengths = torch.zeros((2, self.batch), dtype=torch.int32, device=device)
-        self.n_cached_dev, self.rope_row_dev = self._lengths
+        self.n_cached_dev = torch.zeros(self.batch, dtype=torch.int32, device=device)
         self.max_keys_decode = max(self.n_slots) + q_len + decode_steps
         ws = 256
         if q_len > 0:
@@ -84,13 +82,19 @@ class RequestBatch:
             self.v8 = torch.empty_like(self.k8)
             self.k_scale = torch.empty((L, n_pages, H), dtype=torch.float32, device=device)
             self.v_scale = torch.empty_like(self.k_scale)
+            self._rope_start = torch.arange(self.batch, dtype=torch.int32, device=device) * self.cap
             # of its own: the other calls' scratch would overwrite its counters
             self.workspace8 = torch.zeros(B.c2kv_attend_pages8_workspace_size(geom, self.batch, self.max_keys_decode),
                                           dtype=torch.uint8, device=device)
         self.workspace = torch.zeros(ws, dtype=torch.uint8, device=device)
         B.c2kv_workspace_init(self.workspace)
-        start = [n + q_len for n in self.n_slots]
-        self._dec_start = torch.tensor([start, [b * self.cap + n for b, n in enumerate(start)]], dtype=torch.int32)
+        self._dec_start = torch.tensor([n + q_len for n in self.n_slots], dtype=torch.int32)
+
+    @property
+    def rope_row_dev(self) -> torch.Tensor:
+        """Each request's row of rope_table for its next token, from the lengths as they are."""
+        start = torch.arange(self.batch, dtype=torch.int32, device=self.n_cached_dev.device) * self.cap
+        return start + self.n_cached_dev
 
     def compose(self, stream=None) -> None:
         self.compose_layers(0, self.geom.n_layers, stream)
@@ -116,7 +120,7 @@ class RequestBatch:
         """Point the device lengths at the first decode step (after the question)."""
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
-            self._lengths.copy_(self._dec_start, non_blocking=True)
+            self.n_cached_dev.copy_(self._dec_start, non_blocking=True)
 
     def fill_pages8(self, layer_begin: int = 0, layer_end: Optional[int] = None, stream=None) -> None:
         """The composed and prefilled rows of layers [layer_begin, layer_end) to the 8-bit pages."""
@@ -132,20 +136,21 @@ class RequestBatch:
         layer before) finishes: see C2KV_DECODE_OVERLAP_PREVIOUS."""
         if overlap_previous is None:
             overlap_previous = layer > 0
+        flags = B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0
         if self.page8 is not None:
             B.c2kv_attend_pages8(self.geom, layer, self.k8, self.v8, self.k_scale, self.v_scale, self.page_table,
                                  self.n_cached_dev, self.max_keys_decode, q.view(self.batch, -1, self.geom.head_dim),
                                  k_new.view(self.batch, -1, self.geom.head_dim),
-                                 v_new.view(self.batch, -1, self.geom.head_dim), self.rope_table, self.rope_row_dev,
+                                 v_new.view(self.batch, -1, self.geom.head_dim), self.rope_table, self._rope_start,
                                  out.view(self.batch, -1, self.geom.head_dim), self.workspace8, stream,
-                                 B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0)
+                                 flags | B.C2KV_DECODE_ROW_AT_LENGTH)
             return
         B.c2kv_attend_decode(self.geom, layer, self.k_caches, self.v_caches, self.rope_tables, self.cap,
                              self.n_cached_dev, self.max_keys_decode, q, k_new, v_new, out, self.workspace,
-                             stream, B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0)
+                             stream, flags)
 
     def advance(self, stream=None) -> None:
-        B.c2kv_seq_advance(self._lengths, 1, stream)
+        B.c2kv_seq_advance(self.n_cached_dev, 1, stream)
 
 
 class DecoderModel:

@@ -514,8 +514,12 @@ c2kv_status c2kv_pages8_append(const c2kv_geometry* geom, const c2kv_pages8* pag
  * scratch would overwrite its counters).  flags: C2KV_DECODE_OVERLAP_PREVIOUS, as in
  * c2kv_attend_decode: the kernel before on `stream` must not write the
  * lengths, the page table, the RoPE table and rope_row_dev, or this layer's
- * held rows and their scales.
+ * held rows and their scales.  C2KV_DECODE_ROW_AT_LENGTH: the table row of
+ * sequence b is rope_row_dev[b] + n_cached_dev[b], so that rope_row_dev says
+ * where a sequence's rows begin in the table and the lengths are all that
+ * advances from step to step.
  */
+#define C2KV_DECODE_ROW_AT_LENGTH 4u
 size_t c2kv_attend_pages8_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t max_keys);
 c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
                                const int32_t* page_table, int32_t max_pages, const int32_t* n_cached_dev,

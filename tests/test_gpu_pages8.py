@@ -667,3 +667,37 @@ def test_offsets_beyond_32_bits():
         # sums of the row in another order: a few fp32 roundings of values below 32
         assert (a[-1:].double() - b.double()).abs().max() <= 2.0 ** -17
         assert torch.equal(a[0], a[-2])
+
+
+def test_table_rows_at_the_lengths():
+    """C2KV_DECODE_ROW_AT_LENGTH: the table row is rope_row_dev[b] +
+    n_cached_dev[b] (from a negative start too); the sum is checked."""
+    g = _geom(128, 4, 2)
+    held, place = [100, 7, 0, -1], [3, 300, 500, 5]
+    pool = Pool(g, 32, [n + 1 for n in held])
+    for kv in (0, 1):
+        for b, n in enumerate(held):
+            if n > 0:
+                pool.put(0, b, 0, kv, _f64(_values(pool.rng, (2, n, 128))))
+    q = _dev(S.normal_bf16(pool.rng, (4, 8, 128)))
+    kn, vn = (_dev(S.normal_bf16(pool.rng, (4, 2, 128))) for _ in range(2))
+    tab = _rope(g, np.arange(512))
+    n_dev = torch.tensor(held, dtype=torch.int32, device="cuda")
+    ws = torch.zeros(P.c2kv_attend_pages8_workspace_size(g, 4, 101), dtype=torch.uint8, device="cuda")
+
+    def step(rows, flags):
+        pool.upload()
+        out = torch.full((4, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        P.c2kv_attend_pages8(g, 0, *pool.args(), n_dev, 101, q, kn, vn, tab,
+                             torch.tensor(rows, dtype=torch.int32, device="cuda"), out, ws, flags=flags)
+        torch.cuda.synchronize()
+        return [out] + [t.view(torch.uint8).clone() for t in pool.args()[:4]], P.c2kv_device_error()
+
+    want, code = step(place, 0)
+    assert code == P.C2KV_OK
+    got, code = step([p - n for p, n in zip(place, held)], P.C2KV_DECODE_ROW_AT_LENGTH)
+    assert code == P.C2KV_OK and all(torch.equal(a, b) for a, b in zip(want, got))
+    for bad in (512 - 100, -101, 2 ** 31 - 1, -2 ** 31):
+        got, code = step([bad] + [p - n for p, n in zip(place[1:], held[1:])], P.C2KV_DECODE_ROW_AT_LENGTH)
+        assert code == P.C2KV_EDEVICE
+        assert (got[0][0] == 7.0).all() and torch.equal(got[0][1:], want[0][1:])

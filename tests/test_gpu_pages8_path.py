@@ -309,3 +309,25 @@ def test_many_launches_give_the_same_bits():
         got.append(torch.cat([lp, ent, ids.float().flatten(), tops.flatten()]))
     assert all(torch.equal(t, got[0]) for t in got[1:])
     r.sc.close()
+
+
+@pytest.mark.parametrize("d,page", [(128, 64), (64, 16)])
+def test_lengths_are_the_only_state_that_advances(d, page):
+    """The lengths moved by c2kv_seq_advance, and put back for a step taken
+    again: every key is rotated for the place it goes to."""
+    r = Requests(S.Geometry(2, 8, 2, d, 5.0e5), page)
+    for t in range(r.steps):
+        for again in (True, False):
+            outs = r.outs()
+            for l in range(r.g.n_layers):
+                r.rb.decode(l, r.dev["qd_pre"][t, l], r.dev["kd_pre"][t, l], r.dev["vd"][t, l], outs[l])
+            P.c2kv_seq_advance(r.rb.n_cached_dev)
+            if again:
+                r.rb.n_cached_dev.sub_(1)
+        torch.cuda.synchronize()
+        assert P.c2kv_device_error() == P.C2KV_OK
+        _near(outs, r.oracle_step(t), t)
+        r.check_pages()
+    want = [b * r.rb.cap + n + r.steps for b, n in enumerate(r.rows)]
+    assert r.rb.rope_row_dev.tolist() == want
+    r.sc.close()
