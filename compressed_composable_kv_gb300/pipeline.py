@@ -29,7 +29,9 @@ class RequestBatch:
     page8: tokens of a page (16, 32, 64 or 128) to decode over an 8-bit paged
     cache, half the bytes of the bf16 one: after composition and question
     prefill, fill_pages8 takes the bf16 rows over, and decode appends to and
-    attends over the pages.
+    attends over the pages.  `filled` holds the layers whose pages hold the rows
+    (a program that writes pages by calls of its own adds to it); decode refuses
+    the others, but not while a graph is captured.
     """
 
     def __init__(self, store: int, geom, requests: Sequence[RequestSpec], k: int, q_len: int,
@@ -74,6 +76,7 @@ class RequestBatch:
             ws = max(ws, B.c2kv_attend_workspace_size(geom, self.batch, q_len, max(self.n_slots) + q_len))
         ws = max(ws, B.c2kv_attend_workspace_size(geom, self.batch, 1, self.max_keys_decode))
         self.page8 = page8
+        self.filled = set()
         if page8 is not None:
             most = -(-self.max_keys_decode // page8)
             n_pages = most * self.batch
@@ -111,10 +114,25 @@ class RequestBatch:
                                            layer_end, self.k_caches[b], self.v_caches[b], self.cap,
                                            self.rope_tables[b], self.pos[b], stream)
             assert n == self.n_slots[b] and nxt == self.l_tot[b]
+        self._rows_change(range(layer_begin, layer_end), stream)
+
+    def _capturing(self, stream) -> bool:
+        if not self.n_cached_dev.is_cuda:
+            return False
+        if stream is not None and not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream))
+        with torch.cuda.stream(stream):
+            return torch.cuda.is_current_stream_capturing()
+
+    def _rows_change(self, layers, stream) -> None:
+        """The bf16 rows of these layers are no longer what their pages hold."""
+        if self.filled and not self._capturing(stream):
+            self.filled.difference_update(layers)
 
     def prefill(self, layer: int, q, k_new, v_new, out, stream=None) -> None:
         B.c2kv_attend_prefill(self.geom, layer, self.k_caches, self.v_caches, self.rope_tables, self.cap,
                               self.n_slots, q, k_new, v_new, out, self.workspace, stream)
+        self._rows_change((layer,), stream)
 
     def reset_decode(self, stream=None) -> None:
         """Point the device lengths at the first decode step (after the question)."""
@@ -126,9 +144,11 @@ class RequestBatch:
         """The composed and prefilled rows of layers [layer_begin, layer_end) to the 8-bit pages."""
         if self.page8 is None:
             raise ValueError("this batch was made without page8")
-        B.c2kv_pages8_fill(self.geom, layer_begin, self.geom.n_layers if layer_end is None else layer_end,
-                           self.k_caches, self.v_caches, self.cap, [n + self.q_len for n in self.n_slots],
-                           self.k8, self.v8, self.k_scale, self.v_scale, self.page_table, stream)
+        layer_end = self.geom.n_layers if layer_end is None else layer_end
+        B.c2kv_pages8_fill(self.geom, layer_begin, layer_end, self.k_caches, self.v_caches, self.cap,
+                           [n + self.q_len for n in self.n_slots], self.k8, self.v8, self.k_scale, self.v_scale,
+                           self.page_table, stream)
+        self.filled.update(range(layer_begin, layer_end))
 
     def decode(self, layer: int, q, k_new, v_new, out, stream=None, overlap_previous: Optional[bool] = None) -> None:
         """One decode step of one layer.  By default a layer > 0 call may start
@@ -138,6 +158,8 @@ class RequestBatch:
             overlap_previous = layer > 0
         flags = B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0
         if self.page8 is not None:
+            if layer not in self.filled and 0 <= layer < self.geom.n_layers and not self._capturing(stream):
+                raise ValueError(f"the pages of layer {layer} do not hold the batch's rows: fill_pages8 comes first")
             B.c2kv_attend_pages8(self.geom, layer, self.k8, self.v8, self.k_scale, self.v_scale, self.page_table,
                                  self.n_cached_dev, self.max_keys_decode, q.view(self.batch, -1, self.geom.head_dim),
                                  k_new.view(self.batch, -1, self.geom.head_dim),

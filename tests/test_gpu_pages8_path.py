@@ -331,3 +331,35 @@ def test_lengths_are_the_only_state_that_advances(d, page):
     want = [b * r.rb.cap + n + r.steps for b, n in enumerate(r.rows)]
     assert r.rb.rope_row_dev.tolist() == want
     r.sc.close()
+
+
+def test_a_step_captured_before_the_pages_are_filled():
+    """A program may capture its decode step before the first request's rows are
+    there, on the current stream or one it names; run at once, the same call is
+    refused, and a fill that is replayed counts."""
+    r = Requests(S.Geometry(2, 8, 2, 128, 5.0e5), 32)
+    rb, outs = r.rb, r.outs()
+    rb.compose()
+    for l in range(2):
+        o = torch.empty_like(r.dev["q_pre"][l])
+        rb.prefill(l, r.dev["q_pre"][l], r.dev["kq_pre"][l], r.dev["vq"][l], o)
+    with pytest.raises(ValueError, match="fill_pages8"):
+        rb.decode(0, r.dev["qd_pre"][0, 0], r.dev["kd_pre"][0, 0], r.dev["vd"][0, 0], outs[0])
+    side = torch.cuda.Stream()
+    step, fill = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(step, stream=side):
+        for l, st in ((0, None), (1, side.cuda_stream)):
+            rb.decode(l, r.dev["qd_pre"][0, l], r.dev["kd_pre"][0, l], r.dev["vd"][0, l], outs[l], st)
+        rb.advance()
+    with torch.cuda.graph(fill, stream=side):
+        rb.fill_pages8()
+        rb.compose_layers(0, 2)   # (captured, not run: the rows stay)
+    assert rb.filled == {0, 1}
+    rb.fill_pages8()
+    step.replay()
+    torch.cuda.synchronize()
+    assert P.c2kv_device_error() == P.C2KV_OK
+    _near(outs, r.oracle_step(0), 0)
+    r.check_pages()
+    r.sc.close()

@@ -171,3 +171,57 @@ def test_request_batch_refuses_other_page_sizes(P):
     for page8 in (0, 8, 48, 256):
         with pytest.raises(ValueError, match="page8"):
             P.RequestBatch(None, S.TINY, [], 4, 0, 1, page8=page8)
+
+
+@pytest.fixture
+def paged_batch(P, monkeypatch):
+    """A paged RequestBatch of two layers on the CPU: its calls of the library
+    are noted, not made."""
+    B = P.pipeline.B
+    calls = []
+    monkeypatch.setattr(B, "c2kv_store_lookup", lambda store, d: (40, 10, 0))
+    monkeypatch.setattr(B, "c2kv_workspace_init", lambda ws: None)
+    monkeypatch.setattr(B, "c2kv_compose_layers", lambda *a: (10, 40))
+    monkeypatch.setattr(B, "c2kv_attend_prefill", lambda *a: None)
+    monkeypatch.setattr(B, "c2kv_pages8_fill", lambda g, l0, l1, *a: calls.append(("fill", l0, l1)))
+    monkeypatch.setattr(B, "c2kv_attend_pages8",
+                        lambda g, l, *a: calls.append(("attend", l, bool(a[-1] & B.C2KV_DECODE_OVERLAP_PREVIOUS))))
+    g = S.Geometry(2, 4, 2, 64, 1e4)
+    rb = P.RequestBatch(None, g, [P.RequestSpec([0]), P.RequestSpec([1])], 4, 3, 5, device="cpu", page8=16)
+    x = torch.zeros((2, 4, 64))
+
+    def decode(layer, **kw):
+        rb.decode(layer, x, x[:, :2], x[:, :2], x, **kw)
+
+    return rb, decode, calls
+
+
+def test_pages_that_do_not_hold_the_rows_are_refused(paged_batch):
+    """Before fill_pages8, and after rows were composed or prefilled anew: of
+    the layers concerned alone."""
+    rb, decode, calls = paged_batch
+
+    def refused():
+        bad = []
+        for l in (0, 1):
+            calls.clear()
+            try:
+                decode(l)
+            except ValueError as e:
+                assert f"layer {l}" in str(e) and "fill_pages8" in str(e) and not calls
+                bad.append(l)
+        return bad
+
+    rb.compose()
+    assert refused() == [0, 1]
+    rb.fill_pages8(0, 1)
+    assert refused() == [1]
+    rb.fill_pages8()
+    assert refused() == []
+    rb.prefill(1, None, None, None, None)
+    assert refused() == [1]
+    rb.fill_pages8(1, 2)
+    rb.compose_layers(0, 1)
+    assert refused() == [0]
+    rb.filled.add(0)     # by a program that wrote the pages itself
+    assert refused() == []
