@@ -77,6 +77,7 @@ class RequestBatch:
         ws = max(ws, B.c2kv_attend_workspace_size(geom, self.batch, 1, self.max_keys_decode))
         self.page8 = page8
         self.filled = set()
+        self._fill_before = False   # the batch's last call was fill_pages8
         if page8 is not None:
             most = -(-self.max_keys_decode // page8)
             n_pages = most * self.batch
@@ -149,13 +150,15 @@ class RequestBatch:
                            [n + self.q_len for n in self.n_slots], self.k8, self.v8, self.k_scale, self.v_scale,
                            self.page_table, stream)
         self.filled.update(range(layer_begin, layer_end))
+        self._fill_before = True
 
     def decode(self, layer: int, q, k_new, v_new, out, stream=None, overlap_previous: Optional[bool] = None) -> None:
         """One decode step of one layer.  By default a layer > 0 call may start
         while the previous kernel on the stream (this batch's decode of the
-        layer before) finishes: see C2KV_DECODE_OVERLAP_PREVIOUS."""
+        layer before) finishes: see C2KV_DECODE_OVERLAP_PREVIOUS.  A call right
+        behind fill_pages8, which writes what it reads, does not."""
         if overlap_previous is None:
-            overlap_previous = layer > 0
+            overlap_previous = layer > 0 and not self._fill_before
         flags = B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0
         if self.page8 is not None:
             if layer not in self.filled and 0 <= layer < self.geom.n_layers and not self._capturing(stream):
@@ -166,6 +169,7 @@ class RequestBatch:
                                  v_new.view(self.batch, -1, self.geom.head_dim), self.rope_table, self._rope_start,
                                  out.view(self.batch, -1, self.geom.head_dim), self.workspace8, stream,
                                  flags | B.C2KV_DECODE_ROW_AT_LENGTH)
+            self._fill_before = False
             return
         B.c2kv_attend_decode(self.geom, layer, self.k_caches, self.v_caches, self.rope_tables, self.cap,
                              self.n_cached_dev, self.max_keys_decode, q, k_new, v_new, out, self.workspace,

@@ -225,3 +225,25 @@ def test_pages_that_do_not_hold_the_rows_are_refused(paged_batch):
     assert refused() == [0]
     rb.filled.add(0)     # by a program that wrote the pages itself
     assert refused() == []
+
+
+def test_a_step_behind_a_fill_does_not_overlap_it(paged_batch):
+    """C2KV_DECODE_OVERLAP_PREVIOUS reads the layer's pages before the kernel
+    before is done, so the first step behind a fill goes without; a caller that
+    asks for either gets it."""
+    rb, decode, calls = paged_batch
+    rb.compose()
+    for l in (0, 1):
+        rb.fill_pages8(l, l + 1)
+        decode(l)
+    decode(1)
+    decode(0)
+    decode(1, overlap_previous=False)
+    decode(0, overlap_previous=True)
+    rb.fill_pages8()
+    decode(0)
+    decode(1)
+    want = [("fill", 0, 1), ("attend", 0, False), ("fill", 1, 2), ("attend", 1, False), ("attend", 1, True),
+            ("attend", 0, False), ("attend", 1, False), ("attend", 0, True), ("fill", 0, 2), ("attend", 0, False),
+            ("attend", 1, True)]
+    assert calls == want
