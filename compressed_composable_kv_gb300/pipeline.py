@@ -251,6 +251,8 @@ class DecoderModel:
         """Of the last step's logits: logprob of tokens [batch] (int32 on the
         device; negative: none), entropy, and the top_k alternatives in top_ids
         and top_logprobs."""
+        if self.logits is None:
+            raise ValueError("the model's weights have no lm_head: there are no logits")
         B.c2kv_token_logprobs(self.logits, tokens, self.top_ids.shape[1], self.logprob, self.entropy, self.top_ids,
                               self.top_logprobs, stream)
 

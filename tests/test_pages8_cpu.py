@@ -247,3 +247,10 @@ def test_a_step_behind_a_fill_does_not_overlap_it(paged_batch):
             ("attend", 0, False), ("attend", 1, False), ("attend", 0, True), ("fill", 0, 2), ("attend", 0, False),
             ("attend", 1, True)]
     assert calls == want
+
+
+def test_log_probabilities_need_an_lm_head(P, monkeypatch):
+    monkeypatch.setattr(P.pipeline.B, "c2kv_workspace_init", lambda ws: None)
+    m = P.DecoderModel(S.TINY, S.ModelShape(64, 128, 32, 1e-5), {"layers": []}, 2, device="cpu", top_k=3)
+    with pytest.raises(ValueError, match="lm_head"):
+        m.token_logprobs(torch.zeros(2, dtype=torch.int32))
