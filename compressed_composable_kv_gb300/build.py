@@ -40,53 +40,53 @@ def _flags(extra=()):
                    "-I", INCLUDE, "-I", CSRC] + list(extra)
 
 
-def _deps():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
-    files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cpp"))]
-    files.append(os.path.join(INCLUDE, "c2kv.h"))
-    files.append(os.path.abspath(__file__))
-    return files
+def _fresh(target: str, deps) -> bool:
+    return os.path.exists(target) and all(os.path.getmtime(f) <= os.path.getmtime(target) for f in deps)
+
+
+def _lib_fresh() -> bool:
+    files = [os.path.join(CSRC, f) for f in SOURCES + [f for f in os.listdir(CSRC) if f.endswith(".h")]]
+    return _fresh(LIB, files + [os.path.join(INCLUDE, "c2kv.h"), os.path.abspath(__file__)])
+
+
+def _marshal_fresh() -> bool:
+    return _fresh(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "c2kv.h"), os.path.abspath(__file__)])
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(MARSHAL):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(MARSHAL))
-    return all(os.path.getmtime(f) <= t for f in _deps())
+    return _lib_fresh() and _marshal_fresh()
 
 
 def _torch_dir() -> str:
     return os.path.dirname(importlib.util.find_spec("torch").origin)
 
 
+def _run(cmd):
+    try:
+        return subprocess.run(cmd, capture_output=True, text=True)
+    except FileNotFoundError as e:
+        return subprocess.CompletedProcess(cmd, 1, "", f"{e}\n")
+
+
 def _compile_marshal():
     """marshal.cpp to an object; it is linked once libc2kv.so is there."""
-    obj = os.path.join(BUILD, "marshal.o")
     inc = os.path.join(_torch_dir(), "include")
-    cmd = ["g++", "-O2", "-std=c++20", "-fPIC", "-I", INCLUDE, "-isystem", inc, "-isystem",
-           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
-           "-c", os.path.join(CSRC, "marshal.cpp"), "-o", obj]
-    return obj, subprocess.run(cmd, capture_output=True, text=True)
+    return _run(["g++", "-O2", "-std=c++20", "-fPIC", "-I", INCLUDE, "-isystem", inc, "-isystem",
+                 os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", sysconfig.get_paths()["include"],
+                 "-c", os.path.join(CSRC, "marshal.cpp"), "-o", os.path.join(BUILD, "marshal.o")])
 
 
-def _link_marshal(obj: str) -> None:
+def _link_marshal():
     lib = os.path.join(_torch_dir(), "lib")
-    cmd = ["g++", "-shared", "-o", MARSHAL + ".tmp", obj, LIB, "-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
-           "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("linking _marshal.so failed")
-    os.replace(MARSHAL + ".tmp", MARSHAL)
+    r = _run(["g++", "-shared", "-o", MARSHAL + ".tmp", os.path.join(BUILD, "marshal.o"), LIB, "-L", lib,
+              "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
+    if r.returncode == 0:
+        os.replace(MARSHAL + ".tmp", MARSHAL)
+    return r
 
 
-def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
-    """Compile libc2kv.so if it is missing or stale; return its path."""
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD, exist_ok=True)
+def _build_lib(verbose: bool, extra) -> None:
     cc = nvcc()
-    extra = ["-Xptxas", "-v"] if ptxas_verbose else []
 
     def compile_one(src):
         obj = os.path.join(BUILD, src.replace(".cu", ".o"))
@@ -94,15 +94,10 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: boo
         r = subprocess.run(cmd, capture_output=True, text=True)
         return src, obj, r
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        marshal = ex.submit(_compile_marshal)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         results = list(ex.map(compile_one, SOURCES))
-        marshal_obj, r = marshal.result()
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("g++ failed on marshal.cpp")
     for src, _, r in results:
-        if verbose or ptxas_verbose or r.returncode != 0:
+        if verbose or r.returncode != 0:
             sys.stderr.write(r.stdout + r.stderr)
         if r.returncode != 0:
             raise RuntimeError(f"nvcc failed on {src}")
@@ -118,7 +113,27 @@ def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: boo
         sys.stderr.write(r.stdout + r.stderr)
         raise RuntimeError("linking libc2kv.so failed")
     os.replace(tmp, LIB)
-    _link_marshal(marshal_obj)
+
+
+def build_library(force: bool = False, verbose: bool = False, ptxas_verbose: bool = False) -> str:
+    """Compile what is missing or stale; return libc2kv.so's path.  Where
+    _marshal.so cannot be built (no g++ with C++20, no torch headers) the
+    compiler's message is shown and libc2kv.so is built all the same: only the
+    calls that go by way of that module raise ImportError."""
+    lib, marshal = force or not _lib_fresh(), force or not _marshal_fresh()
+    os.makedirs(BUILD, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        compiled = ex.submit(_compile_marshal) if marshal else None
+        if lib:
+            _build_lib(verbose or ptxas_verbose, ["-Xptxas", "-v"] if ptxas_verbose else [])
+    if marshal:
+        r = compiled.result()
+        if r.returncode == 0:
+            r = _link_marshal()
+        if r.returncode != 0:
+            sys.stderr.write(r.stdout + r.stderr + "_marshal.so is not built\n")
+            if os.path.exists(MARSHAL):   # of older sources
+                os.remove(MARSHAL)
     return LIB
 
 

@@ -254,3 +254,42 @@ def test_log_probabilities_need_an_lm_head(P, monkeypatch):
     m = P.DecoderModel(S.TINY, S.ModelShape(64, 128, 32, 1e-5), {"layers": []}, 2, device="cpu", top_k=3)
     with pytest.raises(ValueError, match="lm_head"):
         m.token_logprobs(torch.zeros(2, dtype=torch.int32))
+
+
+@pytest.fixture
+def fake_build(tmp_path, monkeypatch):
+    """A build into an empty folder whose compilers only make their outputs;
+    `gxx` says what becomes of g++: its return code, or None: there is none."""
+    state = dict(gxx=0, ran=[])
+    for name, file in (("LIB", "libc2kv.so"), ("MARSHAL", "_marshal.so")):
+        monkeypatch.setattr(build, name, str(tmp_path / file))
+    monkeypatch.setattr(build, "BUILD", str(tmp_path))
+    monkeypatch.setattr(build, "nvcc", lambda: "nvcc")
+
+    def run(cmd, **kw):
+        state["ran"].append(cmd[0])
+        if cmd[0] == "g++" and state["gxx"] is None:
+            raise FileNotFoundError("g++")
+        code = state["gxx"] if cmd[0] == "g++" else 0
+        if code == 0:
+            open(cmd[cmd.index("-o") + 1], "w").close()
+        return build.subprocess.CompletedProcess(cmd, code, "", "no such header")
+
+    monkeypatch.setattr(build.subprocess, "run", run)
+    return state
+
+
+@pytest.mark.parametrize("gxx", [1, None])
+def test_the_library_is_built_where_the_marshalling_module_cannot_be(fake_build, gxx, capsys):
+    import os
+    fake_build["gxx"] = gxx
+    open(build.MARSHAL, "w").close()    # of an older source: not to be loaded
+    os.utime(build.MARSHAL, (0, 0))
+    assert build.build_library() == build.LIB and os.path.exists(build.LIB)
+    assert not os.path.exists(build.MARSHAL) and "_marshal.so" in capsys.readouterr().err
+    fake_build.update(gxx=0, ran=[])
+    build.build_library()
+    assert os.path.exists(build.MARSHAL) and "nvcc" not in fake_build["ran"]
+    fake_build["ran"] = []
+    build.build_library()
+    assert fake_build["ran"] == []
