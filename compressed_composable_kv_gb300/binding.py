@@ -16,7 +16,7 @@ from typing import Optional, Sequence
 import numpy as np
 import torch
 
-from .build import LIB, MARSHAL
+from .build import LIB, MARSHAL, marshal_fits_torch
 
 C2KV_OK, C2KV_EINVAL, C2KV_ENOMEM, C2KV_ENOTFOUND = 0, 1, 2, 3
 C2KV_ECAPACITY, C2KV_ECUDA, C2KV_ETIMEOUT, C2KV_EDEVICE, C2KV_EIO = 4, 5, 6, 7, 8
@@ -521,6 +521,9 @@ def _load_marshal():
     load_library()
     if not os.path.exists(MARSHAL):
         raise ImportError(f"_marshal.so is not built ({MARSHAL}); run "
+                          "compressed_composable_kv_gb300.build.build_library()")
+    if not marshal_fits_torch():
+        raise ImportError(f"_marshal.so ({MARSHAL}) was built for another torch or Python; run "
                           "compressed_composable_kv_gb300.build.build_library()")
     loader = importlib.machinery.ExtensionFileLoader("_marshal", MARSHAL)
     spec = importlib.util.spec_from_file_location("_marshal", MARSHAL, loader=loader)

@@ -50,7 +50,23 @@ def _lib_fresh() -> bool:
 
 
 def _marshal_fresh() -> bool:
-    return _fresh(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "c2kv.h"), os.path.abspath(__file__)])
+    return marshal_fits_torch() and _fresh(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "c2kv.h"),
+                                                     os.path.abspath(__file__)])
+
+
+def _torch_tag() -> str:
+    """What _marshal.so is bound to: this torch, by place and version, and this Python."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return "\n".join([_torch_dir(), sys.implementation.cache_tag, f.read()])
+
+
+def marshal_fits_torch() -> bool:
+    """Whether _marshal.so was built for the torch and Python that run."""
+    try:
+        with open(MARSHAL + ".torch") as f:
+            return f.read() == _torch_tag()
+    except OSError:
+        return False
 
 
 def up_to_date() -> bool:
@@ -81,6 +97,8 @@ def _link_marshal():
     r = _run(["g++", "-shared", "-o", MARSHAL + ".tmp", os.path.join(BUILD, "marshal.o"), LIB, "-L", lib,
               "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
     if r.returncode == 0:
+        with open(MARSHAL + ".torch", "w") as f:
+            f.write(_torch_tag())
         os.replace(MARSHAL + ".tmp", MARSHAL)
     return r
 

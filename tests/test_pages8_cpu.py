@@ -293,3 +293,22 @@ def test_the_library_is_built_where_the_marshalling_module_cannot_be(fake_build,
     fake_build["ran"] = []
     build.build_library()
     assert fake_build["ran"] == []
+
+
+def test_the_marshalling_module_belongs_to_one_torch(fake_build, monkeypatch, tmp_path):
+    """Built anew for another torch, and not loaded before it is."""
+    from compressed_composable_kv_gb300 import binding
+    build.build_library()
+    assert build.up_to_date()
+    other = tmp_path / "site" / "torch"
+    other.mkdir(parents=True)
+    (other / "version.py").write_text("__version__ = '0.0'\n")
+    monkeypatch.setattr(build, "_torch_dir", lambda: str(other))
+    assert not build.up_to_date()
+    monkeypatch.setattr(binding, "MARSHAL", build.MARSHAL)
+    monkeypatch.setattr(binding, "load_library", lambda: None)
+    with pytest.raises(ImportError, match="another torch"):
+        binding._load_marshal()
+    fake_build["ran"] = []
+    build.build_library()
+    assert build.up_to_date() and fake_build["ran"] == ["g++", "g++"]
