@@ -827,13 +827,6 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
     // and that alone decides who leaves: a barrier or a tensor memory load that
     // some had left before would never end.
     bool failed = false, gave_up = false;
-    auto expire = [&]() {   // test hook: a wait that runs out
-      failed |= !mbar_wait(never, 0, kInjectWaitCycles);
-      if (lane == 0) {
-        *abort_flag = 1;
-        atomicOr(p.err, kErrTimeout);
-      }
-    };
     int k_red = 0;      // uses of red, whose two halves take turns
     int arrived = -1;   // last segment whose tiles were added to its unit's counter
     // out[b][h * G + g] from the lanes' o[g] over l[g]
@@ -890,7 +883,13 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
         const int sb = j & 1;
         const float* scs = sc + j % C::SCALES * 2 * AP_MAX_PPT;
         const int key0 = (sg.t0 + tt) * C::TILE_KEYS + tid * KPR;
-        if (p.inject_timeout && (cta & 1) == 0 && j == 0) expire();
+        if (p.inject_timeout && (cta & 1) == 0 && j == 0) {
+          failed = !mbar_wait(never, 0, kInjectWaitCycles);
+          if (tid == 0) {
+            *abort_flag = 1;
+            atomicOr(p.err, kErrTimeout);
+          }
+        }
         failed |= !ap_wait(&s_full[sb], (j >> 1) & 1, abort_flag, p.err);
         __syncwarp();
         tc_fence_after();
@@ -945,8 +944,11 @@ __global__ void __launch_bounds__(AP_THREADS, 2)
             l_part[g] += s[par][g];
           }
         }
-        // in every other CTA one warp alone gives up, where no barrier follows before the unit's end
-        if (p.inject_timeout && (cta & 1) != 0 && tt == sg.n - 1 && warp == 2) expire();
+        // the test hook, in every other CTA: one warp gives up, where no barrier follows before the unit's end
+        if (p.inject_timeout && (cta & 1) != 0 && tt == sg.n - 1 && warp == 2) {
+          failed = true;
+          *abort_flag = 1;
+        }
         if (j >= 2) failed |= !ap_wait(&p_free[sb], ((j - 2) >> 1) & 1, abort_flag, p.err);
         // weights are written as 256 p (V scale / the tile's largest): at most 256
         const float v_inv = vmax > 0.f ? 1.f / vmax : 0.f;

@@ -572,8 +572,8 @@ c2kv_status c2kv_kernel_launches(uint64_t* count);
  * error word, lets its copies in flight land and returns; that launch's
  * outputs are undefined, the cache rows it appends are written, and the
  * context stays usable.  c2kv_attend_pages8 counts among them; the rows it
- * appends may then be missing, and in every other of its CTAs the wait runs out
- * in one warp alone, at the last tile of a sequence's head.  0 disarms it.  Process-wide; C2KV_EINVAL for n < 0.
+ * appends may then be missing, and in every other of its CTAs one warp alone
+ * gives up, at the last tile of a sequence's head.  0 disarms it.  Process-wide; C2KV_EINVAL for n < 0.
  */
 c2kv_status c2kv_test_expire_next_waits(int32_t n_launches);
 
