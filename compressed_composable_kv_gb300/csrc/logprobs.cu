@@ -291,9 +291,14 @@ __device__ __forceinline__ void note(LpShared& sh, const uint4& d, int v) {
   }
 }
 
-// Whether x reaches a bound that is its step's k-th largest group maximum; a NaN
-// bound (k groups hold one) is reached by NaN alone, which rank above the rest.
-__device__ __forceinline__ bool reaches_bound(float x, float bound) { return bound == bound ? !(x < bound) : x != x; }
+// What the logits x that reach a bound (in the order of order_bits) exceed, as
+// !(x <= it): the next value below the bound. A NaN bound (k groups hold one) is
+// reached by NaN alone, which exceed +inf so; -inf by all, which exceed NaN so.
+__device__ __forceinline__ float below(float bound) {
+  if (bound != bound) return INFINITY;
+  const uint32_t o = order_bits(bound) - 1;
+  return from_order(o == 0x7FFFFFFFu ? o - 1 : o);   // below 0 comes no -0
+}
 
 // Notes a step's vectors that reach the step's bound.  Where many equal it (a
 // mask's value, say, or NaN) the first k of these in order will do: each holds
@@ -302,7 +307,8 @@ template <typename T>
 __device__ __forceinline__ void note_step(LpShared& sh, const Piece<T>& pc, const uint4 (&d)[LP_VECS],
                                           const float (&vm)[LP_VECS], int vb, float bound, int k) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  auto reaches = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && reaches_bound(vm[c], bound); };
+  const float least = below(bound);
+  auto reaches = [&](int c) { return vb + c * LP_THREADS + tid < pc.v1 && !(vm[c] <= least); };
   auto above = [&](int c) { return reaches(c) && bound == bound && !(vm[c] <= bound); };
 #pragma unroll
   for (int c = 0; c < LP_VECS; ++c)
@@ -350,6 +356,7 @@ __device__ __noinline__ bool step_by_step(LpShared& sh, const Piece<T>& pc, int 
     }
     if (tid < have) sh.cand[tid] = sh.top[tid];
     const float bound = group_bound(sh, vm, tid, k);
+    const float least = below(bound);
     note_step(sh, pc, d, vm, w, bound, k);
     __syncthreads();
     if (sh.n_hits > LP_HITS) return false;
@@ -360,7 +367,7 @@ __device__ __noinline__ bool step_by_step(LpShared& sh, const Piece<T>& pc, int 
     };
     for (int i = tid; i < sh.n_hits * N; i += LP_THREADS) {
       const float v = (float)reinterpret_cast<const T*>(sh.hit)[i];
-      if (sh.hit_at[i / N] >= vb && reaches_bound(v, bound)) list(v, pc.index(sh.hit_at[i / N], i % N));
+      if (sh.hit_at[i / N] >= vb && !(v <= least)) list(v, pc.index(sh.hit_at[i / N], i % N));
     }
     if (vb == pc.v0 && tid < pc.extra) list((float)pc.x[pc.extra_at(tid)], pc.extra_at(tid));
     __syncthreads();
@@ -482,8 +489,9 @@ __global__ void __launch_bounds__(LP_THREADS, 4) token_logprobs_kernel(const __g
   }
   if (k > 0) {
     const int n_hits = sh.n_hits;
+    const float least = below(bound);
     auto list = [&](float v, int i) {
-      if (!reaches_bound(v, bound)) return;
+      if (v <= least) return;
       const int at = atomicAdd(&sh.count, 1);
       if (at < LP_CAND) sh.cand[at] = list_key(v, i);
     };
