@@ -29,19 +29,23 @@
 // holds up the loads of one while it ends the other; else (more units than
 // CTAs, or lengths so mixed that the longest part would be 1.5 times an even
 // share) the tiles are laid end to end and cut into one equal range per CTA.
-// 8 x 8000 keys of 5 heads to a kv head: 34 us by parts, 39 us by ranges; 16
-// sequences of 1 to 8 thousand keys 35 and 39; 4 x 32768 52 and 58.  (A cluster
-// to a unit, merged in shared memory: 40, 34 and 68: its CTAs stream slower.)
+// 8 x 8000 keys of 5 heads to a kv head: 32.2 us by parts, 34.6 us by ranges; 16
+// sequences of 1 to 8 thousand keys 33.8 and 34.3; 4 x 32768 49.5 and 51.7; 1 x
+// 8000 12.1 and 12.8; but 32 sequences of 200 to 6000 keys 54 and 43 (44 with the
+// search that finds parts too long).  (A cluster to a unit, merged in shared
+// memory, took 40, 34 and 68 us for the first three on an earlier form: its CTAs
+// stream slower.)
 // A unit that one CTA holds whole is written at once; else its CTAs write
 // partial (m, l, O), and the one whose tiles complete the unit's counter merges
 // them, in the order of the keys whoever it is.
 //
 // Measured (one call among others in a graph; 6.8 TB/s is a plain copy's rate):
-//   4 x 32768 keys, 8 kv heads of 4 (269 MB)   49 us   5.5 TB/s
+//   4 x 32768 keys, 8 kv heads of 4 (269 MB)   50 us   5.4 TB/s
 //   8 x 8000 keys, 8 kv heads of 5 (131 MB)    32 us   4.1 TB/s
-//   16 ragged, 8 kv heads of 4 (142 MB)        33 us   4.2 TB/s
-//   64 of up to 1560 keys, as these (105 MB)   31 us   3.4 TB/s
-//   1 x 8000 keys, 8 kv heads of 4 (16 MB)     12.0 us
+//   16 ragged, 8 kv heads of 4 (142 MB)        34 us   4.2 TB/s
+//   64 of up to 1560 keys, as these (105 MB)   32 us   3.3 TB/s
+//   4 x 16384 keys, 8 heads of 64 (67 MB)      20 us   3.4 TB/s
+//   1 x 8000 keys, 8 kv heads of 4 (16 MB)     12.1 us
 //   16 sequences of up to 300 keys, 2 heads     7.9 us
 // While tiles stream they come at 6.9 TB/s.  What is left is the latency of a
 // call: 2.5 to 3.5 us for a launch that finds nothing to do, about 2 us to the
@@ -73,10 +77,11 @@ constexpr int AP_STAGE = 2 * AP_KV_BYTES;
 constexpr int AP_MAX_PPT = 16;                  // pages of a tile
 
 // Tiles of a CTA below which fewer CTAs work: more partials cost the merge more
-// than they save the stream (1 x 8000 keys at 2, 3, 4: 13.4, 12.9, 12.4 us).
+// than they save the stream (at 2, 3, 4: 1 x 8000 keys 12.5, 12.5, 12.1 us; 8000
+// keys beside 15 x 100 13.0, 13.0, 13.4).
 constexpr int kMinTiles = 4;
 // What the end of a unit costs a CTA, in tiles (see PageCut): 64 sequences of up to
-// 1560 keys take 39.9, 32.5, 31.5, 31.2, 31.6 us at 0 to 4.
+// 1560 keys take 42.9, 34.6, 32.2, 31.8, 31.9 us at 0 to 4.
 constexpr int kUnitTiles = 3;
 constexpr int kMergeRows = 64;   // partials of one round of a merge
 
@@ -1148,7 +1153,7 @@ cudaError_t launch_ap(const AttendPages8Params& p, int sms, cudaStream_t st) {
     if (s.state[dev] != 1) return (cudaError_t)(-s.state[dev]);
   }
   // Two CTAs to an SM, but no more than the longest sequences could use (1 x 8000
-  // keys: 12.0 us with 128 CTAs, 12.5 with 304).
+  // keys: 12.1 us with 128 CTAs, 12.5 with 304; 16 of up to 300: 7.9 and 8.5).
   const int64_t parts = ((p.max_keys - 1) / C::TILE_KEYS + kMinTiles) / kMinTiles;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)std::min<int64_t>(2 * sms, parts * p.batch * p.pool.n_kv));

@@ -23,7 +23,7 @@
 // Measured (one call among others in a graph; 6.8 TB/s is a plain copy's rate):
 // 256 x 50257 fp32 logits with a fifth masked, top 20: 17.6 us (2.9 TB/s), with
 // no alternatives 13 us (4.0 TB/s), all but 50 masked 23 us, rising along the row
-// 80 us; 256 x 128256 bf16, top 5: 19.7 us (3.3 TB/s); 4 x 128256: 5.3 us.  About
+// 84 us; 256 x 128256 bf16, top 5: 19.7 us (3.3 TB/s); 4 x 128256: 5.3 us.  About
 // 5 us of a call are launch, first loads and the join of a row's CTAs, 5 us more
 // the bound and the lists: at these sizes every CTA runs at once, so no logits
 // stream meanwhile.
@@ -33,8 +33,8 @@ namespace c2kv {
 
 namespace {
 
-// 512 threads take 1.2 us off 256 rows and add 1 us to 4 rows; steps of 4 vectors
-// with the next ones loaded ahead add 4 us to 256 rows.
+// 512 threads took 1.2 us off 256 rows and added 1 us to 4 rows, steps of 4 vectors
+// with the next ones loaded ahead added 4 us to 256 rows (on an earlier form).
 constexpr int LP_THREADS = 256;
 constexpr int LP_WARPS = LP_THREADS / 32;
 constexpr int LP_VECS = 8;                            // 16-byte loads of a thread
@@ -577,8 +577,8 @@ cudaError_t launch_lp(LogprobParams p, int sms, cudaStream_t st) {
     if (s.state[dev] != 1) return (cudaError_t)(-s.state[dev]);
   }
   // Two CTAs for each SM where the rows are fewer, but at least two vectors for
-  // each thread and at most 16 CTAs to a row (256 x 50257 fp32: 19.8 us with half
-  // as many CTAs, 17.9 so, 21 with twice as many).
+  // each thread and at most 16 CTAs to a row (256 x 50257 fp32: 21.2 us with half
+  // as many CTAs, 17.6 so, 21.2 with twice as many).
   const int64_t nvec = p.vocab / Vec<T>::N;
   int cs = 1;
   while (cs < LP_MAX_CLUSTER && (int64_t)p.rows * cs < 2 * sms && nvec >= (int64_t)cs * 4 * LP_THREADS) cs *= 2;

@@ -20,8 +20,8 @@
 // (1.57 GB) 224 us, 7.0 TB/s (a plain copy: 6.8).  Append is bound by the
 // rotation and by latency: the two halves of a pair must round as the exact
 // values do, which costs a test for each and cos/sin in two parts, 1 KB of table
-// for each token of each kv head (from L2).  1 x 4000 tokens 11.6 us (28 MB), 8
-// ragged sequences of up to 128 7.6 us, 16 x 1 4.8 us, which is a launch and four
+// for each token of each kv head (from L2).  1 x 4000 tokens 11.5 us (28 MB), 8
+// ragged sequences of up to 128 7.5 us, 16 x 1 4.9 us, which is a launch and four
 // dependent reads.
 #include "pages8.h"
 
@@ -70,7 +70,7 @@ __device__ __forceinline__ void tame(uint32_t& w, uint32_t& m) {
 
 // D: head_dim.  APPEND: rows [n_cached, n_cached + new) from the new tokens,
 // K rotated; else rows [0, n_rows) from the bf16 caches.
-// CTAs per SM: append takes 12.1 us at 2 and 13.2 at 3 for 1 x 4000 tokens
+// CTAs per SM: append takes 11.5 us at 2 and 12.4 at 3 for 1 x 4000 tokens
 // (registers for the rows in flight); fill is fastest at 3.
 template <int D, bool APPEND>
 __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 : 3) put_kernel(const __grid_constant__ PutParams p) {

@@ -27,7 +27,8 @@ class RequestBatch:
     """Device state of `len(requests)` composed requests sharing one store.
 
     page8: tokens of a page (16, 32, 64 or 128) to decode over an 8-bit paged
-    cache, half the bytes of the bf16 one: after composition and question
+    cache, which reads half the bytes of the bf16 one (that stays allocated beside
+    it: composition and prefill write there): after composition and question
     prefill, fill_pages8 takes the bf16 rows over, and decode appends to and
     attends over the pages.  `filled` holds the layers whose pages hold the rows
     (a program that writes pages by calls of its own adds to it); decode refuses
