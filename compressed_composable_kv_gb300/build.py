@@ -97,9 +97,11 @@ def _link_marshal():
     r = _run(["g++", "-shared", "-o", MARSHAL + ".tmp", os.path.join(BUILD, "marshal.o"), LIB, "-L", lib,
               "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN", "-Wl,-rpath," + lib])
     if r.returncode == 0:
+        if os.path.exists(MARSHAL + ".torch"):   # no tag while it may be another module's
+            os.remove(MARSHAL + ".torch")
+        os.replace(MARSHAL + ".tmp", MARSHAL)
         with open(MARSHAL + ".torch", "w") as f:
             f.write(_torch_tag())
-        os.replace(MARSHAL + ".tmp", MARSHAL)
     return r
 
 

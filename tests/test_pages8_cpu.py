@@ -312,3 +312,19 @@ def test_the_marshalling_module_belongs_to_one_torch(fake_build, monkeypatch, tm
     fake_build["ran"] = []
     build.build_library()
     assert build.up_to_date() and fake_build["ran"] == ["g++", "g++"]
+
+
+def test_a_marshalling_module_build_cut_short_is_not_taken_for_done(fake_build, monkeypatch):
+    build.build_library()
+    assert build.marshal_fits_torch()
+    real = build.os.replace
+
+    def cut(src, dst):
+        if dst == build.MARSHAL:
+            raise KeyboardInterrupt
+        real(src, dst)
+
+    monkeypatch.setattr(build.os, "replace", cut)
+    with pytest.raises(KeyboardInterrupt):
+        build.build_library(force=True)
+    assert not build.marshal_fits_torch()
