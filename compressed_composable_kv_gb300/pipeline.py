@@ -70,7 +70,11 @@ class RequestBatch:
         # request b's row r is row b * cap + r
         self.rope_table = torch.empty((self.batch, tb // 4), dtype=torch.float32, device=device)
         self.rope_tables = list(self.rope_table)
-        self.n_cached_dev = torch.zeros(self.batch, dtype=torch.int32, device=device)
+        # the lengths, and behind them the RoPE rows that go with them
+        self._lengths = torch.zeros((2, self.batch), dtype=torch.int32, device=device)
+        self.n_cached_dev, self._rope_row = self._lengths
+        self._own_lengths = self.n_cached_dev
+        self._rope_start = torch.arange(self.batch, dtype=torch.int32, device=device) * self.cap
         self.max_keys_decode = max(self.n_slots) + q_len + decode_steps
         ws = 256
         if q_len > 0:
@@ -87,19 +91,20 @@ class RequestBatch:
             self.v8 = torch.empty_like(self.k8)
             self.k_scale = torch.empty((L, n_pages, H), dtype=torch.float32, device=device)
             self.v_scale = torch.empty_like(self.k_scale)
-            self._rope_start = torch.arange(self.batch, dtype=torch.int32, device=device) * self.cap
             # of its own: the other calls' scratch would overwrite its counters
             self.workspace8 = torch.zeros(B.c2kv_attend_pages8_workspace_size(geom, self.batch, self.max_keys_decode),
                                           dtype=torch.uint8, device=device)
         self.workspace = torch.zeros(ws, dtype=torch.uint8, device=device)
         B.c2kv_workspace_init(self.workspace)
-        self._dec_start = torch.tensor([n + q_len for n in self.n_slots], dtype=torch.int32)
+        start = [n + q_len for n in self.n_slots]
+        self._dec_start = torch.tensor([start, [b * self.cap + n for b, n in enumerate(start)]], dtype=torch.int32)
 
     @property
     def rope_row_dev(self) -> torch.Tensor:
-        """Each request's row of rope_table for its next token, from the lengths as they are."""
-        start = torch.arange(self.batch, dtype=torch.int32, device=self.n_cached_dev.device) * self.cap
-        return start + self.n_cached_dev
+        """Each request's row of rope_table for its next token, from the lengths
+        as they are (on the current stream).  The same tensor each time; it moves
+        with reset_decode and advance.  decode does not need it."""
+        return torch.add(self._rope_start, self.n_cached_dev, out=self._rope_row)
 
     def compose(self, stream=None) -> None:
         self.compose_layers(0, self.geom.n_layers, stream)
@@ -140,7 +145,10 @@ class RequestBatch:
         """Point the device lengths at the first decode step (after the question)."""
         s = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(s):
-            self.n_cached_dev.copy_(self._dec_start, non_blocking=True)
+            if self.n_cached_dev is self._own_lengths:
+                self._lengths.copy_(self._dec_start, non_blocking=True)
+            else:   # a program's own tensor
+                self.n_cached_dev.copy_(self._dec_start[0], non_blocking=True)
 
     def fill_pages8(self, layer_begin: int = 0, layer_end: Optional[int] = None, stream=None) -> None:
         """The composed and prefilled rows of layers [layer_begin, layer_end) to the 8-bit pages."""
@@ -177,7 +185,8 @@ class RequestBatch:
                              stream, flags)
 
     def advance(self, stream=None) -> None:
-        B.c2kv_seq_advance(self.n_cached_dev, 1, stream)
+        own = self.n_cached_dev is self._own_lengths
+        B.c2kv_seq_advance(self._lengths if own else self.n_cached_dev, 1, stream)
 
 
 class DecoderModel:

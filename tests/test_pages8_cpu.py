@@ -328,3 +328,32 @@ def test_a_marshalling_module_build_cut_short_is_not_taken_for_done(fake_build, 
     with pytest.raises(KeyboardInterrupt):
         build.build_library(force=True)
     assert not build.marshal_fits_torch()
+
+
+def test_rope_rows_kept_by_a_program_follow_the_batch(paged_batch, P, monkeypatch):
+    """A tensor taken from rope_row_dev once moves with reset_decode and
+    advance; lengths that the program moves, or puts in place of the batch's,
+    show when the rows are next asked for."""
+    rb, _, _ = paged_batch
+
+    class Here:   # the host has no streams
+        def __init__(self, *a): pass
+        def __enter__(self): pass
+        def __exit__(self, *a): pass
+
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: None)
+    monkeypatch.setattr(torch.cuda, "stream", Here)
+    monkeypatch.setattr(P.pipeline.B, "c2kv_seq_advance", lambda t, d, s: t.add_(d))
+    row = rb.rope_row_dev
+    assert row.tolist() == [0, rb.cap]
+    rb.reset_decode()
+    assert rb.n_cached_dev.tolist() == [13, 13] and row.tolist() == [13, rb.cap + 13]
+    rb.advance()
+    assert rb.n_cached_dev.tolist() == [14, 14] and row.tolist() == [14, rb.cap + 14]
+    rb.n_cached_dev.sub_(1)
+    assert rb.rope_row_dev.tolist() == [13, rb.cap + 13]
+    rb.n_cached_dev = torch.tensor([3, 5], dtype=torch.int32)
+    rb.advance()
+    assert rb.n_cached_dev.tolist() == [4, 6] and rb.rope_row_dev.tolist() == [4, rb.cap + 6]
+    rb.reset_decode()
+    assert rb.n_cached_dev.tolist() == [13, 13]
