@@ -88,6 +88,12 @@ _SIGNATURES = {
     "c2kv_attend_pages8_workspace_size": (_sz, [_pg, _i32, _i32]),
     "c2kv_attend_pages8": (_i32, [_pg, _pp, _i32, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _vp,
                                   _vp, _sz, ctypes.c_uint32, _vp]),
+    "c2kv_attend_pages8_chunk_workspace_size": (_sz, [_pg, _i32, _i32, _i32]),
+    "c2kv_attend_pages8_chunk": (_i32, [_pg, _pp, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp, _i32,
+                                        _vp, _vp, _vp, _sz, ctypes.c_uint32, _vp]),
+    "c2kv_pages8_plan_workspace_size": (_sz, [_i32, _i32, _i32]),
+    "c2kv_pages8_fork": (_i32, [_pg, _pp, _i32, _vp, _i32, _vp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "c2kv_pages8_compact": (_i32, [_pg, _pp, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
     "c2kv_token_logprobs": (_i32, [_vp, _i32, _i32, _i32, ctypes.c_int64, _vp, _i32, _vp, _vp, _vp, _vp, _vp]),
 }
 
@@ -590,6 +596,59 @@ def c2kv_attend_pages8(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_s
         geom.n_layers, geom.n_q_heads, geom.n_kv_heads, geom.head_dim, geom.rope_theta, dev, k8, v8, k_scale,
         v_scale, page_table, layer, n_cached_dev, max_keys, q, k_new, v_new, rope_table, rope_row_dev, out,
         workspace, flags, _launch_stream(stream, dev)))
+
+
+def c2kv_attend_pages8_chunk_workspace_size(geom, batch: int, t_len: int, max_keys: int) -> int:
+    g = as_geometry(geom)
+    return int(load_library().c2kv_attend_pages8_chunk_workspace_size(ctypes.byref(g), int(batch), int(t_len),
+                                                                      int(max_keys)))
+
+
+def c2kv_attend_pages8_chunk(geom, layer: int, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor,
+                             v_scale: torch.Tensor, page_table: torch.Tensor, n_cached_dev: torch.Tensor,
+                             max_keys: int, q: torch.Tensor, k_new: Optional[torch.Tensor],
+                             v_new: Optional[torch.Tensor], rope_table: torch.Tensor, rope_row_dev: torch.Tensor,
+                             out: torch.Tensor, workspace: torch.Tensor, n_new_dev: Optional[torch.Tensor] = None,
+                             stream=None, flags: int = 0) -> None:
+    """Appends k_new, v_new [batch][t_len][n_kv_heads][head_dim] to 8-bit pages
+    and attends with q [batch][t_len][n_q_heads][head_dim], each token over the
+    rows up to its own (k_new, v_new None: the tokens' rows are held already);
+    n_new_dev: int32 [batch] tokens of a padded batch."""
+    dev = k8.get_device()
+    _check((_marshal_module or _load_marshal()).attend_pages8_chunk(
+        geom.n_layers, geom.n_q_heads, geom.n_kv_heads, geom.head_dim, geom.rope_theta, dev, k8, v8, k_scale,
+        v_scale, page_table, layer, n_cached_dev, n_new_dev, max_keys, q, k_new, v_new, rope_table, rope_row_dev, out,
+        workspace, flags, _launch_stream(stream, dev)))
+
+
+def c2kv_pages8_plan_workspace_size(n_pages: int, batch: int, max_pages: int) -> int:
+    return int(load_library().c2kv_pages8_plan_workspace_size(int(n_pages), int(batch), int(max_pages)))
+
+
+def c2kv_pages8_fork(geom, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                     refs: torch.Tensor, page_table: torch.Tensor, n_cached_dev: torch.Tensor,
+                     parent_dev: torch.Tensor, room: int, refs_out: torch.Tensor, page_table_out: torch.Tensor,
+                     n_cached_out: torch.Tensor, workspace: torch.Tensor, stream=None) -> None:
+    """A new batch of sequences on the pool's pages: place i goes on with
+    sequence parent_dev[i] (negative: none) and has room for `room` more tokens.
+    refs: int32 [n_pages] sequences that hold each page; outputs may be inputs."""
+    dev = k8.get_device()
+    _check((_marshal_module or _load_marshal()).pages8_fork(
+        geom.n_layers, geom.n_q_heads, geom.n_kv_heads, geom.head_dim, geom.rope_theta, dev, k8, v8, k_scale,
+        v_scale, page_table, n_cached_dev, parent_dev, room, refs, refs_out, page_table_out, n_cached_out, workspace,
+        _launch_stream(stream, dev)))
+
+
+def c2kv_pages8_compact(geom, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                        refs: torch.Tensor, page_table: torch.Tensor, refs_out: torch.Tensor,
+                        page_table_out: torch.Tensor, moved_out: Optional[torch.Tensor], workspace: torch.Tensor,
+                        stream=None) -> None:
+    """Moves the pages in use to the front of the pool; moved_out: int32
+    [n_pages], the new index of each page (-1: free).  Outputs may be inputs."""
+    dev = k8.get_device()
+    _check((_marshal_module or _load_marshal()).pages8_compact(
+        geom.n_layers, geom.n_q_heads, geom.n_kv_heads, geom.head_dim, geom.rope_theta, dev, k8, v8, k_scale,
+        v_scale, page_table, refs, refs_out, page_table_out, moved_out, workspace, _launch_stream(stream, dev)))
 
 
 def c2kv_token_logprobs(logits: torch.Tensor, tokens: Optional[torch.Tensor], top_k: int,

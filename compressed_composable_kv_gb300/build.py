@@ -24,7 +24,8 @@ LIB = os.path.join(BUILD, "libc2kv.so")
 MARSHAL = os.path.join(BUILD, "_marshal.so")
 
 SOURCES = ["api.cu", "rope.cu", "attn.cu", "prefill_tc.cu", "decode_tc.cu", "linear_tc.cu",
-           "api_pages8.cu", "pages8.cu", "attend_pages8.cu", "logprobs.cu"]
+           "api_pages8.cu", "pages8.cu", "attend_pages8.cu", "attend_chunk8.cu",
+           "pages8_move.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

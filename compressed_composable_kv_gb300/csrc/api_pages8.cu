@@ -1,5 +1,5 @@
 // C ABI of the 8-bit paged cache and of the token log probabilities: argument
-// checks on the host, then one launch.  See include/c2kv.h for each call.
+// checks on the host, then its launches.  See include/c2kv.h for each call.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -69,6 +69,65 @@ AttendWs attend_workspace(const c2kv_geometry* g, int sms) {
   return w;
 }
 
+// An append's arguments, k_new and v_new apart from their alignment.
+c2kv_status append_params(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
+                          int32_t t_len, const int32_t* page_table, int32_t max_pages, const int32_t* n_cached_dev,
+                          const int32_t* n_new_dev, const void* k_new, const void* v_new, const void* rope_table,
+                          int32_t table_rows, const int32_t* rope_row_dev, PutParams* p) {
+  std::memset(p, 0, sizeof(*p));
+  c2kv_status s = check_pages(geom, pages, layer, page_table, max_pages, &p->pool);
+  if (s != C2KV_OK) return s;
+  s = check_new_tokens(batch, n_cached_dev, k_new, v_new, rope_table, table_rows, rope_row_dev);
+  if (s != C2KV_OK) return s;
+  if ((int64_t)batch * geom->n_kv_heads > 65535) return api_fail(C2KV_EINVAL, "batch * n_kv_heads must be below 65536");
+  if (t_len < 1 || t_len > INT32_MAX / 2) return api_fail(C2KV_EINVAL, "t_len must be >= 1");
+  if (t_len > max_pages * pages->page) return api_fail(C2KV_ECAPACITY, "t_len exceeds max_pages * page");
+  p->page_table = page_table;
+  p->max_pages = max_pages;
+  p->batch = batch;
+  p->n_layers = 1;
+  p->fresh[0] = static_cast<const __nv_bfloat16*>(k_new);
+  p->fresh[1] = static_cast<const __nv_bfloat16*>(v_new);
+  p->n_cached = n_cached_dev;
+  p->n_new = n_new_dev;
+  p->tab = static_cast<const CosSin2*>(rope_table);
+  p->rope_row = rope_row_dev;
+  p->t_len = t_len;
+  p->table_rows = table_rows;
+  p->max_rows = max_pages * pages->page;
+  return C2KV_OK;
+}
+
+// The checks that the calls on a pool's pages share, then their two launches.
+c2kv_status move_pages(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t batch, const int32_t* page_table,
+                       int32_t max_pages, const int32_t* refs, int32_t* refs_out, int32_t* page_table_out,
+                       void* workspace, size_t workspace_bytes, const char* what, cudaStream_t st, MoveParams* p) {
+  c2kv_status s = check_pages(geom, pages, 0, page_table, max_pages, &p->pool);
+  if (s != C2KV_OK) return s;
+  if (batch < 1 || batch > kMaxPagedSeqs) return api_fail(C2KV_EINVAL, "batch must be in [1, 256]");
+  if (geom->n_layers > 32767) return api_fail(C2KV_EINVAL, "n_layers must be below 32768");
+  if (!refs || !refs_out || !page_table_out || !workspace) return api_fail(C2KV_EINVAL, "null pointer");
+  if (workspace_bytes < c2kv_pages8_plan_workspace_size(pages->n_pages, std::max(batch, p->batch_out), max_pages) ||
+      !aligned(workspace, 16))
+    return api_fail(C2KV_EINVAL, "workspace too small or not 16-byte aligned");
+  int sms = 0;
+  s = api_device_state(&p->err, &sms);
+  if (s != C2KV_OK) return s;
+  p->scale_layer = (int64_t)pages->n_pages * geom->n_kv_heads;
+  p->code_layer = p->scale_layer * pages->page * geom->head_dim;
+  p->page_table = page_table;
+  p->refs = refs;
+  p->refs_out = refs_out;
+  p->page_table_out = page_table_out;
+  p->ws = static_cast<int32_t*>(workspace);
+  p->batch = batch;
+  p->max_pages = max_pages;
+  p->n_layers = geom->n_layers;
+  s = api_launched(launch_pages8_plan(*p, st), what);
+  if (s != C2KV_OK) return s;
+  return api_launched(launch_pages8_move(*p, geom->head_dim, sms, st), what);
+}
+
 }  // namespace
 
 extern "C" {
@@ -119,29 +178,12 @@ c2kv_status c2kv_pages8_append(const c2kv_geometry* geom, const c2kv_pages8* pag
                                const void* v_new, const void* rope_table, int32_t table_rows,
                                const int32_t* rope_row_dev, void* stream) {
   PutParams p;
-  std::memset(&p, 0, sizeof(p));
-  c2kv_status s = check_pages(geom, pages, layer, page_table, max_pages, &p.pool);
-  if (s != C2KV_OK) return s;
-  s = check_new_tokens(batch, n_cached_dev, k_new, v_new, rope_table, table_rows, rope_row_dev);
+  c2kv_status s = append_params(geom, pages, layer, batch, t_len, page_table, max_pages, n_cached_dev, n_new_dev, k_new,
+                                v_new, rope_table, table_rows, rope_row_dev, &p);
   if (s != C2KV_OK) return s;
   if (!k_new || !v_new) return api_fail(C2KV_EINVAL, "null pointer");
-  if ((int64_t)batch * geom->n_kv_heads > 65535) return api_fail(C2KV_EINVAL, "batch * n_kv_heads must be below 65536");
-  if (t_len < 1 || t_len > INT32_MAX / 2) return api_fail(C2KV_EINVAL, "t_len must be >= 1");
-  if (t_len > max_pages * pages->page) return api_fail(C2KV_ECAPACITY, "t_len exceeds max_pages * page");
   s = api_device_state(&p.err, nullptr);
   if (s != C2KV_OK) return s;
-  p.page_table = page_table;
-  p.max_pages = max_pages;
-  p.batch = batch;
-  p.n_layers = 1;
-  p.fresh[0] = static_cast<const __nv_bfloat16*>(k_new);
-  p.fresh[1] = static_cast<const __nv_bfloat16*>(v_new);
-  p.n_cached = n_cached_dev;
-  p.n_new = n_new_dev;
-  p.tab = static_cast<const CosSin2*>(rope_table);
-  p.rope_row = rope_row_dev;
-  p.t_len = t_len;
-  p.table_rows = table_rows;
   return api_launched(launch_pages8_append(p, geom->head_dim, static_cast<cudaStream_t>(stream)),
                       "c2kv_pages8_append");
 }
@@ -208,6 +250,99 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
   return api_launched(launch_attend_pages8(p, geom->head_dim, geom->n_q_heads / geom->n_kv_heads, sms,
                                            static_cast<cudaStream_t>(stream)),
                       "c2kv_attend_pages8");
+}
+
+size_t c2kv_attend_pages8_chunk_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t t_len,
+                                               int32_t max_keys) {
+  if (api_check_geom(geom) != C2KV_OK || batch < 1 || batch > kMaxPagedSeqs || t_len < 1 || max_keys < 1) return 0;
+  return 16;
+}
+
+c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
+                                     int32_t t_len, const int32_t* page_table, int32_t max_pages,
+                                     const int32_t* n_cached_dev, const int32_t* n_new_dev, int32_t max_keys,
+                                     const void* q, const void* k_new, const void* v_new, const void* rope_table,
+                                     int32_t table_rows, const int32_t* rope_row_dev, void* out, void* workspace,
+                                     size_t workspace_bytes, uint32_t flags, void* stream) {
+  if (flags & ~uint32_t(C2KV_DECODE_ROW_AT_LENGTH)) return api_fail(C2KV_EINVAL, "unknown flags for a chunk");
+  PutParams put;
+  c2kv_status s = append_params(geom, pages, layer, batch, t_len, page_table, max_pages, n_cached_dev, n_new_dev, k_new,
+                                v_new, rope_table, table_rows, rope_row_dev, &put);
+  if (s != C2KV_OK) return s;
+  if (!q || !out || !workspace) return api_fail(C2KV_EINVAL, "null pointer");
+  if ((k_new == nullptr) != (v_new == nullptr)) return api_fail(C2KV_EINVAL, "k_new and v_new go together");
+  if (!aligned(q, 16) || !aligned(out, 16)) return api_fail(C2KV_EINVAL, "q and out must be 16-byte aligned");
+  if (max_keys < 1 || max_keys > max_pages * pages->page)
+    return api_fail(C2KV_EINVAL, "max_keys must be in [1, max_pages * page]");
+  if (workspace_bytes < c2kv_attend_pages8_chunk_workspace_size(geom, batch, t_len, max_keys) || !aligned(workspace, 16))
+    return api_fail(C2KV_EINVAL, "workspace too small or not 16-byte aligned");
+  int sms = 0;
+  s = api_device_state(&put.err, &sms);
+  if (s != C2KV_OK) return s;
+  put.max_rows = max_keys;
+  put.row_at_length = (flags & C2KV_DECODE_ROW_AT_LENGTH) != 0 ? 1 : 0;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (k_new) {
+    s = api_launched(launch_pages8_append(put, geom->head_dim, st), "c2kv_attend_pages8_chunk");
+    if (s != C2KV_OK) return s;
+  }
+  ChunkParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.pool = put.pool;
+  p.page_table = page_table;
+  p.n_cached = n_cached_dev;
+  p.n_new = n_new_dev;
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.tab = put.tab;
+  p.rope_row = rope_row_dev;
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.err = put.err;
+  p.batch = batch;
+  p.t_len = t_len;
+  p.n_q = geom->n_q_heads;
+  p.max_pages = max_pages;
+  p.max_keys = max_keys;
+  p.table_rows = table_rows;
+  p.row_at_length = put.row_at_length;
+  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)geom->head_dim));
+  return api_launched(launch_attend_chunk8(p, geom->head_dim, geom->n_q_heads / geom->n_kv_heads, sms, st),
+                      "c2kv_attend_pages8_chunk");
+}
+
+size_t c2kv_pages8_plan_workspace_size(int32_t n_pages, int32_t batch, int32_t max_pages) {
+  if (n_pages < 1 || batch < 1 || batch > kMaxPagedSeqs || max_pages < 1) return 0;
+  return move_workspace_ints(n_pages, batch, max_pages) * sizeof(int32_t);
+}
+
+c2kv_status c2kv_pages8_fork(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t batch,
+                             const int32_t* page_table, int32_t max_pages, const int32_t* n_cached_dev,
+                             int32_t batch_out, const int32_t* parent_dev, int32_t room, const int32_t* refs,
+                             int32_t* refs_out, int32_t* page_table_out, int32_t* n_cached_out, void* workspace,
+                             size_t workspace_bytes, void* stream) {
+  if (!n_cached_dev || !parent_dev || !n_cached_out) return api_fail(C2KV_EINVAL, "null pointer");
+  if (batch_out < 1 || batch_out > kMaxPagedSeqs) return api_fail(C2KV_EINVAL, "batch_out must be in [1, 256]");
+  if (room < 0 || room > INT32_MAX / 4) return api_fail(C2KV_EINVAL, "room must be in [0, 2^29)");
+  MoveParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.n_cached = n_cached_dev;
+  p.parent = parent_dev;
+  p.n_cached_out = n_cached_out;
+  p.batch_out = batch_out;
+  p.room = room;
+  return move_pages(geom, pages, batch, page_table, max_pages, refs, refs_out, page_table_out, workspace,
+                    workspace_bytes, "c2kv_pages8_fork", static_cast<cudaStream_t>(stream), &p);
+}
+
+c2kv_status c2kv_pages8_compact(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t batch,
+                                const int32_t* page_table, int32_t max_pages, const int32_t* refs, int32_t* refs_out,
+                                int32_t* page_table_out, int32_t* moved_out, void* workspace, size_t workspace_bytes,
+                                void* stream) {
+  MoveParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.moved_out = moved_out;
+  p.batch_out = batch;
+  return move_pages(geom, pages, batch, page_table, max_pages, refs, refs_out, page_table_out, workspace,
+                    workspace_bytes, "c2kv_pages8_compact", static_cast<cudaStream_t>(stream), &p);
 }
 
 c2kv_status c2kv_token_logprobs(const void* logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,

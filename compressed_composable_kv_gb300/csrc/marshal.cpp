@@ -219,6 +219,79 @@ PyObject* attend_pages8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// attend_pages8_chunk(pages..., layer, n_cached, n_new, max_keys, q, k_new, v_new, rope_table, rope_row, out, workspace,
+//                     flags, stream)
+PyObject* attend_pages8_chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, kPagesArgs + 13, [&]() -> PyObject* {
+    PyObject* const* r = a + kPagesArgs;
+    const at::Tensor& q = tensor(r[4], "q");
+    if (q.dim() != 4 || q.size(0) > INT32_MAX || q.size(1) > INT32_MAX)
+      throw Bad("q must be [batch][t_len][n_q_heads][head_dim]");
+    const int64_t batch = q.size(0), t_len = q.size(1);
+    const Pages p(a, batch);
+    const int64_t hq = p.g.n_q_heads, h = p.g.n_kv_heads, d = p.g.head_dim;
+    void *rope, *ws;
+    const int32_t rows = p.rope_rows(r[7], &rope);
+    const size_t ws_bytes = bytes(r[10], "workspace", p.dev, &ws);
+    return status(c2kv_attend_pages8_chunk(
+        &p.g, &p.pages, as_int32(r[0], "layer"), (int32_t)batch, (int32_t)t_len, p.table, p.max_pages,
+        (const int32_t*)address(r[1], "n_cached_dev", at::kInt, {batch}, p.dev),
+        (const int32_t*)optional(r[2], "n_new_dev", at::kInt, {batch}, p.dev), as_int32(r[3], "max_keys"),
+        address(r[4], "q", at::kBFloat16, {batch, t_len, hq, d}, p.dev),
+        optional(r[5], "k_new", at::kBFloat16, {batch, t_len, h, d}, p.dev),
+        optional(r[6], "v_new", at::kBFloat16, {batch, t_len, h, d}, p.dev), rope, rows,
+        (const int32_t*)address(r[8], "rope_row_dev", at::kInt, {batch}, p.dev),
+        address(r[9], "out", at::kBFloat16, {batch, t_len, hq, d}, p.dev), ws, ws_bytes,
+        (uint32_t)as_int32(r[11], "flags"), (void*)as_int(r[12])));
+  });
+}
+
+// The batch of a page table among the arguments (argument 10).
+int64_t table_rows(PyObject* const* a) {
+  const at::Tensor& t = tensor(a[kPagesArgs - 1], "page_table");
+  if (t.dim() != 2 || t.size(0) > INT32_MAX) throw Bad("page_table must be [batch][max_pages]");
+  return t.size(0);
+}
+
+// pages8_fork(pages..., n_cached, parent, room, refs, refs_out, page_table_out, n_cached_out, workspace, stream)
+PyObject* pages8_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, kPagesArgs + 9, [&]() -> PyObject* {
+    PyObject* const* r = a + kPagesArgs;
+    const int64_t batch = table_rows(a);
+    const Pages p(a, batch);
+    const at::Tensor& parent = tensor(r[1], "parent_dev");
+    if (parent.dim() != 1 || parent.size(0) > INT32_MAX) throw Bad("parent_dev must be [batch_out]");
+    const int64_t out = parent.size(0);
+    void* ws;
+    const size_t ws_bytes = bytes(r[7], "workspace", p.dev, &ws);
+    return status(c2kv_pages8_fork(
+        &p.g, &p.pages, (int32_t)batch, p.table, p.max_pages,
+        (const int32_t*)address(r[0], "n_cached_dev", at::kInt, {batch}, p.dev), (int32_t)out,
+        (const int32_t*)address(r[1], "parent_dev", at::kInt, {out}, p.dev), as_int32(r[2], "room"),
+        (const int32_t*)address(r[3], "refs", at::kInt, {p.pages.n_pages}, p.dev),
+        (int32_t*)address(r[4], "refs_out", at::kInt, {p.pages.n_pages}, p.dev),
+        (int32_t*)address(r[5], "page_table_out", at::kInt, {out, p.max_pages}, p.dev),
+        (int32_t*)address(r[6], "n_cached_out", at::kInt, {out}, p.dev), ws, ws_bytes, (void*)as_int(r[8])));
+  });
+}
+
+// pages8_compact(pages..., refs, refs_out, page_table_out, moved_out, workspace, stream)
+PyObject* pages8_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, kPagesArgs + 6, [&]() -> PyObject* {
+    PyObject* const* r = a + kPagesArgs;
+    const int64_t batch = table_rows(a);
+    const Pages p(a, batch);
+    void* ws;
+    const size_t ws_bytes = bytes(r[4], "workspace", p.dev, &ws);
+    return status(c2kv_pages8_compact(
+        &p.g, &p.pages, (int32_t)batch, p.table, p.max_pages,
+        (const int32_t*)address(r[0], "refs", at::kInt, {p.pages.n_pages}, p.dev),
+        (int32_t*)address(r[1], "refs_out", at::kInt, {p.pages.n_pages}, p.dev),
+        (int32_t*)address(r[2], "page_table_out", at::kInt, {batch, p.max_pages}, p.dev),
+        (int32_t*)optional(r[3], "moved_out", at::kInt, {p.pages.n_pages}, p.dev), ws, ws_bytes, (void*)as_int(r[5])));
+  });
+}
+
 // token_logprobs(device, logits, tokens, top_k, logprob, entropy, top_ids, top_logprobs, stream)
 PyObject* token_logprobs(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 9, [&]() -> PyObject* {
@@ -247,6 +320,9 @@ PyMethodDef methods[] = {
     {"pages8_fill", (PyCFunction)(void (*)(void))pages8_fill, METH_FASTCALL, nullptr},
     {"pages8_append", (PyCFunction)(void (*)(void))pages8_append, METH_FASTCALL, nullptr},
     {"attend_pages8", (PyCFunction)(void (*)(void))attend_pages8, METH_FASTCALL, nullptr},
+    {"attend_pages8_chunk", (PyCFunction)(void (*)(void))attend_pages8_chunk, METH_FASTCALL, nullptr},
+    {"pages8_fork", (PyCFunction)(void (*)(void))pages8_fork, METH_FASTCALL, nullptr},
+    {"pages8_compact", (PyCFunction)(void (*)(void))pages8_compact, METH_FASTCALL, nullptr},
     {"token_logprobs", (PyCFunction)(void (*)(void))token_logprobs, METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 

@@ -89,13 +89,14 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   if (APPEND) {
     first = p.n_cached[b];
     count = p.n_new ? p.n_new[b] : p.t_len;
-    rr = p.rope_row[b];
+    const int64_t row = (int64_t)p.rope_row[b] + (p.row_at_length ? first : 0);
     if (first < 0) return;   // an empty place of the batch
-    if (count < 0 || count > p.t_len || (int64_t)first + count > (int64_t)p.max_pages * p.pool.page ||
-        (count > 0 && (rr < 0 || (int64_t)rr + count > p.table_rows))) {
+    if (count < 0 || count > p.t_len || (int64_t)first + count > p.max_rows ||
+        (count > 0 && (row < 0 || row + count > p.table_rows))) {
       if (threadIdx.x == 0) atomicOr(p.err, kErrLength);
       return;
     }
+    rr = (int)row;
   } else {
     count = p.n_rows[b];
   }

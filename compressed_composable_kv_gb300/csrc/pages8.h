@@ -95,6 +95,41 @@ struct PutParams {
   const CosSin2* tab;
   const int32_t* rope_row;
   int32_t t_len, table_rows;
+  int32_t row_at_length;         // token i's table row is rope_row + n_cached + i
+  int32_t max_rows;              // a sequence that would get more is left out
+};
+
+// A chunk of new tokens over the pages (attend_chunk8.cu): token i of sequence
+// b, i < n_new[b], sees rows [0, n_cached[b] + i].
+struct ChunkParams {
+  PagePool pool;
+  const int32_t* page_table;
+  const int32_t* n_cached;
+  const int32_t* n_new;          // null: t_len each
+  const __nv_bfloat16* q;        // [batch][t_len][n_q][d], before RoPE
+  const CosSin2* tab;
+  const int32_t* rope_row;
+  __nv_bfloat16* out;            // [batch][t_len][n_q][d]
+  unsigned* err;
+  int32_t batch, t_len, n_q, max_pages, max_keys, table_rows, row_at_length;
+  float scale_log2;
+};
+
+// What becomes of a pool's pages (pages8_move.cu).  `n_cached` null: compact.
+struct MoveParams {
+  PagePool pool;                 // of layer 0
+  int64_t code_layer, scale_layer;   // bytes of codes, scales, from one layer to the next
+  const int32_t* page_table;     // [batch][max_pages]
+  const int32_t* refs;           // [n_pages]
+  const int32_t* n_cached;       // [batch]
+  const int32_t* parent;         // [batch_out]
+  int32_t* refs_out;
+  int32_t* page_table_out;       // [batch_out][max_pages]
+  int32_t* n_cached_out;         // [batch_out]
+  int32_t* moved_out;            // [n_pages] or null
+  int32_t* ws;                   // move_workspace_ints
+  unsigned* err;
+  int32_t batch, batch_out, max_pages, room, n_layers;
 };
 
 // One decode step over the pages of `batch` sequences (attend_pages8.cu).
@@ -147,6 +182,10 @@ __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.la
 cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, cudaStream_t st);
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st);
 cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, cudaStream_t st);
+cudaError_t launch_attend_chunk8(const ChunkParams& p, int head_dim, int group, int sms, cudaStream_t st);
+size_t move_workspace_ints(int n_pages, int batch, int max_pages);
+cudaError_t launch_pages8_plan(const MoveParams& p, cudaStream_t st);
+cudaError_t launch_pages8_move(const MoveParams& p, int head_dim, int sms, cudaStream_t st);
 cudaError_t launch_token_logprobs(const LogprobParams& p, int sms, cudaStream_t st);
 
 // What the entry points of another translation unit share with api.cu.

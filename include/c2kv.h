@@ -528,6 +528,82 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
                                void* workspace, size_t workspace_bytes, uint32_t flags, void* stream);
 
 /*
+ * Attention of a chunk of new tokens of one layer over the pages, their append
+ * included: a further question on a composed cache, drafted tokens checked at
+ * once, a document taken in piece by piece ([EXPL] "pipeline": what is asked
+ * goes behind the composed cache).  As c2kv_pages8_append, then for token i of
+ * sequence b, i < n_new_dev[b], with q_bi rotated by the token's table row,
+ * out[b][i] = softmax(q_bi K^T / sqrt(d)) V over rows [0, n_cached_dev[b] + i].
+ * k_new and v_new NULL: nothing is appended, the tokens' rows are held already.
+ * q, out: device bf16 [batch][t_len][n_q_heads][head_dim], 16-byte aligned;
+ * out behind a sequence's last new token is left as it was.  max_keys bounds
+ * n_cached_dev[b] + n_new_dev[b]; a sequence with more, or one that the append
+ * leaves out, is left out whole.  Rows on pages outside the pool are not
+ * attended over, and a token that sees no other row gets 0.  workspace:
+ * c2kv_attend_pages8_chunk_workspace_size bytes, 16-byte aligned, of any
+ * contents; calls that do not overlap on the GPU may share it, whatever their
+ * shapes.  flags: C2KV_DECODE_ROW_AT_LENGTH, for the append as well.  The
+ * queries are held to 11 bits, in fp16, and so are the softmax weights; sums
+ * are in fp32.  A query that is not finite gives NaN, a held NaN gives NaN to
+ * the tokens that see it.
+ */
+size_t c2kv_attend_pages8_chunk_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t t_len,
+                                               int32_t max_keys);
+c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
+                                     int32_t t_len, const int32_t* page_table, int32_t max_pages,
+                                     const int32_t* n_cached_dev, const int32_t* n_new_dev, int32_t max_keys,
+                                     const void* q, const void* k_new, const void* v_new, const void* rope_table,
+                                     int32_t table_rows, const int32_t* rope_row_dev, void* out, void* workspace,
+                                     size_t workspace_bytes, uint32_t flags, void* stream);
+
+/*
+ * The pages of a pool among its sequences.  refs: device int32 [n_pages], how
+ * many sequences hold a page, 0 where it is free.  For these two calls a row of
+ * page_table names all the pages that its sequence holds: its entries up to the
+ * first negative one.  All layers have one table; all layers are copied.
+ *
+ * c2kv_pages8_fork makes a new batch of batch_out sequences out of the old one
+ * of `batch`: place i goes on with sequence parent_dev[i] (negative, or a
+ * sequence with a length below 0: an empty place).  So it forks answers, moves
+ * and drops beams, ends sequences and takes pages for new tokens:
+ *   - A parent's full pages are shared by its children.  The first of them, by
+ *     place, keeps the others as well; the rest get a copy of the page that the
+ *     length ends in (its held rows), so that every page that will be written
+ *     to belongs to one sequence.
+ *   - Pages of sequences that no place goes on with are given back.
+ *   - Each sequence gets pages until it has room for its length and `room` more
+ *     tokens.  Pages are taken in the order of places and entries, the free page
+ *     of the lowest index first; what the call itself gives back is free.
+ * Written are refs_out, page_table_out [batch_out][max_pages] (entries behind
+ * the held pages -1) and n_cached_out [batch_out] (-1: empty); each may be the
+ * call's own input, else they must not overlap it.  A parent >= batch, an entry
+ * that names no page in use, a length beyond the pages held, more pages than
+ * max_pages for a sequence or than are free: C2KV_EDEVICE in the device error
+ * word, and nothing is written.
+ *
+ * c2kv_pages8_compact moves the U pages in use to indices [0, U): the i-th
+ * page in use of index >= U goes to the i-th free index, so a pool can be cut
+ * off there or a large run of pages be had.  Written are refs_out,
+ * page_table_out [batch][max_pages] (entries behind the held pages -1) and, if
+ * not NULL, moved_out [n_pages]: the new index of each page, -1 for free ones.
+ * Outputs may be inputs, and bad values end the call, as for the fork.
+ *
+ * batch, batch_out <= 256.  workspace: c2kv_pages8_plan_workspace_size bytes
+ * for the larger batch, 16-byte aligned, of any contents, shared by calls that
+ * do not overlap on the GPU.  Errors: C2KV_EINVAL, C2KV_ECUDA.
+ */
+size_t c2kv_pages8_plan_workspace_size(int32_t n_pages, int32_t batch, int32_t max_pages);
+c2kv_status c2kv_pages8_fork(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t batch,
+                             const int32_t* page_table, int32_t max_pages, const int32_t* n_cached_dev,
+                             int32_t batch_out, const int32_t* parent_dev, int32_t room, const int32_t* refs,
+                             int32_t* refs_out, int32_t* page_table_out, int32_t* n_cached_out, void* workspace,
+                             size_t workspace_bytes, void* stream);
+c2kv_status c2kv_pages8_compact(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t batch,
+                                const int32_t* page_table, int32_t max_pages, const int32_t* refs, int32_t* refs_out,
+                                int32_t* page_table_out, int32_t* moved_out, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/*
  * Log probabilities from logits x [rows][vocab] (device, C2KV_BF16 or
  * C2KV_F32, row_stride elements from one row to the next): for each row, with
  * m = max x and S = sum exp(x - m),

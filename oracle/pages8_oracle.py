@@ -95,6 +95,90 @@ def attend(q: np.ndarray, k: np.ndarray, v: np.ndarray) -> np.ndarray:
     return out
 
 
+def attend_chunk(q: np.ndarray, k: np.ndarray, v: np.ndarray, n: int) -> np.ndarray:
+    """q [t][q heads][d] rotated, token i at row n + i; k, v [kv head][n + t][d]
+    held values; out [t][q heads][d]."""
+    return np.stack([attend(q[i], k[:, :n + i + 1], v[:, :n + i + 1]) for i in range(q.shape[0])])
+
+
+def fork(refs, table, n_cached, parent, room: int, page: int):
+    """(refs, table, n_cached, copies) of the new batch; copies: (source page,
+    new page, rows).  None where the call has to end without writing."""
+    refs = [int(r) for r in refs]
+    held = []
+    for row in table:
+        pages = []
+        for e in row:
+            if e < 0:
+                break
+            pages.append(int(e))
+        held.append(pages)
+    width, batch = len(table[0]), len(table)
+    if any(r < 0 for r in refs) or any(p >= len(refs) or refs[p] < 1 for row in held for p in row):
+        return None
+    if any(p >= batch for p in parent) or any(n > len(h) * page for n, h in zip(n_cached, held)):
+        return None
+    out, new, firsts = list(refs), [], set()
+    for pages in held:
+        for p in pages:
+            out[p] -= 1
+    for r in parent:
+        if r < 0 or n_cached[r] < 0:
+            new.append(None)
+            continue
+        pages = list(held[r]) if r not in firsts else held[r][: n_cached[r] // page]
+        firsts.add(r)
+        for p in pages:
+            out[p] += 1
+        new.append(pages)
+    if any(c < 0 for c in out):
+        return None
+    free = [p for p, c in enumerate(out) if c == 0]
+    copies = []
+    for i, pages in enumerate(new):
+        if pages is None:
+            continue
+        n = int(n_cached[parent[i]])
+        if n % page and len(pages) == n // page:
+            if not free:
+                return None
+            copies.append((held[parent[i]][n // page], free[0], n % page))
+        while len(pages) * page < n + room:
+            if not free:
+                return None
+            out[free[0]] = 1
+            pages.append(free.pop(0))
+        if len(pages) > width:
+            return None
+    rows = [(pages or []) + [-1] * (width - len(pages or [])) for pages in new]
+    return out, rows, [-1 if pages is None else int(n_cached[parent[i]]) for i, pages in enumerate(new)], copies
+
+
+def compact(refs, table):
+    """(refs, table, moved, moves) or None; moves: (old page, new page)."""
+    used = [p for p, c in enumerate(refs) if c > 0]
+    holes = [p for p in range(len(used)) if refs[p] == 0]
+    moves = list(zip([p for p in used if p >= len(used)], holes))
+    to = {p: p for p in used}
+    to.update(moves)
+    out = [0] * len(refs)
+    for p in used:
+        out[to[p]] = int(refs[p])
+    rows = []
+    for row in table:
+        new = []
+        for e in row:
+            if e < 0:
+                break
+            if e >= len(refs) or refs[e] < 1:
+                return None
+            new.append(to[int(e)])
+        rows.append(new + [-1] * (len(row) - len(new)))
+    if any(c < 0 for c in refs):
+        return None
+    return out, rows, [to.get(p, -1) for p in range(len(refs))], moves
+
+
 def token_logprobs(x: np.ndarray, tokens, top_k: int):
     """(logprob, entropy, top_ids, top_logprobs) of logits x [rows][vocab]."""
     rows, vocab = x.shape
