@@ -69,6 +69,22 @@ AttendWs attend_workspace(const c2kv_geometry* g, int sms) {
   return w;
 }
 
+// Scratch of a chunk's attention: what is shared by whom, then two partial
+// results per CTA.
+struct ChunkWs {
+  size_t ml_off, o_off, total;
+};
+
+ChunkWs chunk_workspace(const c2kv_geometry* g, int t_len, int sms) {
+  const size_t ctas = std::min(sms, kMaxChunkCtas);
+  const size_t rows = 2 * ctas * chunk_part_rows(t_len, g->n_q_heads / g->n_kv_heads);
+  ChunkWs w;
+  w.ml_off = up256(ctas * 8 * sizeof(int32_t));
+  w.o_off = w.ml_off + up256(rows * sizeof(float2));
+  w.total = w.o_off + up256(rows * g->head_dim * sizeof(float));
+  return w;
+}
+
 // An append's arguments, k_new and v_new apart from their alignment.
 c2kv_status append_params(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
                           int32_t t_len, const int32_t* page_table, int32_t max_pages, const int32_t* n_cached_dev,
@@ -255,7 +271,7 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
 size_t c2kv_attend_pages8_chunk_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t t_len,
                                                int32_t max_keys) {
   if (api_check_geom(geom) != C2KV_OK || batch < 1 || batch > kMaxPagedSeqs || t_len < 1 || max_keys < 1) return 0;
-  return 16;
+  return chunk_workspace(geom, t_len, api_sm_count_for_sizing()).total;
 }
 
 c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
@@ -274,10 +290,14 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
   if (!aligned(q, 16) || !aligned(out, 16)) return api_fail(C2KV_EINVAL, "q and out must be 16-byte aligned");
   if (max_keys < 1 || max_keys > max_pages * pages->page)
     return api_fail(C2KV_EINVAL, "max_keys must be in [1, max_pages * page]");
-  if (workspace_bytes < c2kv_attend_pages8_chunk_workspace_size(geom, batch, t_len, max_keys) || !aligned(workspace, 16))
+  const int group = geom->n_q_heads / geom->n_kv_heads;
+  if (chunk_places(batch, geom->n_kv_heads, t_len, group, max_keys) > INT32_MAX / 2 || (int64_t)t_len * group > INT32_MAX / 2)
+    return api_fail(C2KV_EINVAL, "batch * n_q_heads * t_len * max_keys is above 2^30 products of 256 x 128");
+  const int sms = std::min(api_sm_count_for_sizing(), kMaxChunkCtas);
+  const ChunkWs w = chunk_workspace(geom, t_len, sms);
+  if (workspace_bytes < w.total || !aligned(workspace, 16))
     return api_fail(C2KV_EINVAL, "workspace too small or not 16-byte aligned");
-  int sms = 0;
-  s = api_device_state(&put.err, &sms);
+  s = api_device_state(&put.err, nullptr);
   if (s != C2KV_OK) return s;
   put.max_rows = max_keys;
   put.row_at_length = (flags & C2KV_DECODE_ROW_AT_LENGTH) != 0 ? 1 : 0;
@@ -304,9 +324,17 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
   p.max_keys = max_keys;
   p.table_rows = table_rows;
   p.row_at_length = put.row_at_length;
+  p.group = group;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  p.desc = reinterpret_cast<int32_t*>(ws);
+  p.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
+  p.part_o = reinterpret_cast<float4*>(ws + w.o_off);
+  p.part_rows = chunk_part_rows(t_len, group);
+  p.inject_timeout = api_take_injected_timeout();
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)geom->head_dim));
-  return api_launched(launch_attend_chunk8(p, geom->head_dim, geom->n_q_heads / geom->n_kv_heads, sms, st),
-                      "c2kv_attend_pages8_chunk");
+  s = api_launched(launch_attend_chunk8(p, geom->head_dim, sms, st), "c2kv_attend_pages8_chunk");
+  if (s != C2KV_OK) return s;
+  return api_launched(launch_attend_chunk8_merge(p, geom->head_dim, sms, st), "c2kv_attend_pages8_chunk");
 }
 
 size_t c2kv_pages8_plan_workspace_size(int32_t n_pages, int32_t batch, int32_t max_pages) {

@@ -111,9 +111,13 @@ struct ChunkParams {
   const int32_t* rope_row;
   __nv_bfloat16* out;            // [batch][t_len][n_q][d]
   unsigned* err;
-  int32_t batch, t_len, n_q, max_pages, max_keys, table_rows, row_at_length;
+  int32_t* desc;                 // [CTAs][8] the unit that begins in a CTA and goes on in others: rows (0: none), b, h, first row, CTAs
+  float2* part_ml;               // [2 * CTAs][part_rows] (m, l) of shared units
+  float4* part_o;                // [2 * CTAs][d / 4][part_rows] their O
+  int32_t batch, t_len, n_q, group, max_pages, max_keys, table_rows, row_at_length, part_rows, inject_timeout;
   float scale_log2;
 };
+constexpr int kMaxChunkCtas = 160;
 
 // What becomes of a pool's pages (pages8_move.cu).  `n_cached` null: compact.
 struct MoveParams {
@@ -182,7 +186,10 @@ __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.la
 cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, cudaStream_t st);
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st);
 cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, cudaStream_t st);
-cudaError_t launch_attend_chunk8(const ChunkParams& p, int head_dim, int group, int sms, cudaStream_t st);
+cudaError_t launch_attend_chunk8(const ChunkParams& p, int head_dim, int sms, cudaStream_t st);
+cudaError_t launch_attend_chunk8_merge(const ChunkParams& p, int head_dim, int sms, cudaStream_t st);
+int chunk_part_rows(int t_len, int group);
+int64_t chunk_places(int batch, int n_kv, int t_len, int group, int max_keys);   // at most
 size_t move_workspace_ints(int n_pages, int batch, int max_pages);
 cudaError_t launch_pages8_plan(const MoveParams& p, cudaStream_t st);
 cudaError_t launch_pages8_move(const MoveParams& p, int head_dim, int sms, cudaStream_t st);
