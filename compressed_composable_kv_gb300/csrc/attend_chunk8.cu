@@ -20,8 +20,8 @@
 // CTAs write partial (m, l, O) and merge_kernel joins them in the order of the keys.
 //
 // Roles: warps 0-3 and 4-7 softmax and epilogue of the unit's two 128-row tiles
-// (a thread to a row), warps 8-11 codes to fp16, warp 12 page ids and scales ahead
-// of them, warp 13 the MMAs, warp 14 tensor memory.
+// (a thread to a row), warps 8-11 and 12-15 the codes of K and V to fp16, warp 16
+// page ids and scales ahead of them, warp 17 the MMAs, warp 19 tensor memory.
 #include <float.h>
 
 #include <algorithm>
@@ -33,7 +33,7 @@ namespace c2kv {
 
 namespace {
 
-constexpr int CK_THREADS = 512;
+constexpr int CK_THREADS = 640;
 constexpr int CK_ROWS = 256;       // rows of a unit
 constexpr int CK_KEYS = 128;       // keys of a tile
 constexpr int kSlots = 8;          // tiles whose pages are known ahead
@@ -43,7 +43,8 @@ constexpr int kNoScale = -1000;    // exponent of a tile without a page
 constexpr float kRescaleLog2 = 8.f;   // a row's maximum may lag behind by this (weights up to 2^15, sums exact)
 constexpr float kWeightLog2 = 7.f;
 
-// What warp 12 finds out about a tile.
+// What warp 16 finds out about a tile, and the segment that it belongs to.
+enum : uint32_t { kWhole = 2, kEnd = 4, kWide = 8, kNone = 16 };
 struct TileSlot {
   int32_t grp[8];      // 16 rows each: index of the first of them in the layer, in 16s; -1: no page
   uint32_t kf[8];      // half2: the page's scale over the tile's, of K and of V
@@ -53,9 +54,14 @@ struct TileSlot {
   uint32_t bad;        // bit g: the rows of grp[g] take no part
   int32_t rows;        // keys of the tile that any row of the unit sees
   int32_t diag;        // keys below this are seen by every row
-  int32_t seg;
-  uint32_t flags;      // 1: kf are not all 1, 2: vf, 4: the CTA's last tile
-  int32_t pad;
+  // from here on known (seg_full) before the rest (slot_full)
+  uint32_t flags;      // kWhole: the segment is a whole unit, kEnd: it is
+                       // the CTA's last, kWide: a unit of more than 128 rows, kNone: the CTA has no tile
+  int32_t seg;         // segments of the CTA before this one
+  int32_t b, h, first; // sequence, kv head, the unit's first row
+  int32_t tile, n;     // of the unit, and how many of the segment are left
+  int32_t ctas;        // CTAs that hold the unit, if this is the first
+  int32_t pad[3];
 };
 
 struct ChunkMap {
@@ -76,8 +82,11 @@ struct CkCfg {
   static constexpr int OFF_SLOT = 6 * TILE;
   static constexpr int OFF_MAP = OFF_SLOT + kSlots * (int)sizeof(TileSlot);
   static constexpr int OFF_BAR = OFF_MAP + (int)((sizeof(ChunkMap) + 15) / 16 * 16);
-  static constexpr int N_BAR = 2 * 8 + 2 * kSlots + 2;
-  static constexpr int OFF_MISC = OFF_BAR + N_BAR * 8;
+  static constexpr int OFF_QS = OFF_BAR;                // the queries' scales, then what the second warps hand over
+  static constexpr int OFF_X = OFF_QS + CK_ROWS * 4;
+  static constexpr int OFF_BARS = OFF_X + 128 * 16;
+  static constexpr int N_BAR = 2 * 8 + 3 * kSlots + 5;
+  static constexpr int OFF_MISC = OFF_BARS + N_BAR * 8;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;    // + slack for 1024-byte alignment
   static_assert(SMEM <= 232448, "shared memory per CTA");
   static constexpr int TMEM_O = 256;                   // two S tiles of 128 columns, then two O tiles
@@ -87,7 +96,7 @@ __host__ __device__ constexpr uint32_t idesc_f16_m128(int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
-__device__ __noinline__ bool ck_slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+__device__ __forceinline__ bool ck_slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
   return wait_or_abort(bar, parity, abort_flag, err);
 }
 __device__ __forceinline__ bool ck_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
@@ -100,24 +109,66 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
+__device__ __forceinline__ float2 f32_of_f16x2(uint32_t h) {
+  float2 f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
+      : "=f"(f.x), "=f"(f.y)
+      : "r"(h));
+  return f;
+}
 // Two e4m3 codes to fp16 (exact).
 __device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t codes) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
   return r;
 }
+__device__ __forceinline__ uint64_t pack_f32x2(float2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f32x2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(pack_f32x2(a)), "l"(pack_f32x2(b)), "l"(pack_f32x2(c)));
+  return unpack_f32x2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(pack_f32x2(a)), "l"(pack_f32x2(b)));
+  return unpack_f32x2(r);
+}
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
-__device__ __forceinline__ uint4 load_codes(const uint8_t* p) {
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// 16 codes, or zeros.  One instruction sequence: where the compiler joins the two
+// cases it waits for the load there and then.
+__device__ __forceinline__ uint4 load_codes(const uint8_t* p, bool on) {
   uint4 u;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "l"(p));
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\t"
+      "mov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+      "@p ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(u.x), "=&r"(u.y), "=&r"(u.z), "=&r"(u.w)
+      : "l"(p), "r"((uint32_t)on));
   return u;
 }
+
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 __device__ __forceinline__ void tmem_st_cols16(uint32_t taddr, const float (&r)[16]) {
   asm volatile(
@@ -181,7 +232,7 @@ struct CkSeg {
 };
 
 // The CTA's next segment at place x or behind it; false: none before x1.
-__device__ __noinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, int x, int x1, CkSeg& s) {
+__device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, int x, int x1, CkSeg& s) {
   for (;;) {
     if (x >= x1) return false;
     s.b = ck_seq_of(m.start, batch, x);
@@ -218,7 +269,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TileSlot* slots = reinterpret_cast<TileSlot*>(smem + C::OFF_SLOT);
   ChunkMap& M = *reinterpret_cast<ChunkMap*>(smem + C::OFF_MAP);
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);   // two each: of a row tile, or of a stage
+  float* q_scale = reinterpret_cast<float*>(smem + C::OFF_QS);
+  float4* hand = reinterpret_cast<float4*>(smem + C::OFF_X);
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);   // two each: of a row tile, or of a stage
   uint64_t* s_full = q_full + 2;
   uint64_t* p_full = s_full + 2;
   uint64_t* o_done = p_full + 2;
@@ -228,22 +281,25 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   uint64_t* v_empty = v_full + 2;
   uint64_t* slot_full = v_empty + 2;
   uint64_t* slot_empty = slot_full + kSlots;
-  uint64_t* mma_done = slot_empty + kSlots;
+  uint64_t* seg_full = slot_empty + kSlots;
+  uint64_t* handed = seg_full + kSlots;
+  uint64_t* q_free = handed + 1;
+  uint64_t* mma_done = q_free + 1;
   uint64_t* never = mma_done + 1;   // test hook: nothing arrives
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
   volatile int* nan_seg = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);   // [4]: segment + 1 with NaN values some rows do not see
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int cta = blockIdx.x, G = p.group;
 
-  if (warp == 14) {
+  if (warp == 19) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr((const void*)tmem_slot)),
                  "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else if (warp == 13 && lane == 0) {
+  } else if (warp == 17 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);   // one arrival per warp
       mbar_init(&s_full[i], 1);
@@ -256,8 +312,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&slot_full[i], 1);
-      mbar_init(&slot_empty[i], 1);
+      mbar_init(&slot_empty[i], 12);   // 8 softmax warps, 4 of V's
+      mbar_init(&seg_full[i], 1);
     }
+    mbar_init(handed, 4);
+    mbar_init(q_free, 1);
     mbar_init(mma_done, 1);
     mbar_init(never, 1);
     *abort_flag = 0;
@@ -316,7 +375,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   CkCut cut;
   const int places = M.start[kMaxPagedSeqs];
   cut.ctas = min((int)gridDim.x, max(1, M.tiles / kChunkMinTiles));
@@ -325,60 +384,92 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   const int x0 = cta < cut.ctas ? cut.first(cta) : places, x1 = cta < cut.ctas ? cut.first(cta + 1) : places;
   if (tid == 0) p.desc[cta * 8] = 0;   // no unit to merge, so far
 
-  if (warp >= 12) {
-    if (warp == 12) {
+  if (warp >= 16) {
+    regs_down<64>();
+    if (warp == 16) {
       // ---------------- page ids and scales: lane 8 k + g has group g of the k-th
       // tile of four; the ids of the next four are on their way meanwhile
       const int g = lane & 7;
       CkSeg sg;
       int seg = 0, at = lane >> 3, j = lane >> 3;   // tile `at` of segment `seg`, the CTA's j-th
       bool more = ck_seg_at(M, p.batch, G, x0, x1, sg);
+      int done = 0;   // tiles of the segments before
       struct Ref {
-        int32_t id, key0, rows, diag, h, seg;   // id: -1 no page here, -2 outside the pool
-        bool on, last;
+        int32_t id, key0, rows, diag, ctas;   // id: -1 no page here, -2 outside the pool
+        int32_t b, h, first, tile, n, seg;
+        uint32_t flags;
+        bool on;
       };
       auto ask = [&]() {
         Ref r;
         r.id = -1;
-        while (more && at >= sg.n) {
-          at -= sg.n;
+        while (more && at - done >= sg.n) {
+          done += sg.n;
           ++seg;
           more = ck_next(M, p.batch, G, x1, sg);
         }
         r.on = more;
-        r.last = false;
         if (more) {
-          const int n = M.n[sg.b], tok0 = sg.i * CK_ROWS / G;
-          const int end = n + min((sg.i * CK_ROWS + CK_ROWS - 1) / G + 1, M.count[sg.b]);
-          r.key0 = (sg.t0 + at) * CK_KEYS;
-          r.rows = min(end - r.key0, CK_KEYS);
-          r.diag = n + tok0 + 1 - r.key0;
+          const int n = M.n[sg.b], first = sg.i * CK_ROWS, t = at - done, all = M.count[sg.b] * G;
+          const int end = n + min((first + CK_ROWS - 1) / G + 1, M.count[sg.b]);
+          r.b = sg.b;
           r.h = sg.h;
+          r.first = first;
+          r.tile = sg.t0 + t;
+          r.n = sg.n - t;
           r.seg = seg;
+          r.key0 = r.tile * CK_KEYS;
+          r.rows = min(end - r.key0, CK_KEYS);
+          r.diag = n + first / G + 1 - r.key0;
+          r.ctas = sg.t0 == 0 && !sg.whole() ? cut.of(sg.place + sg.tiles - 1) - cta + 1 : 0;
+          const bool ends = sg.t0 + sg.n < sg.tiles || sg.place + sg.tiles + kChunkUnitTiles >= x1;
+          r.flags = (sg.whole() ? kWhole : 0u) | (ends ? kEnd : 0u) | (all - first > 128 ? kWide : 0u);
           if (16 * g < r.rows) {
             r.id = p.page_table[(size_t)sg.b * p.max_pages + (r.key0 + 16 * g) / p.pool.page];
             if (r.id < 0) r.id = -2;
-          }
-          if (at == sg.n - 1) {
-            CkSeg t = sg;
-            r.last = !ck_next(M, p.batch, G, x1, t);
           }
         }
         at += 4;
         return r;
       };
       Ref cur = ask();
-      bool ok = true;
+      if (!__any_sync(0xffffffffu, cur.on)) {
+        if (lane == 0) {
+          slots[0].flags = kNone;
+          mbar_arrive(&seg_full[0]);
+          mbar_arrive(&slot_full[0]);
+        }
+      }
       while (__any_sync(0xffffffffu, cur.on)) {
         const Ref nxt = ask();
         if (cur.id >= p.pool.n_pages) cur.id = -2;
         float ks = 0.f, vs = 0.f;
         const size_t block = cur.id >= 0 ? (size_t)cur.id * p.pool.n_kv + cur.h : 0;
+        const size_t row = block * p.pool.page + (cur.key0 + 16 * g) % p.pool.page;
         if (cur.id >= 0) {
           ks = p.pool.scales[0][block];
           vs = p.pool.scales[1][block];
+          // the codes to L2, some tiles before the warps that read them
+          prefetch_l2(p.pool.codes[0] + row * D, 16 * D);
+          prefetch_l2(p.pool.codes[1] + row * D, 16 * D);
         }
         if (cur.id == -2) atomicOr(p.err, kErrLength);
+        TileSlot& s = slots[j % kSlots];
+        const bool ok = !cur.on || j < kSlots || ck_wait(&slot_empty[j % kSlots], ((j / kSlots) - 1) & 1, abort_flag, p.err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        if (cur.on && g == 0) {
+          s.rows = cur.rows;
+          s.diag = cur.diag;
+          s.flags = cur.flags;
+          s.seg = cur.seg;
+          s.b = cur.b;
+          s.h = cur.h;
+          s.first = cur.first;
+          s.tile = cur.tile;
+          s.n = cur.n;
+          s.ctas = cur.ctas;
+          mbar_arrive(&seg_full[j % kSlots]);
+        }
         const int ke = cur.id >= 0 ? exponent_of_scale(ks) : kNoScale, ve = cur.id >= 0 ? exponent_of_scale(vs) : kNoScale;
         int km = ke, vm = ve;
         uint32_t bad = cur.id == -2 ? 1u << g : 0;
@@ -388,13 +479,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           vm = max(vm, __shfl_xor_sync(0xffffffffu, vm, off));
           bad |= __shfl_xor_sync(0xffffffffu, bad, off);
         }
-        const bool mixed_k = cur.id >= 0 && ke != km, mixed_v = cur.id >= 0 && ve != vm;
-        const uint32_t mk = __ballot_sync(0xffffffffu, mixed_k) >> (lane & 24), mv = __ballot_sync(0xffffffffu, mixed_v) >> (lane & 24);
-        TileSlot& s = slots[j % kSlots];
-        ok = !cur.on || j < kSlots || ck_wait(&slot_empty[j % kSlots], ((j / kSlots) - 1) & 1, abort_flag, p.err);
-        if (!__all_sync(0xffffffffu, ok)) break;
         if (cur.on) {
-          s.grp[g] = cur.id >= 0 ? (int32_t)((block * p.pool.page + (cur.key0 + 16 * g) % p.pool.page) >> 4) : -1;
+          s.grp[g] = cur.id >= 0 ? (int32_t)(row >> 4) : -1;
           const float kf = pow2_float(max(ke - km, -126)), vf = pow2_float(max(ve - vm, -126));
           s.kf[g] = f16x2(kf, kf);
           s.vf[g] = f16x2(vf, vf);
@@ -402,10 +488,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             s.k_scale = km == kNoScale ? 1.f : pow2_float(km);
             s.v_exp = vm;
             s.bad = bad;
-            s.rows = cur.rows;
-            s.diag = cur.diag;
-            s.seg = cur.seg;
-            s.flags = ((mk & 0xFF) ? 1u : 0u) | ((mv & 0xFF) ? 2u : 0u) | (cur.last ? 4u : 0u);
           }
         }
         __syncwarp();
@@ -413,208 +495,207 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         cur = nxt;
         j += 4;
       }
-    } else if (warp == 13 && lane == 0) {
-      // ---------------- MMA issuer.  The two row tiles take turns: while the
-      // softmax of one works, the products of the other run.
+    } else if (warp == 17 && lane == 0) {
+      // ---------------- MMA issuer.  A wide unit has two row tiles, which take turns:
+      // while the softmax of one works, the products of the other run.  A narrow one
+      // has a single row tile: its even and odd key tiles take turns, each with scores
+      // and sums of its own.
       constexpr uint32_t idesc_qk = idesc_f16_m128(CK_KEYS, false);   // B = K (K-major)
       constexpr uint32_t idesc_pv = idesc_f16_m128(D, true);          // B = V (MN-major)
-      auto qk = [&](int m, int j) {
-        tc_fence_after();
-        const uint32_t q = smem_addr(smem + C::OFF_Q + m * C::TILE), k = smem_addr(smem + C::OFF_K + (j & 1) * C::TILE);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * 16384 + (kk % 4) * 32;
-          mma_bf16(tmem + m * 128, sw128_desc(q + off, 16, 1024), sw128_desc(k + off, 16, 1024), idesc_qk, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&s_full[m]);
-      };
-      auto pv = [&](int m, int j, bool first) {
-        tc_fence_after();
-        const uint32_t v = smem_addr(smem + C::OFF_V + (j & 1) * C::TILE);
-#pragma unroll
-        for (int kk = 0; kk < CK_KEYS / 16; ++kk)
-          mma_bf16_tmem_a(tmem + C::TMEM_O + m * 128, tmem + m * 128 + kk * 8, sw128_desc(v + kk * 2048, 16384, 1024),
-                          idesc_pv, !first || kk > 0 ? 1u : 0u);
-        mma_commit(&o_done[m]);
-      };
-      int j = 0, n0 = 0, n1 = 0, seg0 = 0, seg1 = 0;   // tiles and segments of each row tile
-      CkSeg sg;
+      const uint32_t base = smem_addr(smem);
+      const uint64_t q_desc = sw128_desc(base + C::OFF_Q, 16, 1024), k_desc = sw128_desc(base + C::OFF_K, 16, 1024),
+                     v_desc = sw128_desc(base + C::OFF_V, 16384, 1024);
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return ck_wait(bar, parity, abort_flag, p.err); };
       bool ok = true;
-      for (bool more = ck_seg_at(M, p.batch, G, x0, x1, sg); ok && more; more = ck_next(M, p.batch, G, x1, sg)) {
-        const bool two = M.count[sg.b] * G - sg.i * CK_ROWS > 128;
-        ok = ck_wait(&k_full[j & 1], (j >> 1) & 1, abort_flag, p.err) && ck_wait(&q_full[0], seg0++ & 1, abort_flag, p.err);
+      uint32_t np = 0;   // bit m: parity of p_full[m]
+      for (int j = 0, seg = 0; ok; ++seg) {
+        ok = wait(&seg_full[j % kSlots], (j / kSlots) & 1);
         if (!ok) break;
-        qk(0, j);
-        if (two) {
-          ok = ck_wait(&q_full[1], seg1++ & 1, abort_flag, p.err);
+        const TileSlot& s = slots[j % kSlots];
+        const uint32_t flags = s.flags;
+        if (flags & kNone) break;
+        const int n = s.n, wide = (flags & kWide) ? 1 : 0, step = 2 - wide;
+        ok = wait(&q_full[0], seg & 1) && wait(&q_full[1], seg & 1);
+        // P V of tile t, then the scores of the next, which take the weights' place
+#pragma unroll 1
+        for (int t = -step; ok && t < n; ++t) {
+          const int jt = j + t, tn = t + step, jn = j + tn;
+#pragma unroll 1
+          for (int i = 0; i <= wide; ++i) {
+            const int m = wide ? i : t & 1;
+            const uint32_t s_col = tmem + m * 128;
+            if (t >= 0) {
+              ok = (i > 0 || wait(&v_full[jt & 1], (jt >> 1) & 1)) && wait(&p_full[m], np >> m & 1);
+              if (!ok) break;
+              np ^= 1u << m;
+              tc_fence_after();
+              const uint64_t v = v_desc + (uint32_t)(jt & 1) * (C::TILE >> 4);
+#pragma unroll
+              for (int kk = 0; kk < CK_KEYS / 16; ++kk)
+                mma_bf16_tmem_a(s_col + C::TMEM_O, s_col + kk * 8, v + kk * (2048 >> 4), idesc_pv, t >= step || kk > 0 ? 1u : 0u);
+            }
+            if (tn < n) {
+              if (i == 0) {
+                ok = wait(&k_full[jn & 1], (jn >> 1) & 1);
+                if (!ok) break;
+                tc_fence_after();
+              }
+              const uint64_t k = k_desc + (uint32_t)(jn & 1) * (C::TILE >> 4),
+                             q = q_desc + (uint32_t)i * (C::TILE >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk / 4) * (16384 >> 4) + (kk % 4) * 2;
+                mma_bf16(s_col, q + off, k + off, idesc_qk, kk > 0 ? 1u : 0u);
+              }
+              mma_commit(&s_full[m]);   // P V of the tile before has completed as well
+            } else if (t >= 0) {
+              mma_commit(&o_done[m]);
+            }
+          }
           if (!ok) break;
-          qk(1, j);
+          if (tn < n) {
+            mma_commit(&k_empty[jn & 1]);
+            if (tn == n - 1) mma_commit(q_free);
+          }
+          if (t >= 0) mma_commit(&v_empty[jt & 1]);
         }
-        mma_commit(&k_empty[j & 1]);
-        for (int t = 0; t < sg.n; ++t, ++j) {
-          const bool next = t + 1 < sg.n;
-          ok = ck_wait(&v_full[j & 1], (j >> 1) & 1, abort_flag, p.err) && ck_wait(&p_full[0], n0++ & 1, abort_flag, p.err);
-          if (!ok) break;
-          pv(0, j, t == 0);
-          if (next) {
-            ok = ck_wait(&k_full[(j + 1) & 1], ((j + 1) >> 1) & 1, abort_flag, p.err);
-            if (!ok) break;
-            qk(0, j + 1);
-          }
-          if (two) {
-            ok = ck_wait(&p_full[1], n1++ & 1, abort_flag, p.err);
-            if (!ok) break;
-            pv(1, j, t == 0);
-          }
-          mma_commit(&v_empty[j & 1]);
-          mbar_arrive(&slot_empty[j % kSlots]);   // the softmax has its part of it, the codes are in fp16
-          if (next) {
-            if (two) qk(1, j + 1);
-            mma_commit(&k_empty[(j + 1) & 1]);
-          }
-        }
+        j += n;
+        if (flags & kEnd) break;
       }
       // every MMA issued above must complete before TMEM is released
       mma_commit(mma_done);
       mbar_wait(mma_done, 0);
     }
   } else if (warp >= 8) {
-    // ---------------- codes to fp16: a thread has 16 codes of a row, 8 (at
-    // head_dim 64, 4) times a tile of K and as often of V; the codes of the next
-    // tile are asked for as soon as this one's registers are free
+    regs_down<80>();
+    // ---------------- codes to fp16, warps 8-11 of K, 12-15 of V: a thread has 16
+    // codes of a row, 8 (at head_dim 64, 4) times a tile; the next tile's are asked
+    // for as soon as the registers are free.  Eight neighbouring lanes have two rows'
+    // neighbouring chunks: their stores meet all banks.
+    const int kv = (warp - 8) >> 2;
     constexpr int LPR = D / 16, RPP = 128 / LPR, NP = 128 / RPP;   // lanes of a row, rows at a time, times
-    const int ct = tid - 256, c = ct % LPR, r0 = ct / LPR;
-    // the 16-byte units of the row in fp16 that the codes go to; at head_dim 128 the
-    // upper half of a row writes its second unit first, so that the eight lanes of a
-    // row meet different banks
-    const bool swap = c >= 4;
-    const uint32_t sub = (uint32_t)(c / 4) * 16384;
-    const int u0 = 2 * (c % 4);
-    uint4 kc[NP], vc[NP];
-    auto ask = [&](int j, int kv, uint4 (&u)[NP]) {
+    const int c = D == 128 ? (lane & 3) + (lane >> 1 & 4) : lane & 3;
+    const int r0 = D == 128 ? (lane >> 2 & 1) + (lane >> 3 & 2) + (warp & 3) * 4 : (lane >> 2) + (warp & 3) * 8;
+    // a chunk's two 16-byte units of the row in fp16; rows of a thread are a multiple of 8 apart
+    const int u0 = 2 * (c & 3);
+    const uint32_t at0 = (uint32_t)(c >> 2) * 16384 + r0 * 128 + ((u0 ^ (r0 & 7)) << 4);
+    const uint32_t at1 = (uint32_t)(c >> 2) * 16384 + r0 * 128 + (((u0 + 1) ^ (r0 & 7)) << 4);
+    const uint8_t* codes = p.pool.codes[kv] + (r0 & 15) * D + c * 16;
+    uint64_t* full = kv == 0 ? k_full : v_full;
+    uint64_t* empty = kv == 0 ? k_empty : v_empty;
+    uint8_t* ring = smem + (kv == 0 ? C::OFF_K : C::OFF_V);
+    uint4 u[NP];
+    bool ok = true;
+    auto ask = [&](int j) {
+      ok = ck_wait(&slot_full[j % kSlots], (j / kSlots) & 1, abort_flag, p.err);
+      if (!__all_sync(0xffffffffu, ok)) return false;
       const TileSlot& s = slots[j % kSlots];
+      const int rows = (s.flags & kNone) ? 0 : s.rows;
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const int row = k * RPP + r0, grp = s.grp[row >> 4];
-        u[k] = make_uint4(0, 0, 0, 0);
-        if (grp >= 0 && row < s.rows) u[k] = load_codes(p.pool.codes[kv] + (size_t)grp * (16 * D) + (row & 15) * D + c * 16);
+        u[k] = load_codes(codes + (int64_t)grp * (16 * D), grp >= 0 && row < rows);
       }
+      return true;
     };
-    auto put = [&](int j, uint4 (&u)[NP], uint8_t* tile, const uint32_t* factors, bool mixed, int diag) {
-      bool nan = false;
+    if (ask(0)) {
+      for (int j = 0;; ++j) {
+        const TileSlot& s = slots[j % kSlots];
+        const bool last = (s.flags & kEnd) && s.n == 1;
+        if (s.flags & kNone) break;
+        if (kv == 1 && s.diag < CK_KEYS) {
+          // a NaN that some rows of the unit do not see must not reach them: see the epilogue
+          bool nan = false;
 #pragma unroll
-      for (int k = 0; k < NP; ++k) {
-        const int row = k * RPP + r0;
-        uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-        if (row >= diag) {   // a NaN that some rows do not see must not reach them: see the epilogue
+          for (int k = 0; k < NP; ++k) {
+            uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t is = k * RPP + r0 < s.diag ? 0 : __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+              nan |= is != 0;
+              w[i] &= ~is;
+            }
+            u[k] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          if (nan) nan_seg[s.seg & 3] = s.seg + 1;
+        }
+        if (j >= 2) ok = ck_wait(&empty[j & 1], ((j >> 1) - 1) & 1, abort_flag, p.err);
+        if (!__all_sync(0xffffffffu, ok)) break;
+        uint8_t* tile = ring + (j & 1) * C::TILE;
+        const uint32_t* factors = kv == 0 ? s.kf : s.vf;
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const uint32_t w[4] = {u[k].x, u[k].y, u[k].z, u[k].w}, f = factors[(k * RPP + r0) >> 4];
+          uint32_t h[8];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t is = __vcmpeq4(w[i] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            nan |= is != 0;
-            w[i] &= ~is;
+            h[2 * i] = mul_f16x2(f16x2_of_codes(w[i]), f);
+            h[2 * i + 1] = mul_f16x2(f16x2_of_codes(w[i] >> 16), f);
           }
+          *reinterpret_cast<uint4*>(tile + at0 + k * RPP * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(tile + at1 + k * RPP * 128) = make_uint4(h[4], h[5], h[6], h[7]);
         }
-        uint32_t h[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          h[2 * i] = f16x2_of_codes(w[i]);
-          h[2 * i + 1] = f16x2_of_codes(w[i] >> 16);
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&full[j & 1]);
+          if (kv == 1) mbar_arrive(&slot_empty[j % kSlots]);
         }
-        if (mixed) {
-          const uint32_t f = factors[row >> 4];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) h[i] = mul_f16x2(h[i], f);
-        }
-        const uint4 lo = make_uint4(h[0], h[1], h[2], h[3]), hi = make_uint4(h[4], h[5], h[6], h[7]);
-        uint8_t* at = tile + sub + row * 128;
-        *reinterpret_cast<uint4*>(at + (((u0 + swap) ^ (row & 7)) << 4)) = swap ? hi : lo;
-        *reinterpret_cast<uint4*>(at + (((u0 + !swap) ^ (row & 7)) << 4)) = swap ? lo : hi;
+        if (last || !ask(j + 1)) break;
       }
-      return nan;
-    };
-    bool ok = x0 < x1;
-    if (ok) {
-      CkSeg sg;
-      ok = ck_seg_at(M, p.batch, G, x0, x1, sg);   // a tile at all
-    }
-    if (ok) {
-      ok = ck_wait(&slot_full[0], 0, abort_flag, p.err);
-      if (__all_sync(0xffffffffu, ok)) {
-        ask(0, 0, kc);
-        ask(0, 1, vc);
-      } else {
-        ok = false;
-      }
-    }
-    for (int j = 0; ok; ++j) {
-      const TileSlot& s = slots[j % kSlots];
-      const uint32_t flags = s.flags;
-      const int diag = s.diag, seg = s.seg;
-      if (j >= 2) ok = ck_wait(&k_empty[j & 1], ((j >> 1) - 1) & 1, abort_flag, p.err);
-      put(j, kc, smem + C::OFF_K + (j & 1) * C::TILE, s.kf, flags & 1, CK_KEYS);
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&k_full[j & 1]);
-      if (!(flags & 4)) {
-        ok = ck_wait(&slot_full[(j + 1) % kSlots], ((j + 1) / kSlots) & 1, abort_flag, p.err) && ok;
-        if (!__all_sync(0xffffffffu, ok)) break;
-        ask(j + 1, 0, kc);
-      }
-      if (j >= 2) ok = ck_wait(&v_empty[j & 1], ((j >> 1) - 1) & 1, abort_flag, p.err);
-      if (put(j, vc, smem + C::OFF_V + (j & 1) * C::TILE, s.vf, flags & 2, diag)) nan_seg[seg & 3] = seg + 1;
-      fence_proxy_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&v_full[j & 1]);
-      if (flags & 4) break;
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok) ask(j + 1, 1, vc);
     }
   } else {
+    regs_up<128>();
     // ---------------- softmax and epilogue: row `row` of the unit
-    const int m = warp >> 2;                      // row tile
-    const int row = tid;                          // 0 .. 255
+    const int m = warp >> 2;                      // row tile, or parity of the key tiles
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lane_base + m * 128, o_at = lane_base + C::TMEM_O + m * 128;
-    int j = 0, nt = 0, seg = 0;                   // the CTA's tiles, this row tile's, segments
+    int nt = 0;                                   // tiles of this half
+    int ends[2] = {0, 0}, hands = 0;              // segments that the halves had tiles of; that both had of narrow units
     bool ok = true;
-    CkSeg sg;
-    for (bool more = ck_seg_at(M, p.batch, G, x0, x1, sg); ok && more; ++seg, more = ck_next(M, p.batch, G, x1, sg)) {
-      const int n = M.n[sg.b], count = M.count[sg.b];
-      const int first = sg.i * CK_ROWS, rows = min(count * G - first, CK_ROWS);   // of the unit
-      if (sg.t0 == 0 && !sg.whole() && tid == 0) {
+    for (int j = 0, seg = 0; ok; ++seg) {
+      ok = __all_sync(0xffffffffu, ck_wait(&seg_full[j % kSlots], (j / kSlots) & 1, abort_flag, p.err));
+      if (!ok) break;
+      const TileSlot& head_slot = slots[j % kSlots];
+      const uint32_t flags = head_slot.flags;
+      if (flags & kNone) break;
+      const bool wide = flags & kWide, whole = flags & kWhole;
+      const int b = head_slot.b, h = head_slot.h, first = head_slot.first, t0 = head_slot.tile, tiles = head_slot.n;
+      const int n = M.n[b], rows = min(M.count[b] * G - first, CK_ROWS);   // of the unit
+      if (tid == 0 && head_slot.ctas > 0) {
         // this CTA has the unit's first tile: it says who has the others
         int32_t* d = p.desc + cta * 8;
-        d[1] = sg.b;
-        d[2] = sg.h;
+        d[1] = b;
+        d[2] = h;
         d[3] = first;
-        d[4] = cut.of(sg.place + sg.tiles - 1) - cta + 1;   // CTAs
+        d[4] = head_slot.ctas;
         d[0] = rows;
       }
-      if (m == 1 && rows <= 128) {   // nothing in this row tile
-        j += sg.n;
-        continue;
-      }
-      const int tok = (first + row) / G, head = sg.h * G + (first + row) % G;
+      const int row = wide ? tid : tid & 127;
+      const int tok = (first + row) / G, head = h * G + (first + row) % G;
       const bool live = row < rows;
       const bool warp_live = (row & ~31) < rows;
       // ---- the queries: rotated, times log2(e)/sqrt(d), over a power of two of
       // the row, in fp16.  8 (4) lanes to a row.
-      float qs = 0.f;
+      if (seg > 0) {
+        ok = __all_sync(0xffffffffu, ck_wait(q_free, (seg - 1) & 1, abort_flag, p.err));
+        if (!ok) break;
+      }
       {
         constexpr int CH = D / 16, RPW = 32 / CH;   // lanes of a row, rows at a time
         const int c = lane % CH;
-        uint8_t* qt = smem + C::OFF_Q + m * C::TILE;
-#pragma unroll 2
-        for (int k = 0; k < CH; ++k) {
-          const int r = (row & ~31) + k * RPW + lane / CH;   // of the unit
+        const int base = wide ? tid & ~31 : m * 64 + (warp & 3) * 16, times = (wide ? 32 : 16) / RPW;
+#pragma unroll 1
+        for (int k = 0; k < times; ++k) {
+          const int r = base + k * RPW + lane / CH;   // of the unit
           float x[8], y[8];
           uint32_t top = 0;
           if (r < rows) {
             const int rq = first + r, tk = rq / G;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (((size_t)sg.b * p.t_len + tk) * p.n_q + sg.h * G + rq % G) * D);
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + (((size_t)b * p.t_len + tk) * p.n_q + h * G + rq % G) * D);
             unpack8(src[c], x);
             unpack8(src[c + CH], y);
-            const CosSin2* t = p.tab + ((size_t)M.rope[sg.b] + tk) * (D / 2) + c * 8;
+            const CosSin2* t = p.tab + ((size_t)M.rope[b] + tk) * (D / 2) + c * 8;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float2 co = *reinterpret_cast<const float2*>(t + e), si = *reinterpret_cast<const float2*>(&t[e].sh);
@@ -638,18 +719,16 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             hy[i] = f16x2(y[2 * i] * inv, y[2 * i + 1] * inv);
           }
           const int rt = r & 127, ux = c, uy = D == 128 ? c : c + 4;
-          *reinterpret_cast<uint4*>(qt + rt * 128 + ((ux ^ (rt & 7)) << 4)) = make_uint4(hx[0], hx[1], hx[2], hx[3]);
-          *reinterpret_cast<uint4*>(qt + (D == 128 ? 16384 : 0) + rt * 128 + ((uy ^ (rt & 7)) << 4)) =
-              make_uint4(hy[0], hy[1], hy[2], hy[3]);
-          const float scale = top < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
-          const float mine = __shfl_sync(0xffffffffu, scale, lane % RPW * CH);
-          if (lane / RPW == k) qs = mine;
+          uint8_t* qt = smem + C::OFF_Q + (r >> 7) * C::TILE + rt * 128;
+          *reinterpret_cast<uint4*>(qt + ((ux ^ (rt & 7)) << 4)) = make_uint4(hx[0], hx[1], hx[2], hx[3]);
+          *reinterpret_cast<uint4*>(qt + (D == 128 ? 16384 : 0) + ((uy ^ (rt & 7)) << 4)) = make_uint4(hy[0], hy[1], hy[2], hy[3]);
+          if (c == 0) q_scale[r] = top < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
         }
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[m]);
       }
-      float m_run = -INFINITY, l_run = 0.f;
+      float m_run = -INFINITY, l_run = 0.f, qs = 0.f;
       int v_ref = kNoScale;
       const int lim = n + tok + 1;   // keys that the row sees
       if (p.inject_timeout && (cta & 1) == 0 && seg == 0) {
@@ -658,71 +737,114 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         if (tid == 0) atomicOr(p.err, kErrTimeout);
         break;
       }
-      for (int t = 0; t < sg.n; ++t, ++j, ++nt) {
+      const int step = wide ? 1 : 2;
+      for (int t = 0; t < tiles; ++t, ++j) {
+        if (!wide && (t & 1) != m) {   // the other half's: only let it go
+          ok = __all_sync(0xffffffffu, ck_wait(&seg_full[j % kSlots], (j / kSlots) & 1, abort_flag, p.err));
+          if (!ok) break;
+          if (lane == 0) mbar_arrive(&slot_empty[j % kSlots]);
+          continue;
+        }
         ok = __all_sync(0xffffffffu, ck_wait(&s_full[m], nt & 1, abort_flag, p.err));
         if (!ok) break;
+        ++nt;
         if (warp_live) {
           tc_fence_after();
+          if (t < step) qs = q_scale[row];
           const TileSlot& ts = slots[j % kSlots];
-          const int nvis = live ? lim - (sg.t0 + t) * CK_KEYS : 0;
+          const int nvis = live ? lim - (t0 + t) * CK_KEYS : 0;
           float sc = qs * ts.k_scale;   // in range, so that a masked score stays -inf; NaN stays
           sc = sc < FLT_MIN ? FLT_MIN : sc > FLT_MAX ? FLT_MAX : sc;
           const uint32_t bad = ts.bad;
           const int v_exp = ts.v_exp;
-          // the scores are read twice, 32 at a time: once for the maximum, once for
-          // the weights, which take the place of the scores read before them
+          // One pass, 32 scores at a time: the weights take the place of the scores
+          // read before them.  The row's maximum may lag behind by kRescaleLog2; where
+          // it is further behind (seldom), what was computed with it is brought down:
+          // the sums, this tile's weights so far, and, at the end, O.  The loop is
+          // rolled: unrolled code did not stay in the instruction cache, and the warp
+          // that issues the MMAs starved.
           const bool partial = nvis < CK_KEYS || bad;
-          auto mask = [&](int i0, float (&x)[32]) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i0 + i >= nvis || (bad >> ((i0 + i) >> 4) & 1)) x[i] = -INFINITY;
-          };
-          float top = -INFINITY;
-#pragma unroll
-          for (int i0 = 0; i0 < CK_KEYS; i0 += 64) {
-            float x[32], y[32];
-            tmem_ld32(s_at + i0, x);
-            tmem_ld32(s_at + i0 + 32, y);
-            tmem_wait_ld();
-            if (partial) {
-              mask(i0, x);
-              mask(i0 + 32, y);
-            }
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              t0 = fmaxf(t0, x[i]);
-              t1 = fmaxf(t1, y[i]);
-            }
-            top = fmaxf(top, fmaxf(t0, t1));
-          }
-          top = top == -INFINITY ? top : top * sc;
-          float alpha = 1.f;
-          bool rescale = false;
-          if (top > m_run) {
-            if (m_run == -INFINITY) {
-              m_run = top;   // nothing accumulated yet: O holds zeros
-            } else if (top - m_run > kRescaleLog2) {
-              alpha = ex2_approx(m_run - top);
-              m_run = top;
-              rescale = true;
-            }
-          }
-          l_run *= alpha;
+          const float2 sc2 = make_float2(sc, sc);
+          float alpha = 1.f;   // what O is multiplied by
           if (v_exp > v_ref) {   // the same in every row
-            if (v_ref != kNoScale) {
-              alpha *= pow2_float(max(v_ref - v_exp, -126));
-              rescale = true;
-            }
+            if (v_ref != kNoScale) alpha = pow2_float(max(v_ref - v_exp, -126));
             v_ref = v_exp;
           }
-          const float v_mul = v_exp == kNoScale || v_exp < v_ref - 126 ? 0.f : pow2_float(v_exp - v_ref);
-          const float mu = (m_run == -INFINITY ? 0.f : m_run) - kWeightLog2;
-          if (__any_sync(0xffffffffu, rescale) && t > 0) {
-            ok = __all_sync(0xffffffffu, ck_wait(&o_done[m], (nt - 1) & 1, abort_flag, p.err));
-            if (!ok) break;
-            tc_fence_after();
+          // the tile's V scale over the largest so far goes into the weights' exponent
+          const int v_by = v_exp == kNoScale ? 0 : max(v_exp - v_ref, -60);
+          const float off = kWeightLog2 + (float)v_by, v_inv = pow2_float(-v_by);
+          float2 l4[4];
 #pragma unroll
+          for (int i = 0; i < 4; ++i) l4[i] = make_float2(0.f, 0.f);
+          auto part = [&](int i0, float (&x)[32]) {
+            if (partial) {
+              const int left = nvis - i0;
+              uint32_t vis = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1;
+              if (bad >> (i0 >> 4) & 1) vis &= 0xFFFF0000u;
+              if (bad >> (i0 >> 4) & 2) vis &= 0x0000FFFFu;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = (vis >> i & 1) ? x[i] : -INFINITY;
+            }
+            float tops[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) tops[i] = fmaxf(x[8 * i], x[8 * i + 1]);
+#pragma unroll
+            for (int i = 2; i < 8; i += 2)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], fmaxf(x[8 * k + i], x[8 * k + i + 1]));
+            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+            const bool up = top != -INFINITY && top * sc > m_run + kRescaleLog2;
+            if (__any_sync(0xffffffffu, up)) {
+              const float by = up ? ex2_approx(m_run - top * sc) : 1.f;   // 0 for the first scores of a row
+              if (up) m_run = top * sc;
+              alpha *= by;
+              l_run *= by;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) l4[i].x *= by, l4[i].y *= by;
+              if (i0 > 0) {
+                tmem_wait_st();
+#pragma unroll 1
+                for (int c = 0; c < i0 / 2; c += 16) {
+                  float w[16];
+                  tmem_ld_cols<16>(s_at + c, w);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const float2 v = f32_of_f16x2(__float_as_uint(w[i]));
+                    w[i] = __uint_as_float(f16x2(v.x * by, v.y * by));
+                  }
+                  tmem_st_cols16(s_at + c, w);
+                }
+              }
+            }
+            const float mu = off - (m_run == -INFINITY ? 0.f : m_run);
+            const float2 mu2 = make_float2(mu, mu);
+            float w[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float2 e = fma2(make_float2(x[i], x[i + 1]), sc2, mu2);
+              e.x = ex2_approx(e.x);
+              e.y = ex2_approx(e.y);
+              l4[i / 2 % 4] = add2(l4[i / 2 % 4], e);
+              w[i / 2] = __uint_as_float(f16x2(e.x, e.y));
+            }
+            tmem_st_cols16(s_at + i0 / 2, w);
+          };
+          float xa[32], xb[32];   // the next scores are on their way while one part's are worked on
+          tmem_ld32(s_at, xa);
+#pragma unroll 1
+          for (int i0 = 0; i0 < CK_KEYS; i0 += 64) {
+            tmem_wait_ld();
+            tmem_ld32(s_at + i0 + 32, xb);
+            part(i0, xa);
+            tmem_wait_ld();
+            if (i0 == 0) tmem_ld32(s_at + 64, xa);
+            part(i0 + 32, xb);
+          }
+          const float2 l2 = add2(add2(l4[0], l4[1]), add2(l4[2], l4[3]));
+          l_run = fmaf(l2.x + l2.y, v_inv, l_run);
+          if (t >= step && __any_sync(0xffffffffu, alpha != 1.f)) {   // (the scores came behind the P V before)
+#pragma unroll 1
             for (int c0 = 0; c0 < D; c0 += 32) {
               float o[32];
               tmem_ld32(o_at + c0, o);
@@ -732,65 +854,92 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               tmem_st32(o_at + c0, o);
             }
           }
-          float l0 = 0.f, l1 = 0.f;
-          float x[2][32];
-          tmem_ld32(s_at, x[0]);
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) {
-            tmem_wait_ld();
-            if (q4 < 3) tmem_ld32(s_at + (q4 + 1) * 32, x[(q4 + 1) & 1]);
-            float (&y)[32] = x[q4 & 1];
-            if (partial) mask(q4 * 32, y);
-            float w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float a = ex2_approx(fmaf(y[i], sc, -mu)), b = ex2_approx(fmaf(y[i + 1], sc, -mu));
-              l0 += a;
-              l1 += b;
-              w[i / 2] = __uint_as_float(f16x2(a * v_mul, b * v_mul));
-            }
-            tmem_st_cols16(s_at + q4 * 16, w);
-          }
-          l_run += l0 + l1;
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[m]);
+        if (lane == 0) {
+          mbar_arrive(&p_full[m]);
+          mbar_arrive(&slot_empty[j % kSlots]);
+        }
       }
       if (!ok) break;
       // ---- epilogue
-      ok = __all_sync(0xffffffffu, ck_wait(&o_done[m], (nt - 1) & 1, abort_flag, p.err));
-      if (!ok) break;
-      if (!warp_live) continue;
+      const bool mine = wide || m == 0 || tiles > 1;   // this half had a tile
+      if (mine) {
+        ok = __all_sync(0xffffffffu, ck_wait(&o_done[m], ends[m] & 1, abort_flag, p.err));
+        if (!ok) break;
+      }
+      const int ends1 = ends[1];
+      ++ends[0];
+      if (wide || tiles > 1) ++ends[1];
+      const bool two = !wide && tiles > 1;   // a narrow unit's halves are added up by the first
+      float4 other = make_float4(-INFINITY, 0.f, 0.f, 0.f);   // m, l, 2^v_ref of the second half
+      if (two && m == 1) {
+        if (warp_live) hand[row] = make_float4(m_run, l_run, v_ref == kNoScale ? 0.f : pow2_float(v_ref), 0.f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(handed);
+      }
+      if (!wide && m == 1) {
+        if (flags & kEnd) break;
+        continue;
+      }
+      if (two) {
+        ok = __all_sync(0xffffffffu, ck_wait(handed, hands++ & 1, abort_flag, p.err) &&
+                                         ck_wait(&o_done[1], ends1 & 1, abort_flag, p.err));
+        if (!ok) break;
+        if (warp_live) other = hand[row];
+      }
+      if (!warp_live) {
+        if (flags & kEnd) break;
+        continue;
+      }
       tc_fence_after();
       const bool nan = nan_seg[seg & 3] == seg + 1;
-      const bool whole = sg.whole();
-      const float scale = v_ref == kNoScale ? 0.f : pow2_float(v_ref);
-      const float f = whole ? (l_run == 0.f ? 0.f : scale / l_run) : scale;
-      const int slot = 2 * cta + (sg.t0 == 0 ? 1 : 0);   // of a unit's first part: see the merge
+      float f = v_ref == kNoScale ? 0.f : pow2_float(v_ref), f1 = 0.f;
+      if (two) {
+        const float top = fmaxf(m_run, other.x), base = top == -INFINITY ? 0.f : top;
+        const float w0 = ex2_approx(m_run - base), w1 = ex2_approx(other.x - base);
+        f *= w0;
+        f1 = other.z * w1;
+        l_run = l_run * w0 + other.y * w1;
+        m_run = top;
+      }
+      if (whole) {
+        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+        f *= inv;
+        f1 *= inv;
+      }
+      const int slot = 2 * cta + (t0 == 0 ? 1 : 0);   // of a unit's first part: see the merge
       if (!whole && live) p.part_ml[(size_t)slot * p.part_rows + row] = make_float2(m_run, l_run);
-#pragma unroll
+#pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 32) {
         float o[32];
         tmem_ld32(o_at + c0, o);
         tmem_wait_ld();
-        if (!live) continue;
 #pragma unroll
         for (int i = 0; i < 32; ++i) o[i] *= f;
+        if (two) {
+          float y[32];
+          tmem_ld32(o_at + 128 + c0, y);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = fmaf(y[i], f1, o[i]);
+        }
+        if (!live) continue;
         if (nan) {   // values that are not numbers, for the rows that see them
-          const int end = min(lim, (sg.t0 + sg.n) * CK_KEYS);
-          for (int key = max(n + first / G + 1, sg.t0 * CK_KEYS); key < end; ++key) {
-            const int id = p.page_table[(size_t)sg.b * p.max_pages + key / p.pool.page];
+          const int end = min(lim, (t0 + tiles) * CK_KEYS);
+          for (int key = max(n + first / G + 1, t0 * CK_KEYS); key < end; ++key) {
+            const int id = p.page_table[(size_t)b * p.max_pages + key / p.pool.page];
             if (id < 0 || id >= p.pool.n_pages) continue;
-            const uint8_t* v = p.pool.codes[1] + (((size_t)id * p.pool.n_kv + sg.h) * p.pool.page + key % p.pool.page) * D + c0;
+            const uint8_t* v = p.pool.codes[1] + (((size_t)id * p.pool.n_kv + h) * p.pool.page + key % p.pool.page) * D + c0;
 #pragma unroll
             for (int i = 0; i < 32; ++i)
               if ((v[i] & 0x7F) == 0x7F) o[i] = __uint_as_float(0x7FFFFFFFu);
           }
         }
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (((size_t)sg.b * p.t_len + tok) * p.n_q + head) * D + c0);
+          uint4* dst = reinterpret_cast<uint4*>(p.out + (((size_t)b * p.t_len + tok) * p.n_q + head) * D + c0);
 #pragma unroll
           for (int i = 0; i < 32; i += 8) {
             const float e[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
@@ -803,11 +952,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         }
       }
       tc_fence_before();
+      if (flags & kEnd) break;
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 14) {
+  if (warp == 19) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
