@@ -331,6 +331,7 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
   p.part_o = reinterpret_cast<float4*>(ws + w.o_off);
   p.part_rows = chunk_part_rows(t_len, group);
   p.inject_timeout = api_take_injected_timeout();
+  p.early = k_new != nullptr ? 1 : 0;
   p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)geom->head_dim));
   s = api_launched(launch_attend_chunk8(p, geom->head_dim, sms, st), "c2kv_attend_pages8_chunk");
   if (s != C2KV_OK) return s;

@@ -21,7 +21,7 @@
 //
 // Roles: warps 0-3 and 4-7 softmax and epilogue of the unit's two 128-row tiles
 // (a thread to a row), warps 8-11 and 12-15 the codes of K and V to fp16, warp 16
-// page ids and scales ahead of them, warp 17 the MMAs, warp 19 tensor memory.
+// page ids and scales ahead of them, warps 17 and 18 the MMAs, warp 19 tensor memory.
 #include <float.h>
 
 #include <algorithm>
@@ -44,7 +44,7 @@ constexpr float kRescaleLog2 = 8.f;   // a row's maximum may lag behind by this 
 constexpr float kWeightLog2 = 7.f;
 
 // What warp 16 finds out about a tile, and the segment that it belongs to.
-enum : uint32_t { kWhole = 2, kEnd = 4, kWide = 8, kNone = 16 };
+enum : uint32_t { kWhole = 2, kEnd = 4, kWide = 8, kNone = 16, kFresh = 32 };
 struct TileSlot {
   int32_t grp[8];      // 16 rows each: index of the first of them in the layer, in 16s; -1: no page
   uint32_t kf[8];      // half2: the page's scale over the tile's, of K and of V
@@ -56,7 +56,8 @@ struct TileSlot {
   int32_t diag;        // keys below this are seen by every row
   // from here on known (seg_full) before the rest (slot_full)
   uint32_t flags;      // kWhole: the segment is a whole unit, kEnd: it is
-                       // the CTA's last, kWide: a unit of more than 128 rows, kNone: the CTA has no tile
+                       // the CTA's last, kWide: a unit of more than 128 rows, kNone: the CTA has no
+                       // tile, kFresh: the tile has rows that the append writes
   int32_t seg;         // segments of the CTA before this one
   int32_t b, h, first; // sequence, kv head, the unit's first row
   int32_t tile, n;     // of the unit, and how many of the segment are left
@@ -85,7 +86,7 @@ struct CkCfg {
   static constexpr int OFF_QS = OFF_BAR;                // the queries' scales, then what the second warps hand over
   static constexpr int OFF_X = OFF_QS + CK_ROWS * 4;
   static constexpr int OFF_BARS = OFF_X + 128 * 16;
-  static constexpr int N_BAR = 2 * 8 + 3 * kSlots + 5;
+  static constexpr int N_BAR = 2 * 9 + 3 * kSlots + 5;
   static constexpr int OFF_MISC = OFF_BARS + N_BAR * 8;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;    // + slack for 1024-byte alignment
   static_assert(SMEM <= 232448, "shared memory per CTA");
@@ -96,8 +97,27 @@ __host__ __device__ constexpr uint32_t idesc_f16_m128(int n, bool b_mn_major) {
   return (1u << 4) | ((b_mn_major ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// A bounded wait that gives up once another thread has aborted the CTA.  The thread
+// sleeps some microseconds at a time: warps that poll take issue slots from the rest.
 __device__ __forceinline__ bool ck_slow_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
-  return wait_or_abort(bar, parity, abort_flag, err);
+  const long long t0 = clock64();
+  for (;;) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(20000u)
+        : "memory");
+    if (done) return true;
+    if (*abort_flag) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *abort_flag = 1;
+      atomicOr(err, kErrTimeout);
+      return false;
+    }
+  }
 }
 __device__ __forceinline__ bool ck_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
   return mbar_try_wait(bar, parity) || ck_slow_wait(bar, parity, abort_flag, err);
@@ -109,18 +129,14 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
   return r;
 }
-__device__ __forceinline__ float2 f32_of_f16x2(uint32_t h) {
-  float2 f;
-  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\tcvt.f32.f16 %1, hi;\n\t}"
-      : "=f"(f.x), "=f"(f.y)
-      : "r"(h));
-  return f;
-}
 // Two e4m3 codes to fp16 (exact).
 __device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t codes) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)codes));
   return r;
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
 }
 __device__ __forceinline__ uint64_t pack_f32x2(float2 a) {
   uint64_t r;
@@ -273,9 +289,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   float4* hand = reinterpret_cast<float4*>(smem + C::OFF_X);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);   // two each: of a row tile, or of a stage
   uint64_t* s_full = q_full + 2;
-  uint64_t* p_full = s_full + 2;
-  uint64_t* o_done = p_full + 2;
-  uint64_t* k_full = o_done + 2;
+  uint64_t* p_full = s_full + 4;
+  uint64_t* k_full = p_full + 4;
   uint64_t* k_empty = k_full + 2;
   uint64_t* v_full = k_empty + 2;
   uint64_t* v_empty = v_full + 2;
@@ -285,7 +300,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   uint64_t* handed = seg_full + kSlots;
   uint64_t* q_free = handed + 1;
   uint64_t* mma_done = q_free + 1;
-  uint64_t* never = mma_done + 1;   // test hook: nothing arrives
+  uint64_t* never = mma_done + 2;   // test hook: nothing arrives
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
   volatile int* nan_seg = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);   // [4]: segment + 1 with NaN values some rows do not see
@@ -302,13 +317,14 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   } else if (warp == 17 && lane == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&q_full[i], 4);   // one arrival per warp
-      mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
-      mbar_init(&o_done[i], 1);
+      for (int k = 0; k < 2; ++k) {
+        mbar_init(&s_full[2 * i + k], 1);
+        mbar_init(&p_full[2 * i + k], 4);
+      }
       mbar_init(&k_full[i], 4);
-      mbar_init(&k_empty[i], 1);
+      mbar_init(&k_empty[i], 8);   // softmax warps; of a narrow unit four, twice
       mbar_init(&v_full[i], 4);
-      mbar_init(&v_empty[i], 1);
+      mbar_init(&v_empty[i], 8);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&slot_full[i], 1);
@@ -316,14 +332,18 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       mbar_init(&seg_full[i], 1);
     }
     mbar_init(handed, 4);
-    mbar_init(q_free, 1);
-    mbar_init(mma_done, 1);
+    mbar_init(q_free, 2);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&mma_done[i], 1);
+    }
     mbar_init(never, 1);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) nan_seg[i] = 0;
     fence_barrier_init();
   }
-  grid_wait();
+  // Behind its own append (p.early) the launch reads before the wait what no append
+  // writes: everything but the pages from the one that the length ends in on.
+  if (!p.early) grid_wait();
   grid_release();
   if (warp == 0) {
     // the map, 32 sequences at a time
@@ -423,7 +443,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           r.diag = n + first / G + 1 - r.key0;
           r.ctas = sg.t0 == 0 && !sg.whole() ? cut.of(sg.place + sg.tiles - 1) - cta + 1 : 0;
           const bool ends = sg.t0 + sg.n < sg.tiles || sg.place + sg.tiles + kChunkUnitTiles >= x1;
-          r.flags = (sg.whole() ? kWhole : 0u) | (ends ? kEnd : 0u) | (all - first > 128 ? kWide : 0u);
+          r.flags = (r.key0 + r.rows > n / p.pool.page * p.pool.page ? kFresh : 0u) | (sg.whole() ? kWhole : 0u) | (ends ? kEnd : 0u) | (all - first > 128 ? kWide : 0u);
           if (16 * g < r.rows) {
             r.id = p.page_table[(size_t)sg.b * p.max_pages + (r.key0 + 16 * g) / p.pool.page];
             if (r.id < 0) r.id = -2;
@@ -446,6 +466,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         float ks = 0.f, vs = 0.f;
         const size_t block = cur.id >= 0 ? (size_t)cur.id * p.pool.n_kv + cur.h : 0;
         const size_t row = block * p.pool.page + (cur.key0 + 16 * g) % p.pool.page;
+        if (__any_sync(0xffffffffu, cur.on && (cur.flags & kFresh))) grid_wait();
         if (cur.id >= 0) {
           ks = p.pool.scales[0][block];
           vs = p.pool.scales[1][block];
@@ -495,79 +516,75 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         cur = nxt;
         j += 4;
       }
-    } else if (warp == 17 && lane == 0) {
-      // ---------------- MMA issuer.  A wide unit has two row tiles, which take turns:
-      // while the softmax of one works, the products of the other run.  A narrow one
-      // has a single row tile: its even and odd key tiles take turns, each with scores
-      // and sums of its own.
-      constexpr uint32_t idesc_qk = idesc_f16_m128(CK_KEYS, false);   // B = K (K-major)
+    } else if (warp < 19 && lane == 0) {
+      // ---------------- MMA issuers, one to each half of the softmax: a few MMAs fill
+      // the tensor core's queue, so that a single issuer's waits were time that it stood
+      // still.  A wide unit has two row tiles, one to an issuer.  A narrow one has a
+      // single row tile: one issuer has its even key tiles, the other the odd ones, each
+      // with sums of its own.  Scores are made 64 keys at a time, the two parts of a tile
+      // by turns, so that a part's scores are there while the softmax works on the other
+      // (tensor memory holds no second set of 128; N = 64 costs the scores half again as
+      // much: at 128 bytes of shared memory a cycle Q's operand is what bounds them).
+      constexpr uint32_t idesc_qk = idesc_f16_m128(64, false);   // B = K (K-major)
       constexpr uint32_t idesc_pv = idesc_f16_m128(D, true);          // B = V (MN-major)
-      const uint32_t base = smem_addr(smem);
+      const int m = warp - 17;
+      const uint32_t base = smem_addr(smem), o_col = tmem + C::TMEM_O + m * 128;
       const uint64_t q_desc = sw128_desc(base + C::OFF_Q, 16, 1024), k_desc = sw128_desc(base + C::OFF_K, 16, 1024),
                      v_desc = sw128_desc(base + C::OFF_V, 16384, 1024);
       auto wait = [&](uint64_t* bar, uint32_t parity) { return ck_wait(bar, parity, abort_flag, p.err); };
       bool ok = true;
-      uint32_t np = 0;   // bit m: parity of p_full[m]
+      int np = 0;   // tiles whose weights were seen
       for (int j = 0, seg = 0; ok; ++seg) {
         ok = wait(&seg_full[j % kSlots], (j / kSlots) & 1);
         if (!ok) break;
         const TileSlot& s = slots[j % kSlots];
         const uint32_t flags = s.flags;
         if (flags & kNone) break;
-        const int n = s.n, wide = (flags & kWide) ? 1 : 0, step = 2 - wide;
+        const int n = s.n, wide = (flags & kWide) ? 1 : 0, step = 2 - wide, t0 = wide ? 0 : m;
+        const uint64_t q = q_desc + (uint32_t)(wide ? m : 0) * (C::TILE >> 4);
         ok = wait(&q_full[0], seg & 1) && wait(&q_full[1], seg & 1);
-        // P V of tile t, then the scores of the next, which take the weights' place
+        if (t0 >= n) mbar_arrive(q_free);
+        // P V of a part of tile t, then the same part's scores of the next, which take
+        // the weights' place
 #pragma unroll 1
-        for (int t = -step; ok && t < n; ++t) {
+        for (int t = t0 - step; ok && t < n; t += step) {
           const int jt = j + t, tn = t + step, jn = j + tn;
+          const uint64_t v = v_desc + (uint32_t)(jt & 1) * (C::TILE >> 4), k = k_desc + (uint32_t)(jn & 1) * (C::TILE >> 4);
+          if (tn < n) ok = wait(&k_full[jn & 1], (jn >> 1) & 1);
+          if (ok && t >= t0) ok = wait(&v_full[jt & 1], (jt >> 1) & 1);
 #pragma unroll 1
-          for (int i = 0; i <= wide; ++i) {
-            const int m = wide ? i : t & 1;
-            const uint32_t s_col = tmem + m * 128;
-            if (t >= 0) {
-              ok = (i > 0 || wait(&v_full[jt & 1], (jt >> 1) & 1)) && wait(&p_full[m], np >> m & 1);
+          for (int part = 0; ok && part < 2; ++part) {
+            const uint32_t s_col = tmem + m * 128 + part * 64;
+            if (t >= t0) {
+              ok = wait(&p_full[2 * m + part], np & 1);
               if (!ok) break;
-              np ^= 1u << m;
               tc_fence_after();
-              const uint64_t v = v_desc + (uint32_t)(jt & 1) * (C::TILE >> 4);
 #pragma unroll
-              for (int kk = 0; kk < CK_KEYS / 16; ++kk)
-                mma_bf16_tmem_a(s_col + C::TMEM_O, s_col + kk * 8, v + kk * (2048 >> 4), idesc_pv, t >= step || kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_tmem_a(o_col, s_col + kk * 8, v + (uint32_t)(4 * part + kk) * (2048 >> 4), idesc_pv,
+                                t > t0 || part + kk > 0 ? 1u : 0u);
             }
             if (tn < n) {
-              if (i == 0) {
-                ok = wait(&k_full[jn & 1], (jn >> 1) & 1);
-                if (!ok) break;
-                tc_fence_after();
-              }
-              const uint64_t k = k_desc + (uint32_t)(jn & 1) * (C::TILE >> 4),
-                             q = q_desc + (uint32_t)i * (C::TILE >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t off = (kk / 4) * (16384 >> 4) + (kk % 4) * 2;
-                mma_bf16(s_col, q + off, k + off, idesc_qk, kk > 0 ? 1u : 0u);
+                mma_bf16(s_col, q + off, k + off + (uint32_t)part * (8192 >> 4), idesc_qk, kk > 0 ? 1u : 0u);
               }
-              mma_commit(&s_full[m]);   // P V of the tile before has completed as well
-            } else if (t >= 0) {
-              mma_commit(&o_done[m]);
             }
+            if (tn < n || t >= t0) mma_commit(&s_full[2 * m + part]);
           }
-          if (!ok) break;
-          if (tn < n) {
-            mma_commit(&k_empty[jn & 1]);
-            if (tn == n - 1) mma_commit(q_free);
-          }
-          if (t >= 0) mma_commit(&v_empty[jt & 1]);
+          if (t >= t0) ++np;
+          if (tn < n && tn + step >= n) mma_commit(q_free);
         }
         j += n;
         if (flags & kEnd) break;
       }
       // every MMA issued above must complete before TMEM is released
-      mma_commit(mma_done);
-      mbar_wait(mma_done, 0);
+      mma_commit(&mma_done[m]);
+      mbar_wait(&mma_done[m], 0);
     }
   } else if (warp >= 8) {
-    regs_down<80>();
+    regs_down<64>();
     // ---------------- codes to fp16, warps 8-11 of K, 12-15 of V: a thread has 16
     // codes of a row, 8 (at head_dim 64, 4) times a tile; the next tile's are asked
     // for as soon as the registers are free.  Eight neighbouring lanes have two rows'
@@ -591,6 +608,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       if (!__all_sync(0xffffffffu, ok)) return false;
       const TileSlot& s = slots[j % kSlots];
       const int rows = (s.flags & kNone) ? 0 : s.rows;
+      if (s.flags & kFresh) grid_wait();
 #pragma unroll
       for (int k = 0; k < NP; ++k) {
         const int row = k * RPP + r0, grp = s.grp[row >> 4];
@@ -645,13 +663,13 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       }
     }
   } else {
-    regs_up<128>();
+    regs_up<144>();
     // ---------------- softmax and epilogue: row `row` of the unit
     const int m = warp >> 2;                      // row tile, or parity of the key tiles
     const uint32_t lane_base = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t s_at = lane_base + m * 128, o_at = lane_base + C::TMEM_O + m * 128;
-    int nt = 0;                                   // tiles of this half
-    int ends[2] = {0, 0}, hands = 0;              // segments that the halves had tiles of; that both had of narrow units
+    int ns = 0;                                   // phases of s_full so far: a tile each, and one for a segment's end
+    int hands = 0;                                // narrow segments that both halves had tiles of
     bool ok = true;
     for (int j = 0, seg = 0; ok; ++seg) {
       ok = __all_sync(0xffffffffu, ck_wait(&seg_full[j % kSlots], (j / kSlots) & 1, abort_flag, p.err));
@@ -684,10 +702,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       {
         constexpr int CH = D / 16, RPW = 32 / CH;   // lanes of a row, rows at a time
         const int c = lane % CH;
-        const int base = wide ? tid & ~31 : m * 64 + (warp & 3) * 16, times = (wide ? 32 : 16) / RPW;
-#pragma unroll 1
-        for (int k = 0; k < times; ++k) {
-          const int r = base + k * RPW + lane / CH;   // of the unit
+        // rows behind the last one are left as they are: what comes of them is not used
+        const int base = wide ? m * 128 + (warp & 3) * RPW : warp * RPW, stride = (wide ? 4 : 8) * RPW;
+        const int end = min(rows, wide ? m * 128 + 128 : 128);
+#pragma unroll 2
+        for (int r0 = base; r0 < end; r0 += stride) {
+          const int r = r0 + lane / CH;   // of the unit
           float x[8], y[8];
           uint32_t top = 0;
           if (r < rows) {
@@ -722,7 +742,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           uint8_t* qt = smem + C::OFF_Q + (r >> 7) * C::TILE + rt * 128;
           *reinterpret_cast<uint4*>(qt + ((ux ^ (rt & 7)) << 4)) = make_uint4(hx[0], hx[1], hx[2], hx[3]);
           *reinterpret_cast<uint4*>(qt + (D == 128 ? 16384 : 0) + ((uy ^ (rt & 7)) << 4)) = make_uint4(hy[0], hy[1], hy[2], hy[3]);
-          if (c == 0) q_scale[r] = top < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
+          if (c == 0 && r < rows) q_scale[r] = top < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
         }
         fence_proxy_async();
         __syncwarp();
@@ -745,137 +765,135 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           if (lane == 0) mbar_arrive(&slot_empty[j % kSlots]);
           continue;
         }
-        ok = __all_sync(0xffffffffu, ck_wait(&s_full[m], nt & 1, abort_flag, p.err));
-        if (!ok) break;
-        ++nt;
-        if (warp_live) {
-          tc_fence_after();
-          if (t < step) qs = q_scale[row];
-          const TileSlot& ts = slots[j % kSlots];
-          const int nvis = live ? lim - (t0 + t) * CK_KEYS : 0;
-          float sc = qs * ts.k_scale;   // in range, so that a masked score stays -inf; NaN stays
-          sc = sc < FLT_MIN ? FLT_MIN : sc > FLT_MAX ? FLT_MAX : sc;
-          const uint32_t bad = ts.bad;
-          const int v_exp = ts.v_exp;
-          // One pass, 32 scores at a time: the weights take the place of the scores
-          // read before them.  The row's maximum may lag behind by kRescaleLog2; where
-          // it is further behind (seldom), what was computed with it is brought down:
-          // the sums, this tile's weights so far, and, at the end, O.  The loop is
-          // rolled: unrolled code did not stay in the instruction cache, and the warp
-          // that issues the MMAs starved.
-          const bool partial = nvis < CK_KEYS || bad;
-          const float2 sc2 = make_float2(sc, sc);
-          float alpha = 1.f;   // what O is multiplied by
-          if (v_exp > v_ref) {   // the same in every row
-            if (v_ref != kNoScale) alpha = pow2_float(max(v_ref - v_exp, -126));
-            v_ref = v_exp;
-          }
-          // the tile's V scale over the largest so far goes into the weights' exponent
-          const int v_by = v_exp == kNoScale ? 0 : max(v_exp - v_ref, -60);
-          const float off = kWeightLog2 + (float)v_by, v_inv = pow2_float(-v_by);
-          float2 l4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) l4[i] = make_float2(0.f, 0.f);
-          auto part = [&](int i0, float (&x)[32]) {
-            if (partial) {
-              const int left = nvis - i0;
-              uint32_t vis = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1;
-              if (bad >> (i0 >> 4) & 1) vis &= 0xFFFF0000u;
-              if (bad >> (i0 >> 4) & 2) vis &= 0x0000FFFFu;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = (vis >> i & 1) ? x[i] : -INFINITY;
-            }
-            float tops[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tops[i] = fmaxf(x[8 * i], x[8 * i + 1]);
-#pragma unroll
-            for (int i = 2; i < 8; i += 2)
-#pragma unroll
-              for (int k = 0; k < 4; ++k) tops[k] = fmaxf(tops[k], fmaxf(x[8 * k + i], x[8 * k + i + 1]));
-            const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-            const bool up = top != -INFINITY && top * sc > m_run + kRescaleLog2;
-            if (__any_sync(0xffffffffu, up)) {
-              const float by = up ? ex2_approx(m_run - top * sc) : 1.f;   // 0 for the first scores of a row
-              if (up) m_run = top * sc;
-              alpha *= by;
-              l_run *= by;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) l4[i].x *= by, l4[i].y *= by;
-              if (i0 > 0) {
-                tmem_wait_st();
+        float sc = 0.f, off = 0.f, v_inv = 1.f;
+        uint32_t bad = 0;
+        int nvis = 0;
 #pragma unroll 1
-                for (int c = 0; c < i0 / 2; c += 16) {
-                  float w[16];
-                  tmem_ld_cols<16>(s_at + c, w);
-                  tmem_wait_ld();
+        for (int part = 0; part < 2; ++part) {
+          ok = __all_sync(0xffffffffu, ck_wait(&s_full[2 * m + part], ns & 1, abort_flag, p.err));
+          if (!ok) break;
+          // The products behind these scores have read K, those before them V.  (Before
+          // the wait below: the other part's next scores may need these stages.)
+          if (lane == 0 && part == 1) {
+            mbar_arrive_n(&k_empty[j & 1], step);
+            if (t >= step) mbar_arrive_n(&v_empty[(j - step) & 1], step);
+          }
+          if (warp_live) {
+            tc_fence_after();
+            // The row's maximum may lag behind by kRescaleLog2; where it is further
+            // behind (seldom), the sum and O are brought down.  The weights take the
+            // place of the scores.  (The loop is rolled: unrolled code did not stay in
+            // the instruction cache.)
+            float x[2][32];
+            tmem_ld32(s_at + part * 64, x[0]);
+            tmem_ld32(s_at + part * 64 + 32, x[1]);
+            float alpha = 1.f;   // what O is multiplied by
+            if (part == 0) {
+              const TileSlot& ts = slots[j % kSlots];
+              if (t < step) qs = q_scale[row];
+              nvis = live ? lim - (t0 + t) * CK_KEYS : 0;
+              sc = qs * ts.k_scale;   // in range, so that a masked score stays -inf; NaN stays
+              sc = sc < FLT_MIN ? FLT_MIN : sc > FLT_MAX ? FLT_MAX : sc;
+              bad = ts.bad;
+              const int v_exp = ts.v_exp;
+              if (v_exp > v_ref) {   // the same in every row
+                if (v_ref != kNoScale) alpha = pow2_float(max(v_ref - v_exp, -126));
+                v_ref = v_exp;
+              }
+              // the tile's V scale over the largest so far goes into the weights' exponent
+              const int v_by = v_exp == kNoScale ? 0 : max(v_exp - v_ref, -60);
+              off = kWeightLog2 + (float)v_by;
+              v_inv = pow2_float(-v_by);
+            }
+            tmem_wait_ld();
+            if (nvis < CK_KEYS || bad) {
 #pragma unroll
-                  for (int i = 0; i < 16; ++i) {
-                    const float2 v = f32_of_f16x2(__float_as_uint(w[i]));
-                    w[i] = __uint_as_float(f16x2(v.x * by, v.y * by));
-                  }
-                  tmem_st_cols16(s_at + c, w);
-                }
+              for (int k = 0; k < 2; ++k) {
+                const int i1 = 64 * part + 32 * k, left = nvis - i1;
+                uint32_t vis = left >= 32 ? 0xFFFFFFFFu : left <= 0 ? 0u : (1u << left) - 1;
+                if (bad >> (i1 >> 4) & 1) vis &= 0xFFFF0000u;
+                if (bad >> (i1 >> 4) & 2) vis &= 0x0000FFFFu;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[k][i] = (vis >> i & 1) ? x[k][i] : -INFINITY;
               }
             }
-            const float mu = off - (m_run == -INFINITY ? 0.f : m_run);
-            const float2 mu2 = make_float2(mu, mu);
-            float w[16];
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float2 e = fma2(make_float2(x[i], x[i + 1]), sc2, mu2);
-              e.x = ex2_approx(e.x);
-              e.y = ex2_approx(e.y);
-              l4[i / 2 % 4] = add2(l4[i / 2 % 4], e);
-              w[i / 2] = __uint_as_float(f16x2(e.x, e.y));
-            }
-            tmem_st_cols16(s_at + i0 / 2, w);
-          };
-          float xa[32], xb[32];   // the next scores are on their way while one part's are worked on
-          tmem_ld32(s_at, xa);
+            // The weights are computed from the maximum so far while these scores' is
+            // found, and once more where it is too far above.
+            float w[32];
+            float2 l4[4];
+            const float2 sc2 = make_float2(sc, sc);
 #pragma unroll 1
-          for (int i0 = 0; i0 < CK_KEYS; i0 += 64) {
-            tmem_wait_ld();
-            tmem_ld32(s_at + i0 + 32, xb);
-            part(i0, xa);
-            tmem_wait_ld();
-            if (i0 == 0) tmem_ld32(s_at + 64, xa);
-            part(i0 + 32, xb);
-          }
-          const float2 l2 = add2(add2(l4[0], l4[1]), add2(l4[2], l4[3]));
-          l_run = fmaf(l2.x + l2.y, v_inv, l_run);
-          if (t >= step && __any_sync(0xffffffffu, alpha != 1.f)) {   // (the scores came behind the P V before)
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              float o[32];
-              tmem_ld32(o_at + c0, o);
-              tmem_wait_ld();
+            for (;;) {
+              const float mu = off - (m_run == -INFINITY ? 0.f : m_run);
+              const float2 mu2 = make_float2(mu, mu);
+              float tops[4];
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] *= alpha;
-              tmem_st32(o_at + c0, o);
+              for (int i = 0; i < 4; ++i) {
+                l4[i] = make_float2(0.f, 0.f);
+                tops[i] = -INFINITY;
+              }
+#pragma unroll
+              for (int i = 0; i < 64; i += 2) {
+                const float a = x[i / 32][i % 32], b = x[i / 32][i % 32 + 1];
+                tops[i / 2 % 4] = fmaxf(tops[i / 2 % 4], fmaxf(a, b));
+                float2 e = fma2(make_float2(a, b), sc2, mu2);
+                e.x = ex2_approx(e.x);
+                e.y = ex2_approx(e.y);
+                l4[i / 2 % 4] = add2(l4[i / 2 % 4], e);
+                w[i / 2] = __uint_as_float(f16x2(e.x, e.y));
+              }
+              const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+              const bool up = top != -INFINITY && top * sc > m_run + kRescaleLog2;
+              if (!__any_sync(0xffffffffu, up)) break;
+              if (up) {
+                const float by = ex2_approx(m_run - top * sc);   // 0 for the first scores of a row
+                m_run = top * sc;
+                alpha *= by;
+                l_run *= by;
+              }
             }
+            if ((t >= step || part == 1) && __any_sync(0xffffffffu, alpha != 1.f)) {
+              // what was added to O is there once the other part's next scores are
+              ok = __all_sync(0xffffffffu, ck_wait(&s_full[2 * m + 1 - part], (ns + part) & 1, abort_flag, p.err));
+              if (!ok) break;
+              tc_fence_after();
+#pragma unroll 1
+              for (int c0 = 0; c0 < D; c0 += 16) {
+                float o[16];
+                tmem_ld_cols<16>(o_at + c0, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] *= alpha;
+                tmem_st_cols16(o_at + c0, o);
+              }
+            }
+            tmem_st32(s_at + part * 64, w);
+            const float2 l2 = add2(add2(l4[0], l4[1]), add2(l4[2], l4[3]));
+            l_run = fmaf(l2.x + l2.y, v_inv, l_run);
+            tmem_wait_st();
           }
-          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&p_full[2 * m + part]);
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(&p_full[m]);
-          mbar_arrive(&slot_empty[j % kSlots]);
-        }
+        if (!ok) break;
+        ++ns;
+        if (lane == 0) mbar_arrive(&slot_empty[j % kSlots]);
       }
       if (!ok) break;
       // ---- epilogue
       const bool mine = wide || m == 0 || tiles > 1;   // this half had a tile
       if (mine) {
-        ok = __all_sync(0xffffffffu, ck_wait(&o_done[m], ends[m] & 1, abort_flag, p.err));
+        ok = __all_sync(0xffffffffu, ck_wait(&s_full[2 * m + 1], ns & 1, abort_flag, p.err));
         if (!ok) break;
+        ++ns;
+        // this half's last tile: j - 1, or the one before it
+        if (lane == 0) mbar_arrive_n(&v_empty[(j - 1 - (wide || ((tiles - 1) & 1) == m ? 0 : 1)) & 1], step);
       }
-      const int ends1 = ends[1];
-      ++ends[0];
-      if (wide || tiles > 1) ++ends[1];
       const bool two = !wide && tiles > 1;   // a narrow unit's halves are added up by the first
       float4 other = make_float4(-INFINITY, 0.f, 0.f, 0.f);   // m, l, 2^v_ref of the second half
       if (two && m == 1) {
+        tc_fence_before();   // its sums are complete
         if (warp_live) hand[row] = make_float4(m_run, l_run, v_ref == kNoScale ? 0.f : pow2_float(v_ref), 0.f);
         __syncwarp();
         if (lane == 0) mbar_arrive(handed);
@@ -885,8 +903,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         continue;
       }
       if (two) {
-        ok = __all_sync(0xffffffffu, ck_wait(handed, hands++ & 1, abort_flag, p.err) &&
-                                         ck_wait(&o_done[1], ends1 & 1, abort_flag, p.err));
+        ok = __all_sync(0xffffffffu, ck_wait(handed, hands++ & 1, abort_flag, p.err));
         if (!ok) break;
         if (warp_live) other = hand[row];
       }
@@ -928,6 +945,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         }
         if (!live) continue;
         if (nan) {   // values that are not numbers, for the rows that see them
+          grid_wait();
           const int end = min(lim, (t0 + tiles) * CK_KEYS);
           for (int key = max(n + first / G + 1, t0 * CK_KEYS); key < end; ++key) {
             const int id = p.page_table[(size_t)b * p.max_pages + key / p.pool.page];
@@ -955,6 +973,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       if (flags & kEnd) break;
     }
   }
+  grid_wait();   // the launch completes only behind the append
   tc_fence_before();
   __syncthreads();
   if (warp == 19) {

@@ -115,6 +115,7 @@ struct ChunkParams {
   float2* part_ml;               // [2 * CTAs][part_rows] (m, l) of shared units
   float4* part_o;                // [2 * CTAs][d / 4][part_rows] their O
   int32_t batch, t_len, n_q, group, max_pages, max_keys, table_rows, row_at_length, part_rows, inject_timeout;
+  int32_t early;                 // right behind its own append
   float scale_log2;
 };
 constexpr int kMaxChunkCtas = 160;
