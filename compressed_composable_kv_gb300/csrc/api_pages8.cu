@@ -69,17 +69,18 @@ AttendWs attend_workspace(const c2kv_geometry* g, int sms) {
   return w;
 }
 
-// Scratch of a chunk's attention: what is shared by whom, then two partial
-// results per CTA.
+// Scratch of a chunk's attention: what is shared by whom, the queries' scales,
+// then two partial results per CTA.
 struct ChunkWs {
-  size_t ml_off, o_off, total;
+  size_t q_off, ml_off, o_off, total;
 };
 
-ChunkWs chunk_workspace(const c2kv_geometry* g, int t_len, int sms) {
+ChunkWs chunk_workspace(const c2kv_geometry* g, int batch, int t_len, int wide, int sms) {
   const size_t ctas = std::min(sms, kMaxChunkCtas);
-  const size_t rows = 2 * ctas * chunk_part_rows(t_len, g->n_q_heads / g->n_kv_heads);
+  const size_t rows = 2 * ctas * chunk_part_rows(t_len, g->n_q_heads / g->n_kv_heads, wide);
   ChunkWs w;
-  w.ml_off = up256(ctas * 8 * sizeof(int32_t));
+  w.q_off = up256(ctas * 8 * sizeof(int32_t));
+  w.ml_off = w.q_off + up256((size_t)batch * t_len * g->n_q_heads * sizeof(float));
   w.o_off = w.ml_off + up256(rows * sizeof(float2));
   w.total = w.o_off + up256(rows * g->head_dim * sizeof(float));
   return w;
@@ -271,7 +272,9 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
 size_t c2kv_attend_pages8_chunk_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t t_len,
                                                int32_t max_keys) {
   if (api_check_geom(geom) != C2KV_OK || batch < 1 || batch > kMaxPagedSeqs || t_len < 1 || max_keys < 1) return 0;
-  return chunk_workspace(geom, t_len, api_sm_count_for_sizing()).total;
+  const int sms = std::min(api_sm_count_for_sizing(), kMaxChunkCtas);
+  const int wide = chunk_wide(batch, geom->n_kv_heads, t_len, geom->n_q_heads / geom->n_kv_heads, max_keys, sms);
+  return chunk_workspace(geom, batch, t_len, wide, sms).total;
 }
 
 c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages8* pages, int32_t layer, int32_t batch,
@@ -294,7 +297,8 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
   if (chunk_places(batch, geom->n_kv_heads, t_len, group, max_keys) > INT32_MAX / 2 || (int64_t)t_len * group > INT32_MAX / 2)
     return api_fail(C2KV_EINVAL, "batch * n_q_heads * t_len * max_keys is above 2^30 products of 256 x 128");
   const int sms = std::min(api_sm_count_for_sizing(), kMaxChunkCtas);
-  const ChunkWs w = chunk_workspace(geom, t_len, sms);
+  const int wide = chunk_wide(batch, geom->n_kv_heads, t_len, group, max_keys, sms);
+  const ChunkWs w = chunk_workspace(geom, batch, t_len, wide, sms);
   if (workspace_bytes < w.total || !aligned(workspace, 16))
     return api_fail(C2KV_EINVAL, "workspace too small or not 16-byte aligned");
   s = api_device_state(&put.err, nullptr);
@@ -302,18 +306,23 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
   put.max_rows = max_keys;
   put.row_at_length = (flags & C2KV_DECODE_ROW_AT_LENGTH) != 0 ? 1 : 0;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (k_new) {
-    s = api_launched(launch_pages8_append(put, geom->head_dim, st), "c2kv_attend_pages8_chunk");
-    if (s != C2KV_OK) return s;
-  }
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  put.q = static_cast<const __nv_bfloat16*>(q);
+  put.q16 = static_cast<uint16_t*>(out);
+  put.q_scale = reinterpret_cast<float*>(ws + w.q_off);
+  put.n_q = geom->n_q_heads;
+  put.group = group;
+  put.z0 = k_new ? 0 : 2;
+  put.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)geom->head_dim));
+  s = api_launched(launch_pages8_append(put, geom->head_dim, st), "c2kv_attend_pages8_chunk");
+  if (s != C2KV_OK) return s;
   ChunkParams p;
   std::memset(&p, 0, sizeof(p));
   p.pool = put.pool;
   p.page_table = page_table;
   p.n_cached = n_cached_dev;
   p.n_new = n_new_dev;
-  p.q = static_cast<const __nv_bfloat16*>(q);
-  p.tab = put.tab;
+  p.q_scale = put.q_scale;
   p.rope_row = rope_row_dev;
   p.out = static_cast<__nv_bfloat16*>(out);
   p.err = put.err;
@@ -325,14 +334,12 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
   p.table_rows = table_rows;
   p.row_at_length = put.row_at_length;
   p.group = group;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.desc = reinterpret_cast<int32_t*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
   p.part_o = reinterpret_cast<float4*>(ws + w.o_off);
-  p.part_rows = chunk_part_rows(t_len, group);
+  p.wide = wide;
+  p.part_rows = chunk_part_rows(t_len, group, wide);
   p.inject_timeout = api_take_injected_timeout();
-  p.early = k_new != nullptr ? 1 : 0;
-  p.scale_log2 = (float)(1.4426950408889634 / std::sqrt((double)geom->head_dim));
   s = api_launched(launch_attend_chunk8(p, geom->head_dim, sms, st), "c2kv_attend_pages8_chunk");
   if (s != C2KV_OK) return s;
   return api_launched(launch_attend_chunk8_merge(p, geom->head_dim, sms, st), "c2kv_attend_pages8_chunk");

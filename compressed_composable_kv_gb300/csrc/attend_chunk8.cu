@@ -3,7 +3,7 @@
 //   s_j = (R q . K_j) / sqrt(d),  out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)
 // over the rows j up to the token's own; K_j and V_j = code * scale of their page.
 //
-// A unit is 256 (token, query head) rows of one (sequence, kv head), token-major,
+// A unit is 256 (or 128) (token, query head) rows of one (sequence, kv head), token-major,
 // against the key tiles (128 rows) that they see.  Every e4m3 code is an fp16
 // number, so a tile's codes are brought to fp16 once for all 256 rows, and both
 // products run as kind::f16 (fp32 accumulators): the keys and values lose
@@ -39,6 +39,7 @@ constexpr int CK_KEYS = 128;       // keys of a tile
 constexpr int kSlots = 8;          // tiles whose pages are known ahead
 constexpr int kChunkMinTiles = 2;  // tiles of a CTA below which fewer CTAs work
 constexpr int kChunkUnitTiles = 2; // what a unit's begin and end cost, in tiles
+constexpr int kChunkFewTiles = 8;  // see chunk_wide
 constexpr int kNoScale = -1000;    // exponent of a tile without a page
 constexpr float kRescaleLog2 = 8.f;   // a row's maximum may lag behind by this (weights up to 2^15, sums exact)
 constexpr float kWeightLog2 = 7.f;
@@ -83,8 +84,7 @@ struct CkCfg {
   static constexpr int OFF_SLOT = 6 * TILE;
   static constexpr int OFF_MAP = OFF_SLOT + kSlots * (int)sizeof(TileSlot);
   static constexpr int OFF_BAR = OFF_MAP + (int)((sizeof(ChunkMap) + 15) / 16 * 16);
-  static constexpr int OFF_QS = OFF_BAR;                // the queries' scales, then what the second warps hand over
-  static constexpr int OFF_X = OFF_QS + CK_ROWS * 4;
+  static constexpr int OFF_X = OFF_BAR;                 // what the second softmax warps hand over
   static constexpr int OFF_BARS = OFF_X + 128 * 16;
   static constexpr int N_BAR = 2 * 9 + 3 * kSlots + 5;
   static constexpr int OFF_MISC = OFF_BARS + N_BAR * 8;
@@ -198,27 +198,29 @@ __device__ __forceinline__ void tmem_st_cols16(uint32_t taddr, const float (&r)[
 }
 
 // ---------------------------------------------------------------- work
-// Unit i of a sequence (n rows held, `count` new tokens, G heads of a group)
-// sees n + e(i) keys, e(i) = floor((256 i + 255) / G) + 1 tokens having rows up to
-// its end, `count` for the last: ceil((n + e(i)) / 128) = floor((2 i + c) / G)
-// tiles with c = floor((255 + G (n + 128)) / 128).
+// Unit i of a sequence (n rows held, `count` new tokens, G heads of a group) has
+// 128 w rows, w = 1 or 2, and sees n + e(i) keys, e(i) = floor((128 w (i + 1) - 1) / G)
+// + 1 tokens having rows up to its end, `count` for the last: ceil((n + e(i)) / 128) =
+// floor((w i + c) / G) tiles with c = floor((128 w - 1 + G (n + 128)) / 128).
 struct UnitMath {
-  int c, q, r, G, units, last;   // c = G q + r; last: tiles of the last unit
+  int c, q, r, G, w, units, last;   // c = G q + r; last: tiles of the last unit
 
-  __device__ __forceinline__ UnitMath(int n, int count, int g) : G(g) {
-    c = (int)((255 + (int64_t)g * (n + 128)) >> 7);
+  __device__ __forceinline__ UnitMath(int n, int count, int g, int wide) : G(g), w(wide) {
+    c = (int)((128 * w - 1 + (int64_t)g * (n + 128)) >> 7);
     q = c / g;
     r = c - q * g;
-    units = (int)(((int64_t)count * g + CK_ROWS - 1) / CK_ROWS);
+    units = (int)(((int64_t)count * g + 128 * w - 1) / (128 * w));
     last = (n + count + CK_KEYS - 1) / CK_KEYS;
   }
-  __device__ __forceinline__ int tiles(int i) const { return i == units - 1 ? last : (2 * i + c) / G; }
-  // sum of floor((2 k + r) / G) over k < v <= G: the terms are 0, 1 or 2
-  __device__ __forceinline__ int part(int v) const { return max(0, v - (G - r + 1) / 2) + max(0, v - (2 * G - r + 1) / 2); }
+  __device__ __forceinline__ int tiles(int i) const { return i == units - 1 ? last : (w * i + c) / G; }
+  // sum of floor((w k + r) / G) over k < v <= G: the terms are 0 to w
+  __device__ __forceinline__ int part(int v) const {
+    return w == 1 ? max(0, v - (G - r)) : max(0, v - (G - r + 1) / 2) + max(0, v - (2 * G - r + 1) / 2);
+  }
   // places before unit i, with i = G u + v
   __device__ __forceinline__ int before(int i) const {
     const int m = min(i, units - 1), u = m / G, v = m - u * G;
-    return m * q + G * u * (u - 1) + 2 * u * v + u * part(G) + part(v) + (i == units ? last : 0) + i * kChunkUnitTiles;
+    return m * q + w * (G * (u * (u - 1) / 2) + u * v) + u * part(G) + part(v) + (i == units ? last : 0) + i * kChunkUnitTiles;
   }
 };
 
@@ -233,6 +235,7 @@ struct CkCut {   // CTA c owns places [first(c), first(c + 1))
 
 __device__ __forceinline__ int ck_seq_of(const int32_t* from, int batch, int x) {   // the last b with from[b] <= x
   int lo = 0, hi = batch;
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (from[mid] <= x) lo = mid;
@@ -248,15 +251,16 @@ struct CkSeg {
 };
 
 // The CTA's next segment at place x or behind it; false: none before x1.
-__device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, int x, int x1, CkSeg& s) {
+__device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, int w, int x, int x1, CkSeg& s) {
   for (;;) {
     if (x >= x1) return false;
     s.b = ck_seq_of(m.start, batch, x);
-    const UnitMath um(m.n[s.b], m.count[s.b], G);
+    const UnitMath um(m.n[s.b], m.count[s.b], G, w);
     const int per = m.per[s.b], r = x - m.start[s.b];
     s.h = (int)((uint32_t)r / (uint32_t)per);
     const int at = r - s.h * per;
     int lo = 0, hi = um.units;
+#pragma unroll 1
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (um.before(mid) <= at) lo = mid;
@@ -273,9 +277,9 @@ __device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, i
     x = s.place + s.tiles + kChunkUnitTiles;
   }
 }
-__device__ __forceinline__ bool ck_next(const ChunkMap& m, int batch, int G, int x1, CkSeg& s) {
+__device__ __forceinline__ bool ck_next(const ChunkMap& m, int batch, int G, int w, int x1, CkSeg& s) {
   const int x = s.place + s.t0 + s.n;
-  return ck_seg_at(m, batch, G, s.t0 + s.n == s.tiles ? x + kChunkUnitTiles : x, x1, s);
+  return ck_seg_at(m, batch, G, w, s.t0 + s.n == s.tiles ? x + kChunkUnitTiles : x, x1, s);
 }
 
 template <int D>
@@ -285,7 +289,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TileSlot* slots = reinterpret_cast<TileSlot*>(smem + C::OFF_SLOT);
   ChunkMap& M = *reinterpret_cast<ChunkMap*>(smem + C::OFF_MAP);
-  float* q_scale = reinterpret_cast<float*>(smem + C::OFF_QS);
   float4* hand = reinterpret_cast<float4*>(smem + C::OFF_X);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + C::OFF_BARS);   // two each: of a row tile, or of a stage
   uint64_t* s_full = q_full + 2;
@@ -341,9 +344,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
     for (int i = 0; i < 4; ++i) nan_seg[i] = 0;
     fence_barrier_init();
   }
-  // Behind its own append (p.early) the launch reads before the wait what no append
-  // writes: everything but the pages from the one that the length ends in on.
-  if (!p.early) grid_wait();
+  // The launch before is the call's own, of the append and the queries, and itself
+  // began behind what came before it: what it does not write is read without a wait,
+  // everything but the queries and the pages from the one that the length ends in on.
   grid_release();
   if (warp == 0) {
     // the map, 32 sequences at a time
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       }
       int per = 0, all = 0;
       if (count > 0) {
-        const UnitMath um(n, count, G);
+        const UnitMath um(n, count, G, p.wide);
         per = um.before(um.units);
         all = (per - um.units * kChunkUnitTiles) * p.pool.n_kv;
       }
@@ -412,7 +415,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       const int g = lane & 7;
       CkSeg sg;
       int seg = 0, at = lane >> 3, j = lane >> 3;   // tile `at` of segment `seg`, the CTA's j-th
-      bool more = ck_seg_at(M, p.batch, G, x0, x1, sg);
+      bool more = ck_seg_at(M, p.batch, G, p.wide, x0, x1, sg);
       int done = 0;   // tiles of the segments before
       struct Ref {
         int32_t id, key0, rows, diag, ctas;   // id: -1 no page here, -2 outside the pool
@@ -426,12 +429,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         while (more && at - done >= sg.n) {
           done += sg.n;
           ++seg;
-          more = ck_next(M, p.batch, G, x1, sg);
+          more = ck_next(M, p.batch, G, p.wide, x1, sg);
         }
         r.on = more;
         if (more) {
-          const int n = M.n[sg.b], first = sg.i * CK_ROWS, t = at - done, all = M.count[sg.b] * G;
-          const int end = n + min((first + CK_ROWS - 1) / G + 1, M.count[sg.b]);
+          const int n = M.n[sg.b], unit = 128 * p.wide, first = sg.i * unit, t = at - done, all = M.count[sg.b] * G;
+          const int end = n + min((first + unit - 1) / G + 1, M.count[sg.b]);
           r.b = sg.b;
           r.h = sg.h;
           r.first = first;
@@ -443,7 +446,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           r.diag = n + first / G + 1 - r.key0;
           r.ctas = sg.t0 == 0 && !sg.whole() ? cut.of(sg.place + sg.tiles - 1) - cta + 1 : 0;
           const bool ends = sg.t0 + sg.n < sg.tiles || sg.place + sg.tiles + kChunkUnitTiles >= x1;
-          r.flags = (r.key0 + r.rows > n / p.pool.page * p.pool.page ? kFresh : 0u) | (sg.whole() ? kWhole : 0u) | (ends ? kEnd : 0u) | (all - first > 128 ? kWide : 0u);
+          r.flags = (r.key0 + r.rows > n / p.pool.page * p.pool.page ? kFresh : 0u) | (sg.whole() ? kWhole : 0u) | (ends ? kEnd : 0u) | (min(all - first, unit) > 128 ? kWide : 0u);
           if (16 * g < r.rows) {
             r.id = p.page_table[(size_t)sg.b * p.max_pages + (r.key0 + 16 * g) / p.pool.page];
             if (r.id < 0) r.id = -2;
@@ -679,7 +682,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       if (flags & kNone) break;
       const bool wide = flags & kWide, whole = flags & kWhole;
       const int b = head_slot.b, h = head_slot.h, first = head_slot.first, t0 = head_slot.tile, tiles = head_slot.n;
-      const int n = M.n[b], rows = min(M.count[b] * G - first, CK_ROWS);   // of the unit
+      const int n = M.n[b], rows = min(M.count[b] * G - first, 128 * p.wide);   // of the unit
       if (tid == 0 && head_slot.ctas > 0) {
         // this CTA has the unit's first tile: it says who has the others
         int32_t* d = p.desc + cta * 8;
@@ -693,62 +696,31 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       const int tok = (first + row) / G, head = h * G + (first + row) % G;
       const bool live = row < rows;
       const bool warp_live = (row & ~31) < rows;
-      // ---- the queries: rotated, times log2(e)/sqrt(d), over a power of two of
-      // the row, in fp16.  8 (4) lanes to a row.
+      // ---- the queries, as the launch before left them
+      float qs = 0.f;
       if (seg > 0) {
         ok = __all_sync(0xffffffffu, ck_wait(q_free, (seg - 1) & 1, abort_flag, p.err));
         if (!ok) break;
       }
       {
-        constexpr int CH = D / 16, RPW = 32 / CH;   // lanes of a row, rows at a time
-        const int c = lane % CH;
         // rows behind the last one are left as they are: what comes of them is not used
-        const int base = wide ? m * 128 + (warp & 3) * RPW : warp * RPW, stride = (wide ? 4 : 8) * RPW;
-        const int end = min(rows, wide ? m * 128 + 128 : 128);
-#pragma unroll 2
-        for (int r0 = base; r0 < end; r0 += stride) {
-          const int r = r0 + lane / CH;   // of the unit
-          float x[8], y[8];
-          uint32_t top = 0;
-          if (r < rows) {
-            const int rq = first + r, tk = rq / G;
-            const uint4* src = reinterpret_cast<const uint4*>(p.q + (((size_t)b * p.t_len + tk) * p.n_q + h * G + rq % G) * D);
-            unpack8(src[c], x);
-            unpack8(src[c + CH], y);
-            const CosSin2* t = p.tab + ((size_t)M.rope[b] + tk) * (D / 2) + c * 8;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float2 co = *reinterpret_cast<const float2*>(t + e), si = *reinterpret_cast<const float2*>(&t[e].sh);
-              const float a = (x[e] * co.x - y[e] * si.x) * p.scale_log2;
-              y[e] = (y[e] * co.x + x[e] * si.x) * p.scale_log2;
-              x[e] = a;
-              top = max(top, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
-          }
-#pragma unroll
-          for (int off = CH / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-          const int e = top < 0x7F800000u ? scale_exponent(top) : 0;   // a query that is not finite answers NaN
-          const float inv = pow2_float(-e);
-          uint32_t hx[4], hy[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            hx[i] = f16x2(x[2 * i] * inv, x[2 * i + 1] * inv);
-            hy[i] = f16x2(y[2 * i] * inv, y[2 * i + 1] * inv);
-          }
-          const int rt = r & 127, ux = c, uy = D == 128 ? c : c + 4;
-          uint8_t* qt = smem + C::OFF_Q + (r >> 7) * C::TILE + rt * 128;
-          *reinterpret_cast<uint4*>(qt + ((ux ^ (rt & 7)) << 4)) = make_uint4(hx[0], hx[1], hx[2], hx[3]);
-          *reinterpret_cast<uint4*>(qt + (D == 128 ? 16384 : 0) + ((uy ^ (rt & 7)) << 4)) = make_uint4(hy[0], hy[1], hy[2], hy[3]);
-          if (c == 0 && r < rows) q_scale[r] = top < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
+        constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows at a time
+        const int c = lane % LPR, begin = (wide ? m * 128 : m * 64) + (warp & 3) * (wide ? 32 : 16);
+        const int end = min(rows, begin + (wide ? 32 : 16));
+        grid_wait();
+        for (int r = begin + lane / LPR; r < end; r += RPI) {
+          const int rq = first + r, rt = r & 127;
+          const __nv_bfloat16* src = p.out + (((size_t)b * p.t_len + rq / G) * p.n_q + h * G + rq % G) * D + c * 8;
+          const uint32_t dst = smem_addr(smem + C::OFF_Q) + (r >> 7) * C::TILE + (c >> 3) * 16384 + rt * 128 + (((c & 7) ^ (rt & 7)) << 4);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
         }
+        if (live) qs = p.q_scale[((size_t)b * p.pool.n_kv + h) * p.t_len * G + first + row];
+        asm volatile("cp.async.wait_all;" ::: "memory");
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[m]);
       }
-      float m_run = -INFINITY, l_run = 0.f, qs = 0.f;
+      float m_run = -INFINITY, l_run = 0.f;
       int v_ref = kNoScale;
       const int lim = n + tok + 1;   // keys that the row sees
       if (p.inject_timeout && (cta & 1) == 0 && seg == 0) {
@@ -790,7 +762,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             float alpha = 1.f;   // what O is multiplied by
             if (part == 0) {
               const TileSlot& ts = slots[j % kSlots];
-              if (t < step) qs = q_scale[row];
               nvis = live ? lim - (t0 + t) * CK_KEYS : 0;
               sc = qs * ts.k_scale;   // in range, so that a masked score stays -inf; NaN stays
               sc = sc < FLT_MIN ? FLT_MIN : sc > FLT_MAX ? FLT_MAX : sc;
@@ -984,11 +955,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
 
 // Joins the parts of the units that several CTAs hold.  blockIdx.x: the CTA with
 // the unit's first tile (its part is slot 2 c + 1, those of the CTAs behind it slot
-// 2 c'); blockIdx.y: 32 rows; a lane to a row, a warp to D / 8 columns.
+// 2 c'); blockIdx.y: 32 rows, blockIdx.z: 32 columns; a lane to a row, a warp to four
+// columns.
 constexpr int MG_THREADS = 256;
 template <int D>
 __global__ void __launch_bounds__(MG_THREADS) merge_kernel(const __grid_constant__ ChunkParams p) {
-  constexpr int C4 = D / 4 / 8;
   __shared__ float wts[kMaxChunkCtas][32];
   __shared__ float red[8][32];
   grid_wait();
@@ -999,6 +970,13 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(const __grid_constant
   const int b = d[1], h = d[2], rq = d[3] + row, parts = d[4], G = p.group;
   auto slot = [&](int k) { return (size_t)(2 * ((int)blockIdx.x + k) + (k == 0 ? 1 : 0)); };
   const bool live = row < rows;
+  const int c4 = blockIdx.z * 8 + warp;
+  auto part = [&](int k) { return live ? p.part_o[(slot(k) * (D / 4) + c4) * p.part_rows + row] : make_float4(0.f, 0.f, 0.f, 0.f); };
+  constexpr int AHEAD = 8;   // parts whose loads are in flight, the first since before the weights
+  float4 v[AHEAD];
+#pragma unroll
+  for (int i = 0; i < AHEAD; ++i)
+    if (i < parts) v[i] = part(i);
   float mx = -INFINITY;
   for (int k = warp; k < parts; k += 8) {
     const float m = live ? p.part_ml[slot(k) * p.part_rows + row].x : -INFINITY;
@@ -1022,27 +1000,26 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(const __grid_constant
   l = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) l += red[i][lane];
-  if (!live) return;
-  float4 acc[C4];
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+  for (int k0 = 0; k0 < parts; k0 += AHEAD) {
 #pragma unroll
-  for (int i = 0; i < C4; ++i) acc[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < parts; ++k) {
-    const float w = wts[k][lane];
-    const float4* o = p.part_o + (slot(k) * (D / 4) + warp * C4) * p.part_rows + row;
-#pragma unroll
-    for (int i = 0; i < C4; ++i) {
-      const float4 v = o[(size_t)i * p.part_rows];
-      acc[i].x = fmaf(w, v.x, acc[i].x);
-      acc[i].y = fmaf(w, v.y, acc[i].y);
-      acc[i].z = fmaf(w, v.z, acc[i].z);
-      acc[i].w = fmaf(w, v.w, acc[i].w);
+    for (int i = 0; i < AHEAD; ++i) {
+      if (k0 + i >= parts) break;
+      const float w = wts[k0 + i][lane];
+      acc.x = fmaf(w, v[i].x, acc.x);
+      acc.y = fmaf(w, v[i].y, acc.y);
+      acc.z = fmaf(w, v[i].z, acc.z);
+      acc.w = fmaf(w, v[i].w, acc.w);
     }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint2* dst = reinterpret_cast<uint2*>(p.out + (((size_t)b * p.t_len + rq / G) * p.n_q + h * G + rq % G) * D) + warp * C4;
 #pragma unroll
-  for (int i = 0; i < C4; ++i) dst[i] = make_uint2(pack2(acc[i].x * inv, acc[i].y * inv), pack2(acc[i].z * inv, acc[i].w * inv));
+    for (int i = 0; i < AHEAD; ++i)
+      if (k0 + AHEAD + i < parts) v[i] = part(k0 + AHEAD + i);
+  }
+  if (!live) return;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint2* dst = reinterpret_cast<uint2*>(p.out + (((size_t)b * p.t_len + rq / G) * p.n_q + h * G + rq % G) * D) + c4;
+  *dst = make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
 }
 
 template <int D>
@@ -1076,7 +1053,7 @@ cudaError_t launch_chunk(const ChunkParams& p, int sms, cudaStream_t st) {
 template <int D>
 cudaError_t launch_merge(const ChunkParams& p, int sms, cudaStream_t st) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sms, p.part_rows / 32);
+  cfg.gridDim = dim3((unsigned)sms, p.part_rows / 32, D / 32);
   cfg.blockDim = dim3(MG_THREADS);
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
@@ -1089,12 +1066,22 @@ cudaError_t launch_merge(const ChunkParams& p, int sms, cudaStream_t st) {
 
 }  // namespace
 
-int chunk_part_rows(int t_len, int group) {
-  return (int)std::min<int64_t>(CK_ROWS, ((int64_t)t_len * group + 31) / 32 * 32);
+// 128-row tiles of a unit: one where that leaves each CTA few tiles (a part's sums are
+// half as much to store and to join, which then is much of the time), else two, whose
+// rows share the work of bringing the codes to fp16.
+int chunk_wide(int batch, int n_kv, int t_len, int group, int max_keys, int ctas) {
+  const int64_t rows = (int64_t)t_len * group;
+  if (rows <= 128) return 1;
+  const int64_t tiles = batch * (int64_t)n_kv * ((rows + CK_ROWS - 1) / CK_ROWS) * ((max_keys + CK_KEYS - 1) / CK_KEYS);
+  return tiles < (int64_t)kChunkFewTiles * ctas ? 1 : 2;
+}
+
+int chunk_part_rows(int t_len, int group, int wide) {
+  return (int)std::min<int64_t>(128 * wide, ((int64_t)t_len * group + 31) / 32 * 32);
 }
 
 int64_t chunk_places(int batch, int n_kv, int t_len, int group, int max_keys) {
-  const int64_t units = ((int64_t)t_len * group + CK_ROWS - 1) / CK_ROWS;
+  const int64_t units = ((int64_t)t_len * group + 127) / 128;
   return batch * (int64_t)n_kv * units * ((max_keys + CK_KEYS - 1) / CK_KEYS + kChunkUnitTiles);
 }
 

@@ -68,6 +68,59 @@ __device__ __forceinline__ void tame(uint32_t& w, uint32_t& m) {
   else m = max(m, hi << 16);
 }
 
+// Two fp32 values to fp16, `a` in the low half.
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
+// The queries of rows [row0, end) of a sequence (its first new token at row
+// `first`), head h * G + g: rotated and scaled in fp32, then fp16 over a power of two
+// that brings the largest element of the row to (224, 448].  A warp takes 16 rows, 8
+// (at head_dim 64, 4) lanes to a row.
+template <int D>
+__device__ __noinline__ void put_queries(const PutParams& p, int b, int h, int g, int first, int row0, int end, int rr) {
+  constexpr int CH = D / 16, RPW = 32 / CH;
+  const int lane = threadIdx.x & 31, c = lane % CH;
+#pragma unroll 2
+  for (int r = row0 + lane / CH; r - lane / CH < end; r += RPW) {
+    const bool on = r >= first && r < end;
+    const int t = r - first;
+    const size_t at = (((size_t)b * p.t_len + t) * p.n_q + h * p.group + g) * D;
+    float x[8], y[8];
+    uint32_t top = 0;
+    if (on) {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + at);
+      const uint4 u = src[c], v = src[c + CH];
+      const CosSin2* cs = p.tab + (size_t)(rr + t) * (D / 2) + c * 8;
+      unpack8(u, x);
+      unpack8(v, y);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float co = cs[e].ch, si = cs[e].sh;
+        const float a = (x[e] * co - y[e] * si) * p.scale_log2;
+        y[e] = (y[e] * co + x[e] * si) * p.scale_log2;
+        x[e] = a;
+        top = max(top, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
+      }
+    }
+#pragma unroll
+    for (int off = CH / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (!on) continue;
+    const int e = top < 0x7F800000u ? scale_exponent(top) : 0;   // a query that is not finite answers NaN
+    const float inv = pow2_float(-e);
+    uint4* dst = reinterpret_cast<uint4*>(p.q16 + at);
+    dst[c] = make_uint4(f16x2(x[0] * inv, x[1] * inv), f16x2(x[2] * inv, x[3] * inv), f16x2(x[4] * inv, x[5] * inv),
+                        f16x2(x[6] * inv, x[7] * inv));
+    dst[c + CH] = make_uint4(f16x2(y[0] * inv, y[1] * inv), f16x2(y[2] * inv, y[3] * inv),
+                             f16x2(y[4] * inv, y[5] * inv), f16x2(y[6] * inv, y[7] * inv));
+    if (c == 0)
+      p.q_scale[((size_t)b * p.pool.n_kv + h) * p.t_len * p.group + (size_t)t * p.group + g] =
+          top < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
+  }
+}
+
 // D: head_dim.  APPEND: rows [n_cached, n_cached + new) from the new tokens,
 // K rotated; else rows [0, n_rows) from the bf16 caches.
 // CTAs per SM: append takes 11.5 us at 2 and 12.4 at 3 for 1 x 4000 tokens
@@ -81,7 +134,7 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   extern __shared__ __align__(128) CosSin2 rope_rows[];   // APPEND: 8 KB for each warp
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int b = blockIdx.y / p.pool.n_kv, h = blockIdx.y % p.pool.n_kv;
-  const int kv = blockIdx.z & 1, layer = blockIdx.z >> 1;
+  const int kv = blockIdx.z & 1, layer = blockIdx.z >> 1;   // an append has one layer, and its queries behind V
   const int rows = blockDim.x / 32 * PUT_WARP_ROWS;   // of a CTA
   grid_wait();
   grid_release();
@@ -105,6 +158,10 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   if (row0 >= end || count == 0) return;
   const int page = p.pool.page;
   const int wrow = row0 + warp * PUT_WARP_ROWS;
+  if (APPEND && (int)blockIdx.z + p.z0 >= 2) {
+    put_queries<D>(p, b, h, (int)blockIdx.z + p.z0 - 2, first, wrow, min(end, wrow + PUT_WARP_ROWS), rr);
+    return;
+  }
   const int prow = wrow / page * page;                  // first row of this warp's page
   const bool touched = prow < end && prow + page > first;
   const int pid = touched ? p.page_table[(size_t)b * p.max_pages + wrow / page] : -1;
@@ -339,7 +396,7 @@ cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, c
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st) {
   // rows [n, n + t_len) meet at most this many CTAs' rows
   const int rows = put_rows(p), threads = rows / PUT_WARP_ROWS * 32;
-  const dim3 grid((p.t_len + 2 * rows - 2) / rows, p.batch * p.pool.n_kv, 2);
+  const dim3 grid((p.t_len + 2 * rows - 2) / rows, p.batch * p.pool.n_kv, (p.q ? 2 + p.group : 2) - p.z0);
   return head_dim == 128 ? launch_put<128, true>(p, grid, threads, st) : launch_put<64, true>(p, grid, threads, st);
 }
 

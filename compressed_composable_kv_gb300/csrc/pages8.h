@@ -95,6 +95,15 @@ struct PutParams {
   const CosSin2* tab;
   const int32_t* rope_row;
   int32_t t_len, table_rows;
+  // the queries of the new tokens (chunk attention), rotated, times log2(e) /
+  // sqrt(d), each row as fp16 over a power of two: [batch][t_len][n_q][d] to q16 (the
+  // call's output, until the attention writes it), powers to [batch][n_kv][t_len * G]
+  const __nv_bfloat16* q;        // null: none
+  uint16_t* q16;
+  float* q_scale;
+  int32_t n_q, group;
+  int32_t z0;                    // first blockIdx.z: 0 K, 1 V, 2 + g the g-th query head of the group
+  float scale_log2;
   int32_t row_at_length;         // token i's table row is rope_row + n_cached + i
   int32_t max_rows;              // a sequence that would get more is left out
 };
@@ -106,17 +115,15 @@ struct ChunkParams {
   const int32_t* page_table;
   const int32_t* n_cached;
   const int32_t* n_new;          // null: t_len each
-  const __nv_bfloat16* q;        // [batch][t_len][n_q][d], before RoPE
-  const CosSin2* tab;
-  const int32_t* rope_row;
+  const float* q_scale;          // [batch][n_kv][t_len * G], with the queries in `out` (PutParams::q16)
+  const int32_t* rope_row;       // of a sequence's first new token, to tell what the append leaves out
   __nv_bfloat16* out;            // [batch][t_len][n_q][d]
   unsigned* err;
   int32_t* desc;                 // [CTAs][8] the unit that begins in a CTA and goes on in others: rows (0: none), b, h, first row, CTAs
   float2* part_ml;               // [2 * CTAs][part_rows] (m, l) of shared units
   float4* part_o;                // [2 * CTAs][d / 4][part_rows] their O
   int32_t batch, t_len, n_q, group, max_pages, max_keys, table_rows, row_at_length, part_rows, inject_timeout;
-  int32_t early;                 // right behind its own append
-  float scale_log2;
+  int32_t wide;                  // a unit has 128 * wide rows
 };
 constexpr int kMaxChunkCtas = 160;
 
@@ -189,7 +196,8 @@ cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t 
 cudaError_t launch_attend_pages8(const AttendPages8Params& p, int head_dim, int group, int sms, cudaStream_t st);
 cudaError_t launch_attend_chunk8(const ChunkParams& p, int head_dim, int sms, cudaStream_t st);
 cudaError_t launch_attend_chunk8_merge(const ChunkParams& p, int head_dim, int sms, cudaStream_t st);
-int chunk_part_rows(int t_len, int group);
+int chunk_wide(int batch, int n_kv, int t_len, int group, int max_keys, int ctas);   // ChunkParams::wide
+int chunk_part_rows(int t_len, int group, int wide);
 int64_t chunk_places(int batch, int n_kv, int t_len, int group, int max_keys);   // at most
 size_t move_workspace_ints(int n_pages, int batch, int max_pages);
 cudaError_t launch_pages8_plan(const MoveParams& p, cudaStream_t st);
