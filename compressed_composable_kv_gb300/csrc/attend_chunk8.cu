@@ -40,6 +40,7 @@ constexpr int kSlots = 8;          // tiles whose pages are known ahead
 constexpr int kChunkMinTiles = 2;  // tiles of a CTA below which fewer CTAs work
 constexpr int kChunkUnitTiles = 2; // what a unit's begin and end cost, in tiles
 constexpr int kChunkFewTiles = 8;  // see chunk_wide
+constexpr int kChunkWholeKeys = 512;  // see chunk_whole
 constexpr int kNoScale = -1000;    // exponent of a tile without a page
 constexpr float kRescaleLog2 = 8.f;   // a row's maximum may lag behind by this (weights up to 2^15, sums exact)
 constexpr float kWeightLog2 = 7.f;
@@ -250,26 +251,32 @@ struct CkSeg {
   __device__ __forceinline__ bool whole() const { return n == tiles; }
 };
 
+// The unit at place x, and where in it x is (t0 >= tiles: behind its last tile).
+__device__ __forceinline__ void ck_locate(const ChunkMap& m, int batch, int G, int w, int x, CkSeg& s) {
+  s.b = ck_seq_of(m.start, batch, x);
+  const UnitMath um(m.n[s.b], m.count[s.b], G, w);
+  const int per = m.per[s.b], r = x - m.start[s.b];
+  s.h = (int)((uint32_t)r / (uint32_t)per);
+  const int at = r - s.h * per;
+  int lo = 0, hi = um.units;
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (um.before(mid) <= at) lo = mid;
+    else hi = mid;
+  }
+  s.i = lo;
+  s.tiles = um.tiles(lo);
+  s.t0 = at - um.before(lo);
+  s.place = x - s.t0;
+}
+
 // The CTA's next segment at place x or behind it; false: none before x1.
 __device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, int w, int x, int x1, CkSeg& s) {
+#pragma unroll 1
   for (;;) {
     if (x >= x1) return false;
-    s.b = ck_seq_of(m.start, batch, x);
-    const UnitMath um(m.n[s.b], m.count[s.b], G, w);
-    const int per = m.per[s.b], r = x - m.start[s.b];
-    s.h = (int)((uint32_t)r / (uint32_t)per);
-    const int at = r - s.h * per;
-    int lo = 0, hi = um.units;
-#pragma unroll 1
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (um.before(mid) <= at) lo = mid;
-      else hi = mid;
-    }
-    s.i = lo;
-    s.tiles = um.tiles(lo);
-    s.t0 = at - um.before(lo);
-    s.place = x - s.t0;
+    ck_locate(m, batch, G, w, x, s);
     if (s.t0 < s.tiles) {
       s.n = min(s.tiles - s.t0, x1 - x);
       return true;
@@ -404,7 +411,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   cut.ctas = min((int)gridDim.x, max(1, M.tiles / kChunkMinTiles));
   cut.base = places / cut.ctas;
   cut.rem = places - cut.base * cut.ctas;
-  const int x0 = cta < cut.ctas ? cut.first(cta) : places, x1 = cta < cut.ctas ? cut.first(cta + 1) : places;
   if (tid == 0) p.desc[cta * 8] = 0;   // no unit to merge, so far
 
   if (warp >= 16) {
@@ -414,6 +420,16 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       // tile of four; the ids of the next four are on their way meanwhile
       const int g = lane & 7;
       CkSeg sg;
+      int x0 = cta < cut.ctas ? cut.first(cta) : places, x1 = cta < cut.ctas ? cut.first(cta + 1) : places;
+      if (p.whole) {   // no unit is cut: the ranges begin where one does
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          int& x = i == 0 ? x0 : x1;
+          if (x >= places) continue;
+          ck_locate(M, p.batch, G, p.wide, x, sg);
+          if (sg.t0 > 0) x = sg.place + sg.tiles + kChunkUnitTiles;
+        }
+      }
       int seg = 0, at = lane >> 3, j = lane >> 3;   // tile `at` of segment `seg`, the CTA's j-th
       bool more = ck_seg_at(M, p.batch, G, p.wide, x0, x1, sg);
       int done = 0;   // tiles of the segments before
@@ -674,61 +690,77 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
     int ns = 0;                                   // phases of s_full so far: a tile each, and one for a segment's end
     int hands = 0;                                // narrow segments that both halves had tiles of
     bool ok = true;
-    for (int j = 0, seg = 0; ok; ++seg) {
-      ok = __all_sync(0xffffffffu, ck_wait(&seg_full[j % kSlots], (j / kSlots) & 1, abort_flag, p.err));
-      if (!ok) break;
-      const TileSlot& head_slot = slots[j % kSlots];
-      const uint32_t flags = head_slot.flags;
-      if (flags & kNone) break;
-      const bool wide = flags & kWide, whole = flags & kWhole;
-      const int b = head_slot.b, h = head_slot.h, first = head_slot.first, t0 = head_slot.tile, tiles = head_slot.n;
-      const int n = M.n[b], rows = min(M.count[b] * G - first, 128 * p.wide);   // of the unit
-      if (tid == 0 && head_slot.ctas > 0) {
+    struct Seg {
+      uint32_t flags;
+      int b, h, first, t0, tiles, rows;
+    } sg;
+    float qs = 0.f, qs_next = 0.f;   // the row's power of two
+    int j = 0, seg = 0;
+    // The segment that begins with tile j, and its queries, as the launch before left them.
+    auto take = [&]() -> bool {
+      if (!__all_sync(0xffffffffu, ck_wait(&seg_full[j % kSlots], (j / kSlots) & 1, abort_flag, p.err))) return false;
+      const TileSlot& s = slots[j % kSlots];
+      sg.flags = s.flags;
+      if (sg.flags & kNone) return true;
+      sg.b = s.b;
+      sg.h = s.h;
+      sg.first = s.first;
+      sg.t0 = s.tile;
+      sg.tiles = s.n;
+      sg.rows = min(M.count[sg.b] * G - sg.first, 128 * p.wide);   // of the unit
+      if (tid == 0 && s.ctas > 0) {
         // this CTA has the unit's first tile: it says who has the others
         int32_t* d = p.desc + cta * 8;
-        d[1] = b;
-        d[2] = h;
-        d[3] = first;
-        d[4] = head_slot.ctas;
-        d[0] = rows;
+        d[1] = sg.b;
+        d[2] = sg.h;
+        d[3] = sg.first;
+        d[4] = s.ctas;
+        d[0] = sg.rows;
       }
+      return true;
+    };
+    auto load_queries = [&](int before) -> bool {   // `before`: segments whose queries these take the place of
+      if (before > 0 && !__all_sync(0xffffffffu, ck_wait(q_free, (before - 1) & 1, abort_flag, p.err))) return false;
+      const bool wide = sg.flags & kWide;
+      // rows behind the last one are left as they are: what comes of them is not used
+      constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows at a time
+      const int c = lane % LPR, begin = (wide ? m * 128 : m * 64) + (warp & 3) * (wide ? 32 : 16);
+      const int end = min(sg.rows, begin + (wide ? 32 : 16)), row = wide ? tid : tid & 127;
+      grid_wait();
+      for (int r = begin + lane / LPR; r < end; r += RPI) {
+        const int rq = sg.first + r, rt = r & 127;
+        const __nv_bfloat16* src = p.out + (((size_t)sg.b * p.t_len + rq / G) * p.n_q + sg.h * G + rq % G) * D + c * 8;
+        const uint32_t dst = smem_addr(smem + C::OFF_Q) + (r >> 7) * C::TILE + (c >> 3) * 16384 + rt * 128 + (((c & 7) ^ (rt & 7)) << 4);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+      }
+      qs_next = row < sg.rows ? p.q_scale[((size_t)sg.b * p.pool.n_kv + sg.h) * p.t_len * G + sg.first + row] : 0.f;
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[m]);
+      return true;
+    };
+    ok = take();
+    if (ok && !(sg.flags & kNone)) {
+      ok = load_queries(0);
+    } else {
+      ok = false;
+    }
+    if (ok && p.inject_timeout && (cta & 1) == 0) {
+      ok = mbar_wait(never, 0, kInjectWaitCycles);
+      *abort_flag = 1;
+      if (tid == 0) atomicOr(p.err, kErrTimeout);
+    }
+    for (; ok; ++seg) {
+      const bool wide = sg.flags & kWide;
+      const int t0 = sg.t0, tiles = sg.tiles;
       const int row = wide ? tid : tid & 127;
-      const int tok = (first + row) / G, head = h * G + (first + row) % G;
-      const bool live = row < rows;
-      const bool warp_live = (row & ~31) < rows;
-      // ---- the queries, as the launch before left them
-      float qs = 0.f;
-      if (seg > 0) {
-        ok = __all_sync(0xffffffffu, ck_wait(q_free, (seg - 1) & 1, abort_flag, p.err));
-        if (!ok) break;
-      }
-      {
-        // rows behind the last one are left as they are: what comes of them is not used
-        constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows at a time
-        const int c = lane % LPR, begin = (wide ? m * 128 : m * 64) + (warp & 3) * (wide ? 32 : 16);
-        const int end = min(rows, begin + (wide ? 32 : 16));
-        grid_wait();
-        for (int r = begin + lane / LPR; r < end; r += RPI) {
-          const int rq = first + r, rt = r & 127;
-          const __nv_bfloat16* src = p.out + (((size_t)b * p.t_len + rq / G) * p.n_q + h * G + rq % G) * D + c * 8;
-          const uint32_t dst = smem_addr(smem + C::OFF_Q) + (r >> 7) * C::TILE + (c >> 3) * 16384 + rt * 128 + (((c & 7) ^ (rt & 7)) << 4);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-        }
-        if (live) qs = p.q_scale[((size_t)b * p.pool.n_kv + h) * p.t_len * G + first + row];
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&q_full[m]);
-      }
+      const bool live = row < sg.rows;
+      const bool warp_live = (row & ~31) < sg.rows;
+      const int lim = M.n[sg.b] + (sg.first + row) / G + 1;   // keys that the row sees
+      qs = qs_next;
       float m_run = -INFINITY, l_run = 0.f;
       int v_ref = kNoScale;
-      const int lim = n + tok + 1;   // keys that the row sees
-      if (p.inject_timeout && (cta & 1) == 0 && seg == 0) {
-        ok = mbar_wait(never, 0, kInjectWaitCycles);
-        *abort_flag = 1;
-        if (tid == 0) atomicOr(p.err, kErrTimeout);
-        break;
-      }
       const int step = wide ? 1 : 2;
       for (int t = 0; t < tiles; ++t, ++j) {
         if (!wide && (t & 1) != m) {   // the other half's: only let it go
@@ -869,79 +901,89 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         __syncwarp();
         if (lane == 0) mbar_arrive(handed);
       }
-      if (!wide && m == 1) {
-        if (flags & kEnd) break;
-        continue;
-      }
-      if (two) {
+      if (two && m == 0) {
         ok = __all_sync(0xffffffffu, ck_wait(handed, hands++ & 1, abort_flag, p.err));
         if (!ok) break;
         if (warp_live) other = hand[row];
       }
-      if (!warp_live) {
-        if (flags & kEnd) break;
-        continue;
+      // The next segment's queries come first, so that its first scores are made
+      // meanwhile; but not while the first half still reads the second half's sums.
+      const Seg was = sg;
+      const bool ends = was.flags & kEnd;
+      if (!ends && !two) {
+        ok = take() && load_queries(seg + 1);
+        if (!ok) break;
       }
-      tc_fence_after();
-      const bool nan = nan_seg[seg & 3] == seg + 1;
-      float f = v_ref == kNoScale ? 0.f : pow2_float(v_ref), f1 = 0.f;
-      if (two) {
-        const float top = fmaxf(m_run, other.x), base = top == -INFINITY ? 0.f : top;
-        const float w0 = ex2_approx(m_run - base), w1 = ex2_approx(other.x - base);
-        f *= w0;
-        f1 = other.z * w1;
-        l_run = l_run * w0 + other.y * w1;
-        m_run = top;
-      }
-      if (whole) {
-        const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-        f *= inv;
-        f1 *= inv;
-      }
-      const int slot = 2 * cta + (t0 == 0 ? 1 : 0);   // of a unit's first part: see the merge
-      if (!whole && live) p.part_ml[(size_t)slot * p.part_rows + row] = make_float2(m_run, l_run);
-#pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 32) {
-        float o[32];
-        tmem_ld32(o_at + c0, o);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] *= f;
+      if (warp_live && (wide || m == 0)) {
+        tc_fence_after();
+        const bool whole = was.flags & kWhole;
+        const int rq = was.first + row, n = M.n[was.b];
+        const bool nan = nan_seg[seg & 3] == seg + 1;
+        float f = v_ref == kNoScale ? 0.f : pow2_float(v_ref), f1 = 0.f;
         if (two) {
-          float y[32];
-          tmem_ld32(o_at + 128 + c0, y);
-          tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = fmaf(y[i], f1, o[i]);
-        }
-        if (!live) continue;
-        if (nan) {   // values that are not numbers, for the rows that see them
-          grid_wait();
-          const int end = min(lim, (t0 + tiles) * CK_KEYS);
-          for (int key = max(n + first / G + 1, t0 * CK_KEYS); key < end; ++key) {
-            const int id = p.page_table[(size_t)b * p.max_pages + key / p.pool.page];
-            if (id < 0 || id >= p.pool.n_pages) continue;
-            const uint8_t* v = p.pool.codes[1] + (((size_t)id * p.pool.n_kv + h) * p.pool.page + key % p.pool.page) * D + c0;
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if ((v[i] & 0x7F) == 0x7F) o[i] = __uint_as_float(0x7FFFFFFFu);
-          }
+          const float top = fmaxf(m_run, other.x), base = top == -INFINITY ? 0.f : top;
+          const float w0 = ex2_approx(m_run - base), w1 = ex2_approx(other.x - base);
+          f *= w0;
+          f1 = other.z * w1;
+          l_run = l_run * w0 + other.y * w1;
+          m_run = top;
         }
         if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + (((size_t)b * p.t_len + tok) * p.n_q + head) * D + c0);
-#pragma unroll
-          for (int i = 0; i < 32; i += 8) {
-            const float e[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
-            dst[i / 8] = pack8(e);
-          }
-        } else {
-          float4* dst = p.part_o + ((size_t)slot * (D / 4) + c0 / 4) * p.part_rows + row;
-#pragma unroll
-          for (int i = 0; i < 32; i += 4) dst[(size_t)(i / 4) * p.part_rows] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
+          f *= inv;
+          f1 *= inv;
         }
+        const int slot = 2 * cta + (t0 == 0 ? 1 : 0);   // of a unit's first part: see the merge
+        if (!whole && live) p.part_ml[(size_t)slot * p.part_rows + row] = make_float2(m_run, l_run);
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          float o[32];
+          tmem_ld32(o_at + c0, o);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= f;
+          if (two) {
+            float y[32];
+            tmem_ld32(o_at + 128 + c0, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(y[i], f1, o[i]);
+          }
+          if (!live) continue;
+          if (nan) {   // values that are not numbers, for the rows that see them
+            const int end = min(lim, (t0 + tiles) * CK_KEYS);
+            for (int key = max(n + was.first / G + 1, t0 * CK_KEYS); key < end; ++key) {
+              const int id = p.page_table[(size_t)was.b * p.max_pages + key / p.pool.page];
+              if (id < 0 || id >= p.pool.n_pages) continue;
+              const uint8_t* v =
+                  p.pool.codes[1] + (((size_t)id * p.pool.n_kv + was.h) * p.pool.page + key % p.pool.page) * D + c0;
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if ((v[i] & 0x7F) == 0x7F) o[i] = __uint_as_float(0x7FFFFFFFu);
+            }
+          }
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(
+                p.out + (((size_t)was.b * p.t_len + rq / G) * p.n_q + was.h * G + rq % G) * D + c0);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8) {
+              const float e[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
+              dst[i / 8] = pack8(e);
+            }
+          } else {
+            float4* dst = p.part_o + ((size_t)slot * (D / 4) + c0 / 4) * p.part_rows + row;
+#pragma unroll
+            for (int i = 0; i < 32; i += 4)
+              dst[(size_t)(i / 4) * p.part_rows] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          }
+        }
+        tc_fence_before();
       }
-      tc_fence_before();
-      if (flags & kEnd) break;
+      if (ends) break;
+      if (two) {
+        ok = take() && load_queries(seg + 1);
+        if (!ok) break;
+      }
     }
   }
   grid_wait();   // the launch completes only behind the append
@@ -1075,6 +1117,10 @@ int chunk_wide(int batch, int n_kv, int t_len, int group, int max_keys, int ctas
   const int64_t tiles = batch * (int64_t)n_kv * ((rows + CK_ROWS - 1) / CK_ROWS) * ((max_keys + CK_KEYS - 1) / CK_KEYS);
   return tiles < (int64_t)kChunkFewTiles * ctas ? 1 : 2;
 }
+
+// Units of few tiles are not cut: a third launch costs more than their tiles one
+// after another.
+bool chunk_whole(int max_keys) { return max_keys <= kChunkWholeKeys; }
 
 int chunk_part_rows(int t_len, int group, int wide) {
   return (int)std::min<int64_t>(128 * wide, ((int64_t)t_len * group + 31) / 32 * 32);

@@ -124,6 +124,7 @@ struct ChunkParams {
   float4* part_o;                // [2 * CTAs][d / 4][part_rows] their O
   int32_t batch, t_len, n_q, group, max_pages, max_keys, table_rows, row_at_length, part_rows, inject_timeout;
   int32_t wide;                  // a unit has 128 * wide rows
+  int32_t whole;                 // no unit is cut, there is nothing to join
 };
 constexpr int kMaxChunkCtas = 160;
 
@@ -198,6 +199,7 @@ cudaError_t launch_attend_chunk8(const ChunkParams& p, int head_dim, int sms, cu
 cudaError_t launch_attend_chunk8_merge(const ChunkParams& p, int head_dim, int sms, cudaStream_t st);
 int chunk_wide(int batch, int n_kv, int t_len, int group, int max_keys, int ctas);   // ChunkParams::wide
 int chunk_part_rows(int t_len, int group, int wide);
+bool chunk_whole(int max_keys);   // ChunkParams::whole
 int64_t chunk_places(int batch, int n_kv, int t_len, int group, int max_keys);   // at most
 size_t move_workspace_ints(int n_pages, int batch, int max_pages);
 cudaError_t launch_pages8_plan(const MoveParams& p, cudaStream_t st);
