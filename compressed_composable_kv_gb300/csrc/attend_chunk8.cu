@@ -354,7 +354,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   // The launch before is the call's own, of the append and the queries, and itself
   // began behind what came before it: what it does not write is read without a wait,
   // everything but the queries and the pages from the one that the length ends in on.
-  grid_release();
+  // What comes behind is let go where the append is known to be done, so that a launch
+  // that reads some of its data early finds that, too.
   if (warp == 0) {
     // the map, 32 sequences at a time
     int at = 0, tiles = 0;
@@ -987,6 +988,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
     }
   }
   grid_wait();   // the launch completes only behind the append
+  grid_release();
   tc_fence_before();
   __syncthreads();
   if (warp == 19) {

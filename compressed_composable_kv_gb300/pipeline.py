@@ -32,12 +32,15 @@ class RequestBatch:
     prefill, fill_pages8 takes the bf16 rows over, and decode appends to and
     attends over the pages.  `filled` holds the layers whose pages hold the rows
     (a program that writes pages by calls of its own adds to it); decode refuses
-    the others, but not while a graph is captured.
+    the others, but not while a graph is captured.  spare_pages: further pages of the
+    pool, for `answers`.
     """
 
     def __init__(self, store: int, geom, requests: Sequence[RequestSpec], k: int, q_len: int,
                  decode_steps: int, device: str = "cuda", cap_multiple: int = 32, realign: bool = True,
-                 page8: Optional[int] = None):
+                 page8: Optional[int] = None, spare_pages: int = 0):
+        if spare_pages < 0 or (spare_pages and page8 is None):
+            raise ValueError("spare_pages must be >= 0, and go with page8")
         if page8 not in (None, 16, 32, 64, 128):
             raise ValueError(f"page8 must be None, 16, 32, 64 or 128, not {page8}")
         self.store, self.geom, self.k = store, geom, k
@@ -85,8 +88,8 @@ class RequestBatch:
         self._fill_before = False   # the batch's last call was fill_pages8
         if page8 is not None:
             most = -(-self.max_keys_decode // page8)
-            n_pages = most * self.batch
-            self.page_table = torch.arange(n_pages, dtype=torch.int32, device=device).reshape(self.batch, most)
+            self.page_table = torch.arange(most * self.batch, dtype=torch.int32, device=device).reshape(self.batch, most)
+            n_pages = most * self.batch + spare_pages
             self.k8 = torch.empty((L, n_pages, H, page8, D), dtype=torch.float8_e4m3fn, device=device)
             self.v8 = torch.empty_like(self.k8)
             self.k_scale = torch.empty((L, n_pages, H), dtype=torch.float32, device=device)
@@ -187,6 +190,143 @@ class RequestBatch:
     def advance(self, stream=None) -> None:
         own = self.n_cached_dev is self._own_lengths
         B.c2kv_seq_advance(self._lengths if own else self.n_cached_dev, 1, stream)
+
+    def answers(self, n: int = 1, room: int = 1, stream=None) -> "PagedSequences":
+        """n sequences for each request, on the pool's pages: they share the composed
+        cache and the question, each with room for `room` tokens of its own.  The pool
+        is theirs from here on (all layers of it have to be filled)."""
+        if self.page8 is None:
+            raise ValueError("this batch was made without page8")
+        missing = sorted(set(range(self.geom.n_layers)) - self.filled)
+        if missing:
+            raise ValueError(f"the pages of layers {missing} do not hold the batch's rows: fill_pages8 comes first")
+        if n < 1:
+            raise ValueError("n must be at least 1")
+        dev = self.page_table.device
+        rows = [s + self.q_len for s in self.n_slots]
+        held = torch.tensor([-(-r // self.page8) for r in rows], device=dev)[:, None]
+        s = torch.cuda.current_stream(dev) if stream is None and dev.type == "cuda" else stream
+        with torch.cuda.stream(s):
+            width = self.page_table.shape[1]
+            mine = torch.arange(width, device=dev) < held
+            seqs = PagedSequences(self.geom, self.k8, self.v8, self.k_scale, self.v_scale, self.rope_table,
+                                  max_keys=self.max_keys_decode)
+            seqs.page_table = torch.where(mine, self.page_table, -1).to(torch.int32)
+            seqs.refs.index_add_(0, self.page_table[mine].long(), torch.ones_like(self.page_table[mine]))
+            seqs.n_cached_dev = torch.tensor(rows, dtype=torch.int32, device=dev)
+            seqs.rope_start = self._rope_start.clone()
+        seqs.fork([b for b in range(self.batch) for _ in range(n)], room, stream)
+        self.filled.clear()
+        return seqs
+
+
+class PagedSequences:
+    """Sequences on the pages of a pool that they may share (RequestBatch.answers):
+    parallel answers, beams, further questions.
+
+    page_table int32 [sequences][max_pages] (-1 behind a sequence's pages),
+    n_cached_dev their lengths (-1: an empty place), rope_start where a sequence's
+    rows begin in rope_table, refs [n_pages] how many sequences hold each page.  A
+    fork makes new tensors of them, so a graph is captured anew behind it; compact
+    changes them in place.  Tokens are written to pages that `fork` has taken: its
+    `room` says how many may follow before the next one.
+    """
+
+    def __init__(self, geom, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 rope_table: torch.Tensor, max_keys: int):
+        self.geom, self.max_keys = geom, max_keys
+        self.k8, self.v8, self.k_scale, self.v_scale, self.rope_table = k8, v8, k_scale, v_scale, rope_table
+        dev = k8.device
+        n_pages, self.page = k8.shape[1], k8.shape[3]
+        self.refs = torch.zeros(n_pages, dtype=torch.int32, device=dev)
+        self.page_table = torch.full((1, -(-max_keys // self.page)), -1, dtype=torch.int32, device=dev)
+        self.n_cached_dev = torch.full((1,), -1, dtype=torch.int32, device=dev)
+        self.rope_start = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._chunk_ws: Optional[torch.Tensor] = None
+        self._decode_ws: Optional[torch.Tensor] = None
+        self._pages_change = True   # the last call wrote pages or lengths: what reads some early waits
+
+    @property
+    def batch(self) -> int:
+        return self.page_table.shape[0]
+
+    def _pool(self):
+        return self.k8, self.v8, self.k_scale, self.v_scale
+
+    def fork(self, parents, room: int = 1, stream=None) -> None:
+        """Place i goes on with sequence parents[i] (a list, or int32 on the device;
+        negative: an empty place): more answers, beams moved or dropped, sequences
+        ended.  Each gets room for `room` more tokens."""
+        dev = self.page_table.device
+        with torch.cuda.stream(self._stream(stream)):
+            if not isinstance(parents, torch.Tensor):
+                parents = torch.tensor(list(parents), dtype=torch.int32).to(dev, non_blocking=True)
+            n, width = parents.numel(), self.page_table.shape[1]
+            table = torch.empty((n, width), dtype=torch.int32, device=dev)
+            lengths = torch.empty(n, dtype=torch.int32, device=dev)
+            ws = torch.empty(B.c2kv_pages8_plan_workspace_size(self.refs.numel(), max(n, self.batch), width),
+                             dtype=torch.uint8, device=dev)
+            # a call that finds too few pages writes nothing: these then stay empty places
+            table.fill_(-1)
+            lengths.fill_(-1)
+            B.c2kv_pages8_fork(self.geom, *self._pool(), self.refs, self.page_table, self.n_cached_dev, parents, room,
+                               self.refs, table, lengths, ws, stream)
+            self.rope_start = self.rope_start[parents.clamp(min=0, max=self.batch - 1).long()]
+            self.page_table, self.n_cached_dev = table, lengths
+        self._pages_change = True
+
+    def compact(self, stream=None) -> None:
+        """The pages in use to the front of the pool."""
+        with torch.cuda.stream(self._stream(stream)):
+            ws = torch.empty(B.c2kv_pages8_plan_workspace_size(self.refs.numel(), self.batch, self.page_table.shape[1]),
+                             dtype=torch.uint8, device=self.refs.device)
+            B.c2kv_pages8_compact(self.geom, *self._pool(), self.refs, self.page_table, self.refs, self.page_table,
+                                  None, ws, stream)
+        self._pages_change = True
+
+    def chunk(self, layer: int, q, k_new, v_new, out, n_new: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Attention of t_len new tokens of each sequence (q, out [batch][t_len][n_q_heads]
+        [head_dim]) over its pages, their append included; n_new: int32 [batch], the
+        tokens of a padded batch."""
+        need = B.c2kv_attend_pages8_chunk_workspace_size(self.geom, self.batch, q.shape[1], self.max_keys)
+        with torch.cuda.stream(self._stream(stream)):
+            if self._chunk_ws is None or self._chunk_ws.numel() < need:
+                self._chunk_ws = torch.empty(need, dtype=torch.uint8, device=self.refs.device)
+        B.c2kv_attend_pages8_chunk(self.geom, layer, *self._pool(), self.page_table, self.n_cached_dev, self.max_keys, q,
+                                   k_new, v_new, self.rope_table, self.rope_start, out, self._chunk_ws, n_new, stream,
+                                   B.C2KV_DECODE_ROW_AT_LENGTH)
+        self._pages_change = True
+
+    def decode(self, layer: int, q, k_new, v_new, out, stream=None, overlap_previous: Optional[bool] = None) -> None:
+        """One token of each sequence, as RequestBatch.decode over pages."""
+        if overlap_previous is None:
+            overlap_previous = layer > 0 and not self._pages_change
+        if self._decode_ws is None or self._decode_ws.shape[0] != self.batch:
+            with torch.cuda.stream(self._stream(stream)):
+                self._decode_ws = torch.zeros(
+                    (self.batch, -(-B.c2kv_attend_pages8_workspace_size(self.geom, self.batch, self.max_keys) // self.batch)),
+                    dtype=torch.uint8, device=self.refs.device)
+        d = self.geom.head_dim
+        B.c2kv_attend_pages8(self.geom, layer, *self._pool(), self.page_table, self.n_cached_dev, self.max_keys,
+                             q.view(self.batch, -1, d), k_new.view(self.batch, -1, d), v_new.view(self.batch, -1, d),
+                             self.rope_table, self.rope_start, out.view(self.batch, -1, d), self._decode_ws, stream,
+                             (B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0) | B.C2KV_DECODE_ROW_AT_LENGTH)
+        self._pages_change = False
+
+    def advance(self, stream=None, n=1) -> None:
+        """The lengths by n tokens: a number, or int32 [batch] (the n_new of a chunk).
+        Empty places stay empty."""
+        with torch.cuda.stream(self._stream(stream)):
+            self.n_cached_dev.add_(torch.where(self.n_cached_dev >= 0, n, 0).to(torch.int32))
+        self._pages_change = True
+
+    def _stream(self, stream):
+        """The stream of a call, as a torch stream (None on the host)."""
+        if not self.page_table.is_cuda:
+            return None
+        if stream is None:
+            return torch.cuda.current_stream(self.page_table.device)
+        return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
 
 
 class DecoderModel:

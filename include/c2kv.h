@@ -535,7 +535,8 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
  * sequence b, i < n_new_dev[b], with q_bi rotated by the token's table row,
  * out[b][i] = softmax(q_bi K^T / sqrt(d)) V over rows [0, n_cached_dev[b] + i].
  * k_new and v_new NULL: nothing is appended, the tokens' rows are held already.
- * q, out: device bf16 [batch][t_len][n_q_heads][head_dim], 16-byte aligned;
+ * q, out: device bf16 [batch][t_len][n_q_heads][head_dim], 16-byte aligned (out
+ * holds the rotated queries until their answers take their place; it may be q);
  * out behind a sequence's last new token is left as it was.  max_keys bounds
  * n_cached_dev[b] + n_new_dev[b]; a sequence with more, or one that the append
  * leaves out, is left out whole.  Rows on pages outside the pool are not
@@ -647,9 +648,10 @@ c2kv_status c2kv_kernel_launches(uint64_t* count);
  * the kernel takes its timeout path: it records C2KV_ETIMEOUT in the device
  * error word, lets its copies in flight land and returns; that launch's
  * outputs are undefined, the cache rows it appends are written, and the
- * context stays usable.  c2kv_attend_pages8 counts among them; the rows it
- * appends may then be missing, and in every other of its CTAs one warp alone
- * gives up, at the last tile of a sequence's head.  0 disarms it.  Process-wide; C2KV_EINVAL for n < 0.
+ * context stays usable.  c2kv_attend_pages8_chunk counts among them, and
+ * c2kv_attend_pages8: the rows that it appends may then be missing, and in
+ * every other of its CTAs one warp alone gives up, at the last tile of a
+ * sequence's head.  0 disarms it.  Process-wide; C2KV_EINVAL for n < 0.
  */
 c2kv_status c2kv_test_expire_next_waits(int32_t n_launches);
 

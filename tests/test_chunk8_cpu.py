@@ -138,3 +138,86 @@ def test_binding_checks_shapes_and_types(P):  # noqa: F811
                 call(g, **dict(good, **{name: t}))
         with pytest.raises(ValueError, match="CUDA"):   # host tensors
             call(g, **good)
+
+
+# ------------------------------------------------------------------ sequences on shared pages
+
+@pytest.fixture
+def noted(P, monkeypatch):  # noqa: F811
+    """A paged RequestBatch of two layers on the CPU: its calls of the library are
+    noted, a fork done by the oracle."""
+    B = P.pipeline.B
+    calls = []
+    monkeypatch.setattr(B, "c2kv_store_lookup", lambda store, d: (40, 10, 0))
+    monkeypatch.setattr(B, "c2kv_workspace_init", lambda ws: None)
+    monkeypatch.setattr(B, "c2kv_pages8_fill", lambda *a: None)
+
+    def fork(g, k8, v8, ks, vs, refs, table, n, parent, room, refs_out, table_out, n_out, ws, stream=None):
+        got = Q.fork(refs.tolist(), table.tolist(), n.tolist(), parent.tolist(), room, k8.shape[3])
+        assert ws.numel() >= P.c2kv_pages8_plan_workspace_size(refs.numel(), max(len(parent), len(n)), table.shape[1])
+        for dst, src in zip((refs_out, table_out, n_out), got):
+            dst.copy_(torch.tensor(src))
+        calls.append(("fork", parent.tolist(), room))
+
+    monkeypatch.setattr(B, "c2kv_pages8_fork", fork)
+    monkeypatch.setattr(B, "c2kv_pages8_compact", lambda *a: calls.append(("compact",)))
+    monkeypatch.setattr(B, "c2kv_attend_pages8_chunk", lambda g, l, *a: calls.append(("chunk", l, a[-1], a[12].numel())))
+    monkeypatch.setattr(B, "c2kv_attend_pages8",
+                        lambda g, l, *a: calls.append(("decode", l, bool(a[-1] & B.C2KV_DECODE_OVERLAP_PREVIOUS))))
+    rb = P.RequestBatch(None, S.Geometry(2, 4, 2, 64, 1e4), [P.RequestSpec([0]), P.RequestSpec([1])], 4, 3, 20, device="cpu",
+                        page8=16, spare_pages=5)
+    return rb, calls
+
+
+def test_answers_share_the_composed_rows(noted):
+    rb, calls = noted
+    with pytest.raises(ValueError, match="fill_pages8"):
+        rb.answers(2)
+    rb.fill_pages8()
+    with pytest.raises(ValueError):
+        rb.answers(0)
+    seqs = rb.answers(2, room=4)   # 13 rows of 16 each: one page, which the second answer copies
+    assert seqs.page_table.tolist() == [[0, 1, -1], [2, 4, -1], [3, 5, -1], [6, 7, -1]]
+    assert seqs.n_cached_dev.tolist() == [13] * 4 and seqs.batch == 4
+    assert seqs.rope_start.tolist() == [0, 0, rb.cap, rb.cap]
+    assert calls == [("fork", [0, 0, 1, 1], 4)]
+    seqs.advance()
+    seqs.advance(n=torch.tensor([3, 0, 1, 2], dtype=torch.int32))
+    assert seqs.n_cached_dev.tolist() == [17, 14, 15, 16]
+    seqs.fork([3, -1, 0], 2)
+    assert seqs.n_cached_dev.tolist() == [16, -1, 17] and seqs.rope_start.tolist()[::2] == [rb.cap, 0]
+    seqs.advance(n=2)
+    assert seqs.n_cached_dev.tolist() == [18, -1, 19]
+    assert sum(seqs.refs.tolist()) == sum(e >= 0 for row in seqs.page_table.tolist() for e in row)
+
+
+def test_what_may_overlap_among_sequences(noted):
+    """A decode behind a call that wrote pages or lengths waits for it."""
+    rb, calls = noted
+    rb.fill_pages8()
+    seqs = rb.answers(2, room=4)
+    calls.clear()
+    x = torch.zeros((4, 4, 64))
+
+    def decode(l, **kw):
+        seqs.decode(l, x, x[:, :2], x[:, :2], x, **kw)
+
+    decode(1)
+    decode(1)
+    decode(0)
+    seqs.advance()
+    decode(1)
+    seqs.chunk(0, x[:, None], x[:, None, :2], x[:, None, :2], x[:, None])
+    decode(1)
+    seqs.compact()
+    decode(1, overlap_previous=True)
+    assert [c for c in calls if c[0] == "decode"] == [("decode", 1, False), ("decode", 1, True), ("decode", 0, False),
+                                                      ("decode", 1, False), ("decode", 1, False), ("decode", 1, True)]
+    chunk = [c for c in calls if c[0] == "chunk"][0]
+    assert chunk[1] == 0 and chunk[2] == 4 and chunk[3] > 0
+
+
+def test_request_batch_refuses_spare_pages_without_pages(P):  # noqa: F811
+    for kw in (dict(spare_pages=3), dict(page8=16, spare_pages=-1)):
+        with pytest.raises(ValueError, match="spare_pages"):
+            P.RequestBatch(None, S.TINY, [], 4, 0, 1, **kw)

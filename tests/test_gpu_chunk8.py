@@ -407,3 +407,45 @@ def test_pages_beyond_32_bit_offsets():
     ref = Q.attend_chunk(_rotate(g, _f64(q[0]), pos), k, v, held)
     err = np.abs(out[0].double().cpu().numpy() - ref)
     assert np.sqrt((err ** 2).sum() / (ref ** 2).sum()) < 1.2 * 2.0 ** -8 / np.sqrt(3)
+
+
+@pytest.mark.parametrize("d,group", [(128, 4), (64, 8)])
+@pytest.mark.parametrize("held,new", [([3000, 700, 90], [40, 9, 70]), ([100] * 6, [3] * 6), ([0, 37], [300, 200])])
+def test_a_wait_that_runs_out_ends_the_launch(d, group, held, new):
+    """The test hook lets a wait of every other CTA run out: the launch ends, says so,
+    and the next one is as before."""
+    g = _geom(d, group, 4)
+    c = Chunk(g, 32, held, new, seed=21)
+    good = c.call().clone()
+    _ok()
+    for _ in range(2):
+        P.c2kv_test_expire_next_waits(1)
+        c.call()
+        torch.cuda.synchronize()
+        P.c2kv_test_expire_next_waits(0)
+        assert P.c2kv_device_error() == P.C2KV_ETIMEOUT
+        c.out.fill_(-7.0)
+        assert torch.equal(c.call(), good)
+        _ok()
+
+
+@pytest.mark.parametrize("t_len,held", [(64, 8000), (200, 30000), (33, 500), (700, 600)])
+def test_units_of_both_sizes(t_len, held):
+    """Rows of 128 and of 256 to a unit, cut and whole, a lengths' end inside a page."""
+    g = _geom(128, 4, 4)
+    c = Chunk(g, 128, [held, 0], [t_len, t_len // 2], t_len=t_len, seed=t_len, sharp=2.0)
+    c.call()
+    _ok()
+    c.put_new()
+    c.check("units", rows=[0, 31, 32, 63, 64, t_len // 2, t_len - 1])
+
+
+def test_queries_in_the_output_buffer():
+    """out may be q itself."""
+    g = _geom(128, 4, 2)
+    c = Chunk(g, 32, [900, 40], [50, 50], seed=22)
+    want = c.call().clone()
+    q = _dev(c.q)
+    got = c.call(q=q, out=q)
+    _ok()
+    assert torch.equal(got, want)
