@@ -76,17 +76,19 @@ struct ChunkMap {
   int32_t tiles;                      // of the launch
 };
 
-template <int D>
+template <int D, int W>
 struct CkCfg {
   static constexpr int TILE = 128 * D * 2;             // a query, K or V tile in fp16
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = 2 * TILE;
-  static constexpr int OFF_V = 4 * TILE;
-  static constexpr int OFF_SLOT = 6 * TILE;
+  static constexpr int OFF_K = W * TILE;
+  static constexpr int OFF_V = OFF_K + 2 * TILE;
+  // what the second softmax half hands to the first (W == 1): O of 64 rows, column
+  // by column of four; then (m, l, scale) of 128
+  static constexpr int OFF_HO = OFF_V + 2 * TILE;
+  static constexpr int OFF_X = OFF_HO + (W == 1 ? 64 * D * 4 : 0);
+  static constexpr int OFF_SLOT = OFF_X + 128 * 16;
   static constexpr int OFF_MAP = OFF_SLOT + kSlots * (int)sizeof(TileSlot);
-  static constexpr int OFF_BAR = OFF_MAP + (int)((sizeof(ChunkMap) + 15) / 16 * 16);
-  static constexpr int OFF_X = OFF_BAR;                 // what the second softmax warps hand over
-  static constexpr int OFF_BARS = OFF_X + 128 * 16;
+  static constexpr int OFF_BARS = OFF_MAP + (int)((sizeof(ChunkMap) + 15) / 16 * 16);
   static constexpr int N_BAR = 2 * 9 + 3 * kSlots + 5;
   static constexpr int OFF_MISC = OFF_BARS + N_BAR * 8;
   static constexpr int SMEM = OFF_MISC + 64 + 1024;    // + slack for 1024-byte alignment
@@ -289,9 +291,10 @@ __device__ __forceinline__ bool ck_next(const ChunkMap& m, int batch, int G, int
   return ck_seg_at(m, batch, G, w, s.t0 + s.n == s.tiles ? x + kChunkUnitTiles : x, x1, s);
 }
 
-template <int D>
+// W: units of 128 W rows.
+template <int D, int W>
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
-  using C = CkCfg<D>;
+  using C = CkCfg<D, W>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   TileSlot* slots = reinterpret_cast<TileSlot*>(smem + C::OFF_SLOT);
@@ -332,9 +335,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         mbar_init(&p_full[2 * i + k], 4);
       }
       mbar_init(&k_full[i], 4);
-      mbar_init(&k_empty[i], 8);   // softmax warps; of a narrow unit four, twice
+      mbar_init(&k_empty[i], W == 1 ? 1 : 8);   // an MMA issuer; softmax warps, of a narrow unit four, twice
       mbar_init(&v_full[i], 4);
-      mbar_init(&v_empty[i], 8);
+      mbar_init(&v_empty[i], W == 1 ? 1 : 8);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&slot_full[i], 1);
@@ -377,7 +380,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       }
       int per = 0, all = 0;
       if (count > 0) {
-        const UnitMath um(n, count, G, p.wide);
+        const UnitMath um(n, count, G, W);
         per = um.before(um.units);
         all = (per - um.units * kChunkUnitTiles) * p.pool.n_kv;
       }
@@ -427,12 +430,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         for (int i = 0; i < 2; ++i) {
           int& x = i == 0 ? x0 : x1;
           if (x >= places) continue;
-          ck_locate(M, p.batch, G, p.wide, x, sg);
+          ck_locate(M, p.batch, G, W, x, sg);
           if (sg.t0 > 0) x = sg.place + sg.tiles + kChunkUnitTiles;
         }
       }
       int seg = 0, at = lane >> 3, j = lane >> 3;   // tile `at` of segment `seg`, the CTA's j-th
-      bool more = ck_seg_at(M, p.batch, G, p.wide, x0, x1, sg);
+      bool more = ck_seg_at(M, p.batch, G, W, x0, x1, sg);
       int done = 0;   // tiles of the segments before
       struct Ref {
         int32_t id, key0, rows, diag, ctas;   // id: -1 no page here, -2 outside the pool
@@ -446,11 +449,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         while (more && at - done >= sg.n) {
           done += sg.n;
           ++seg;
-          more = ck_next(M, p.batch, G, p.wide, x1, sg);
+          more = ck_next(M, p.batch, G, W, x1, sg);
         }
         r.on = more;
         if (more) {
-          const int n = M.n[sg.b], unit = 128 * p.wide, first = sg.i * unit, t = at - done, all = M.count[sg.b] * G;
+          const int n = M.n[sg.b], unit = 128 * W, first = sg.i * unit, t = at - done, all = M.count[sg.b] * G;
           const int end = n + min((first + unit - 1) / G + 1, M.count[sg.b]);
           r.b = sg.b;
           r.h = sg.h;
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         const TileSlot& s = slots[j % kSlots];
         const uint32_t flags = s.flags;
         if (flags & kNone) break;
-        const int n = s.n, wide = (flags & kWide) ? 1 : 0, step = 2 - wide, t0 = wide ? 0 : m;
+        const int n = s.n, wide = W == 2 && (flags & kWide) ? 1 : 0, step = 2 - wide, t0 = wide ? 0 : m;
         const uint64_t q = q_desc + (uint32_t)(wide ? m : 0) * (C::TILE >> 4);
         ok = wait(&q_full[0], seg & 1) && wait(&q_full[1], seg & 1);
         if (t0 >= n) mbar_arrive(q_free);
@@ -583,6 +586,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               for (int kk = 0; kk < 4; ++kk)
                 mma_bf16_tmem_a(o_col, s_col + kk * 8, v + (uint32_t)(4 * part + kk) * (2048 >> 4), idesc_pv,
                                 t > t0 || part + kk > 0 ? 1u : 0u);
+              // at once: the next tile of this half takes the same stage (beside the
+              // work of wide units the commits cost more than the wait)
+              if (W == 1 && part == 1) mma_commit(&v_empty[jt & 1]);
             }
             if (tn < n) {
 #pragma unroll
@@ -592,6 +598,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               }
             }
             if (tn < n || t >= t0) mma_commit(&s_full[2 * m + part]);
+            if (W == 1 && tn < n && part == 1) mma_commit(&k_empty[jn & 1]);
           }
           if (t >= t0) ++np;
           if (tn < n && tn + step >= n) mma_commit(q_free);
@@ -696,6 +703,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       int b, h, first, t0, tiles, rows;
     } sg;
     float qs = 0.f, qs_next = 0.f;   // the row's power of two
+    // The thread's row of the unit.  Up to 64 rows stand twice in a tile, the second
+    // half works on the second 64 lanes: on other parts of the SM than the first.
+    auto row_of = [&](bool wide, bool twice) { return wide ? tid : twice ? (tid & 127) - 64 * m : tid & 127; };
     int j = 0, seg = 0;
     // The segment that begins with tile j, and its queries, as the launch before left them.
     auto take = [&]() -> bool {
@@ -708,7 +718,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       sg.first = s.first;
       sg.t0 = s.tile;
       sg.tiles = s.n;
-      sg.rows = min(M.count[sg.b] * G - sg.first, 128 * p.wide);   // of the unit
+      sg.rows = min(M.count[sg.b] * G - sg.first, 128 * W);   // of the unit
       if (tid == 0 && s.ctas > 0) {
         // this CTA has the unit's first tile: it says who has the others
         int32_t* d = p.desc + cta * 8;
@@ -722,19 +732,19 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
     };
     auto load_queries = [&](int before) -> bool {   // `before`: segments whose queries these take the place of
       if (before > 0 && !__all_sync(0xffffffffu, ck_wait(q_free, (before - 1) & 1, abort_flag, p.err))) return false;
-      const bool wide = sg.flags & kWide;
+      const bool wide = W == 2 && (sg.flags & kWide), twice = W == 1 && sg.rows <= 64;
       // rows behind the last one are left as they are: what comes of them is not used
       constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows at a time
-      const int c = lane % LPR, begin = (wide ? m * 128 : m * 64) + (warp & 3) * (wide ? 32 : 16);
-      const int end = min(sg.rows, begin + (wide ? 32 : 16)), row = wide ? tid : tid & 127;
+      const int c = lane % LPR, begin = (wide ? m * 128 : twice ? 0 : m * 64) + (warp & 3) * (wide ? 32 : 16);
+      const int end = min(sg.rows, begin + (wide ? 32 : 16)), row = row_of(wide, twice);
       grid_wait();
       for (int r = begin + lane / LPR; r < end; r += RPI) {
-        const int rq = sg.first + r, rt = r & 127;
+        const int rq = sg.first + r, rt = twice ? m * 64 + r : r & 127;
         const __nv_bfloat16* src = p.out + (((size_t)sg.b * p.t_len + rq / G) * p.n_q + sg.h * G + rq % G) * D + c * 8;
         const uint32_t dst = smem_addr(smem + C::OFF_Q) + (r >> 7) * C::TILE + (c >> 3) * 16384 + rt * 128 + (((c & 7) ^ (rt & 7)) << 4);
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
       }
-      qs_next = row < sg.rows ? p.q_scale[((size_t)sg.b * p.pool.n_kv + sg.h) * p.t_len * G + sg.first + row] : 0.f;
+      qs_next = (uint32_t)row < (uint32_t)sg.rows ? p.q_scale[((size_t)sg.b * p.pool.n_kv + sg.h) * p.t_len * G + sg.first + row] : 0.f;
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async();
       __syncwarp();
@@ -753,11 +763,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       if (tid == 0) atomicOr(p.err, kErrTimeout);
     }
     for (; ok; ++seg) {
-      const bool wide = sg.flags & kWide;
+      const bool wide = W == 2 && (sg.flags & kWide), twice = W == 1 && sg.rows <= 64;
       const int t0 = sg.t0, tiles = sg.tiles;
-      const int row = wide ? tid : tid & 127;
-      const bool live = row < sg.rows;
-      const bool warp_live = (row & ~31) < sg.rows;
+      const int row = row_of(wide, twice);
+      const bool live = (uint32_t)row < (uint32_t)sg.rows;
+      const bool warp_live = (uint32_t)(row & ~31) < (uint32_t)sg.rows;
       const int lim = M.n[sg.b] + (sg.first + row) / G + 1;   // keys that the row sees
       qs = qs_next;
       float m_run = -INFINITY, l_run = 0.f;
@@ -779,7 +789,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           if (!ok) break;
           // The products behind these scores have read K, those before them V.  (Before
           // the wait below: the other part's next scores may need these stages.)
-          if (lane == 0 && part == 1) {
+          if (W == 2 && lane == 0 && part == 1) {
             mbar_arrive_n(&k_empty[j & 1], step);
             if (t >= step) mbar_arrive_n(&v_empty[(j - step) & 1], step);
           }
@@ -892,20 +902,35 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         if (!ok) break;
         ++ns;
         // this half's last tile: j - 1, or the one before it
-        if (lane == 0) mbar_arrive_n(&v_empty[(j - 1 - (wide || ((tiles - 1) & 1) == m ? 0 : 1)) & 1], step);
+        if (W == 2 && lane == 0) mbar_arrive_n(&v_empty[(j - 1 - (wide || ((tiles - 1) & 1) == m ? 0 : 1)) & 1], step);
       }
       const bool two = !wide && tiles > 1;   // a narrow unit's halves are added up by the first
       float4 other = make_float4(-INFINITY, 0.f, 0.f, 0.f);   // m, l, 2^v_ref of the second half
+      float4* hand_o = reinterpret_cast<float4*>(smem + C::OFF_HO);
       if (two && m == 1) {
-        tc_fence_before();   // its sums are complete
-        if (warp_live) hand[row] = make_float4(m_run, l_run, v_ref == kNoScale ? 0.f : pow2_float(v_ref), 0.f);
+        // its sums are complete; the first half cannot read tensor memory of other lanes
+        if (twice && warp_live) {
+          tc_fence_after();
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 16) {
+            float o[16];
+            tmem_ld_cols<16>(o_at + c0, o);
+            tmem_wait_ld();
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) hand_o[(c0 + i) / 4 * 64 + row] = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            }
+          }
+        }
+        tc_fence_before();
+        if (live) hand[row] = make_float4(m_run, l_run, v_ref == kNoScale ? 0.f : pow2_float(v_ref), 0.f);
         __syncwarp();
         if (lane == 0) mbar_arrive(handed);
       }
       if (two && m == 0) {
         ok = __all_sync(0xffffffffu, ck_wait(handed, hands++ & 1, abort_flag, p.err));
         if (!ok) break;
-        if (warp_live) other = hand[row];
+        if (live) other = hand[row];
       }
       // The next segment's queries come first, so that its first scores are made
       // meanwhile; but not while the first half still reads the second half's sums.
@@ -943,7 +968,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] *= f;
-          if (two) {
+          if (two && !twice) {
             float y[32];
             tmem_ld32(o_at + 128 + c0, y);
             tmem_wait_ld();
@@ -951,6 +976,16 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             for (int i = 0; i < 32; ++i) o[i] = fmaf(y[i], f1, o[i]);
           }
           if (!live) continue;
+          if (two && twice) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              const float4 y = hand_o[(c0 + i) / 4 * 64 + row];
+              o[i] = fmaf(y.x, f1, o[i]);
+              o[i + 1] = fmaf(y.y, f1, o[i + 1]);
+              o[i + 2] = fmaf(y.z, f1, o[i + 2]);
+              o[i + 3] = fmaf(y.w, f1, o[i + 3]);
+            }
+          }
           if (nan) {   // values that are not numbers, for the rows that see them
             const int end = min(lim, (t0 + tiles) * CK_KEYS);
             for (int key = max(n + was.first / G + 1, t0 * CK_KEYS); key < end; ++key) {
@@ -1066,16 +1101,16 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(const __grid_constant
   *dst = make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
 }
 
-template <int D>
+template <int D, int W>
 cudaError_t launch_chunk(const ChunkParams& p, int sms, cudaStream_t st) {
-  using C = CkCfg<D>;
+  using C = CkCfg<D, W>;
   static KernelSetup s;
   const int dev = setup_device();
   if (dev < 0) return cudaErrorInvalidDevice;
   {
     std::lock_guard<std::mutex> lk(s.mu);
     if (s.state[dev] == 0) {
-      const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+      const cudaError_t e = cudaFuncSetAttribute(chunk_kernel<D, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
       if (e != cudaSuccess) cudaGetLastError();
       s.state[dev] = e == cudaSuccess ? 1 : -(int)e;
     }
@@ -1091,7 +1126,7 @@ cudaError_t launch_chunk(const ChunkParams& p, int sms, cudaStream_t st) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_kernel<D>, p);
+  return cudaLaunchKernelEx(&cfg, chunk_kernel<D, W>, p);
 }
 
 template <int D>
@@ -1134,7 +1169,8 @@ int64_t chunk_places(int batch, int n_kv, int t_len, int group, int max_keys) {
 }
 
 cudaError_t launch_attend_chunk8(const ChunkParams& p, int head_dim, int sms, cudaStream_t st) {
-  return head_dim == 128 ? launch_chunk<128>(p, sms, st) : launch_chunk<64>(p, sms, st);
+  if (p.wide == 2) return head_dim == 128 ? launch_chunk<128, 2>(p, sms, st) : launch_chunk<64, 2>(p, sms, st);
+  return head_dim == 128 ? launch_chunk<128, 1>(p, sms, st) : launch_chunk<64, 1>(p, sms, st);
 }
 
 cudaError_t launch_attend_chunk8_merge(const ChunkParams& p, int head_dim, int sms, cudaStream_t st) {
