@@ -1,12 +1,19 @@
 // The pages of an 8-bit pool among its sequences: forking a batch (with what it
 // gives back and takes) and compacting the pool.
 //
-// Both are a plan, then a copy.  The plan is one launch of a cluster of eight
-// CTAs, which counts, ranks and lists pages in the order of their indices, with
-// cluster barriers between its steps; every rank is a prefix sum, so a result
-// does not depend on who comes first.  It writes its results to the workspace, so
-// that the second launch may write outputs over inputs, and nothing where the
-// plan found a bad value.  The copy moves the listed pages of every layer.
+// Both are a plan, then a copy.  The plan is one launch of a cluster of CTAs, which
+// counts, ranks and lists pages in the order of their indices, with cluster barriers
+// between its steps; every rank is a prefix sum, so a result does not depend on who
+// comes first: a fork's k-th free page is the one with k free ones before it, and a
+// compaction's k-th hole among the first `used` pages takes the k-th page in use behind
+// them.  The plan writes its results to the workspace, so that the second launch may
+// write outputs over inputs, and nothing where the plan found a bad value.  The copy
+// moves the listed pages of every layer.
+//
+// What bounds them: a copy of some MB the memory (32 layers, 4 sequences forked to 32:
+// 35.0 us, 6.8 TB/s read and written; 16 layers, 512 pages of 64 rows compacted: 88.3 us,
+// 6.0 TB/s), a smaller call the plan's chain of steps, each a trip to L2 and a barrier, and
+// the two launches (3 sequences forked to 7: 11.4 us; 97 pages compacted: 7.9 us).
 #include <algorithm>
 
 #include <cooperative_groups.h>
@@ -19,9 +26,10 @@ namespace c2kv {
 
 namespace {
 
-constexpr int PL_CTAS = 8;
+constexpr int PL_CTAS = 8;   // at most; see plan_ctas
 constexpr int PL_THREADS = 1024;
 constexpr int MV_THREADS = 256;
+constexpr int kPlanFewPages = 2048;   // see plan_ctas
 
 // The workspace, in ints.
 struct MoveWs {
@@ -76,7 +84,7 @@ __device__ __forceinline__ int block_scan(int v, int* warp_sums, int& total) {  
 // Sum over the CTAs of a count each, and over those before this one.
 __device__ __forceinline__ void counts_of(const int32_t* counts, int rank, int& before, int& total) {
   before = total = 0;
-  for (int i = 0; i < PL_CTAS; ++i) {
+  for (int i = 0; i < (int)gridDim.x; ++i) {
     const int c = __ldcg(counts + i);
     if (i < rank) before += c;
     total += c;
@@ -85,18 +93,17 @@ __device__ __forceinline__ void counts_of(const int32_t* counts, int rank, int& 
 
 __device__ __forceinline__ bool any_bad(const int32_t* flags) {
   int bad = 0;
-  for (int i = 0; i < PL_CTAS; ++i) bad |= __ldcg(flags + i);
+  for (int i = 0; i < (int)gridDim.x; ++i) bad |= __ldcg(flags + i);
   return bad != 0;
 }
 
 template <bool FORK>
-__global__ void __cluster_dims__(PL_CTAS, 1, 1) __launch_bounds__(PL_THREADS, 1)
-    plan_kernel(const __grid_constant__ MoveParams p) {
+__global__ void __launch_bounds__(PL_THREADS, 1) plan_kernel(const __grid_constant__ MoveParams p) {
   __shared__ int warp_sums[33];
   __shared__ int s_n[kMaxPagedSeqs], s_held[kMaxPagedSeqs], s_kids[kMaxPagedSeqs], s_first[kMaxPagedSeqs];
   __shared__ int s_par[kMaxPagedSeqs], s_keep[kMaxPagedSeqs], s_want[kMaxPagedSeqs], s_base[kMaxPagedSeqs];
   cg::cluster_group cl = cg::this_cluster();
-  const int rank = (int)cl.block_rank(), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int ctas = (int)gridDim.x, rank = (int)cl.block_rank(), tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int n_pages = p.pool.n_pages, page = p.pool.page, W = p.max_pages;
   const MoveWs ws(p.ws, n_pages);
   grid_wait();
@@ -104,7 +111,7 @@ __global__ void __cluster_dims__(PL_CTAS, 1, 1) __launch_bounds__(PL_THREADS, 1)
 
   // ---------------- the pages of each sequence (a warp each), checked
   bool bad = false;
-  static_assert(PL_CTAS * PL_THREADS / 32 >= kMaxPagedSeqs, "a warp for each sequence");
+  static_assert(PL_CTAS * PL_THREADS / 32 >= kMaxPagedSeqs, "a warp for each sequence");   // see plan_ctas
   const int row = rank * (PL_THREADS / 32) + warp;
   if (row < p.batch) {
     const int32_t* t = p.page_table + (size_t)row * W;
@@ -125,7 +132,7 @@ __global__ void __cluster_dims__(PL_CTAS, 1, 1) __launch_bounds__(PL_THREADS, 1)
     }
     if (lane == 0) ws.held[row] = held;
   }
-  const int slice = (n_pages + PL_CTAS - 1) / PL_CTAS, lo = min(rank * slice, n_pages), hi = min(lo + slice, n_pages);
+  const int slice = (n_pages + ctas - 1) / ctas, lo = min(rank * slice, n_pages), hi = min(lo + slice, n_pages);
   int mine = 0;
   for (int x = lo + tid; x < hi; x += PL_THREADS) {
     const int32_t c = p.refs[x];
@@ -231,7 +238,7 @@ __global__ void __cluster_dims__(PL_CTAS, 1, 1) __launch_bounds__(PL_THREADS, 1)
     }
     cl.sync();
     // ---------------- the new table, and what is copied
-    for (int64_t i = (int64_t)rank * PL_THREADS + tid; i < (int64_t)p.batch_out * W; i += PL_CTAS * PL_THREADS) {
+    for (int64_t i = (int64_t)rank * PL_THREADS + tid; i < (int64_t)p.batch_out * W; i += ctas * PL_THREADS) {
       const int b = (int)(i / W), e = (int)(i % W);
       int32_t v = -1;
       if (e < s_keep[b]) v = p.page_table[(size_t)s_par[b] * W + e];
@@ -291,7 +298,7 @@ __global__ void __cluster_dims__(PL_CTAS, 1, 1) __launch_bounds__(PL_THREADS, 1)
         if (c == 0) ws.map[x] = -1;
       }
     }
-    for (int k = rank * PL_THREADS + tid; k < moves; k += PL_CTAS * PL_THREADS) {
+    for (int k = rank * PL_THREADS + tid; k < moves; k += ctas * PL_THREADS) {
       const int src = __ldcg(ws.src + first + k), dst = __ldcg(ws.dst + k);
       ws.map[src] = dst;
       ws.refs[dst] = p.refs[src];
@@ -353,16 +360,19 @@ __global__ void __launch_bounds__(MV_THREADS) move_kernel(const __grid_constant_
 }
 
 template <typename K, typename... A>
-cudaError_t launch_pdl(K kernel, dim3 grid, int threads, cudaStream_t st, const A&... args) {
+cudaError_t launch_pdl(K kernel, dim3 grid, int cluster, int threads, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -373,16 +383,29 @@ size_t move_workspace_ints(int n_pages, int batch, int max_pages) {
          (size_t)batch * max_pages;
 }
 
-cudaError_t launch_pages8_plan(const MoveParams& p, cudaStream_t st) {
-  return p.n_cached ? launch_pdl(plan_kernel<true>, dim3(PL_CTAS), PL_THREADS, st, p)
-                    : launch_pdl(plan_kernel<false>, dim3(PL_CTAS), PL_THREADS, st, p);
+// CTAs of the plan.  One spares the barriers of a cluster and its launch, eight share
+// a long list of pages.  Compacting 256, 2048, 4096 and 16384 pages took 7.9, 9.3, 10.7
+// and 17.7 us with one, 10.6, 11.3, 10.8 and 11.9 us with eight; a fork of 30 sequences
+// with 2086 pages 13.4 against 15.2 us, with 7712 pages 22.1 against 18.7 us.
+static int plan_ctas(const MoveParams& p) {
+  const int rows = (p.batch + PL_THREADS / 32 - 1) / (PL_THREADS / 32);
+  return rows == 1 && p.pool.n_pages <= kPlanFewPages ? 1 : PL_CTAS;
 }
 
+cudaError_t launch_pages8_plan(const MoveParams& p, cudaStream_t st) {
+  const int n = plan_ctas(p);
+  return p.n_cached ? launch_pdl(plan_kernel<true>, dim3(n), n, PL_THREADS, st, p)
+                    : launch_pdl(plan_kernel<false>, dim3(n), n, PL_THREADS, st, p);
+}
+
+// A warp for each page and kv head that may have to be copied, up to eight CTAs an SM.
 cudaError_t launch_pages8_move(const MoveParams& p, int head_dim, int sms, cudaStream_t st) {
-  const int y = 2 * p.n_layers;
-  const dim3 grid((8 * sms + y - 1) / y, y);
-  return p.n_cached ? launch_pdl(move_kernel<true>, grid, MV_THREADS, st, p, head_dim)
-                    : launch_pdl(move_kernel<false>, grid, MV_THREADS, st, p, head_dim);
+  const int y = 2 * p.n_layers, warps = MV_THREADS / 32;
+  const int64_t copies = p.n_cached ? p.batch_out : p.pool.n_pages / 2;
+  const int64_t want = std::max<int64_t>(1, (copies * p.pool.n_kv + warps - 1) / warps);
+  const dim3 grid((unsigned)std::min<int64_t>(want, (8 * sms + y - 1) / y), y);
+  return p.n_cached ? launch_pdl(move_kernel<true>, grid, 1, MV_THREADS, st, p, head_dim)
+                    : launch_pdl(move_kernel<false>, grid, 1, MV_THREADS, st, p, head_dim);
 }
 
 }  // namespace c2kv

@@ -264,6 +264,18 @@ def test_compact_in_place_without_the_map():
     p.check_bytes()
 
 
+@pytest.mark.parametrize("batch,n_pages", [(32, 2048), (33, 2048), (32, 2049), (1, 2047), (33, 2049)])
+def test_few_and_many_pages(batch, n_pages):
+    """The plan is made by one block of threads or by several: both sides of the border."""
+    rng = np.random.default_rng(batch + n_pages)
+    lens = [int(x) for x in rng.integers(0, 600, batch)]
+    shared = [int(x) for x in rng.integers(0, 8, batch)]
+    p = Pages(lens, 16, n_pages, layers=1, heads=1, width=60, shared=shared, seed=batch)
+    p.check_fork([int(x) for x in rng.integers(-2, batch, 40)], 33)
+    p = Pages(lens, 16, n_pages, layers=1, heads=1, shared=shared, seed=batch)
+    p.check_compact()
+
+
 def test_fork_and_compact_in_a_graph_and_on_another_stream():
     p = Pages([100, 50, 17, 64], 16, 90, seed=18)
     side = torch.cuda.Stream()
