@@ -32,6 +32,7 @@ namespace {
 constexpr int PUT_MAX_ROWS = 128;
 constexpr int PUT_MIN_ROWS = 64;
 constexpr int PUT_WARP_ROWS = 16;
+constexpr int PUT_SLICES = 4;     // CTAs that share the queries of the same rows
 
 __device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
@@ -75,49 +76,64 @@ __device__ __forceinline__ uint32_t f16x2(float a, float b) {
   return r;
 }
 
-// The queries of rows [row0, end) of a sequence (its first new token at row
-// `first`), head h * G + g: rotated and scaled in fp32, then fp16 over a power of two
-// that brings the largest element of the row to (224, 448].  A warp takes 16 rows, 8
-// (at head_dim 64, 4) lanes to a row.
+// The queries of new tokens at rows wrow + slice, + PUT_SLICES, ... before wrow + 16 and
+// `end` (the sequence's first new token is at row `first`), all heads of group h: rotated
+// and scaled in fp32, then fp16 over a power of two that brings the largest element of a
+// head to (224, 448].  A lane has two neighbouring pairs of a head's halves, a warp
+// (at head_dim 64, half a warp) a head: loads and stores are whole lines, and a token's
+// RoPE row is read once for the group (16 elements a lane, a head at a time, took 79 us
+// for 4000 tokens of 32 heads, most of it for the table's lines in L1).
 template <int D>
-__device__ __noinline__ void put_queries(const PutParams& p, int b, int h, int g, int first, int row0, int end, int rr) {
-  constexpr int CH = D / 16, RPW = 32 / CH;
-  const int lane = threadIdx.x & 31, c = lane % CH;
-#pragma unroll 2
-  for (int r = row0 + lane / CH; r - lane / CH < end; r += RPW) {
-    const bool on = r >= first && r < end;
-    const int t = r - first;
-    const size_t at = (((size_t)b * p.t_len + t) * p.n_q + h * p.group + g) * D;
-    float x[8], y[8];
-    uint32_t top = 0;
+__device__ __noinline__ void put_queries(const PutParams& p, int b, int h, int slice, int first, int wrow, int end, int rr) {
+  constexpr int LPR = D / 4, RPI = 32 / LPR;   // lanes of a row, rows at a time
+  const int lane = threadIdx.x & 31, c = lane % LPR;
+#pragma unroll 1
+  for (int r0 = wrow + slice * RPI; r0 < min(end, wrow + PUT_WARP_ROWS); r0 += PUT_SLICES * RPI) {
+    const int r = r0 + lane / LPR, t = r - first;
+    const bool on = t >= 0 && r < end;
+    const size_t at = (((size_t)b * p.t_len + (on ? t : 0)) * p.n_q + h * p.group) * D;
+    const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + at) + c;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.q16 + at) + c;
+    float* scale = p.q_scale + ((size_t)b * p.pool.n_kv + h) * p.t_len * p.group + (size_t)(on ? t : 0) * p.group;
+    float2 c0 = {}, c1 = {};   // cos, sin
     if (on) {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + at);
-      const uint4 u = src[c], v = src[c + CH];
-      const CosSin2* cs = p.tab + (size_t)(rr + t) * (D / 2) + c * 8;
-      unpack8(u, x);
-      unpack8(v, y);
+      const CosSin2* cs = p.tab + (size_t)(rr + t) * (D / 2) + 2 * c;
+      c0 = make_float2(cs[0].ch, cs[0].sh);
+      c1 = make_float2(cs[1].ch, cs[1].sh);
+    }
+#pragma unroll 1
+    for (int g0 = 0; g0 < p.group; g0 += 4) {
+      uint32_t u[4], v[4];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float co = cs[e].ch, si = cs[e].sh;
-        const float a = (x[e] * co - y[e] * si) * p.scale_log2;
-        y[e] = (y[e] * co + x[e] * si) * p.scale_log2;
-        x[e] = a;
-        top = max(top, max(__float_as_uint(x[e]) & 0x7FFFFFFFu, __float_as_uint(y[e]) & 0x7FFFFFFFu));
+      for (int k = 0; k < 4; ++k) {
+        const bool some = on && g0 + k < p.group;
+        u[k] = some ? src[(g0 + k) * (D / 2)] : 0;
+        v[k] = some ? src[(g0 + k) * (D / 2) + D / 4] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (g0 + k >= p.group) break;
+        const float x0 = __uint_as_float(u[k] << 16), x1 = __uint_as_float(u[k] & 0xFFFF0000u);
+        const float y0 = __uint_as_float(v[k] << 16), y1 = __uint_as_float(v[k] & 0xFFFF0000u);
+        const float a0 = (x0 * c0.x - y0 * c0.y) * p.scale_log2, b0 = (y0 * c0.x + x0 * c0.y) * p.scale_log2;
+        const float a1 = (x1 * c1.x - y1 * c1.y) * p.scale_log2, b1 = (y1 * c1.x + x1 * c1.y) * p.scale_log2;
+        uint32_t top = max(max(__float_as_uint(a0) & 0x7FFFFFFFu, __float_as_uint(b0) & 0x7FFFFFFFu),
+                           max(__float_as_uint(a1) & 0x7FFFFFFFu, __float_as_uint(b1) & 0x7FFFFFFFu));
+        if (LPR == 32) {
+          top = __reduce_max_sync(0xffffffffu, top);
+        } else {
+#pragma unroll
+          for (int off = LPR / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+        }
+        const int e = top < 0x7F800000u ? scale_exponent(top) : 0;   // a query that is not finite answers NaN
+        const float inv = pow2_float(-e);
+        if (on) {
+          dst[(g0 + k) * (D / 2)] = f16x2(a0 * inv, a1 * inv);
+          dst[(g0 + k) * (D / 2) + D / 4] = f16x2(b0 * inv, b1 * inv);
+          if (c == 0) scale[g0 + k] = top < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
+        }
       }
     }
-#pragma unroll
-    for (int off = CH / 2; off >= 1; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-    if (!on) continue;
-    const int e = top < 0x7F800000u ? scale_exponent(top) : 0;   // a query that is not finite answers NaN
-    const float inv = pow2_float(-e);
-    uint4* dst = reinterpret_cast<uint4*>(p.q16 + at);
-    dst[c] = make_uint4(f16x2(x[0] * inv, x[1] * inv), f16x2(x[2] * inv, x[3] * inv), f16x2(x[4] * inv, x[5] * inv),
-                        f16x2(x[6] * inv, x[7] * inv));
-    dst[c + CH] = make_uint4(f16x2(y[0] * inv, y[1] * inv), f16x2(y[2] * inv, y[3] * inv),
-                             f16x2(y[4] * inv, y[5] * inv), f16x2(y[6] * inv, y[7] * inv));
-    if (c == 0)
-      p.q_scale[((size_t)b * p.pool.n_kv + h) * p.t_len * p.group + (size_t)t * p.group + g] =
-          top < 0x7F800000u ? pow2_float(e) : __uint_as_float(0x7FFFFFFFu);
   }
 }
 
@@ -159,7 +175,7 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   const int page = p.pool.page;
   const int wrow = row0 + warp * PUT_WARP_ROWS;
   if (APPEND && (int)blockIdx.z + p.z0 >= 2) {
-    put_queries<D>(p, b, h, (int)blockIdx.z + p.z0 - 2, first, wrow, min(end, wrow + PUT_WARP_ROWS), rr);
+    put_queries<D>(p, b, h, (int)blockIdx.z + p.z0 - 2, first, wrow, end, rr);
     return;
   }
   const int prow = wrow / page * page;                  // first row of this warp's page
@@ -396,7 +412,7 @@ cudaError_t launch_pages8_fill(const PutParams& p, int head_dim, int max_rows, c
 cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t st) {
   // rows [n, n + t_len) meet at most this many CTAs' rows
   const int rows = put_rows(p), threads = rows / PUT_WARP_ROWS * 32;
-  const dim3 grid((p.t_len + 2 * rows - 2) / rows, p.batch * p.pool.n_kv, (p.q ? 2 + p.group : 2) - p.z0);
+  const dim3 grid((p.t_len + 2 * rows - 2) / rows, p.batch * p.pool.n_kv, (p.q ? 2 + PUT_SLICES : 2) - p.z0);
   return head_dim == 128 ? launch_put<128, true>(p, grid, threads, st) : launch_put<64, true>(p, grid, threads, st);
 }
 
