@@ -294,10 +294,11 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
   if (max_keys < 1 || max_keys > max_pages * pages->page)
     return api_fail(C2KV_EINVAL, "max_keys must be in [1, max_pages * page]");
   const int group = geom->n_q_heads / geom->n_kv_heads;
-  if (chunk_places(batch, geom->n_kv_heads, t_len, group, max_keys) > INT32_MAX / 2 || (int64_t)t_len * group > INT32_MAX / 2)
-    return api_fail(C2KV_EINVAL, "batch * n_q_heads * t_len * max_keys is above 2^30 products of 256 x 128");
   const int sms = std::min(api_sm_count_for_sizing(), kMaxChunkCtas);
   const int wide = chunk_wide(batch, geom->n_kv_heads, t_len, group, max_keys, sms);
+  if (chunk_places(batch, geom->n_kv_heads, t_len, group, max_keys, wide) > INT32_MAX - (1 << 16) ||
+      (int64_t)t_len * group > INT32_MAX / 2)
+    return api_fail(C2KV_EINVAL, "batch * n_q_heads * t_len * max_keys is above about 2^44");
   const ChunkWs w = chunk_workspace(geom, batch, t_len, wide, sms);
   if (workspace_bytes < w.total || !aligned(workspace, 16))
     return api_fail(C2KV_EINVAL, "workspace too small or not 16-byte aligned");

@@ -39,6 +39,7 @@ constexpr int CK_KEYS = 128;       // keys of a tile
 constexpr int kSlots = 8;          // tiles whose pages are known ahead
 constexpr int kChunkMinTiles = 2;  // tiles of a CTA below which fewer CTAs work
 constexpr int kChunkUnitTiles = 2; // what a unit's begin and end cost, in tiles
+constexpr int kChunkWidePlaces = 3, kChunkNarrowPlaces = 2;   // see UnitMath
 constexpr int kChunkFewTiles = 8;  // see chunk_wide
 constexpr int kChunkWholeKeys = 512;  // see chunk_whole
 constexpr int kNoScale = -1000;    // exponent of a tile without a page
@@ -205,8 +206,12 @@ __device__ __forceinline__ void tmem_st_cols16(uint32_t taddr, const float (&r)[
 // 128 w rows, w = 1 or 2, and sees n + e(i) keys, e(i) = floor((128 w (i + 1) - 1) / G)
 // + 1 tokens having rows up to its end, `count` for the last: ceil((n + e(i)) / 128) =
 // floor((w i + c) / G) tiles with c = floor((128 w - 1 + G (n + 128)) / 128).
+// A tile of a unit is `full` places of the work, one of the last unit `cost` (in a batch
+// of 256-row units a unit of up to 128 rows takes two thirds of the time), and the end
+// of a unit `end`.
 struct UnitMath {
   int c, q, r, G, w, units, last;   // c = G q + r; last: tiles of the last unit
+  int full, cost, end;
 
   __device__ __forceinline__ UnitMath(int n, int count, int g, int wide) : G(g), w(wide) {
     c = (int)((128 * w - 1 + (int64_t)g * (n + 128)) >> 7);
@@ -214,18 +219,30 @@ struct UnitMath {
     r = c - q * g;
     units = (int)(((int64_t)count * g + 128 * w - 1) / (128 * w));
     last = (n + count + CK_KEYS - 1) / CK_KEYS;
+    full = w == 1 ? 1 : kChunkWidePlaces;
+    cost = w == 2 && (int64_t)count * g - 256 * (int64_t)(units - 1) <= 128 ? kChunkNarrowPlaces : full;
+    end = full * kChunkUnitTiles;
   }
   __device__ __forceinline__ int tiles(int i) const { return i == units - 1 ? last : (w * i + c) / G; }
   // sum of floor((w k + r) / G) over k < v <= G: the terms are 0 to w
   __device__ __forceinline__ int part(int v) const {
     return w == 1 ? max(0, v - (G - r)) : max(0, v - (G - r + 1) / 2) + max(0, v - (2 * G - r + 1) / 2);
   }
-  // places before unit i, with i = G u + v
+  // tiles of units before unit i < units, with i = G u + v
+  __device__ __forceinline__ int tiles_before(int i) const {
+    const int u = i / G, v = i - u * G;
+    return i * q + w * (G * (u * (u - 1) / 2) + u * v) + u * part(G) + part(v);
+  }
+  __device__ __forceinline__ int all_tiles() const { return tiles_before(units - 1) + last; }
+  __device__ __forceinline__ int cost_of(int i) const { return i == units - 1 ? cost : full; }
+  // places before unit i
   __device__ __forceinline__ int before(int i) const {
-    const int m = min(i, units - 1), u = m / G, v = m - u * G;
-    return m * q + w * (G * (u * (u - 1) / 2) + u * v) + u * part(G) + part(v) + (i == units ? last : 0) + i * kChunkUnitTiles;
+    return full * tiles_before(min(i, units - 1)) + (i == units ? last * cost : 0) + i * end;
   }
 };
+
+template <int W>
+constexpr int kUnitEnd = (W == 1 ? 1 : kChunkWidePlaces) * kChunkUnitTiles;   // places of a unit's end
 
 struct CkCut {   // CTA c owns places [first(c), first(c + 1))
   int base, rem, ctas;
@@ -247,13 +264,15 @@ __device__ __forceinline__ int ck_seq_of(const int32_t* from, int batch, int x) 
   return lo;
 }
 
-// Tiles [t0, t0 + n) of unit i of (b, h); the unit has `tiles`, its first place is `place`.
+// Tiles [t0, t0 + n) of unit i of (b, h); the unit has `tiles` of `cost` places each,
+// its first place is `place`.  A tile is the CTA's that has its first place.
 struct CkSeg {
-  int b, h, i, t0, n, tiles, place;
+  int b, h, i, t0, n, tiles, place, cost;
   __device__ __forceinline__ bool whole() const { return n == tiles; }
+  __device__ __forceinline__ int behind(int end) const { return place + tiles * cost + end; }   // the next unit's place
 };
 
-// The unit at place x, and where in it x is (t0 >= tiles: behind its last tile).
+// The unit at place x, and its first tile at x or behind it (t0 >= tiles: none is).
 __device__ __forceinline__ void ck_locate(const ChunkMap& m, int batch, int G, int w, int x, CkSeg& s) {
   s.b = ck_seq_of(m.start, batch, x);
   const UnitMath um(m.n[s.b], m.count[s.b], G, w);
@@ -269,26 +288,66 @@ __device__ __forceinline__ void ck_locate(const ChunkMap& m, int batch, int G, i
   }
   s.i = lo;
   s.tiles = um.tiles(lo);
-  s.t0 = at - um.before(lo);
-  s.place = x - s.t0;
+  s.cost = um.cost_of(lo);
+  const int off = at - um.before(lo);
+  s.t0 = (int)((uint32_t)(off + s.cost - 1) / (uint32_t)s.cost);
+  s.place = x - off;
 }
 
 // The CTA's next segment at place x or behind it; false: none before x1.
-__device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, int w, int x, int x1, CkSeg& s) {
+template <int W>
+__device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, int x, int x1, CkSeg& s) {
 #pragma unroll 1
   for (;;) {
     if (x >= x1) return false;
-    ck_locate(m, batch, G, w, x, s);
+    ck_locate(m, batch, G, W, x, s);
     if (s.t0 < s.tiles) {
-      s.n = min(s.tiles - s.t0, x1 - x);
-      return true;
+      s.n = min(s.tiles, (int)((uint32_t)(x1 - s.place + s.cost - 1) / (uint32_t)s.cost)) - s.t0;
+      return s.n > 0;
     }
-    x = s.place + s.tiles + kChunkUnitTiles;
+    x = s.behind(kUnitEnd<W>);
   }
 }
-__device__ __forceinline__ bool ck_next(const ChunkMap& m, int batch, int G, int w, int x1, CkSeg& s) {
-  const int x = s.place + s.t0 + s.n;
-  return ck_seg_at(m, batch, G, w, s.t0 + s.n == s.tiles ? x + kChunkUnitTiles : x, x1, s);
+template <int W>
+__device__ __forceinline__ bool ck_next(const ChunkMap& m, int batch, int G, int x1, CkSeg& s) {
+  return s.t0 + s.n == s.tiles && ck_seg_at<W>(m, batch, G, s.behind(kUnitEnd<W>), x1, s);
+}
+
+// Rows begin, begin + 2 (at head_dim 64: 4) - 1 by a warp, and so on before `end`, of the
+// unit that begins at row `first` of (b, h): its queries, as the launch before left
+// them, to row rt0 + r mod 128 of their tile.
+template <int D>
+__device__ __forceinline__ void ck_copy_queries(const ChunkParams& p, uint32_t q_smem, int b, int h, int first, int begin, int end, int rt0) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows at a time
+  const int lane = threadIdx.x & 31, c = lane % LPR, G = p.group;
+  int r = begin + lane / LPR, t = (first + r) / G, g = first + r - t * G;
+  const __nv_bfloat16* src = p.out + ((size_t)b * p.t_len * p.n_q + h * G) * D + c * 8;
+#pragma unroll 4
+  for (; r < end; r += RPI) {
+    const int rt = rt0 + (r & 127);
+    const uint32_t dst = q_smem + (r >> 7) * (128 * D * 2) + (c >> 3) * 16384 + rt * 128 + (((c & 7) ^ (rt & 7)) << 4);
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src + ((size_t)t * p.n_q + g) * D) : "memory");
+    for (g += RPI; g >= G; g -= G) ++t;
+  }
+}
+
+// Lane l of each four has row l's four pieces: afterwards piece l of the four rows.
+__device__ __forceinline__ void transpose4(uint4 (&a)[4]) {
+  const bool b0 = threadIdx.x & 1, b1 = threadIdx.x & 2;
+  auto swap = [](uint4& keep0, uint4& keep1, bool hi, int by) {
+    const uint4 give = hi ? keep0 : keep1;
+    uint4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, by);
+    got.y = __shfl_xor_sync(0xffffffffu, give.y, by);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, by);
+    got.w = __shfl_xor_sync(0xffffffffu, give.w, by);
+    if (hi) keep0 = got;
+    else keep1 = got;
+  };
+  swap(a[0], a[1], b0, 1);
+  swap(a[2], a[3], b0, 1);
+  swap(a[0], a[2], b1, 2);
+  swap(a[1], a[3], b1, 2);
 }
 
 // W: units of 128 W rows.
@@ -382,7 +441,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       if (count > 0) {
         const UnitMath um(n, count, G, W);
         per = um.before(um.units);
-        all = (per - um.units * kChunkUnitTiles) * p.pool.n_kv;
+        all = um.all_tiles() * p.pool.n_kv;
       }
       const int v = per * p.pool.n_kv;
       int incl = v;
@@ -431,11 +490,11 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           int& x = i == 0 ? x0 : x1;
           if (x >= places) continue;
           ck_locate(M, p.batch, G, W, x, sg);
-          if (sg.t0 > 0) x = sg.place + sg.tiles + kChunkUnitTiles;
+          if (x > sg.place) x = sg.behind(kUnitEnd<W>);
         }
       }
       int seg = 0, at = lane >> 3, j = lane >> 3;   // tile `at` of segment `seg`, the CTA's j-th
-      bool more = ck_seg_at(M, p.batch, G, W, x0, x1, sg);
+      bool more = ck_seg_at<W>(M, p.batch, G, x0, x1, sg);
       int done = 0;   // tiles of the segments before
       struct Ref {
         int32_t id, key0, rows, diag, ctas;   // id: -1 no page here, -2 outside the pool
@@ -449,7 +508,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         while (more && at - done >= sg.n) {
           done += sg.n;
           ++seg;
-          more = ck_next(M, p.batch, G, W, x1, sg);
+          more = ck_next<W>(M, p.batch, G, x1, sg);
         }
         r.on = more;
         if (more) {
@@ -464,8 +523,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           r.key0 = r.tile * CK_KEYS;
           r.rows = min(end - r.key0, CK_KEYS);
           r.diag = n + first / G + 1 - r.key0;
-          r.ctas = sg.t0 == 0 && !sg.whole() ? cut.of(sg.place + sg.tiles - 1) - cta + 1 : 0;
-          const bool ends = sg.t0 + sg.n < sg.tiles || sg.place + sg.tiles + kChunkUnitTiles >= x1;
+          r.ctas = sg.t0 == 0 && !sg.whole() ? cut.of(sg.place + (sg.tiles - 1) * sg.cost) - cta + 1 : 0;
+          const bool ends = sg.t0 + sg.n < sg.tiles || sg.behind(kUnitEnd<W>) >= x1;
           r.flags = (r.key0 + r.rows > n / p.pool.page * p.pool.page ? kFresh : 0u) | (sg.whole() ? kWhole : 0u) | (ends ? kEnd : 0u) | (min(all - first, unit) > 128 ? kWide : 0u);
           if (16 * g < r.rows) {
             r.id = p.page_table[(size_t)sg.b * p.max_pages + (r.key0 + 16 * g) / p.pool.page];
@@ -730,30 +789,29 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       }
       return true;
     };
-    auto load_queries = [&](int before) -> bool {   // `before`: segments whose queries these take the place of
+    // The segment's queries are asked for ...
+    auto ask_queries = [&](int before) -> bool {   // `before`: segments whose queries these take the place of
       if (before > 0 && !__all_sync(0xffffffffu, ck_wait(q_free, (before - 1) & 1, abort_flag, p.err))) return false;
       const bool wide = W == 2 && (sg.flags & kWide), twice = W == 1 && sg.rows <= 64;
       // rows behind the last one are left as they are: what comes of them is not used
-      constexpr int LPR = D / 8, RPI = 32 / LPR;   // lanes of a row, rows at a time
-      const int c = lane % LPR, begin = (wide ? m * 128 : twice ? 0 : m * 64) + (warp & 3) * (wide ? 32 : 16);
-      const int end = min(sg.rows, begin + (wide ? 32 : 16)), row = row_of(wide, twice);
+      const int begin = (wide ? m * 128 : twice ? 0 : m * 64) + (warp & 3) * (wide ? 32 : 16), row = row_of(wide, twice);
       grid_wait();
-      for (int r = begin + lane / LPR; r < end; r += RPI) {
-        const int rq = sg.first + r, rt = twice ? m * 64 + r : r & 127;
-        const __nv_bfloat16* src = p.out + (((size_t)sg.b * p.t_len + rq / G) * p.n_q + sg.h * G + rq % G) * D + c * 8;
-        const uint32_t dst = smem_addr(smem + C::OFF_Q) + (r >> 7) * C::TILE + (c >> 3) * 16384 + rt * 128 + (((c & 7) ^ (rt & 7)) << 4);
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-      }
+      ck_copy_queries<D>(p, smem_addr(smem + C::OFF_Q), sg.b, sg.h, sg.first, begin, min(sg.rows, begin + (wide ? 32 : 16)),
+                         twice ? m * 64 : 0);
       qs_next = (uint32_t)row < (uint32_t)sg.rows ? p.q_scale[((size_t)sg.b * p.pool.n_kv + sg.h) * p.t_len * G + sg.first + row] : 0.f;
+      return true;
+    };
+    // ... and are there.
+    auto queries_here = [&]() {
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[m]);
-      return true;
     };
     ok = take();
     if (ok && !(sg.flags & kNone)) {
-      ok = load_queries(0);
+      ok = ask_queries(0);
+      if (ok) queries_here();
     } else {
       ok = false;
     }
@@ -896,6 +954,13 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       }
       if (!ok) break;
       // ---- epilogue
+      // The next segment's queries are copied while the last products are made.
+      const Seg was = sg;
+      const bool ends = was.flags & kEnd;
+      if (!ends) {
+        ok = take() && ask_queries(seg + 1);
+        if (!ok) break;
+      }
       const bool mine = wide || m == 0 || tiles > 1;   // this half had a tile
       if (mine) {
         ok = __all_sync(0xffffffffu, ck_wait(&s_full[2 * m + 1], ns & 1, abort_flag, p.err));
@@ -932,18 +997,13 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         if (!ok) break;
         if (live) other = hand[row];
       }
-      // The next segment's queries come first, so that its first scores are made
-      // meanwhile; but not while the first half still reads the second half's sums.
-      const Seg was = sg;
-      const bool ends = was.flags & kEnd;
-      if (!ends && !two) {
-        ok = take() && load_queries(seg + 1);
-        if (!ok) break;
-      }
+      // The next scores are made meanwhile; but not while the first half still reads the
+      // second half's sums.
+      if (!ends && !two) queries_here();
       if (warp_live && (wide || m == 0)) {
         tc_fence_after();
         const bool whole = was.flags & kWhole;
-        const int rq = was.first + row, n = M.n[was.b];
+        const int n = M.n[was.b];
         const bool nan = nan_seg[seg & 3] == seg + 1;
         float f = v_ref == kNoScale ? 0.f : pow2_float(v_ref), f1 = 0.f;
         if (two) {
@@ -959,6 +1019,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           f *= inv;
           f1 *= inv;
         }
+        const int t_of = (was.first + row) / G;
+        const uint32_t to = live ? (uint32_t)((was.b * p.t_len + t_of) * p.n_q + was.h * G + was.first + row - t_of * G) : ~0u;   // row of out
         const int slot = 2 * cta + (t0 == 0 ? 1 : 0);   // of a unit's first part: see the merge
         if (!whole && live) p.part_ml[(size_t)slot * p.part_rows + row] = make_float2(m_run, l_run);
 #pragma unroll 1
@@ -975,8 +1037,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = fmaf(y[i], f1, o[i]);
           }
-          if (!live) continue;
-          if (two && twice) {
+          if (live && two && twice) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               const float4 y = hand_o[(c0 + i) / 4 * 64 + row];
@@ -986,7 +1047,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               o[i + 3] = fmaf(y.w, f1, o[i + 3]);
             }
           }
-          if (nan) {   // values that are not numbers, for the rows that see them
+          if (live && nan) {   // values that are not numbers, for the rows that see them
             const int end = min(lim, (t0 + tiles) * CK_KEYS);
             for (int key = max(n + was.first / G + 1, t0 * CK_KEYS); key < end; ++key) {
               const int id = p.page_table[(size_t)was.b * p.max_pages + key / p.pool.page];
@@ -999,14 +1060,21 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             }
           }
           if (whole) {
-            uint4* dst = reinterpret_cast<uint4*>(
-                p.out + (((size_t)was.b * p.t_len + rq / G) * p.n_q + was.h * G + rq % G) * D + c0);
+            uint4 out[4];
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               const float e[8] = {o[i], o[i + 1], o[i + 2], o[i + 3], o[i + 4], o[i + 5], o[i + 6], o[i + 7]};
-              dst[i / 8] = pack8(e);
+              out[i / 8] = pack8(e);
             }
-          } else {
+            // four lanes have a row's 64 bytes, and so whole sectors: a lane's own row is
+            // 16 bytes of 32 lines a store (a unit of 256 rows then took 2 us longer)
+            transpose4(out);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t at = __shfl_sync(0xffffffffu, to, (lane & ~3) + k);
+              if (at != ~0u) reinterpret_cast<uint4*>(p.out)[(size_t)at * (D / 8) + c0 / 8 + (lane & 3)] = out[k];
+            }
+          } else if (live) {
             float4* dst = p.part_o + ((size_t)slot * (D / 4) + c0 / 4) * p.part_rows + row;
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
@@ -1016,10 +1084,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         tc_fence_before();
       }
       if (ends) break;
-      if (two) {
-        ok = take() && load_queries(seg + 1);
-        if (!ok) break;
-      }
+      if (two) queries_here();
     }
   }
   grid_wait();   // the launch completes only behind the append
@@ -1163,9 +1228,9 @@ int chunk_part_rows(int t_len, int group, int wide) {
   return (int)std::min<int64_t>(128 * wide, ((int64_t)t_len * group + 31) / 32 * 32);
 }
 
-int64_t chunk_places(int batch, int n_kv, int t_len, int group, int max_keys) {
-  const int64_t units = ((int64_t)t_len * group + 127) / 128;
-  return batch * (int64_t)n_kv * units * ((max_keys + CK_KEYS - 1) / CK_KEYS + kChunkUnitTiles);
+int64_t chunk_places(int batch, int n_kv, int t_len, int group, int max_keys, int wide) {
+  const int64_t units = ((int64_t)t_len * group + 128 * wide - 1) / (128 * wide);
+  return batch * (int64_t)n_kv * units * ((max_keys + CK_KEYS - 1) / CK_KEYS + kChunkUnitTiles) * (wide == 1 ? 1 : kChunkWidePlaces);
 }
 
 cudaError_t launch_attend_chunk8(const ChunkParams& p, int head_dim, int sms, cudaStream_t st) {
