@@ -339,7 +339,7 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
   p.part_ml = reinterpret_cast<float2*>(ws + w.ml_off);
   p.part_o = reinterpret_cast<float4*>(ws + w.o_off);
   p.wide = wide;
-  p.whole = chunk_whole(max_keys) ? 1 : 0;
+  p.whole = chunk_whole(batch, geom->n_kv_heads, t_len, group, max_keys, wide, sms) ? 1 : 0;
   p.part_rows = chunk_part_rows(t_len, group, wide);
   p.inject_timeout = api_take_injected_timeout();
   s = api_launched(launch_attend_chunk8(p, geom->head_dim, sms, st), "c2kv_attend_pages8_chunk");

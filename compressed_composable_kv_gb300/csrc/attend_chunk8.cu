@@ -40,8 +40,8 @@ constexpr int kSlots = 8;          // tiles whose pages are known ahead
 constexpr int kChunkMinTiles = 2;  // tiles of a CTA below which fewer CTAs work
 constexpr int kChunkUnitTiles = 2; // what a unit's begin and end cost, in tiles
 constexpr int kChunkWidePlaces = 3, kChunkNarrowPlaces = 2;   // see UnitMath
-constexpr int kChunkFewTiles = 8;  // see chunk_wide
-constexpr int kChunkWholeKeys = 512;  // see chunk_whole
+constexpr int kChunkFewTiles = 16;  // see chunk_wide
+constexpr int kChunkWholeKeys = 512, kChunkMergeTiles = 4;  // see chunk_whole
 constexpr int kNoScale = -1000;    // exponent of a tile without a page
 constexpr float kRescaleLog2 = 8.f;   // a row's maximum may lag behind by this (weights up to 2^15, sums exact)
 constexpr float kWeightLog2 = 7.f;
@@ -241,9 +241,6 @@ struct UnitMath {
   }
 };
 
-template <int W>
-constexpr int kUnitEnd = (W == 1 ? 1 : kChunkWidePlaces) * kChunkUnitTiles;   // places of a unit's end
-
 struct CkCut {   // CTA c owns places [first(c), first(c + 1))
   int base, rem, ctas;
   __device__ __forceinline__ int first(int c) const { return c * base + min(c, rem); }
@@ -265,20 +262,30 @@ __device__ __forceinline__ int ck_seq_of(const int32_t* from, int batch, int x) 
 }
 
 // Tiles [t0, t0 + n) of unit i of (b, h); the unit has `tiles` of `cost` places each,
-// its first place is `place`.  A tile is the CTA's that has its first place.
+// its first place is `place`, the next unit's `next`.  A tile is the CTA's that has its
+// first place.  Where units are left whole, each is one place.
 struct CkSeg {
-  int b, h, i, t0, n, tiles, place, cost;
+  int b, h, i, t0, n, tiles, place, cost, next;
   __device__ __forceinline__ bool whole() const { return n == tiles; }
-  __device__ __forceinline__ int behind(int end) const { return place + tiles * cost + end; }   // the next unit's place
 };
 
 // The unit at place x, and its first tile at x or behind it (t0 >= tiles: none is).
-__device__ __forceinline__ void ck_locate(const ChunkMap& m, int batch, int G, int w, int x, CkSeg& s) {
+template <int W>
+__device__ __forceinline__ void ck_locate(const ChunkMap& m, int batch, int G, bool whole, int x, CkSeg& s) {
   s.b = ck_seq_of(m.start, batch, x);
-  const UnitMath um(m.n[s.b], m.count[s.b], G, w);
+  const UnitMath um(m.n[s.b], m.count[s.b], G, W);
   const int per = m.per[s.b], r = x - m.start[s.b];
   s.h = (int)((uint32_t)r / (uint32_t)per);
   const int at = r - s.h * per;
+  if (whole) {
+    s.i = at;
+    s.tiles = um.tiles(at);
+    s.t0 = 0;
+    s.cost = 1;
+    s.place = x;
+    s.next = x + 1;
+    return;
+  }
   int lo = 0, hi = um.units;
 #pragma unroll 1
   while (hi - lo > 1) {
@@ -292,25 +299,26 @@ __device__ __forceinline__ void ck_locate(const ChunkMap& m, int batch, int G, i
   const int off = at - um.before(lo);
   s.t0 = (int)((uint32_t)(off + s.cost - 1) / (uint32_t)s.cost);
   s.place = x - off;
+  s.next = s.place + s.tiles * s.cost + um.end;
 }
 
 // The CTA's next segment at place x or behind it; false: none before x1.
 template <int W>
-__device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, int x, int x1, CkSeg& s) {
+__device__ __forceinline__ bool ck_seg_at(const ChunkMap& m, int batch, int G, bool whole, int x, int x1, CkSeg& s) {
 #pragma unroll 1
   for (;;) {
     if (x >= x1) return false;
-    ck_locate(m, batch, G, W, x, s);
+    ck_locate<W>(m, batch, G, whole, x, s);
     if (s.t0 < s.tiles) {
-      s.n = min(s.tiles, (int)((uint32_t)(x1 - s.place + s.cost - 1) / (uint32_t)s.cost)) - s.t0;
+      s.n = whole ? s.tiles : min(s.tiles, (int)((uint32_t)(x1 - s.place + s.cost - 1) / (uint32_t)s.cost)) - s.t0;
       return s.n > 0;
     }
-    x = s.behind(kUnitEnd<W>);
+    x = s.next;
   }
 }
 template <int W>
-__device__ __forceinline__ bool ck_next(const ChunkMap& m, int batch, int G, int x1, CkSeg& s) {
-  return s.t0 + s.n == s.tiles && ck_seg_at<W>(m, batch, G, s.behind(kUnitEnd<W>), x1, s);
+__device__ __forceinline__ bool ck_next(const ChunkMap& m, int batch, int G, bool whole, int x1, CkSeg& s) {
+  return s.t0 + s.n == s.tiles && ck_seg_at<W>(m, batch, G, whole, s.next, x1, s);
 }
 
 // Rows begin, begin + 2 (at head_dim 64: 4) - 1 by a warp, and so on before `end`, of the
@@ -440,7 +448,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       int per = 0, all = 0;
       if (count > 0) {
         const UnitMath um(n, count, G, W);
-        per = um.before(um.units);
+        per = p.whole ? um.units : um.before(um.units);
         all = um.all_tiles() * p.pool.n_kv;
       }
       const int v = per * p.pool.n_kv;
@@ -471,7 +479,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   CkCut cut;
   const int places = M.start[kMaxPagedSeqs];
-  cut.ctas = min((int)gridDim.x, max(1, M.tiles / kChunkMinTiles));
+  // (where units are cut, a CTA's range holds a tile's first place, so that none between
+  // a unit's first and last CTA is left out)
+  cut.ctas = min((int)gridDim.x,
+                 max(1, p.whole ? places : min(M.tiles / kChunkMinTiles, places / (W == 1 ? 1 : kChunkWidePlaces))));
   cut.base = places / cut.ctas;
   cut.rem = places - cut.base * cut.ctas;
   if (tid == 0) p.desc[cta * 8] = 0;   // no unit to merge, so far
@@ -483,18 +494,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       // tile of four; the ids of the next four are on their way meanwhile
       const int g = lane & 7;
       CkSeg sg;
-      int x0 = cta < cut.ctas ? cut.first(cta) : places, x1 = cta < cut.ctas ? cut.first(cta + 1) : places;
-      if (p.whole) {   // no unit is cut: the ranges begin where one does
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          int& x = i == 0 ? x0 : x1;
-          if (x >= places) continue;
-          ck_locate(M, p.batch, G, W, x, sg);
-          if (x > sg.place) x = sg.behind(kUnitEnd<W>);
-        }
-      }
+      const int x0 = cta < cut.ctas ? cut.first(cta) : places, x1 = cta < cut.ctas ? cut.first(cta + 1) : places;
       int seg = 0, at = lane >> 3, j = lane >> 3;   // tile `at` of segment `seg`, the CTA's j-th
-      bool more = ck_seg_at<W>(M, p.batch, G, x0, x1, sg);
+      bool more = ck_seg_at<W>(M, p.batch, G, p.whole, x0, x1, sg);
       int done = 0;   // tiles of the segments before
       struct Ref {
         int32_t id, key0, rows, diag, ctas;   // id: -1 no page here, -2 outside the pool
@@ -508,7 +510,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         while (more && at - done >= sg.n) {
           done += sg.n;
           ++seg;
-          more = ck_next<W>(M, p.batch, G, x1, sg);
+          more = ck_next<W>(M, p.batch, G, p.whole, x1, sg);
         }
         r.on = more;
         if (more) {
@@ -524,7 +526,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           r.rows = min(end - r.key0, CK_KEYS);
           r.diag = n + first / G + 1 - r.key0;
           r.ctas = sg.t0 == 0 && !sg.whole() ? cut.of(sg.place + (sg.tiles - 1) * sg.cost) - cta + 1 : 0;
-          const bool ends = sg.t0 + sg.n < sg.tiles || sg.behind(kUnitEnd<W>) >= x1;
+          const bool ends = sg.t0 + sg.n < sg.tiles || sg.next >= x1;
           r.flags = (r.key0 + r.rows > n / p.pool.page * p.pool.page ? kFresh : 0u) | (sg.whole() ? kWhole : 0u) | (ends ? kEnd : 0u) | (min(all - first, unit) > 128 ? kWide : 0u);
           if (16 * g < r.rows) {
             r.id = p.page_table[(size_t)sg.b * p.max_pages + (r.key0 + 16 * g) / p.pool.page];
@@ -1220,9 +1222,17 @@ int chunk_wide(int batch, int n_kv, int t_len, int group, int max_keys, int ctas
   return tiles < (int64_t)kChunkFewTiles * ctas ? 1 : 2;
 }
 
-// Units of few tiles are not cut: a third launch costs more than their tiles one
-// after another.
-bool chunk_whole(int max_keys) { return max_keys <= kChunkWholeKeys; }
+// Whether units are left whole: the call then has no third launch, and no CTA a second
+// end.  In tiles, of the longest CTA: its units one after another, against an even
+// share, another end and what the third launch takes (kChunkMergeTiles).  Units of few
+// tiles are whole in any case.
+bool chunk_whole(int batch, int n_kv, int t_len, int group, int max_keys, int wide, int ctas) {
+  if (max_keys <= kChunkWholeKeys) return true;
+  const int64_t units = batch * (int64_t)n_kv * (((int64_t)t_len * group + 128 * wide - 1) / (128 * wide));
+  const int64_t tiles = (max_keys + CK_KEYS - 1) / CK_KEYS + kChunkUnitTiles;
+  const int64_t each = (units + ctas - 1) / ctas;
+  return each * tiles * ctas <= units * tiles + std::min<int64_t>(units, ctas) * kChunkUnitTiles + ctas * (int64_t)kChunkMergeTiles;
+}
 
 int chunk_part_rows(int t_len, int group, int wide) {
   return (int)std::min<int64_t>(128 * wide, ((int64_t)t_len * group + 31) / 32 * 32);

@@ -199,7 +199,7 @@ cudaError_t launch_attend_chunk8(const ChunkParams& p, int head_dim, int sms, cu
 cudaError_t launch_attend_chunk8_merge(const ChunkParams& p, int head_dim, int sms, cudaStream_t st);
 int chunk_wide(int batch, int n_kv, int t_len, int group, int max_keys, int ctas);   // ChunkParams::wide
 int chunk_part_rows(int t_len, int group, int wide);
-bool chunk_whole(int max_keys);   // ChunkParams::whole
+bool chunk_whole(int batch, int n_kv, int t_len, int group, int max_keys, int wide, int ctas);   // ChunkParams::whole
 int64_t chunk_places(int batch, int n_kv, int t_len, int group, int max_keys, int wide);   // at most
 size_t move_workspace_ints(int n_pages, int batch, int max_pages);
 cudaError_t launch_pages8_plan(const MoveParams& p, cudaStream_t st);

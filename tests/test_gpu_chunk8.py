@@ -440,6 +440,22 @@ def test_units_of_both_sizes(t_len, held):
     c.check("units", rows=[0, 31, 32, 63, 64, t_len // 2, t_len - 1])
 
 
+@pytest.mark.parametrize("group,t_len,held", [
+    (4, 8, [(53 * i * i) % 870 if i % 9 != 4 else -1 for i in range(30)]),   # two units to a CTA, left whole; empty places
+    (5, 170, [3800, 17, 3500, 129]),                                         # one to a CTA, of 256 rows and of 82
+    (5, 170, [5600, 5555, 3]),                                               # the same, cut
+    (4, 8, [2500] * 20),                                                     # of 32 rows, cut
+])
+def test_units_left_whole_and_cut(group, t_len, held):
+    g = _geom(64, group, 8)
+    new = [0 if h < 0 else t_len - (3 * i) % min(t_len, 8) for i, h in enumerate(held)]
+    c = Chunk(g, 64, held, new, t_len=t_len, seed=group + t_len)
+    c.call()
+    _ok()
+    c.put_new()
+    c.check("%s %s" % (group, t_len), rows=[0, 1, t_len // 2, t_len - 1])
+
+
 def test_queries_in_the_output_buffer():
     """out may be q itself."""
     g = _geom(128, 4, 2)
