@@ -3,9 +3,9 @@
 //   s_j = (R q . K_j) / sqrt(d),  out = sum_j exp(s_j - m) V_j / sum_j exp(s_j - m)
 // over the rows j up to the token's own; K_j and V_j = code * scale of their page.
 //
-// A unit is 256 (or 128) (token, query head) rows of one (sequence, kv head), token-major,
+// A unit is 256 or 128 (token, query head) rows of one (sequence, kv head), token-major,
 // against the key tiles (128 rows) that they see.  Every e4m3 code is an fp16
-// number, so a tile's codes are brought to fp16 once for all 256 rows, and both
+// number, so a tile's codes are brought to fp16 once for all rows of the unit, and both
 // products run as kind::f16 (fp32 accumulators): the keys and values lose
 // nothing; a query row is held in fp16 times a power of two of its own, 2^-11 of
 // each element, and so is a weight (2^7 exp(s - m), so that weights down to 2^-21
@@ -14,14 +14,35 @@
 // of them by an exact multiplication in fp16; the tile's K scale multiplies the
 // scores, its V scale, over the largest so far, the weights.
 //
-// The places of all units (their tiles, and kUnitTiles for the end of each) are
-// laid end to end, from the device-side lengths, and cut into one even range per
-// CTA (one to an SM).  A unit that one CTA holds whole is written at once; else its
-// CTAs write partial (m, l, O) and merge_kernel joins them in the order of the keys.
+// The places of all units (their tiles, and some for the end of each) are laid end to
+// end, from the device-side lengths, and cut into one even range per CTA (one to an SM).
+// A unit that one CTA holds whole is written at once; else its CTAs write partial
+// (m, l, O) and merge_kernel joins them in the order of the keys.
 //
-// Roles: warps 0-3 and 4-7 softmax and epilogue of the unit's two 128-row tiles
-// (a thread to a row), warps 8-11 and 12-15 the codes of K and V to fp16, warp 16
-// page ids and scales ahead of them, warps 17 and 18 the MMAs, warp 19 tensor memory.
+// A call is two launches, or three: the append, whose further CTAs rotate the queries
+// into the output buffer (fp16, pages8.cu), this kernel, and the join where units are
+// cut.  Each is set up, and reads what the one before does not write, while that one runs.
+//
+// Roles: warps 0-3 and 4-7 softmax and epilogue, a thread to a row (of a unit of 256 rows
+// each four have 128; of a smaller one each four have every other key tile), warps 8-11
+// and 12-15 the codes of K and V to fp16, warp 16 page ids and scales ahead of them and
+// their codes to L2, warps 17 and 18 the MMAs of a half each, warp 19 tensor memory.
+//
+// What bounds it.  256 rows: scores, weights and products of 64 keys go round in two parts
+// of a tile for each half, and the two halves fill each other's waits.  A tile takes
+// 2.3 us of an SM, against 1.3 at the bf16 rate that a library product reaches: left out,
+// the conversion is worth 4 %, three quarters of the scores' products 5 %, the exponentials
+// 5 %, all of the softmax 15 %, so no part alone is the limit; N = 64 costs the scores'
+// products half again as much (Q's rows come from shared memory, 128 bytes a cycle), but
+// N = 128 leaves a half nothing to do while its scores are made (4 x 512 tokens over 32768
+// 974-1040 us against 990, 8 x 128 137 against 132, 16 x 5 75 against 73).  128 rows: a
+// tile takes 1.5 us, the halves' chains of scores, weights, products and the next stage's
+// codes, of which none can be left out for more than 7 %.  Few rows over short caches: the
+// launches, 3 to 4 us each, and the way through the first tile, 4 us.
+//
+// 32 query heads of 128 over 8 kv heads: 4 x 512 tokens over 32768 990 us (1.12 PFLOP/s),
+// 1 x 4000 over nothing 203 us, 16 x 5 over 1000 to 8000 67 us (2.1 TB/s), 1 x 64 over 8000
+// 34 us; 40 heads over 8, 8 x 128 over 7000 to 8000 111 us (0.55 PFLOP/s).
 #include <float.h>
 
 #include <algorithm>
@@ -34,13 +55,19 @@ namespace c2kv {
 namespace {
 
 constexpr int CK_THREADS = 640;
-constexpr int CK_ROWS = 256;       // rows of a unit
 constexpr int CK_KEYS = 128;       // keys of a tile
 constexpr int kSlots = 8;          // tiles whose pages are known ahead
-constexpr int kChunkMinTiles = 2;  // tiles of a CTA below which fewer CTAs work
-constexpr int kChunkUnitTiles = 2; // what a unit's begin and end cost, in tiles
-constexpr int kChunkWidePlaces = 3, kChunkNarrowPlaces = 2;   // see UnitMath
-constexpr int kChunkFewTiles = 16;  // see chunk_wide
+// Tiles of a CTA below which fewer CTAs work, where units are cut: a part costs its sums
+// and their joining (7 x 7 tokens over 58 to 847 rows 23.4 us at 1, 21.0 at 2, 24.8 at 3).
+constexpr int kChunkMinTiles = 2;
+// What a unit's begin and end cost, in tiles (16 x 5 over 1000 to 8000 72 us at 1, 67 at 2;
+// 1 x 4000 222 and 203 us).
+constexpr int kChunkUnitTiles = 2;
+// What a tile of a 256-row unit counts, and one of up to 128 rows among them (8 x 128 of
+// group 5, whose units have 256, 256 and 128 rows: 124 us where both count the same, 115 at
+// 8 to 5, 114 at 3 to 2).
+constexpr int kChunkWidePlaces = 3, kChunkNarrowPlaces = 2;
+constexpr int kChunkFewTiles = 16; // see chunk_wide
 constexpr int kChunkWholeKeys = 512, kChunkMergeTiles = 4;  // see chunk_whole
 constexpr int kNoScale = -1000;    // exponent of a tile without a page
 constexpr float kRescaleLog2 = 8.f;   // a row's maximum may lag behind by this (weights up to 2^15, sums exact)
@@ -402,7 +429,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         mbar_init(&p_full[2 * i + k], 4);
       }
       mbar_init(&k_full[i], 4);
-      mbar_init(&k_empty[i], W == 1 ? 1 : 8);   // an MMA issuer; softmax warps, of a narrow unit four, twice
+      // an MMA issuer's commit; with 256-row units the softmax warps, of a smaller one four,
+      // twice (there the commits cost more than the wait: 4 x 512 over 32768 1112 us, not
+      // 1013; here 16 x 5 70 us, not 73)
+      mbar_init(&k_empty[i], W == 1 ? 1 : 8);
       mbar_init(&v_full[i], 4);
       mbar_init(&v_empty[i], W == 1 ? 1 : 8);
     }
@@ -647,8 +677,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               for (int kk = 0; kk < 4; ++kk)
                 mma_bf16_tmem_a(o_col, s_col + kk * 8, v + (uint32_t)(4 * part + kk) * (2048 >> 4), idesc_pv,
                                 t > t0 || part + kk > 0 ? 1u : 0u);
-              // at once: the next tile of this half takes the same stage (beside the
-              // work of wide units the commits cost more than the wait)
+              // the next tile of this half takes the same stage
               if (W == 1 && part == 1) mma_commit(&v_empty[jt & 1]);
             }
             if (tn < n) {
@@ -765,7 +794,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
     } sg;
     float qs = 0.f, qs_next = 0.f;   // the row's power of two
     // The thread's row of the unit.  Up to 64 rows stand twice in a tile, the second
-    // half works on the second 64 lanes: on other parts of the SM than the first.
+    // half works on the second 64 lanes: on other parts of the SM than the first (16 x 5
+    // 67 us, not 70).
     auto row_of = [&](bool wide, bool twice) { return wide ? tid : twice ? (tid & 127) - 64 * m : tid & 127; };
     int j = 0, seg = 0;
     // The segment that begins with tile j, and its queries, as the launch before left them.
@@ -1103,6 +1133,8 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
 // the unit's first tile (its part is slot 2 c + 1, those of the CTAs behind it slot
 // 2 c'); blockIdx.y: 32 rows, blockIdx.z: 32 columns; a lane to a row, a warp to four
 // columns.
+// Bound by the parts' bytes (1 x 4000 tokens 34 MB: 22 us from memory, less where they
+// are in L2) and, where they are few, by its launch and two dependent reads (5 us).
 constexpr int MG_THREADS = 256;
 template <int D>
 __global__ void __launch_bounds__(MG_THREADS) merge_kernel(const __grid_constant__ ChunkParams p) {
@@ -1214,18 +1246,24 @@ cudaError_t launch_merge(const ChunkParams& p, int sms, cudaStream_t st) {
 
 // 128-row tiles of a unit: one where that leaves each CTA few tiles (a part's sums are
 // half as much to store and to join, which then is much of the time), else two, whose
-// rows share the work of bringing the codes to fp16.
+// rows share the work of bringing the codes to fp16.  3 x 333 tokens over 100 to 4999 rows,
+// 10 tiles of 256 rows to a CTA: 29 us by 128 rows, 32 by 256; 16 x 64 over 4000, 27 tiles:
+// 122 and 113 us.
 int chunk_wide(int batch, int n_kv, int t_len, int group, int max_keys, int ctas) {
   const int64_t rows = (int64_t)t_len * group;
   if (rows <= 128) return 1;
-  const int64_t tiles = batch * (int64_t)n_kv * ((rows + CK_ROWS - 1) / CK_ROWS) * ((max_keys + CK_KEYS - 1) / CK_KEYS);
+  const int64_t tiles = batch * (int64_t)n_kv * ((rows + 255) / 256) * ((max_keys + CK_KEYS - 1) / CK_KEYS);
   return tiles < (int64_t)kChunkFewTiles * ctas ? 1 : 2;
 }
 
 // Whether units are left whole: the call then has no third launch, and no CTA a second
 // end.  In tiles, of the longest CTA: its units one after another, against an even
-// share, another end and what the third launch takes (kChunkMergeTiles).  Units of few
-// tiles are whole in any case.
+// share, another end and what the third launch takes (kChunkMergeTiles).  Whole and cut,
+// in us, 32 query heads over 8: 8 x 128 tokens over 4000 rows 90 and 108, 4 x 200 over 4000
+// 88 and 95, 16 x 30 over 1000 31 and 42, 4 x 33 over 1800 41 and 35, 2 x 100 over 900 31
+// and 30.  (All units count as long as max_keys allows: where lengths differ and a CTA has
+// several units it may be wrong by a tenth, 32 x 5 over 100 to 2000 70 and 62.)  Units of
+// few tiles are whole in any case: 8 x 4 over up to 300 rows of head_dim 64 17 and 19.
 bool chunk_whole(int batch, int n_kv, int t_len, int group, int max_keys, int wide, int ctas) {
   if (max_keys <= kChunkWholeKeys) return true;
   const int64_t units = batch * (int64_t)n_kv * (((int64_t)t_len * group + 128 * wide - 1) / (128 * wide));

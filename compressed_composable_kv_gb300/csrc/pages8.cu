@@ -23,6 +23,9 @@
 // for each token of each kv head (from L2).  1 x 4000 tokens 11.5 us (28 MB), 8
 // ragged sequences of up to 128 7.5 us, 16 x 1 4.9 us, which is a launch and four
 // dependent reads.
+//
+// In a chunk's call further CTAs of the append's launch rotate the queries (put_queries),
+// bound by their bytes: 4000 tokens of 32 heads 65 MB, of 8 kv heads' rows 29 MB more.
 #include "pages8.h"
 
 namespace c2kv {

@@ -102,7 +102,7 @@ struct PutParams {
   uint16_t* q16;
   float* q_scale;
   int32_t n_q, group;
-  int32_t z0;                    // first blockIdx.z: 0 K, 1 V, 2 + g the g-th query head of the group
+  int32_t z0;                    // first blockIdx.z: 0 K, 1 V, from 2 on the queries (a slice of the rows each)
   float scale_log2;
   int32_t row_at_length;         // token i's table row is rope_row + n_cached + i
   int32_t max_rows;              // a sequence that would get more is left out
