@@ -229,7 +229,8 @@ class PagedSequences:
     rows begin in rope_table, refs [n_pages] how many sequences hold each page.  A
     fork makes new tensors of them, so a graph is captured anew behind it; compact
     changes them in place.  Tokens are written to pages that `fork` has taken: its
-    `room` says how many may follow before the next one.
+    `room` says how many may follow before the next one.  A fork that finds too few free
+    pages, or a parent that is none, records C2KV_EDEVICE and leaves all places empty.
     """
 
     def __init__(self, geom, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
@@ -242,7 +243,7 @@ class PagedSequences:
         self.page_table = torch.full((1, -(-max_keys // self.page)), -1, dtype=torch.int32, device=dev)
         self.n_cached_dev = torch.full((1,), -1, dtype=torch.int32, device=dev)
         self.rope_start = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._chunk_ws: Optional[torch.Tensor] = None
+        self._chunk_ws: List[torch.Tensor] = []   # the last one serves; captured graphs may hold the others
         self._decode_ws: Optional[torch.Tensor] = None
         self._pages_change = True   # the last call wrote pages or lengths: what reads some early waits
 
@@ -258,7 +259,8 @@ class PagedSequences:
         negative: an empty place): more answers, beams moved or dropped, sequences
         ended.  Each gets room for `room` more tokens."""
         dev = self.page_table.device
-        with torch.cuda.stream(self._stream(stream)):
+        s = self._stream(stream)
+        with torch.cuda.stream(s):
             if not isinstance(parents, torch.Tensor):
                 parents = torch.tensor(list(parents), dtype=torch.int32).to(dev, non_blocking=True)
             n, width = parents.numel(), self.page_table.shape[1]
@@ -271,6 +273,10 @@ class PagedSequences:
             lengths.fill_(-1)
             B.c2kv_pages8_fork(self.geom, *self._pool(), self.refs, self.page_table, self.n_cached_dev, parents, room,
                                self.refs, table, lengths, ws, stream)
+            if s is not None and not torch.cuda.is_current_stream_capturing():
+                # these are let go while the call may still be to run, and may be of other streams
+                for x in (self.page_table, self.n_cached_dev, self.rope_start, parents):
+                    x.record_stream(s)
             self.rope_start = self.rope_start[parents.clamp(min=0, max=self.batch - 1).long()]
             self.page_table, self.n_cached_dev = table, lengths
         self._pages_change = True
@@ -290,10 +296,10 @@ class PagedSequences:
         tokens of a padded batch."""
         need = B.c2kv_attend_pages8_chunk_workspace_size(self.geom, self.batch, q.shape[1], self.max_keys)
         with torch.cuda.stream(self._stream(stream)):
-            if self._chunk_ws is None or self._chunk_ws.numel() < need:
-                self._chunk_ws = torch.empty(need, dtype=torch.uint8, device=self.refs.device)
+            if not self._chunk_ws or self._chunk_ws[-1].numel() < need:
+                self._chunk_ws.append(torch.empty(need, dtype=torch.uint8, device=self.refs.device))
         B.c2kv_attend_pages8_chunk(self.geom, layer, *self._pool(), self.page_table, self.n_cached_dev, self.max_keys, q,
-                                   k_new, v_new, self.rope_table, self.rope_start, out, self._chunk_ws, n_new, stream,
+                                   k_new, v_new, self.rope_table, self.rope_start, out, self._chunk_ws[-1], n_new, stream,
                                    B.C2KV_DECODE_ROW_AT_LENGTH)
         self._pages_change = True
 

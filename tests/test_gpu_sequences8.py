@@ -241,3 +241,64 @@ def test_a_pool_without_enough_pages_says_so(n):
         assert (seqs.n_cached_dev == -1).all() and (seqs.page_table == -1).all()
         assert all(torch.equal(a, b) for a, b in zip(before, (seqs.k8.view(torch.uint8), seqs.k_scale, seqs.refs)))
     w.sc.close()
+
+
+def test_fork_behind_a_busy_stream():
+    """What a fork lets go of stays until its stream has come to it."""
+    g = S.Geometry(2, 4, 2, 64, 1e4)
+    tables = []
+    for late in (False, True):
+        w = World(g, 16, spare=60)
+        seqs = w.rb.answers(2, room=3)
+        parents = torch.tensor([3, 0, -1, 2, 2], dtype=torch.int32, device="cuda")
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        shapes = [(x.shape, x.dtype) for x in (seqs.page_table, seqs.n_cached_dev, seqs.rope_start, parents)]
+        if late:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(200_000_000)
+            seqs.fork(parents, 20, side)
+            del parents
+            junk = [torch.full(s, -1, dtype=t, device="cuda") for s, t in shapes for _ in range(3)]
+        else:
+            seqs.fork(parents, 20)
+        torch.cuda.synchronize()
+        assert P.c2kv_device_error() == P.C2KV_OK
+        tables.append((seqs.page_table.clone(), seqs.n_cached_dev.clone(), seqs.rope_start.clone(), seqs.refs.clone()))
+        w.sc.close()
+    assert all(int((x != -1).sum()) == 0 for x in junk)
+    for a, b in zip(*tables):
+        assert torch.equal(a, b)
+
+
+def test_a_larger_chunk_between_capture_and_replay():
+    """A captured chunk keeps its workspace when a larger one is asked for."""
+    g = S.Geometry(2, 4, 2, 64, 1e4)
+    w = World(g, 16, spare=120, steps=120)   # max_keys is the request's rows and 120
+    seqs = w.rb.answers(2, room=100)
+
+    def args(t):
+        q = _dev(_values(w.rng, (4, t, 4, 64)))
+        k, v = (_dev(_values(w.rng, (4, t, 2, 64))) for _ in range(2))
+        return q, k, v, torch.zeros_like(q)
+
+    small, large = args(3), args(90)
+    seqs.chunk(0, *small)
+    torch.cuda.synchronize()
+    size = seqs._chunk_ws[-1].numel()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        seqs.chunk(0, *small)
+    seqs.chunk(0, *large)
+    assert seqs._chunk_ws[-1].numel() > size
+    seqs.chunk(0, *small)
+    torch.cuda.synchronize()
+    want = small[3].clone()
+    junk = [torch.full((size,), 0x5A, dtype=torch.uint8, device="cuda") for _ in range(3)]
+    small[3].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert P.c2kv_device_error() == P.C2KV_OK
+    assert all(bool((x == 0x5A).all()) for x in junk)
+    assert torch.equal(small[3], want)
+    w.sc.close()
