@@ -13,7 +13,7 @@
 // What bounds them: a copy of some MB the memory (32 layers, 4 sequences forked to 32:
 // 35.0 us, 6.8 TB/s read and written; 16 layers, 512 pages of 64 rows compacted: 88.3 us,
 // 6.0 TB/s), a smaller call the plan's chain of steps, each a trip to L2 and a barrier, and
-// the two launches (3 sequences forked to 7: 11.4 us; 97 pages compacted: 7.9 us).
+// the two launches (3 sequences forked to 7: 10.9 us; 97 pages compacted: 7.9 us).
 #include <algorithm>
 
 #include <cooperative_groups.h>
