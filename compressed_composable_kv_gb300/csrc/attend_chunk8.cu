@@ -41,8 +41,8 @@
 // launches, 3 to 4 us each, and the way through the first tile, 4 us.
 //
 // 32 query heads of 128 over 8 kv heads: 4 x 512 tokens over 32768 990 us (1.12 PFLOP/s),
-// 1 x 4000 over nothing 203 us, 16 x 5 over 1000 to 8000 67 us (2.1 TB/s), 1 x 64 over 8000
-// 34 us; 40 heads over 8, 8 x 128 over 7000 to 8000 111 us (0.55 PFLOP/s).
+// 1 x 4000 over nothing 195 us, 16 x 5 over 1000 to 8000 67 us (2.1 TB/s), 1 x 64 over 8000
+// 35 us; 40 heads over 8, 8 x 128 over 7000 to 8000 113 us (0.55 PFLOP/s).
 #include <float.h>
 
 #include <algorithm>

@@ -143,9 +143,10 @@ __device__ __noinline__ void put_queries(const PutParams& p, int b, int h, int s
 // D: head_dim.  APPEND: rows [n_cached, n_cached + new) from the new tokens,
 // K rotated; else rows [0, n_rows) from the bf16 caches.
 // CTAs per SM: append takes 11.5 us at 2 and 12.4 at 3 for 1 x 4000 tokens
-// (registers for the rows in flight); fill is fastest at 3.
-template <int D, bool APPEND>
-__global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 : 3) put_kernel(const __grid_constant__ PutParams p) {
+// (registers for the rows in flight); fill is fastest at 3, and so is an append with
+// queries (Q), most of whose CTAs have those: a chunk of 1 x 4000 203 us at 2, 195 at 3.
+template <int D, bool APPEND, bool Q = false>
+__global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND && !Q ? 2 : 3) put_kernel(const __grid_constant__ PutParams p) {
   constexpr int CH = D / 16;              // items (16 elements) of a row
   constexpr int IT = D / 32;              // items of a lane
   __shared__ uint32_t warp_max[8];
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   if (row0 >= end || count == 0) return;
   const int page = p.pool.page;
   const int wrow = row0 + warp * PUT_WARP_ROWS;
-  if (APPEND && (int)blockIdx.z + p.z0 >= 2) {
+  if (Q && (int)blockIdx.z + p.z0 >= 2) {
     put_queries<D>(p, b, h, (int)blockIdx.z + p.z0 - 2, first, wrow, end, rr);
     return;
   }
@@ -373,7 +374,7 @@ __global__ void __launch_bounds__(PUT_MAX_ROWS / PUT_WARP_ROWS * 32, APPEND ? 2 
   if (warp == w0 && lane == 0) *scale = pow2_float(e);
 }
 
-template <int D, bool APPEND>
+template <int D, bool APPEND, bool Q = false>
 cudaError_t launch_put(const PutParams& p, dim3 grid, int threads, cudaStream_t st) {
   static KernelSetup s;
   const int dev = setup_device();
@@ -381,7 +382,7 @@ cudaError_t launch_put(const PutParams& p, dim3 grid, int threads, cudaStream_t 
   if (APPEND) {
     std::lock_guard<std::mutex> lk(s.mu);
     if (s.state[dev] == 0) {
-      const cudaError_t e = cudaFuncSetAttribute(put_kernel<D, APPEND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+      const cudaError_t e = cudaFuncSetAttribute(put_kernel<D, APPEND, Q>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                  PUT_MAX_ROWS / PUT_WARP_ROWS * 8192);
       if (e != cudaSuccess) cudaGetLastError();
       s.state[dev] = e == cudaSuccess ? 1 : -(int)e;
@@ -398,7 +399,7 @@ cudaError_t launch_put(const PutParams& p, dim3 grid, int threads, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, put_kernel<D, APPEND>, p);
+  return cudaLaunchKernelEx(&cfg, put_kernel<D, APPEND, Q>, p);
 }
 
 // Rows of a CTA for this page size.
@@ -416,6 +417,8 @@ cudaError_t launch_pages8_append(const PutParams& p, int head_dim, cudaStream_t 
   // rows [n, n + t_len) meet at most this many CTAs' rows
   const int rows = put_rows(p), threads = rows / PUT_WARP_ROWS * 32;
   const dim3 grid((p.t_len + 2 * rows - 2) / rows, p.batch * p.pool.n_kv, (p.q ? 2 + PUT_SLICES : 2) - p.z0);
+  if (p.q)
+    return head_dim == 128 ? launch_put<128, true, true>(p, grid, threads, st) : launch_put<64, true, true>(p, grid, threads, st);
   return head_dim == 128 ? launch_put<128, true>(p, grid, threads, st) : launch_put<64, true>(p, grid, threads, st);
 }
 
