@@ -100,7 +100,6 @@ struct ChunkMap {
   int32_t per[kMaxPagedSeqs];         // places of one kv head of it
   int32_t n[kMaxPagedSeqs];           // rows held before the chunk
   int32_t count[kMaxPagedSeqs];       // new tokens
-  int32_t rope[kMaxPagedSeqs];
   int32_t tiles;                      // of the launch
 };
 
@@ -492,7 +491,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       M.per[b] = per;
       M.n[b] = n;
       M.count[b] = count;
-      M.rope[b] = (int32_t)rr;   // of an empty or bad place: not used
       at += __shfl_sync(0xffffffffu, incl, 31);
       tiles += __reduce_add_sync(0xffffffffu, all);
     }

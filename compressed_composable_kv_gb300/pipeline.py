@@ -204,9 +204,9 @@ class RequestBatch:
             raise ValueError("n must be at least 1")
         dev = self.page_table.device
         rows = [s + self.q_len for s in self.n_slots]
-        held = torch.tensor([-(-r // self.page8) for r in rows], device=dev)[:, None]
         s = torch.cuda.current_stream(dev) if stream is None and dev.type == "cuda" else stream
         with torch.cuda.stream(s):
+            held = torch.tensor([-(-r // self.page8) for r in rows], device=dev)[:, None]
             width = self.page_table.shape[1]
             mine = torch.arange(width, device=dev) < held
             seqs = PagedSequences(self.geom, self.k8, self.v8, self.k_scale, self.v_scale, self.rope_table,
