@@ -40,7 +40,7 @@
 // codes, of which none can be left out for more than 7 %.  Few rows over short caches: the
 // launches, 3 to 4 us each, and the way through the first tile, 4 us.
 //
-// 32 query heads of 128 over 8 kv heads: 4 x 512 tokens over 32768 990 us (1.12 PFLOP/s),
+// 32 query heads of 128 over 8 kv heads: 4 x 512 tokens over 32768 980 us (1.13 PFLOP/s),
 // 1 x 4000 over nothing 195 us, 16 x 5 over 1000 to 8000 67 us (2.1 TB/s), 1 x 64 over 8000
 // 35 us; 40 heads over 8, 8 x 128 over 7000 to 8000 113 us (0.55 PFLOP/s).
 #include <float.h>
@@ -662,8 +662,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         for (int t = t0 - step; ok && t < n; t += step) {
           const int jt = j + t, tn = t + step, jn = j + tn;
           const uint64_t v = v_desc + (uint32_t)(jt & 1) * (C::TILE >> 4), k = k_desc + (uint32_t)(jn & 1) * (C::TILE >> 4);
-          if (tn < n) ok = wait(&k_full[jn & 1], (jn >> 1) & 1);
-          if (ok && t >= t0) ok = wait(&v_full[jt & 1], (jt >> 1) & 1);
+          if (t >= t0) ok = wait(&v_full[jt & 1], (jt >> 1) & 1);
 #pragma unroll 1
           for (int part = 0; ok && part < 2; ++part) {
             const uint32_t s_col = tmem + m * 128 + part * 64;
@@ -678,6 +677,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               // the next tile of this half takes the same stage
               if (W == 1 && part == 1) mma_commit(&v_empty[jt & 1]);
             }
+            // (the products above do not wait for the next keys)
+            if (tn < n && part == 0) ok = wait(&k_full[jn & 1], (jn >> 1) & 1);
+            if (!ok) break;
             if (tn < n) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
