@@ -410,6 +410,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   volatile uint32_t* tmem_slot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 8);
   volatile int* nan_seg = reinterpret_cast<volatile int*>(smem + C::OFF_MISC + 16);   // [4]: segment + 1 with NaN values some rows do not see
+  // [2]: flags and tiles of a segment, for the MMA issuers: with q_full, and there until
+  // both have arrived at q_free (a tile's slot may be filled anew before an issuer that
+  // has none of its scores to make comes to it)
+  volatile uint2* seg_word = reinterpret_cast<volatile uint2*>(smem + C::OFF_MISC + 32);
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int cta = blockIdx.x, G = p.group;
@@ -647,14 +651,12 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       bool ok = true;
       int np = 0;   // tiles whose weights were seen
       for (int j = 0, seg = 0; ok; ++seg) {
-        ok = wait(&seg_full[j % kSlots], (j / kSlots) & 1);
-        if (!ok) break;
-        const TileSlot& s = slots[j % kSlots];
-        const uint32_t flags = s.flags;
-        if (flags & kNone) break;
-        const int n = s.n, wide = W == 2 && (flags & kWide) ? 1 : 0, step = 2 - wide, t0 = wide ? 0 : m;
-        const uint64_t q = q_desc + (uint32_t)(wide ? m : 0) * (C::TILE >> 4);
         ok = wait(&q_full[0], seg & 1) && wait(&q_full[1], seg & 1);
+        if (!ok) break;
+        const uint32_t flags = seg_word[seg & 1].x;
+        if (flags & kNone) break;
+        const int n = (int)seg_word[seg & 1].y, wide = W == 2 && (flags & kWide) ? 1 : 0, step = 2 - wide, t0 = wide ? 0 : m;
+        const uint64_t q = q_desc + (uint32_t)(wide ? m : 0) * (C::TILE >> 4);
         if (t0 >= n) mbar_arrive(q_free);
         // P V of a part of tile t, then the same part's scores of the next, which take
         // the weights' place
@@ -834,19 +836,22 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       return true;
     };
     // ... and are there.
-    auto queries_here = [&]() {
+    auto queries_here = [&](int of) {   // `of`: the segment
       asm volatile("cp.async.wait_all;" ::: "memory");
       fence_proxy_async();
       __syncwarp();
+      if (tid == 0) {
+        seg_word[of & 1].x = sg.flags;
+        seg_word[of & 1].y = (uint32_t)sg.tiles;
+      }
       if (lane == 0) mbar_arrive(&q_full[m]);
     };
+    sg.flags = 0;
+    sg.tiles = 0;
     ok = take();
-    if (ok && !(sg.flags & kNone)) {
-      ok = ask_queries(0);
-      if (ok) queries_here();
-    } else {
-      ok = false;
-    }
+    if (ok && !(sg.flags & kNone)) ok = ask_queries(0);
+    if (ok) queries_here(0);
+    if (sg.flags & kNone) ok = false;
     if (ok && p.inject_timeout && (cta & 1) == 0) {
       ok = mbar_wait(never, 0, kInjectWaitCycles);
       *abort_flag = 1;
@@ -1031,7 +1036,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
       }
       // The next scores are made meanwhile; but not while the first half still reads the
       // second half's sums.
-      if (!ends && !two) queries_here();
+      if (!ends && !two) queries_here(seg + 1);
       if (warp_live && (wide || m == 0)) {
         tc_fence_after();
         const bool whole = was.flags & kWhole;
@@ -1116,7 +1121,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         tc_fence_before();
       }
       if (ends) break;
-      if (two) queries_here();
+      if (two) queries_here(seg + 1);
     }
   }
   grid_wait();   // the launch completes only behind the append
