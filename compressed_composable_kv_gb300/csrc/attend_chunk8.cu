@@ -17,7 +17,7 @@
 // The places of all units (their tiles, and some for the end of each) are laid end to
 // end, from the device-side lengths, and cut into one even range per CTA (one to an SM).
 // A unit that one CTA holds whole is written at once; else its CTAs write partial
-// (m, l, O) and merge_kernel joins them in the order of the keys.
+// (m, l, O / l) and merge_kernel joins them in the order of the keys.
 //
 // A call is two launches, or three: the append, whose further CTAs rotate the queries
 // into the output buffer (fp16, pages8.cu), this kernel, and the join where units are
@@ -1007,7 +1007,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         if (W == 2 && lane == 0) mbar_arrive_n(&v_empty[(j - 1 - (wide || ((tiles - 1) & 1) == m ? 0 : 1)) & 1], step);
       }
       const bool two = !wide && tiles > 1;   // a narrow unit's halves are added up by the first
-      float4 other = make_float4(-INFINITY, 0.f, 0.f, 0.f);   // m, l, 2^v_ref of the second half
+      float4 other = make_float4(-INFINITY, 0.f, (float)kNoScale, 0.f);   // m, l, v_ref of the second half
       float4* hand_o = reinterpret_cast<float4*>(smem + C::OFF_HO);
       if (two && m == 1) {
         // its sums are complete; the first half cannot read tensor memory of other lanes
@@ -1025,7 +1025,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           }
         }
         tc_fence_before();
-        if (live) hand[row] = make_float4(m_run, l_run, v_ref == kNoScale ? 0.f : pow2_float(v_ref), 0.f);
+        if (live) hand[row] = make_float4(m_run, l_run, (float)v_ref, 0.f);
         __syncwarp();
         if (lane == 0) mbar_arrive(handed);
       }
@@ -1042,20 +1042,26 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         const bool whole = was.flags & kWhole;
         const int n = M.n[was.b];
         const bool nan = nan_seg[seg & 3] == seg + 1;
-        float f = v_ref == kNoScale ? 0.f : pow2_float(v_ref), f1 = 0.f;
+        // A part's O is divided by its own sum, too: what is stored is a mean of values, and
+        // in range as they are.  Its unit 2^v_ref is multiplied in where that stays in range.
+        float f = 1.f, f1 = 0.f;
+        int unit = v_ref;
         if (two) {
           const float top = fmaxf(m_run, other.x), base = top == -INFINITY ? 0.f : top;
           const float w0 = ex2_approx(m_run - base), w1 = ex2_approx(other.x - base);
-          f *= w0;
-          f1 = other.z * w1;
+          const int v_other = (int)other.z;
+          unit = max(v_ref, v_other);
+          f = w0 * pow2_float(max(v_ref - unit, -126));
+          f1 = w1 * pow2_float(max(v_other - unit, -126));
           l_run = l_run * w0 + other.y * w1;
           m_run = top;
         }
-        if (whole) {
-          const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
-          f *= inv;
-          f1 *= inv;
-        }
+        if (unit == kNoScale) unit = 0;
+        const int near = min(max(unit, -64), 64);
+        const float inv = l_run == 0.f ? 0.f : pow2_float(near) / l_run, rest = pow2_float(unit - near);
+        const bool far = __any_sync(0xffffffffu, unit != near);
+        f *= inv;
+        f1 *= inv;
         const int t_of = (was.first + row) / G;
         const uint32_t to = live ? (uint32_t)((was.b * p.t_len + t_of) * p.n_q + was.h * G + was.first + row - t_of * G) : ~0u;   // row of out
         const int slot = 2 * cta + (t0 == 0 ? 1 : 0);   // of a unit's first part: see the merge
@@ -1083,6 +1089,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               o[i + 2] = fmaf(y.z, f1, o[i + 2]);
               o[i + 3] = fmaf(y.w, f1, o[i + 3]);
             }
+          }
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= rest;
           }
           if (live && nan) {   // values that are not numbers, for the rows that see them
             const int end = min(lim, (t0 + tiles) * CK_KEYS);
@@ -1174,22 +1184,23 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(const __grid_constant
   const float base = mx == -INFINITY ? 0.f : mx;
   float l = 0.f;
   for (int k = warp; k < parts; k += 8) {
-    const float w = ex2_approx(wts[k][lane] - base);
+    const float w = ex2_approx(wts[k][lane] - base) * (live ? p.part_ml[slot(k) * p.part_rows + row].y : 0.f);
     wts[k][lane] = w;
-    l = fmaf(w, live ? p.part_ml[slot(k) * p.part_rows + row].y : 0.f, l);
+    l += w;
   }
   red[warp][lane] = l;
   __syncthreads();
   l = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) l += red[i][lane];
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 1
   for (int k0 = 0; k0 < parts; k0 += AHEAD) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       if (k0 + i >= parts) break;
-      const float w = wts[k0 + i][lane];
+      const float w = wts[k0 + i][lane] * inv;
       acc.x = fmaf(w, v[i].x, acc.x);
       acc.y = fmaf(w, v[i].y, acc.y);
       acc.z = fmaf(w, v[i].z, acc.z);
@@ -1200,9 +1211,8 @@ __global__ void __launch_bounds__(MG_THREADS) merge_kernel(const __grid_constant
       if (k0 + AHEAD + i < parts) v[i] = part(k0 + AHEAD + i);
   }
   if (!live) return;
-  const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2* dst = reinterpret_cast<uint2*>(p.out + (((size_t)b * p.t_len + rq / G) * p.n_q + h * G + rq % G) * D) + c4;
-  *dst = make_uint2(pack2(acc.x * inv, acc.y * inv), pack2(acc.z * inv, acc.w * inv));
+  *dst = make_uint2(pack2(acc.x, acc.y), pack2(acc.z, acc.w));
 }
 
 template <int D, int W>

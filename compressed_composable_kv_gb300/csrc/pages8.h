@@ -121,7 +121,7 @@ struct ChunkParams {
   unsigned* err;
   int32_t* desc;                 // [CTAs][8] the unit that begins in a CTA and goes on in others: rows (0: none), b, h, first row, CTAs
   float2* part_ml;               // [2 * CTAs][part_rows] (m, l) of shared units
-  float4* part_o;                // [2 * CTAs][d / 4][part_rows] their O
+  float4* part_o;                // [2 * CTAs][d / 4][part_rows] their O / l
   int32_t batch, t_len, n_q, group, max_pages, max_keys, table_rows, row_at_length, part_rows, inject_timeout;
   int32_t wide;                  // a unit has 128 * wide rows
   int32_t whole;                 // no unit is cut, there is nothing to join

@@ -1,9 +1,13 @@
 """Chunk attention over the 8-bit pages at the ends of its range, against the fp64
-oracle (oracle/pages8_oracle.py): units of one tile, many to a CTA."""
+oracle (oracle/pages8_oracle.py): units of one tile, many to a CTA; pages whose scales
+are far apart."""
+import numpy as np
 import pytest
+import torch
 
+import oracle.pages8_oracle as Q
 from test_gpu_chunk8 import Chunk
-from test_gpu_pages8 import _geom, _ok
+from test_gpu_pages8 import _f64, _geom, _ok, _rotate, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -22,3 +26,72 @@ def test_many_units_of_few_tiles(t_len, held):
     _ok()
     c.put_new()
     c.check("few tiles", rows=[0, 1, t_len - 1])
+
+
+# ------------------------------------------------------------------ scales far apart
+
+def _bits(x):
+    return torch.from_numpy(np.asarray(x)).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
+
+
+def _hold(c, b, keys, values):
+    """The held rows of sequence b: [kv head][row][d]."""
+    for kv, x in ((0, keys), (1, values)):
+        c.pool.put(0, b, 0, kv, x)
+    c.pool.upload()
+
+
+def _normal_rows(c, n):
+    shape = (c.g.n_kv_heads, n, c.g.head_dim)
+    return _f64(_values(c.pool.rng, shape)), _f64(_values(c.pool.rng, shape))
+
+
+def _check_by_column(c, what):
+    """Each element of the answer against what the keys' own weights and that column's own
+    values may move it by: a logit is off by ds_j = (2^-11 + 2^-18) sum_i |q_i K_ji| / sqrt(d)
+    (queries in fp16, sums in fp32), so numerator and denominator by ds_j p_j; a weight is
+    rounded to fp16, 2^-11 of itself or, below fp16's normal range, 2^-25 of the largest
+    but no more than itself; sums in fp32 add 2^-15; then the rounding to bf16, 2^-8 or
+    2^-134.  1.1: products of these."""
+    c.pool.check(what)
+    g, pl = c.g, c.pool
+    out = c.out.float().cpu().numpy().astype(np.float64)
+    worst = 0.0
+    for b, (h, n) in enumerate(zip(c.held, c.new)):
+        k, v = (Q.held(pl.codes[x][0], pl.scales[x][0], c.page, pl.table[b], h + n) for x in (0, 1))
+        q = _rotate(g, _f64(c.q[b, :n]), c.pos[b, :n])
+        for i in range(n):
+            for head in range(g.n_q_heads):
+                kv = head // (g.n_q_heads // g.n_kv_heads)
+                K, V = k[kv, :h + i + 1], v[kv, :h + i + 1]
+                s = K @ q[i, head] / np.sqrt(g.head_dim)
+                p = np.exp(s - s.max())
+                top = 1.0 / p.sum()
+                p = p * top
+                ds = (2.0 ** -11 + 2.0 ** -18) * (np.abs(K) @ np.abs(q[i, head])) / np.sqrt(g.head_dim)
+                ds = np.where(p > 0, ds, 0.0)
+                ref = p @ V
+                moved = p * (ds + p @ ds + 2.0 ** -11 + 2.0 ** -15) + np.minimum(2.0 ** -25 * top, p)
+                tol = 2.0 ** -8 * np.abs(ref) + 2.0 ** -134 + 1.1 * moved @ np.abs(V)
+                err = np.abs(out[b, i, head] - ref)
+                at = int(np.argmax(np.where(err <= tol, 0.0, err)))
+                assert (err <= tol).all(), f"{what}: sequence {b} token {i} head {head} column {at}: {out[b, i, head, at]:.6e}, not {ref[at]:.6e} ({err[at] / tol[at]:.1f} of the bar)"
+                worst = max(worst, (err / tol).max())
+    return worst
+
+
+@pytest.mark.parametrize("size", [2.0 ** 124, 2.0 ** -112])
+@pytest.mark.parametrize("held,new", [([300, 40], [20, 20]), ([6000, 3], [3, 40]), ([3000], [300])])
+def test_values_at_the_ends_of_the_range(size, held, new):
+    """Values near the largest and the smallest that a page holds, units cut and whole: the
+    answer is a mean of them, and so in range, at every step on the way to it."""
+    g = _geom(128, 4, 2)
+    c = Chunk(g, 64, held, new, t_len=max(new), seed=31)
+    for b, n in enumerate(held):
+        k, v = _normal_rows(c, n)
+        _hold(c, b, k, np.clip(v, -2.5, 2.5) * size)
+        c.v[b] = _bits(np.clip(_f64(c.v[b]), -2.5, 2.5) * size)
+    c.call()
+    _ok()
+    c.put_new()
+    _check_by_column(c, "ends")
