@@ -70,6 +70,9 @@ constexpr int kChunkWidePlaces = 3, kChunkNarrowPlaces = 2;
 constexpr int kChunkFewTiles = 16; // see chunk_wide
 constexpr int kChunkWholeKeys = 512, kChunkMergeTiles = 4;  // see chunk_whole
 constexpr int kNoScale = -1000;    // exponent of a tile without a page
+// A code times 2^-15 is an fp16 number, times less it may not be (codes are multiples of
+// 2^-9, fp16 numbers of 2^-24).
+constexpr int kMostBelow = 15;
 constexpr float kRescaleLog2 = 8.f;   // a row's maximum may lag behind by this (weights up to 2^15, sums exact)
 constexpr float kWeightLog2 = 7.f;
 
@@ -81,7 +84,9 @@ struct TileSlot {
   uint32_t vf[8];
   float k_scale;       // the tile's
   int32_t v_exp;
-  uint32_t bad;        // bit g: the rows of grp[g] take no part
+  uint32_t bad;        // bit g: the rows of grp[g] take no part, bit 8 + g: their keys' codes
+                       // are held as they are, their scores times k_by[g]
+  float k_by[8];
   int32_t rows;        // keys of the tile that any row of the unit sees
   int32_t diag;        // keys below this are seen by every row
   // from here on known (seg_full) before the rest (slot_full)
@@ -616,11 +621,14 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           vm = max(vm, __shfl_xor_sync(0xffffffffu, vm, off));
           bad |= __shfl_xor_sync(0xffffffffu, bad, off);
         }
+        const bool k_far = cur.id >= 0 && ke - km < -kMostBelow;
+        bad |= (__ballot_sync(0xffffffffu, k_far) >> (lane & 24) & 0xFFu) << 8;
         if (cur.on) {
           s.grp[g] = cur.id >= 0 ? (int32_t)(row >> 4) : -1;
-          const float kf = pow2_float(max(ke - km, -126)), vf = pow2_float(max(ve - vm, -126));
+          const float kf = k_far ? 1.f : pow2_float(max(ke - km, -126)), vf = pow2_float(max(ve - vm, -126));
           s.kf[g] = f16x2(kf, kf);
           s.vf[g] = f16x2(vf, vf);
+          s.k_by[g] = k_far ? pow2_float(max(ke - km, -126)) : 1.f;
           if (g == 0) {
             s.k_scale = km == kNoScale ? 1.f : pow2_float(km);
             s.v_exp = vm;
@@ -916,6 +924,10 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             }
             tmem_wait_ld();
             if (nvis < CK_KEYS || bad) {
+              if (bad >> 8) {   // pages whose K scales are far below the tile's (seldom)
+#pragma unroll
+                for (int i = 0; i < 64; ++i) x[i / 32][i % 32] *= slots[j % kSlots].k_by[4 * part + i / 16];
+              }
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 const int i1 = 64 * part + 32 * k, left = nvis - i1;

@@ -30,6 +30,19 @@ def test_many_units_of_few_tiles(t_len, held):
 
 # ------------------------------------------------------------------ scales far apart
 
+FIRST = 8.0   # element 0 of every rotated query
+
+
+def _aimed(g, page, held, new, seed):
+    """A chunk whose queries, once rotated, have FIRST in element 0."""
+    c = Chunk(g, page, held, new, seed=seed)
+    for b in range(len(held)):
+        turned = c.pool.rng.standard_normal((c.t_len, g.n_q_heads, g.head_dim))
+        turned[..., 0] = FIRST
+        c.q[b] = _bits(_rotate(g, turned, -c.pos[b]))
+    return c
+
+
 def _bits(x):
     return torch.from_numpy(np.asarray(x)).to(torch.bfloat16).view(torch.int16).numpy().view(np.uint16)
 
@@ -78,6 +91,31 @@ def _check_by_column(c, what):
                 assert (err <= tol).all(), f"{what}: sequence {b} token {i} head {head} column {at}: {out[b, i, head, at]:.6e}, not {ref[at]:.6e} ({err[at] / tol[at]:.1f} of the bar)"
                 worst = max(worst, (err / tol).max())
     return worst
+
+
+SPREADS = [(d, group, page, t, far) for d, group, t in ((128, 4, 20), (64, 2, 70), (128, 5, 60)) for page in (16, 128) for far in (6, 14, 20, 26, 33, 60, 110)]
+
+
+@pytest.mark.parametrize("d,group,page,t,far", SPREADS)
+def test_large_keys_that_no_query_looks_at(d, group, page, t, far):
+    """A key of 2^far that every query turns away from: logits of rows on neighbouring pages
+    are as exact as ever."""
+    if far > 60:   # the logit itself stays in fp32's range
+        far = 80
+    g = _geom(d, group, 2)
+    held = [129, 600]
+    c = _aimed(g, page, held, [t] * 2, seed=far + 2)
+    for b, n in enumerate(held):
+        k, v = _normal_rows(c, n)
+        k[:, page:, 1] *= 4.0
+        for first in (0, 512)[:1 + b]:
+            k[:, first] = 0.0
+            k[:, first, 0] = -2.0 ** far
+        _hold(c, b, k, v)
+    c.call()
+    _ok()
+    c.put_new()
+    _check_by_column(c, f"2^{far}")
 
 
 @pytest.mark.parametrize("size", [2.0 ** 124, 2.0 ** -112])
