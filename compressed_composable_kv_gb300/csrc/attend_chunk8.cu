@@ -8,11 +8,11 @@
 // number, so a tile's codes are brought to fp16 once for all rows of the unit, and both
 // products run as kind::f16 (fp32 accumulators): the keys and values lose
 // nothing; a query row is held in fp16 times a power of two of its own, 2^-11 of
-// each element, and so is a weight (2^7 exp(s - m), so that weights down to 2^-21
-// of the largest keep their 11 bits), which is well below what the bf16 output
-// itself rounds away.  Pages of one tile with different scales meet at the largest
-// of them by an exact multiplication in fp16; the tile's K scale multiplies the
-// scores, its V scale, over the largest so far, the weights.
+// each element, and so is a weight (2^7 exp(s - m), so that weights down to 2^-15
+// of the largest keep their 11 bits; the bf16 output itself rounds away 2^-8).  Pages
+// of one tile with different scales meet at the largest of them by an exact multiplication
+// in fp16; the tile's K scale multiplies the scores, its V scale the weights, over a unit that
+// each row of O has for itself.
 //
 // The places of all units (their tiles, and some for the end of each) are laid end to
 // end, from the device-side lengths, and cut into one even range per CTA (one to an SM).
@@ -75,6 +75,10 @@ constexpr int kNoScale = -1000;    // exponent of a tile without a page
 constexpr int kMostBelow = 15;
 constexpr float kRescaleLog2 = 8.f;   // a row's maximum may lag behind by this (weights up to 2^15, sums exact)
 constexpr float kWeightLog2 = 7.f;
+// How far a tile's V scale may be below the unit of a row's O before the unit is brought
+// down to it: weights below 2^-21 of the row's largest lose bits, with this 2^-15.
+constexpr int kUnitAbove = 6;
+constexpr int kMostLog2 = 120;        // O's largest element stays below 2^this when its unit is brought down
 
 // What warp 16 finds out about a tile, and the segment that it belongs to.
 enum : uint32_t { kWhole = 2, kEnd = 4, kWide = 8, kNone = 16, kFresh = 32 };
@@ -387,6 +391,34 @@ __device__ __forceinline__ void transpose4(uint4 (&a)[4]) {
   swap(a[2], a[3], b0, 1);
   swap(a[0], a[2], b1, 2);
   swap(a[1], a[3], b1, 2);
+}
+
+// O (D columns of a row in each lane of the warp, all of it there) to a unit 2^-down of its
+// present one, or as far in that direction as keeps it in range.  Returns how far.
+template <int D>
+__device__ __forceinline__ int lower_unit(uint32_t o_at, int down) {
+  float most = 0.f;
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 16) {
+    float o[16];
+    tmem_ld_cols<16>(o_at + c0, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(o[i]));
+  }
+  if (most > 0.f) down = min(down, max(kMostLog2 - exponent_of_scale(most), 0));
+  const float by = pow2_float(min(down, 120)), more = pow2_float(down - min(down, 120));
+#pragma unroll 1
+  for (int c0 = 0; c0 < D; c0 += 16) {
+    float o[16];
+    tmem_ld_cols<16>(o_at + c0, o);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = o[i] * by * more;
+    tmem_st_cols16(o_at + c0, o);
+  }
+  tmem_wait_st();
+  return down;
 }
 
 // W: units of 128 W rows.
@@ -883,9 +915,9 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           if (lane == 0) mbar_arrive(&slot_empty[j % kSlots]);
           continue;
         }
-        float sc = 0.f, off = 0.f, v_inv = 1.f;
+        float sc = 0.f;
         uint32_t bad = 0;
-        int nvis = 0;
+        int nvis = 0, v_by = 0;   // 2^v_by: the tile's V scale over the unit of the row's O
 #pragma unroll 1
         for (int part = 0; part < 2; ++part) {
           ok = __all_sync(0xffffffffu, ck_wait(&s_full[2 * m + part], ns & 1, abort_flag, p.err));
@@ -902,26 +934,33 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             // behind (seldom), the sum and O are brought down.  The weights take the
             // place of the scores.  (The loop is rolled: unrolled code did not stay in
             // the instruction cache.)
-            float x[2][32];
-            tmem_ld32(s_at + part * 64, x[0]);
-            tmem_ld32(s_at + part * 64 + 32, x[1]);
-            float alpha = 1.f;   // what O is multiplied by
             if (part == 0) {
               const TileSlot& ts = slots[j % kSlots];
               nvis = live ? lim - (t0 + t) * CK_KEYS : 0;
               sc = qs * ts.k_scale;   // in range, so that a masked score stays -inf; NaN stays
               sc = sc < FLT_MIN ? FLT_MIN : sc > FLT_MAX ? FLT_MAX : sc;
               bad = ts.bad;
+              // The weights hold the tile's V scale over 2^v_ref, the unit of the row's O.  Where
+              // the scale is far below it, O is brought to a smaller unit first (as far as
+              // its largest element stays in range), so that these weights keep their bits; where it
+              // is above, the unit is raised below, by as much as the row's weights need.  So a large
+              // scale costs a row nothing that gives its page no weight.
               const int v_exp = ts.v_exp;
-              if (v_exp > v_ref) {   // the same in every row
-                if (v_ref != kNoScale) alpha = pow2_float(max(v_ref - v_exp, -126));
-                v_ref = v_exp;
+              if (v_ref == kNoScale) v_ref = v_exp;
+              v_by = v_exp == kNoScale ? 0 : v_exp - v_ref;
+              if (__any_sync(0xffffffffu, v_by < -kUnitAbove)) {
+                ok = __all_sync(0xffffffffu, ck_wait(&s_full[2 * m + 1], ns & 1, abort_flag, p.err));   // O is there
+                if (!ok) break;
+                tc_fence_after();
+                const int down = lower_unit<D>(o_at, v_by < -kUnitAbove ? -v_by : 0);
+                v_ref -= down;
+                v_by += down;
               }
-              // the tile's V scale over the largest so far goes into the weights' exponent
-              const int v_by = v_exp == kNoScale ? 0 : max(v_exp - v_ref, -60);
-              off = kWeightLog2 + (float)v_by;
-              v_inv = pow2_float(-v_by);
             }
+            float x[2][32];
+            tmem_ld32(s_at + part * 64, x[0]);
+            tmem_ld32(s_at + part * 64 + 32, x[1]);
+            float alpha = 1.f;   // what O is multiplied by
             tmem_wait_ld();
             if (nvis < CK_KEYS || bad) {
               if (bad >> 8) {   // pages whose K scales are far below the tile's (seldom)
@@ -945,7 +984,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             const float2 sc2 = make_float2(sc, sc);
 #pragma unroll 1
             for (;;) {
-              const float mu = off - (m_run == -INFINITY ? 0.f : m_run);
+              const float mu = kWeightLog2 + (float)max(v_by, -60) - (m_run == -INFINITY ? 0.f : m_run);
               const float2 mu2 = make_float2(mu, mu);
               float tops[4];
 #pragma unroll
@@ -964,13 +1003,22 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
                 w[i / 2] = __uint_as_float(f16x2(e.x, e.y));
               }
               const float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
-              const bool up = top != -INFINITY && top * sc > m_run + kRescaleLog2;
+              // (a weight is at most 2^(kWeightLog2 + kRescaleLog2), with the V scale in it, too)
+              const bool up = top != -INFINITY && top * sc > m_run + (kRescaleLog2 - (float)max(v_by, 0));
               if (!__any_sync(0xffffffffu, up)) break;
               if (up) {
-                const float by = ex2_approx(m_run - top * sc);   // 0 for the first scores of a row
-                m_run = top * sc;
-                alpha *= by;
-                l_run *= by;
+                if (top * sc > m_run + kRescaleLog2) {
+                  const float by = ex2_approx(m_run - top * sc);   // 0 for the first scores of a row
+                  m_run = top * sc;
+                  alpha *= by;
+                  l_run *= by;
+                }
+                const int room = (int)fmaxf(floorf(m_run - top * sc), 0.f);   // NaN: 0
+                if (v_by > room) {
+                  v_ref += v_by - room;
+                  alpha *= v_by - room > 126 ? 0.f : pow2_float(room - v_by);
+                  v_by = room;
+                }
               }
             }
             if ((t >= step || part == 1) && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -990,7 +1038,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             }
             tmem_st32(s_at + part * 64, w);
             const float2 l2 = add2(add2(l4[0], l4[1]), add2(l4[2], l4[3]));
-            l_run = fmaf(l2.x + l2.y, v_inv, l_run);
+            l_run = fmaf(l2.x + l2.y, pow2_float(min(max(-v_by, -126), 60)), l_run);
             tmem_wait_st();
           }
           tc_fence_before();

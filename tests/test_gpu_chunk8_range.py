@@ -96,6 +96,46 @@ def _check_by_column(c, what):
 SPREADS = [(d, group, page, t, far) for d, group, t in ((128, 4, 20), (64, 2, 70), (128, 5, 60)) for page in (16, 128) for far in (6, 14, 20, 26, 33, 60, 110)]
 
 
+@pytest.mark.parametrize("d,group,page,t,far", [s for s in SPREADS if s[2] == 128])
+def test_large_values_that_no_query_looks_at(d, group, page, t, far):
+    """Pages whose values are 2^far of the others', and whose keys no query looks at, cost the
+    other rows' answer nothing, before them, behind them or among 128 neighbouring rows."""
+    g = _geom(d, group, 2)
+    held = [129, 600, 1500]
+    c = _aimed(g, page, held, [t] * 3, seed=far)
+    for b, n in enumerate(held):
+        k, v = _normal_rows(c, n)
+        for first in (0, 256, 1152)[:1 + b]:
+            far_rows = slice(first, first + page)
+            k[:, far_rows] = 0.0
+            k[:, far_rows, 0] = -2.0 ** 13   # -5800 and less as a logit
+            v[:, far_rows] *= 2.0 ** far
+        _hold(c, b, k, v)
+    c.call()
+    _ok()
+    c.put_new()
+    _check_by_column(c, f"2^{far}")
+
+
+@pytest.mark.parametrize("d,group,page,t,far", [s for s in SPREADS if s[2] == 128])
+def test_large_values_in_one_column(d, group, page, t, far):
+    """Pages with 2^far in one column, which the queries look at as at any other: the other
+    columns keep what the other pages put there."""
+    g = _geom(d, group, 2)
+    held = [128, 600, 1500]
+    c = _aimed(g, page, held, [t] * 3, seed=far + 1)
+    for b, n in enumerate(held):
+        k, v = _normal_rows(c, n)
+        for first in (0, 256, 1152)[:1 + b]:
+            v[:, first:first + page] = 0.0
+            v[:, first:first + page, 7] = 2.0 ** far
+        _hold(c, b, k, v)
+    c.call()
+    _ok()
+    c.put_new()
+    _check_by_column(c, f"2^{far}")
+
+
 @pytest.mark.parametrize("d,group,page,t,far", SPREADS)
 def test_large_keys_that_no_query_looks_at(d, group, page, t, far):
     """A key of 2^far that every query turns away from: logits of rows on neighbouring pages
