@@ -11,8 +11,8 @@
 // each element, and so is a weight (2^7 exp(s - m), so that weights down to 2^-15
 // of the largest keep their 11 bits; the bf16 output itself rounds away 2^-8).  Pages
 // of one tile with different scales meet at the largest of them by an exact multiplication
-// in fp16; the tile's K scale multiplies the scores, its V scale the weights, over a unit that
-// each row of O has for itself.
+// in fp16 (apart_tile has what is too far apart for that); the tile's K scale multiplies the
+// scores, its V scale the weights, over a unit that each row of O has for itself.
 //
 // The places of all units (their tiles, and some for the end of each) are laid end to
 // end, from the device-side lengths, and cut into one even range per CTA (one to an SM).
@@ -89,8 +89,10 @@ struct TileSlot {
   float k_scale;       // the tile's
   int32_t v_exp;
   uint32_t bad;        // bit g: the rows of grp[g] take no part, bit 8 + g: their keys' codes
-                       // are held as they are, their scores times k_by[g]
+                       // are held as they are, their scores times k_by[g], bit 16 + g: their V
+                       // scale is further below v_exp than fp16 has room for (see apart_tile)
   float k_by[8];
+  int32_t v_of[8];     // exponents of the V scales
   int32_t rows;        // keys of the tile that any row of the unit sees
   int32_t diag;        // keys below this are seen by every row
   // from here on known (seg_full) before the rest (slot_full)
@@ -421,6 +423,182 @@ __device__ __forceinline__ int lower_unit(uint32_t o_at, int down) {
   return down;
 }
 
+// Rows 16 g, 16 g + 1, ... of the tile that any row of the unit sees, and where their values are.
+template <int D>
+__device__ __forceinline__ const uint4* values_of(const ChunkParams& p, const TileSlot& s, int g, int& rows) {
+  rows = s.grp[g] < 0 || (s.bad >> g & 1) ? 0 : min(max(s.rows - 16 * g, 0), 16);
+  return reinterpret_cast<const uint4*>(p.pool.codes[1] + (int64_t)s.grp[g] * (16 * D));
+}
+
+// Whether any value of these groups of 16 rows is not 0 (the same in every lane).
+template <int D>
+__device__ __forceinline__ bool any_value(const ChunkParams& p, const TileSlot& s, uint32_t groups) {
+  uint32_t some = 0;
+#pragma unroll 1
+  for (; groups; groups &= groups - 1) {
+    int rows;
+    const uint4* v = values_of<D>(p, s, __ffs(groups) - 1, rows);
+    for (int i = threadIdx.x & 31; i < rows * (D / 16); i += 32) {
+      const uint4 u = v[i];
+      some |= (u.x | u.y | u.z | u.w) & 0x7F7F7F7Fu;
+    }
+  }
+  return __any_sync(0xffffffffu, some != 0);
+}
+
+// Adds rows 16 g, ... of the tile to O in fp32, each lane for its own row of the unit.
+// The unit of O moves as before a tile's products.  s_at: the group's scores.
+template <int D>
+__device__ __forceinline__ void add_values(const ChunkParams& p, const TileSlot& s, int g, uint32_t s_at, uint32_t o_at,
+                                           int nvis, float sc, float m_run, int& v_ref) {
+  int rows;
+  const uint4* v = values_of<D>(p, s, g, rows);
+  if (rows == 0 || !any_value<D>(p, s, 1u << g)) return;
+  if (v_ref == kNoScale) v_ref = s.v_of[g];
+  int v_by = s.v_of[g] - v_ref;
+  sc *= s.bad >> (8 + g) & 1 ? s.k_by[g] : 1.f;
+  if (__any_sync(0xffffffffu, v_by < -60)) {
+    const int down = lower_unit<D>(o_at, v_by < -60 ? -v_by : 0);
+    v_ref -= down;
+    v_by += down;
+  }
+  float x[16], top = -INFINITY;
+  tmem_ld_cols<16>(s_at, x);
+  tmem_wait_ld();
+#pragma unroll
+  for (int i = 0; i < 16; ++i) top = fmaxf(top, 16 * g + i < nvis ? x[i] : -INFINITY);
+  const int room = (int)fmaxf(floorf(m_run - top * sc), 0.f), up = top != -INFINITY ? max(v_by - room, 0) : 0;
+  float by = up > 126 ? 0.f : pow2_float(-up);   // what O is multiplied by, once
+  v_ref += up;
+  v_by -= up;
+#pragma unroll 1
+  for (int i = 0; i < rows; i += 2) {
+    float e[2];
+    tmem_ld_cols<2>(s_at + i, e);
+    tmem_wait_ld();
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      e[k] = i + k < rows && 16 * g + i + k < nvis ? ex2_approx(fmaf(e[k], sc, kWeightLog2 + (float)v_by - m_run)) : 0.f;
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      float o[16];
+      tmem_ld_cols<16>(o_at + 16 * c, o);
+      tmem_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint4 u = i + k < rows ? v[(i + k) * (D / 16) + c] : make_uint4(0, 0, 0, 0);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+          // NaN that some rows of the unit do not see: see the epilogue
+          const uint32_t codes = w[n] & ~(16 * g + i + k < s.diag ? 0u : __vcmpeq4(w[n] & 0x7F7F7F7Fu, 0x7F7F7F7Fu));
+          const float2 a = e4m3x2_to_float2(codes & 0xFFFFu), b = e4m3x2_to_float2(codes >> 16);
+          float* to = o + 4 * n;
+          if (k == 0) to[0] *= by, to[1] *= by, to[2] *= by, to[3] *= by;
+          to[0] = fmaf(e[k], a.x, to[0]);
+          to[1] = fmaf(e[k], a.y, to[1]);
+          to[2] = fmaf(e[k], b.x, to[2]);
+          to[3] = fmaf(e[k], b.y, to[3]);
+        }
+      }
+      tmem_st_cols16(o_at + 16 * c, o);
+      tmem_wait_st();
+    }
+    by = 1.f;
+  }
+}
+
+// A tile some of whose pages have V scales more than 2^15 apart, which share no fp16 scale
+// that all fit: its values are added in fp32, page by page, and its weights are 0 for the
+// products that the issuer makes of them all the same (60 to 80 us a tile: right, not fast).
+// From the scores of its first part, which are there, to the end of its second.
+struct RowSums {
+  float m, l;
+  int v_ref;
+};
+template <int D, int W>
+__device__ __forceinline__ bool apart_tile(const ChunkParams& p, const TileSlot& s, uint64_t* s_full, uint64_t* p_full, uint64_t* k_empty,
+                                        uint64_t* v_empty, int step, bool has_o, volatile uint32_t* o_set, uint32_t s_at,
+                                        uint32_t o_at, int nvis, float sc, int ns, volatile int* abort_flag, RowSums& r) {
+  const int lane = threadIdx.x & 31;
+  auto wait = [&](uint64_t* bar, int phase) {
+    return __all_sync(0xffffffffu, ck_wait(bar, (uint32_t)phase & 1, abort_flag, p.err)) != 0;
+  };
+#pragma unroll 1
+  for (int part = 0; part < 2; ++part) {
+    if (part == 1) {
+      if (!wait(s_full + 1, ns)) return false;
+      if (W == 2 && lane == 0) {
+        mbar_arrive_n(k_empty, step);
+        if (has_o) mbar_arrive_n(v_empty, step);
+      }
+    }
+    tc_fence_after();
+    float x[16], top = -INFINITY, l = 0.f;
+    auto score = [&](int g, int i) {   // of the row's key 16 g + i
+      return 16 * g + i < nvis && !(s.bad >> g & 1) ? x[i] * (s.bad >> (8 + g) & 1 ? s.k_by[g] : 1.f) * sc : -INFINITY;
+    };
+#pragma unroll 1
+    for (int g = 4 * part; g < 4 * part + 4; ++g) {
+      tmem_ld_cols<16>(s_at + 16 * g, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, score(g, i));
+    }
+    const float m = fmaxf(r.m, top), by = m == -INFINITY ? 1.f : ex2_approx(r.m - m), base = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+    for (int g = 4 * part; g < 4 * part + 4; ++g) {
+      tmem_ld_cols<16>(s_at + 16 * g, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) l += ex2_approx(score(g, i) + (kWeightLog2 - base));
+    }
+    r.m = m;
+    r.l = fmaf(r.l, by, l);
+    // O is there once the other part's next scores are
+    const bool begins = part == 0 && !has_o;
+    if (!begins) {
+      if (!wait(s_full + 1 - part, ns + part)) return false;
+      tc_fence_after();
+    } else if (lane == 0) {
+      *o_set = 1;
+    }
+#pragma unroll 1
+    for (int c0 = 0; c0 < D; c0 += 16) {
+      tmem_ld_cols<16>(o_at + c0, x);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = begins ? 0.f : x[i] * by;
+      tmem_st_cols16(o_at + c0, x);
+    }
+    tmem_wait_st();
+#pragma unroll 1
+    for (int g = 4 * part; g < 4 * part + 4; ++g) add_values<D>(p, s, g, s_at + 16 * g, o_at, nvis, sc, base, r.v_ref);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) x[i] = 0.f;
+    tmem_st_cols16(s_at + part * 64, x);
+    tmem_st_cols16(s_at + part * 64 + 16, x);
+    tmem_wait_st();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(p_full + part);
+  }
+  return true;
+}
+
+// The same by calls, for 256-row units: what is in line there slows the tiles that do not need it
+// (4 x 512 over 32768 1030 us, not 1010; with 128-row units a call does, 16 x 5 75 us, not 72).
+template <int D>
+__device__ __noinline__ bool any_value_call(const ChunkParams& p, const TileSlot& s, uint32_t groups) {
+  return any_value<D>(p, s, groups);
+}
+template <int D>
+__device__ __noinline__ bool apart_tile_call(const ChunkParams& p, const TileSlot& s, uint64_t* s_full, uint64_t* p_full, uint64_t* k_empty,
+                                             uint64_t* v_empty, int step, bool has_o, volatile uint32_t* o_set, uint32_t s_at,
+                                             uint32_t o_at, int nvis, float sc, int ns, volatile int* abort_flag, RowSums& r) {
+  return apart_tile<D, 2>(p, s, s_full, p_full, k_empty, v_empty, step, has_o, o_set, s_at, o_at, nvis, sc, ns, abort_flag, r);
+}
+
 // W: units of 128 W rows.
 template <int D, int W>
 __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_constant__ ChunkParams p) {
@@ -451,6 +629,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
   // both have arrived at q_free (a tile's slot may be filled anew before an issuer that
   // has none of its scores to make comes to it)
   volatile uint2* seg_word = reinterpret_cast<volatile uint2*>(smem + C::OFF_MISC + 32);
+  volatile uint32_t* o_set = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_MISC + 48);   // [2]: O has sums before a half's first products
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int cta = blockIdx.x, G = p.group;
@@ -489,6 +668,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
     mbar_init(never, 1);
     *abort_flag = 0;
     for (int i = 0; i < 4; ++i) nan_seg[i] = 0;
+    o_set[0] = o_set[1] = 0;
     fence_barrier_init();
   }
   // The launch before is the call's own, of the append and the queries, and itself
@@ -654,12 +834,15 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           bad |= __shfl_xor_sync(0xffffffffu, bad, off);
         }
         const bool k_far = cur.id >= 0 && ke - km < -kMostBelow;
+        const bool v_far = cur.id >= 0 && ve - vm < -kMostBelow;
         bad |= (__ballot_sync(0xffffffffu, k_far) >> (lane & 24) & 0xFFu) << 8;
+        bad |= (__ballot_sync(0xffffffffu, v_far) >> (lane & 24) & 0xFFu) << 16;
         if (cur.on) {
           s.grp[g] = cur.id >= 0 ? (int32_t)(row >> 4) : -1;
           const float kf = k_far ? 1.f : pow2_float(max(ke - km, -126)), vf = pow2_float(max(ve - vm, -126));
           s.kf[g] = f16x2(kf, kf);
           s.vf[g] = f16x2(vf, vf);
+          s.v_of[g] = ve;
           s.k_by[g] = k_far ? pow2_float(max(ke - km, -126)) : 1.f;
           if (g == 0) {
             s.k_scale = km == kNoScale ? 1.f : pow2_float(km);
@@ -712,10 +895,14 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               ok = wait(&p_full[2 * m + part], np & 1);
               if (!ok) break;
               tc_fence_after();
+              uint32_t onto = t > t0 || part > 0 ? 1 : 0;
+              if (!onto) {
+                onto = o_set[m];
+                o_set[m] = 0;
+              }
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_tmem_a(o_col, s_col + kk * 8, v + (uint32_t)(4 * part + kk) * (2048 >> 4), idesc_pv,
-                                t > t0 || part + kk > 0 ? 1u : 0u);
+                mma_bf16_tmem_a(o_col, s_col + kk * 8, v + (uint32_t)(4 * part + kk) * (2048 >> 4), idesc_pv, kk > 0 ? 1u : onto);
               // the next tile of this half takes the same stage
               if (W == 1 && part == 1) mma_commit(&v_empty[jt & 1]);
             }
@@ -940,6 +1127,16 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               sc = qs * ts.k_scale;   // in range, so that a masked score stays -inf; NaN stays
               sc = sc < FLT_MIN ? FLT_MIN : sc > FLT_MAX ? FLT_MAX : sc;
               bad = ts.bad;
+              if (bad >> 16 && (W == 1 ? any_value<D>(p, ts, bad >> 16) : any_value_call<D>(p, ts, bad >> 16))) {   // (seldom)
+                RowSums sums = {m_run, l_run, v_ref};
+                auto* tile = W == 1 ? apart_tile<D, 1> : apart_tile_call<D>;
+                ok = tile(p, ts, s_full + 2 * m, p_full + 2 * m, &k_empty[j & 1], &v_empty[(j - step) & 1], step, t >= step, o_set + m, s_at, o_at,
+                          nvis, sc, ns, abort_flag, sums);
+                m_run = sums.m;
+                l_run = sums.l;
+                v_ref = sums.v_ref;
+                break;
+              }
               // The weights hold the tile's V scale over 2^v_ref, the unit of the row's O.  Where
               // the scale is far below it, O is brought to a smaller unit first (as far as
               // its largest element stays in range), so that these weights keep their bits; where it
@@ -963,7 +1160,7 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
             float alpha = 1.f;   // what O is multiplied by
             tmem_wait_ld();
             if (nvis < CK_KEYS || bad) {
-              if (bad >> 8) {   // pages whose K scales are far below the tile's (seldom)
+              if (bad >> 8 & 0xFFu) {   // pages whose K scales are far below the tile's (seldom)
 #pragma unroll
                 for (int i = 0; i < 64; ++i) x[i / 32][i % 32] *= slots[j % kSlots].k_by[4 * part + i / 16];
               }

@@ -544,9 +544,12 @@ c2kv_status c2kv_attend_pages8(const c2kv_geometry* geom, const c2kv_pages8* pag
  * c2kv_attend_pages8_chunk_workspace_size bytes, 16-byte aligned, of any
  * contents; calls that do not overlap on the GPU may share it, whatever their
  * shapes.  flags: C2KV_DECODE_ROW_AT_LENGTH, for the append as well.  The
- * queries are held to 11 bits, in fp16, and so are the softmax weights; sums
- * are in fp32.  A query that is not finite gives NaN, a held NaN gives NaN to
- * the tokens that see it.
+ * queries are held to 11 bits, in fp16 times a power of two for each head, and
+ * so are the softmax weights, down to 2^-15 of a row's largest; sums are in fp32.
+ * The scales of a sequence's pages may be as far apart as they get; where V
+ * scales among 128 neighbouring rows are more than 2^15 apart, those rows take
+ * some 30 times as long.  A query that is not finite gives NaN, a held NaN gives
+ * NaN to the tokens that see it.
  */
 size_t c2kv_attend_pages8_chunk_workspace_size(const c2kv_geometry* geom, int32_t batch, int32_t t_len,
                                                int32_t max_keys);
