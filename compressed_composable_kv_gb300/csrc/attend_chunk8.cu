@@ -534,7 +534,7 @@ __device__ __forceinline__ bool apart_tile(const ChunkParams& p, const TileSlot&
       }
     }
     tc_fence_after();
-    float x[16], top = -INFINITY, l = 0.f;
+    float x[16] = {}, top = -INFINITY, l = 0.f;
     auto score = [&](int g, int i) {   // of the row's key 16 g + i
       return 16 * g + i < nvis && !(s.bad >> g & 1) ? x[i] * (s.bad >> (8 + g) & 1 ? s.k_by[g] : 1.f) * sc : -INFINITY;
     };

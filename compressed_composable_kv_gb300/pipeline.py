@@ -244,7 +244,9 @@ class PagedSequences:
         self.n_cached_dev = torch.full((1,), -1, dtype=torch.int32, device=dev)
         self.rope_start = torch.zeros(1, dtype=torch.int32, device=dev)
         self._chunk_ws: List[torch.Tensor] = []   # the last one serves; captured graphs may hold the others
-        self._decode_ws: Optional[torch.Tensor] = None
+        # zeroed here, not by a first call that may be a graph's; of a size that the
+        # number of sequences does not change
+        self._decode_ws = torch.zeros(B.c2kv_attend_pages8_workspace_size(geom, 1, max_keys), dtype=torch.uint8, device=dev)
         self._pages_change = True   # the last call wrote pages or lengths: what reads some early waits
 
     @property
@@ -307,11 +309,6 @@ class PagedSequences:
         """One token of each sequence, as RequestBatch.decode over pages."""
         if overlap_previous is None:
             overlap_previous = layer > 0 and not self._pages_change
-        if self._decode_ws is None or self._decode_ws.shape[0] != self.batch:
-            with torch.cuda.stream(self._stream(stream)):
-                self._decode_ws = torch.zeros(
-                    (self.batch, -(-B.c2kv_attend_pages8_workspace_size(self.geom, self.batch, self.max_keys) // self.batch)),
-                    dtype=torch.uint8, device=self.refs.device)
         d = self.geom.head_dim
         B.c2kv_attend_pages8(self.geom, layer, *self._pool(), self.page_table, self.n_cached_dev, self.max_keys,
                              q.view(self.batch, -1, d), k_new.view(self.batch, -1, d), v_new.view(self.batch, -1, d),

@@ -1,0 +1,37 @@
+"""PagedSequences without a GPU: what it keeps, gives back and refuses.  The library's
+calls are noted, forks are the oracle's."""
+import pytest
+import torch
+
+import oracle.pages8_oracle as Q
+from compressed_composable_kv_gb300 import synth as S
+from test_chunk8_cpu import noted  # noqa: F401
+from test_pages8_cpu import P  # noqa: F401
+
+
+def _decode(seqs, layer=0):
+    x = torch.zeros((seqs.batch, 4, 64))
+    seqs.decode(layer, x, x[:, :2], x[:, :2], x)
+
+
+def test_decode_keeps_one_workspace(noted, P, monkeypatch):  # noqa: F811
+    """Its counters are zeroed once, before the first call (a fill while a graph is captured
+    would run at its first replay only), and it serves every number of sequences."""
+    rb, calls = noted
+    used = []
+    monkeypatch.setattr(P.pipeline.B, "c2kv_attend_pages8", lambda g, l, *a: used.append(a[13]))
+    rb.fill_pages8()
+    seqs = rb.answers(2, room=4)
+    made = []
+    zeros = torch.zeros
+    monkeypatch.setattr(torch, "zeros", lambda *a, **kw: made.append(zeros(*a, **kw)) or made[-1])
+    _decode(seqs)
+    seqs.fork([0, -1, 1], 1)
+    _decode(seqs)
+    seqs.fork([2], 1)
+    _decode(seqs)
+    monkeypatch.undo()
+    assert len(used) == 3 and all(w is used[0] for w in used)
+    assert not any(w.data_ptr() == x.data_ptr() for x in made for w in used) and int(used[0].sum()) == 0
+    for batch in (1, 2, 256):
+        assert used[0].numel() >= P.c2kv_attend_pages8_workspace_size(seqs.geom, batch, seqs.max_keys)
