@@ -243,7 +243,9 @@ class PagedSequences:
         self.page_table = torch.full((1, -(-max_keys // self.page)), -1, dtype=torch.int32, device=dev)
         self.n_cached_dev = torch.full((1,), -1, dtype=torch.int32, device=dev)
         self.rope_start = torch.zeros(1, dtype=torch.int32, device=dev)
-        self._chunk_ws: List[torch.Tensor] = []   # the last one serves; captured graphs may hold the others
+        self._chunk_ws: List[torch.Tensor] = []   # the last one serves; captured graphs hold the others
+        self._chunk_ws_held = False   # by a graph, the last one
+        self._chunk_ws_stream = None  # that it was allocated on
         # zeroed here, not by a first call that may be a graph's; of a size that the
         # number of sequences does not change
         self._decode_ws = torch.zeros(B.c2kv_attend_pages8_workspace_size(geom, 1, max_keys), dtype=torch.uint8, device=dev)
@@ -297,13 +299,30 @@ class PagedSequences:
         [head_dim]) over its pages, their append included; n_new: int32 [batch], the
         tokens of a padded batch."""
         need = B.c2kv_attend_pages8_chunk_workspace_size(self.geom, self.batch, q.shape[1], self.max_keys)
-        with torch.cuda.stream(self._stream(stream)):
-            if not self._chunk_ws or self._chunk_ws[-1].numel() < need:
-                self._chunk_ws.append(torch.empty(need, dtype=torch.uint8, device=self.refs.device))
         B.c2kv_attend_pages8_chunk(self.geom, layer, *self._pool(), self.page_table, self.n_cached_dev, self.max_keys, q,
-                                   k_new, v_new, self.rope_table, self.rope_start, out, self._chunk_ws[-1], n_new, stream,
-                                   B.C2KV_DECODE_ROW_AT_LENGTH)
+                                   k_new, v_new, self.rope_table, self.rope_start, out, self._chunk_workspace(need, stream),
+                                   n_new, stream, B.C2KV_DECODE_ROW_AT_LENGTH)
         self._pages_change = True
+
+    def _chunk_workspace(self, need: int, stream) -> torch.Tensor:
+        """Scratch of at least `need` bytes for a call on this stream.  One that has become too
+        small is let go, unless a captured graph works on it."""
+        s = self._stream(stream)
+        with torch.cuda.stream(s):
+            if not self._chunk_ws or self._chunk_ws[-1].numel() < need:
+                if self._chunk_ws:
+                    need = max(need, self._chunk_ws[-1].numel() * 3 // 2)   # so few of them, whatever is asked for
+                    if not self._chunk_ws_held:
+                        self._chunk_ws.pop()
+                self._chunk_ws.append(torch.empty(need, dtype=torch.uint8, device=self.refs.device))
+                self._chunk_ws_held, self._chunk_ws_stream = False, s
+            ws = self._chunk_ws[-1]
+            if s is not None:
+                if torch.cuda.is_current_stream_capturing():
+                    self._chunk_ws_held = True
+                elif s != self._chunk_ws_stream:
+                    ws.record_stream(s)
+        return ws
 
     def decode(self, layer: int, q, k_new, v_new, out, stream=None, overlap_previous: Optional[bool] = None) -> None:
         """One token of each sequence, as RequestBatch.decode over pages."""

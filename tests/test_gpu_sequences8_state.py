@@ -39,3 +39,46 @@ def test_first_decode_behind_a_fork_is_captured():
     torch.cuda.synchronize()
     assert torch.equal(o, want) and P.c2kv_device_error() == P.C2KV_OK
     w.sc.close()
+
+
+def test_chunks_that_grow_on_several_streams():
+    """Longer and longer chunks on two streams by turns, each still to run when the next one
+    asks for more scratch: the answers are those of one stream, and of a graph captured on the way."""
+    g = S.Geometry(1, 4, 2, 64, 1e4)
+    w = World(g, 16, spare=160, steps=700)
+    seqs = w.rb.answers(2, room=640)
+    sides = [torch.cuda.Stream() for _ in range(2)]
+    lens = [3, 40, 90, 200, 330, 640]
+    args = []
+    for t in lens:
+        q = _dev(_values(w.rng, (4, t, 4, 64)))
+        k, v = (_dev(_values(w.rng, (4, t, 2, 64))) for _ in range(2))
+        args.append((q, k, v, torch.zeros_like(q)))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    for i, a in enumerate(args):
+        side, other = sides[i % 2], sides[1 - i % 2]
+        side.wait_stream(other)   # chunks of one pool follow one another
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        seqs.chunk(0, *a, stream=side)
+        if i == 2:
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                seqs.chunk(0, *a)
+        with torch.cuda.stream(side):   # takes the place of what was let go
+            junk = [torch.full((n,), 0x5A, dtype=torch.uint8, device="cuda") for n in (1 << 20, 1 << 22, 1 << 23)]
+            del junk
+    torch.cuda.synchronize()
+    assert P.c2kv_device_error() == P.C2KV_OK
+    assert len(seqs._chunk_ws) <= 2   # the captured one and the last
+    got = [a[3].clone() for a in args]
+    for a, x in zip(args, got):
+        a[3].zero_()
+        seqs.chunk(0, *a)
+        assert torch.equal(a[3], x)
+    args[2][3].zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(args[2][3], got[2]) and P.c2kv_device_error() == P.C2KV_OK
+    w.sc.close()

@@ -35,3 +35,22 @@ def test_decode_keeps_one_workspace(noted, P, monkeypatch):  # noqa: F811
     assert not any(w.data_ptr() == x.data_ptr() for x in made for w in used) and int(used[0].sum()) == 0
     for batch in (1, 2, 256):
         assert used[0].numel() >= P.c2kv_attend_pages8_workspace_size(seqs.geom, batch, seqs.max_keys)
+
+
+def _chunk(seqs, t_len):
+    x = torch.zeros((seqs.batch, t_len, 4, 64), dtype=torch.bfloat16)
+    seqs.chunk(0, x, x[:, :, :2], x[:, :, :2], x)
+
+
+def test_chunks_keep_one_workspace(noted, P, monkeypatch):  # noqa: F811
+    """Chunks longer from call to call: the scratch grows by steps, and what it has grown out of is let go."""
+    rb, calls = noted
+    used = []
+    monkeypatch.setattr(P.pipeline.B, "c2kv_attend_pages8_chunk", lambda g, l, *a: used.append(a[13].numel()))
+    rb.fill_pages8()
+    seqs = rb.answers(2, room=4)
+    for t_len in range(1, 1200, 7):
+        _chunk(seqs, t_len)
+        assert used[-1] >= P.c2kv_attend_pages8_chunk_workspace_size(seqs.geom, 4, t_len, seqs.max_keys)
+    assert len(seqs._chunk_ws) == 1
+    assert len(set(used)) < 8
