@@ -17,6 +17,15 @@ import torch
 from . import binding as B
 
 
+def _stream_on(device: torch.device, stream):
+    """The stream of a call (None: the device's current one, or a handle) as a torch stream; None on the host."""
+    if device.type != "cuda":
+        return None
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device)
+
+
 @dataclass
 class RequestSpec:
     doc_ids: List[int]
@@ -204,8 +213,7 @@ class RequestBatch:
             raise ValueError("n must be at least 1")
         dev = self.page_table.device
         rows = [s + self.q_len for s in self.n_slots]
-        s = torch.cuda.current_stream(dev) if stream is None and dev.type == "cuda" else stream
-        with torch.cuda.stream(s):
+        with torch.cuda.stream(_stream_on(dev, stream)):
             held = torch.tensor([-(-r // self.page8) for r in rows], device=dev)[:, None]
             width = self.page_table.shape[1]
             mine = torch.arange(width, device=dev) < held
@@ -343,12 +351,7 @@ class PagedSequences:
         self._pages_change = True
 
     def _stream(self, stream):
-        """The stream of a call, as a torch stream (None on the host)."""
-        if not self.page_table.is_cuda:
-            return None
-        if stream is None:
-            return torch.cuda.current_stream(self.page_table.device)
-        return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream))
+        return _stream_on(self.refs.device, stream)
 
 
 class DecoderModel:

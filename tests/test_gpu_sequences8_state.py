@@ -82,3 +82,15 @@ def test_chunks_that_grow_on_several_streams():
     torch.cuda.synchronize()
     assert torch.equal(args[2][3], got[2]) and P.c2kv_device_error() == P.C2KV_OK
     w.sc.close()
+
+
+def test_answers_on_a_stream_given_by_its_handle():
+    """A stream is a torch stream or a handle, as in every other call."""
+    g = S.Geometry(1, 4, 2, 64, 1e4)
+    w = World(g, 16, spare=20)
+    side = torch.cuda.Stream()
+    seqs = w.rb.answers(2, room=3, stream=side.cuda_stream)
+    w.fork([0, 0, 1, 1], 3)
+    side.synchronize()
+    w.check(seqs, "answers")
+    w.sc.close()
