@@ -9,6 +9,7 @@ then generate.
 """
 from __future__ import annotations
 
+import weakref
 from dataclasses import dataclass
 from typing import List, Optional, Sequence
 
@@ -95,6 +96,7 @@ class RequestBatch:
         self.page8 = page8
         self.filled = set()
         self._fill_before = False   # the batch's last call was fill_pages8
+        self._answers = lambda: None   # the sequences that have the pool's pages, while they are there
         if page8 is not None:
             most = -(-self.max_keys_decode // page8)
             self.page_table = torch.arange(most * self.batch, dtype=torch.int32, device=device).reshape(self.batch, most)
@@ -166,6 +168,7 @@ class RequestBatch:
         """The composed and prefilled rows of layers [layer_begin, layer_end) to the 8-bit pages."""
         if self.page8 is None:
             raise ValueError("this batch was made without page8")
+        self._refuse_lent_pool()
         layer_end = self.geom.n_layers if layer_end is None else layer_end
         B.c2kv_pages8_fill(self.geom, layer_begin, layer_end, self.k_caches, self.v_caches, self.cap,
                            [n + self.q_len for n in self.n_slots], self.k8, self.v8, self.k_scale, self.v_scale,
@@ -182,6 +185,7 @@ class RequestBatch:
             overlap_previous = layer > 0 and not self._fill_before
         flags = B.C2KV_DECODE_OVERLAP_PREVIOUS if overlap_previous else 0
         if self.page8 is not None:
+            self._refuse_lent_pool()
             if layer not in self.filled and 0 <= layer < self.geom.n_layers and not self._capturing(stream):
                 raise ValueError(f"the pages of layer {layer} do not hold the batch's rows: fill_pages8 comes first")
             B.c2kv_attend_pages8(self.geom, layer, self.k8, self.v8, self.k_scale, self.v_scale, self.page_table,
@@ -196,6 +200,11 @@ class RequestBatch:
                              self.n_cached_dev, self.max_keys_decode, q, k_new, v_new, out, self.workspace,
                              stream, flags)
 
+    def _refuse_lent_pool(self) -> None:
+        seqs = self._answers()
+        if seqs is not None and not seqs.released:
+            raise ValueError("the pool's pages are those of the sequences that answers made: their release() comes first")
+
     def advance(self, stream=None) -> None:
         own = self.n_cached_dev is self._own_lengths
         B.c2kv_seq_advance(self._lengths if own else self.n_cached_dev, 1, stream)
@@ -203,9 +212,12 @@ class RequestBatch:
     def answers(self, n: int = 1, room: int = 1, stream=None) -> "PagedSequences":
         """n sequences for each request, on the pool's pages: they share the composed
         cache and the question, each with room for `room` tokens of its own.  The pool
-        is theirs from here on (all layers of it have to be filled)."""
+        is theirs from here on (all layers of it have to be filled): while they are there,
+        fill_pages8 and decode of this batch are refused, until their release().  (The next
+        composition and prefill, which write bf16 rows, are not.)"""
         if self.page8 is None:
             raise ValueError("this batch was made without page8")
+        self._refuse_lent_pool()
         missing = sorted(set(range(self.geom.n_layers)) - self.filled)
         if missing:
             raise ValueError(f"the pages of layers {missing} do not hold the batch's rows: fill_pages8 comes first")
@@ -225,6 +237,7 @@ class RequestBatch:
             seqs.rope_start = self._rope_start.clone()
         seqs.fork([b for b in range(self.batch) for _ in range(n)], room, stream)
         self.filled.clear()
+        self._answers = weakref.ref(seqs)
         return seqs
 
 
@@ -257,6 +270,7 @@ class PagedSequences:
         # zeroed here, not by a first call that may be a graph's; of a size that the
         # number of sequences does not change
         self._decode_ws = torch.zeros(B.c2kv_attend_pages8_workspace_size(geom, 1, max_keys), dtype=torch.uint8, device=dev)
+        self.released = False
         self._pages_change = True   # the last call wrote pages or lengths: what reads some early waits
 
     @property
@@ -264,6 +278,8 @@ class PagedSequences:
         return self.page_table.shape[0]
 
     def _pool(self):
+        if self.released:
+            raise ValueError("these sequences were released: the pool is the batch's again")
         return self.k8, self.v8, self.k_scale, self.v_scale
 
     def fork(self, parents, room: int = 1, stream=None) -> None:
@@ -292,6 +308,10 @@ class PagedSequences:
             self.rope_start = self.rope_start[parents.clamp(min=0, max=self.batch - 1).long()]
             self.page_table, self.n_cached_dev = table, lengths
         self._pages_change = True
+
+    def release(self) -> None:
+        """The pool goes back to the batch that made these sequences; they take no more calls."""
+        self.released = True
 
     def compact(self, stream=None) -> None:
         """The pages in use to the front of the pool."""

@@ -54,3 +54,36 @@ def test_chunks_keep_one_workspace(noted, P, monkeypatch):  # noqa: F811
         assert used[-1] >= P.c2kv_attend_pages8_chunk_workspace_size(seqs.geom, 4, t_len, seqs.max_keys)
     assert len(seqs._chunk_ws) == 1
     assert len(set(used)) < 8
+
+
+def test_the_pool_is_refused_while_sequences_live_on_it(noted):  # noqa: F811
+    """What would write the batch's own rows over pages that answers share is refused until
+    the sequences are released, or gone."""
+    rb, calls = noted
+    x = torch.zeros((2, 4, 64))
+
+    def decode():
+        rb.decode(0, x, x[:, :2], x[:, :2], x)
+
+    rb.fill_pages8()
+    decode()
+    seqs = rb.answers(2, room=4)
+    rb.filled.update({0, 1})   # as a program does that writes pages by calls of its own
+    for call in (rb.fill_pages8, lambda: rb.fill_pages8(0, 1), decode, lambda: rb.answers(1)):
+        with pytest.raises(ValueError, match="release"):
+            call()
+    _decode(seqs)
+    seqs.release()
+    n = len(calls)
+    for call in (lambda: _decode(seqs), lambda: _chunk(seqs, 2), lambda: seqs.fork([0], 1), seqs.compact):
+        with pytest.raises(ValueError, match="released"):
+            call()
+    assert len(calls) == n
+    rb.fill_pages8()
+    decode()
+    seqs = rb.answers(1)
+    with pytest.raises(ValueError, match="release"):
+        rb.fill_pages8()
+    del seqs
+    rb.fill_pages8()
+    decode()
