@@ -251,7 +251,8 @@ class PagedSequences:
     fork makes new tensors of them, so a graph is captured anew behind it; compact
     changes them in place.  Tokens are written to pages that `fork` has taken: its
     `room` says how many may follow before the next one.  A fork that finds too few free
-    pages, or a parent that is none, records C2KV_EDEVICE and leaves all places empty.
+    pages, no place for `room` more tokens in a row of the table, or a parent that is none
+    records C2KV_EDEVICE and leaves all places empty; `restore` brings the sequences back.
     """
 
     def __init__(self, geom, k8: torch.Tensor, v8: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
@@ -264,6 +265,11 @@ class PagedSequences:
         self.page_table = torch.full((1, -(-max_keys // self.page)), -1, dtype=torch.int32, device=dev)
         self.n_cached_dev = torch.full((1,), -1, dtype=torch.int32, device=dev)
         self.rope_start = torch.zeros(1, dtype=torch.int32, device=dev)
+        # page_table, n_cached_dev and rope_start lie one behind the other, each with room for
+        # as many places (the rest is -1), here and as the last fork that found a sequence found them
+        self._state = self._kept = self.refs[:0]
+        self._same = torch.arange(-1, n_pages, dtype=torch.int32, device=dev)
+        self._parts = ()
         self._chunk_ws: List[torch.Tensor] = []   # the last one serves; captured graphs hold the others
         self._chunk_ws_held = False   # by a graph, the last one
         self._chunk_ws_stream = None  # that it was allocated on
@@ -292,22 +298,81 @@ class PagedSequences:
             if not isinstance(parents, torch.Tensor):
                 parents = torch.tensor(list(parents), dtype=torch.int32).to(dev, non_blocking=True)
             n, width = parents.numel(), self.page_table.shape[1]
-            table = torch.empty((n, width), dtype=torch.int32, device=dev)
-            lengths = torch.empty(n, dtype=torch.int32, device=dev)
+            now = self._packed(n, s)
+            # (all places are empty behind a fork that failed: what it found is kept)
+            torch.where(self.n_cached_dev.max() >= 0, now, self._kept, out=self._kept)
+            # a call that fails writes nothing: all places then stay empty
+            state = torch.full_like(now, -1)
+            table, lengths, rope = self._views(state, n, width)
             ws = torch.empty(B.c2kv_pages8_plan_workspace_size(self.refs.numel(), max(n, self.batch), width),
                              dtype=torch.uint8, device=dev)
-            # a call that finds too few pages writes nothing: these then stay empty places
-            table.fill_(-1)
-            lengths.fill_(-1)
             B.c2kv_pages8_fork(self.geom, *self._pool(), self.refs, self.page_table, self.n_cached_dev, parents, room,
                                self.refs, table, lengths, ws, stream)
-            if s is not None and not torch.cuda.is_current_stream_capturing():
-                # these are let go while the call may still be to run, and may be of other streams
-                for x in (self.page_table, self.n_cached_dev, self.rope_start, parents):
-                    x.record_stream(s)
-            self.rope_start = self.rope_start[parents.clamp(min=0, max=self.batch - 1).long()]
-            self.page_table, self.n_cached_dev = table, lengths
+            torch.index_select(self.rope_start, 0, parents.clamp(min=0, max=self.batch - 1), out=rope)
+            self._let_go(s, self.page_table, self.n_cached_dev, self.rope_start, parents)
+            self._adopt(state, n, width)
         self._pages_change = True
+
+    def restore(self, stream=None) -> bool:
+        """Behind a fork that failed (C2KV_EDEVICE): the sequences as that fork found them,
+        however many steps, forks and compactions came after it.  False, and nothing is
+        changed, where none has failed.  Waits for the stream."""
+        s = self._stream(stream)
+        with torch.cuda.stream(s):
+            width = self.page_table.shape[1]
+            table, lengths, rope = self._views(self._kept, None, width)
+            if table.shape[0] == 0 or bool((self.n_cached_dev >= 0).any()):
+                return False
+            n = int((rope >= 0).sum())
+            held = (table >= 0).cumprod(1).bool()
+            uses = torch.bincount(table[held].long(), minlength=self.refs.numel())
+            if n == 0 or bool((self.refs < uses).any()) or bool((held.sum(1) * self.page < lengths).any()):
+                return False   # ended by a fork: their pages were given back
+            self._let_go(s, self.page_table, self.n_cached_dev, self.rope_start)
+            self._adopt(self._kept.clone(), n, width)
+        self._pages_change = True
+        return True
+
+    @staticmethod
+    def _let_go(s, *tensors) -> None:
+        """These are let go while calls on the stream may still read them, and may be of other streams."""
+        if s is not None and not torch.cuda.is_current_stream_capturing():
+            for x in tensors:
+                x.record_stream(s)
+
+    @staticmethod
+    def _views(state, n, width):
+        """Page table, lengths and RoPE rows of n places (None: of all) in a state."""
+        cap = state.numel() // (width + 2)
+        if n is None or n == cap:
+            table, lengths, rope = state.split_with_sizes((cap * width, cap, cap))
+        else:
+            rest = cap - n
+            table, _, lengths, _, rope, _ = state.split_with_sizes((n * width, rest * width, n, rest, n, rest))
+        return table.view(-1, width), lengths, rope
+
+    def _adopt(self, state, n, width) -> None:
+        self._state = state
+        self._parts = self.page_table, self.n_cached_dev, self.rope_start = self._views(state, n, width)
+
+    def _packed(self, n, s) -> torch.Tensor:
+        """The present state, with room for n places; what is kept gets as much."""
+        width, now = self.page_table.shape[1], (self.page_table, self.n_cached_dev, self.rope_start)
+        cap = max(n, self.batch)
+        if all(x is y for x, y in zip(now, self._parts)) and len(self._parts) == 3 and self._state.numel() >= cap * (width + 2):
+            return self._state
+        cap = max(cap, self._kept.numel() // (width + 2))
+
+        def pack(parts):
+            state = torch.full((cap * (width + 2),), -1, dtype=torch.int32, device=self.refs.device)
+            for dst, src in zip(self._views(state, parts[0].shape[0], width), parts):
+                dst.copy_(src)
+            return state
+
+        if self._kept.numel() < cap * (width + 2):
+            self._let_go(s, self._kept)
+            self._kept = pack(self._views(self._kept, None, width))
+        return pack(now)
 
     def release(self) -> None:
         """The pool goes back to the batch that made these sequences; they take no more calls."""
@@ -316,10 +381,14 @@ class PagedSequences:
     def compact(self, stream=None) -> None:
         """The pages in use to the front of the pool."""
         with torch.cuda.stream(self._stream(stream)):
-            ws = torch.empty(B.c2kv_pages8_plan_workspace_size(self.refs.numel(), self.batch, self.page_table.shape[1]),
+            width = self.page_table.shape[1]
+            ws = torch.empty(B.c2kv_pages8_plan_workspace_size(self.refs.numel(), self.batch, width),
                              dtype=torch.uint8, device=self.refs.device)
+            to = self._same.clone()   # where page i is, in place 1 + i; -1 in place 0 and of free pages
             B.c2kv_pages8_compact(self.geom, *self._pool(), self.refs, self.page_table, self.refs, self.page_table,
-                                  None, ws, stream)
+                                  to[1:], ws, stream)
+            kept = self._views(self._kept, None, width)[0].view(-1)   # what a failed fork found has moved, too
+            torch.index_select(to, 0, torch.clamp(kept, -1, to.numel() - 2).add_(1), out=kept)
         self._pages_change = True
 
     def chunk(self, layer: int, q, k_new, v_new, out, n_new: Optional[torch.Tensor] = None, stream=None) -> None:

@@ -94,3 +94,64 @@ def test_answers_on_a_stream_given_by_its_handle():
     side.synchronize()
     w.check(seqs, "answers")
     w.sc.close()
+
+
+@pytest.mark.parametrize("parents,room", [([0] * 250, 1), ([3, 1, 0, 2], 500), ([0, 9], 1)])
+def test_sequences_go_on_behind_a_failed_fork(parents, room):
+    """Too few pages, more room than the table has, a parent that is none; found after
+    further steps, another fork and a compaction."""
+    g = S.Geometry(2, 8, 2, 128, 5.0e5)
+    w = World(g, 16, spare=25)
+    side = torch.cuda.Stream()
+    seqs = w.rb.answers(2, room=10)
+    w.fork([0, 0, 1, 1], 10)
+    w.decode(seqs, 2, "before")
+    side.wait_stream(torch.cuda.current_stream())
+    seqs.fork(parents, room, side)
+    x = [torch.zeros((len(parents), h, 128), dtype=torch.bfloat16, device="cuda") for h in (8, 2, 8)]
+    side.wait_stream(torch.cuda.current_stream())
+    seqs.decode(0, x[0], x[1], x[1], x[2], side)
+    seqs.advance(side)
+    seqs.fork([0, 0, 1], 4, side)
+    seqs.compact(side)
+    w.compact()
+    torch.cuda.synchronize()
+    assert P.c2kv_device_error() == P.C2KV_EDEVICE
+    assert (seqs.n_cached_dev == -1).all()
+    assert seqs.restore(side)
+    torch.cuda.synchronize()
+    w.check(seqs, "restored")
+    w.decode(seqs, 2, "restored")
+    seqs.fork([2, -1, 0], 3)
+    w.fork([2, -1, 0], 3)
+    w.chunk(seqs, [2, 0, 3], "restored")
+    w.check(seqs, "at the end")
+    assert not seqs.restore()
+    w.sc.close()
+
+
+def test_beams_in_a_graph():
+    """A step with its fork of the same number of places, captured: the fork's tensors are the
+    next step's, so a program copies them back; replays follow the oracle's pages."""
+    g = S.Geometry(1, 4, 2, 64, 1e4)
+    w = World(g, 16, spare=60)
+    seqs = w.rb.answers(2, room=40)
+    w.fork([0, 0, 1, 1], 40)
+    seqs.fork([0, 1, 2, 3], 1)
+    w.fork([0, 1, 2, 3], 1)
+    torch.cuda.synchronize()
+    was = seqs.page_table, seqs.n_cached_dev, seqs.rope_start
+    parents = torch.tensor([1, 0, 2, 2], dtype=torch.int32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        seqs.fork(parents, 1)
+        for a, b in zip(was, (seqs.page_table, seqs.n_cached_dev, seqs.rope_start)):
+            a.copy_(b)
+    seqs.page_table, seqs.n_cached_dev, seqs.rope_start = was
+    for step in range(3):
+        graph.replay()
+        w.fork([1, 0, 2, 2], 1)
+        w.check(seqs, f"step {step}")
+    w.decode(seqs, 1, "behind the graph")
+    w.check(seqs, "behind the graph")
+    w.sc.close()

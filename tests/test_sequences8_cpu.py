@@ -87,3 +87,104 @@ def test_the_pool_is_refused_while_sequences_live_on_it(noted):  # noqa: F811
     del seqs
     rb.fill_pages8()
     decode()
+
+
+@pytest.fixture
+def strict(noted, P, monkeypatch):  # noqa: F811
+    """As `noted`, with forks that write nothing where the oracle finds none, and the oracle's compaction."""
+    rb, calls = noted
+    B = P.pipeline.B
+
+    def fork(g, k8, v8, ks, vs, refs, table, n, parent, room, refs_out, table_out, n_out, ws, stream=None):
+        got = Q.fork(refs.tolist(), table.tolist(), n.tolist(), parent.tolist(), room, k8.shape[3])
+        calls.append(("fork", got is not None))
+        if got is not None:
+            for dst, src in zip((refs_out, table_out, n_out), got):
+                dst.copy_(torch.tensor(src))
+
+    def compact(g, k8, v8, ks, vs, refs, table, refs_out, table_out, moved_out, ws, stream=None):
+        got = Q.compact(refs.tolist(), table.tolist())
+        for dst, src in zip((refs_out, table_out, moved_out), got):
+            if dst is not None:
+                dst.copy_(torch.tensor(src))
+
+    monkeypatch.setattr(B, "c2kv_pages8_fork", fork)
+    monkeypatch.setattr(B, "c2kv_pages8_compact", compact)
+    rb.fill_pages8()
+    return rb.answers(2, room=4), calls
+
+
+def _state(seqs):
+    return [x.tolist() for x in (seqs.page_table, seqs.n_cached_dev, seqs.rope_start, seqs.refs)]
+
+
+@pytest.mark.parametrize("parents,room", [([0] * 40, 4), ([3, 2, 1, 0], 30), ([1], 300), ([0, 1, 2, 3, 7], 1)])
+def test_a_failed_fork_loses_nothing(strict, parents, room):
+    """Too few pages, more room than a row of the table has, a parent that is none: all
+    places are empty, and restore brings back the sequences as they were."""
+    seqs, calls = strict
+    seqs.advance(n=torch.tensor([2, 0, 1, 3], dtype=torch.int32))
+    before = _state(seqs)
+    assert not seqs.restore() and _state(seqs) == before   # nothing has failed
+    seqs.fork(parents, room)
+    assert calls[-1] == ("fork", False)
+    assert seqs.batch == len(parents) and (seqs.n_cached_dev == -1).all() and (seqs.page_table == -1).all()
+    assert seqs.restore()
+    assert _state(seqs) == before
+    seqs.fork([3, -1, 0], 2)   # and they go on
+    assert calls[-1] == ("fork", True) and seqs.n_cached_dev.tolist() == [16, -1, 15]
+    assert not seqs.restore()
+    assert sum(seqs.refs.tolist()) == sum(e >= 0 for row in seqs.page_table.tolist() for e in row)
+
+
+def test_a_failed_fork_is_found_late(strict):
+    """Steps go on with the empty places, forks and a compaction among them, before the
+    program reads the error: the sequences are still those of before it."""
+    seqs, calls = strict
+    seqs.fork([0, -1, 3], 1)
+    seqs.compact()
+    lengths, starts = seqs.n_cached_dev.tolist(), seqs.rope_start.tolist()
+    pages = [sum(e >= 0 for e in row) for row in seqs.page_table.tolist()]
+    seqs.fork([0, 2] * 9, 20)
+    assert calls[-1] == ("fork", False)
+    seqs.advance()
+    seqs.fork([1, 0, 2], 4)
+    seqs.fork(list(range(30)), 1)   # (more places than ever before)
+    seqs.compact()
+    seqs.advance(n=3)
+    assert seqs.restore()
+    assert seqs.n_cached_dev.tolist() == lengths and seqs.rope_start.tolist() == starts
+    assert [sum(e >= 0 for e in row) for row in seqs.page_table.tolist()] == pages
+    assert sum(seqs.refs.tolist()) == sum(pages)
+
+
+def test_a_compaction_moves_what_a_failed_fork_left(strict):
+    seqs, calls = strict
+    seqs.fork([2, 3], 4)
+    table = seqs.page_table.tolist()
+    seqs.fork([0, 1], 300)
+    assert calls[-1] == ("fork", False)
+    moved = Q.compact(seqs.refs.tolist(), [])[2]
+    assert any(m >= 0 and m != i for i, m in enumerate(moved))
+    seqs.compact()
+    assert seqs.restore()
+    assert seqs.page_table.tolist() == [[moved[e] if e >= 0 else -1 for e in row] for row in table]
+
+
+def test_sequences_that_were_ended_do_not_come_back(strict):
+    seqs, calls = strict
+    seqs.fork([-1, -1], 1)
+    assert calls[-1] == ("fork", True) and sum(seqs.refs.tolist()) == 0
+    assert not seqs.restore() and seqs.n_cached_dev.tolist() == [-1, -1]
+    seqs.compact()
+    seqs.fork([0], 1)
+    assert not seqs.restore()
+
+
+def test_a_failed_fork_of_tensors_that_the_program_has_set(strict):
+    seqs, calls = strict
+    seqs.fork([0, 1], 4)
+    seqs.rope_start = torch.tensor([7, 9], dtype=torch.int32)
+    before = _state(seqs)
+    seqs.fork([0, 1, 1], 300)
+    assert calls[-1] == ("fork", False) and seqs.restore() and _state(seqs) == before
