@@ -360,6 +360,8 @@ c2kv_status c2kv_pages8_fork(const c2kv_geometry* geom, const c2kv_pages8* pages
   if (!n_cached_dev || !parent_dev || !n_cached_out) return api_fail(C2KV_EINVAL, "null pointer");
   if (batch_out < 1 || batch_out > kMaxPagedSeqs) return api_fail(C2KV_EINVAL, "batch_out must be in [1, 256]");
   if (room < 0 || room > INT32_MAX / 4) return api_fail(C2KV_EINVAL, "room must be in [0, 2^29)");
+  // what a fork takes is counted in 32 bits
+  if ((int64_t)batch_out * max_pages > INT32_MAX) return api_fail(C2KV_EINVAL, "batch_out * max_pages must be below 2^31");
   MoveParams p;
   std::memset(&p, 0, sizeof(p));
   p.n_cached = n_cached_dev;

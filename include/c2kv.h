@@ -592,7 +592,7 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
  * not NULL, moved_out [n_pages]: the new index of each page, -1 for free ones.
  * Outputs may be inputs, and bad values end the call, as for the fork.
  *
- * batch, batch_out <= 256.  workspace: c2kv_pages8_plan_workspace_size bytes
+ * batch, batch_out <= 256; batch_out * max_pages < 2^31.  workspace: c2kv_pages8_plan_workspace_size bytes
  * for the larger batch, 16-byte aligned, of any contents, shared by calls that
  * do not overlap on the GPU.  Errors: C2KV_EINVAL, C2KV_ECUDA.
  */

@@ -5,8 +5,8 @@ import torch
 
 import oracle.pages8_oracle as Q
 from compressed_composable_kv_gb300 import synth as S
-from test_chunk8_cpu import noted  # noqa: F401
-from test_pages8_cpu import P  # noqa: F401
+from test_chunk8_cpu import _fork, noted  # noqa: F401
+from test_pages8_cpu import P, _pages  # noqa: F401
 
 
 def _decode(seqs, layer=0):
@@ -188,3 +188,10 @@ def test_a_failed_fork_of_tensors_that_the_program_has_set(strict):
     before = _state(seqs)
     seqs.fork([0, 1, 1], 300)
     assert calls[-1] == ("fork", False) and seqs.restore() and _state(seqs) == before
+
+
+def test_a_table_of_more_entries_than_can_be_counted(P):  # noqa: F811
+    """What all places together may take is counted in 32 bits."""
+    for batch_out, max_pages in ((256, 1 << 23), (64, 1 << 25), (255, 8421505)):
+        assert _fork(P, pages=_pages(P), batch_out=batch_out, max_pages=max_pages) == P.C2KV_EINVAL
+        assert "2^31" in P.c2kv_last_error()
