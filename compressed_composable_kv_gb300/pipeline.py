@@ -325,8 +325,11 @@ class PagedSequences:
                 return False
             n = int((rope >= 0).sum())
             held = (table >= 0).cumprod(1).bool()
-            uses = torch.bincount(table[held].long(), minlength=self.refs.numel())
-            if n == 0 or bool((self.refs < uses).any()) or bool((held.sum(1) * self.page < lengths).any()):
+            ids = table[held].long()
+            if n == 0 or bool((ids >= self.refs.numel()).any()):
+                return False   # pages that are none: not of a fork
+            uses = torch.bincount(ids, minlength=self.refs.numel())
+            if bool((self.refs < uses).any()) or bool((held.sum(1) * self.page < lengths).any()):
                 return False   # ended by a fork: their pages were given back
             self._let_go(s, self.page_table, self.n_cached_dev, self.rope_start)
             self._adopt(self._kept.clone(), n, width)

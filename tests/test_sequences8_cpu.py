@@ -195,3 +195,13 @@ def test_a_table_of_more_entries_than_can_be_counted(P):  # noqa: F811
     for batch_out, max_pages in ((256, 1 << 23), (64, 1 << 25), (255, 8421505)):
         assert _fork(P, pages=_pages(P), batch_out=batch_out, max_pages=max_pages) == P.C2KV_EINVAL
         assert "2^31" in P.c2kv_last_error()
+
+
+def test_pages_that_are_none_do_not_come_back(strict):
+    """A table whose entries are no pages makes a fork fail; it is not taken for sequences."""
+    seqs, calls = strict
+    seqs.page_table[1, 0] = 1 << 30
+    seqs.fork([0, 1], 1)
+    assert calls[-1] == ("fork", False) and not seqs.restore()
+    seqs.compact()
+    assert not seqs.restore() and (seqs.n_cached_dev == -1).all()
