@@ -59,7 +59,7 @@ def _normal_rows(c, n):
     return _f64(_values(c.pool.rng, shape)), _f64(_values(c.pool.rng, shape))
 
 
-def _check_by_column(c, what, skip=None):
+def _check_by_column(c, what, skip=None, rows=None):
     """Each element of the answer against what the keys' own weights and that column's own
     values may move it by: a logit is off by ds_j = (2^-11 + 2^-18) sum_i |q_i K_ji| / sqrt(d)
     (queries in fp16, sums in fp32), so numerator and denominator by ds_j p_j; a weight is
@@ -73,7 +73,7 @@ def _check_by_column(c, what, skip=None):
     for b, (h, n) in enumerate(zip(c.held, c.new)):
         k, v = (Q.held(pl.codes[x][0], pl.scales[x][0], c.page, pl.table[b], h + n) for x in (0, 1))
         q = _rotate(g, _f64(c.q[b, :n]), c.pos[b, :n])
-        for i in range(n):
+        for i in range(n) if rows is None else sorted({r % n for r in rows}):
             for head in range(g.n_q_heads):
                 kv = head // (g.n_q_heads // g.n_kv_heads)
                 K, V = k[kv, :h + i + 1], v[kv, :h + i + 1]
@@ -220,3 +220,41 @@ def test_pages_of_zeros_beside_others():
     _ok()
     c.put_new()
     _check_by_column(c, "zeros")
+
+
+@pytest.mark.parametrize("d,group,page,t,held", [
+    (128, 5, 16, 70, [5000, 4990, 128, 3100]),    # units of 256 and of 94 rows, cut
+    (128, 5, 128, 70, [5000, 4990, 128, 3100]),
+    (64, 4, 32, 300, [2700, 129, 2700]),          # of 256 and of 176 rows
+])
+@pytest.mark.parametrize("kind", ["values", "column", "keys", "all"])
+def test_units_of_256_rows(d, group, page, t, held, kind):
+    """The same at the sizes that take 256 rows to a unit: a large value or key that no query
+    looks at, one column, neighbouring pages of every scale, zeros among them."""
+    g = _geom(d, group, 8)
+    c = _aimed(g, page, held, [t] * len(held), seed=t + page)
+    rng = c.pool.rng
+    for b, n in enumerate(held):
+        k, v = _normal_rows(c, n)
+        pages = -(-n // page)
+        if kind == "all":
+            k *= np.exp2(np.repeat(rng.integers(-60, 2, (8, pages)), page, 1)[:, :n, None])
+            size = np.exp2(rng.choice([-100, -40, -14, -3, 0, 0, 9, 30, 80], (8, pages))) * (rng.random((8, pages)) > 0.2)
+            v *= np.repeat(size, page, 1)[:, :n, None]
+        for i, first in enumerate((0, 640, 1408, 2304) if kind != "all" else ()):
+            at, far = slice(first, first + page), (20, 40, 14, 100)[i]
+            if kind == "values":
+                k[:, at] = 0.0
+                k[:, at, 0] = -2.0 ** 13
+                v[:, at] *= 2.0 ** far
+            elif kind == "column":
+                v[:, at] = 0.0
+                v[:, at, 7] = 2.0 ** far
+            else:
+                k[:, at] = 0.0
+                k[:, at, 0] = -2.0 ** min(far, 80)
+        _hold(c, b, k, v)
+    c.call()
+    _ok()
+    c.put_new()
+    _check_by_column(c, kind, rows=[0, 31, 32, 50, 51, t - 1])
