@@ -164,12 +164,6 @@ __device__ __forceinline__ bool ck_wait(uint64_t* bar, uint32_t parity, volatile
   return mbar_try_wait(bar, parity) || ck_slow_wait(bar, parity, abort_flag, err);
 }
 
-// Two fp32 values to fp16, `a` in the low half.
-__device__ __forceinline__ uint32_t f16x2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
 // Two e4m3 codes to fp16 (exact).
 __device__ __forceinline__ uint32_t f16x2_of_codes(uint32_t codes) {
   uint32_t r;

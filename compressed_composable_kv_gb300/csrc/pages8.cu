@@ -72,13 +72,6 @@ __device__ __forceinline__ void tame(uint32_t& w, uint32_t& m) {
   else m = max(m, hi << 16);
 }
 
-// Two fp32 values to fp16, `a` in the low half.
-__device__ __forceinline__ uint32_t f16x2(float a, float b) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-  return r;
-}
-
 // The queries of new tokens at rows wrow + slice, + PUT_SLICES, ... before wrow + 16 and
 // `end` (the sequence's first new token is at row `first`), all heads of group h: rotated
 // and scaled in fp32, then fp16 over a power of two that brings the largest element of a

@@ -41,6 +41,13 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t codes) {
   return f;
 }
 
+// Two fp32 values to fp16, `a` in the low half.
+__device__ __forceinline__ uint32_t f16x2(float a, float b) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+  return r;
+}
+
 // a (bh + bl) + c (dh + dl), one element of a rotated key, rounded to fp32 and
 // from there to bf16 (the two roundings of a conversion that goes by way of
 // fp32; they differ from a single one in about 2^-17 of elements).  Where the
