@@ -9,7 +9,11 @@
 // products run as kind::f16 (fp32 accumulators): the keys and values lose
 // nothing; a query row is held in fp16 times a power of two of its own, 2^-11 of
 // each element, and so is a weight (2^7 exp(s - m), so that weights down to 2^-15
-// of the largest keep their 11 bits; the bf16 output itself rounds away 2^-8).  Pages
+// of the largest keep their 11 bits).  The bf16 output itself rounds away 2^-8: answers are
+// 0.00161 to 0.00172 off the exact ones in the mean square, most where logits are large (a query
+// moves one by up to 2^-11 sum |q_i K_i| / sqrt(d)), sums of bf16 queries in fp32 0.00159 to 0.00166.
+// Twice the query's bits would be twice the scores' products, and their tiles do not fit beside
+// those of K and V with 256 rows.  Pages
 // of one tile with different scales meet at the largest of them by an exact multiplication
 // in fp16 (apart_tile has what is too far apart for that); the tile's K scale multiplies the
 // scores, its V scale the weights, over a unit that each row of O has for itself.
@@ -30,7 +34,7 @@
 //
 // What bounds it.  256 rows: scores, weights and products of 64 keys go round in two parts
 // of a tile for each half, and the two halves fill each other's waits.  A tile takes
-// 2.3 us of an SM, against 1.3 at the bf16 rate that a library product reaches: left out,
+// 2.3 to 2.4 us of an SM, against 1.3 at the bf16 rate that a library product reaches: left out,
 // the conversion is worth 4 %, three quarters of the scores' products 5 %, the exponentials
 // 5 %, all of the softmax 15 %, so no part alone is the limit; N = 64 costs the scores'
 // products half again as much (Q's rows come from shared memory, 128 bytes a cycle), but
@@ -40,9 +44,10 @@
 // codes, of which none can be left out for more than 7 %.  Few rows over short caches: the
 // launches, 3 to 4 us each, and the way through the first tile, 4 us.
 //
-// 32 query heads of 128 over 8 kv heads: 4 x 512 tokens over 32768 980 us (1.13 PFLOP/s),
-// 1 x 4000 over nothing 195 us, 16 x 5 over 1000 to 8000 67 us (2.1 TB/s), 1 x 64 over 8000
-// 35 us; 40 heads over 8, 8 x 128 over 7000 to 8000 113 us (0.55 PFLOP/s).
+// 32 query heads of 128 over 8 kv heads: 4 x 512 tokens over 32768 1010 us (1.10 PFLOP/s),
+// 1 x 4000 over nothing 201 us, 16 x 5 over 1000 to 8000 72 us (2.0 TB/s), 1 x 64 over 8000
+// 35 us; 40 heads over 8, 8 x 128 over 7000 to 8000 118 us (0.53 PFLOP/s).
+// Figures beside a choice, here and below, are of both sides at the time it was made.
 #include <float.h>
 
 #include <algorithm>
@@ -1527,9 +1532,12 @@ int chunk_wide(int batch, int n_kv, int t_len, int group, int max_keys, int ctas
 // share, another end and what the third launch takes (kChunkMergeTiles).  Whole and cut,
 // in us, 32 query heads over 8: 8 x 128 tokens over 4000 rows 90 and 108, 4 x 200 over 4000
 // 88 and 95, 16 x 30 over 1000 31 and 42, 4 x 33 over 1800 41 and 35, 2 x 100 over 900 31
-// and 30.  (All units count as long as max_keys allows: where lengths differ and a CTA has
-// several units it may be wrong by a tenth, 32 x 5 over 100 to 2000 70 and 62.)  Units of
-// few tiles are whole in any case: 8 x 4 over up to 300 rows of head_dim 64 17 and 19.
+// and 30.  (All units count as long as max_keys allows, so lengths that differ mislead it: 32 x 5
+// over 100 to 2000 70 and 62; 152 units, 19 x 5, are whole at any max_keys, and with one sequence of
+// 32768 rows and the others of 500 that is 359 us, where 16 x 5 of such lengths, cut, are 56.)
+// Units of few tiles are whole in any case: 8 x 4 over 300 rows, head_dim 64, 15.2 and 19.4, 3 x 100
+// over 400 17.7 and 19.4, 2 x 30 over 480 of llama8b's heads 22.3 and 23.5, 16 x 8 over 400 23.1
+// and 23.2, but 4 x 4 over 500 22.7 and 21.7, 1 x 5 over 500 of qwen14b's 22.2 and 20.9.
 bool chunk_whole(int batch, int n_kv, int t_len, int group, int max_keys, int wide, int ctas) {
   if (max_keys <= kChunkWholeKeys) return true;
   const int64_t units = batch * (int64_t)n_kv * (((int64_t)t_len * group + 128 * wide - 1) / (128 * wide));

@@ -573,7 +573,9 @@ c2kv_status c2kv_attend_pages8_chunk(const c2kv_geometry* geom, const c2kv_pages
  *   - A parent's full pages are shared by its children.  The first of them, by
  *     place, keeps the others as well; the rest get a copy of the page that the
  *     length ends in (its held rows), so that every page that will be written
- *     to belongs to one sequence.
+ *     to belongs to one sequence.  (In the old batch, too, a page that a length
+ *     ends in, and those behind it, are their sequence's alone; a length is not
+ *     taken back below what a fork has shared.)
  *   - Pages of sequences that no place goes on with are given back.
  *   - Each sequence gets pages until it has room for its length and `room` more
  *     tokens.  Pages are taken in the order of places and entries, the free page
