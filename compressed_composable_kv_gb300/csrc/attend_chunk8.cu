@@ -83,7 +83,12 @@ constexpr float kWeightLog2 = 7.f;
 // How far a tile's V scale may be below the unit of a row's O before the unit is brought
 // down to it: weights below 2^-21 of the row's largest lose bits, with this 2^-15.
 constexpr int kUnitAbove = 6;
-constexpr int kMostLog2 = 120;        // O's largest element stays below 2^this when its unit is brought down
+// ... or above it before its products are made in fp32 (see apart_tile): to raise the unit by
+// more costs columns that only other pages have values in their place in fp32's range.
+constexpr int kUnitBelow = 60;
+constexpr int kMostLog2 = 120;        // O's largest element stays below 2^this when its unit is brought down,
+constexpr int kLeastLog2 = 100;       // its least above 2^-this when the unit is raised for a tile's scale
+constexpr int kSumLog2 = 80;          // weights in fp32 are up to 2^(kWeightLog2 + this)
 
 // What warp 16 finds out about a tile, and the segment that it belongs to.
 enum : uint32_t { kWhole = 2, kEnd = 4, kWide = 8, kNone = 16, kFresh = 32 };
@@ -395,20 +400,28 @@ __device__ __forceinline__ void transpose4(uint4 (&a)[4]) {
 }
 
 // O (D columns of a row in each lane of the warp, all of it there) to a unit 2^-down of its
-// present one, or as far in that direction as keeps it in range.  Returns how far.
+// present one, `down` of either sign, or as far in that direction as keeps it in fp32's
+// range.  Returns how far.
 template <int D>
-__device__ __forceinline__ int lower_unit(uint32_t o_at, int down) {
-  float most = 0.f;
+__device__ __forceinline__ int move_unit(uint32_t o_at, int down) {
+  float most = 0.f, least = INFINITY;   // of what is not 0
 #pragma unroll 1
   for (int c0 = 0; c0 < D; c0 += 16) {
     float o[16];
     tmem_ld_cols<16>(o_at + c0, o);
     tmem_wait_ld();
 #pragma unroll
-    for (int i = 0; i < 16; ++i) most = fmaxf(most, fabsf(o[i]));
+    for (int i = 0; i < 16; ++i) {
+      most = fmaxf(most, fabsf(o[i]));
+      if (o[i] != 0.f) least = fminf(least, fabsf(o[i]));
+    }
   }
-  if (most > 0.f) down = min(down, max(kMostLog2 - exponent_of_scale(most), 0));
-  const float by = pow2_float(min(down, 120)), more = pow2_float(down - min(down, 120));
+  if (most > 0.f) {
+    down = min(down, max(kMostLog2 - exponent_of_scale(most), 0));
+    down = max(down, min(-kLeastLog2 - exponent_of_scale(least), 0));
+  }
+  const int half = min(max(down, -120), 120);
+  const float by = pow2_float(half), more = pow2_float(down - half);
 #pragma unroll 1
   for (int c0 = 0; c0 < D; c0 += 16) {
     float o[16];
@@ -457,7 +470,7 @@ __device__ __forceinline__ void add_values(const ChunkParams& p, const TileSlot&
   int v_by = s.v_of[g] - v_ref;
   sc *= s.bad >> (8 + g) & 1 ? s.k_by[g] : 1.f;
   if (__any_sync(0xffffffffu, v_by < -60)) {
-    const int down = lower_unit<D>(o_at, v_by < -60 ? -v_by : 0);
+    const int down = move_unit<D>(o_at, v_by < -60 ? -v_by : 0);
     v_ref -= down;
     v_by += down;
   }
@@ -466,7 +479,7 @@ __device__ __forceinline__ void add_values(const ChunkParams& p, const TileSlot&
   tmem_wait_ld();
 #pragma unroll
   for (int i = 0; i < 16; ++i) top = fmaxf(top, 16 * g + i < nvis ? x[i] : -INFINITY);
-  const int room = (int)fmaxf(floorf(m_run - top * sc), 0.f), up = top != -INFINITY ? max(v_by - room, 0) : 0;
+  const int room = (int)fmaxf(floorf(m_run - top * sc), 0.f), up = top != -INFINITY ? max(v_by - room - kSumLog2, 0) : 0;
   float by = up > 126 ? 0.f : pow2_float(-up);   // what O is multiplied by, once
   v_ref += up;
   v_by -= up;
@@ -508,7 +521,7 @@ __device__ __forceinline__ void add_values(const ChunkParams& p, const TileSlot&
 }
 
 // A tile some of whose pages have V scales more than 2^15 apart, which share no fp16 scale
-// that all fit: its values are added in fp32, page by page, and its weights are 0 for the
+// that all fit, or one whose scale is too far from O's unit for that to be moved: its values are added in fp32, page by page, and its weights are 0 for the
 // products that the issuer makes of them all the same (60 to 80 us a tile: right, not fast).
 // From the scores of its first part, which are there, to the end of its second.
 struct RowSums {
@@ -587,6 +600,10 @@ __device__ __forceinline__ bool apart_tile(const ChunkParams& p, const TileSlot&
 
 // The same by calls, for 256-row units: what is in line there slows the tiles that do not need it
 // (4 x 512 over 32768 1030 us, not 1010; with 128-row units a call does, 16 x 5 75 us, not 72).
+template <int D>
+__device__ __noinline__ int move_unit_call(uint32_t o_at, int down) {
+  return move_unit<D>(o_at, down);
+}
 template <int D>
 __device__ __noinline__ bool any_value_call(const ChunkParams& p, const TileSlot& s, uint32_t groups) {
   return any_value<D>(p, s, groups);
@@ -1126,7 +1143,30 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
               sc = qs * ts.k_scale;   // in range, so that a masked score stays -inf; NaN stays
               sc = sc < FLT_MIN ? FLT_MIN : sc > FLT_MAX ? FLT_MAX : sc;
               bad = ts.bad;
-              if (bad >> 16 && (W == 1 ? any_value<D>(p, ts, bad >> 16) : any_value_call<D>(p, ts, bad >> 16))) {   // (seldom)
+              // The weights hold the tile's V scale over 2^v_ref, the unit of the row's O.  Where
+              // the scale is far below it, O is brought to a smaller unit first (as far as
+              // its largest element stays in range), so that these weights keep their bits; where it
+              // is above, the unit is raised below, by as much as the row's weights need, or far above, here,
+              // by as much as leaves all of O in range.  So a large scale costs a row nothing that gives
+              // its page no weight.
+              const int v_exp = ts.v_exp;
+              bool apart = bad >> 16 && (W == 1 ? any_value<D>(p, ts, bad >> 16) : any_value_call<D>(p, ts, bad >> 16));   // (seldom)
+              if (!apart) {
+                if (v_ref == kNoScale) v_ref = v_exp;
+                v_by = v_exp == kNoScale ? 0 : v_exp - v_ref;
+                if (__any_sync(0xffffffffu, (uint32_t)(v_by + kUnitAbove) > (uint32_t)(kUnitAbove + kUnitBelow))) {
+                  ok = __all_sync(0xffffffffu, ck_wait(&s_full[2 * m + 1], ns & 1, abort_flag, p.err));   // O is there
+                  if (!ok) break;
+                  tc_fence_after();
+                  const int by = v_by < -kUnitAbove || v_by > kUnitBelow ? -v_by : 0;
+                  const int down = W == 1 ? move_unit<D>(o_at, by) : move_unit_call<D>(o_at, by);
+                  v_ref -= down;
+                  v_by += down;
+                  // (O has no room to be moved so far)
+                  apart = __any_sync(0xffffffffu, (uint32_t)(v_by + kUnitAbove) > (uint32_t)(kUnitAbove + kUnitBelow));
+                }
+              }
+              if (apart) {
                 RowSums sums = {m_run, l_run, v_ref};
                 auto* tile = W == 1 ? apart_tile<D, 1> : apart_tile_call<D>;
                 ok = tile(p, ts, s_full + 2 * m, p_full + 2 * m, &k_empty[j & 1], &v_empty[(j - step) & 1], step, t >= step, o_set + m, s_at, o_at,
@@ -1135,22 +1175,6 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
                 l_run = sums.l;
                 v_ref = sums.v_ref;
                 break;
-              }
-              // The weights hold the tile's V scale over 2^v_ref, the unit of the row's O.  Where
-              // the scale is far below it, O is brought to a smaller unit first (as far as
-              // its largest element stays in range), so that these weights keep their bits; where it
-              // is above, the unit is raised below, by as much as the row's weights need.  So a large
-              // scale costs a row nothing that gives its page no weight.
-              const int v_exp = ts.v_exp;
-              if (v_ref == kNoScale) v_ref = v_exp;
-              v_by = v_exp == kNoScale ? 0 : v_exp - v_ref;
-              if (__any_sync(0xffffffffu, v_by < -kUnitAbove)) {
-                ok = __all_sync(0xffffffffu, ck_wait(&s_full[2 * m + 1], ns & 1, abort_flag, p.err));   // O is there
-                if (!ok) break;
-                tc_fence_after();
-                const int down = lower_unit<D>(o_at, v_by < -kUnitAbove ? -v_by : 0);
-                v_ref -= down;
-                v_by += down;
               }
             }
             float x[2][32];
@@ -1300,22 +1324,25 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
         const bool nan = nan_seg[seg & 3] == seg + 1;
         // A part's O is divided by its own sum, too: what is stored is a mean of values, and
         // in range as they are.  Its unit 2^v_ref is multiplied in where that stays in range.
-        float f = 1.f, f1 = 0.f;
+        float f = 1.f, f1 = 0.f, g = 1.f, g1 = 1.f;
         int unit = v_ref;
-        if (two) {
+        if (two) {   // O's common unit: the larger of the halves', with the weight that each has
           const float top = fmaxf(m_run, other.x), base = top == -INFINITY ? 0.f : top;
-          const float w0 = ex2_approx(m_run - base), w1 = ex2_approx(other.x - base);
-          const int v_other = (int)other.z;
-          unit = max(v_ref, v_other);
-          f = w0 * pow2_float(max(v_ref - unit, -126));
-          f1 = w1 * pow2_float(max(v_other - unit, -126));
-          l_run = l_run * w0 + other.y * w1;
+          const float a = m_run - base, a1 = other.x - base;
+          const float top_unit = ceilf(fmaxf((float)v_ref + a, other.z + a1));
+          unit = (int)fminf(fmaxf(top_unit, -120.f), 120.f);
+          const float d = (float)(v_ref - unit) + a, d1 = other.z - (float)unit + a1;
+          f = ex2_approx(fmaxf(d, -100.f));
+          g = ex2_approx(fminf(d + 100.f, 0.f));   // (far below the other, and still all that some columns have)
+          f1 = ex2_approx(fmaxf(d1, -100.f));
+          g1 = ex2_approx(fminf(d1 + 100.f, 0.f));
+          l_run = l_run * ex2_approx(a) + other.y * ex2_approx(a1);
           m_run = top;
         }
         if (unit == kNoScale) unit = 0;
         const int near = min(max(unit, -64), 64);
         const float inv = l_run == 0.f ? 0.f : pow2_float(near) / l_run, rest = pow2_float(unit - near);
-        const bool far = __any_sync(0xffffffffu, unit != near);
+        const bool far = __any_sync(0xffffffffu, unit != near || g * g1 != 1.f);
         f *= inv;
         f1 *= inv;
         const int t_of = (was.first + row) / G;
@@ -1329,17 +1356,22 @@ __global__ void __launch_bounds__(CK_THREADS, 1) chunk_kernel(const __grid_const
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] *= f;
+          if (far) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= g;
+          }
           if (two && !twice) {
             float y[32];
             tmem_ld32(o_at + 128 + c0, y);
             tmem_wait_ld();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = fmaf(y[i], f1, o[i]);
+            for (int i = 0; i < 32; ++i) o[i] = fmaf(y[i] * g1, f1, o[i]);
           }
           if (live && two && twice) {
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
-              const float4 y = hand_o[(c0 + i) / 4 * 64 + row];
+              float4 y = hand_o[(c0 + i) / 4 * 64 + row];
+              if (far) y.x *= g1, y.y *= g1, y.z *= g1, y.w *= g1;
               o[i] = fmaf(y.x, f1, o[i]);
               o[i + 1] = fmaf(y.y, f1, o[i + 1]);
               o[i + 2] = fmaf(y.z, f1, o[i + 2]);

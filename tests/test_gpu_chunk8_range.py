@@ -54,9 +54,16 @@ def _hold(c, b, keys, values):
     c.pool.upload()
 
 
-def _normal_rows(c, n):
+def _normal_rows(c, n, size=1.0):
     shape = (c.g.n_kv_heads, n, c.g.head_dim)
-    return _f64(_values(c.pool.rng, shape)), _f64(_values(c.pool.rng, shape))
+    return _f64(_values(c.pool.rng, shape)), _f64(_values(c.pool.rng, shape)) * size
+
+
+def _size(c, far):
+    """What all values are multiplied by, so that those 2^far above are numbers, too."""
+    size = 1.0 if far < 120 else 2.0 ** -60
+    c.v = _bits(_f64(c.v) * size)
+    return size
 
 
 def _check_by_column(c, what, skip=None, rows=None):
@@ -95,7 +102,7 @@ def _check_by_column(c, what, skip=None, rows=None):
     return worst
 
 
-SPREADS = [(d, group, page, t, far) for d, group, t in ((128, 4, 20), (64, 2, 70), (128, 5, 60)) for page in (16, 128) for far in (6, 14, 20, 26, 33, 60, 110)]
+SPREADS = [(d, group, page, t, far) for d, group, t in ((128, 4, 20), (64, 2, 70), (128, 5, 60)) for page in (16, 128) for far in (6, 14, 20, 26, 33, 60, 110, 160, 180)]
 
 
 @pytest.mark.parametrize("d,group,page,t,far", SPREADS)
@@ -105,8 +112,9 @@ def test_large_values_that_no_query_looks_at(d, group, page, t, far):
     g = _geom(d, group, 2)
     held = [129, 600, 1500]
     c = _aimed(g, page, held, [t] * 3, seed=far)
+    size = _size(c, far)
     for b, n in enumerate(held):
-        k, v = _normal_rows(c, n)
+        k, v = _normal_rows(c, n, size)
         for first in (0, 256, 1152)[:1 + b]:
             far_rows = slice(first, first + page)
             k[:, far_rows] = 0.0
@@ -126,11 +134,12 @@ def test_large_values_in_one_column(d, group, page, t, far):
     g = _geom(d, group, 2)
     held = [128, 600, 1500]
     c = _aimed(g, page, held, [t] * 3, seed=far + 1)
+    size = _size(c, far)
     for b, n in enumerate(held):
-        k, v = _normal_rows(c, n)
+        k, v = _normal_rows(c, n, size)
         for first in (0, 256, 1152)[:1 + b]:
             v[:, first:first + page] = 0.0
-            v[:, first:first + page, 7] = 2.0 ** far
+            v[:, first:first + page, 7] = 2.0 ** far * size
         _hold(c, b, k, v)
     c.call()
     _ok()
