@@ -44,9 +44,9 @@
 // codes, of which none can be left out for more than 7 %.  Few rows over short caches: the
 // launches, 3 to 4 us each, and the way through the first tile, 4 us.
 //
-// 32 query heads of 128 over 8 kv heads: 4 x 512 tokens over 32768 1010 us (1.10 PFLOP/s),
-// 1 x 4000 over nothing 201 us, 16 x 5 over 1000 to 8000 72 us (2.0 TB/s), 1 x 64 over 8000
-// 35 us; 40 heads over 8, 8 x 128 over 7000 to 8000 118 us (0.53 PFLOP/s).
+// 32 query heads of 128 over 8 kv heads: 4 x 512 tokens over 32768 1008 us (1.10 PFLOP/s),
+// 1 x 4000 over nothing 202 us, 16 x 5 over 1000 to 8000 74 us (1.9 TB/s), 1 x 64 over 8000
+// 35 us; 40 heads over 8, 8 x 128 over 7000 to 8000 119 us (0.53 PFLOP/s).
 // Figures beside a choice, here and below, are of both sides at the time it was made.
 #include <float.h>
 
