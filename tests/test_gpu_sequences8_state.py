@@ -6,6 +6,7 @@ import torch
 import compressed_composable_kv_gb300 as P
 from compressed_composable_kv_gb300 import synth as S
 from test_gpu_pages8 import _dev, _values
+from test_gpu_pages8_move import Pages
 from test_gpu_sequences8 import World
 
 pytestmark = pytest.mark.gpu
@@ -155,3 +156,13 @@ def test_beams_in_a_graph():
     w.decode(seqs, 1, "behind the graph")
     w.check(seqs, "behind the graph")
     w.sc.close()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("page,room", [(16, 300), (16, 299), (32, 500)])
+def test_a_fork_with_much_room(d, page, room):
+    """Room for hundreds of tokens in the smallest pages, from a pool that has them."""
+    lens = [0, 1, page - 1, page, page + 1, 2 * page, -1, 200, 133]
+    p = Pages(lens, page, 500, d=d, width=50, shared=[0, 0, 0, 0, 1, 1, 0, 0, 1], seed=page + d + room)
+    want = p.check_fork([8, 0, 8, -1, 2, 3, 3, 3, 6, 7, 4, 4, -5, 5, 5, 8, 1], room)
+    assert want is not None and len(want[3]) > 3
