@@ -165,4 +165,4 @@ def test_a_fork_with_much_room(d, page, room):
     lens = [0, 1, page - 1, page, page + 1, 2 * page, -1, 200, 133]
     p = Pages(lens, page, 500, d=d, width=50, shared=[0, 0, 0, 0, 1, 1, 0, 0, 1], seed=page + d + room)
     want = p.check_fork([8, 0, 8, -1, 2, 3, 3, 3, 6, 7, 4, 4, -5, 5, 5, 8, 1], room)
-    assert want is not None and len(want[3]) > 3
+    assert want is not None and len(want[3]) == 3   # of sequence 8 for two places, of 4 for one
